@@ -45,7 +45,9 @@ typedef enum {
     IQLH_ENONFINITE = -5  /* iql_status: the device saw a non-finite value   */
 } iqlh_status;
 
-typedef enum { IQLH_F32 = 0, IQLH_BF16 = 1 } iqlh_dtype;
+/* IQLH_F16 (IEEE binary16) is a type of the tensor lists and of the 4-bit
+ * matrices' float operands only; the trainers take IQLH_F32 and IQLH_BF16. */
+typedef enum { IQLH_F32 = 0, IQLH_BF16 = 1, IQLH_F16 = 2 } iqlh_dtype;
 
 /* Sticky device flag bits (iql_status, her_out.d_flags, iqlh_adam.d_flags). */
 #define IQLH_FLAG_NONFINITE_GRAD 0x1  /* Adam saw a non-finite clipped grad  */
@@ -474,6 +476,69 @@ int per_sample_indices(const float* d_priorities, int64_t size, int32_t n, uint6
  * also checks the p, m, v it writes and raises IQLH_FLAG_NONFINITE_STATE.) */
 int iqlh_nonfinite_check(const float* const* d_bufs, const int64_t* lens, int32_t num_slots,
                          int32_t* d_slot_flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norm and clip of the gradients of a whole network held as a list of
+ * tensors (the flat-vector form is grad_budget_accumulate above).
+ *
+ * A tensor set is the list cut into pieces.  iqlh_tensor_set_fill writes the
+ * piece table into host memory; the caller copies those bytes to the device
+ * once and puts the device address into set->d_table.  The table holds the
+ * tensors' addresses, so it is good for as long as they stay in place (as a
+ * captured graph is), and any number of calls, on any stream, may read it.
+ *   d_tensors  host array of device pointers, aligned to their element; may
+ *              be NULL where lens[i] is 0.
+ *   lens       host array of element counts, >= 0.
+ *   dtypes     host array of iqlh_dtype (F32, BF16, F16, in any mix).
+ *   host_table >= iqlh_tensor_set_bytes bytes, 16-byte aligned, and so must
+ *              be its device copy.  1 <= count <= 2^20, host only, no HIP call. */
+typedef struct iqlh_tensor_set {
+    const void* d_table;     /* device copy of the table (set by the caller)  */
+    size_t table_bytes;      /* bytes of the table to copy                    */
+    int64_t numel;           /* elements of all tensors together              */
+    int32_t count;           /* tensors                                       */
+    int32_t pieces;          /* pieces they are cut into                      */
+    int32_t overlap;         /* 1 when two tensors share memory               */
+    int32_t reserved0;
+} iqlh_tensor_set;
+
+typedef enum { IQLH_NORM_L2 = 0, IQLH_NORM_MAX = 1 } iqlh_norm_kind;
+
+int iqlh_tensor_set_bytes(const int64_t* lens, const int32_t* dtypes, int32_t count, size_t* bytes);
+int iqlh_tensor_set_fill(const void* const* d_tensors, const int64_t* lens, const int32_t* dtypes,
+                         int32_t count, void* host_table, size_t bytes, iqlh_tensor_set* set);
+
+/* Norm over every element of the set.
+ *   IQLH_NORM_L2: sqrt(sum x^2), squares and sums in binary64, rounded once;
+ *   IQLH_NORM_MAX: max |x|.  A NaN anywhere gives NaN, an infinity without a
+ *   NaN infinity (both kinds); a set without elements 0.
+ *   out_norm   device [1] f32.
+ *   out_each   device [count] f32, each tensor's own norm, or NULL.
+ *   d_flags    device sticky flag word or NULL: IQLH_FLAG_NONFINITE_GRAD when
+ *              the set holds a NaN or an infinity.
+ *   workspace  device, >= iqlh_grad_norm_workspace_bytes(set), 8-byte
+ *              aligned, no initial contents required; calls that overlap in
+ *              time need one each.
+ * The results do not depend on timing: every sum has a fixed order. */
+int iqlh_grad_norm_workspace_bytes(const iqlh_tensor_set* set, size_t* bytes);
+int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, float* out_each,
+                   int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Global clip: c = max_norm / norm when norm > max_norm, else 1 (the norm of
+ * iqlh_grad_norm in binary64, c rounded to binary32), and x -> c x.
+ *   out_flat   NULL: in place, each product rounded once to the tensor's type;
+ *              nothing is written when c is 1, and a set whose tensors
+ *              overlap is refused (they would be scaled twice).
+ *              Else device [numel] f32: the tensors one after the other, each
+ *              times c (c = 1 included), the tensors unchanged -- the flat
+ *              vector that grad_budget_accumulate takes as a source.  It must
+ *              not overlap the tensors.
+ *   out        device [2] f32: norm (before the clip) and c.
+ *   d_flags    device sticky flag word or NULL: a set with a NaN or an
+ *              infinity sets IQLH_FLAG_NONFINITE_GRAD; c is then 1.
+ * max_norm > 0 (infinity: never clips). */
+int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, float* out_flat,
+                   float* out, int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Thread-local text of the last error returned on this thread ("" if none). */
 const char* iqlh_last_error(void);

@@ -6,6 +6,7 @@ and the work is enqueued on torch's current HIP stream.  There is no CPU or
 PyTorch fallback: importing this module fails loudly when the library has not
 been built (``python offline_rl_step_amd/build.py``).
 """
+import bisect
 import ctypes
 import os
 
@@ -21,7 +22,8 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 OK, EINVAL, ESHAPE, ENOMEM, EHIP, ENONFINITE = 0, -1, -2, -3, -4, -5
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
+NORM_L2, NORM_MAX = 0, 1
 HER_FINAL, HER_FUTURE, HER_RANDOM = 0, 1, 2
 FLAG_NONFINITE_GRAD, FLAG_BAD_INDEX, FLAG_NONFINITE_LOSS, FLAG_NONFINITE_STATE = 0x1, 0x2, 0x4, 0x8
 MAX_SOURCES = 8
@@ -72,6 +74,11 @@ class BudgetStep(ctypes.Structure):
                 ("max_grad_norm", _f)]
 
 
+class TensorSetStruct(ctypes.Structure):
+    _fields_ = [("d_table", _p), ("table_bytes", ctypes.c_size_t), ("numel", _i64), ("count", _i32),
+                ("pieces", _i32), ("overlap", _i32), ("reserved0", _i32)]
+
+
 def _sig(name, res, args):
     fn = getattr(_lib, name)
     fn.restype = res
@@ -120,6 +127,16 @@ _lib_iql_aux_step_phase_stamps = _sig("iql_aux_step_phase_stamps", _i32,
 _lib_per_ws = _sig("per_workspace_bytes", _i32, [_i64, ctypes.POINTER(ctypes.c_size_t)])
 _lib_per_sample = _sig("per_sample_indices", _i32, [_p, _i64, _i32, _u64, _p, _f, _p, _p, _p, _p, ctypes.c_size_t, _p])
 _lib_nonfinite_check = _sig("iqlh_nonfinite_check", _i32, [ctypes.POINTER(_p), ctypes.POINTER(_i64), _i32, _p, _p])
+_lib_set_bytes = _sig("iqlh_tensor_set_bytes", _i32, [ctypes.POINTER(_i64), ctypes.POINTER(_i32), _i32,
+                                                      ctypes.POINTER(ctypes.c_size_t)])
+_lib_set_fill = _sig("iqlh_tensor_set_fill", _i32, [ctypes.POINTER(_p), ctypes.POINTER(_i64), ctypes.POINTER(_i32),
+                                                    _i32, _p, ctypes.c_size_t, ctypes.POINTER(TensorSetStruct)])
+_lib_norm_ws = _sig("iqlh_grad_norm_workspace_bytes", _i32, [ctypes.POINTER(TensorSetStruct),
+                                                             ctypes.POINTER(ctypes.c_size_t)])
+_lib_grad_norm = _sig("iqlh_grad_norm", _i32, [ctypes.POINTER(TensorSetStruct), _i32, _p, _p, _p, _p,
+                                               ctypes.c_size_t, _p])
+_lib_grad_clip = _sig("iqlh_grad_clip", _i32, [ctypes.POINTER(TensorSetStruct), _i32, _f, _p, _p, _p, _p,
+                                               ctypes.c_size_t, _p])
 _lib_last_error = _sig("iqlh_last_error", ctypes.c_char_p, [])
 
 
@@ -312,6 +329,119 @@ def iql_status(h):
 def iql_aw_policy(q, v, num_groups, batch, num_actions, beta, out_pi, stream=None):
     _check(_lib_iql_aw_policy(_ptr(q), _ptr(v), num_groups, batch, num_actions, beta, _ptr(out_pi),
                               _stream(stream)), "iql_aw_policy")
+
+
+# ----------------------------------------------- norm and clip of tensor lists
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _float_code(t, what):
+    _need(t.dtype in _DTYPES, f"{what}: {t.dtype} is none of float32, bfloat16, float16")
+    return _DTYPES[t.dtype]
+
+
+def _need_f32(t, numel, device, what):
+    """t: a contiguous float32 tensor of at least `numel` elements on `device`."""
+    _need(t.dtype == torch.float32 and t.is_contiguous() and t.numel() >= numel and t.device == device,
+          f"{what} must be a contiguous float32 tensor of at least {numel} elements on {device}")
+
+
+def _need_current(device):
+    """The library enqueues on the current device."""
+    _need(device.type == "cuda", f"tensors are on {device}: the kernels read device memory")
+    _need(device.index == torch.cuda.current_device(),
+          f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+class TensorSet:
+    """The tensors of one network (float32, bfloat16, float16 in any mix, each
+    contiguous, all on the current device), cut into pieces once for any number of
+    grad_norm / grad_clip calls.  Keeps the tensors; their storage must stay
+    where it is (``p.grad`` cleared with ``set_to_none=False``)."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors = list(tensors)
+        _need(len(tensors) > 0, "TensorSet needs at least one tensor")
+        self.device = tensors[0].device
+        _need_current(self.device)
+        for i, t in enumerate(tensors):
+            _need(t.device == self.device, f"tensor {i} is on {t.device}, the first on {self.device}")
+            _need(t.is_contiguous(), f"tensor {i} is not contiguous")
+            _float_code(t, f"tensor {i}")
+        k = len(tensors)
+        ptrs = (_p * k)(*[t.data_ptr() or None for t in tensors])
+        lens = (_i64 * k)(*[t.numel() for t in tensors])
+        types = (_i32 * k)(*[_DTYPES[t.dtype] for t in tensors])
+        need = ctypes.c_size_t()
+        _check(_lib_set_bytes(lens, types, k, ctypes.byref(need)), "iqlh_tensor_set_bytes")
+        host = torch.empty(need.value + 16, dtype=torch.uint8)
+        lead = -host.data_ptr() % 16
+        host = host[lead:lead + need.value]
+        self.struct = TensorSetStruct()
+        _check(_lib_set_fill(ptrs, lens, types, k, host.data_ptr(), need.value, ctypes.byref(self.struct)),
+               "iqlh_tensor_set_fill")
+        # a copy from pageable memory: complete when it returns, for any stream
+        self.table = host[:self.struct.table_bytes].to(self.device)
+        self.struct.d_table = self.table.data_ptr()
+        self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
+
+    @property
+    def numel(self):
+        return self.struct.numel
+
+    def overlaps(self, t):
+        """Whether t (contiguous) shares memory with a tensor of the set."""
+        lo, hi = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+        if self.struct.overlap:  # ranges are not disjoint: look at each
+            return any(a < hi and lo < b for a, b in self._ranges)
+        i = bisect.bisect_left(self._ranges, (hi,))
+        return any(a < hi and lo < b for a, b in self._ranges[max(0, i - 1):i])
+
+
+def grad_norm_workspace(tensor_set):
+    """A workspace for grad_norm / grad_clip calls on the set."""
+    out = ctypes.c_size_t()
+    _check(_lib_norm_ws(ctypes.byref(tensor_set.struct), ctypes.byref(out)), "iqlh_grad_norm_workspace_bytes")
+    return torch.empty(out.value, dtype=torch.uint8, device=tensor_set.device)
+
+
+def _need_aux(device, workspace, flags):
+    _need(workspace.device == device and workspace.is_contiguous(), f"workspace must be contiguous on {device}")
+    _need(flags is None or (flags.dtype == torch.int32 and flags.device == device and flags.numel() >= 1),
+          f"flags must be an int32 tensor on {device}")
+
+
+def grad_norm(tensor_set, out_norm, workspace, kind=NORM_L2, out_each=None, flags=None, stream=None):
+    """Norm over all tensors of the set into out_norm [1], with out_each
+    [count] each tensor's own too."""
+    s = tensor_set
+    _need_current(s.device)
+    _need_f32(out_norm, 1, s.device, "out_norm")
+    if out_each is not None:
+        _need_f32(out_each, s.struct.count, s.device, "out_each")
+    _need_aux(s.device, workspace, flags)
+    _check(_lib_grad_norm(ctypes.byref(s.struct), kind, _ptr(out_norm), _ptr(out_each), _ptr(flags), _ptr(workspace),
+                          workspace.numel() * workspace.element_size(), _stream(stream)), "iqlh_grad_norm")
+
+
+def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None, flags=None, stream=None):
+    """Clips the set to max_norm: in place, or into the flat float32 vector
+    out_flat [numel] with the tensors unchanged.  out [2]: norm and factor."""
+    s = tensor_set
+    _need_current(s.device)
+    _need_f32(out, 2, s.device, "out")
+    if out_flat is not None:
+        _need_f32(out_flat, s.numel, s.device, "out_flat")
+        _need(not s.overlaps(out_flat[:s.numel]), "out_flat shares memory with a tensor of the set")
+    _need_aux(s.device, workspace, flags)
+    _check(_lib_grad_clip(ctypes.byref(s.struct), kind, max_norm, _ptr(out_flat), _ptr(out), _ptr(flags),
+                          _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "iqlh_grad_clip")
 
 
 # ------------------------------------------------------------------- HER

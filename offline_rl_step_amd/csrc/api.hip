@@ -3,6 +3,7 @@
 // that can fail on the host runs before the first HIP call.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -492,6 +493,156 @@ int iqlh_nonfinite_check(const float* const* d_bufs, const int64_t* lens, int32_
     a.block0[num_slots] = (int)blocks;
     hipError_t e = launch_nonfinite_sentinel(a, (int)blocks, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_nonfinite_check");
+    return IQLH_OK;
+}
+
+// ------------------------------------------- norm and clip of tensor lists
+static int dtype_bytes(int32_t dtype) {
+    return dtype == IQLH_F32 ? 4 : dtype == IQLH_BF16 || dtype == IQLH_F16 ? 2 : 0;
+}
+
+static int check_tensor_list(const char* who, const int64_t* lens, const int32_t* dtypes, int32_t count,
+                             int64_t* piece_bytes, int64_t* pieces) {
+    if (!lens || !dtypes) return fail(IQLH_EINVAL, "%s: NULL argument", who);
+    if (count < 1 || count > 1 << 20) return fail(IQLH_EINVAL, "%s: count %d outside [1, 2^20]", who, count);
+    int64_t total = 0;
+    for (int i = 0; i < count; ++i) {
+        const int es = dtype_bytes(dtypes[i]);
+        if (!es) return fail(IQLH_EINVAL, "%s: dtypes[%d] = %d is no float type", who, i, dtypes[i]);
+        if (lens[i] < 0 || lens[i] > (int64_t)1 << 40) return fail(IQLH_EINVAL, "%s: lens[%d] outside [0, 2^40]", who, i);
+        total += lens[i] * es;
+        if (total > (int64_t)1 << 44) return fail(IQLH_EINVAL, "%s: more than 2^44 bytes", who);
+    }
+    // 32 KB a piece where there are pieces enough for every compute unit,
+    // down to 4 KB (one 16-byte load a thread) for small sets
+    int64_t pb = (total / kNormBlocks + 4095) / 4096 * 4096;
+    pb = pb < 4096 ? 4096 : pb > 32768 ? 32768 : pb;
+    int64_t np = 0;
+    for (int i = 0; i < count; ++i) np += (lens[i] * dtype_bytes(dtypes[i]) + pb - 1) / pb;
+    *piece_bytes = pb;
+    *pieces = np;
+    return IQLH_OK;
+}
+
+struct TensorRange { uint64_t begin, end; };
+
+int iqlh_tensor_set_bytes(const int64_t* lens, const int32_t* dtypes, int32_t count, size_t* bytes) {
+    if (!bytes) return fail(IQLH_EINVAL, "iqlh_tensor_set_bytes: bytes is NULL");
+    int64_t pb = 0, np = 0;
+    int rc = check_tensor_list("iqlh_tensor_set_bytes", lens, dtypes, count, &pb, &np);
+    if (rc) return rc;
+    // pieces, the tensors' piece ranges, and the address ranges that fill sorts
+    *bytes = (size_t)np * sizeof(TensorPiece) + ((size_t)count + 4) / 4 * 16 + (size_t)count * sizeof(TensorRange);
+    return IQLH_OK;
+}
+
+int iqlh_tensor_set_fill(const void* const* d_tensors, const int64_t* lens, const int32_t* dtypes, int32_t count,
+                         void* host_table, size_t bytes, iqlh_tensor_set* set) {
+    int64_t pb = 0, np = 0;
+    size_t need = 0;
+    int rc = check_tensor_list("iqlh_tensor_set_fill", lens, dtypes, count, &pb, &np);
+    if (rc) return rc;
+    if (!d_tensors || !host_table || !set) return fail(IQLH_EINVAL, "iqlh_tensor_set_fill: NULL argument");
+    iqlh_tensor_set_bytes(lens, dtypes, count, &need);
+    if (bytes < need) return fail(IQLH_EINVAL, "iqlh_tensor_set_fill: table of %zu bytes, needs %zu", bytes, need);
+    if ((uintptr_t)host_table & 15u) return fail(IQLH_EINVAL, "iqlh_tensor_set_fill: table not 16-byte aligned");
+    for (int i = 0; i < count; ++i) {
+        if (lens[i] && !d_tensors[i]) return fail(IQLH_EINVAL, "iqlh_tensor_set_fill: d_tensors[%d] is NULL", i);
+        if ((uintptr_t)d_tensors[i] % dtype_bytes(dtypes[i]))
+            return fail(IQLH_EINVAL, "iqlh_tensor_set_fill: d_tensors[%d] not aligned to its element", i);
+    }
+    TensorPiece* pc = (TensorPiece*)host_table;
+    int32_t* first = (int32_t*)(pc + np);
+    TensorRange* range = (TensorRange*)((char*)first + ((size_t)count + 4) / 4 * 16);
+    int64_t off = 0, k = 0;
+    for (int i = 0; i < count; ++i) {
+        const int es = dtype_bytes(dtypes[i]);
+        const uint64_t p = (uint64_t)(uintptr_t)d_tensors[i];
+        const int64_t pe = pb / es;
+        first[i] = (int32_t)k;
+        range[i] = TensorRange{p, p + (uint64_t)lens[i] * es};
+        // every piece but a tensor's first starts on a 16-byte boundary: the
+        // first also takes the elements before the tensor's first boundary
+        const int64_t head = (int64_t)((16 - (p & 15u)) & 15u) / es;
+        for (int64_t e = 0; e < lens[i];) {
+            int64_t n = pe + (e == 0 ? head : 0);
+            if (n > lens[i] - e) n = lens[i] - e;
+            pc[k++] = TensorPiece{p + (uint64_t)(e * es), off + e, (int32_t)n, dtypes[i], {0, 0}};
+            e += n;
+        }
+        off += lens[i];
+    }
+    first[count] = (int32_t)k;
+    std::sort(range, range + count, [](const TensorRange& a, const TensorRange& b) { return a.begin < b.begin; });
+    int overlap = 0;
+    uint64_t end = 0;
+    for (int i = 0; i < count; ++i) {
+        if (range[i].end == range[i].begin) continue;
+        if (range[i].begin < end) overlap = 1;
+        if (range[i].end > end) end = range[i].end;
+    }
+    std::memset(set, 0, sizeof(*set));
+    set->table_bytes = (size_t)((char*)range - (char*)host_table);
+    // the ranges follow np pieces at most; fewer leave the piece ranges where
+    // the kernels look for them, behind the last piece
+    std::memmove(pc + k, first, sizeof(int32_t) * ((size_t)count + 1));
+    set->numel = off;
+    set->count = count;
+    set->pieces = (int32_t)k;
+    set->overlap = overlap;
+    return IQLH_OK;
+}
+
+int iqlh_grad_norm_workspace_bytes(const iqlh_tensor_set* set, size_t* bytes) {
+    if (!set || !bytes) return fail(IQLH_EINVAL, "iqlh_grad_norm_workspace_bytes: NULL argument");
+    if (set->pieces < 0) return fail(IQLH_EINVAL, "iqlh_grad_norm_workspace_bytes: set not filled");
+    *bytes = sizeof(uint64_t) * ((size_t)kNormBlocks + 4 * (size_t)set->pieces);
+    return IQLH_OK;
+}
+
+static int make_tensor_set_args(const char* who, const iqlh_tensor_set* set, int32_t kind, int32_t* d_flags,
+                                void* workspace, size_t workspace_bytes, TensorSetArgs* a) {
+    size_t need = 0;
+    int rc = iqlh_grad_norm_workspace_bytes(set, &need);
+    if (rc) return rc;
+    if (!set->d_table || set->count < 1) return fail(IQLH_EINVAL, "%s: set->d_table is NULL", who);
+    if ((uintptr_t)set->d_table & 15u) return fail(IQLH_EINVAL, "%s: set->d_table not 16-byte aligned", who);
+    if (kind != IQLH_NORM_L2 && kind != IQLH_NORM_MAX) return fail(IQLH_EINVAL, "%s: unknown norm kind %d", who, kind);
+    if (!workspace || ((uintptr_t)workspace & 7u)) return fail(IQLH_EINVAL, "%s: workspace NULL or not 8-byte aligned", who);
+    if (workspace_bytes < need) return fail(IQLH_EINVAL, "%s: workspace too small: %zu < %zu", who, workspace_bytes, need);
+    a->pieces = (const TensorPiece*)set->d_table;
+    a->first = (const int32_t*)(a->pieces + set->pieces);
+    a->npieces = set->pieces;
+    a->count = set->count;
+    a->part = (uint64_t*)workspace;
+    a->each = nullptr;
+    a->flags = d_flags;
+    return IQLH_OK;
+}
+
+int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, float* out_each, int32_t* d_flags,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+    TensorSetArgs a;
+    int rc = make_tensor_set_args("iqlh_grad_norm", set, kind, d_flags, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    if (!out_norm) return fail(IQLH_EINVAL, "iqlh_grad_norm: out_norm is NULL");
+    if (out_each) a.each = a.part + kNormBlocks;
+    hipError_t e = launch_grad_norm(a, kind, out_norm, out_each, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_grad_norm launch");
+    return IQLH_OK;
+}
+
+int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, float* out_flat, float* out,
+                   int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream) {
+    TensorSetArgs a;
+    int rc = make_tensor_set_args("iqlh_grad_clip", set, kind, d_flags, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    if (!out) return fail(IQLH_EINVAL, "iqlh_grad_clip: out is NULL");
+    if (!(max_norm > 0.f)) return fail(IQLH_EINVAL, "iqlh_grad_clip: max_norm must be > 0");
+    if (!out_flat && set->overlap)
+        return fail(IQLH_EINVAL, "iqlh_grad_clip: tensors that share memory cannot be clipped in place");
+    hipError_t e = launch_grad_clip(a, kind, max_norm, out_flat, out, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_grad_clip launch");
     return IQLH_OK;
 }
 

@@ -216,6 +216,31 @@ struct SentinelArgs {
 };
 hipError_t launch_nonfinite_sentinel(const SentinelArgs& a, int blocks, hipStream_t stream);
 
+// ------------------------------------------- norm and clip of tensor lists
+// One piece of a tensor: n elements from ptr on, and their offset in the
+// concatenation of all tensors.  The last piece is followed by the int32
+// piece range of each tensor (count + 1 entries).
+struct TensorPiece {
+    uint64_t ptr;
+    int64_t off;
+    int32_t n;
+    int32_t dtype;  // iqlh_dtype
+    int32_t reserved[2];
+};
+static_assert(sizeof(TensorPiece) == 32, "piece table entry");
+constexpr int kNormBlocks = 1024;  // most workgroups of the norm pass
+struct TensorSetArgs {
+    const TensorPiece* pieces;
+    const int32_t* first;  // [count + 1]
+    int32_t npieces, count;
+    uint64_t* part;        // [kNormBlocks] block sums (binary64 bits) or maxima (binary32 bits)
+    uint64_t* each;        // [npieces][4] the same of every wave of every piece, or null
+    int32_t* flags;
+};
+hipError_t launch_grad_norm(const TensorSetArgs& a, int kind, float* out_norm, float* out_each, hipStream_t stream);
+hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, float max_norm, float* flat, float* out,
+                            hipStream_t stream);
+
 // ------------------------------------------------------- whole step
 // One pass of the hot path in four launches:
 //   A  HER relabelling + budget source norms   (independent of each other)

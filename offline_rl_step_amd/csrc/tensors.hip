@@ -1,0 +1,319 @@
+// Norm and clip of the gradients of a network held as a list of tensors.
+//
+//   norm = sqrt(sum_t sum_i x_ti^2)   (or max |x_ti|)
+//   c    = max_norm / norm if norm > max_norm else 1,   x <- c x
+//
+// HBM-bound: the norm reads every element once, the clip once more (from the
+// Infinity Cache where the set fits it) and writes it once.  The list is cut
+// into pieces on the host (TensorPiece), so a workgroup streams whole pieces
+// whatever the tensors' sizes are, and one launch serves any number of
+// tensors and any mix of types.
+//   1. norm pass: a workgroup takes the pieces b, b + grid, ..; block sums (and
+//      with per-tensor norms each wave's sum of each piece) to the workspace;
+//   2. finish: block 0 adds the block sums; one wave per tensor adds its
+//      pieces' sums;   or
+//   2. scale pass: every workgroup adds the block sums itself, in the same
+//      order, and scales its pieces.
+// No atomics on sums: every order is fixed, results repeat bit for bit.
+//
+// Squares and sums are held in binary64: a product of two binary32 values is
+// exact there, nothing overflows or vanishes (binary32 squares do from
+// |x| = 1.8e19 up and 1e-23 down), and the norm does not depend on how the
+// list is cut.  One conversion and one fma per element at half rate stay
+// under the loads' time.
+#include "common.hpp"
+#include "iqlher.h"
+#include "launch.hpp"
+
+namespace iqlh {
+
+namespace {
+
+constexpr int kNT = 256;
+constexpr int kAhead = 8;  // 16-byte loads in flight per thread
+
+template <int DT> struct Elem;
+template <> struct Elem<IQLH_F32> {
+    typedef float type;
+    static constexpr int kQ = 4;  // elements per 16 bytes
+    static IQLH_DEV float get(uint4 q, int i) { return __uint_as_float((&q.x)[i]); }
+    static IQLH_DEV float load(const void* p, int64_t i) { return ((const float*)p)[i]; }
+    static IQLH_DEV void store(void* p, int64_t i, float v) { ((float*)p)[i] = v; }
+    static IQLH_DEV uint4 pack(const float* v) {
+        return uint4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+};
+template <> struct Elem<IQLH_BF16> {
+    typedef uint16_t type;
+    static constexpr int kQ = 8;
+    static IQLH_DEV float get(uint4 q, int i) {
+        const uint32_t w = (&q.x)[i >> 1];
+        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
+    }
+    static IQLH_DEV float load(const void* p, int64_t i) { return bf2f(((const uint16_t*)p)[i]); }
+    static IQLH_DEV void store(void* p, int64_t i, float v) { ((uint16_t*)p)[i] = f2bf(v); }
+    static IQLH_DEV uint4 pack(const float* v) {
+        return uint4{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7])};
+    }
+};
+template <> struct Elem<IQLH_F16> {
+    typedef _Float16 type;
+    static constexpr int kQ = 8;
+    static IQLH_DEV float get(uint4 q, int i) {
+        const uint32_t w = (&q.x)[i >> 1];
+        return (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? w >> 16 : w));
+    }
+    static IQLH_DEV float load(const void* p, int64_t i) { return (float)((const _Float16*)p)[i]; }
+    static IQLH_DEV void store(void* p, int64_t i, float v) { ((_Float16*)p)[i] = (_Float16)v; }
+    static IQLH_DEV uint32_t pack2(float a, float b) {
+        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+               (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+    }
+    static IQLH_DEV uint4 pack(const float* v) {
+        return uint4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+    }
+};
+
+// Running value of a norm: the sum of squares, or the largest |x| as its
+// bits (whose order is that of the values, NaN above infinity).
+template <int KIND> struct Stat;
+template <> struct Stat<IQLH_NORM_L2> {
+    double s;
+    IQLH_DEV Stat() : s(0.0) {}
+    IQLH_DEV void add(float x) { s = fma((double)x, (double)x, s); }
+    IQLH_DEV void join(uint64_t bits) { s += __longlong_as_double((long long)bits); }
+    IQLH_DEV uint64_t bits() const { return (uint64_t)__double_as_longlong(s); }
+    IQLH_DEV double norm() const { return sqrt(s); }
+};
+template <> struct Stat<IQLH_NORM_MAX> {
+    uint32_t s;
+    IQLH_DEV Stat() : s(0u) {}
+    IQLH_DEV void add(float x) {
+        const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+        s = b > s ? b : s;
+    }
+    IQLH_DEV void join(uint64_t bits) { s = (uint32_t)bits > s ? (uint32_t)bits : s; }
+    IQLH_DEV uint64_t bits() const { return s; }
+    IQLH_DEV double norm() const { return (double)__uint_as_float(s); }
+};
+
+template <int KIND>
+IQLH_DEV Stat<KIND> wave_join(Stat<KIND> v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const uint64_t b = v.bits();
+        const uint32_t lo = __shfl_xor((uint32_t)b, o, kWave), hi = __shfl_xor((uint32_t)(b >> 32), o, kWave);
+        v.join((uint64_t)hi << 32 | lo);
+    }
+    return v;
+}
+
+template <int KIND>
+IQLH_DEV Stat<KIND> block_join(Stat<KIND> v, uint64_t* red) {
+    v = wave_join(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x / kWave] = v.bits();
+    __syncthreads();
+    Stat<KIND> s;
+#pragma unroll
+    for (int i = 0; i < kNT / kWave; ++i) s.join(red[i]);
+    return s;
+}
+
+// A piece as [head elements][nq whole 16-byte quads on a boundary][tail elements]
+template <int DT>
+struct Cut {
+    int head, nq, tail;
+    const uint4* q;
+    IQLH_DEV explicit Cut(const TensorPiece& p) {
+        const int to_edge = (int)((16u - (uint32_t)(p.ptr & 15u)) & 15u) / (int)sizeof(typename Elem<DT>::type);
+        head = to_edge < p.n ? to_edge : p.n;
+        nq = (p.n - head) / Elem<DT>::kQ;
+        tail = p.n - head - nq * Elem<DT>::kQ;
+        q = (const uint4*)(p.ptr + (uint64_t)head * sizeof(typename Elem<DT>::type));
+    }
+    // element index of the thread's edge element, or -1
+    IQLH_DEV int edge() const {
+        const int t = threadIdx.x;
+        return t < head ? t : t < head + tail ? nq * Elem<DT>::kQ + t : -1;
+    }
+};
+
+template <int DT, int KIND>
+IQLH_DEV void piece_stat(const TensorPiece& p, Stat<KIND>& a0, Stat<KIND>& a1) {
+    typedef Elem<DT> E;
+    const Cut<DT> c(p);
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * kNT < c.nq; i += kAhead * kNT) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = c.q[i + k * kNT];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int j = 0; j < E::kQ; ++j) (j & 1 ? a1 : a0).add(E::get(x[k], j));
+    }
+    for (; i < c.nq; i += kNT) {
+        const uint4 x = c.q[i];
+#pragma unroll
+        for (int j = 0; j < E::kQ; ++j) (j & 1 ? a1 : a0).add(E::get(x, j));
+    }
+    const int e = c.edge();
+    if (e >= 0) a0.add(E::load((const void*)p.ptr, e));
+}
+
+template <int KIND, bool EACH>
+__global__ __launch_bounds__(kNT) void grad_norm_kernel(TensorSetArgs a) {
+    __shared__ uint64_t red[kNT / kWave];
+    Stat<KIND> total;
+    for (int k = blockIdx.x; k < a.npieces; k += gridDim.x) {
+        const TensorPiece p = a.pieces[k];
+        Stat<KIND> s0, s1;
+        if (p.dtype == IQLH_F32) piece_stat<IQLH_F32>(p, s0, s1);
+        else if (p.dtype == IQLH_BF16) piece_stat<IQLH_BF16>(p, s0, s1);
+        else piece_stat<IQLH_F16>(p, s0, s1);
+        s0.join(s1.bits());
+        total.join(s0.bits());
+        if (EACH) {
+            const Stat<KIND> w = wave_join(s0);
+            if ((threadIdx.x & 63) == 0) a.each[(int64_t)k * 4 + threadIdx.x / kWave] = w.bits();
+        }
+    }
+    total = block_join(total, red);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = total.bits();
+}
+
+template <int KIND>
+IQLH_DEV double norm_of_parts(const uint64_t* part, int nb, uint64_t* red) {
+    Stat<KIND> s;
+    for (int i = threadIdx.x; i < nb; i += kNT) s.join(part[i]);
+    return block_join(s, red).norm();
+}
+
+IQLH_DEV bool finite64(double x) { return fabs(x) < __longlong_as_double(0x7FF0000000000000ll); }
+
+// Block 0: the whole norm.  The others: one wave per tensor.
+template <int KIND>
+__global__ __launch_bounds__(kNT) void grad_norm_finish_kernel(TensorSetArgs a, int nb, float* __restrict__ out_norm,
+                                                               float* __restrict__ out_each) {
+    __shared__ uint64_t red[kNT / kWave];
+    if (blockIdx.x == 0) {
+        const double n = norm_of_parts<KIND>(a.part, nb, red);
+        if (threadIdx.x == 0) {
+            *out_norm = (float)n;
+            if (!finite64(n)) set_flag(a.flags, IQLH_FLAG_NONFINITE_GRAD);
+        }
+        return;
+    }
+    const int t = (blockIdx.x - 1) * (kNT / kWave) + threadIdx.x / kWave;
+    if (t >= a.count) return;
+    Stat<KIND> s;
+    const int64_t end = (int64_t)a.first[t + 1] * 4;
+    for (int64_t i = (int64_t)a.first[t] * 4 + (threadIdx.x & 63); i < end; i += kWave) s.join(a.each[i]);
+    s = wave_join(s);
+    if ((threadIdx.x & 63) == 0) out_each[t] = (float)s.norm();
+}
+
+template <int DT>
+IQLH_DEV void scale_piece(const TensorPiece& p, float c, float* flat) {
+    typedef Elem<DT> E;
+    const Cut<DT> cut(p);
+    const int e = cut.edge();
+    if (!flat) {
+        uint4* q = (uint4*)cut.q;
+        for (int i = threadIdx.x; i < cut.nq; i += kNT) {
+            const uint4 x = q[i];
+            float v[E::kQ];
+#pragma unroll
+            for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
+            q[i] = E::pack(v);
+        }
+        if (e >= 0) E::store((void*)p.ptr, e, E::load((const void*)p.ptr, e) * c);
+        return;
+    }
+    float* out = flat + p.off;
+    float* body = out + cut.head;
+    const bool wide = ((uintptr_t)body & 15u) == 0;  // the same for the whole block
+    for (int i = threadIdx.x; i < cut.nq; i += kNT) {
+        const uint4 x = cut.q[i];
+        float v[E::kQ];
+#pragma unroll
+        for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
+        if (wide) {
+#pragma unroll
+            for (int j = 0; j < E::kQ; j += 4)
+                *(float4*)(body + (int64_t)i * E::kQ + j) = float4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < E::kQ; ++j) body[(int64_t)i * E::kQ + j] = v[j];
+        }
+    }
+    if (e >= 0) out[e] = E::load((const void*)p.ptr, e) * c;
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kNT) void grad_scale_kernel(TensorSetArgs a, int nb, float max_norm,
+                                                         float* __restrict__ flat, float* __restrict__ out) {
+    __shared__ uint64_t red[kNT / kWave];
+    const double n = norm_of_parts<KIND>(a.part, nb, red);
+    const bool ok = finite64(n);
+    const float c = ok && n > (double)max_norm ? (float)((double)max_norm / n) : 1.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        out[0] = (float)n;
+        out[1] = c;
+        if (!ok) set_flag(a.flags, IQLH_FLAG_NONFINITE_GRAD);
+    }
+    if (!flat && c == 1.f) return;
+    // last piece first: the end of the list is what the norm pass read last
+    // and what a list larger than the Infinity Cache still finds there
+    for (int k = a.npieces - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
+        const TensorPiece p = a.pieces[k];
+        if (p.dtype == IQLH_F32) scale_piece<IQLH_F32>(p, c, flat);
+        else if (p.dtype == IQLH_BF16) scale_piece<IQLH_BF16>(p, c, flat);
+        else scale_piece<IQLH_F16>(p, c, flat);
+    }
+}
+
+int norm_blocks(int npieces) { return npieces < 1 ? 1 : npieces < kNormBlocks ? npieces : kNormBlocks; }
+
+template <int KIND>
+hipError_t norm_pass(const TensorSetArgs& a, hipStream_t stream) {
+    const dim3 grid(norm_blocks(a.npieces)), block(kNT);
+    if (a.each) hipLaunchKernelGGL((grad_norm_kernel<KIND, true>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((grad_norm_kernel<KIND, false>), grid, block, 0, stream, a);
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t norm_launch(const TensorSetArgs& a, float* out_norm, float* out_each, hipStream_t stream) {
+    hipError_t e = norm_pass<KIND>(a, stream);
+    if (e != hipSuccess) return e;
+    const int grid = 1 + (out_each ? (a.count + 3) / 4 : 0);
+    hipLaunchKernelGGL(grad_norm_finish_kernel<KIND>, dim3(grid), dim3(kNT), 0, stream, a, norm_blocks(a.npieces),
+                       out_norm, out_each);
+    return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t clip_launch(const TensorSetArgs& a, float max_norm, float* flat, float* out, hipStream_t stream) {
+    hipError_t e = norm_pass<KIND>(a, stream);
+    if (e != hipSuccess) return e;
+    const int nb = norm_blocks(a.npieces);
+    hipLaunchKernelGGL(grad_scale_kernel<KIND>, dim3(nb), dim3(kNT), 0, stream, a, nb, max_norm, flat, out);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(const TensorSetArgs& a, int kind, float* out_norm, float* out_each, hipStream_t stream) {
+    return kind == IQLH_NORM_L2 ? norm_launch<IQLH_NORM_L2>(a, out_norm, out_each, stream)
+                                : norm_launch<IQLH_NORM_MAX>(a, out_norm, out_each, stream);
+}
+
+hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, float max_norm, float* flat, float* out,
+                            hipStream_t stream) {
+    return kind == IQLH_NORM_L2 ? clip_launch<IQLH_NORM_L2>(a, max_norm, flat, out, stream)
+                                : clip_launch<IQLH_NORM_MAX>(a, max_norm, flat, out, stream);
+}
+
+}  // namespace iqlh
