@@ -540,6 +540,77 @@ int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, fl
 int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, float* out_flat,
                    float* out, int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit matrices (the MXFP4 format of the OCP Microscaling
+ * Formats specification v1.0): blocks of 32 consecutive elements of a row
+ * share one power-of-two scale (E8M0, 2^(byte - 127), 255 = NaN), and each
+ * element is a 4-bit E2M1 number: sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6.  4.25
+ * bits per element.
+ *
+ *   codes   device [rows][kb * 16] bytes, kb = ceil(cols / 32), 16-byte
+ *           aligned: element 2j of a row in the low half of byte j, 2j + 1 in
+ *           the high half; the elements behind cols in the last block are 0.
+ *   scales  device [rows][kb] bytes.
+ * 1 <= rows, cols <= 2^30. */
+typedef struct iqlh_mx4 {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows;
+    int64_t cols;
+} iqlh_mx4;
+
+/* Quantises a float matrix.  Per block, with a = the largest |x|:
+ *   scale = 2^(floor(log2 a) - 2), at least 2^-127 (which all-zero blocks
+ *   take); code = x / scale rounded to the nearest E2M1 number, ties to the
+ *   even one, |.| above 6 to 6 (a / scale < 8).
+ * A block with a NaN or an infinity gets the NaN scale and zero codes: every
+ * element of it reads back as NaN, and so does every product it enters.
+ *   x          device, `dtype` (IQLH_F32, IQLH_BF16, IQLH_F16), aligned to its
+ *              element.
+ *   transposed 0: x is [out->rows][ld], ld >= out->cols, blocks along x's
+ *              rows.  1: x is [out->cols][ld], ld >= out->rows, and the
+ *              transpose is quantised: blocks along x's columns (the operand
+ *              of a product that sums over x's rows). */
+int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transposed, const iqlh_mx4* out,
+                      void* stream);
+
+/* out[r][c] = value of element (r, c), rounded once to `dtype` (exact in
+ * binary32); ld >= q->cols. */
+int iqlh_mx4_dequantize(const iqlh_mx4* q, void* out, int32_t dtype, int64_t ld, void* stream);
+
+/* out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]), a [M, K] and b [N, K]
+ * (a->cols == b->cols): products exact, sums in binary32, one rounding to
+ * out_dtype.
+ *   bias   device [N] f32, or NULL (0).
+ *   relu   0: act is the identity; 1: max(., 0) (a NaN stays).
+ *   out    device [M][ld_out], ld_out >= N; must not overlap an operand.
+ *   workspace  device, >= iqlh_mx4_workspace_bytes(M, N, K), 16-byte
+ *          aligned, no initial contents required; calls that overlap in time
+ *          need one each.
+ * iqlh_mx4_linear: the same with a = x [M][ld] quantised on the way (as
+ * iqlh_mx4_quantize does, bit for bit the same result). */
+int iqlh_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int iqlh_mx4_matmul(const iqlh_mx4* a, const iqlh_mx4* b, const float* bias, int32_t relu, void* out,
+                    int32_t out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,
+                    void* stream);
+int iqlh_mx4_linear(const void* x, int32_t dtype, int64_t ld, int64_t M, const iqlh_mx4* b,
+                    const float* bias, int32_t relu, void* out, int32_t out_dtype, int64_t ld_out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* iql_forward_values with the two hidden layers' operands in 4 bits: states,
+ * W1, h1 and W2 quantised as above along the summed axis, biases, w3 and b3 and
+ * all sums in binary32:
+ *   h1 = relu(q(s) q(W1)^T + b1), h2 = relu(q(h1) q(W2)^T + b2), V = w3 . h2 + b3.
+ * For large replay batches, where V's few-percent 4-bit error is accepted.
+ * The current parameters are quantised in every call.  Arguments as iql_forward_values;
+ *   workspace  device, >= iql_forward_values_mx4_workspace_bytes(h, batch),
+ *              16-byte aligned, no initial contents required. */
+int iql_forward_values_mx4_workspace_bytes(iql_handle h, int32_t batch, size_t* bytes);
+int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states_dtype, int64_t states_ld,
+                           int32_t batch, float* out_v, const float* rewards, const float* dones,
+                           float gamma, float* out_target, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
 /* Thread-local text of the last error returned on this thread ("" if none). */
 const char* iqlh_last_error(void);
 

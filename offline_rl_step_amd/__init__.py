@@ -79,6 +79,10 @@ class TensorSetStruct(ctypes.Structure):
                 ("pieces", _i32), ("overlap", _i32), ("reserved0", _i32)]
 
 
+class Mx4Struct(ctypes.Structure):
+    _fields_ = [("codes", _p), ("scales", _p), ("rows", _i64), ("cols", _i64)]
+
+
 def _sig(name, res, args):
     fn = getattr(_lib, name)
     fn.restype = res
@@ -137,6 +141,17 @@ _lib_grad_norm = _sig("iqlh_grad_norm", _i32, [ctypes.POINTER(TensorSetStruct), 
                                                ctypes.c_size_t, _p])
 _lib_grad_clip = _sig("iqlh_grad_clip", _i32, [ctypes.POINTER(TensorSetStruct), _i32, _f, _p, _p, _p, _p,
                                                ctypes.c_size_t, _p])
+_lib_mx4_quantize = _sig("iqlh_mx4_quantize", _i32, [_p, _i32, _i64, _i32, ctypes.POINTER(Mx4Struct), _p])
+_lib_mx4_dequantize = _sig("iqlh_mx4_dequantize", _i32, [ctypes.POINTER(Mx4Struct), _p, _i32, _i64, _p])
+_lib_mx4_ws = _sig("iqlh_mx4_workspace_bytes", _i32, [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)])
+_lib_mx4_matmul = _sig("iqlh_mx4_matmul", _i32, [ctypes.POINTER(Mx4Struct), ctypes.POINTER(Mx4Struct), _p, _i32, _p,
+                                                 _i32, _i64, _p, ctypes.c_size_t, _p])
+_lib_mx4_linear = _sig("iqlh_mx4_linear", _i32, [_p, _i32, _i64, _i64, ctypes.POINTER(Mx4Struct), _p, _i32, _p, _i32,
+                                                 _i64, _p, ctypes.c_size_t, _p])
+_lib_forward_mx4_ws = _sig("iql_forward_values_mx4_workspace_bytes", _i32, [_p, _i32,
+                                                                            ctypes.POINTER(ctypes.c_size_t)])
+_lib_forward_mx4 = _sig("iql_forward_values_mx4", _i32, [_p, _p, _i32, _i64, _i32, _p, _p, _p, _f, _p, _p,
+                                                         ctypes.c_size_t, _p])
 _lib_last_error = _sig("iqlh_last_error", ctypes.c_char_p, [])
 
 
@@ -444,6 +459,116 @@ def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None,
            "iqlh_grad_clip")
 
 
+# --------------------------------------------- microscaled 4-bit matrices
+class Mx4:
+    """A matrix [rows, cols] in blocks of 32 elements along its rows: `codes`
+    uint8 [rows, kb * 16] and `scales` uint8 [rows, kb], kb = ceil(cols / 32),
+    both contiguous on one device."""
+
+    def __init__(self, codes, scales, rows, cols):
+        kb = -(-cols // 32)
+        _need(codes.dtype == torch.uint8 and codes.is_contiguous() and codes.numel() == rows * kb * 16,
+              f"codes must be contiguous uint8 of {rows} x {kb * 16}")
+        _need(scales.dtype == torch.uint8 and scales.is_contiguous() and scales.numel() == rows * kb
+              and scales.device == codes.device, f"scales must be contiguous uint8 of {rows} x {kb} beside the codes")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.struct = Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def mx4_empty(rows, cols, axis=1, device=None):
+    """An Mx4 for mx4_quantize(x, .., axis) of x [rows, cols]; with axis 0 it
+    holds the transpose, [cols, rows]."""
+    _need(axis in (0, 1), "axis must be 0 or 1")
+    if axis == 0:
+        rows, cols = cols, rows
+    kb = -(-cols // 32)
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return Mx4(torch.empty((rows, kb * 16), dtype=torch.uint8, device=device),
+               torch.empty((rows, kb), dtype=torch.uint8, device=device), rows, cols)
+
+
+def _matrix(t, rows, cols, device, what):
+    """(dtype code, row stride) of a [rows, cols] tensor with unit column stride."""
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols and t.device == device,
+          f"{what} must be [{rows}, {cols}] on {device}, is {list(t.shape)} on {t.device}")
+    _need((cols == 1 or t.stride(1) == 1) and (rows == 1 or t.stride(0) >= cols),
+          f"{what} must have neighbouring columns and rows that do not overlap")
+    return _float_code(t, what), cols if rows == 1 else t.stride(0)
+
+
+def mx4_quantize(x, out, axis=1, stream=None):
+    """Quantises x [rows, cols] (float32, bfloat16, float16; rows may be
+    strided) in blocks along its rows (axis=1) or, transposed, its columns
+    (axis=0) into the Mx4 `out`."""
+    _need(axis in (0, 1), "axis must be 0 or 1")
+    _need_current(out.device)
+    r, c = (out.rows, out.cols) if axis == 1 else (out.cols, out.rows)
+    dt, ld = _matrix(x, r, c, out.device, "x")
+    _check(_lib_mx4_quantize(_ptr(x), dt, ld, 1 - axis, ctypes.byref(out.struct), _stream(stream)),
+           "iqlh_mx4_quantize")
+
+
+def mx4_dequantize(q, out, stream=None):
+    """Values of q into out [rows, cols] (float32, bfloat16, float16)."""
+    _need_current(q.device)
+    dt, ld = _matrix(out, q.rows, q.cols, q.device, "out")
+    _check(_lib_mx4_dequantize(ctypes.byref(q.struct), _ptr(out), dt, ld, _stream(stream)), "iqlh_mx4_dequantize")
+
+
+def mx4_matmul_workspace(m, n, k, device=None):
+    """A workspace for mx4_matmul / mx4_linear calls of these sizes."""
+    out = ctypes.c_size_t()
+    _check(_lib_mx4_ws(m, n, k, ctypes.byref(out)), "iqlh_mx4_workspace_bytes")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return torch.empty(out.value, dtype=torch.uint8, device=device)
+
+
+def _need_product(rows, b, out, workspace, bias):
+    _need_current(b.device)
+    _need_aux(b.device, workspace, None)
+    if bias is not None:
+        _need_f32(bias, b.rows, b.device, "bias")
+    return _matrix(out, rows, b.rows, b.device, "out")
+
+
+def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
+    """out[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]) of two Mx4."""
+    _need(a.device == b.device, f"a is on {a.device}, b on {b.device}")
+    dt, ld = _need_product(a.rows, b, out, workspace, bias)
+    _check(_lib_mx4_matmul(ctypes.byref(a.struct), ctypes.byref(b.struct), _ptr(bias), int(relu), _ptr(out), dt, ld,
+                           _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "iqlh_mx4_matmul")
+
+
+def mx4_linear(x, b, out, workspace, bias=None, relu=False, stream=None):
+    """mx4_matmul with a = x [m, k] (float32, bfloat16, float16) quantised on the way."""
+    dt, ld = _need_product(x.shape[0], b, out, workspace, bias)
+    xdt, xld = _matrix(x, x.shape[0], b.cols, b.device, "x")
+    _check(_lib_mx4_linear(_ptr(x), xdt, xld, x.shape[0], ctypes.byref(b.struct), _ptr(bias), int(relu), _ptr(out),
+                           dt, ld, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "iqlh_mx4_linear")
+
+
+def iql_forward_values_mx4_workspace(h, batch):
+    out = ctypes.c_size_t()
+    _check(_lib_forward_mx4_ws(h, batch, ctypes.byref(out)), "iql_forward_values_mx4_workspace_bytes")
+    return torch.empty(out.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+
+
+def iql_forward_values_mx4(h, next_states, batch, out_v, workspace, rewards=None, dones=None, gamma=0.99,
+                           out_target=None, states_ld=None, stream=None):
+    """iql_forward_values with both hidden layers' operands in 4 bits."""
+    _need(next_states.dtype in (torch.float32, torch.bfloat16), "next_states must be float32 or bfloat16")
+    ld = states_ld if states_ld is not None else next_states.stride(0)
+    _check(_lib_forward_mx4(h, _ptr(next_states), _DTYPES[next_states.dtype], ld, batch, _ptr(out_v), _ptr(rewards),
+                            _ptr(dones), gamma, _ptr(out_target), _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), _stream(stream)), "iql_forward_values_mx4")
+
+
 # ------------------------------------------------------------------- HER
 def her_relabel(cfg, buf, source_idx, n, seed, d_step, out, stream=None):
     """cfg: HerConfig, buf: HerBuffer, out: HerOut (device addresses filled in)."""
@@ -615,6 +740,14 @@ class IqlTrainer:
     def forward_values(self, next_states, batch, out_v, rewards=None, dones=None, gamma=0.99, out_target=None,
                        states_ld=None, stream=None):
         iql_forward_values(self.h, next_states, batch, out_v, rewards, dones, gamma, out_target, states_ld, stream)
+
+    def forward_values_mx4_workspace(self, batch):
+        return iql_forward_values_mx4_workspace(self.h, batch)
+
+    def forward_values_mx4(self, next_states, batch, out_v, workspace, rewards=None, dones=None, gamma=0.99,
+                           out_target=None, states_ld=None, stream=None):
+        iql_forward_values_mx4(self.h, next_states, batch, out_v, workspace, rewards, dones, gamma, out_target,
+                               states_ld, stream)
 
     def target_ema_update(self, tau, stream=None):
         iql_target_ema_update(self.h, tau, stream)

@@ -350,9 +350,9 @@ int iql_set_state(iql_handle h, int32_t group, const float* d_params, const floa
     return IQLH_OK;
 }
 
-int iql_forward_values(iql_handle h, const void* next_states, int32_t states_dtype, int64_t states_ld, int32_t batch,
-                       float* out_v, const float* rewards, const float* dones, float gamma, float* out_target,
-                       void* stream) {
+static int check_forward_values(iql_handle h, const void* next_states, int32_t states_dtype, int64_t states_ld,
+                                int32_t batch, const float* out_v, const float* rewards, const float* dones,
+                                float gamma, const float* out_target) {
     if (!h) return fail(IQLH_EINVAL, "handle is NULL");
     if (!next_states || !out_v) return fail(IQLH_EINVAL, "next_states and out_v must be non-NULL");
     if (batch < 1 || batch > h->cfg.max_batch)
@@ -364,6 +364,15 @@ int iql_forward_values(iql_handle h, const void* next_states, int32_t states_dty
         return fail(IQLH_EINVAL, "rewards and out_target go together");
     if (dones && !rewards) return fail(IQLH_EINVAL, "dones without rewards");
     if (!std::isfinite(gamma)) return fail(IQLH_EINVAL, "gamma must be finite");
+    return IQLH_OK;
+}
+
+int iql_forward_values(iql_handle h, const void* next_states, int32_t states_dtype, int64_t states_ld, int32_t batch,
+                       float* out_v, const float* rewards, const float* dones, float gamma, float* out_target,
+                       void* stream) {
+    int rc = check_forward_values(h, next_states, states_dtype, states_ld, batch, out_v, rewards, dones, gamma,
+                                  out_target);
+    if (rc) return rc;
     const IqlDims& d = h->dims;
     hipStream_t s = (hipStream_t)stream;
     const void* x = next_states;
@@ -380,6 +389,32 @@ int iql_forward_values(iql_handle h, const void* next_states, int32_t states_dty
     ValueOut vo{out_v, rewards, dones, gamma, out_target};
     hipError_t e = launch_iql_forward_values(d, h->buf, x, ld, batch, vo, s);
     if (e != hipSuccess) return hip_fail(e, "iql_forward_values launch");
+    return IQLH_OK;
+}
+
+int iql_forward_values_mx4_workspace_bytes(iql_handle h, int32_t batch, size_t* bytes) {
+    if (!h || !bytes) return fail(IQLH_EINVAL, "iql_forward_values_mx4_workspace_bytes: NULL argument");
+    if (batch < 1 || batch > h->cfg.max_batch)
+        return fail(IQLH_EINVAL, "batch %d outside [1, max_batch=%d]", batch, h->cfg.max_batch);
+    *bytes = iql_mx4_workspace_bytes(h->dims, batch);
+    return IQLH_OK;
+}
+
+int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states_dtype, int64_t states_ld,
+                           int32_t batch, float* out_v, const float* rewards, const float* dones, float gamma,
+                           float* out_target, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_forward_values(h, next_states, states_dtype, states_ld, batch, out_v, rewards, dones, gamma,
+                                  out_target);
+    if (rc) return rc;
+    const size_t need = iql_mx4_workspace_bytes(h->dims, batch);
+    if (!workspace || ((uintptr_t)workspace & 15u))
+        return fail(IQLH_EINVAL, "iql_forward_values_mx4: workspace NULL or not 16-byte aligned");
+    if (workspace_bytes < need)
+        return fail(IQLH_EINVAL, "iql_forward_values_mx4: workspace too small: %zu < %zu", workspace_bytes, need);
+    ValueOut vo{out_v, rewards, dones, gamma, out_target};
+    hipError_t e = launch_iql_mx4_forward(h->dims, h->buf, next_states, states_dtype, states_ld, batch, vo, workspace,
+                                          (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iql_forward_values_mx4 launch");
     return IQLH_OK;
 }
 
@@ -643,6 +678,111 @@ int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, flo
         return fail(IQLH_EINVAL, "iqlh_grad_clip: tensors that share memory cannot be clipped in place");
     hipError_t e = launch_grad_clip(a, kind, max_norm, out_flat, out, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_grad_clip launch");
+    return IQLH_OK;
+}
+
+// ------------------------------------------- microscaled 4-bit matrices
+static int check_mx4(const char* who, const char* what, const iqlh_mx4* q, Mx4Mat* m) {
+    if (!q || !q->codes || !q->scales) return fail(IQLH_EINVAL, "%s: %s is NULL", who, what);
+    const int64_t top = (int64_t)1 << 30;
+    if (q->rows < 1 || q->rows > top || q->cols < 1 || q->cols > top)
+        return fail(IQLH_EINVAL, "%s: %s of %lld x %lld, sizes must be in [1, 2^30]", who, what, (long long)q->rows,
+                    (long long)q->cols);
+    if ((uintptr_t)q->codes & 15u) return fail(IQLH_EINVAL, "%s: %s codes not 16-byte aligned", who, what);
+    *m = Mx4Mat{q->codes, q->scales, q->rows, q->cols};
+    return IQLH_OK;
+}
+
+static int check_float_matrix(const char* who, const void* x, int32_t dtype, int64_t ld, int64_t cols) {
+    if (!x) return fail(IQLH_EINVAL, "%s: NULL matrix", who);
+    const int es = dtype_bytes(dtype);
+    if (!es) return fail(IQLH_EINVAL, "%s: dtype %d is no float type", who, dtype);
+    if ((uintptr_t)x % es) return fail(IQLH_EINVAL, "%s: matrix not aligned to its element", who);
+    if (ld < cols || ld > (int64_t)1 << 40) return fail(IQLH_EINVAL, "%s: row stride %lld below %lld columns", who,
+                                                        (long long)ld, (long long)cols);
+    return IQLH_OK;
+}
+
+int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transposed, const iqlh_mx4* out,
+                      void* stream) {
+    Mx4Mat q;
+    int rc = check_mx4("iqlh_mx4_quantize", "out", out, &q);
+    if (rc) return rc;
+    if (transposed != 0 && transposed != 1) return fail(IQLH_EINVAL, "iqlh_mx4_quantize: transposed must be 0 or 1");
+    rc = check_float_matrix("iqlh_mx4_quantize", x, dtype, ld, transposed ? q.rows : q.cols);
+    if (rc) return rc;
+    hipError_t e = launch_mx4_quantize(x, dtype, ld, transposed != 0, q, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_quantize launch");
+    return IQLH_OK;
+}
+
+int iqlh_mx4_dequantize(const iqlh_mx4* in, void* out, int32_t dtype, int64_t ld, void* stream) {
+    Mx4Mat q;
+    int rc = check_mx4("iqlh_mx4_dequantize", "q", in, &q);
+    if (rc) return rc;
+    rc = check_float_matrix("iqlh_mx4_dequantize", out, dtype, ld, q.cols);
+    if (rc) return rc;
+    hipError_t e = launch_mx4_dequantize(q, out, dtype, ld, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_dequantize launch");
+    return IQLH_OK;
+}
+
+int iqlh_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return fail(IQLH_EINVAL, "iqlh_mx4_workspace_bytes: bytes is NULL");
+    const int64_t top = (int64_t)1 << 30;
+    if (M < 1 || N < 1 || K < 1 || M > top || N > top || K > top)
+        return fail(IQLH_EINVAL, "iqlh_mx4_workspace_bytes: sizes must be in [1, 2^30]");
+    *bytes = mx4_workspace_bytes(M, N, K);
+    return IQLH_OK;
+}
+
+static int check_mx4_product(const char* who, int64_t M, const Mx4Mat& b, const float* bias, int32_t relu, void* out,
+                             int32_t out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, Mx4Out* o) {
+    int rc = check_float_matrix(who, out, out_dtype, ld_out, b.rows);
+    if (rc) return rc;
+    if (M < 1 || M > (int64_t)1 << 30) return fail(IQLH_EINVAL, "%s: M outside [1, 2^30]", who);
+    if (((M + 15) / 16) * ((b.rows + 15) / 16) > (int64_t)1 << 31)
+        return fail(IQLH_ESHAPE, "%s: %lld x %lld outputs are more than one launch takes", who, (long long)M,
+                    (long long)b.rows);
+    if (relu != 0 && relu != 1) return fail(IQLH_EINVAL, "%s: relu must be 0 or 1", who);
+    const size_t need = mx4_workspace_bytes(M, b.rows, b.cols);
+    if (!workspace || ((uintptr_t)workspace & 15u))
+        return fail(IQLH_EINVAL, "%s: workspace NULL or not 16-byte aligned", who);
+    if (workspace_bytes < need)
+        return fail(IQLH_EINVAL, "%s: workspace too small: %zu < %zu", who, workspace_bytes, need);
+    *o = Mx4Out{out, out_dtype, relu, ld_out, bias};
+    return IQLH_OK;
+}
+
+int iqlh_mx4_matmul(const iqlh_mx4* a, const iqlh_mx4* b, const float* bias, int32_t relu, void* out,
+                    int32_t out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream) {
+    Mx4Mat am, bm;
+    Mx4Out o;
+    int rc = check_mx4("iqlh_mx4_matmul", "a", a, &am);
+    if (!rc) rc = check_mx4("iqlh_mx4_matmul", "b", b, &bm);
+    if (rc) return rc;
+    if (am.cols != bm.cols)
+        return fail(IQLH_EINVAL, "iqlh_mx4_matmul: a has %lld columns, b %lld", (long long)am.cols, (long long)bm.cols);
+    rc = check_mx4_product("iqlh_mx4_matmul", am.rows, bm, bias, relu, out, out_dtype, ld_out, workspace,
+                           workspace_bytes, &o);
+    if (rc) return rc;
+    hipError_t e = launch_mx4_matmul(am, bm, o, workspace, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_matmul launch");
+    return IQLH_OK;
+}
+
+int iqlh_mx4_linear(const void* x, int32_t dtype, int64_t ld, int64_t M, const iqlh_mx4* b, const float* bias,
+                    int32_t relu, void* out, int32_t out_dtype, int64_t ld_out, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    Mx4Mat bm;
+    Mx4Out o;
+    int rc = check_mx4("iqlh_mx4_linear", "b", b, &bm);
+    if (!rc) rc = check_float_matrix("iqlh_mx4_linear", x, dtype, ld, bm.cols);
+    if (!rc) rc = check_mx4_product("iqlh_mx4_linear", M, bm, bias, relu, out, out_dtype, ld_out, workspace,
+                                    workspace_bytes, &o);
+    if (rc) return rc;
+    hipError_t e = launch_mx4_linear(x, dtype, ld, M, bm, o, workspace, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_linear launch");
     return IQLH_OK;
 }
 

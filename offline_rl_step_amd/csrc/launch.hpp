@@ -241,6 +241,35 @@ hipError_t launch_grad_norm(const TensorSetArgs& a, int kind, float* out_norm, f
 hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, float max_norm, float* flat, float* out,
                             hipStream_t stream);
 
+// ------------------------------------------- microscaled 4-bit matrices
+struct Mx4Mat {
+    uint8_t* codes;   // [rows][kb * 16]
+    uint8_t* scales;  // [rows][kb]
+    int64_t rows, cols;
+    __host__ __device__ int64_t kb() const { return (cols + 31) / 32; }
+};
+struct Mx4Out {
+    void* p;
+    int32_t dtype;
+    int32_t relu;
+    int64_t ld;
+    const float* bias;  // or null
+};
+// workspace of a product: the left operand quantised on the way, then the
+// partial sums of a split summed axis
+size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
+                               hipStream_t stream);
+hipError_t launch_mx4_dequantize(const Mx4Mat& q, void* out, int dtype, int64_t ld, hipStream_t stream);
+hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace,
+                             hipStream_t stream);
+hipError_t launch_mx4_linear(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
+                             void* workspace, hipStream_t stream);
+// V(s) with both hidden layers in 4 bits
+size_t iql_mx4_workspace_bytes(const IqlDims& d, int B);
+hipError_t launch_iql_mx4_forward(const IqlDims& d, const IqlBuffers& b, const void* states, int dtype, int64_t ld,
+                                  int B, const ValueOut& vo, void* workspace, hipStream_t stream);
+
 // ------------------------------------------------------- whole step
 // One pass of the hot path in four launches:
 //   A  HER relabelling + budget source norms   (independent of each other)

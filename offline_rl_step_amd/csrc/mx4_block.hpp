@@ -1,0 +1,87 @@
+// Device helpers of the microscaled 4-bit matrices: conversion of one block
+// of 32 elements, and the matrix instruction on blocks.
+#pragma once
+#include "common.hpp"
+#include "iqlher.h"
+
+namespace iqlh {
+
+typedef int mx_i8 __attribute__((ext_vector_type(8)));
+typedef float mx_f4 __attribute__((ext_vector_type(4)));
+
+template <int DT> struct MxFloat;
+template <> struct MxFloat<IQLH_F32> {
+    typedef float type;
+    static IQLH_DEV float get(float x) { return x; }
+    static IQLH_DEV float put(float x) { return x; }
+};
+template <> struct MxFloat<IQLH_BF16> {
+    typedef uint16_t type;
+    static IQLH_DEV float get(uint16_t x) { return bf2f(x); }
+    static IQLH_DEV uint16_t put(float x) { return f2bf(x); }
+};
+template <> struct MxFloat<IQLH_F16> {
+    typedef _Float16 type;
+    static IQLH_DEV float get(_Float16 x) { return (float)x; }
+    static IQLH_DEV _Float16 put(float x) { return (_Float16)x; }
+};
+
+// |x| as its bits: ordered as the values are, infinities and NaN on top
+IQLH_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+IQLH_DEV uint32_t umax2(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The scale byte of a block whose largest |x| has these bits, and the factor
+// 1 / scale (a power of two, exact; 0 for a block that is not finite, whose
+// codes are then forced to 0).  e - 2 = the byte of 2^(floor(log2 a) - 2) for
+// a normal a of biased exponent e; subnormal a have e = 0 and take the
+// smallest scale.
+IQLH_DEV uint32_t mx4_scale(uint32_t amax) {
+    const int e = (int)(amax >> 23) - 2;
+    return amax >= 0x7F800000u ? 255u : (uint32_t)(e < 0 ? 0 : e);
+}
+IQLH_DEV float mx4_inverse(uint32_t scale) { return __uint_as_float((254u - scale) << 23); }  // scale <= 252
+IQLH_DEV float mx4_scale_value(uint32_t scale) {
+    return scale == 0u ? __uint_as_float(0x00400000u) : scale == 255u ? __uint_as_float(0x7FC00000u)
+                                                                     : __uint_as_float(scale << 23);
+}
+
+// Eight values of a block times `inv` as eight codes, the first in the lowest
+// bits.  The conversion instruction rounds to nearest, ties to even, and
+// saturates at 6 (its scale operand is 1: the product with the power of two is
+// exact, subnormals included).
+IQLH_DEV uint32_t mx4_codes8(const float* x, float inv) {
+    uint32_t w = 0u;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0] * inv, x[1] * inv, 1.f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2] * inv, x[3] * inv, 1.f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4] * inv, x[5] * inv, 1.f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6] * inv, x[7] * inv, 1.f, 3);
+    return w;
+}
+
+// The value of a code (sign and 0, .5, 1, 1.5, 2, 3, 4, 6): exponent field
+// c >> 1 over one mantissa bit, the subnormal code 1 being 0.5.
+IQLH_DEV float mx4_value(uint32_t code) {
+    const uint32_t c = code & 7u;
+    const uint32_t mag = c < 2u ? (c ? 0x3F000000u : 0u) : ((c >> 1) + 126u) << 23 | (c & 1u) << 22;
+    return __uint_as_float(mag | (code & 8u) << 28);
+}
+
+// largest of the four lanes 4j .. 4j + 3, in all of them
+IQLH_DEV uint32_t quad_umax(uint32_t v) {
+    v = umax2(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // quad_perm 1,0,3,2
+    v = umax2(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));  // quad_perm 2,3,0,1
+    return v;
+}
+
+// D[i][j] += sum over 128 k of A[i][k] B[j][k], both 16 x 128 in 4 bits with
+// scales: lane l holds row l & 15, block l >> 4 (32 elements, 16 bytes) of
+// each, the scale in byte 0; of D it holds column (l & 15) and rows
+// 4 (l >> 4) + 0..3.  Checked against binary64 sums lane by lane, NaN scales
+// included.
+IQLH_DEV mx_f4 mx4_mma(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) {
+    const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+}  // namespace iqlh

@@ -28,10 +28,11 @@ aw       advantage-weighted policy.
 budget   budgeted clipped-SAXPY gradient accumulation.
 bf16     round-to-nearest-even float32 -> bfloat16 (storage rounding).
 tensors  norm and clip over a list of tensors.
+mx4      microscaled 4-bit quantisation and the value network on it.
 
 Parity status: every function is pinned by tests in ``tests/test_oracle_*.py``
 (closed forms, library special cases, finite differences, brute force and
 hand-worked fixtures); none is "parity unpinned".
 """
 
-from . import philox, her, iql, aw, budget, bf16, tensors  # noqa: F401
+from . import philox, her, iql, aw, budget, bf16, tensors, mx4  # noqa: F401
