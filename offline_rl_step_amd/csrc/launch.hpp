@@ -257,6 +257,8 @@ struct Mx4Out {
 };
 // workspace of a product: the left operand quantised on the way, then the
 // partial sums of a split summed axis
+size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+bool mx4_use_tiles(int64_t M, int64_t N, int64_t K);
 size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream);

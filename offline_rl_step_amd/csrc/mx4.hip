@@ -1,8 +1,5 @@
 // Microscaled 4-bit matrices: quantisation along either axis, the values
-// back, and the product of two of them on the scaled matrix instructions.
-#include <type_traits>
-
-#include "launch.hpp"
+// back, and the product whose left operand is quantised on the way.
 #include "mx4_block.hpp"
 
 namespace iqlh {
@@ -109,68 +106,6 @@ __global__ __launch_bounds__(kNT) void mx4_dequantize_kernel(Mx4Mat q, typename 
     }
 }
 
-// ----------------------------------------------------------------- product
-// One wave per 64 x 64 outputs, four waves 128 x 128.  The instruction's row
-// operand is b: a lane then holds four neighbouring n of one output row.
-template <int DT>
-__global__ __launch_bounds__(kNT) void mx4_matmul_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o, int n_tiles) {
-    typedef typename MxFloat<DT>::type T;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, blk = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * 128 + (wave >> 1) * 64;
-    const int64_t n0 = (int64_t)(blockIdx.x % n_tiles) * 128 + (wave & 1) * 64;
-    const int64_t kb = a.kb();
-    int64_t arow[4], brow[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + r, n = n0 + 16 * i + r;
-        arow[i] = (m < a.rows ? m : a.rows - 1) * kb;  // rows past the end read the last one; nothing is stored for them
-        brow[i] = (n < b.rows ? n : b.rows - 1) * kb;
-    }
-    mx_f4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k = 0; k < kb; k += 4) {
-        const bool in = k + blk < kb;
-        const int64_t kk = in ? k + blk : 0;
-        uint4 av[4], bv[4];
-        uint32_t as[4], bs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            av[i] = ((const uint4*)a.codes)[arow[i] + kk];
-            as[i] = a.scales[arow[i] + kk];
-            bv[i] = ((const uint4*)b.codes)[brow[i] + kk];
-            bs[i] = b.scales[brow[i] + kk];
-            if (!in) {  // behind the last block: zeros of scale 1
-                av[i] = bv[i] = uint4{0u, 0u, 0u, 0u};
-                as[i] = bs[i] = 127u;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mx4_mma(bv[j], av[i], acc[i][j], bs[j], as[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + r;
-        if (m >= a.rows) continue;
-        T* row = (T*)o.p + m * o.ld;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t n = n0 + 16 * j + 4 * blk + e;
-                if (n >= b.rows) continue;
-                float y = acc[i][j][e] + (o.bias ? o.bias[n] : 0.f);
-                if (o.relu && y < 0.f) y = 0.f;
-                row[n] = MxFloat<DT>::put(y);
-            }
-    }
-}
-
 int capped_blocks(int64_t threads) {
     const int64_t nb = (threads + kNT - 1) / kNT;
     return (int)(nb < 16384 ? nb : 16384);
@@ -203,24 +138,16 @@ hipError_t launch_mx4_dequantize(const Mx4Mat& q, void* out, int dtype, int64_t 
 
 size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const size_t kb = (size_t)(K + 31) / 32;
-    return (size_t)M * kb * 16 + ((size_t)M * kb + 15) / 16 * 16;
-}
-
-hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace,
-                             hipStream_t stream) {
-    const int64_t mt = (a.rows + 127) / 128, nt = (b.rows + 127) / 128;
-    return by_dtype(out.dtype, [&](auto dt) {
-        hipLaunchKernelGGL(mx4_matmul_kernel<decltype(dt)::value>, dim3((uint32_t)(mt * nt)), dim3(kNT), 0, stream, a,
-                           b, out, (int)nt);
-    });
+    return (size_t)M * kb * 16 + ((size_t)M * kb + 15) / 16 * 16 + mx4_matmul_workspace_bytes(M, N, K);
 }
 
 hipError_t launch_mx4_linear(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                              void* workspace, hipStream_t stream) {
-    const Mx4Mat a{(uint8_t*)workspace, (uint8_t*)workspace + M * b.kb() * 16, M, b.cols};
+    const int64_t blocks = M * b.kb();
+    const Mx4Mat a{(uint8_t*)workspace, (uint8_t*)workspace + blocks * 16, M, b.cols};
     hipError_t e = launch_mx4_quantize(x, dtype, ld, false, a, stream);
     if (e != hipSuccess) return e;
-    return launch_mx4_matmul(a, b, out, workspace, stream);
+    return launch_mx4_matmul(a, b, out, (uint8_t*)workspace + blocks * 16 + (blocks + 15) / 16 * 16, stream);
 }
 
 }  // namespace iqlh

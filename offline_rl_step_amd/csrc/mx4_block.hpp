@@ -1,8 +1,12 @@
 // Device helpers of the microscaled 4-bit matrices: conversion of one block
 // of 32 elements, and the matrix instruction on blocks.
 #pragma once
+#include <type_traits>
+#include <utility>
+
 #include "common.hpp"
 #include "iqlher.h"
+#include "launch.hpp"
 
 namespace iqlh {
 
@@ -82,6 +86,59 @@ IQLH_DEV mx_f4 mx4_mma(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) {
     const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// The same with the scales in byte OA of sa and byte OB of sb.
+template <int OA, int OB>
+IQLH_DEV mx_f4 mx4_mma_sel(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) {
+    const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, OA, (int)sa, OB, (int)sb);
+}
+
+// f(std::integral_constant<int, 0>) .. f(<N - 1>)
+template <class F, int... I>
+IQLH_DEV void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+IQLH_DEV void static_for(F&& f) {
+    static_for_impl(f, std::make_integer_sequence<int, N>());
+}
+
+// Four neighbouring outputs of a row, n .. n + 3, the first `count` of them
+// inside the matrix: bias, activation, one rounding.  `wide`: the row allows a
+// store of all four at once.
+template <int DT>
+IQLH_DEV void mx4_store4(const Mx4Out& o, int64_t m, int64_t n, int count, mx_f4 acc, bool wide) {
+    typedef typename MxFloat<DT>::type T;
+    if (count <= 0) return;
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        y[e] = acc[e] + (o.bias && e < count ? o.bias[n + e] : 0.f);
+        if (o.relu && y[e] < 0.f) y[e] = 0.f;  // a NaN stays
+    }
+    T* p = (T*)o.p + m * o.ld + n;
+    if (wide && count >= 4) {
+        if constexpr (DT == IQLH_F32) {
+            *(float4*)p = float4{y[0], y[1], y[2], y[3]};
+        } else if constexpr (DT == IQLH_BF16) {
+            *(uint2*)p = uint2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+        } else {
+            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+            *(h4*)p = h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < count) p[e] = MxFloat<DT>::put(y[e]);
+    }
+}
+// whether every row of the output starts on a boundary of four elements
+template <int DT>
+IQLH_DEV bool mx4_wide_rows(const Mx4Out& o) {
+    return ((uintptr_t)o.p % (4 * sizeof(typename MxFloat<DT>::type))) == 0 && o.ld % 4 == 0;
 }
 
 }  // namespace iqlh

@@ -189,6 +189,44 @@ def test_product_exact_on_the_grid(m, mnk):
                 assert torch.all(buf[:, N:] == 77.0)
 
 
+@pytest.mark.parametrize("mnk", [(2900, 2950, 1056), (2817, 3000, 1500), (8200, 1030, 1024), (1000, 9000, 2100),
+                                 (33000, 250, 1024), (4096, 4096, 4096)])
+def test_large_products_exact_on_the_grid(m, mnk):
+    """Products of many tiles, ragged in each size: equality with the oracle
+    at the matrix's corners, edges and a sample of rows, and of all rows with a
+    second product (sums of each row against a vector of ones)."""
+    import torch
+    M, N, K = mnk
+    g = np.random.default_rng(M + N + K)
+    a, b = _grid(g, M, K), _grid(g, N, K)
+    aq, bq = _operand(m, a), _operand(m, b)
+    bias = g.integers(-40, 40, N) * 0.25
+    tb = torch.from_numpy(bias.astype(np.float32)).to(dev())
+    ws = m.mx4_matmul_workspace(M, N, K)
+    rows = np.unique(np.concatenate([[0, 1, 127, 128, 255, 256, M - 257, M - 2, M - 1], g.integers(0, M, 200)]))
+    want = torch.from_numpy(a[rows] @ b.T).to(dev())
+    total = torch.from_numpy(a @ b.sum(0)).to(dev())
+    tr = torch.from_numpy(rows).to(dev())
+    for od, use_bias, relu, pad in (("float32", False, False, 0), ("bfloat16", True, True, 4), ("float16", False, True, 7),
+                                    ("float32", True, False, 1)):
+        buf = torch.full((M, N + pad), 77.0, dtype=_t(od), device=dev())
+        ws.fill_(0xFF)
+        m.mx4_matmul(aq, bq, buf[:, :N], ws, bias=tb if use_bias else None, relu=relu)
+        w = want + (tb.double() if use_bias else 0.0)
+        w = w.clamp(min=0) if relu else w
+        sync()
+        assert torch.equal(buf[tr, :N], w.float().to(_t(od))), (od, use_bias, relu)
+        assert torch.all(buf[:, N:] == 77.0)
+        if od == "float32" and not use_bias:
+            assert torch.equal(buf[:, :N].double().sum(1), total)
+        x = _float(a, "bfloat16", lead=1, pad=1)
+        other = torch.full_like(buf, 77.0)
+        ws.fill_(0xFF)
+        m.mx4_linear(x, bq, other[:, :N], ws, bias=tb if use_bias else None, relu=relu)
+        sync()
+        assert torch.equal(other, buf)
+
+
 @pytest.mark.parametrize("od", DTYPES)
 @pytest.mark.parametrize("mnk", [(1, 1000, 1000), (9, 300, 2000), (200, 130, 555), (600, 512, 256)])
 def test_product_of_wide_ranging_values(m, mnk, od):
