@@ -17,70 +17,132 @@ hipError_t by_dtype(int dtype, F f) {
 }
 
 // ------------------------------------------------------------ quantisation
-// Blocks along x's rows.  A thread converts 8 elements (one dword of codes),
-// four neighbouring lanes a block; the groups of 8 are numbered over the
-// padded matrix.
+// Eight neighbouring elements at p, which is aligned to its element only (the
+// hardware takes 16-byte loads at any address).  count < 8: the rest are 0.
+template <int DT>
+IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
+    typedef typename MxFloat<DT>::type T;
+    if (count >= 8) {
+        if constexpr (DT == IQLH_F32) {
+            typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+            const f4u a = *(const f4u*)p, b = *(const f4u*)(p + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = a[j];
+                v[4 + j] = b[j];
+            }
+        } else {
+            typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
+            const t8u a = *(const t8u*)p;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = MxFloat<DT>::get(a[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < count ? MxFloat<DT>::get(p[j]) : 0.f;
+    }
+}
+
+constexpr int kQRows = 4;  // rows (times the workgroup's) a thread converts
+
+// Blocks along x's rows.  HBM-bound.  A thread converts 8 elements (one dword
+// of codes) of kQRows rows, all loaded before the first is used; four
+// neighbouring lanes share a block.  A workgroup is 2^c_log groups of 8 wide
+// and 256 / 2^c_log rows high.
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloat<DT>::type* __restrict__ x, int64_t ld,
-                                                           Mx4Mat q) {
+                                                           Mx4Mat q, int c_log, int col_tiles) {
     const int64_t gpr = q.kb() * 4;  // groups per row
-    const int64_t ngroups = q.rows * gpr;
-    for (int64_t g = (int64_t)blockIdx.x * kNT + threadIdx.x; g < (ngroups + 63) / 64 * 64;
-         g += (int64_t)gridDim.x * kNT) {
-        const bool in = g < ngroups;
-        const int64_t row = in ? g / gpr : 0;
-        const int64_t c0 = (in ? g - row * gpr : 0) * 8;
-        const typename MxFloat<DT>::type* p = x + row * ld;
-        float v[8];
+    const int rows_high = kNT >> c_log;
+    const int64_t g = ((int64_t)(blockIdx.x % col_tiles) << c_log) + (threadIdx.x & ((1 << c_log) - 1));
+    const int64_t row0 = (int64_t)(blockIdx.x / col_tiles) * rows_high * kQRows + (threadIdx.x >> c_log);
+    const int count = (int)(q.cols - g * 8 < 8 ? q.cols - g * 8 : 8);
+    float v[kQRows][8];
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+        const int64_t row = row0 + i * rows_high;
+        load8<DT>(x + (row < q.rows ? row : q.rows - 1) * ld + g * 8, g < gpr ? count : 0, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+        const int64_t row = row0 + i * rows_high;
         uint32_t amax = 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bool ok = in && c0 + j < q.cols;
-            v[j] = ok ? MxFloat<DT>::get(p[c0 + j]) : 0.f;
-            amax = umax2(amax, abs_bits(v[j]));
-        }
-        amax = quad_umax(amax);
-        const uint32_t s = mx4_scale(amax);
-        const uint32_t w = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
-        if (in) {
-            ((uint32_t*)q.codes)[g] = w;
-            if ((g & 3) == 0) q.scales[g >> 2] = (uint8_t)s;
+        for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[i][j]));
+        const uint32_t s = mx4_scale(quad_umax(amax));
+        const uint32_t w = s == 255u ? 0u : mx4_codes8(v[i], mx4_inverse(s));
+        if (row < q.rows && g < gpr) {
+            ((uint32_t*)q.codes)[row * gpr + g] = w;
+            if ((g & 3) == 0) q.scales[(row * gpr + g) >> 2] = (uint8_t)s;
         }
     }
 }
 
-// Blocks along x's columns: x is [q.cols][ld].  A workgroup takes 64 columns
-// of x (rows of q) and 256 of its rows: a lane reads its column, 32 rows a
-// block, neighbouring lanes neighbouring addresses; the codes pass through LDS
-// so that a row of q is written 128 bytes at a time.
+// Blocks along x's columns: x is [q.cols][ld].  HBM-bound.  A lane takes one
+// column of x (16-bit types: two neighbouring ones, a dword per load), 32 rows a
+// block, neighbouring lanes neighbouring addresses; a workgroup 64 (128) columns
+// and 256 rows.  The codes pass through LDS so that a row of q is written 128
+// bytes at a time.
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typename MxFloat<DT>::type* __restrict__ x,
                                                                    int64_t ld, Mx4Mat q, int row_tiles) {
-    __shared__ uint4 codes[64][9];  // 9: lanes of a store to one block column fall on different banks
-    __shared__ uint8_t scales[64][8];
+    typedef typename MxFloat<DT>::type T;
+    constexpr int CPL = DT == IQLH_F32 ? 1 : 2;
+    __shared__ uint4 codes[64 * CPL][9];  // 9: the lanes of a store to one block column fall on different banks
+    __shared__ uint8_t scales[64 * CPL][8];
     const int64_t kb = q.kb();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * 64, b0 = (int64_t)(blockIdx.x / row_tiles) * 8;
-    const int64_t r = r0 + lane;
-    for (int i = wave; i < 8; i += 4) {
-        const int64_t k0 = (b0 + i) * 32;
-        float v[32];
-        uint32_t amax = 0u;
+    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * (64 * CPL), b0 = (int64_t)(blockIdx.x / row_tiles) * 8;
+    const int64_t r = r0 + lane * CPL;
+    const int64_t rc = CPL > 1 || r < q.rows ? r : q.rows - 1;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const bool ok = r < q.rows && k0 + j < q.cols;
-            v[j] = ok ? MxFloat<DT>::get(x[(k0 + j) * ld + r]) : 0.f;
-            amax = umax2(amax, abs_bits(v[j]));
+    for (int half = 0; half < 2; ++half) {
+        const int i = wave + 4 * half;
+        const int64_t k0 = (b0 + i) * 32;
+        float v[CPL][32];
+        if (b0 + i < kb) {
+            if (CPL == 1 || r + CPL <= q.rows) {
+                // loads at clamped rows, those behind the last one masked: no branch between them
+                const int left = (int)(q.cols - k0 < 32 ? q.cols - k0 : 32);
+                const T* p = x + k0 * ld + rc;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const T* pj = p + (j < left ? j : 0) * ld;
+                    if constexpr (CPL == 1) {
+                        v[0][j] = keep_if(j < left, (float)*pj);
+                    } else {
+                        typedef T t2u __attribute__((ext_vector_type(2), aligned(2)));
+                        const t2u w = *(const t2u*)pj;
+                        v[0][j] = keep_if(j < left, MxFloat<DT>::get(w[0]));
+                        v[1][j] = keep_if(j < left, MxFloat<DT>::get(w[1]));
+                    }
+                }
+            } else {  // the last of an odd number of columns, and lanes past it
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+#pragma unroll
+                    for (int c = 0; c < CPL; ++c)
+                        v[c][j] = r + c < q.rows && k0 + j < q.cols ? MxFloat<DT>::get(x[(k0 + j) * ld + r + c]) : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                uint32_t amax = 0u;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[c][j]));
+                const uint32_t s = mx4_scale(amax);
+                uint4 w{0u, 0u, 0u, 0u};
+                if (s != 255u) {
+                    const float inv = mx4_inverse(s);
+                    w = uint4{mx4_codes8(v[c], inv), mx4_codes8(v[c] + 8, inv), mx4_codes8(v[c] + 16, inv),
+                              mx4_codes8(v[c] + 24, inv)};
+                }
+                codes[lane * CPL + c][i] = w;
+                scales[lane * CPL + c][i] = (uint8_t)s;
+            }
         }
-        const uint32_t s = mx4_scale(amax);
-        const float inv = s == 255u ? 0.f : mx4_inverse(s);
-        uint4 w{0u, 0u, 0u, 0u};
-        if (s != 255u) w = uint4{mx4_codes8(v, inv), mx4_codes8(v + 8, inv), mx4_codes8(v + 16, inv), mx4_codes8(v + 24, inv)};
-        codes[lane][i] = w;
-        scales[lane][i] = (uint8_t)s;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 512; e += kNT) {
+    for (int e = threadIdx.x; e < 512 * CPL; e += kNT) {
         const int rr = e >> 3, i = e & 7;
         if (r0 + rr < q.rows && b0 + i < kb) {
             ((uint4*)q.codes)[(r0 + rr) * kb + b0 + i] = codes[rr][i];
@@ -89,26 +151,67 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
     }
 }
 
+// HBM-bound on its stores: a thread writes 16 bytes of kQRows rows, so that
+// neighbouring lanes write neighbouring 16 bytes.
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_dequantize_kernel(Mx4Mat q, typename MxFloat<DT>::type* __restrict__ out,
-                                                             int64_t ld) {
-    const int64_t gpr = q.kb() * 4;
-    const int64_t ngroups = q.rows * gpr;
-    for (int64_t g = (int64_t)blockIdx.x * kNT + threadIdx.x; g < ngroups; g += (int64_t)gridDim.x * kNT) {
-        const int64_t row = g / gpr;
-        const int64_t c0 = (g - row * gpr) * 8;
-        const uint32_t w = ((const uint32_t*)q.codes)[g];
-        const float s = mx4_scale_value(q.scales[g >> 2]);
-        typename MxFloat<DT>::type* p = out + row * ld;
+                                                             int64_t ld, int c_log, int col_tiles) {
+    typedef typename MxFloat<DT>::type T;
+    constexpr int E = 16 / sizeof(T);  // elements a thread converts: a dword of codes or half of one
+    const int rows_high = kNT >> c_log;
+    const int64_t c0 = (((int64_t)(blockIdx.x % col_tiles) << c_log) + (threadIdx.x & ((1 << c_log) - 1))) * E;
+    const int64_t row0 = (int64_t)(blockIdx.x / col_tiles) * rows_high * kQRows + (threadIdx.x >> c_log);
+    if (c0 >= q.cols) return;
+    const int64_t kb = q.kb();
+    uint32_t w[kQRows], s[kQRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j < q.cols) p[c0 + j] = MxFloat<DT>::put(mx4_value(w >> (4 * j)) * s);
+    for (int i = 0; i < kQRows; ++i) {
+        const int64_t row = row0 + i * rows_high < q.rows ? row0 + i * rows_high : q.rows - 1;
+        const uint8_t* p = q.codes + row * kb * 16 + c0 / 2;
+        w[i] = E == 8 ? *(const uint32_t*)p : *(const uint16_t*)p;
+        s[i] = q.scales[row * kb + c0 / 32];
+    }
+#pragma unroll
+    for (int i = 0; i < kQRows; ++i) {
+        const int64_t row = row0 + i * rows_high;
+        if (row >= q.rows) break;
+        const float sc = mx4_scale_value(s[i]);
+        T y[E];
+        static_for<E / 2>([&](auto j) __attribute__((always_inline)) {
+            constexpr int J = decltype(j)::value;
+            const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.f, J);
+            y[2 * J] = MxFloat<DT>::put(v[0] * sc);
+            y[2 * J + 1] = MxFloat<DT>::put(v[1] * sc);
+        });
+        T* p = out + row * ld + c0;
+        if (c0 + E <= q.cols) {
+            typedef T tu __attribute__((ext_vector_type(E), aligned(sizeof(T))));
+            tu o;
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] = y[j];
+            *(tu*)p = o;
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (c0 + j < q.cols) p[j] = y[j];
+        }
     }
 }
 
-int capped_blocks(int64_t threads) {
-    const int64_t nb = (threads + kNT - 1) / kNT;
-    return (int)(nb < 16384 ? nb : 16384);
+// Workgroups of 2^c_log columns (at most 256) for `across` column groups a
+// row, and how many of them the matrix takes.
+struct Shape {
+    int c_log, col_tiles;
+    int64_t blocks;
+};
+Shape shape_for(int64_t rows, int64_t across) {
+    Shape s;
+    s.c_log = 2;
+    while (s.c_log < 8 && ((int64_t)1 << s.c_log) < across) ++s.c_log;
+    s.col_tiles = (int)((across + (1 << s.c_log) - 1) >> s.c_log);
+    const int64_t high = (int64_t)(kNT >> s.c_log) * kQRows;
+    s.blocks = (rows + high - 1) / high * s.col_tiles;
+    return s;
 }
 
 }  // namespace
@@ -116,23 +219,28 @@ int capped_blocks(int64_t threads) {
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream) {
     return by_dtype(dtype, [&](auto dt) {
-        typedef typename MxFloat<decltype(dt)::value>::type T;
+        constexpr int DT = decltype(dt)::value;
+        typedef typename MxFloat<DT>::type T;
         if (transposed) {
-            const int64_t row_tiles = (q.rows + 63) / 64, k_tiles = (q.kb() + 7) / 8;
-            hipLaunchKernelGGL(mx4_quantize_columns_kernel<decltype(dt)::value>, dim3((uint32_t)(row_tiles * k_tiles)),
-                               dim3(kNT), 0, stream, (const T*)x, ld, q, (int)row_tiles);
+            constexpr int cols = DT == IQLH_F32 ? 64 : 128;
+            const int64_t row_tiles = (q.rows + cols - 1) / cols, k_tiles = (q.kb() + 7) / 8;
+            hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)(row_tiles * k_tiles)), dim3(kNT), 0, stream,
+                               (const T*)x, ld, q, (int)row_tiles);
         } else {
-            hipLaunchKernelGGL(mx4_quantize_kernel<decltype(dt)::value>, dim3(capped_blocks(q.rows * q.kb() * 4)),
-                               dim3(kNT), 0, stream, (const T*)x, ld, q);
+            const Shape s = shape_for(q.rows, q.kb() * 4);
+            hipLaunchKernelGGL(mx4_quantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld, q,
+                               s.c_log, s.col_tiles);
         }
     });
 }
 
 hipError_t launch_mx4_dequantize(const Mx4Mat& q, void* out, int dtype, int64_t ld, hipStream_t stream) {
     return by_dtype(dtype, [&](auto dt) {
-        typedef typename MxFloat<decltype(dt)::value>::type T;
-        hipLaunchKernelGGL(mx4_dequantize_kernel<decltype(dt)::value>, dim3(capped_blocks(q.rows * q.kb() * 4)),
-                           dim3(kNT), 0, stream, q, (T*)out, ld);
+        constexpr int DT = decltype(dt)::value;
+        typedef typename MxFloat<DT>::type T;
+        const Shape s = shape_for(q.rows, (q.cols * (int64_t)sizeof(T) + 15) / 16);
+        hipLaunchKernelGGL(mx4_dequantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, q, (T*)out, ld, s.c_log,
+                           s.col_tiles);
     });
 }
 
