@@ -96,6 +96,17 @@ IQLH_DEV mx_f4 mx4_mma_sel(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) 
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, OA, (int)sa, OB, (int)sb);
 }
 
+// D[i][j] += sum over 64 k of A[i][k] B[j][k], both 32 x 64: lane l holds row
+// l & 31, block l >> 5 of each, the scales in bytes OA, OB; of D column l & 31 and
+// the rows 8 (e >> 2) + 4 (l >> 5) + (e & 3).
+typedef float mx_f16 __attribute__((ext_vector_type(16)));
+template <int OA, int OB>
+IQLH_DEV mx_f16 mx4_mma32(uint4 a, uint4 b, mx_f16 c, uint32_t sa, uint32_t sb) {
+    const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, OA, (int)sa, OB, (int)sb);
+}
+
 // f(std::integral_constant<int, 0>) .. f(<N - 1>)
 template <class F, int... I>
 IQLH_DEV void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
@@ -104,6 +115,19 @@ IQLH_DEV void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
 template <int N, class F>
 IQLH_DEV void static_for(F&& f) {
     static_for_impl(f, std::make_integer_sequence<int, N>());
+}
+
+// Four values rounded and stored at once
+template <int DT>
+IQLH_DEV void mx4_put4(typename MxFloat<DT>::type* p, const float* y) {
+    if constexpr (DT == IQLH_F32) {
+        *(float4*)p = float4{y[0], y[1], y[2], y[3]};
+    } else if constexpr (DT == IQLH_BF16) {
+        *(uint2*)p = uint2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+    } else {
+        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        *(h4*)p = h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+    }
 }
 
 // Four neighbouring outputs of a row, n .. n + 3, the first `count` of them
@@ -121,14 +145,7 @@ IQLH_DEV void mx4_store4(const Mx4Out& o, int64_t m, int64_t n, int count, mx_f4
     }
     T* p = (T*)o.p + m * o.ld + n;
     if (wide && count >= 4) {
-        if constexpr (DT == IQLH_F32) {
-            *(float4*)p = float4{y[0], y[1], y[2], y[3]};
-        } else if constexpr (DT == IQLH_BF16) {
-            *(uint2*)p = uint2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
-        } else {
-            typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-            *(h4*)p = h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
-        }
+        mx4_put4<DT>(p, y);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)

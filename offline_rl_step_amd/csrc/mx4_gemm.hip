@@ -18,7 +18,6 @@ namespace iqlh {
 namespace {
 
 constexpr int kNT = 256;
-#define IQLH_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
 template <typename F>
 hipError_t by_dtype(int dtype, F f) {
@@ -146,50 +145,79 @@ __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4
 }
 
 // ------------------------------------------------------- tiles through LDS
-// Scales regrouped for the tile kernel: for 64 rows and 4 blocks of a step one
-// dword per lane, byte i the scale of row 16 i + (lane & 15), block lane >> 4, so
-// that a lane's dword serves four fragments (the instruction selects the
-// byte).  [64-row group][step][lane]; rows and blocks past the end get 127.
+// Scales regrouped for the tile kernel: for 32 rows and the 8 blocks of a
+// step one dword per lane, byte i the scale of row lane & 31, block
+// 2 i + (lane >> 5), so that a lane's dword serves the step's four matrix
+// instructions of a fragment (the instruction selects the byte).
+// [32-row group][step][lane]; rows and blocks past the end get 127.
+// A workgroup takes 32 rows and 8 steps, 64 bytes of each row.
 __global__ __launch_bounds__(kNT) void mx4_scale_groups_kernel(Mx4Mat a, Mx4Mat b, uint32_t* __restrict__ ga,
-                                                               uint32_t* __restrict__ gb, int64_t na, int64_t nb) {
-    int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x;
-    if (e >= na + nb) return;
-    const Mx4Mat& q = e < na ? a : b;
-    uint32_t* g = e < na ? ga : gb;
-    e = e < na ? e : e - na;
-    const int64_t kb = q.kb(), steps = (kb + 3) / 4;
-    const int lane = (int)(e & 63);
-    const int64_t block = (e >> 6) % steps * 4 + (lane >> 4), row = (e >> 6) / steps * 64 + (lane & 15);
-    uint32_t w = 0u;
+                                                               uint32_t* __restrict__ gb, int a_groups) {
+    const bool is_a = (int)blockIdx.x < a_groups;
+    const Mx4Mat& q = is_a ? a : b;
+    const int64_t group = is_a ? blockIdx.x : blockIdx.x - a_groups;
+    const int64_t kb = q.kb(), steps = (kb + 7) / 8;
+    const int r = threadIdx.x & 31;
+    const int64_t step = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5), row = group * 32 + r;
+    if (step >= steps) return;
+    const uint8_t* p = q.scales + row * kb + step * 8;
+    uint32_t even = 0x7F7F7F7Fu, odd = 0x7F7F7F7Fu;
+    if (row < q.rows) {
+        if (step * 8 + 8 <= kb) {
+            typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(1)));
+            const u2 w = *(const u2*)p;
+            even = __builtin_amdgcn_perm(w.y, w.x, 0x06040200u);
+            odd = __builtin_amdgcn_perm(w.y, w.x, 0x07050301u);
+        } else {
+            even = odd = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = row + 16 * i < q.rows && block < kb;
-        w |= (in ? (uint32_t)q.scales[(row + 16 * i) * kb + block] : 127u) << (8 * i);
+            for (int i = 0; i < 4; ++i) {
+                even |= (step * 8 + 2 * i < kb ? (uint32_t)p[2 * i] : 127u) << (8 * i);
+                odd |= (step * 8 + 2 * i + 1 < kb ? (uint32_t)p[2 * i + 1] : 127u) << (8 * i);
+            }
+        }
     }
-    g[e] = w;
+    uint32_t* g = (is_a ? ga : gb) + (group * steps + step) * 64;
+    g[r] = even;
+    g[32 + r] = odd;
 }
 
 __device__ __align__(16) const uint4 kZeroChunk[1] = {};
 
 constexpr int kTile = 256;
-constexpr int kStages = 4;                        // ring of 4 k steps, 3 in flight
-constexpr int kStageBytes = 2 * kTile * 64;       // codes of both operands, 128 k
-constexpr int kScaleBytes = 2 * (kTile / 64) * 256;
 constexpr int kTNT = 512;
-constexpr int kCodeCopies = kStageBytes / 16 / kTNT;
-constexpr int kCopies = kCodeCopies + kScaleBytes / 4 / kTNT;  // asynchronous copies a thread issues per step
+constexpr int kStageBytes = 2 * kTile * 128;             // codes of both operands, 256 k
+constexpr int kScaleBytes = 2 * (kTile / 32) * 256;
+constexpr int kBufBytes = kStageBytes + kScaleBytes;     // two of them in LDS
+constexpr int kCodeCopies = kStageBytes / 16 / kTNT;     // asynchronous copies a thread issues per step
+constexpr int kScaleCopies = kScaleBytes / 4 / kTNT;
 
 template <int N>
 IQLH_DEV void wait_vm() {
     static_assert(N >= 0 && N < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
-// Workgroup barrier that leaves the asynchronous copies in flight
+// Asynchronous copy of 16 (4) bytes per lane, global -> LDS, to lds_at + 16 (4)
+// lane.  As an instruction of its own and not the compiler's builtin: behind
+// the builtin the compiler waits for every copy in flight before each LDS
+// read that may alias one, which is all of them, and the ring runs empty.  It
+// has no output registers; wait_vm orders it against the reads.  (One wait
+// state between writing M0 and its use by the copy.)
+IQLH_DEV void copy16(const void* src, uint32_t lds_at) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
+}
+IQLH_DEV void copy4(const void* src, uint32_t lds_at) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
+}
+// Workgroup barrier after this wave's LDS reads, leaving the asynchronous
+// copies it has in flight
 IQLH_DEV void bar() {
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
+
 struct TileArgs {
     Mx4Mat a, b;
     const uint32_t* ga;
@@ -198,18 +226,81 @@ struct TileArgs {
     int m_tiles, n_tiles;
 };
 
-// Eight waves, 2 x 4, each 128 x 64 outputs (8 x 4 fragments, 128 registers
-// of sums), two waves per SIMD.
-// Ring: step s lives in buffer s % kStages; its buffer is refilled (step s +
-// kStages) after the barrier of step s + 1, which every wave reaches with its
-// reads of step s done.  A row's 64 bytes of a step lie at 64 row, chunk u at
-// u ^ ((row >> 1) & 3): the 16 lanes of a fragment column then fall on all
-// banks.
+// The workgroup's 256 x 256 sums to memory: through LDS, so that a row leaves
+// as neighbouring 16-byte stores and not as the matrix instruction's 4-element
+// pieces.  Waves 0..3 hold the rows 0..127 of the tile, 4..7 the others; a
+// 32-bit tile passes in two halves of 128 rows.  A row's 16-byte unit v lies at
+// v ^ (row & 7).
+template <int DT>
+IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* lds, int64_t m0, int64_t n0, int wm,
+                         int wn) {
+    typedef typename MxFloat<DT>::type T;
+    constexpr int HALVES = DT == IQLH_F32 ? 2 : 1, ROWS = kTile / HALVES;
+    constexpr int E = 16 / sizeof(T), UNITS = kTile / E;  // elements of a unit, units of a row
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const Mx4Out& o = t.o;
+#pragma unroll
+    for (int half = 0; half < HALVES; ++half) {
+        if (half) __syncthreads();
+        if (HALVES == 1 || wm / 128 == half) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int n = wn + 32 * j + 8 * g + 4 * h;
+                    float bias[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bias[e] = o.bias && n0 + n + e < t.b.rows ? o.bias[n0 + n + e] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = (HALVES == 1 ? wm : 0) + 32 * i + r;
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            y[e] = acc[i][j][4 * g + e] + bias[e];
+                            if (o.relu && y[e] < 0.f) y[e] = 0.f;  // a NaN stays
+                        }
+                        uint8_t* p = lds + row * (kTile * sizeof(T)) + 16 * ((n / E) ^ (row & 7)) + (n % E) * sizeof(T);
+                        mx4_put4<DT>((T*)p, y);
+                    }
+                }
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int c = threadIdx.x; c < ROWS * UNITS; c += kTNT) {
+            const int row = c / UNITS, v = c % UNITS;
+            const int64_t m = m0 + half * ROWS + row, n = n0 + v * E;
+            if (m >= t.a.rows || n >= t.b.rows) continue;
+            const uint4 w = *(const uint4*)(lds + row * (kTile * sizeof(T)) + 16 * (v ^ (row & 7)));
+            T* p = (T*)o.p + m * o.ld + n;
+            if (n + E <= t.b.rows) {
+                typedef T tu __attribute__((ext_vector_type(E), aligned(sizeof(T))));
+                *(tu*)p = __builtin_bit_cast(tu, w);
+            } else {
+                const T* e = (const T*)&w;
+                for (int k = 0; k < E; ++k)
+                    if (n + k < t.b.rows) p[k] = e[k];
+            }
+        }
+    }
+}
+
+// Eight waves, 2 x 4, each 128 x 64 outputs (4 x 2 fragments of 32 x 32, 128
+// registers of sums), two waves per SIMD.  A step is 256 k, 128 bytes of a
+// row: whole cache lines per request.  Two buffers: in the last quarter of
+// step s every wave waits for its copies of step s + 1, passes the barrier
+// (behind which all reads of step s's buffer are done), issues step s + 2 into
+// that buffer and reads the first fragments of step s + 1 while the matrix
+// instructions of the quarter run.  A row's chunk u (16 bytes) lies at
+// 128 row + 16 (u ^ ((row >> 1) & 7)): 16 lanes of a fragment column fall on
+// all 64 banks.
 template <int DT>
 __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
     extern __shared__ __align__(16) uint8_t lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wbase = tid & ~63;
-    const int r = lane & 15, blk = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const int r = lane & 31, h = lane >> 5;
     // consecutive workgroups go to different XCDs: give each XCD a run of
     // tiles, walked in columns of 4 tile rows, so that its L2 serves a
     // patch of about 4 x 8 tiles at a time
@@ -223,87 +314,122 @@ __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
     const int rows_in = t.m_tiles - band * 4 < 4 ? t.m_tiles - band * 4 : 4;
     const int tm = band * 4 + in_band % rows_in, tn = in_band / rows_in;
     const int64_t kb = t.a.kb();
-    const int steps = (int)((kb + 3) / 4);
+    const int steps = (int)((kb + 7) / 8);
     const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-    // copy addresses: chunk c = i 512 + tid holds row c >> 2, chunk (c & 3) ^ ((row >> 1) & 3)
-    const int u = (tid & 3) ^ ((tid >> 3) & 3);
+    // copy addresses: chunk c = i 512 + tid fills place c & 7 of row c >> 3
+    const int u = (tid & 7) ^ ((tid >> 4) & 7);
     const uint8_t* abase = t.a.codes + m0 * kb * 16;
     const uint8_t* bbase = t.b.codes + n0 * kb * 16;
     uint32_t off[kCodeCopies];  // b's rows, then a's
 #pragma unroll
     for (int i = 0; i < kCodeCopies; ++i) {
-        const int row = (i & 1) * 128 + (tid >> 2);
-        const int64_t left = (i < 2 ? t.b.rows - n0 : t.a.rows - m0) - 1;
+        const int row = (i & 3) * 64 + (tid >> 3);
+        const int64_t left = (i < 4 ? t.b.rows - n0 : t.a.rows - m0) - 1;
         off[i] = (uint32_t)((row < left ? row : (int)left) * kb * 16) + 16u * u;
     }
-    const uint32_t* sbase;  // scale group `wave`: b's four, then a's four
+    const uint32_t* sbase[kScaleCopies];  // scale groups `wave` of b and of a
     {
-        const int64_t grp = wave < 4 ? n0 / 64 + wave : m0 / 64 + wave - 4;
-        const int64_t last = (wave < 4 ? t.b.rows + 63 : t.a.rows + 63) / 64 - 1;
-        sbase = (wave < 4 ? t.gb : t.ga) + (grp < last ? grp : last) * steps * 64 + lane;
+        const int64_t gb = n0 / 32 + wave, ga = m0 / 32 + wave;
+        const int64_t lb = (t.b.rows + 31) / 32 - 1, la = (t.a.rows + 31) / 32 - 1;
+        sbase[0] = t.gb + (gb < lb ? gb : lb) * steps * 64 + lane;
+        sbase[1] = t.ga + (ga < la ? ga : la) * steps * 64 + lane;
     }
     // every step issues the same copies, those behind the last one from the
-    // zero chunk, so that the loop has no branch and one wait count
+    // zero chunk, so that the loop has no branch
     auto issue = [&](int s) __attribute__((always_inline)) {
-        uint8_t* dst = lds + (s & (kStages - 1)) * (kStageBytes + kScaleBytes);
-        const int64_t k0 = (int64_t)s * 64;
-        const bool in = 4 * s + u < kb;
+        const uint32_t dst = lds_at + (s & 1) * kBufBytes;
+        const int64_t k0 = (int64_t)s * 128;
+        const bool in = 8 * s + u < kb;
 #pragma unroll
         for (int i = 0; i < kCodeCopies; ++i) {
-            const uint8_t* src = (i < 2 ? bbase : abase) + k0 + off[i];
-            __builtin_amdgcn_global_load_lds((const void*)(in ? src : (const uint8_t*)kZeroChunk),
-                                             IQLH_LDS(dst + (i * kTNT + wbase) * 16), 16, 0, 0);
+            const uint8_t* src = (i < 4 ? bbase : abase) + k0 + off[i];
+            copy16(in ? src : (const uint8_t*)kZeroChunk, dst + i * kTNT * 16 + wave * 1024);
         }
-        __builtin_amdgcn_global_load_lds((const void*)(sbase + (int64_t)(s < steps ? s : steps - 1) * 64),
-                                         IQLH_LDS(dst + kStageBytes + wave * 256), 4, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kScaleCopies; ++i)
+            copy4(sbase[i] + (int64_t)(s < steps ? s : steps - 1) * 64, dst + kStageBytes + (8 * i + wave) * 256);
     };
     const int wm = (wave >> 2) * 128, wn = (wave & 3) * 64;
-    const int foff = r * 64 + 16 * (blk ^ ((r >> 1) & 3));
-    mx_f4 acc[8][4];
+    struct Frags {
+        uint4 a[4], b[2];
+    } f[2];
+    uint32_t sa[2][4], sb[2][2];
+    auto load = [&](int s, auto quarter, auto p) __attribute__((always_inline)) {
+        constexpr int Q = decltype(quarter)::value;
+        const uint8_t* src = lds + (s & 1) * kBufBytes;
+        const int foff = r * 128 + 16 * ((2 * Q + h) ^ ((r >> 1) & 7));
+        Frags& g = f[decltype(p)::value];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 2; ++i) g.b[i] = *(const uint4*)(src + (wn + 32 * i) * 128 + foff);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) g.a[i] = *(const uint4*)(src + (kTile + wm + 32 * i) * 128 + foff);
+    };
+    auto load_scales = [&](int s, uint32_t (&pa)[4], uint32_t (&pb)[2]) __attribute__((always_inline)) {
+        const uint8_t* src = lds + (s & 1) * kBufBytes + kStageBytes + lane * 4;
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(s);
+        for (int i = 0; i < 2; ++i) pb[i] = *(const uint32_t*)(src + (wn / 32 + i) * 256);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pa[i] = *(const uint32_t*)(src + (8 + wm / 32 + i) * 256);
+    };
+    mx_f16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mx_f16{};
+    auto mma = [&](auto quarter, auto p, const uint32_t (&pa)[4], const uint32_t (&pb)[2]) __attribute__((always_inline)) {
+        constexpr int Q = decltype(quarter)::value;
+        const Frags& g = f[decltype(p)::value];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = mx4_mma32<Q, Q>(g.b[j], g.a[i], acc[i][j], pb[j], pa[i]);
+    };
+    typedef std::integral_constant<int, 0> C0;
+    typedef std::integral_constant<int, 1> C1;
+    typedef std::integral_constant<int, 2> C2;
+    typedef std::integral_constant<int, 3> C3;
+    issue(0);
+    wait_vm<0>();
+    bar();
+    issue(1);
+    load(0, C0(), C0());
+    load_scales(0, sa[0], sb[0]);
+    // per quarter: the next one's LDS reads, then this one's matrix instructions
+    auto reads_first = [] __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
     for (int s = 0; s < steps; ++s) {
-        wait_vm<(kStages - 2) * kCopies>();  // step s has landed, the two behind it may be in flight
+        load(s, C1(), C1());
+        mma(C0(), C0(), sa[0], sb[0]);
+        reads_first();
+        load(s, C2(), C0());
+        mma(C1(), C1(), sa[0], sb[0]);
+        reads_first();
+        load(s, C3(), C1());
+        mma(C2(), C0(), sa[0], sb[0]);
+        reads_first();
+        wait_vm<0>();  // step s + 1 has landed
         bar();
-        issue(s + kStages - 1);
-        const uint8_t* src = lds + (s & (kStages - 1)) * (kStageBytes + kScaleBytes);
-        uint4 av[8], bv[4];
-        uint32_t sa[2];
-        const uint32_t sb = *(const uint32_t*)(src + kStageBytes + (wn / 64) * 256 + lane * 4);
+        issue(s + 2);
+        load(s + 1, C0(), C0());
+        load_scales(s + 1, sa[1], sb[1]);
+        mma(C3(), C1(), sa[0], sb[0]);
+        __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) sa[i] = *(const uint32_t*)(src + kStageBytes + (4 + wm / 64 + i) * 256 + lane * 4);
+        for (int i = 0; i < 4; ++i) sa[0][i] = sa[1][i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bv[i] = *(const uint4*)(src + (wn + 16 * i) * 64 + foff);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) av[i] = *(const uint4*)(src + (kTile + wm + 16 * i) * 64 + foff);
-        static_for<8>([&](auto i) __attribute__((always_inline)) {
-            static_for<4>([&](auto j) __attribute__((always_inline)) {
-                constexpr int I = decltype(i)::value, J = decltype(j)::value;
-                acc[I][J] = mx4_mma_sel<J & 3, I & 3>(bv[J], av[I], acc[I][J], sb, sa[I >> 2]);
-            });
-        });
-        __builtin_amdgcn_sched_group_barrier(0x100, 15, 0);  // the LDS reads
-        __builtin_amdgcn_sched_group_barrier(0x008, 32, 0);  // then the matrix instructions
+        for (int i = 0; i < 2; ++i) sb[0][i] = sb[1][i];
     }
-    wait_vm<0>();  // the copies behind the last step, before this workgroup's LDS is given away
-    const bool wide = mx4_wide_rows<DT>(t.o);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t m = m0 + wm + 16 * i + r;
-        if (m >= t.a.rows) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + wn + 16 * j + 4 * blk;
-            mx4_store4<DT>(t.o, m, n, (int)(t.b.rows - n < 4 ? t.b.rows - n : 4), acc[i][j], wide);
-        }
-    }
+    wait_vm<0>();  // the copies behind the last step, before their buffers are used again
+    bar();
+    store_tile<DT>(t, acc, lds, m0, n0, wm, wn);
 }
 
-size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 63) / 64) * (size_t)((kb + 3) / 4) * 256; }
+size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 31) / 32) * (size_t)((kb + 7) / 8) * 256; }
 
 }  // namespace
 
@@ -329,13 +455,13 @@ hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out
     }
     if (mx4_use_tiles(a.rows, b.rows, a.cols)) {
         TileArgs t{a, b, nullptr, nullptr, out, (int)((a.rows + kTile - 1) / kTile), (int)((b.rows + kTile - 1) / kTile)};
-        const size_t na = group_bytes(a.rows, a.kb()), nb = group_bytes(b.rows, b.kb());
         t.ga = (const uint32_t*)workspace;
-        t.gb = (const uint32_t*)((const char*)workspace + na);
-        hipLaunchKernelGGL(mx4_scale_groups_kernel, dim3((uint32_t)(((na + nb) / 4 + kNT - 1) / kNT)), dim3(kNT), 0,
-                           stream, a, b, (uint32_t*)t.ga, (uint32_t*)t.gb, (int64_t)na / 4, (int64_t)nb / 4);
+        t.gb = (const uint32_t*)((const char*)workspace + group_bytes(a.rows, a.kb()));
+        const uint32_t ag = (uint32_t)((a.rows + 31) / 32), bg = (uint32_t)((b.rows + 31) / 32);
+        hipLaunchKernelGGL(mx4_scale_groups_kernel, dim3(ag + bg, (uint32_t)((a.kb() + 63) / 64)), dim3(kNT), 0, stream, a,
+                           b, (uint32_t*)t.ga, (uint32_t*)t.gb, (int)ag);
         return by_dtype(out.dtype, [&](auto dt) {
-            constexpr int bytes = kStages * (kStageBytes + kScaleBytes);
+            constexpr int bytes = 2 * kBufBytes;
             static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
             auto kernel = mx4_tile_kernel<decltype(dt)::value>;
             (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
