@@ -550,7 +550,7 @@ static int check_tensor_list(const char* who, const int64_t* lens, const int32_t
     }
     // 32 KB a piece where there are pieces enough for every compute unit,
     // down to 4 KB (one 16-byte load a thread) for small sets
-    int64_t pb = (total / kNormBlocks + 4095) / 4096 * 4096;
+    int64_t pb = (total / 1024 + 4095) / 4096 * 4096;
     pb = pb < 4096 ? 4096 : pb > 32768 ? 32768 : pb;
     int64_t np = 0;
     for (int i = 0; i < count; ++i) np += (lens[i] * dtype_bytes(dtypes[i]) + pb - 1) / pb;

@@ -228,7 +228,7 @@ struct TensorPiece {
     int32_t reserved[2];
 };
 static_assert(sizeof(TensorPiece) == 32, "piece table entry");
-constexpr int kNormBlocks = 1024;  // most workgroups of the norm pass
+constexpr int kNormBlocks = 2048;  // most workgroups of the norm pass
 struct TensorSetArgs {
     const TensorPiece* pieces;
     const int32_t* first;  // [count + 1]

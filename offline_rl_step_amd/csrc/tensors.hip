@@ -186,13 +186,14 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(TensorSetArgs a) {
 template <int KIND>
 IQLH_DEV double norm_of_parts(const uint64_t* part, int nb, uint64_t* red) {
     Stat<KIND> s;
+#pragma unroll 8
     for (int i = threadIdx.x; i < nb; i += kNT) s.join(part[i]);
     return block_join(s, red).norm();
 }
 
 IQLH_DEV bool finite64(double x) { return fabs(x) < __longlong_as_double(0x7FF0000000000000ll); }
 
-// Block 0: the whole norm.  The others: one wave per tensor.
+// Block 0: the whole norm.  Block 1 + t: tensor t.
 template <int KIND>
 __global__ __launch_bounds__(kNT) void grad_norm_finish_kernel(TensorSetArgs a, int nb, float* __restrict__ out_norm,
                                                                float* __restrict__ out_each) {
@@ -205,13 +206,67 @@ __global__ __launch_bounds__(kNT) void grad_norm_finish_kernel(TensorSetArgs a, 
         }
         return;
     }
-    const int t = (blockIdx.x - 1) * (kNT / kWave) + threadIdx.x / kWave;
-    if (t >= a.count) return;
-    Stat<KIND> s;
-    const int64_t end = (int64_t)a.first[t + 1] * 4;
-    for (int64_t i = (int64_t)a.first[t] * 4 + (threadIdx.x & 63); i < end; i += kWave) s.join(a.each[i]);
-    s = wave_join(s);
-    if ((threadIdx.x & 63) == 0) out_each[t] = (float)s.norm();
+    const int t = blockIdx.x - 1;
+    const double n = norm_of_parts<KIND>(a.each + (int64_t)a.first[t] * 4, (a.first[t + 1] - a.first[t]) * 4, red);
+    if (threadIdx.x == 0) out_each[t] = (float)n;
+}
+
+// Elements [0, n) of q times c in place, whole 16-byte quads, kAhead loads in
+// flight per thread.
+template <int DT>
+IQLH_DEV void scale_quads(uint4* q, int nq, float c) {
+    typedef Elem<DT> E;
+    auto scaled = [c](uint4 x) __attribute__((always_inline)) {
+        float v[E::kQ];
+#pragma unroll
+        for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
+        return E::pack(v);
+    };
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * kNT < nq; i += kAhead * kNT) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = q[i + k * kNT];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) q[i + k * kNT] = scaled(x[k]);
+    }
+    for (; i < nq; i += kNT) q[i] = scaled(q[i]);
+}
+
+// Four elements of a body that starts on a 16-byte boundary, times c, to the
+// flat vector: 16 bytes of it per thread whatever the source type, so that
+// neighbouring lanes store neighbouring 16 bytes (which need not lie on a
+// boundary of 16, only of 4).
+template <int DT> struct Four;
+template <> struct Four<IQLH_F32> {
+    typedef uint4 type;
+    static IQLH_DEV float get(uint4 w, int i) { return __uint_as_float((&w.x)[i]); }
+};
+template <> struct Four<IQLH_BF16> {
+    typedef uint2 type;
+    static IQLH_DEV float get(uint2 w, int i) { return Elem<IQLH_BF16>::get(uint4{w.x, w.y, 0u, 0u}, i); }
+};
+template <> struct Four<IQLH_F16> {
+    typedef uint2 type;
+    static IQLH_DEV float get(uint2 w, int i) { return Elem<IQLH_F16>::get(uint4{w.x, w.y, 0u, 0u}, i); }
+};
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+template <int DT>
+IQLH_DEV void scale_flat(const void* src, float* out, int n4, float c) {
+    typedef Four<DT> F;
+    const typename F::type* q = (const typename F::type*)src;
+    auto scaled = [c](typename F::type w) __attribute__((always_inline)) {
+        return f4u{F::get(w, 0) * c, F::get(w, 1) * c, F::get(w, 2) * c, F::get(w, 3) * c};
+    };
+    int i = threadIdx.x;
+    for (; i + (kAhead - 1) * kNT < n4; i += kAhead * kNT) {
+        typename F::type x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = q[i + k * kNT];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) *(f4u*)(out + (int64_t)(i + k * kNT) * 4) = scaled(x[k]);
+    }
+    for (; i < n4; i += kNT) *(f4u*)(out + (int64_t)i * 4) = scaled(q[i]);
 }
 
 template <int DT>
@@ -220,35 +275,12 @@ IQLH_DEV void scale_piece(const TensorPiece& p, float c, float* flat) {
     const Cut<DT> cut(p);
     const int e = cut.edge();
     if (!flat) {
-        uint4* q = (uint4*)cut.q;
-        for (int i = threadIdx.x; i < cut.nq; i += kNT) {
-            const uint4 x = q[i];
-            float v[E::kQ];
-#pragma unroll
-            for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
-            q[i] = E::pack(v);
-        }
+        scale_quads<DT>((uint4*)cut.q, cut.nq, c);
         if (e >= 0) E::store((void*)p.ptr, e, E::load((const void*)p.ptr, e) * c);
         return;
     }
-    float* out = flat + p.off;
-    float* body = out + cut.head;
-    const bool wide = ((uintptr_t)body & 15u) == 0;  // the same for the whole block
-    for (int i = threadIdx.x; i < cut.nq; i += kNT) {
-        const uint4 x = cut.q[i];
-        float v[E::kQ];
-#pragma unroll
-        for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
-        if (wide) {
-#pragma unroll
-            for (int j = 0; j < E::kQ; j += 4)
-                *(float4*)(body + (int64_t)i * E::kQ + j) = float4{v[j], v[j + 1], v[j + 2], v[j + 3]};
-        } else {
-#pragma unroll
-            for (int j = 0; j < E::kQ; ++j) body[(int64_t)i * E::kQ + j] = v[j];
-        }
-    }
-    if (e >= 0) out[e] = E::load((const void*)p.ptr, e) * c;
+    scale_flat<DT>(cut.q, flat + p.off + cut.head, cut.nq * (E::kQ / 4), c);
+    if (e >= 0) flat[p.off + e] = E::load((const void*)p.ptr, e) * c;
 }
 
 template <int KIND>
@@ -288,7 +320,7 @@ template <int KIND>
 hipError_t norm_launch(const TensorSetArgs& a, float* out_norm, float* out_each, hipStream_t stream) {
     hipError_t e = norm_pass<KIND>(a, stream);
     if (e != hipSuccess) return e;
-    const int grid = 1 + (out_each ? (a.count + 3) / 4 : 0);
+    const int grid = 1 + (out_each ? a.count : 0);
     hipLaunchKernelGGL(grad_norm_finish_kernel<KIND>, dim3(grid), dim3(kNT), 0, stream, a, norm_blocks(a.npieces),
                        out_norm, out_each);
     return hipGetLastError();
