@@ -17,32 +17,6 @@ hipError_t by_dtype(int dtype, F f) {
 }
 
 // ------------------------------------------------------------ quantisation
-// Eight neighbouring elements at p, which is aligned to its element only (the
-// hardware takes 16-byte loads at any address).  count < 8: the rest are 0.
-template <int DT>
-IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
-    typedef typename MxFloat<DT>::type T;
-    if (count >= 8) {
-        if constexpr (DT == IQLH_F32) {
-            typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
-            const f4u a = *(const f4u*)p, b = *(const f4u*)(p + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = a[j];
-                v[4 + j] = b[j];
-            }
-        } else {
-            typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
-            const t8u a = *(const t8u*)p;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = MxFloat<DT>::get(a[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < count ? MxFloat<DT>::get(p[j]) : 0.f;
-    }
-}
-
 constexpr int kQRows = 4;  // rows (times the workgroup's) a thread converts
 
 // Blocks along x's rows.  HBM-bound.  A thread converts 8 elements (one dword
@@ -251,6 +225,7 @@ size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx4_linear(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                              void* workspace, hipStream_t stream) {
+    if (mx4_rows_ok(M, b.rows, b.cols)) return launch_mx4_rows(x, dtype, ld, M, b, out, stream);
     const int64_t blocks = M * b.kb();
     const Mx4Mat a{(uint8_t*)workspace, (uint8_t*)workspace + blocks * 16, M, b.cols};
     hipError_t e = launch_mx4_quantize(x, dtype, ld, false, a, stream);

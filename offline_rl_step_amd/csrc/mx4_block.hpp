@@ -70,6 +70,54 @@ IQLH_DEV float mx4_value(uint32_t code) {
     return __uint_as_float(mag | (code & 8u) << 28);
 }
 
+// Eight neighbouring elements at p, which is aligned to its element only (the
+// hardware takes 16-byte loads at any address).  count < 8: the rest are 0.
+template <int DT>
+IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
+    typedef typename MxFloat<DT>::type T;
+    if (count >= 8) {
+        if constexpr (DT == IQLH_F32) {
+            typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+            const f4u a = *(const f4u*)p, b = *(const f4u*)(p + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = a[j];
+                v[4 + j] = b[j];
+            }
+        } else {
+            typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
+            const t8u a = *(const t8u*)p;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = MxFloat<DT>::get(a[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < count ? MxFloat<DT>::get(p[j]) : 0.f;
+    }
+}
+
+// 16 rows from row0 on, blocks 4 step .. 4 step + 3, of a matrix in memory:
+// this lane's 16 bytes and scale.  Rows past the end read the last one (their
+// outputs are never stored), blocks past the end are zeros of scale 1.
+struct RowFrag {
+    const uint4* codes;
+    const uint8_t* scales;
+    int64_t kb;
+    IQLH_DEV RowFrag(const Mx4Mat& q, int64_t row) : kb(q.kb()) {
+        const int64_t r = row < q.rows ? row : q.rows - 1;
+        codes = (const uint4*)q.codes + r * kb;
+        scales = q.scales + r * kb;
+    }
+    IQLH_DEV void load(int64_t block, uint4& v, uint32_t& s) const {
+        const bool in = block < kb;
+        v = codes[in ? block : 0];
+        s = scales[in ? block : 0];
+        const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+        v = uint4{v.x & keep, v.y & keep, v.z & keep, v.w & keep};
+        s = in ? s : 127u;
+    }
+};
+
 // largest of the four lanes 4j .. 4j + 3, in all of them
 IQLH_DEV uint32_t quad_umax(uint32_t v) {
     v = umax2(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));  // quad_perm 1,0,3,2

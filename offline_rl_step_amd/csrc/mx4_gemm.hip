@@ -27,28 +27,6 @@ hipError_t by_dtype(int dtype, F f) {
     return hipGetLastError();
 }
 
-// 16 rows from row0 on, blocks 4 step .. 4 step + 3, of a matrix in memory:
-// this lane's 16 bytes and scale.  Rows past the end read the last one (their
-// outputs are never stored), blocks past the end are zeros of scale 1.
-struct RowFrag {
-    const uint4* codes;
-    const uint8_t* scales;
-    int64_t kb;
-    IQLH_DEV RowFrag(const Mx4Mat& q, int64_t row) : kb(q.kb()) {
-        const int64_t r = row < q.rows ? row : q.rows - 1;
-        codes = (const uint4*)q.codes + r * kb;
-        scales = q.scales + r * kb;
-    }
-    IQLH_DEV void load(int64_t block, uint4& v, uint32_t& s) const {
-        const bool in = block < kb;
-        v = codes[in ? block : 0];
-        s = scales[in ? block : 0];
-        const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
-        v = uint4{v.x & keep, v.y & keep, v.z & keep, v.w & keep};
-        s = in ? s : 127u;
-    }
-};
-
 // ------------------------------------------------------------- few rows
 // M <= 16.  Workgroup: 16 rows of b.  Wave w of WAVES takes the k steps w,
 // w + WAVES, ..; U steps' loads are in flight together.  The waves' sums meet
