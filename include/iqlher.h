@@ -587,8 +587,8 @@ int iqlh_mx4_dequantize(const iqlh_mx4* q, void* out, int32_t dtype, int64_t ld,
  *   workspace  device, >= iqlh_mx4_workspace_bytes(M, N, K), 16-byte
  *          aligned, no initial contents required; calls that overlap in time
  *          need one each.
- * iqlh_mx4_linear: the same with a = x [M][ld] quantised on the way (as
- * iqlh_mx4_quantize does, bit for bit the same result). */
+ * iqlh_mx4_linear: the same with a = x [M][ld], quantised on the way to the
+ * codes and scales that iqlh_mx4_quantize gives. */
 int iqlh_mx4_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
 int iqlh_mx4_matmul(const iqlh_mx4* a, const iqlh_mx4* b, const float* bias, int32_t relu, void* out,
                     int32_t out_dtype, int64_t ld_out, void* workspace, size_t workspace_bytes,

@@ -53,70 +53,45 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloa
 }
 
 // Blocks along x's columns: x is [q.cols][ld].  HBM-bound.  A lane takes one
-// column of x (16-bit types: two neighbouring ones, a dword per load), 32 rows a
-// block, neighbouring lanes neighbouring addresses; a workgroup 64 (128) columns
-// and 256 rows.  The codes pass through LDS so that a row of q is written 128
-// bytes at a time.
+// column of x, 32 rows a block, neighbouring lanes neighbouring addresses; a
+// workgroup 64 columns and 256 rows.  The codes pass through LDS so that a row of
+// q is written 128 bytes at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two
+// 16-bit columns per lane by dword loads 27.5, and 12.3 against 5.2 us at
+// 5001 x 777, where they leave half of the compute units without a workgroup.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typename MxFloat<DT>::type* __restrict__ x,
                                                                    int64_t ld, Mx4Mat q, int row_tiles) {
-    typedef typename MxFloat<DT>::type T;
-    constexpr int CPL = DT == IQLH_F32 ? 1 : 2;
-    __shared__ uint4 codes[64 * CPL][9];  // 9: the lanes of a store to one block column fall on different banks
-    __shared__ uint8_t scales[64 * CPL][8];
+    __shared__ uint4 codes[64][9];  // 9: the lanes of a store to one block column fall on different banks
+    __shared__ uint8_t scales[64][8];
     const int64_t kb = q.kb();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * (64 * CPL), b0 = (int64_t)(blockIdx.x / row_tiles) * 8;
-    const int64_t r = r0 + lane * CPL;
-    const int64_t rc = CPL > 1 || r < q.rows ? r : q.rows - 1;
+    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * 64, b0 = (int64_t)(blockIdx.x / row_tiles) * 8;
+    const int64_t r = r0 + lane < q.rows ? r0 + lane : q.rows - 1;  // lanes past the end: not written below
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int i = wave + 4 * half;
         const int64_t k0 = (b0 + i) * 32;
-        float v[CPL][32];
-        if (b0 + i < kb) {
-            if (CPL == 1 || r + CPL <= q.rows) {
-                // loads at clamped rows, those behind the last one masked: no branch between them
-                const int left = (int)(q.cols - k0 < 32 ? q.cols - k0 : 32);
-                const T* p = x + k0 * ld + rc;
+        if (b0 + i >= kb) break;
+        // loads at clamped rows, those behind the last one masked: no branch between them
+        const int left = (int)(q.cols - k0 < 32 ? q.cols - k0 : 32);
+        const typename MxFloat<DT>::type* p = x + k0 * ld + r;
+        float v[32];
+        uint32_t amax = 0u;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const T* pj = p + (j < left ? j : 0) * ld;
-                    if constexpr (CPL == 1) {
-                        v[0][j] = keep_if(j < left, (float)*pj);
-                    } else {
-                        typedef T t2u __attribute__((ext_vector_type(2), aligned(2)));
-                        const t2u w = *(const t2u*)pj;
-                        v[0][j] = keep_if(j < left, MxFloat<DT>::get(w[0]));
-                        v[1][j] = keep_if(j < left, MxFloat<DT>::get(w[1]));
-                    }
-                }
-            } else {  // the last of an odd number of columns, and lanes past it
+        for (int j = 0; j < 32; ++j) v[j] = keep_if(j < left, MxFloat<DT>::get(p[(j < left ? j : 0) * ld]));
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-#pragma unroll
-                    for (int c = 0; c < CPL; ++c)
-                        v[c][j] = r + c < q.rows && k0 + j < q.cols ? MxFloat<DT>::get(x[(k0 + j) * ld + r + c]) : 0.f;
-            }
-#pragma unroll
-            for (int c = 0; c < CPL; ++c) {
-                uint32_t amax = 0u;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[c][j]));
-                const uint32_t s = mx4_scale(amax);
-                uint4 w{0u, 0u, 0u, 0u};
-                if (s != 255u) {
-                    const float inv = mx4_inverse(s);
-                    w = uint4{mx4_codes8(v[c], inv), mx4_codes8(v[c] + 8, inv), mx4_codes8(v[c] + 16, inv),
-                              mx4_codes8(v[c] + 24, inv)};
-                }
-                codes[lane * CPL + c][i] = w;
-                scales[lane * CPL + c][i] = (uint8_t)s;
-            }
+        for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[j]));
+        const uint32_t s = mx4_scale(amax);
+        uint4 w{0u, 0u, 0u, 0u};
+        if (s != 255u) {
+            const float inv = mx4_inverse(s);
+            w = uint4{mx4_codes8(v, inv), mx4_codes8(v + 8, inv), mx4_codes8(v + 16, inv), mx4_codes8(v + 24, inv)};
         }
+        codes[lane][i] = w;
+        scales[lane][i] = (uint8_t)s;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 512 * CPL; e += kNT) {
+    for (int e = threadIdx.x; e < 512; e += kNT) {
         const int rr = e >> 3, i = e & 7;
         if (r0 + rr < q.rows && b0 + i < kb) {
             ((uint4*)q.codes)[(r0 + rr) * kb + b0 + i] = codes[rr][i];
@@ -196,8 +171,7 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transp
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
         if (transposed) {
-            constexpr int cols = DT == IQLH_F32 ? 64 : 128;
-            const int64_t row_tiles = (q.rows + cols - 1) / cols, k_tiles = (q.kb() + 7) / 8;
+            const int64_t row_tiles = (q.rows + 63) / 64, k_tiles = (q.kb() + 7) / 8;
             hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)(row_tiles * k_tiles)), dim3(kNT), 0, stream,
                                (const T*)x, ld, q, (int)row_tiles);
         } else {

@@ -165,13 +165,30 @@ IQLH_DEV void static_for(F&& f) {
     static_for_impl(f, std::make_integer_sequence<int, N>());
 }
 
+// bias[n .. n + 3], 0 without a bias and behind the last of N
+IQLH_DEV void mx4_bias4(const Mx4Out& o, int64_t n, int64_t N, float* bias) {
+    if (!o.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = 0.f;
+    } else if (n + 4 <= N) {
+        typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+        const f4u w = *(const f4u*)(o.bias + n);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = w[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = n + e < N ? o.bias[n + e] : 0.f;
+    }
+}
+
 // Four values rounded and stored at once
 template <int DT>
 IQLH_DEV void mx4_put4(typename MxFloat<DT>::type* p, const float* y) {
     if constexpr (DT == IQLH_F32) {
         *(float4*)p = float4{y[0], y[1], y[2], y[3]};
     } else if constexpr (DT == IQLH_BF16) {
-        *(uint2*)p = uint2{pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3])};
+        typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+        *(b4*)p = __builtin_convertvector(mx_f4{y[0], y[1], y[2], y[3]}, b4);  // nearest even; a NaN stays one
     } else {
         typedef _Float16 h4 __attribute__((ext_vector_type(4)));
         *(h4*)p = h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
