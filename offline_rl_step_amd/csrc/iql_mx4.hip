@@ -2,9 +2,14 @@
 //   h1 = relu(q(s) q(W1)^T + b1), h2 = relu(q(h1) q(W2)^T + b2), V = w3 . h2 + b3,
 // the value network of iql_forward_values ("GPU IQL + HER Porting Plan",
 // "Rust Integration: gpu_iql_trainer.rs", forward_values) on the 4-bit product.
+//
+// Up to 1024 states and hidden units: two launches, the weights' quantisation
+// and the whole network (a workgroup takes 64 rows through both layers, h1 in
+// 4 bits in LDS, V from registers).  Wider: layer by layer on the linear
+// product.
 #include "iqlher.h"
 #include "launch.hpp"
-#include "mx4_block.hpp"
+#include "mx4_rows_block.hpp"
 
 namespace iqlh {
 
@@ -24,29 +29,186 @@ __global__ __launch_bounds__(256) void iql_mx4_head_kernel(const float* __restri
     if (lane == 0) write_value(vo, g, B, row0 + row, s + w3[H2]);  // b3 follows w3
 }
 
+// W1 and W2 of every group, blocks along their rows: 8 elements a thread.
+struct WeightArgs {
+    const float* params;  // [G][P]
+    int64_t P;
+    uint8_t* ws;          // [G] of `stride` bytes: codes and scales at the offsets below
+    size_t stride, w1c, w1s, w2c, w2s;
+    int S, H, H2;
+    int n1, n2;           // groups of 8: of W1, of W2
+};
+__global__ __launch_bounds__(256) void iql_mx4_weights_kernel(WeightArgs a) {
+    const int e = blockIdx.x * 256 + threadIdx.x;  // n1 and n2 are multiples of 4: a block's four lanes stay together
+    const bool second = e >= a.n1;
+    const int k = second ? a.H : a.S, gpr = (k + 31) / 32 * 4;
+    const int at = second ? e - a.n1 : e, row = at / gpr, g = at - row * gpr;
+    const bool in = e < a.n1 + a.n2;
+    const float* w = a.params + blockIdx.y * a.P + (second ? (int64_t)a.H * a.S + a.H : 0) + (int64_t)row * k + g * 8;
+    float v[8];
+    const int left = in ? k - g * 8 : 0;
+    load8<IQLH_F32>(w, left < 0 ? 0 : left < 8 ? left : 8, v);
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
+    const uint32_t s = mx4_scale(quad_umax(amax));
+    if (!in) return;
+    uint8_t* base = a.ws + blockIdx.y * a.stride;
+    ((uint32_t*)(base + (second ? a.w2c : a.w1c)))[at] = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
+    if ((at & 3) == 0) (base + (second ? a.w2s : a.w1s))[at >> 2] = (uint8_t)s;
+}
+
+struct NetArgs {
+    const void* x;
+    int64_t ld;
+    const float* params;
+    int64_t P;
+    const uint8_t* ws;
+    size_t stride, w1c, w1s, w2c, w2s;
+    int S, H, H2, G, B, kb4x, kb4h;
+    ValueOut vo;
+};
+
+// largest of the lanes l, l ^ 16, l ^ 32, l ^ 48, in all of them
+IQLH_DEV uint32_t group_umax(uint32_t v) {
+    v = umax2(v, (uint32_t)__shfl_xor((int)v, 16, kWave));
+    return umax2(v, (uint32_t)__shfl_xor((int)v, 32, kWave));
+}
+IQLH_DEV float group_sum(float v) {
+    v += __shfl_xor(v, 16, kWave);
+    return v + __shfl_xor(v, 32, kWave);
+}
+
+// 64 rows through the network of every group.  Layer 1: a wave's chunk of 32
+// hidden units is one block of h1, so its scale is found and its codes go to LDS
+// from the lanes that hold its sums.  Layer 2: h2 w3 summed in the lanes, over
+// the wave's chunks, the lanes of a row and the waves, in that order.
+template <int XDT>
+__global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ float part[4][kRows];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, blk = lane >> 4;
+    const int64_t m0 = (int64_t)blockIdx.x * kRows;
+    const LdsRows tx(lds, a.kb4x), th(lds + mx4_lds_bytes(a.kb4x), a.kb4h);
+    mx4_rows_to_lds<XDT>((const typename MxFloat<XDT>::type*)a.x, a.ld, a.B, m0, a.S, tx);
+    __syncthreads();
+    for (int g = 0; g < a.G; ++g) {
+        uint8_t* ws = (uint8_t*)a.ws + g * a.stride;
+        const Mx4Mat w1{ws + a.w1c, ws + a.w1s, a.H, a.S}, w2{ws + a.w2c, ws + a.w2s, a.H2, a.H};
+        const float* b1 = a.params + g * a.P + (int64_t)a.H * a.S;
+        const float* b2 = b1 + a.H + (int64_t)a.H2 * a.H;
+        const float* w3 = b2 + a.H2;
+        const Mx4Out o1{nullptr, IQLH_F32, 1, 0, b1}, o2{nullptr, IQLH_F32, 1, 0, b2}, o3{nullptr, IQLH_F32, 0, 0, w3};
+        float bias[kFrags][4], head[kFrags][4];
+        mx4_rows_chunks(
+            tx, w1, a.kb4h * 32,
+            [&](int64_t n0) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < kFrags; ++j) mx4_bias4(o1, n0 + 16 * j + 4 * blk, a.H, bias[j]);
+            },
+            [&](int64_t n0, mx_f4(&acc)[4][kFrags]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y[8];
+                    uint32_t amax = 0u;
+#pragma unroll
+                    for (int j = 0; j < kFrags; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // hidden units past the last are zeros of the block
+                            const bool in = n0 + 16 * j + 4 * blk + e < a.H;
+                            const float z = in ? acc[i][j][e] + bias[j][e] : 0.f;
+                            y[4 * j + e] = __builtin_elementwise_maximum(z, 0.f);
+                            amax = umax2(amax, abs_bits(y[4 * j + e]));
+                        }
+                    const uint32_t s = mx4_scale(group_umax(amax));
+                    const uint32_t w = s == 255u ? 0u : mx4_codes8(y, mx4_inverse(s));
+                    const int row = 16 * i + r, b = (int)(n0 / 32);
+                    uint8_t* p = th.codes + row * th.rb + b * 16 + 2 * blk;
+                    *(uint16_t*)p = (uint16_t)w;               // units 4 blk .. + 3
+                    *(uint16_t*)(p + 8) = (uint16_t)(w >> 16);  // units 16 + 4 blk .. + 3
+                    if (blk == 0) th.scales[row * th.kb4 + b] = (uint8_t)s;
+                }
+            });
+        __syncthreads();
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        mx4_rows_chunks(
+            th, w2, a.H2,
+            [&](int64_t n0) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < kFrags; ++j) {
+                    mx4_bias4(o2, n0 + 16 * j + 4 * blk, a.H2, bias[j]);
+                    mx4_bias4(o3, n0 + 16 * j + 4 * blk, a.H2, head[j]);
+                }
+            },
+            [&](int64_t n0, mx_f4(&acc)[4][kFrags]) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < kFrags; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const bool in = n0 + 16 * j + 4 * blk + e < a.H2;
+                            const float z = in ? acc[i][j][e] + bias[j][e] : 0.f;
+                            v[i] = fmaf(__builtin_elementwise_maximum(z, 0.f), head[j][e], v[i]);
+                        }
+            });
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float s = group_sum(v[i]);
+            if (blk == 0) part[wave][16 * i + r] = s;
+        }
+        __syncthreads();  // also: every wave is done with this group's h1
+        if (threadIdx.x < kRows && m0 + threadIdx.x < a.B) {
+            const int row = threadIdx.x;
+            write_value(a.vo, g, a.B, (int)(m0 + row), part[0][row] + part[1][row] + part[2][row] + part[3][row] + w3[a.H2]);
+        }
+        __syncthreads();
+    }
+}
+
 size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+bool one_launch(const IqlDims& d) { return d.S <= kRowsMaxBlocks * 32 && d.H <= kRowsMaxBlocks * 32; }
+
 struct Layout {
-    size_t w1c, w1s, w2c, w2s, h1, h2, product, total;
+    size_t w1c, w1s, w2c, w2s, group, h1, h2, product, total;
     int chunk;
 };
 
 Layout layout(const IqlDims& d, int B) {
-    Layout l;
+    Layout l{};
     const size_t k1 = (d.S + 31) / 32, k2 = (d.H + 31) / 32;
-    l.chunk = B < kChunkRows ? B : kChunkRows;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t p = at; at += up16(bytes); return p; };
     l.w1c = take(k1 * 16 * d.H);
     l.w1s = take(k1 * d.H);
     l.w2c = take(k2 * 16 * d.H2);
     l.w2s = take(k2 * d.H2);
+    l.group = at;
+    if (one_launch(d)) {
+        l.total = at * d.G;
+        return l;
+    }
+    l.chunk = B < kChunkRows ? B : kChunkRows;
     l.h1 = take(sizeof(float) * (size_t)l.chunk * d.H);
     l.h2 = take(sizeof(float) * (size_t)l.chunk * d.H2);
     const size_t p1 = mx4_workspace_bytes(l.chunk, d.H, d.S), p2 = mx4_workspace_bytes(l.chunk, d.H2, d.H);
     l.product = take(p1 > p2 ? p1 : p2);
     l.total = at;
     return l;
+}
+
+template <int XDT>
+hipError_t launch_net(const NetArgs& a, hipStream_t stream) {
+    const int bytes = mx4_lds_bytes(a.kb4x) + mx4_lds_bytes(a.kb4h);
+    if (bytes > 60 << 10) {
+        hipError_t e = hipFuncSetAttribute((const void*)iql_mx4_net_kernel<XDT>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(iql_mx4_net_kernel<XDT>, dim3((a.B + kRows - 1) / kRows), dim3(kRowsNT), bytes, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -57,6 +219,16 @@ hipError_t launch_iql_mx4_forward(const IqlDims& d, const IqlBuffers& b, const v
                                   int B, const ValueOut& vo, void* workspace, hipStream_t stream) {
     const Layout l = layout(d, B);
     uint8_t* ws = (uint8_t*)workspace;
+    if (one_launch(d)) {
+        const int n1 = d.H * ((d.S + 31) / 32) * 4, n2 = d.H2 * ((d.H + 31) / 32) * 4;
+        WeightArgs w{b.params, d.P, ws, l.group, l.w1c, l.w1s, l.w2c, l.w2s, d.S, d.H, d.H2, n1, n2};
+        hipLaunchKernelGGL(iql_mx4_weights_kernel, dim3((n1 + n2 + 255) / 256, d.G), dim3(256), 0, stream, w);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const NetArgs a{states, ld, b.params, d.P, ws, l.group, l.w1c, l.w1s, l.w2c, l.w2s, d.S, d.H, d.H2, d.G, B,
+                        (d.S + 127) / 128 * 4, (d.H + 127) / 128 * 4, vo};
+        return dtype == IQLH_F32 ? launch_net<IQLH_F32>(a, stream) : launch_net<IQLH_BF16>(a, stream);
+    }
     float* h1 = (float*)(ws + l.h1);
     float* h2 = (float*)(ws + l.h2);
     const Mx4Mat w1{ws + l.w1c, ws + l.w1s, d.H, d.S}, w2{ws + l.w2c, ws + l.w2s, d.H2, d.H};

@@ -28,27 +28,70 @@ hipError_t by_dtype(int dtype, F f) {
 }
 
 // ------------------------------------------------------------- few rows
-// M <= 16.  Workgroup: 16 rows of b.  Wave w of WAVES takes the k steps w,
-// w + WAVES, ..; U steps' loads are in flight together.  The waves' sums meet
-// in LDS, added in wave order.
-template <int DT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void mx4_few_rows_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o) {
-    constexpr int U = 4;
-    __shared__ mx_f4 part[WAVES][64];
+// M <= 16.  HBM-bound on b, at small sizes on the latency of one pass over it.
+// Workgroup: 16 rows of b.  Wave w of 8 takes the k steps w, w + 8, ..; U
+// steps' loads of b are in flight together, the first of them before anything
+// else.  XDT >= 0: the left operand is a float matrix, quantised into LDS by every
+// workgroup (an eighth of a step per thread at 4096 elements) while they are
+// under way.  The waves' sums meet in LDS, added in wave order.
+constexpr int kFewWaves = 8;
+constexpr int kFewElements = 32768;  // of a float left operand, padded: 16 KB of codes, 1 KB of scales
+template <int XDT, int ODT>
+__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, const void* x, int64_t ld, Mx4Mat b,
+                                                                      Mx4Out o) {
+    constexpr int U = 4, NT = 64 * kFewWaves;
+    extern __shared__ __align__(16) uint8_t lds[];
+    mx_f4(*part)[64] = (mx_f4(*)[64])lds;            // [kFewWaves][64]
+    uint8_t* codes = lds + kFewWaves * 64 * 16;      // [M][kb4 * 16 + 16]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const RowFrag fa(a, r), fb(b, n0 + r);
-    const int64_t steps = (a.kb() + 3) / 4;
+    const RowFrag fb(b, n0 + r);
+    const int64_t steps = (b.kb() + 3) / 4;
+    uint4 bv[U];
+    uint32_t bs[U];
+    auto load_b = [&](int64_t s0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) fb.load((s0 + u * kFewWaves) * 4 + blk, bv[u], bs[u]);
+    };
+    load_b(wave);
+    const int kb4 = XDT >= 0 ? (int)steps * 4 : 0, rb = kb4 * 16 + 16;
+    uint8_t* scales = codes + a.rows * rb;           // [M][kb4]
+    if constexpr (XDT >= 0) {
+        const int gpr = kb4 * 4;                     // groups of 8 a row
+        for (int e = threadIdx.x; e < (int)a.rows * gpr; e += NT) {  // four lanes share a block: gpr is a multiple of 16
+            const int row = e / gpr, g = e - row * gpr;
+            const int64_t left = a.cols - g * 8;
+            float v[8];
+            load8<XDT>((const typename MxFloat<XDT>::type*)x + row * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8), v);
+            uint32_t amax = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
+            const uint32_t s = mx4_scale(quad_umax(amax));
+            *(uint32_t*)(codes + row * rb + g * 4) = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
+            if ((g & 3) == 0) scales[row * kb4 + (g >> 2)] = (uint8_t)s;
+        }
+        __syncthreads();
+    }
+    const RowFrag fa(a, r);
     mx_f4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t s0 = wave; s0 < steps; s0 += WAVES * U) {
-        uint4 av[U], bv[U];
-        uint32_t as[U], bs[U];
+    for (int64_t s0 = wave; s0 < steps; s0 += kFewWaves * U) {
+        if (s0 != wave) load_b(s0);
+        uint4 av[U];
+        uint32_t as[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t block = (s0 + u * WAVES) * 4 + blk;
-            fb.load(block, bv[u], bs[u]);
-            fa.load(block, av[u], as[u]);
+            const int64_t s = s0 + u * kFewWaves;
+            if constexpr (XDT >= 0) {
+                const bool in = s < steps && r < a.rows;
+                const int at = in ? (int)s * 4 + blk : 0, row = in ? r : 0;
+                const uint4 w = *(const uint4*)(codes + row * rb + at * 16);
+                const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+                av[u] = uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep};
+                as[u] = in ? scales[row * kb4 + at] : 127u;
+            } else {
+                fa.load(s * 4 + blk, av[u], as[u]);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) acc = mx4_mma(bv[u], av[u], acc, bs[u], as[u]);
@@ -57,10 +100,21 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_few_rows_kernel(Mx4Mat a, Mx4M
     __syncthreads();
     if (wave == 0 && r < a.rows) {
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) acc += part[w][lane];
+        for (int w = 1; w < kFewWaves; ++w) acc += part[w][lane];
         const int64_t n = n0 + 4 * blk;
-        mx4_store4<DT>(o, r, n, (int)(b.rows - n < 4 ? b.rows - n : 4), acc, mx4_wide_rows<DT>(o));
+        mx4_store4<ODT>(o, r, n, (int)(b.rows - n < 4 ? b.rows - n : 4), acc, mx4_wide_rows<ODT>(o));
     }
+}
+
+template <int XDT>
+hipError_t launch_few_rows(const Mx4Mat& a, const void* x, int64_t ld, const Mx4Mat& b, const Mx4Out& out,
+                           hipStream_t stream) {
+    const int kb4 = (int)((b.kb() + 3) / 4 * 4);
+    const int bytes = kFewWaves * 1024 + (XDT >= 0 ? (int)a.rows * (kb4 * 17 + 16) : 0);
+    return by_dtype(out.dtype, [&](auto dt) {
+        hipLaunchKernelGGL((mx4_few_rows_kernel<XDT, decltype(dt)::value>), dim3((uint32_t)((b.rows + 15) / 16)),
+                           dim3(64 * kFewWaves), bytes, stream, a, x, ld, b, out);
+    });
 }
 
 // ------------------------------------------------- tiles from global memory
@@ -423,14 +477,19 @@ size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return mx4_use_tiles(M, N, K) ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
 }
 
+bool mx4_few_ok(int64_t M, int64_t K) { return M <= 16 && M * ((K + 127) / 128 * 128) <= kFewElements; }
+
+hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
+                          hipStream_t stream) {
+    const Mx4Mat a{nullptr, nullptr, M, b.cols};
+    if (dtype == IQLH_F32) return launch_few_rows<IQLH_F32>(a, x, ld, b, out, stream);
+    if (dtype == IQLH_BF16) return launch_few_rows<IQLH_BF16>(a, x, ld, b, out, stream);
+    return launch_few_rows<IQLH_F16>(a, x, ld, b, out, stream);
+}
+
 hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace,
                              hipStream_t stream) {
-    if (a.rows <= 16) {
-        return by_dtype(out.dtype, [&](auto dt) {
-            hipLaunchKernelGGL((mx4_few_rows_kernel<decltype(dt)::value, 8>), dim3((uint32_t)((b.rows + 15) / 16)),
-                               dim3(512), 0, stream, a, b, out);
-        });
-    }
+    if (a.rows <= 16) return launch_few_rows<-1>(a, nullptr, 0, b, out, stream);
     if (mx4_use_tiles(a.rows, b.rows, a.cols)) {
         TileArgs t{a, b, nullptr, nullptr, out, (int)((a.rows + kTile - 1) / kTile), (int)((b.rows + kTile - 1) / kTile)};
         t.ga = (const uint32_t*)workspace;

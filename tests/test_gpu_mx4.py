@@ -366,7 +366,7 @@ def _trainer(m, S, H, H2, B, groups, params, dtype=0):
 
 
 NETS = [(16, 32, 0, 1), (128, 128, 0, 2), (42, 128, 0, 1), (256, 512, 0, 1), (100, 96, 160, 2), (1, 32, 0, 1),
-        (65, 72, 40, 2), (700, 64, 0, 1)]
+        (65, 72, 40, 2), (700, 64, 0, 1), (1000, 1024, 512, 1), (1100, 96, 0, 2), (40, 1056, 64, 1)]
 
 
 @pytest.mark.parametrize("B", [1, 67, 1000])
@@ -406,7 +406,7 @@ def test_value_network_exact_on_a_grid(m, net, B):
     tr.close()
 
 
-@pytest.mark.parametrize("net", [(128, 128, 0, 2), (256, 512, 0, 1), (100, 96, 160, 2)])
+@pytest.mark.parametrize("net", [(128, 128, 0, 2), (256, 512, 0, 1), (100, 96, 160, 2), (1500, 200, 96, 1)])
 def test_value_network_with_trained_like_weights(m, net):
     """Kaiming-sized weights: V within the oracle's bound for hidden sums
     that are off by K 2^-23 of their terms (a hidden value next to a border may
