@@ -4,7 +4,7 @@
 // "Rust Integration: gpu_iql_trainer.rs", forward_values) on the 4-bit product.
 //
 // Up to 1024 states and hidden units: two launches, the weights' quantisation
-// and the whole network (a workgroup takes 64 rows through both layers, h1 in
+// and the whole network (a workgroup takes 64 or 128 rows through both layers, h1 in
 // 4 bits in LDS, V from registers).  Wider: layer by layer on the linear
 // product.
 #include "iqlher.h"
@@ -79,19 +79,19 @@ IQLH_DEV float group_sum(float v) {
     return v + __shfl_xor(v, 32, kWave);
 }
 
-// 64 rows through the network of every group.  Layer 1: a wave's chunk of 32
+// ROWS rows through the network of every group.  Layer 1: a wave's chunk of 32
 // hidden units is one block of h1, so its scale is found and its codes go to LDS
 // from the lanes that hold its sums.  Layer 2: h2 w3 summed in the lanes, over
 // the wave's chunks, the lanes of a row and the waves, in that order.
-template <int XDT>
-__global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
+template <int ROWS, int NT, int XDT>
+__global__ __launch_bounds__(NT, NT == 256 ? 3 : 2) void iql_mx4_net_kernel(NetArgs a) {
     extern __shared__ __align__(16) uint8_t lds[];
-    __shared__ float part[4][kRows];
+    __shared__ float part[NT / 64][ROWS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * kRows;
-    const LdsRows tx(lds, a.kb4x), th(lds + mx4_lds_bytes(a.kb4x), a.kb4h);
-    mx4_rows_to_lds<XDT>((const typename MxFloat<XDT>::type*)a.x, a.ld, a.B, m0, a.S, tx);
+    const int64_t m0 = (int64_t)blockIdx.x * ROWS;
+    const LdsRows<ROWS> tx(lds, a.kb4x), th(lds + mx4_lds_bytes<ROWS>(a.kb4x), a.kb4h);
+    mx4_rows_to_lds<ROWS, NT, XDT>((const typename MxFloat<XDT>::type*)a.x, a.ld, a.B, m0, a.S, tx);
     __syncthreads();
     for (int g = 0; g < a.G; ++g) {
         uint8_t* ws = (uint8_t*)a.ws + g * a.stride;
@@ -101,15 +101,15 @@ __global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
         const float* w3 = b2 + a.H2;
         const Mx4Out o1{nullptr, IQLH_F32, 1, 0, b1}, o2{nullptr, IQLH_F32, 1, 0, b2}, o3{nullptr, IQLH_F32, 0, 0, w3};
         float bias[kFrags][4], head[kFrags][4];
-        mx4_rows_chunks(
+        mx4_rows_chunks<ROWS, NT>(
             tx, w1, a.kb4h * 32,
             [&](int64_t n0) __attribute__((always_inline)) {
 #pragma unroll
                 for (int j = 0; j < kFrags; ++j) mx4_bias4(o1, n0 + 16 * j + 4 * blk, a.H, bias[j]);
             },
-            [&](int64_t n0, mx_f4(&acc)[4][kFrags]) __attribute__((always_inline)) {
+            [&](int64_t n0, mx_f4(&acc)[ROWS / 16][kFrags]) __attribute__((always_inline)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < ROWS / 16; ++i) {
                     float y[8];
                     uint32_t amax = 0u;
 #pragma unroll
@@ -132,8 +132,8 @@ __global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
                 }
             });
         __syncthreads();
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        mx4_rows_chunks(
+        float v[ROWS / 16] = {};
+        mx4_rows_chunks<ROWS, NT>(
             th, w2, a.H2,
             [&](int64_t n0) __attribute__((always_inline)) {
 #pragma unroll
@@ -142,9 +142,9 @@ __global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
                     mx4_bias4(o3, n0 + 16 * j + 4 * blk, a.H2, head[j]);
                 }
             },
-            [&](int64_t n0, mx_f4(&acc)[4][kFrags]) __attribute__((always_inline)) {
+            [&](int64_t n0, mx_f4(&acc)[ROWS / 16][kFrags]) __attribute__((always_inline)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < ROWS / 16; ++i)
 #pragma unroll
                     for (int j = 0; j < kFrags; ++j)
 #pragma unroll
@@ -155,14 +155,17 @@ __global__ __launch_bounds__(kRowsNT, 3) void iql_mx4_net_kernel(NetArgs a) {
                         }
             });
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < ROWS / 16; ++i) {
             const float s = group_sum(v[i]);
             if (blk == 0) part[wave][16 * i + r] = s;
         }
         __syncthreads();  // also: every wave is done with this group's h1
-        if (threadIdx.x < kRows && m0 + threadIdx.x < a.B) {
+        if (threadIdx.x < ROWS && m0 + threadIdx.x < a.B) {
             const int row = threadIdx.x;
-            write_value(a.vo, g, a.B, (int)(m0 + row), part[0][row] + part[1][row] + part[2][row] + part[3][row] + w3[a.H2]);
+            float sum = part[0][row];
+#pragma unroll
+            for (int w = 1; w < NT / 64; ++w) sum += part[w][row];
+            write_value(a.vo, g, a.B, (int)(m0 + row), sum + w3[a.H2]);
         }
         __syncthreads();
     }
@@ -200,15 +203,24 @@ Layout layout(const IqlDims& d, int B) {
     return l;
 }
 
-template <int XDT>
+template <int ROWS, int NT, int XDT>
 hipError_t launch_net(const NetArgs& a, hipStream_t stream) {
-    const int bytes = mx4_lds_bytes(a.kb4x) + mx4_lds_bytes(a.kb4h);
+    const int bytes = mx4_lds_bytes<ROWS>(a.kb4x) + mx4_lds_bytes<ROWS>(a.kb4h);
+    auto kernel = iql_mx4_net_kernel<ROWS, NT, XDT>;
     if (bytes > 60 << 10) {
-        hipError_t e = hipFuncSetAttribute((const void*)iql_mx4_net_kernel<XDT>, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(iql_mx4_net_kernel<XDT>, dim3((a.B + kRows - 1) / kRows), dim3(kRowsNT), bytes, stream, a);
+    hipLaunchKernelGGL(kernel, dim3((a.B + ROWS - 1) / ROWS), dim3(NT), bytes, stream, a);
     return hipGetLastError();
+}
+// 128 rows a workgroup halve the weights' traffic from L2, 64 rows give twice
+// the workgroups: H 512, S 256, B 65536 54.6 against 63.1 us, H 1024, S 128,
+// B 65536 101 against 154; two networks of H 128, S 128, B 16384 17.3 against 13.6
+template <int XDT>
+hipError_t launch_net(const NetArgs& a, hipStream_t stream) {
+    const bool wide = a.H >= 256 && a.B >= 128 * 256;
+    return wide ? launch_net<128, 512, XDT>(a, stream) : launch_net<64, 256, XDT>(a, stream);
 }
 
 }  // namespace

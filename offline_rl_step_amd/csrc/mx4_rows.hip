@@ -8,26 +8,28 @@ namespace iqlh {
 
 namespace {
 
+constexpr int kRows = 64, kNT = 256;
+
 // Four waves; wave w takes the chunks w, w + 4, .. of 32 rows of b, 64 x 32
 // outputs each.
 template <int XDT, int ODT>
-__global__ __launch_bounds__(kRowsNT, 3) void mx4_rows_kernel(const typename MxFloat<XDT>::type* __restrict__ x, int64_t ld,
+__global__ __launch_bounds__(kNT, 3) void mx4_rows_kernel(const typename MxFloat<XDT>::type* __restrict__ x, int64_t ld,
                                                            int64_t M, Mx4Mat b, Mx4Out o, int kb4, int stream_out) {
     typedef typename MxFloat<ODT>::type T;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
     const int64_t m0 = (int64_t)blockIdx.x * kRows;
-    const LdsRows t(lds, kb4);
-    mx4_rows_to_lds<XDT>(x, ld, M, m0, b.cols, t);
+    const LdsRows<kRows> t(lds, kb4);
+    mx4_rows_to_lds<kRows, kNT, XDT>(x, ld, M, m0, b.cols, t);
     __syncthreads();
     // a chunk's outputs leave through the wave's own LDS, as rows of
     // neighbouring 16-byte units; unit v of a row lies at v ^ row, modulo the units
-    uint8_t* stage = lds + mx4_lds_bytes(kb4) + wave * (kRows * kChunk * (int)sizeof(T));
+    uint8_t* stage = lds + mx4_lds_bytes<kRows>(kb4) + wave * (kRows * kChunk * (int)sizeof(T));
     constexpr int E = 16 / sizeof(T), UNITS = kChunk / E;
     const float lowest = o.relu ? 0.f : -__builtin_huge_valf();
     float bias[kFrags][4];
-    mx4_rows_chunks(
+    mx4_rows_chunks<kRows, kNT>(
         t, b, b.rows,
         [&](int64_t n0) __attribute__((always_inline)) {
 #pragma unroll
@@ -82,7 +84,7 @@ bool mx4_rows_ok(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                            hipStream_t stream) {
-    const int kb4 = (int)((b.kb() + 3) / 4 * 4), es = out.dtype == IQLH_F32 ? 4 : 2, bytes = mx4_lds_bytes(kb4) + 4 * kRows * kChunk * es;
+    const int kb4 = (int)((b.kb() + 3) / 4 * 4), es = out.dtype == IQLH_F32 ? 4 : 2, bytes = mx4_lds_bytes<kRows>(kb4) + 4 * kRows * kChunk * es;
     // outputs that the L2s (8 x 4 MB) cannot keep for a reader are stored past
     // them: 64 MB of outputs 32.5 us, through them 36.0; no difference at 4 MB
     const int stream_out = M * b.rows * es > 32 << 20;
@@ -93,7 +95,7 @@ hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, cons
         auto kernel = mx4_rows_kernel<X, O>;
         if (bytes > 64 << 10) e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return;
-        hipLaunchKernelGGL(kernel, grid, dim3(kRowsNT), bytes, stream, (const typename MxFloat<X>::type*)x, ld, M, b, out, kb4,
+        hipLaunchKernelGGL(kernel, grid, dim3(kNT), bytes, stream, (const typename MxFloat<X>::type*)x, ld, M, b, out, kb4,
                            stream_out);
         e = hipGetLastError();
     };

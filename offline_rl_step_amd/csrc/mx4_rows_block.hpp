@@ -1,50 +1,51 @@
 // Rows of a float matrix quantised into LDS, and their products with a matrix
 // in 4 bits read from L2: the parts of the one-launch linear kernel and of the
-// value network's.  A workgroup of four waves takes kRows rows.
+// value network's.
 #pragma once
 #include "mx4_block.hpp"
 
 namespace iqlh {
 
-constexpr int kRowsNT = 256;
-constexpr int kRows = 64;     // rows a workgroup takes
+// ROWS rows and NT threads a workgroup
 constexpr int kChunk = 32;    // rows of b a wave takes at a time
 constexpr int kFrags = kChunk / 16;
 constexpr int kRowsMaxBlocks = 32;  // K <= 1024
 
-// kRows rows of kb4 blocks in LDS, kb4 a multiple of 4: codes, 16 bytes more
+// ROWS rows of kb4 blocks in LDS, kb4 a multiple of 4: codes, 16 bytes more
 // than they take between two rows so that the 16 lanes of a fragment column
 // fall on different banks, then the scales.
 __host__ __device__ constexpr int mx4_lds_row(int kb4) { return kb4 * 16 + 16; }
-__host__ __device__ constexpr int mx4_lds_bytes(int kb4) { return kRows * (mx4_lds_row(kb4) + kb4); }
+template <int ROWS>
+__host__ __device__ constexpr int mx4_lds_bytes(int kb4) { return ROWS * (mx4_lds_row(kb4) + kb4); }
+template <int ROWS>
 struct LdsRows {
     uint8_t* codes;
     uint8_t* scales;
     int kb4, rb;
-    IQLH_DEV LdsRows(uint8_t* at, int kb4_) : codes(at), scales(at + kRows * mx4_lds_row(kb4_)), kb4(kb4_), rb(mx4_lds_row(kb4_)) {}
+    IQLH_DEV LdsRows(uint8_t* at, int kb4_) : codes(at), scales(at + ROWS * mx4_lds_row(kb4_)), kb4(kb4_), rb(mx4_lds_row(kb4_)) {}
 };
 
-// Rows m0 .. m0 + kRows - 1 of x [M][ld], `cols` wide (rows past the end: the
+// Rows m0 .. m0 + ROWS - 1 of x [M][ld], `cols` wide (rows past the end: the
 // last one), quantised into t.  A thread converts 8 elements at a time, four
 // neighbouring lanes a block.
-template <int XDT>
+template <int ROWS, int NT, int XDT>
 IQLH_DEV void mx4_rows_to_lds(const typename MxFloat<XDT>::type* x, int64_t ld, int64_t M, int64_t m0, int64_t cols,
-                              const LdsRows& t) {
+                              const LdsRows<ROWS>& t) {
     const int gpr = t.kb4 * 4;  // groups of 8 a row, a multiple of 16
     constexpr int U = 4;        // groups in flight per thread
-    for (int g0 = threadIdx.x; g0 < kRows * gpr; g0 += kRowsNT * U) {
+    for (int g0 = threadIdx.x; g0 < ROWS * gpr; g0 += NT * U) {
         float v[U][8];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int e = g0 + i * kRowsNT, row = e / gpr, g = e - row * gpr;
+            const int e = g0 + i * NT, row = e / gpr, g = e - row * gpr;
             const int64_t m = m0 + row < M ? m0 + row : M - 1;
-            const int64_t left = e < kRows * gpr ? cols - g * 8 : 0;
+            const int64_t left = e < ROWS * gpr ? cols - g * 8 : 0;
             load8<XDT>(x + m * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8), v[i]);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int e = g0 + i * kRowsNT, row = e / gpr, g = e - row * gpr;
-            if (e >= kRows * gpr) break;  // the same for the whole workgroup: kRows gpr is a multiple of 256
+            const int e = g0 + i * NT, row = e / gpr, g = e - row * gpr;
+            if (e >= ROWS * gpr) break;  // the same for the whole workgroup: ROWS gpr is a multiple of NT
             uint32_t amax = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[i][j]));
@@ -55,12 +56,12 @@ IQLH_DEV void mx4_rows_to_lds(const typename MxFloat<XDT>::type* x, int64_t ld, 
     }
 }
 
-// For the chunks n0 = 32 wave, + 128, .. below n_end: acc[i][j] (rows 16 i + (lane
+// For the chunks n0 = 32 wave, + 32 waves, .. below n_end: acc[i][j] (rows 16 i + (lane
 // & 15) of t, rows n0 + 16 j + 4 (lane >> 4) + 0..3 of b) = the products' sums, then
 // done(n0, acc).  b's fragments are loaded one step ahead, over the chunks'
 // ends too; first(n0) runs before a chunk's steps (loads for done).
-template <class First, class Done>
-IQLH_DEV void mx4_rows_chunks(const LdsRows& t, const Mx4Mat& b, int64_t n_end, First&& first, Done&& done) {
+template <int ROWS, int NT, class First, class Done>
+IQLH_DEV void mx4_rows_chunks(const LdsRows<ROWS>& t, const Mx4Mat& b, int64_t n_end, First&& first, Done&& done) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
     const int steps = t.kb4 / 4;
@@ -71,30 +72,30 @@ IQLH_DEV void mx4_rows_chunks(const LdsRows& t, const Mx4Mat& b, int64_t n_end, 
         for (int j = 0; j < kFrags; ++j) RowFrag(b, n0 + 16 * j + r).load(s * 4 + blk, bn[j], bsn[j]);
     };
     if (wave * kChunk < n_end) fetch(wave * kChunk, 0);
-    for (int64_t n0 = (int64_t)wave * kChunk; n0 < n_end; n0 += 4 * kChunk) {
+    for (int64_t n0 = (int64_t)wave * kChunk; n0 < n_end; n0 += NT / 64 * kChunk) {
         first(n0);
-        mx_f4 acc[4][kFrags];
+        mx_f4 acc[ROWS / 16][kFrags];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < ROWS / 16; ++i)
 #pragma unroll
             for (int j = 0; j < kFrags; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
         for (int s = 0; s < steps; ++s) {
-            uint4 bv[kFrags], av[4];
-            uint32_t bs[kFrags], as[4];
+            uint4 bv[kFrags], av[ROWS / 16];
+            uint32_t bs[kFrags], as[ROWS / 16];
 #pragma unroll
             for (int j = 0; j < kFrags; ++j) {
                 bv[j] = bn[j];
                 bs[j] = bsn[j];
             }
             if (s + 1 < steps) fetch(n0, s + 1);
-            else if (n0 + 4 * kChunk < n_end) fetch(n0 + 4 * kChunk, 0);
+            else if (n0 + NT / 64 * kChunk < n_end) fetch(n0 + NT / 64 * kChunk, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < ROWS / 16; ++i) {
                 av[i] = *(const uint4*)(t.codes + (16 * i + r) * t.rb + (s * 4 + blk) * 16);
                 as[i] = t.scales[(16 * i + r) * t.kb4 + s * 4 + blk];
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < ROWS / 16; ++i)
 #pragma unroll
                 for (int j = 0; j < kFrags; ++j) acc[i][j] = mx4_mma(bv[j], av[i], acc[i][j], bs[j], as[i]);
         }

@@ -406,6 +406,33 @@ def test_value_network_exact_on_a_grid(m, net, B):
     tr.close()
 
 
+@pytest.mark.parametrize("net", [(256, 512, 0, 1), (33, 288, 257, 2), (1024, 1024, 0, 1)])
+def test_value_network_of_many_rows_exact_on_a_grid(m, net):
+    """The same on a batch large enough for the 128-row workgroups, ragged."""
+    import torch
+    S, H, H2, G = net
+    H2v, B = H2 or H, 32768 + 77
+    g = np.random.default_rng(S + H + 1)
+    params = []
+    for _ in range(G):
+        w1 = g.choice([0.0, 0.0, 0.0, 0.5, -0.5, 1.0], (H, S)) * (g.random((H, S)) < 32 / S)
+        w2 = g.choice([0.0] * 20 + [0.5, -0.5, 1.0], (H2v, H))
+        params.append(np.concatenate([w1.ravel(), g.integers(-4, 5, H) * 0.5, w2.ravel(), g.integers(-4, 5, H2v) * 0.5,
+                                      g.choice([0.0, 0.25, -0.25], H2v), [0.5]]))
+    x = g.choice([0.0, 0.5, 1.0, -1.0, 2.0], (B, S))
+    tr = _trainer(m, S, H, H2, B, G, params, m.BF16)
+    v = torch.zeros((G, B), device=dev())
+    ws = tr.forward_values_mx4_workspace(B)
+    ws.fill_(0xFF)
+    tr.forward_values_mx4(_float(x, "bfloat16", pad=1), B, v, ws)
+    sync()
+    rows = np.unique(np.concatenate([np.arange(200), g.integers(0, B, 300), np.arange(B - 200, B)]))
+    for k in range(G):
+        want = ref.value_network(params[k], S, H, H2v, x[rows])
+        assert np.array_equal(_f64(v[k])[rows], want)
+    tr.close()
+
+
 @pytest.mark.parametrize("net", [(128, 128, 0, 2), (256, 512, 0, 1), (100, 96, 160, 2), (1500, 200, 96, 1)])
 def test_value_network_with_trained_like_weights(m, net):
     """Kaiming-sized weights: V within the oracle's bound for hidden sums
