@@ -517,8 +517,9 @@ int iqlh_tensor_set_fill(const void* const* d_tensors, const int64_t* lens, cons
  *   d_flags    device sticky flag word or NULL: IQLH_FLAG_NONFINITE_GRAD when
  *              the set holds a NaN or an infinity.
  *   workspace  device, >= iqlh_grad_norm_workspace_bytes(set), 8-byte
- *              aligned, no initial contents required; calls that overlap in
- *              time need one each.
+ *              aligned, its first 64 bytes 0 before the first call that takes
+ *              it (every call leaves them 0); calls that overlap in time need
+ *              one each.
  * The results do not depend on timing: every sum has a fixed order. */
 int iqlh_grad_norm_workspace_bytes(const iqlh_tensor_set* set, size_t* bytes);
 int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, float* out_each,

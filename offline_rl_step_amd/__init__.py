@@ -173,15 +173,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# handle of the current stream without building a Stream object (0.1 us
-# against 3 us, which is as long as a launch takes)
+# Current device and the handle of its current stream without building a
+# Stream object (0.1 us each against 3 us, which is as long as a launch takes)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+if _get_device is None:
+    _raw_stream, _get_device = None, torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is None:
-        if _raw_stream is not None:
-            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(_raw_stream(_get_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -379,8 +382,8 @@ def _need_current(device):
     """The library enqueues on the current device."""
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: the kernels read device memory")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device.index != _get_device():  # tensors on it exist, so CUDA is initialised
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{_get_device()}")
 
 
 class TensorSet:
@@ -413,6 +416,7 @@ class TensorSet:
         # a copy from pageable memory: complete when it returns, for any stream
         self.table = host[:self.struct.table_bytes].to(self.device)
         self.struct.d_table = self.table.data_ptr()
+        self.ref = ctypes.byref(self.struct)
         self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
 
     @property
@@ -429,10 +433,12 @@ class TensorSet:
 
 
 def grad_norm_workspace(tensor_set):
-    """A workspace for grad_norm / grad_clip calls on the set."""
+    """A workspace for grad_norm / grad_clip calls on the set (its counter at 0)."""
     out = ctypes.c_size_t()
     _check(_lib_norm_ws(ctypes.byref(tensor_set.struct), ctypes.byref(out)), "iqlh_grad_norm_workspace_bytes")
-    return torch.empty(out.value, dtype=torch.uint8, device=tensor_set.device)
+    ws = torch.empty(out.value, dtype=torch.uint8, device=tensor_set.device)
+    ws[:64].zero_()
+    return ws
 
 
 def _need_aux(device, workspace, flags):
@@ -451,7 +457,7 @@ def grad_norm(tensor_set, out_norm, workspace, kind=NORM_L2, out_each=None, flag
     if out_each is not None:
         _need_f32(out_each, s.struct.count, s.device, "out_each")
     _need_aux(s.device, workspace, flags)
-    _check(_lib_grad_norm(ctypes.byref(s.struct), kind, _ptr(out_norm), _ptr(out_each), _ptr(flags), _ptr(workspace),
+    _check(_lib_grad_norm(s.ref, kind, out_norm.data_ptr(), _ptr(out_each), _ptr(flags), workspace.data_ptr(),
                           workspace.numel() * workspace.element_size(), _stream(stream)), "iqlh_grad_norm")
 
 
@@ -465,8 +471,8 @@ def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None,
         _need_f32(out_flat, s.numel, s.device, "out_flat")
         _need(not s.overlaps(out_flat[:s.numel]), "out_flat shares memory with a tensor of the set")
     _need_aux(s.device, workspace, flags)
-    _check(_lib_grad_clip(ctypes.byref(s.struct), kind, max_norm, _ptr(out_flat), _ptr(out), _ptr(flags),
-                          _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check(_lib_grad_clip(s.ref, kind, max_norm, _ptr(out_flat), out.data_ptr(), _ptr(flags), workspace.data_ptr(),
+                          workspace.numel() * workspace.element_size(), _stream(stream)),
            "iqlh_grad_clip")
 
 
@@ -485,6 +491,7 @@ class Mx4:
         self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
         self.device = codes.device
         self.struct = Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, cols)
+        self.ref = ctypes.byref(self.struct)
 
 
 def mx4_empty(rows, cols, axis=1, device=None):
@@ -518,7 +525,7 @@ def mx4_quantize(x, out, axis=1, stream=None):
     _need_current(out.device)
     r, c = (out.rows, out.cols) if axis == 1 else (out.cols, out.rows)
     dt, ld = _matrix(x, r, c, out.device, "x")
-    _check(_lib_mx4_quantize(_ptr(x), dt, ld, 1 - axis, ctypes.byref(out.struct), _stream(stream)),
+    _check(_lib_mx4_quantize(x.data_ptr(), dt, ld, 1 - axis, out.ref, _stream(stream)),
            "iqlh_mx4_quantize")
 
 
@@ -526,7 +533,7 @@ def mx4_dequantize(q, out, stream=None):
     """Values of q into out [rows, cols] (float32, bfloat16, float16)."""
     _need_current(q.device)
     dt, ld = _matrix(out, q.rows, q.cols, q.device, "out")
-    _check(_lib_mx4_dequantize(ctypes.byref(q.struct), _ptr(out), dt, ld, _stream(stream)), "iqlh_mx4_dequantize")
+    _check(_lib_mx4_dequantize(q.ref, out.data_ptr(), dt, ld, _stream(stream)), "iqlh_mx4_dequantize")
 
 
 def mx4_matmul_workspace(m, n, k, device=None):
@@ -550,8 +557,8 @@ def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
     if a.device != b.device:
         raise ValueError(f"a is on {a.device}, b on {b.device}")
     dt, ld = _need_product(a.rows, b, out, workspace, bias)
-    _check(_lib_mx4_matmul(ctypes.byref(a.struct), ctypes.byref(b.struct), _ptr(bias), int(relu), _ptr(out), dt, ld,
-                           _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check(_lib_mx4_matmul(a.ref, b.ref, _ptr(bias), int(relu), out.data_ptr(), dt, ld, workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), _stream(stream)),
            "iqlh_mx4_matmul")
 
 
@@ -559,8 +566,8 @@ def mx4_linear(x, b, out, workspace, bias=None, relu=False, stream=None):
     """mx4_matmul with a = x [m, k] (float32, bfloat16, float16) quantised on the way."""
     dt, ld = _need_product(x.shape[0], b, out, workspace, bias)
     xdt, xld = _matrix(x, x.shape[0], b.cols, b.device, "x")
-    _check(_lib_mx4_linear(_ptr(x), xdt, xld, x.shape[0], ctypes.byref(b.struct), _ptr(bias), int(relu), _ptr(out),
-                           dt, ld, _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+    _check(_lib_mx4_linear(x.data_ptr(), xdt, xld, x.shape[0], b.ref, _ptr(bias), int(relu), out.data_ptr(), dt, ld,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
            "iqlh_mx4_linear")
 
 

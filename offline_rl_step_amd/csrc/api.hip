@@ -631,7 +631,7 @@ int iqlh_tensor_set_fill(const void* const* d_tensors, const int64_t* lens, cons
 int iqlh_grad_norm_workspace_bytes(const iqlh_tensor_set* set, size_t* bytes) {
     if (!set || !bytes) return fail(IQLH_EINVAL, "iqlh_grad_norm_workspace_bytes: NULL argument");
     if (set->pieces < 0) return fail(IQLH_EINVAL, "iqlh_grad_norm_workspace_bytes: set not filled");
-    *bytes = sizeof(uint64_t) * ((size_t)kNormBlocks + 4 * (size_t)set->pieces);
+    *bytes = sizeof(uint64_t) * (8 + (size_t)kNormBlocks + 4 * (size_t)set->pieces);  // 64 bytes of counter first
     return IQLH_OK;
 }
 
@@ -649,7 +649,8 @@ static int make_tensor_set_args(const char* who, const iqlh_tensor_set* set, int
     a->first = (const int32_t*)(a->pieces + set->pieces);
     a->npieces = set->pieces;
     a->count = set->count;
-    a->part = (uint64_t*)workspace;
+    a->arrived = (int32_t*)workspace;
+    a->part = (uint64_t*)workspace + 8;
     a->each = nullptr;
     a->flags = d_flags;
     return IQLH_OK;

@@ -233,6 +233,7 @@ struct TensorSetArgs {
     const TensorPiece* pieces;
     const int32_t* first;  // [count + 1]
     int32_t npieces, count;
+    int32_t* arrived;      // workgroups that have finished; 0 between launches
     uint64_t* part;        // [kNormBlocks] block sums (binary64 bits) or maxima (binary32 bits)
     uint64_t* each;        // [npieces][4] the same of every wave of every piece, or null
     int32_t* flags;

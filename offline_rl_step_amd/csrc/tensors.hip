@@ -9,11 +9,12 @@
 // whatever the tensors' sizes are, and one launch serves any number of
 // tensors and any mix of types.
 //   1. norm pass: a workgroup takes the pieces b, b + grid, ..; block sums (and
-//      with per-tensor norms each wave's sum of each piece) to the workspace;
-//   2. finish: block 0 adds the block sums; one wave per tensor adds its
-//      pieces' sums;   or
-//   2. scale pass: every workgroup adds the block sums itself, in the same
-//      order, and scales its pieces.
+//      with per-tensor norms each wave's sum of each piece) to the workspace,
+//      added up by the workgroup that finishes last;
+//   2. for many tensors' own norms a launch with a workgroup per tensor adds
+//      them up instead;
+//   2. for a clip the scale pass: every workgroup adds the block sums itself, in
+//      the same order, and scales its pieces.
 // No atomics on sums: every order is fixed, results repeat bit for bit.
 //
 // Squares and sums are held in binary64: a product of two binary32 values is
@@ -97,16 +98,20 @@ template <> struct Stat<IQLH_NORM_MAX> {
     IQLH_DEV double norm() const { return (double)__uint_as_float(s); }
 };
 
-template <int KIND>
-IQLH_DEV Stat<KIND> wave_join(Stat<KIND> v) {
+// joined over 2 TOP neighbouring lanes, in all of them
+template <int TOP, int KIND>
+IQLH_DEV Stat<KIND> lanes_join(Stat<KIND> v) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
+    for (int o = TOP; o > 0; o >>= 1) {
         const uint64_t b = v.bits();
         const uint32_t lo = __shfl_xor((uint32_t)b, o, kWave), hi = __shfl_xor((uint32_t)(b >> 32), o, kWave);
         v.join((uint64_t)hi << 32 | lo);
     }
     return v;
 }
+
+template <int KIND>
+IQLH_DEV Stat<KIND> wave_join(Stat<KIND> v) { return lanes_join<32>(v); }
 
 template <int KIND>
 IQLH_DEV Stat<KIND> block_join(Stat<KIND> v, uint64_t* red) {
@@ -162,9 +167,59 @@ IQLH_DEV void piece_stat(const TensorPiece& p, Stat<KIND>& a0, Stat<KIND>& a1) {
     if (e >= 0) a0.add(E::load((const void*)p.ptr, e));
 }
 
+IQLH_DEV bool finite64(double x) { return fabs(x) < __longlong_as_double(0x7FF0000000000000ll); }
+
+template <int KIND>
+IQLH_DEV double norm_of_parts(const uint64_t* part, int nb, uint64_t* red) {
+    Stat<KIND> s;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < nb; i += kNT) s.join(part[i]);
+    return block_join(s, red).norm();
+}
+
+// Workspace values that another workgroup of the same launch reads: agent-scope
+// atomics, which act past the XCD's own L2.
+IQLH_DEV void put_shared(uint64_t* p, uint64_t v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+IQLH_DEV uint64_t get_shared(const uint64_t* p) {
+    return __hip_atomic_load((uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The last workgroup of a norm launch: the whole norm, and with EACH the
+// tensors' own, 16 lanes a tensor.
 template <int KIND, bool EACH>
-__global__ __launch_bounds__(kNT) void grad_norm_kernel(TensorSetArgs a) {
+IQLH_DEV void finish_norm(const TensorSetArgs& a, int nb, float* out_norm, float* out_each, uint64_t* red) {
+    Stat<KIND> s;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < nb; i += kNT) s.join(get_shared(a.part + i));
+    const double n = block_join(s, red).norm();
+    if (threadIdx.x == 0) {
+        *out_norm = (float)n;
+        if (!finite64(n)) set_flag(a.flags, IQLH_FLAG_NONFINITE_GRAD);
+    }
+    if constexpr (EACH) {
+        for (int t0 = 0; t0 < a.count; t0 += kNT / 16) {  // every lane takes part in the exchanges
+            const int t = t0 + threadIdx.x / 16;
+            Stat<KIND> v;
+            if (t < a.count) {
+                const int end = a.first[t + 1] * 4;
+#pragma unroll 4
+                for (int i = a.first[t] * 4 + (threadIdx.x & 15); i < end; i += 16) v.join(get_shared(a.each + i));
+            }
+            v = lanes_join<8>(v);
+            if (t < a.count && (threadIdx.x & 15) == 0) out_each[t] = (float)v.norm();
+        }
+    }
+}
+
+// ONE: the workgroup that finishes last also adds up, so that the norm takes
+// one launch.  Every wave waits for its stores to the workspace (agent scope, so
+// they are in place then), the workgroup's barrier orders them before its count,
+// and whoever counts last finds all of them.  The count is left at 0.
+template <int KIND, bool EACH, bool ONE>
+__global__ __launch_bounds__(kNT) void grad_norm_kernel(TensorSetArgs a, float* __restrict__ out_norm,
+                                                        float* __restrict__ out_each) {
     __shared__ uint64_t red[kNT / kWave];
+    __shared__ int last;
     Stat<KIND> total;
     for (int k = blockIdx.x; k < a.npieces; k += gridDim.x) {
         const TensorPiece p = a.pieces[k];
@@ -176,22 +231,28 @@ __global__ __launch_bounds__(kNT) void grad_norm_kernel(TensorSetArgs a) {
         total.join(s0.bits());
         if (EACH) {
             const Stat<KIND> w = wave_join(s0);
-            if ((threadIdx.x & 63) == 0) a.each[(int64_t)k * 4 + threadIdx.x / kWave] = w.bits();
+            if ((threadIdx.x & 63) == 0) {
+                uint64_t* e = a.each + (int64_t)k * 4 + threadIdx.x / kWave;
+                if (ONE) put_shared(e, w.bits());
+                else *e = w.bits();
+            }
         }
     }
     total = block_join(total, red);
-    if (threadIdx.x == 0) a.part[blockIdx.x] = total.bits();
+    if (!ONE) {
+        if (threadIdx.x == 0) a.part[blockIdx.x] = total.bits();
+        return;
+    }
+    if (threadIdx.x == 0) put_shared(a.part + blockIdx.x, total.bits());
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(a.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    if (threadIdx.x == 0) __hip_atomic_store(a.arrived, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    finish_norm<KIND, EACH>(a, gridDim.x, out_norm, out_each, red);
 }
-
-template <int KIND>
-IQLH_DEV double norm_of_parts(const uint64_t* part, int nb, uint64_t* red) {
-    Stat<KIND> s;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < nb; i += kNT) s.join(part[i]);
-    return block_join(s, red).norm();
-}
-
-IQLH_DEV bool finite64(double x) { return fabs(x) < __longlong_as_double(0x7FF0000000000000ll); }
 
 // Block 0: the whole norm.  Block 1 + t: tensor t.
 template <int KIND>
@@ -308,27 +369,29 @@ __global__ __launch_bounds__(kNT) void grad_scale_kernel(TensorSetArgs a, int nb
 
 int norm_blocks(int npieces) { return npieces < 1 ? 1 : npieces < kNormBlocks ? npieces : kNormBlocks; }
 
-template <int KIND>
-hipError_t norm_pass(const TensorSetArgs& a, hipStream_t stream) {
-    const dim3 grid(norm_blocks(a.npieces)), block(kNT);
-    if (a.each) hipLaunchKernelGGL((grad_norm_kernel<KIND, true>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((grad_norm_kernel<KIND, false>), grid, block, 0, stream, a);
+template <int KIND, bool EACH, bool ONE>
+hipError_t norm_pass(const TensorSetArgs& a, float* out_norm, float* out_each, hipStream_t stream) {
+    hipLaunchKernelGGL((grad_norm_kernel<KIND, EACH, ONE>), dim3(norm_blocks(a.npieces)), dim3(kNT), 0, stream, a, out_norm,
+                       out_each);
     return hipGetLastError();
 }
 
+// One launch for the whole norm, and for the tensors' own where one workgroup
+// adds up their pieces as fast as a launch of its own would.
 template <int KIND>
 hipError_t norm_launch(const TensorSetArgs& a, float* out_norm, float* out_each, hipStream_t stream) {
-    hipError_t e = norm_pass<KIND>(a, stream);
+    if (!out_each) return norm_pass<KIND, false, true>(a, out_norm, out_each, stream);
+    if (a.count <= 64 && a.npieces <= 512) return norm_pass<KIND, true, true>(a, out_norm, out_each, stream);
+    hipError_t e = norm_pass<KIND, true, false>(a, out_norm, out_each, stream);
     if (e != hipSuccess) return e;
-    const int grid = 1 + (out_each ? a.count : 0);
-    hipLaunchKernelGGL(grad_norm_finish_kernel<KIND>, dim3(grid), dim3(kNT), 0, stream, a, norm_blocks(a.npieces),
+    hipLaunchKernelGGL(grad_norm_finish_kernel<KIND>, dim3(1 + a.count), dim3(kNT), 0, stream, a, norm_blocks(a.npieces),
                        out_norm, out_each);
     return hipGetLastError();
 }
 
 template <int KIND>
 hipError_t clip_launch(const TensorSetArgs& a, float max_norm, float* flat, float* out, hipStream_t stream) {
-    hipError_t e = norm_pass<KIND>(a, stream);
+    hipError_t e = norm_pass<KIND, false, false>(a, nullptr, nullptr, stream);
     if (e != hipSuccess) return e;
     const int nb = norm_blocks(a.npieces);
     hipLaunchKernelGGL(grad_scale_kernel<KIND>, dim3(nb), dim3(kNT), 0, stream, a, nb, max_norm, flat, out);

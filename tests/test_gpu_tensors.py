@@ -52,11 +52,12 @@ def _norm(m, ts, kind, each=True, flags=None, stream=None):
     import torch
     s = m.TensorSet(ts)
     ws = m.grad_norm_workspace(s)
-    ws.fill_(0xA5)
+    ws[64:].fill_(0xA5)
     out = torch.full((1,), -7.0, device=dev())
     oe = torch.full((len(ts),), -7.0, device=dev()) if each else None
     m.grad_norm(s, out, ws, kind=kind, out_each=oe, flags=flags, stream=stream)
     sync()
+    assert int(ws[:64].count_nonzero()) == 0  # as every call leaves it
     return float(out[0]), None if oe is None else oe.cpu().numpy()
 
 
