@@ -259,7 +259,6 @@ struct Mx4Out {
 // workspace of a product: the left operand quantised on the way, then the
 // partial sums of a split summed axis
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
-bool mx4_use_tiles(int64_t M, int64_t N, int64_t K);
 // many rows times a small b, quantisation and product in one launch
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,

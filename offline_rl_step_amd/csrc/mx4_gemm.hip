@@ -117,18 +117,15 @@ hipError_t launch_few_rows(const Mx4Mat& a, const void* x, int64_t ld, const Mx4
     });
 }
 
-// ------------------------------------------------- tiles from global memory
-// A wave computes 64 x 64 outputs, 4 x 4 fragments.  WK = 1: the workgroup's
-// four waves take 128 x 128 outputs; WK = 4: they take the same 64 x 64 and
-// every fourth k step each, and add their sums through LDS in wave order.
-template <int DT, int WK>
+// --------------------------------------------- short sums, straight from memory
+// A wave computes 64 x 64 outputs, the workgroup's four 128 x 128, fragments
+// from L2: for K of a step or two, where a ring would not fill.
+template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o, int n_tiles) {
-    constexpr int T = WK == 1 ? 128 : 64;
-    __shared__ mx_f4 part[WK == 1 ? 1 : 4][WK == 1 ? 1 : 16][WK == 1 ? 1 : 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * T + (WK == 1 ? (wave >> 1) * 64 : 0);
-    const int64_t n0 = (int64_t)(blockIdx.x % n_tiles) * T + (WK == 1 ? (wave & 1) * 64 : 0);
+    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * 128 + (wave >> 1) * 64;
+    const int64_t n0 = (int64_t)(blockIdx.x % n_tiles) * 128 + (wave & 1) * 64;
     const RowFrag fa[4] = {RowFrag(a, m0 + r), RowFrag(a, m0 + 16 + r), RowFrag(a, m0 + 32 + r), RowFrag(a, m0 + 48 + r)};
     const RowFrag fb[4] = {RowFrag(b, n0 + r), RowFrag(b, n0 + 16 + r), RowFrag(b, n0 + 32 + r), RowFrag(b, n0 + 48 + r)};
     mx_f4 acc[4][4];
@@ -137,7 +134,7 @@ __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
     const int64_t steps = (a.kb() + 3) / 4;
-    for (int64_t s = WK == 1 ? 0 : wave; s < steps; s += WK) {
+    for (int64_t s = 0; s < steps; ++s) {
         uint4 av[4], bv[4];
         uint32_t as[4], bs[4];
 #pragma unroll
@@ -151,28 +148,110 @@ __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4
             for (int j = 0; j < 4; ++j) acc[i][j] = mx4_mma(bv[j], av[i], acc[i][j], bs[j], as[i]);
     }
     const bool wide = mx4_wide_rows<DT>(o);
-    auto store = [&](int i, int j, mx_f4 v) {
-        const int64_t m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * blk;
-        if (m < a.rows) mx4_store4<DT>(o, m, n, (int)(b.rows - n < 4 ? b.rows - n : 4), v, wide);
-    };
-    if constexpr (WK == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) store(i, j, acc[i][j]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[wave][4 * i + j][lane] = acc[i][j];
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // wave w: fragments (w, 0..3)
-            mx_f4 v = part[0][4 * wave + j][lane];
-#pragma unroll
-            for (int w = 1; w < 4; ++w) v += part[w][4 * wave + j][lane];
-            store(wave, j, v);
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * blk;
+            if (m < a.rows) mx4_store4<DT>(o, m, n, (int)(b.rows - n < 4 ? b.rows - n : 4), acc[i][j], wide);
         }
+}
+
+// ------------------------------------------------------- waves that split k
+// A workgroup takes 16 MF x 16 NF outputs, its eight waves every eighth k step
+// each, the next step's fragments on their way while this one's are
+// multiplied.  The sums meet in LDS: waves 4..7 add to waves 0..3, then those
+// four are added in wave order.  For few outputs, where what counts is how
+// many loads are in flight over the chip.
+template <int DT, int MF, int NF>
+__global__ __launch_bounds__(512) void mx4_split_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o, int n_tiles) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    mx_f4(*part)[MF * NF][64] = (mx_f4(*)[MF * NF][64])lds;  // [4]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, blk = lane >> 4;
+    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * (16 * MF), n0 = (int64_t)(blockIdx.x % n_tiles) * (16 * NF);
+    const int64_t kb = a.kb();
+    const uint4* ac[MF];
+    const uint8_t* as_[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        const RowFrag f(a, m0 + 16 * i + r);
+        ac[i] = f.codes;
+        as_[i] = f.scales;
+    }
+    const uint4* bc[NF];
+    const uint8_t* bs_[NF];
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+        const RowFrag f(b, n0 + 16 * j + r);
+        bc[j] = f.codes;
+        bs_[j] = f.scales;
+    }
+    struct Frags {
+        uint4 a[MF], b[NF];
+        uint32_t as[MF], bs[NF];
+    } f[2];
+    auto load = [&](int64_t s, Frags& g) __attribute__((always_inline)) {
+        const int64_t block = s * 4 + blk;
+        const bool in = block < kb;
+        const int64_t at = in ? block : 0;
+        const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            g.b[j] = bc[j][at];
+            g.bs[j] = bs_[j][at];
+        }
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const uint4 v = ac[i][at];
+            g.a[i] = uint4{v.x & keep, v.y & keep, v.z & keep, v.w & keep};  // zeros behind the last block
+            g.as[i] = in ? as_[i][at] : 127u;
+        }
+#pragma unroll
+        for (int j = 0; j < NF; ++j) g.bs[j] = in ? g.bs[j] : 127u;
+    };
+    mx_f4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
+    auto mma = [&](const Frags& g) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) acc[i][j] = mx4_mma(g.b[j], g.a[i], acc[i][j], g.bs[j], g.as[i]);
+    };
+    const int64_t steps = (kb + 3) / 4;
+    load(wave, f[0]);
+    int64_t s = wave;
+    for (; s + 8 < steps; s += 16) {
+        load(s + 8, f[1]);
+        mma(f[0]);
+        load(s + 16, f[0]);  // zeros behind the last step
+        mma(f[1]);
+    }
+    if (s < steps) mma(f[0]);
+    if (wave >= 4) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) part[wave - 4][NF * i + j][lane] = acc[i][j];
+    }
+    __syncthreads();
+    if (wave < 4) {
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+            for (int j = 0; j < NF; ++j) part[wave][NF * i + j][lane] += acc[i][j];
+    }
+    __syncthreads();
+    const bool wide = mx4_wide_rows<DT>(o);
+    for (int e = wave; e < MF * NF; e += 8) {
+        mx_f4 v = part[0][e][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) v += part[w][e][lane];
+        const int64_t m = m0 + 16 * (e / NF) + r, n = n0 + 16 * (e % NF) + 4 * blk;
+        if (m < a.rows) mx4_store4<DT>(o, m, n, (int)(b.rows - n < 4 ? b.rows - n : 4), v, wide);
     }
 }
 
@@ -216,13 +295,11 @@ __global__ __launch_bounds__(kNT) void mx4_scale_groups_kernel(Mx4Mat a, Mx4Mat 
 
 __device__ __align__(16) const uint4 kZeroChunk[1] = {};
 
-constexpr int kTile = 256;
-constexpr int kTNT = 512;
-constexpr int kStageBytes = 2 * kTile * 128;             // codes of both operands, 256 k
-constexpr int kScaleBytes = 2 * (kTile / 32) * 256;
-constexpr int kBufBytes = kStageBytes + kScaleBytes;     // two of them in LDS
-constexpr int kCodeCopies = kStageBytes / 16 / kTNT;     // asynchronous copies a thread issues per step
-constexpr int kScaleCopies = kScaleBytes / 4 / kTNT;
+// Workgroups of TILE x TILE outputs, 2 TILE threads
+constexpr int stage_bytes(int tile) { return 2 * tile * 128; }  // codes of both operands, 256 k
+constexpr int buf_bytes(int tile) { return stage_bytes(tile) + 2 * (tile / 32) * 256; }  // and scales; two in LDS
+constexpr int kCodeCopies = 8;   // asynchronous copies a thread issues per step: 2 TILE 128 / 16 / (2 TILE)
+constexpr int kScaleCopies = 2;  // 2 TILE 8 / 4 / (2 TILE)
 
 template <int N>
 IQLH_DEV void wait_vm() {
@@ -258,23 +335,22 @@ struct TileArgs {
     int m_tiles, n_tiles;
 };
 
-// The workgroup's 256 x 256 sums to memory: through LDS, so that a row leaves
-// as neighbouring 16-byte stores and not as the matrix instruction's 4-element
-// pieces.  Waves 0..3 hold the rows 0..127 of the tile, 4..7 the others; a
-// 32-bit tile passes in two halves of 128 rows.  A row's 16-byte unit v lies at
-// v ^ (row & 7).
-template <int DT>
-IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* lds, int64_t m0, int64_t n0, int wm,
+// The workgroup's sums to memory: through LDS, so that a row leaves as
+// neighbouring 16-byte stores and not as the matrix instruction's 4-element
+// pieces.  A 32-bit tile of 256 passes in two halves of 128 rows (one of the
+// waves' rows each).  A row's 16-byte unit v lies at v ^ (row & 7).
+template <int DT, int TILE, int FA>
+IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[FA][2], uint8_t* lds, int64_t m0, int64_t n0, int wm,
                          int wn) {
     typedef typename MxFloat<DT>::type T;
-    constexpr int HALVES = DT == IQLH_F32 ? 2 : 1, ROWS = kTile / HALVES;
-    constexpr int E = 16 / sizeof(T), UNITS = kTile / E;  // elements of a unit, units of a row
+    constexpr int HALVES = TILE * TILE * (int)sizeof(T) > 2 * buf_bytes(TILE) ? 2 : 1, ROWS = TILE / HALVES;
+    constexpr int E = 16 / sizeof(T), UNITS = TILE / E;  // elements of a unit, units of a row
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const Mx4Out& o = t.o;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
         if (half) __syncthreads();
-        if (HALVES == 1 || wm / 128 == half) {
+        if (HALVES == 1 || wm / ROWS == half) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -284,7 +360,7 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) bias[e] = o.bias && n0 + n + e < t.b.rows ? o.bias[n0 + n + e] : 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < FA; ++i) {
                         const int row = (HALVES == 1 ? wm : 0) + 32 * i + r;
                         float y[4];
 #pragma unroll
@@ -292,18 +368,18 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* 
                             y[e] = acc[i][j][4 * g + e] + bias[e];
                             if (o.relu && y[e] < 0.f) y[e] = 0.f;  // a NaN stays
                         }
-                        uint8_t* p = lds + row * (kTile * sizeof(T)) + 16 * ((n / E) ^ (row & 7)) + (n % E) * sizeof(T);
+                        uint8_t* p = lds + row * (TILE * sizeof(T)) + 16 * ((n / E) ^ (row & 7)) + (n % E) * sizeof(T);
                         mx4_put4<DT>((T*)p, y);
                     }
                 }
         }
         __syncthreads();
 #pragma unroll 4
-        for (int c = threadIdx.x; c < ROWS * UNITS; c += kTNT) {
+        for (int c = threadIdx.x; c < ROWS * UNITS; c += 2 * TILE) {
             const int row = c / UNITS, v = c % UNITS;
             const int64_t m = m0 + half * ROWS + row, n = n0 + v * E;
             if (m >= t.a.rows || n >= t.b.rows) continue;
-            const uint4 w = *(const uint4*)(lds + row * (kTile * sizeof(T)) + 16 * (v ^ (row & 7)));
+            const uint4 w = *(const uint4*)(lds + row * (TILE * sizeof(T)) + 16 * (v ^ (row & 7)));
             T* p = (T*)o.p + m * o.ld + n;
             if (n + E <= t.b.rows) {
                 typedef T tu __attribute__((ext_vector_type(E), aligned(sizeof(T))));
@@ -317,8 +393,9 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* 
     }
 }
 
-// Eight waves, 2 x 4, each 128 x 64 outputs (4 x 2 fragments of 32 x 32, 128
-// registers of sums), two waves per SIMD.  A step is 256 k, 128 bytes of a
+// TILE 256: eight waves, 2 x 4, each 128 x 64 outputs (4 x 2 fragments of
+// 32 x 32, 128 registers of sums), one workgroup to a compute unit.  TILE 128: four
+// waves, 2 x 2, each 64 x 64, two workgroups.  A step is 256 k, 128 bytes of a
 // row: whole cache lines per request.  Two buffers: in the last quarter of
 // step s every wave waits for its copies of step s + 1, passes the barrier
 // (behind which all reads of step s's buffer are done), issues step s + 2 into
@@ -326,8 +403,10 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[4][2], uint8_t* 
 // instructions of the quarter run.  A row's chunk u (16 bytes) lies at
 // 128 row + 16 (u ^ ((row >> 1) & 7)): 16 lanes of a fragment column fall on
 // all 64 banks.
-template <int DT>
-__global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
+template <int DT, int TILE>
+__global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
+    constexpr int NT = 2 * TILE, FA = TILE / 64, WN = TILE / 64;  // threads, row fragments a wave, waves along n
+    constexpr int STAGE = stage_bytes(TILE), BUF = buf_bytes(TILE);
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -347,15 +426,15 @@ __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
     const int tm = band * 4 + in_band % rows_in, tn = in_band / rows_in;
     const int64_t kb = t.a.kb();
     const int steps = (int)((kb + 7) / 8);
-    const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
-    // copy addresses: chunk c = i 512 + tid fills place c & 7 of row c >> 3
+    const int64_t m0 = (int64_t)tm * TILE, n0 = (int64_t)tn * TILE;
+    // copy addresses: chunk c = i NT + tid fills place c & 7 of row c >> 3
     const int u = (tid & 7) ^ ((tid >> 4) & 7);
     const uint8_t* abase = t.a.codes + m0 * kb * 16;
     const uint8_t* bbase = t.b.codes + n0 * kb * 16;
     uint32_t off[kCodeCopies];  // b's rows, then a's
 #pragma unroll
     for (int i = 0; i < kCodeCopies; ++i) {
-        const int row = (i & 3) * 64 + (tid >> 3);
+        const int row = (i & 3) * (TILE / 4) + (tid >> 3);
         const int64_t left = (i < 4 ? t.b.rows - n0 : t.a.rows - m0) - 1;
         off[i] = (uint32_t)((row < left ? row : (int)left) * kb * 16) + 16u * u;
     }
@@ -369,50 +448,50 @@ __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
     // every step issues the same copies, those behind the last one from the
     // zero chunk, so that the loop has no branch
     auto issue = [&](int s) __attribute__((always_inline)) {
-        const uint32_t dst = lds_at + (s & 1) * kBufBytes;
+        const uint32_t dst = lds_at + (s & 1) * BUF;
         const int64_t k0 = (int64_t)s * 128;
         const bool in = 8 * s + u < kb;
 #pragma unroll
         for (int i = 0; i < kCodeCopies; ++i) {
             const uint8_t* src = (i < 4 ? bbase : abase) + k0 + off[i];
-            copy16(in ? src : (const uint8_t*)kZeroChunk, dst + i * kTNT * 16 + wave * 1024);
+            copy16(in ? src : (const uint8_t*)kZeroChunk, dst + i * NT * 16 + wave * 1024);
         }
 #pragma unroll
         for (int i = 0; i < kScaleCopies; ++i)
-            copy4(sbase[i] + (int64_t)(s < steps ? s : steps - 1) * 64, dst + kStageBytes + (8 * i + wave) * 256);
+            copy4(sbase[i] + (int64_t)(s < steps ? s : steps - 1) * 64, dst + STAGE + (TILE / 32 * i + wave) * 256);
     };
-    const int wm = (wave >> 2) * 128, wn = (wave & 3) * 64;
+    const int wm = wave / WN * (32 * FA), wn = wave % WN * 64;
     struct Frags {
-        uint4 a[4], b[2];
+        uint4 a[FA], b[2];
     } f[2];
-    uint32_t sa[2][4], sb[2][2];
+    uint32_t sa[2][FA], sb[2][2];
     auto load = [&](int s, auto quarter, auto p) __attribute__((always_inline)) {
         constexpr int Q = decltype(quarter)::value;
-        const uint8_t* src = lds + (s & 1) * kBufBytes;
+        const uint8_t* src = lds + (s & 1) * BUF;
         const int foff = r * 128 + 16 * ((2 * Q + h) ^ ((r >> 1) & 7));
         Frags& g = f[decltype(p)::value];
 #pragma unroll
         for (int i = 0; i < 2; ++i) g.b[i] = *(const uint4*)(src + (wn + 32 * i) * 128 + foff);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g.a[i] = *(const uint4*)(src + (kTile + wm + 32 * i) * 128 + foff);
+        for (int i = 0; i < FA; ++i) g.a[i] = *(const uint4*)(src + (TILE + wm + 32 * i) * 128 + foff);
     };
-    auto load_scales = [&](int s, uint32_t (&pa)[4], uint32_t (&pb)[2]) __attribute__((always_inline)) {
-        const uint8_t* src = lds + (s & 1) * kBufBytes + kStageBytes + lane * 4;
+    auto load_scales = [&](int s, uint32_t (&pa)[FA], uint32_t (&pb)[2]) __attribute__((always_inline)) {
+        const uint8_t* src = lds + (s & 1) * BUF + STAGE + lane * 4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) pb[i] = *(const uint32_t*)(src + (wn / 32 + i) * 256);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pa[i] = *(const uint32_t*)(src + (8 + wm / 32 + i) * 256);
+        for (int i = 0; i < FA; ++i) pa[i] = *(const uint32_t*)(src + (TILE / 32 + wm / 32 + i) * 256);
     };
-    mx_f16 acc[4][2];
+    mx_f16 acc[FA][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mx_f16{};
-    auto mma = [&](auto quarter, auto p, const uint32_t (&pa)[4], const uint32_t (&pb)[2]) __attribute__((always_inline)) {
+    auto mma = [&](auto quarter, auto p, const uint32_t (&pa)[FA], const uint32_t (&pb)[2]) __attribute__((always_inline)) {
         constexpr int Q = decltype(quarter)::value;
         const Frags& g = f[decltype(p)::value];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < FA; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = mx4_mma32<Q, Q>(g.b[j], g.a[i], acc[i][j], pb[j], pa[i]);
     };
@@ -428,8 +507,8 @@ __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
     load_scales(0, sa[0], sb[0]);
     // per quarter: the next one's LDS reads, then this one's matrix instructions
     auto reads_first = [] __attribute__((always_inline)) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, FA + 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2 * FA, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     for (int s = 0; s < steps; ++s) {
@@ -448,33 +527,67 @@ __global__ __launch_bounds__(kTNT, 2) void mx4_tile_kernel(TileArgs t) {
         load(s + 1, C0(), C0());
         load_scales(s + 1, sa[1], sb[1]);
         mma(C3(), C1(), sa[0], sb[0]);
-        __builtin_amdgcn_sched_group_barrier(0x100, 12, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * FA + 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2 * FA, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[0][i] = sa[1][i];
+        for (int i = 0; i < FA; ++i) sa[0][i] = sa[1][i];
 #pragma unroll
         for (int i = 0; i < 2; ++i) sb[0][i] = sb[1][i];
     }
     wait_vm<0>();  // the copies behind the last step, before their buffers are used again
     bar();
-    store_tile<DT>(t, acc, lds, m0, n0, wm, wn);
+    store_tile<DT, TILE, FA>(t, acc, lds, m0, n0, wm, wn);
 }
 
 size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 31) / 32) * (size_t)((kb + 7) / 8) * 256; }
 
-}  // namespace
-
-// the tile kernel: enough tiles for most compute units, and steps enough to
-// fill its ring; its copies address a tile by 32-bit offsets
-bool mx4_use_tiles(int64_t M, int64_t N, int64_t K) {
-    const int64_t tiles = (M + kTile - 1) / kTile * ((N + kTile - 1) / kTile);
-    return tiles >= 128 && tiles < (1 << 30) && K >= 1024 && K <= (1 << 22);
+// Which kernel a product runs on; times at N = K = 4096 unless said.
+enum class Path { few, direct, split1, split2, split4, tile128, tile256 };
+int64_t tiles_of(int64_t M, int64_t N, int64_t T) { return ((M + T - 1) / T) * ((N + T - 1) / T); }
+Path pick(int64_t M, int64_t N, int64_t K) {
+    if (M <= 16) return Path::few;
+    const bool lds_tiles = K <= 1 << 22 && tiles_of(M, N, 128) < 1 << 22;  // 32-bit offsets in a tile, grid sizes
+    if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
+    if (lds_tiles && K >= 512 && tiles_of(M, N, 128) >= 128) return Path::tile128;
+    if (K <= 256) return Path::direct;
+    if (tiles_of(M, N, 64) >= 256) return Path::split4;
+    if (M > 32 && ((M + 63) / 64) * ((N + 31) / 32) >= 256) return Path::split2;
+    return Path::split1;
 }
+
+template <int TILE>
+hipError_t launch_tiles(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace, hipStream_t stream) {
+    TileArgs t{a, b, nullptr, nullptr, out, (int)((a.rows + TILE - 1) / TILE), (int)((b.rows + TILE - 1) / TILE)};
+    t.ga = (const uint32_t*)workspace;
+    t.gb = (const uint32_t*)((const char*)workspace + group_bytes(a.rows, a.kb()));
+    const uint32_t ag = (uint32_t)((a.rows + 31) / 32), bg = (uint32_t)((b.rows + 31) / 32);
+    hipLaunchKernelGGL(mx4_scale_groups_kernel, dim3(ag + bg, (uint32_t)((a.kb() + 63) / 64)), dim3(kNT), 0, stream, a, b,
+                       (uint32_t*)t.ga, (uint32_t*)t.gb, (int)ag);
+    return by_dtype(out.dtype, [&](auto dt) {
+        constexpr int bytes = 2 * buf_bytes(TILE);
+        static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+        auto kernel = mx4_tile_kernel<decltype(dt)::value, TILE>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(t.m_tiles * t.n_tiles)), dim3(2 * TILE), bytes, stream, t);
+    });
+}
+
+template <int MF, int NF>
+hipError_t launch_split(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, hipStream_t stream) {
+    const int64_t mt = (a.rows + 16 * MF - 1) / (16 * MF), nt = (b.rows + 16 * NF - 1) / (16 * NF);
+    return by_dtype(out.dtype, [&](auto dt) {
+        hipLaunchKernelGGL((mx4_split_kernel<decltype(dt)::value, MF, NF>), dim3((uint32_t)(mt * nt)), dim3(512),
+                           4 * MF * NF * 1024, stream, a, b, out, (int)nt);
+    });
+}
+
+}  // namespace
 
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const int64_t kb = (K + 31) / 32;
-    return mx4_use_tiles(M, N, K) ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
+    const Path p = pick(M, N, K);
+    return p == Path::tile256 || p == Path::tile128 ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
 }
 
 bool mx4_few_ok(int64_t M, int64_t K) { return M <= 16 && M * ((K + 127) / 128 * 128) <= kFewElements; }
@@ -489,35 +602,19 @@ hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const
 
 hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace,
                              hipStream_t stream) {
-    if (a.rows <= 16) return launch_few_rows<-1>(a, nullptr, 0, b, out, stream);
-    if (mx4_use_tiles(a.rows, b.rows, a.cols)) {
-        TileArgs t{a, b, nullptr, nullptr, out, (int)((a.rows + kTile - 1) / kTile), (int)((b.rows + kTile - 1) / kTile)};
-        t.ga = (const uint32_t*)workspace;
-        t.gb = (const uint32_t*)((const char*)workspace + group_bytes(a.rows, a.kb()));
-        const uint32_t ag = (uint32_t)((a.rows + 31) / 32), bg = (uint32_t)((b.rows + 31) / 32);
-        hipLaunchKernelGGL(mx4_scale_groups_kernel, dim3(ag + bg, (uint32_t)((a.kb() + 63) / 64)), dim3(kNT), 0, stream, a,
-                           b, (uint32_t*)t.ga, (uint32_t*)t.gb, (int)ag);
-        return by_dtype(out.dtype, [&](auto dt) {
-            constexpr int bytes = 2 * kBufBytes;
-            static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-            auto kernel = mx4_tile_kernel<decltype(dt)::value>;
-            (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            hipLaunchKernelGGL(kernel, dim3((uint32_t)(t.m_tiles * t.n_tiles)), dim3(kTNT), bytes, stream, t);
-        });
+    switch (pick(a.rows, b.rows, a.cols)) {
+        case Path::few: return launch_few_rows<-1>(a, nullptr, 0, b, out, stream);
+        case Path::tile256: return launch_tiles<256>(a, b, out, workspace, stream);
+        case Path::tile128: return launch_tiles<128>(a, b, out, workspace, stream);
+        case Path::split4: return launch_split<4, 4>(a, b, out, stream);
+        case Path::split2: return launch_split<4, 2>(a, b, out, stream);
+        case Path::split1: return a.rows <= 32 ? launch_split<2, 1>(a, b, out, stream) : launch_split<4, 1>(a, b, out, stream);
+        case Path::direct: break;
     }
-    // waves split k where 128 x 128 tiles leave compute units idle and there
-    // are steps to split
-    const int64_t big = ((a.rows + 127) / 128) * ((b.rows + 127) / 128);
-    const bool split = big < 256 && a.cols > 256;
-    const int64_t T = split ? 64 : 128;
-    const int64_t mt = (a.rows + T - 1) / T, nt = (b.rows + T - 1) / T;
+    const int64_t mt = (a.rows + 127) / 128, nt = (b.rows + 127) / 128;
     return by_dtype(out.dtype, [&](auto dt) {
-        if (split)
-            hipLaunchKernelGGL((mx4_direct_kernel<decltype(dt)::value, 4>), dim3((uint32_t)(mt * nt)), dim3(kNT), 0, stream,
-                               a, b, out, (int)nt);
-        else
-            hipLaunchKernelGGL((mx4_direct_kernel<decltype(dt)::value, 1>), dim3((uint32_t)(mt * nt)), dim3(kNT), 0, stream,
-                               a, b, out, (int)nt);
+        hipLaunchKernelGGL(mx4_direct_kernel<decltype(dt)::value>, dim3((uint32_t)(mt * nt)), dim3(kNT), 0, stream, a, b,
+                           out, (int)nt);
     });
 }
 

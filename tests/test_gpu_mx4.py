@@ -151,7 +151,8 @@ def _operand(m, a):
 
 PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 3, 33), (1, 512, 256), (1, 4096, 1024), (5, 100, 64), (16, 129, 96), (17, 16, 128),
             (33, 257, 160), (64, 64, 512), (127, 130, 1000), (129, 128, 31), (200, 333, 777), (256, 512, 2048),
-            (300, 17, 4100), (1024, 1, 200), (1000, 513, 256), (515, 777, 130), (16, 8, 8192), (40, 40, 6500)]
+            (300, 17, 4100), (1024, 1, 200), (1000, 513, 256), (515, 777, 130), (16, 8, 8192), (40, 40, 6500),
+            (1030, 1031, 400), (1500, 1411, 600), (500, 1040, 700), (20, 3000, 2000), (32, 500, 288), (129, 700, 4000)]
 
 
 @pytest.mark.parametrize("mnk", PRODUCTS)
@@ -191,7 +192,7 @@ def test_product_exact_on_the_grid(m, mnk):
 
 @pytest.mark.parametrize("mnk", [(2900, 2950, 1056), (2817, 3000, 1500), (8200, 1030, 1024), (1000, 9000, 2100),
                                  (33000, 250, 1024), (4096, 4096, 4096), (8192, 512, 256), (9001, 77, 33), (12345, 513, 130),
-                                 (65536, 128, 128), (8200, 450, 1000)])
+                                 (65536, 128, 128), (8200, 450, 1000), (4000, 3300, 260), (1409, 1500, 3000), (700, 2500, 1111)])
 def test_large_products_exact_on_the_grid(m, mnk):
     """Products of many tiles, ragged in each size: equality with the oracle
     at the matrix's corners, edges and a sample of rows, and of all rows with a
