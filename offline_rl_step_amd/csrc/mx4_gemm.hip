@@ -31,11 +31,14 @@ hipError_t by_dtype(int dtype, F f) {
 // M <= 16.  HBM-bound on b, at small sizes on the latency of one pass over it.
 // Workgroup: 16 rows of b.  Wave w of 8 takes the k steps w, w + 8, ..; U
 // steps' loads of b are in flight together, the first of them before anything
-// else.  XDT >= 0: the left operand is a float matrix, quantised into LDS by every
-// workgroup (an eighth of a step per thread at 4096 elements) while they are
-// under way.  The waves' sums meet in LDS, added in wave order.
+// else.  The left operand lies in LDS, as rows of whole steps: copied there, or
+// (XDT >= 0, a float matrix) quantised into it by every workgroup, an eighth of a
+// step per thread at 4096 elements, while b's loads are under way.  A wave's
+// 16-byte loads of 16 rows are 64 lookups in the L1, so only b's are made; b's
+// scales come as 4 bytes per row to 16 lanes.  The waves' sums meet in LDS, added in
+// wave order.
 constexpr int kFewWaves = 8;
-constexpr int kFewElements = 32768;  // of a float left operand, padded: 16 KB of codes, 1 KB of scales
+constexpr int kFewElements = 32768;  // of a float left operand, padded
 template <int XDT, int ODT>
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, const void* x, int64_t ld, Mx4Mat b,
                                                                       Mx4Out o) {
@@ -47,15 +50,32 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
     const int r = lane & 15, blk = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const RowFrag fb(b, n0 + r);
-    const int64_t steps = (b.kb() + 3) / 4;
+    const int kb = (int)b.kb(), steps = (kb + 3) / 4;
     uint4 bv[U];
-    uint32_t bs[U];
-    auto load_b = [&](int64_t s0) __attribute__((always_inline)) {
+    uint32_t bw[U];
+    auto load_b = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) fb.load((s0 + u * kFewWaves) * 4 + blk, bv[u], bs[u]);
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * kFewWaves;
+            const int at = s * 4 + blk < kb ? s * 4 + blk : 0;  // blocks past the end: a's are zeros
+            bv[u] = fb.codes[at];
+        }
+        if (blk == 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = (s0 + u * kFewWaves) * 4;
+                typedef uint32_t u1 __attribute__((aligned(1)));
+                if (s + 4 <= kb) {
+                    bw[u] = *(const u1*)(fb.scales + s);
+                } else {
+                    bw[u] = 0x7F7F7F7Fu;
+                    for (int e = 0; s + e < kb; ++e) bw[u] = (bw[u] & ~(255u << (8 * e))) | (uint32_t)fb.scales[s + e] << (8 * e);
+                }
+            }
+        }
     };
     load_b(wave);
-    const int kb4 = XDT >= 0 ? (int)steps * 4 : 0, rb = kb4 * 16 + 16;
+    const int kb4 = steps * 4, rb = kb4 * 16 + 16;
     uint8_t* scales = codes + a.rows * rb;           // [M][kb4]
     if constexpr (XDT >= 0) {
         const int gpr = kb4 * 4;                     // groups of 8 a row
@@ -71,30 +91,32 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
             *(uint32_t*)(codes + row * rb + g * 4) = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
             if ((g & 3) == 0) scales[row * kb4 + (g >> 2)] = (uint8_t)s;
         }
-        __syncthreads();
+    } else {
+        for (int e = threadIdx.x; e < (int)a.rows * kb4; e += NT) {
+            const int row = e / kb4, k = e - row * kb4;
+            const bool in = k < kb;
+            const int64_t at = (int64_t)row * kb + (in ? k : 0);
+            const uint4 w = ((const uint4*)a.codes)[at];
+            const uint32_t s = a.scales[at], keep = in ? 0xFFFFFFFFu : 0u;
+            *(uint4*)(codes + row * rb + k * 16) = uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep};
+            scales[e] = (uint8_t)(in ? s : 127u);
+        }
     }
-    const RowFrag fa(a, r);
+    __syncthreads();
     mx_f4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t s0 = wave; s0 < steps; s0 += kFewWaves * U) {
+    for (int s0 = wave; s0 < steps; s0 += kFewWaves * U) {
         if (s0 != wave) load_b(s0);
-        uint4 av[U];
-        uint32_t as[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t s = s0 + u * kFewWaves;
-            if constexpr (XDT >= 0) {
-                const bool in = s < steps && r < a.rows;
-                const int at = in ? (int)s * 4 + blk : 0, row = in ? r : 0;
-                const uint4 w = *(const uint4*)(codes + row * rb + at * 16);
-                const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
-                av[u] = uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep};
-                as[u] = in ? scales[row * kb4 + at] : 127u;
-            } else {
-                fa.load(s * 4 + blk, av[u], as[u]);
-            }
+            const int s = s0 + u * kFewWaves;
+            const bool in = s < steps && r < a.rows;
+            const int at = in ? s * 4 + blk : 0, row = in ? r : 0;
+            const uint4 w = *(const uint4*)(codes + row * rb + at * 16);
+            const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+            const uint32_t as = in ? scales[row * kb4 + at] : 127u;
+            const uint32_t bs = (uint32_t)__shfl((int)bw[u], r, kWave) >> (8 * blk) & 255u;
+            acc = mx4_mma(bv[u], uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep}, acc, bs, as);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc = mx4_mma(bv[u], av[u], acc, bs[u], as[u]);
     }
     part[wave][lane] = acc;
     __syncthreads();
@@ -106,12 +128,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
     }
 }
 
+// LDS of a left operand of M rows and K columns beside the sums
+int64_t few_bytes(int64_t M, int64_t K) { return kFewWaves * 1024 + M * ((K + 127) / 128 * 68 + 16); }
+
 template <int XDT>
 hipError_t launch_few_rows(const Mx4Mat& a, const void* x, int64_t ld, const Mx4Mat& b, const Mx4Out& out,
                            hipStream_t stream) {
-    const int kb4 = (int)((b.kb() + 3) / 4 * 4);
-    const int bytes = kFewWaves * 1024 + (XDT >= 0 ? (int)a.rows * (kb4 * 17 + 16) : 0);
+    const int bytes = (int)few_bytes(a.rows, b.cols);
     return by_dtype(out.dtype, [&](auto dt) {
+        auto kernel = mx4_few_rows_kernel<XDT, decltype(dt)::value>;
+        if (bytes > 64 << 10)
+            (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         hipLaunchKernelGGL((mx4_few_rows_kernel<XDT, decltype(dt)::value>), dim3((uint32_t)((b.rows + 15) / 16)),
                            dim3(64 * kFewWaves), bytes, stream, a, x, ld, b, out);
     });
@@ -546,7 +573,7 @@ size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 31) / 32)
 enum class Path { few, direct, split1, split2, split4, tile128, tile256 };
 int64_t tiles_of(int64_t M, int64_t N, int64_t T) { return ((M + T - 1) / T) * ((N + T - 1) / T); }
 Path pick(int64_t M, int64_t N, int64_t K) {
-    if (M <= 16) return Path::few;
+    if (M <= 16 && few_bytes(M, K) <= 80 << 10) return Path::few;  // two workgroups to a compute unit
     const bool lds_tiles = K <= 1 << 22 && tiles_of(M, N, 128) < 1 << 22;  // 32-bit offsets in a tile, grid sizes
     if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
     if (lds_tiles && K >= 512 && tiles_of(M, N, 128) >= 128) return Path::tile128;
