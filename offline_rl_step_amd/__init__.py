@@ -415,6 +415,7 @@ class TensorSet:
                "iqlh_tensor_set_fill")
         # a copy from pageable memory: complete when it returns, for any stream
         self.table = host[:self.struct.table_bytes].to(self.device)
+        self._home = _stream(None).value  # the allocator reuses the table's memory in this stream's order
         self.struct.d_table = self.table.data_ptr()
         self.ref = ctypes.byref(self.struct)
         self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
@@ -422,6 +423,13 @@ class TensorSet:
     @property
     def numel(self):
         return self.struct.numel
+
+    def _used_on(self, stream):
+        """Keeps the table's memory from being handed out again, should the set be
+        dropped, before a call on another stream has read it."""
+        if stream.value != self._home and not torch.cuda.is_current_stream_capturing():
+            self.table.record_stream(torch.cuda.ExternalStream(stream.value or 0, device=self.device))
+        return stream
 
     def overlaps(self, t):
         """Whether t (contiguous) shares memory with a tensor of the set."""
@@ -458,7 +466,7 @@ def grad_norm(tensor_set, out_norm, workspace, kind=NORM_L2, out_each=None, flag
         _need_f32(out_each, s.struct.count, s.device, "out_each")
     _need_aux(s.device, workspace, flags)
     _check(_lib_grad_norm(s.ref, kind, out_norm.data_ptr(), _ptr(out_each), _ptr(flags), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), _stream(stream)), "iqlh_grad_norm")
+                          workspace.numel() * workspace.element_size(), s._used_on(_stream(stream))), "iqlh_grad_norm")
 
 
 def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None, flags=None, stream=None):
@@ -472,7 +480,7 @@ def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None,
         _need(not s.overlaps(out_flat[:s.numel]), "out_flat shares memory with a tensor of the set")
     _need_aux(s.device, workspace, flags)
     _check(_lib_grad_clip(s.ref, kind, max_norm, _ptr(out_flat), out.data_ptr(), _ptr(flags), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), _stream(stream)),
+                          workspace.numel() * workspace.element_size(), s._used_on(_stream(stream))),
            "iqlh_grad_clip")
 
 

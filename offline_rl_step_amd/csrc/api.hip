@@ -742,7 +742,7 @@ static int check_mx4_product(const char* who, int64_t M, const Mx4Mat& b, const 
     int rc = check_float_matrix(who, out, out_dtype, ld_out, b.rows);
     if (rc) return rc;
     if (M < 1 || M > (int64_t)1 << 30) return fail(IQLH_EINVAL, "%s: M outside [1, 2^30]", who);
-    if (((M + 15) / 16) * ((b.rows + 15) / 16) > (int64_t)1 << 31)
+    if (!mx4_launchable(M, b.rows, b.cols))
         return fail(IQLH_ESHAPE, "%s: %lld x %lld outputs are more than one launch takes", who, (long long)M,
                     (long long)b.rows);
     if (relu != 0 && relu != 1) return fail(IQLH_EINVAL, "%s: relu must be 0 or 1", who);

@@ -29,33 +29,43 @@ __global__ __launch_bounds__(256) void iql_mx4_head_kernel(const float* __restri
     if (lane == 0) write_value(vo, g, B, row0 + row, s + w3[H2]);  // b3 follows w3
 }
 
-// W1 and W2 of every group, blocks along their rows: 8 elements a thread.
+// W1 and W2 of every group, blocks along their rows, as fragments (FragsOfB): a
+// thread quantises one block of 32.
 struct WeightArgs {
     const float* params;  // [G][P]
     int64_t P;
     uint8_t* ws;          // [G] of `stride` bytes: codes and scales at the offsets below
     size_t stride, w1c, w1s, w2c, w2s;
     int S, H, H2;
-    int n1, n2;           // groups of 8: of W1, of W2
+    int n1, n2;           // lanes of W1's fragments, of W2's
 };
 __global__ __launch_bounds__(256) void iql_mx4_weights_kernel(WeightArgs a) {
-    const int e = blockIdx.x * 256 + threadIdx.x;  // n1 and n2 are multiples of 4: a block's four lanes stay together
+    int e = blockIdx.x * 256 + threadIdx.x;
+    if (e >= a.n1 + a.n2) return;
     const bool second = e >= a.n1;
-    const int k = second ? a.H : a.S, gpr = (k + 31) / 32 * 4;
-    const int at = second ? e - a.n1 : e, row = at / gpr, g = at - row * gpr;
-    const bool in = e < a.n1 + a.n2;
-    const float* w = a.params + blockIdx.y * a.P + (second ? (int64_t)a.H * a.S + a.H : 0) + (int64_t)row * k + g * 8;
-    float v[8];
-    const int left = in ? k - g * 8 : 0;
-    load8<IQLH_F32>(w, left < 0 ? 0 : left < 8 ? left : 8, v);
+    if (second) e -= a.n1;
+    const int rows = second ? a.H2 : a.H, k = second ? a.H : a.S, steps = (k + 127) / 128;
+    const int lane = e & 63, group = (e >> 6) / steps, step = (e >> 6) - group * steps;
+    const int row = group * 16 + (lane & 15), k0 = step * 128 + (lane >> 4) * 32;
+    const float* w = a.params + blockIdx.y * a.P + (second ? (int64_t)a.H * a.S + a.H : 0) + (int64_t)row * k + k0;
+    float v[32];
     uint32_t amax = 0u;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
-    const uint32_t s = mx4_scale(quad_umax(amax));
-    if (!in) return;
+    for (int j = 0; j < 32; j += 8) {
+        const int left = row < rows ? k - k0 - j : 0;
+        load8<IQLH_F32>(w + j, left < 0 ? 0 : left < 8 ? left : 8, v + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[j]));
+    const uint32_t s = mx4_scale(amax);
+    uint4 c{0u, 0u, 0u, 0u};
+    if (s != 255u) {
+        const float inv = mx4_inverse(s);
+        c = uint4{mx4_codes8(v, inv), mx4_codes8(v + 8, inv), mx4_codes8(v + 16, inv), mx4_codes8(v + 24, inv)};
+    }
     uint8_t* base = a.ws + blockIdx.y * a.stride;
-    ((uint32_t*)(base + (second ? a.w2c : a.w1c)))[at] = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
-    if ((at & 3) == 0) (base + (second ? a.w2s : a.w1s))[at >> 2] = (uint8_t)s;
+    ((uint4*)(base + (second ? a.w2c : a.w1c)))[e] = c;
+    (base + (second ? a.w2s : a.w1s))[mx4_frag_scale_at(group, step, steps, lane)] = (uint8_t)s;
 }
 
 struct NetArgs {
@@ -84,7 +94,7 @@ IQLH_DEV float group_sum(float v) {
 // from the lanes that hold its sums.  Layer 2: h2 w3 summed in the lanes, over
 // the wave's chunks, the lanes of a row and the waves, in that order.
 template <int ROWS, int NT, int XDT>
-__global__ __launch_bounds__(NT, NT == 256 ? 3 : 2) void iql_mx4_net_kernel(NetArgs a) {
+__global__ __launch_bounds__(NT, 2) void iql_mx4_net_kernel(NetArgs a) {
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ float part[NT / 64][ROWS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -94,8 +104,9 @@ __global__ __launch_bounds__(NT, NT == 256 ? 3 : 2) void iql_mx4_net_kernel(NetA
     mx4_rows_to_lds<ROWS, NT, XDT>((const typename MxFloat<XDT>::type*)a.x, a.ld, a.B, m0, a.S, tx);
     __syncthreads();
     for (int g = 0; g < a.G; ++g) {
-        uint8_t* ws = (uint8_t*)a.ws + g * a.stride;
-        const Mx4Mat w1{ws + a.w1c, ws + a.w1s, a.H, a.S}, w2{ws + a.w2c, ws + a.w2s, a.H2, a.H};
+        const uint8_t* ws = a.ws + g * a.stride;
+        const FragsOfB w1{(const uint4*)(ws + a.w1c), (const uint32_t*)(ws + a.w1s), a.kb4x / 4};
+        const FragsOfB w2{(const uint4*)(ws + a.w2c), (const uint32_t*)(ws + a.w2s), a.kb4h / 4};
         const float* b1 = a.params + g * a.P + (int64_t)a.H * a.S;
         const float* b2 = b1 + a.H + (int64_t)a.H2 * a.H;
         const float* w3 = b2 + a.H2;
@@ -185,20 +196,27 @@ Layout layout(const IqlDims& d, int B) {
     const size_t k1 = (d.S + 31) / 32, k2 = (d.H + 31) / 32;
     size_t at = 0;
     auto take = [&](size_t bytes) { const size_t p = at; at += up16(bytes); return p; };
+    if (one_launch(d)) {
+        l.w1c = take(mx4_frag_code_bytes(d.H, k1));
+        l.w1s = take(mx4_frag_scale_bytes(d.H, k1));
+        l.w2c = take(mx4_frag_code_bytes(d.H2, k2));
+        l.w2s = take(mx4_frag_scale_bytes(d.H2, k2));
+        l.group = at;
+        l.total = at * d.G;
+        return l;
+    }
     l.w1c = take(k1 * 16 * d.H);
     l.w1s = take(k1 * d.H);
     l.w2c = take(k2 * 16 * d.H2);
     l.w2s = take(k2 * d.H2);
-    l.group = at;
-    if (one_launch(d)) {
-        l.total = at * d.G;
-        return l;
-    }
     l.chunk = B < kChunkRows ? B : kChunkRows;
     l.h1 = take(sizeof(float) * (size_t)l.chunk * d.H);
     l.h2 = take(sizeof(float) * (size_t)l.chunk * d.H2);
-    const size_t p1 = mx4_workspace_bytes(l.chunk, d.H, d.S), p2 = mx4_workspace_bytes(l.chunk, d.H2, d.H);
-    l.product = take(p1 > p2 ? p1 : p2);
+    size_t product = 0;
+    for (int rows : {l.chunk, B % l.chunk ? B % l.chunk : l.chunk})  // the chunks and what is left
+        for (size_t bytes : {mx4_workspace_bytes(rows, d.H, d.S), mx4_workspace_bytes(rows, d.H2, d.H)})
+            if (bytes > product) product = bytes;
+    l.product = take(product);
     l.total = at;
     return l;
 }
@@ -232,7 +250,7 @@ hipError_t launch_iql_mx4_forward(const IqlDims& d, const IqlBuffers& b, const v
     const Layout l = layout(d, B);
     uint8_t* ws = (uint8_t*)workspace;
     if (one_launch(d)) {
-        const int n1 = d.H * ((d.S + 31) / 32) * 4, n2 = d.H2 * ((d.H + 31) / 32) * 4;
+        const int n1 = (int)(mx4_frag_code_bytes(d.H, (d.S + 31) / 32) / 16), n2 = (int)(mx4_frag_code_bytes(d.H2, (d.H + 31) / 32) / 16);
         WeightArgs w{b.params, d.P, ws, l.group, l.w1c, l.w1s, l.w2c, l.w2s, d.S, d.H, d.H2, n1, n2};
         hipLaunchKernelGGL(iql_mx4_weights_kernel, dim3((n1 + n2 + 255) / 256, d.G), dim3(256), 0, stream, w);
         hipError_t e = hipGetLastError();

@@ -258,6 +258,7 @@ struct Mx4Out {
 };
 // workspace of a product: the left operand quantised on the way, then the
 // partial sums of a split summed axis
+bool mx4_launchable(int64_t M, int64_t N, int64_t K);
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 // many rows times a small b, quantisation and product in one launch
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K);

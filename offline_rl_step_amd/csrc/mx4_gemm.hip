@@ -569,15 +569,24 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
 
 size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 31) / 32) * (size_t)((kb + 7) / 8) * 256; }
 
-// Which kernel a product runs on; times at N = K = 4096 unless said.
+// Which kernel a product runs on.
 enum class Path { few, direct, split1, split2, split4, tile128, tile256 };
 int64_t tiles_of(int64_t M, int64_t N, int64_t T) { return ((M + T - 1) / T) * ((N + T - 1) / T); }
 Path pick(int64_t M, int64_t N, int64_t K) {
     if (M <= 16 && few_bytes(M, K) <= 80 << 10) return Path::few;  // two workgroups to a compute unit
     const bool lds_tiles = K <= 1 << 22 && tiles_of(M, N, 128) < 1 << 22;  // 32-bit offsets in a tile, grid sizes
+    // 256 tiles for most compute units (2048 x 4096 x 4096, 128 of them: 39.1 us
+    // against 30.5 with 128 tiles; 4096^3, 256 of them: 45.0)
     if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
-    if (lds_tiles && K >= 512 && tiles_of(M, N, 128) >= 128) return Path::tile128;
+    // 128 tiles against waves that split k, both as measured up to a round of
+    // tiles: the tiles take 8 us and 2.1 per 1000 k whatever their number, the
+    // splitting waves 3 us and 5 per 10^9 products (as many at K 1024 and below,
+    // where waves go without a step).  768 x 1024 x 4096: 16.3 against 29.5 us;
+    // 512 x 512 x 2048: 11.7 against 8.5
+    const double split_us = 3.0 + 5e-9 * (double)M * (double)N * (double)(K < 1024 ? 1024 : K);
+    if (lds_tiles && K >= 512 && split_us > 8.0 + 2.1e-3 * (double)K) return Path::tile128;
     if (K <= 256) return Path::direct;
+    // the largest of its tiles that gives every compute unit one
     if (tiles_of(M, N, 64) >= 256) return Path::split4;
     if (M > 32 && ((M + 63) / 64) * ((N + 31) / 32) >= 256) return Path::split2;
     return Path::split1;
@@ -615,6 +624,21 @@ size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const int64_t kb = (K + 31) / 32;
     const Path p = pick(M, N, K);
     return p == Path::tile256 || p == Path::tile128 ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
+}
+
+// Launches hold less than 2^32 threads
+bool mx4_launchable(int64_t M, int64_t N, int64_t K) {
+    const int64_t top = (int64_t)1 << 32;
+    switch (pick(M, N, K)) {
+        case Path::few: return (N + 15) / 16 * 512 < top;
+        case Path::direct: return tiles_of(M, N, 128) * kNT < top;
+        case Path::split1: return (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64) * ((N + 15) / 16) < top / 512;
+        case Path::split2: return (M + 63) / 64 * ((N + 31) / 32) < top / 512;
+        case Path::split4: return tiles_of(M, N, 64) < top / 512;
+        case Path::tile128:
+        case Path::tile256: break;  // bounded by pick; the scales' regrouping by their rows
+    }
+    return ((M + 31) / 32 + (N + 31) / 32) * kNT < top;
 }
 
 bool mx4_few_ok(int64_t M, int64_t K) { return M <= 16 && M * ((K + 127) / 128 * 128) <= kFewElements; }

@@ -13,7 +13,7 @@ constexpr int kRows = 64, kNT = 256;
 // Four waves; wave w takes the chunks w, w + 4, .. of 32 rows of b, 64 x 32
 // outputs each.
 template <int XDT, int ODT>
-__global__ __launch_bounds__(kNT, 3) void mx4_rows_kernel(const typename MxFloat<XDT>::type* __restrict__ x, int64_t ld,
+__global__ __launch_bounds__(kNT, 4) void mx4_rows_kernel(const typename MxFloat<XDT>::type* __restrict__ x, int64_t ld,
                                                            int64_t M, Mx4Mat b, Mx4Out o, int kb4, int stream_out) {
     typedef typename MxFloat<ODT>::type T;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -30,7 +30,7 @@ __global__ __launch_bounds__(kNT, 3) void mx4_rows_kernel(const typename MxFloat
     const float lowest = o.relu ? 0.f : -__builtin_huge_valf();
     float bias[kFrags][4];
     mx4_rows_chunks<kRows, kNT>(
-        t, b, b.rows,
+        t, RowsOfB{b}, b.rows,
         [&](int64_t n0) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < kFrags; ++j) mx4_bias4(o, n0 + 16 * j + 4 * blk, b.rows, bias[j]);

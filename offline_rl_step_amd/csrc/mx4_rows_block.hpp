@@ -56,20 +56,69 @@ IQLH_DEV void mx4_rows_to_lds(const typename MxFloat<XDT>::type* x, int64_t ld, 
     }
 }
 
+// b in memory as its rows, of 32-bit extent
+struct RowsOfB {
+    Mx4Mat q;
+    struct Step {
+        uint4 v;
+        uint32_t s;
+    };
+    IQLH_DEV void load(int64_t n0, int step, int lane, Step& f) const {
+        const uint32_t n = (uint32_t)n0 + (lane & 15), kb = (uint32_t)q.kb(), block = step * 4 + (lane >> 4);
+        const bool in = block < kb;
+        const uint32_t at = (n < (uint32_t)q.rows ? n : (uint32_t)q.rows - 1) * kb + (in ? block : 0u);
+        const uint4 v = *(const uint4*)(q.codes + at * 16u);
+        const uint32_t keep = in ? 0xFFFFFFFFu : 0u;  // zeros of scale 1 behind the last block
+        f.v = uint4{v.x & keep, v.y & keep, v.z & keep, v.w & keep};
+        f.s = in ? q.scales[at] : 127u;
+    }
+    static IQLH_DEV uint32_t scale(const Step& f, int step) { return f.s; }
+};
+
+// b regrouped by fragments: the codes of 16 rows and a step as the 64 lanes
+// hold them (1 KB in 16 lookups of the L1, not the 64 of a fragment of 16 rows,
+// and the scale bytes' 64 more), and one dword of scales per lane for four
+// steps, byte s & 3 that of step s.  Rows are padded to a multiple of 128, blocks
+// to whole steps, with zeros of scale 1.
+struct FragsOfB {
+    const uint4* codes;      // [rows128 / 16][steps][64]
+    const uint32_t* scales;  // [rows128 / 16][(steps + 3) / 4][64]
+    int steps;
+    struct Step {
+        uint4 v;
+        uint32_t s;
+    };
+    IQLH_DEV void load(int64_t n0, int step, int lane, Step& f) const {
+        f.v = codes[(n0 / 16 * steps + step) * 64 + lane];
+        f.s = scales[(n0 / 16 * ((steps + 3) / 4) + step / 4) * 64 + lane];
+    }
+    static IQLH_DEV uint32_t scale(const Step& f, int step) { return f.s >> (8 * (step & 3)); }
+};
+__host__ __device__ inline int64_t mx4_frag_groups(int64_t rows) { return (rows + 127) / 128 * 8; }
+__host__ __device__ inline int64_t mx4_frag_code_bytes(int64_t rows, int64_t kb) {
+    return mx4_frag_groups(rows) * ((kb + 3) / 4) * 1024;
+}
+__host__ __device__ inline int64_t mx4_frag_scale_bytes(int64_t rows, int64_t kb) {
+    return mx4_frag_groups(rows) * ((kb + 15) / 16) * 256;
+}
+// where the lane's scale byte of (16-row group, step) lies
+IQLH_DEV int64_t mx4_frag_scale_at(int64_t group, int64_t step, int64_t steps, int lane) {
+    return ((group * ((steps + 3) / 4) + step / 4) * 64 + lane) * 4 + (step & 3);
+}
+
 // For the chunks n0 = 32 wave, + 32 waves, .. below n_end: acc[i][j] (rows 16 i + (lane
 // & 15) of t, rows n0 + 16 j + 4 (lane >> 4) + 0..3 of b) = the products' sums, then
 // done(n0, acc).  b's fragments are loaded one step ahead, over the chunks'
 // ends too; first(n0) runs before a chunk's steps (loads for done).
-template <int ROWS, int NT, class First, class Done>
-IQLH_DEV void mx4_rows_chunks(const LdsRows<ROWS>& t, const Mx4Mat& b, int64_t n_end, First&& first, Done&& done) {
+template <int ROWS, int NT, class B, class First, class Done>
+IQLH_DEV void mx4_rows_chunks(const LdsRows<ROWS>& t, const B& b, int64_t n_end, First&& first, Done&& done) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
     const int steps = t.kb4 / 4;
-    uint4 bn[kFrags];
-    uint32_t bsn[kFrags];
+    typename B::Step bn[kFrags];
     auto fetch = [&](int64_t n0, int s) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < kFrags; ++j) RowFrag(b, n0 + 16 * j + r).load(s * 4 + blk, bn[j], bsn[j]);
+        for (int j = 0; j < kFrags; ++j) b.load(n0 + 16 * j, s, lane, bn[j]);
     };
     if (wave * kChunk < n_end) fetch(wave * kChunk, 0);
     for (int64_t n0 = (int64_t)wave * kChunk; n0 < n_end; n0 += NT / 64 * kChunk) {
@@ -84,8 +133,8 @@ IQLH_DEV void mx4_rows_chunks(const LdsRows<ROWS>& t, const Mx4Mat& b, int64_t n
             uint32_t bs[kFrags], as[ROWS / 16];
 #pragma unroll
             for (int j = 0; j < kFrags; ++j) {
-                bv[j] = bn[j];
-                bs[j] = bsn[j];
+                bv[j] = bn[j].v;
+                bs[j] = B::scale(bn[j], s);
             }
             if (s + 1 < steps) fetch(n0, s + 1);
             else if (n0 + NT / 64 * kChunk < n_end) fetch(n0 + NT / 64 * kChunk, 0);

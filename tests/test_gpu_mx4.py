@@ -152,7 +152,8 @@ def _operand(m, a):
 PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 3, 33), (1, 512, 256), (1, 4096, 1024), (5, 100, 64), (16, 129, 96), (17, 16, 128),
             (33, 257, 160), (64, 64, 512), (127, 130, 1000), (129, 128, 31), (200, 333, 777), (256, 512, 2048),
             (300, 17, 4100), (1024, 1, 200), (1000, 513, 256), (515, 777, 130), (16, 8, 8192), (40, 40, 6500),
-            (1030, 1031, 400), (1500, 1411, 600), (500, 1040, 700), (20, 3000, 2000), (32, 500, 288), (129, 700, 4000)]
+            (1030, 1031, 400), (1500, 1411, 600), (500, 1040, 700), (20, 3000, 2000), (32, 500, 288), (129, 700, 4000),
+            (16, 24, 9000), (500, 1040, 900), (1030, 1031, 300)]
 
 
 @pytest.mark.parametrize("mnk", PRODUCTS)
@@ -227,6 +228,69 @@ def test_large_products_exact_on_the_grid(m, mnk):
         m.mx4_linear(x, bq, other[:, :N], ws, bias=tb if use_bias else None, relu=relu)
         sync()
         assert torch.equal(other, buf)
+
+
+@pytest.mark.parametrize("mnk", [(3, 50, 100), (17, 40, 300), (70, 300, 200), (257, 900, 700), (1500, 1411, 600),
+                                 (2900, 2950, 300), (9000, 60, 100)])
+def test_rows_behind_the_last_stay_as_they_were(m, mnk):
+    """Operands and outputs as the first rows of larger buffers: NaN behind the
+    operands' last rows, and nothing written behind the output's."""
+    import torch
+    M, N, K = mnk
+    g = np.random.default_rng(M * N)
+    a, b = _grid(g, M, K), _grid(g, N, K)
+    want = torch.from_numpy(a @ b.T).float().to(dev())
+    kb = -(-K // 32)
+
+    def padded(x, rows):
+        codes = torch.full((rows + 40, kb * 16), 0x77, dtype=torch.uint8, device=dev())
+        scales = torch.full((rows + 40, kb), 255, dtype=torch.uint8, device=dev())
+        q = m.Mx4(codes[:rows], scales[:rows], rows, K)
+        m.mx4_quantize(_float(x, "float32"), q)
+        sync()
+        assert torch.all(codes[rows:] == 0x77) and torch.all(scales[rows:] == 255)
+        return q
+
+    aq, bq = padded(a, M), padded(b, N)
+    ws = m.mx4_matmul_workspace(M, N, K)
+    guard = torch.full((ws.numel() + 256,), 0x5A, dtype=torch.uint8, device=dev())
+    ws = guard[:ws.numel()]
+    for x in (None, _float(np.concatenate([a, np.full((40, K), np.nan)]), "bfloat16")[:M]):
+        buf = torch.full((M + 40, N), 77.0, device=dev())
+        if x is None:
+            m.mx4_matmul(aq, bq, buf[:M], ws)
+        else:
+            m.mx4_linear(x, bq, buf[:M], ws)
+        sync()
+        assert torch.equal(buf[:M], want)
+        assert torch.all(buf[M:] == 77.0)
+        assert torch.all(guard[ws.numel():] == 0x5A)
+    back = torch.full((M + 3, K), 77.0, device=dev())
+    m.mx4_dequantize(aq, back[:M])
+    sync()
+    assert torch.all(back[M:] == 77.0) and np.array_equal(_f64(back[:M]), a)
+
+
+def test_products_on_several_streams_at_once(m):
+    import torch
+    g = np.random.default_rng(5)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    jobs = []
+    for M, N, K in ((1, 500, 900), (200, 333, 777), (3000, 2500, 1100), (9000, 100, 200)):
+        a, b = _grid(g, M, K), _grid(g, N, K)
+        jobs.append((_float(a, "bfloat16"), _operand(m, b), torch.zeros((M, N), device=dev()),
+                     m.mx4_matmul_workspace(M, N, K), torch.from_numpy(a @ b.T).float().to(dev())))
+    sync()
+    for rep in range(4):
+        for x, b, y, ws, _ in jobs:
+            y.zero_()
+        sync()
+        for _ in range(3):
+            for st, (x, b, y, ws, _) in zip(streams, jobs):
+                m.mx4_linear(x, b, y, ws, stream=st)
+        sync()
+        for x, b, y, ws, want in jobs:
+            assert torch.equal(y, want)
 
 
 @pytest.mark.parametrize("od", DTYPES)

@@ -274,6 +274,32 @@ def test_captured_clips_share_a_workspace_and_follow_new_gradients(m):
         assert got[0] == float(eager_out[0])
 
 
+def test_calls_on_several_streams_at_once(m):
+    """Sets and workspaces of their own on four streams, the sets dropped right
+    after their calls."""
+    import torch
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    lists = [_make([50_000 + 7 * k, 33, 2000], ["float32", "bfloat16"], 60 + k) for k in range(4)]
+    want = [ref.norm(_host(ts), 0) for ts in lists]
+    outs = [torch.zeros(8, device=dev()) for _ in range(4)]
+    flats = [torch.zeros(sum(t.numel() for t in ts), device=dev()) for ts in lists]
+    wss = [m.grad_norm_workspace(m.TensorSet(ts)) for ts in lists]
+    sync()
+    for rep in range(8):
+        for k, st in enumerate(streams):
+            s = m.TensorSet(lists[k])
+            m.grad_norm(s, outs[k][rep:rep + 1], wss[k], stream=st)
+            m.grad_clip(s, 0.5, torch.zeros(2, device=dev()), wss[k], out_flat=flats[k], stream=st)
+            del s
+            torch.full((4096,), 7, dtype=torch.uint8, device=dev())  # would take the freed table's place
+    sync()
+    for k in range(4):
+        assert all(_close(float(x), want[k], 60_000) for x in outs[k])
+        c = 0.5 / want[k]
+        x = np.concatenate(_host(lists[k]))
+        assert np.all(np.abs(flats[k].double().cpu().numpy() - x * c) <= 2 * U32 * 1.001 * np.abs(x * c) + 2.0 ** -149)
+
+
 def test_more_elements_than_32_bits_count(m):
     import torch
     n = (1 << 31) + 9

@@ -65,6 +65,7 @@ def test_product_refusals(m):
     assert lin(M=0) == m.EINVAL and lin(M=(1 << 30) + 1) == m.EINVAL
     assert lin(x=None) == m.EINVAL and lin(xdt=5) == m.EINVAL and lin(xld=63) == m.EINVAL
     assert lin(b=_q(m, rows=1 << 30), ld=1 << 30, M=1 << 30, wb=1 << 60) == m.ESHAPE
+    assert lin(b=_q(m, rows=1 << 29), ld=1 << 29, M=1, wb=1 << 60) == m.ESHAPE  # 2^25 workgroups of 512
 
 
 def test_forward_refusals(m):
