@@ -31,11 +31,15 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloa
     const int64_t g = ((int64_t)(blockIdx.x % col_tiles) << c_log) + (threadIdx.x & ((1 << c_log) - 1));
     const int64_t row0 = (int64_t)(blockIdx.x / col_tiles) * rows_high * kQRows + (threadIdx.x >> c_log);
     const int count = (int)(q.cols - g * 8 < 8 ? q.cols - g * 8 : 8);
+    // a row's last group of a 16-bit type is one load where the matrix goes on
+    // behind it (2^21 x 11 bf16: 23.6 us, element by element 32.0; fp32 25.8
+    // against 20.9)
+    const typename MxFloat<DT>::type* end = DT == IQLH_F32 ? nullptr : x + (q.rows - 1) * ld + q.cols;
     float v[kQRows][8];
 #pragma unroll
     for (int i = 0; i < kQRows; ++i) {
         const int64_t row = row0 + i * rows_high;
-        load8<DT>(x + (row < q.rows ? row : q.rows - 1) * ld + g * 8, g < gpr ? count : 0, v[i]);
+        load8<DT>(x + (row < q.rows ? row : q.rows - 1) * ld + g * 8, g < gpr ? count : 0, v[i], end);
     }
 #pragma unroll
     for (int i = 0; i < kQRows; ++i) {
@@ -54,48 +58,52 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloa
 
 // Blocks along x's columns: x is [q.cols][ld].  HBM-bound.  A lane takes one
 // column of x, 32 rows a block, neighbouring lanes neighbouring addresses; a
-// workgroup 64 columns and 256 rows.  The codes pass through LDS so that a row of
-// q is written 128 bytes at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two
-// 16-bit columns per lane by dword loads 27.5, and 12.3 against 5.2 us at
-// 5001 x 777, where they leave half of the compute units without a workgroup.)
+// workgroup 2^c_log columns (64, fewer of a narrow x) and 8 blocks per wave's
+// worth of them.  The codes pass through LDS so that a row of q is written 128 bytes
+// or more at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two 16-bit columns per
+// lane by dword loads 27.5, and 12.3 against 5.2 us at 5001 x 777, where they
+// leave half of the compute units without a workgroup.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typename MxFloat<DT>::type* __restrict__ x,
-                                                                   int64_t ld, Mx4Mat q, int row_tiles) {
-    __shared__ uint4 codes[64][9];  // 9: the lanes of a store to one block column fall on different banks
-    __shared__ uint8_t scales[64][8];
+                                                                   int64_t ld, Mx4Mat q, int c_log, int row_tiles) {
+    __shared__ uint4 codes[576];  // [columns][blocks + 1]: the lanes of a store to one block fall on different banks
+    __shared__ uint8_t scales[576];
     const int64_t kb = q.kb();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * 64, b0 = (int64_t)(blockIdx.x / row_tiles) * 8;
-    const int64_t r = r0 + lane < q.rows ? r0 + lane : q.rows - 1;  // lanes past the end: not written below
+    const int columns = 1 << c_log, b_log = 9 - c_log, blocks = 1 << b_log;
+    const int c = lane & (columns - 1);
+    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * columns, b0 = (int64_t)(blockIdx.x / row_tiles) << b_log;
+    const int64_t r = r0 + c < q.rows ? r0 + c : q.rows - 1;  // lanes past the end: not written below
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const int i = wave + 4 * half;
+        const int i = ((wave + 4 * half) << (6 - c_log)) + (lane >> c_log);
         const int64_t k0 = (b0 + i) * 32;
-        if (b0 + i >= kb) break;
-        // loads at clamped rows, those behind the last one masked: no branch between them
-        const int left = (int)(q.cols - k0 < 32 ? q.cols - k0 : 32);
-        const typename MxFloat<DT>::type* p = x + k0 * ld + r;
-        float v[32];
-        uint32_t amax = 0u;
+        if (b0 + i < kb) {
+            // loads at clamped rows, those behind the last one masked: no branch between them
+            const int left = (int)(q.cols - k0 < 32 ? q.cols - k0 : 32);
+            const typename MxFloat<DT>::type* p = x + k0 * ld + r;
+            float v[32];
+            uint32_t amax = 0u;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = keep_if(j < left, MxFloat<DT>::get(p[(j < left ? j : 0) * ld]));
+            for (int j = 0; j < 32; ++j) v[j] = keep_if(j < left, MxFloat<DT>::get(p[(j < left ? j : 0) * ld]));
 #pragma unroll
-        for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[j]));
-        const uint32_t s = mx4_scale(amax);
-        uint4 w{0u, 0u, 0u, 0u};
-        if (s != 255u) {
-            const float inv = mx4_inverse(s);
-            w = uint4{mx4_codes8(v, inv), mx4_codes8(v + 8, inv), mx4_codes8(v + 16, inv), mx4_codes8(v + 24, inv)};
+            for (int j = 0; j < 32; ++j) amax = umax2(amax, abs_bits(v[j]));
+            const uint32_t s = mx4_scale(amax);
+            uint4 w{0u, 0u, 0u, 0u};
+            if (s != 255u) {
+                const float inv = mx4_inverse(s);
+                w = uint4{mx4_codes8(v, inv), mx4_codes8(v + 8, inv), mx4_codes8(v + 16, inv), mx4_codes8(v + 24, inv)};
+            }
+            codes[c * (blocks + 1) + i] = w;
+            scales[c * (blocks + 1) + i] = (uint8_t)s;
         }
-        codes[lane][i] = w;
-        scales[lane][i] = (uint8_t)s;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 512; e += kNT) {
-        const int rr = e >> 3, i = e & 7;
+        const int rr = e >> b_log, i = e & (blocks - 1);
         if (r0 + rr < q.rows && b0 + i < kb) {
-            ((uint4*)q.codes)[(r0 + rr) * kb + b0 + i] = codes[rr][i];
-            q.scales[(r0 + rr) * kb + b0 + i] = scales[rr][i];
+            ((uint4*)q.codes)[(r0 + rr) * kb + b0 + i] = codes[rr * (blocks + 1) + i];
+            q.scales[(r0 + rr) * kb + b0 + i] = scales[rr * (blocks + 1) + i];
         }
     }
 }
@@ -171,9 +179,13 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transp
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
         if (transposed) {
-            const int64_t row_tiles = (q.rows + 63) / 64, k_tiles = (q.kb() + 7) / 8;
+            // no more columns than x has, as long as there is a workgroup for
+            // every compute unit (2^22 rows of 1: 10.5 us, of 64 82; 2^14: 9.4 against 4.0)
+            int c_log = 0;
+            while (c_log < 6 && ((int64_t)1 << c_log < q.rows || q.kb() >> (9 - c_log) < 256)) ++c_log;
+            const int64_t row_tiles = (q.rows + (1 << c_log) - 1) >> c_log, k_tiles = (q.kb() + (1 << (9 - c_log)) - 1) >> (9 - c_log);
             hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)(row_tiles * k_tiles)), dim3(kNT), 0, stream,
-                               (const T*)x, ld, q, (int)row_tiles);
+                               (const T*)x, ld, q, c_log, (int)row_tiles);
         } else {
             const Shape s = shape_for(q.rows, q.kb() * 4);
             hipLaunchKernelGGL(mx4_quantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld, q,

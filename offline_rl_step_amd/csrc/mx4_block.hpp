@@ -71,11 +71,13 @@ IQLH_DEV float mx4_value(uint32_t code) {
 }
 
 // Eight neighbouring elements at p, which is aligned to its element only (the
-// hardware takes 16-byte loads at any address).  count < 8: the rest are 0.
+// hardware takes 16-byte loads at any address).  count < 8: the rest are 0, and
+// all eight are read where that does not pass `end`.
 template <int DT>
-IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
+IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v,
+                    const typename MxFloat<DT>::type* end = nullptr) {
     typedef typename MxFloat<DT>::type T;
-    if (count >= 8) {
+    if (count >= 8 || (count > 0 && end && p + 8 <= end)) {
         if constexpr (DT == IQLH_F32) {
             typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
             const f4u a = *(const f4u*)p, b = *(const f4u*)(p + 4);
@@ -89,6 +91,10 @@ IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
             const t8u a = *(const t8u*)p;
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = MxFloat<DT>::get(a[j]);
+        }
+        if (count < 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = j < count ? v[j] : 0.f;
         }
     } else {
 #pragma unroll

@@ -52,7 +52,8 @@ def _wide(seed, r, c):
     return x
 
 
-SIZES = [(1, 1), (1, 31), (3, 32), (2, 33), (5, 64), (17, 100), (64, 128), (70, 777), (257, 8), (1, 4097), (1000, 1)]
+SIZES = [(1, 1), (1, 31), (3, 32), (2, 33), (5, 64), (17, 100), (64, 128), (70, 777), (257, 8), (1, 4097), (1000, 1),
+         (20011, 1), (5000, 2), (16500, 3), (700, 5), (9000, 17), (333, 63), (40, 66)]
 
 
 @pytest.mark.parametrize("lead,pad", [(0, 0), (1, 0), (0, 3), (8, 8)])
@@ -78,6 +79,21 @@ def test_quantize_both_axes_bit_exact(m, size, dtype, lead, pad):
             m.mx4_dequantize(q, out)
             sync()
             assert torch.equal(out, torch.from_numpy(want).to(dev()).to(_t(od))), (axis, od)
+
+
+@pytest.mark.parametrize("size", [(140_000, 20), (270_003, 9), (1_100_007, 3), (4_200_005, 1)])
+def test_quantize_narrow_matrices_along_their_columns(m, size):
+    """Few columns and many rows, where a wave takes several blocks of one."""
+    r, c = size
+    x = _float(_wide(r, r, c), "bfloat16", pad=2)
+    q = m.mx4_empty(r, c, 0)
+    q.codes.fill_(0xA5)
+    q.scales.fill_(0xA5)
+    m.mx4_quantize(x, q, axis=0)
+    sync()
+    codes, scales = ref.quantize(_f64(x).T)
+    assert np.array_equal(q.scales.cpu().numpy(), scales.astype(np.uint8))
+    assert np.array_equal(q.codes.cpu().numpy(), ref.pack(codes))
 
 
 def test_quantize_every_rounding_border(m):
