@@ -35,20 +35,22 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloa
     // behind it (2^21 x 11 bf16: 23.6 us, element by element 32.0; fp32 25.8
     // against 20.9)
     const typename MxFloat<DT>::type* end = DT == IQLH_F32 ? nullptr : x + (q.rows - 1) * ld + q.cols;
-    float v[kQRows][8];
+    Eight<DT> raw[kQRows];
 #pragma unroll
     for (int i = 0; i < kQRows; ++i) {
         const int64_t row = row0 + i * rows_high;
-        load8<DT>(x + (row < q.rows ? row : q.rows - 1) * ld + g * 8, g < gpr ? count : 0, v[i], end);
+        raw[i].load(x + (row < q.rows ? row : q.rows - 1) * ld + g * 8, g < gpr ? count : 0, end);
     }
 #pragma unroll
     for (int i = 0; i < kQRows; ++i) {
         const int64_t row = row0 + i * rows_high;
+        float v[8];
+        raw[i].get(v);
         uint32_t amax = 0u;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[i][j]));
+        for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
         const uint32_t s = mx4_scale(quad_umax(amax));
-        const uint32_t w = s == 255u ? 0u : mx4_codes8(v[i], mx4_inverse(s));
+        const uint32_t w = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
         if (row < q.rows && g < gpr) {
             ((uint32_t*)q.codes)[row * gpr + g] = w;
             if ((g & 3) == 0) q.scales[(row * gpr + g) >> 2] = (uint8_t)s;

@@ -71,35 +71,38 @@ IQLH_DEV float mx4_value(uint32_t code) {
 }
 
 // Eight neighbouring elements at p, which is aligned to its element only (the
-// hardware takes 16-byte loads at any address).  count < 8: the rest are 0, and
-// all eight are read where that does not pass `end`.
+// hardware takes 16-byte loads at any address), as they lie in memory.
+// count < 8: the rest are 0, and all eight are read where that does not pass
+// `end`.
 template <int DT>
-IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v,
-                    const typename MxFloat<DT>::type* end = nullptr) {
+struct Eight {
     typedef typename MxFloat<DT>::type T;
-    if (count >= 8 || (count > 0 && end && p + 8 <= end)) {
-        if constexpr (DT == IQLH_F32) {
-            typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
-            const f4u a = *(const f4u*)p, b = *(const f4u*)(p + 4);
+    typedef T vec __attribute__((ext_vector_type(DT == IQLH_F32 ? 4 : 8), aligned(sizeof(T))));
+    static constexpr int kVecs = DT == IQLH_F32 ? 2 : 1, kPer = 8 / kVecs;
+    vec v[kVecs];
+    IQLH_DEV void load(const T* p, int count, const T* end = nullptr) {
+        if (count >= 8 || (count > 0 && end && p + 8 <= end)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = a[j];
-                v[4 + j] = b[j];
+            for (int i = 0; i < kVecs; ++i) v[i] = *(const vec*)(p + i * kPer);
+            if (count < 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j / kPer][j % kPer] = j < count ? v[j / kPer][j % kPer] : T(0);
             }
         } else {
-            typedef T t8u __attribute__((ext_vector_type(8), aligned(2)));
-            const t8u a = *(const t8u*)p;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = MxFloat<DT>::get(a[j]);
+            for (int j = 0; j < 8; ++j) v[j / kPer][j % kPer] = j < count ? p[j] : T(0);
         }
-        if (count < 8) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = j < count ? v[j] : 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < count ? MxFloat<DT>::get(p[j]) : 0.f;
     }
+    IQLH_DEV void get(float* x) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = MxFloat<DT>::get(v[j / kPer][j % kPer]);
+    }
+};
+template <int DT>
+IQLH_DEV void load8(const typename MxFloat<DT>::type* p, int count, float* v) {
+    Eight<DT> e;
+    e.load(p, count);
+    e.get(v);
 }
 
 // 16 rows from row0 on, blocks 4 step .. 4 step + 3, of a matrix in memory:
@@ -187,46 +190,42 @@ IQLH_DEV void mx4_bias4(const Mx4Out& o, int64_t n, int64_t N, float* bias) {
     }
 }
 
-// Four values rounded and stored at once
+// Four values rounded and stored at once, at any address of an element
 template <int DT>
 IQLH_DEV void mx4_put4(typename MxFloat<DT>::type* p, const float* y) {
+    const mx_f4 v = {y[0], y[1], y[2], y[3]};
     if constexpr (DT == IQLH_F32) {
-        *(float4*)p = float4{y[0], y[1], y[2], y[3]};
+        typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+        *(f4u*)p = v;
     } else if constexpr (DT == IQLH_BF16) {
         typedef __bf16 b4 __attribute__((ext_vector_type(4)));
-        *(b4*)p = __builtin_convertvector(mx_f4{y[0], y[1], y[2], y[3]}, b4);  // nearest even; a NaN stays one
+        typedef uint16_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+        *(u4*)p = __builtin_bit_cast(u4, __builtin_convertvector(v, b4));  // nearest even; a NaN stays one
     } else {
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+        typedef _Float16 h4 __attribute__((ext_vector_type(4), aligned(2)));
         *(h4*)p = h4{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
     }
 }
 
-// Four neighbouring outputs of a row, n .. n + 3, the first `count` of them
-// inside the matrix: bias, activation, one rounding.  `wide`: the row allows a
-// store of all four at once.
+// Four neighbouring outputs of a row, n .. n + 3 of N: bias, activation, one
+// rounding, one store where all four are inside.
 template <int DT>
-IQLH_DEV void mx4_store4(const Mx4Out& o, int64_t m, int64_t n, int count, mx_f4 acc, bool wide) {
+IQLH_DEV void mx4_store4(const Mx4Out& o, int64_t m, int64_t n, int64_t N, mx_f4 acc) {
     typedef typename MxFloat<DT>::type T;
-    if (count <= 0) return;
+    if (n >= N) return;
+    const float lowest = o.relu ? 0.f : -__builtin_huge_valf();
     float y[4];
+    mx4_bias4(o, n, N, y);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        y[e] = acc[e] + (o.bias && e < count ? o.bias[n + e] : 0.f);
-        if (o.relu && y[e] < 0.f) y[e] = 0.f;  // a NaN stays
-    }
+    for (int e = 0; e < 4; ++e) y[e] = __builtin_elementwise_maximum(acc[e] + y[e], lowest);  // a NaN stays
     T* p = (T*)o.p + m * o.ld + n;
-    if (wide && count >= 4) {
+    if (n + 4 <= N) {
         mx4_put4<DT>(p, y);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (e < count) p[e] = MxFloat<DT>::put(y[e]);
+            if (n + e < N) p[e] = MxFloat<DT>::put(y[e]);
     }
-}
-// whether every row of the output starts on a boundary of four elements
-template <int DT>
-IQLH_DEV bool mx4_wide_rows(const Mx4Out& o) {
-    return ((uintptr_t)o.p % (4 * sizeof(typename MxFloat<DT>::type))) == 0 && o.ld % 4 == 0;
 }
 
 }  // namespace iqlh

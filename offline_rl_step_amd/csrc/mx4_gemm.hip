@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
 #pragma unroll
         for (int w = 1; w < kFewWaves; ++w) acc += part[w][lane];
         const int64_t n = n0 + 4 * blk;
-        mx4_store4<ODT>(o, r, n, (int)(b.rows - n < 4 ? b.rows - n : 4), acc, mx4_wide_rows<ODT>(o));
+        mx4_store4<ODT>(o, r, n, b.rows, acc);
     }
 }
 
@@ -174,13 +174,12 @@ __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = mx4_mma(bv[j], av[i], acc[i][j], bs[j], as[i]);
     }
-    const bool wide = mx4_wide_rows<DT>(o);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t m = m0 + 16 * i + r, n = n0 + 16 * j + 4 * blk;
-            if (m < a.rows) mx4_store4<DT>(o, m, n, (int)(b.rows - n < 4 ? b.rows - n : 4), acc[i][j], wide);
+            if (m < a.rows) mx4_store4<DT>(o, m, n, b.rows, acc[i][j]);
         }
 }
 
@@ -272,13 +271,12 @@ __global__ __launch_bounds__(512) void mx4_split_kernel(Mx4Mat a, Mx4Mat b, Mx4O
             for (int j = 0; j < NF; ++j) part[wave][NF * i + j][lane] += acc[i][j];
     }
     __syncthreads();
-    const bool wide = mx4_wide_rows<DT>(o);
     for (int e = wave; e < MF * NF; e += 8) {
         mx_f4 v = part[0][e][lane];
 #pragma unroll
         for (int w = 1; w < 4; ++w) v += part[w][e][lane];
         const int64_t m = m0 + 16 * (e / NF) + r, n = n0 + 16 * (e % NF) + 4 * blk;
-        if (m < a.rows) mx4_store4<DT>(o, m, n, (int)(b.rows - n < 4 ? b.rows - n : 4), v, wide);
+        if (m < a.rows) mx4_store4<DT>(o, m, n, b.rows, v);
     }
 }
 

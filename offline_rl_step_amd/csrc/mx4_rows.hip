@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kNT, 4) void mx4_rows_kernel(const typename MxFloat
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K) {
     // rows enough for every compute unit, a b of at most 256 KB
     const int64_t kb = (K + 31) / 32;
-    return M >= 8192 && kb <= kRowsMaxBlocks && N * kb <= 16384;
+    return M >= 16384 && kb <= kRowsMaxBlocks && N * kb <= 16384;
 }
 
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,

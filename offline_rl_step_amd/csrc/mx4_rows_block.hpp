@@ -32,25 +32,27 @@ template <int ROWS, int NT, int XDT>
 IQLH_DEV void mx4_rows_to_lds(const typename MxFloat<XDT>::type* x, int64_t ld, int64_t M, int64_t m0, int64_t cols,
                               const LdsRows<ROWS>& t) {
     const int gpr = t.kb4 * 4;  // groups of 8 a row, a multiple of 16
-    constexpr int U = 4;        // groups in flight per thread
+    constexpr int U = XDT == IQLH_F32 ? 4 : 8;  // groups in flight per thread: 128 bytes
     for (int g0 = threadIdx.x; g0 < ROWS * gpr; g0 += NT * U) {
-        float v[U][8];
+        Eight<XDT> raw[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int e = g0 + i * NT, row = e / gpr, g = e - row * gpr;
             const int64_t m = m0 + row < M ? m0 + row : M - 1;
             const int64_t left = e < ROWS * gpr ? cols - g * 8 : 0;
-            load8<XDT>(x + m * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8), v[i]);
+            raw[i].load(x + m * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8));
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int e = g0 + i * NT, row = e / gpr, g = e - row * gpr;
             if (e >= ROWS * gpr) break;  // the same for the whole workgroup: ROWS gpr is a multiple of NT
+            float v[8];
+            raw[i].get(v);
             uint32_t amax = 0u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[i][j]));
+            for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
             const uint32_t s = mx4_scale(quad_umax(amax));
-            *(uint32_t*)(t.codes + row * t.rb + g * 4) = s == 255u ? 0u : mx4_codes8(v[i], mx4_inverse(s));
+            *(uint32_t*)(t.codes + row * t.rb + g * 4) = s == 255u ? 0u : mx4_codes8(v, mx4_inverse(s));
             if ((g & 3) == 0) t.scales[row * t.kb4 + (g >> 2)] = (uint8_t)s;
         }
     }

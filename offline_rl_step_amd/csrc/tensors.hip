@@ -32,6 +32,9 @@ namespace {
 
 constexpr int kNT = 256;
 constexpr int kAhead = 8;  // 16-byte loads in flight per thread
+// most pieces and tensors whose own norms the last workgroup of the norm launch
+// adds up (more: a launch of their own)
+constexpr int kOnePieces = 256, kOneTensors = 64;
 
 template <int DT> struct Elem;
 template <> struct Elem<IQLH_F32> {
@@ -188,9 +191,21 @@ IQLH_DEV uint64_t get_shared(const uint64_t* p) {
 // tensors' own, 16 lanes a tensor.
 template <int KIND, bool EACH>
 IQLH_DEV void finish_norm(const TensorSetArgs& a, int nb, float* out_norm, float* out_each, uint64_t* red) {
+    __shared__ uint64_t all[EACH ? 4 * kOnePieces : 1];
+    __shared__ int first[EACH ? kOneTensors + 1 : 1];
     Stat<KIND> s;
+    if constexpr (EACH) {
+        // everything that is read, in flight together
+        static_assert(kOneTensors < kNT && kOnePieces <= kNT, "one load a thread");
+        if ((int)threadIdx.x <= a.count) first[threadIdx.x] = a.first[threadIdx.x];
+        if ((int)threadIdx.x < nb) s.join(get_shared(a.part + threadIdx.x));  // nb = npieces, or 1 without any
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((int)threadIdx.x < a.npieces) all[4 * threadIdx.x + i] = get_shared(a.each + 4 * threadIdx.x + i);
+    } else {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < nb; i += kNT) s.join(get_shared(a.part + i));
+        for (int i = threadIdx.x; i < nb; i += kNT) s.join(get_shared(a.part + i));
+    }
     const double n = block_join(s, red).norm();
     if (threadIdx.x == 0) {
         *out_norm = (float)n;
@@ -200,11 +215,8 @@ IQLH_DEV void finish_norm(const TensorSetArgs& a, int nb, float* out_norm, float
         for (int t0 = 0; t0 < a.count; t0 += kNT / 16) {  // every lane takes part in the exchanges
             const int t = t0 + threadIdx.x / 16;
             Stat<KIND> v;
-            if (t < a.count) {
-                const int end = a.first[t + 1] * 4;
-#pragma unroll 4
-                for (int i = a.first[t] * 4 + (threadIdx.x & 15); i < end; i += 16) v.join(get_shared(a.each + i));
-            }
+            if (t < a.count)
+                for (int i = first[t] * 4 + (threadIdx.x & 15); i < first[t + 1] * 4; i += 16) v.join(all[i]);
             v = lanes_join<8>(v);
             if (t < a.count && (threadIdx.x & 15) == 0) out_each[t] = (float)v.norm();
         }
@@ -381,7 +393,7 @@ hipError_t norm_pass(const TensorSetArgs& a, float* out_norm, float* out_each, h
 template <int KIND>
 hipError_t norm_launch(const TensorSetArgs& a, float* out_norm, float* out_each, hipStream_t stream) {
     if (!out_each) return norm_pass<KIND, false, true>(a, out_norm, out_each, stream);
-    if (a.count <= 64 && a.npieces <= 512) return norm_pass<KIND, true, true>(a, out_norm, out_each, stream);
+    if (a.count <= kOneTensors && a.npieces <= kOnePieces) return norm_pass<KIND, true, true>(a, out_norm, out_each, stream);
     hipError_t e = norm_pass<KIND, true, false>(a, out_norm, out_each, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(grad_norm_finish_kernel<KIND>, dim3(1 + a.count), dim3(kNT), 0, stream, a, norm_blocks(a.npieces),

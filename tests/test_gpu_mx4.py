@@ -209,6 +209,7 @@ def test_product_exact_on_the_grid(m, mnk):
 
 @pytest.mark.parametrize("mnk", [(2900, 2950, 1056), (2817, 3000, 1500), (8200, 1030, 1024), (1000, 9000, 2100),
                                  (33000, 250, 1024), (4096, 4096, 4096), (8192, 512, 256), (9001, 77, 33), (12345, 513, 130),
+                                 (16384, 512, 256), (17001, 77, 33), (16399, 513, 130), (16384, 16, 1000),
                                  (65536, 128, 128), (8200, 450, 1000), (4000, 3300, 260), (1409, 1500, 3000), (700, 2500, 1111)])
 def test_large_products_exact_on_the_grid(m, mnk):
     """Products of many tiles, ragged in each size: equality with the oracle
