@@ -576,16 +576,21 @@ Path pick(int64_t M, int64_t N, int64_t K) {
     // 256 tiles for most compute units (2048 x 4096 x 4096, 128 of them: 39.1 us
     // against 30.5 with 128 tiles; 4096^3, 256 of them: 45.0)
     if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
+    // a step or two: the waves that split k have little to split, but eight of
+    // them store a 64 x 64 tile; more tiles than two rounds go to 128 x 128 by four
+    // waves (1000 x 1000 x 128: 5.4 against 6.5 us, 2000 x 2000 x 200 15.9 against 8.2)
+    const int64_t tiles64 = tiles_of(M, N, 64);
+    if (K <= 256) return tiles64 <= 512 ? Path::split4 : Path::direct;
     // 128 tiles against waves that split k, both as measured up to a round of
     // tiles: the tiles take 8 us and 2.1 per 1000 k whatever their number, the
     // splitting waves 3 us and 5 per 10^9 products (as many at K 1024 and below,
     // where waves go without a step).  768 x 1024 x 4096: 16.3 against 29.5 us;
-    // 512 x 512 x 2048: 11.7 against 8.5
+    // 512 x 512 x 2048: 11.7 against 8.5; 6281 x 1202 x 454: 13.3 against 32.2
     const double split_us = 3.0 + 5e-9 * (double)M * (double)N * (double)(K < 1024 ? 1024 : K);
-    if (lds_tiles && K >= 512 && split_us > 8.0 + 2.1e-3 * (double)K) return Path::tile128;
-    if (K <= 256) return Path::direct;
-    // the largest of its tiles that gives every compute unit one
-    if (tiles_of(M, N, 64) >= 256) return Path::split4;
+    if (lds_tiles && split_us > 8.0 + 2.1e-3 * (double)K) return Path::tile128;
+    // the largest of the splitting tiles that gives every compute unit one,
+    // where there are steps for all eight waves
+    if (K <= 512 || tiles64 >= 256) return Path::split4;
     if (M > 32 && ((M + 63) / 64) * ((N + 31) / 32) >= 256) return Path::split2;
     return Path::split1;
 }
