@@ -264,8 +264,8 @@ size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                            hipStream_t stream);
-// at most 16 short rows, in one launch too
-bool mx4_few_ok(int64_t M, int64_t K);
+// few or short rows, in one launch too
+bool mx4_few_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                           hipStream_t stream);
 size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);

@@ -213,7 +213,7 @@ size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx4_linear(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                              void* workspace, hipStream_t stream) {
-    if (mx4_few_ok(M, b.cols)) return launch_mx4_few(x, dtype, ld, M, b, out, stream);
+    if (mx4_few_ok(M, b.rows, b.cols)) return launch_mx4_few(x, dtype, ld, M, b, out, stream);
     if (mx4_rows_ok(M, b.rows, b.cols)) return launch_mx4_rows(x, dtype, ld, M, b, out, stream);
     const int64_t blocks = M * b.kb();
     const Mx4Mat a{(uint8_t*)workspace, (uint8_t*)workspace + blocks * 16, M, b.cols};

@@ -18,6 +18,7 @@ namespace iqlh {
 namespace {
 
 constexpr int kNT = 256;
+constexpr int kComputeUnits = 256;
 
 template <typename F>
 hipError_t by_dtype(int dtype, F f) {
@@ -28,8 +29,8 @@ hipError_t by_dtype(int dtype, F f) {
 }
 
 // ------------------------------------------------------------- few rows
-// M <= 16.  HBM-bound on b, at small sizes on the latency of one pass over it.
-// Workgroup: 16 rows of b.  Wave w of 8 takes the k steps w, w + 8, ..; U
+// HBM-bound on b, at small sizes on the latency of one pass over it.
+// Workgroup: 16 rows of b and up to 16 MF rows of the left operand.  Wave w of 8 takes the k steps w, w + 8, ..; U
 // steps' loads of b are in flight together, the first of them before anything
 // else.  The left operand lies in LDS, as rows of whole steps: copied there, or
 // (XDT >= 0, a float matrix) quantised into it by every workgroup, an eighth of a
@@ -38,17 +39,18 @@ hipError_t by_dtype(int dtype, F f) {
 // scales come as 4 bytes per row to 16 lanes.  The waves' sums meet in LDS, added in
 // wave order.
 constexpr int kFewWaves = 8;
-constexpr int kFewElements = 32768;  // of a float left operand, padded
-template <int XDT, int ODT>
+constexpr int kFewElements = 32768;  // of a workgroup's part of a float left operand, padded
+template <int XDT, int ODT, int MF>
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, const void* x, int64_t ld, Mx4Mat b,
-                                                                      Mx4Out o) {
+                                                                      Mx4Out o, int n_tiles) {
     constexpr int U = 4, NT = 64 * kFewWaves;
     extern __shared__ __align__(16) uint8_t lds[];
-    mx_f4(*part)[64] = (mx_f4(*)[64])lds;            // [kFewWaves][64]
-    uint8_t* codes = lds + kFewWaves * 64 * 16;      // [M][kb4 * 16 + 16]
+    mx_f4(*part)[MF][64] = (mx_f4(*)[MF][64])lds;    // [kFewWaves]
+    uint8_t* codes = lds + kFewWaves * MF * 64 * 16;  // [rows][kb4 * 16 + 16]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = (int64_t)(blockIdx.x % n_tiles) * 16, m0 = (int64_t)(blockIdx.x / n_tiles) * (16 * MF);
+    const int rows = (int)(a.rows - m0 < 16 * MF ? a.rows - m0 : 16 * MF);
     const RowFrag fb(b, n0 + r);
     const int kb = (int)b.kb(), steps = (kb + 3) / 4;
     uint4 bv[U];
@@ -76,14 +78,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
     };
     load_b(wave);
     const int kb4 = steps * 4, rb = kb4 * 16 + 16;
-    uint8_t* scales = codes + a.rows * rb;           // [M][kb4]
+    uint8_t* scales = codes + rows * rb;             // [rows][kb4]
     if constexpr (XDT >= 0) {
         const int gpr = kb4 * 4;                     // groups of 8 a row
-        for (int e = threadIdx.x; e < (int)a.rows * gpr; e += NT) {  // four lanes share a block: gpr is a multiple of 16
+        for (int e = threadIdx.x; e < rows * gpr; e += NT) {  // four lanes share a block: gpr is a multiple of 16
             const int row = e / gpr, g = e - row * gpr;
             const int64_t left = a.cols - g * 8;
             float v[8];
-            load8<XDT>((const typename MxFloat<XDT>::type*)x + row * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8), v);
+            load8<XDT>((const typename MxFloat<XDT>::type*)x + (m0 + row) * ld + g * 8, (int)(left < 0 ? 0 : left < 8 ? left : 8), v);
             uint32_t amax = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) amax = umax2(amax, abs_bits(v[j]));
@@ -92,10 +94,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
             if ((g & 3) == 0) scales[row * kb4 + (g >> 2)] = (uint8_t)s;
         }
     } else {
-        for (int e = threadIdx.x; e < (int)a.rows * kb4; e += NT) {
+        for (int e = threadIdx.x; e < rows * kb4; e += NT) {
             const int row = e / kb4, k = e - row * kb4;
             const bool in = k < kb;
-            const int64_t at = (int64_t)row * kb + (in ? k : 0);
+            const int64_t at = (m0 + row) * kb + (in ? k : 0);
             const uint4 w = ((const uint4*)a.codes)[at];
             const uint32_t s = a.scales[at], keep = in ? 0xFFFFFFFFu : 0u;
             *(uint4*)(codes + row * rb + k * 16) = uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep};
@@ -103,45 +105,60 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
         }
     }
     __syncthreads();
-    mx_f4 acc = {0.f, 0.f, 0.f, 0.f};
+    mx_f4 acc[MF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) acc[i] = mx_f4{0.f, 0.f, 0.f, 0.f};
     for (int s0 = wave; s0 < steps; s0 += kFewWaves * U) {
         if (s0 != wave) load_b(s0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * kFewWaves;
-            const bool in = s < steps && r < a.rows;
-            const int at = in ? s * 4 + blk : 0, row = in ? r : 0;
-            const uint4 w = *(const uint4*)(codes + row * rb + at * 16);
-            const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
-            const uint32_t as = in ? scales[row * kb4 + at] : 127u;
             const uint32_t bs = (uint32_t)__shfl((int)bw[u], r, kWave) >> (8 * blk) & 255u;
-            acc = mx4_mma(bv[u], uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep}, acc, bs, as);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const bool in = s < steps && 16 * i + r < rows;
+                const int at = in ? s * 4 + blk : 0, row = in ? 16 * i + r : 0;
+                const uint4 w = *(const uint4*)(codes + row * rb + at * 16);
+                const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+                const uint32_t as = in ? scales[row * kb4 + at] : 127u;
+                acc[i] = mx4_mma(bv[u], uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep}, acc[i], bs, as);
+            }
         }
     }
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0 && r < a.rows) {
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) acc += part[w][lane];
-        const int64_t n = n0 + 4 * blk;
-        mx4_store4<ODT>(o, r, n, b.rows, acc);
+    for (int i = 0; i < MF; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave < MF && 16 * wave + r < rows) {
+        mx_f4 v = part[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) v += part[w][wave][lane];
+        mx4_store4<ODT>(o, m0 + 16 * wave + r, n0 + 4 * blk, b.rows, v);
     }
 }
 
-// LDS of a left operand of M rows and K columns beside the sums
-int64_t few_bytes(int64_t M, int64_t K) { return kFewWaves * 1024 + M * ((K + 127) / 128 * 68 + 16); }
+// LDS of a left operand of `rows` rows and K columns, and of the sums
+int64_t few_bytes(int64_t rows, int64_t K, int MF = 1) {
+    return kFewWaves * 1024 * MF + rows * ((K + 127) / 128 * 68 + 16);
+}
 
-template <int XDT>
+template <int XDT, int MF>
 hipError_t launch_few_rows(const Mx4Mat& a, const void* x, int64_t ld, const Mx4Mat& b, const Mx4Out& out,
                            hipStream_t stream) {
-    const int bytes = (int)few_bytes(a.rows, b.cols);
+    const int bytes = (int)few_bytes(a.rows < 16 * MF ? a.rows : 16 * MF, b.cols, MF);
+    const int64_t nt = (b.rows + 15) / 16, mt = (a.rows + 16 * MF - 1) / (16 * MF);
     return by_dtype(out.dtype, [&](auto dt) {
-        auto kernel = mx4_few_rows_kernel<XDT, decltype(dt)::value>;
+        auto kernel = mx4_few_rows_kernel<XDT, decltype(dt)::value, MF>;
         if (bytes > 64 << 10)
             (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        hipLaunchKernelGGL((mx4_few_rows_kernel<XDT, decltype(dt)::value>), dim3((uint32_t)((b.rows + 15) / 16)),
-                           dim3(64 * kFewWaves), bytes, stream, a, x, ld, b, out);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(nt * mt)), dim3(64 * kFewWaves), bytes, stream, a, x, ld, b, out, (int)nt);
     });
+}
+template <int XDT>
+hipError_t launch_few_rows_of(const Mx4Mat& a, const void* x, int64_t ld, const Mx4Mat& b, const Mx4Out& out,
+                              hipStream_t stream) {
+    return a.rows <= 16   ? launch_few_rows<XDT, 1>(a, x, ld, b, out, stream)
+           : a.rows <= 32 ? launch_few_rows<XDT, 2>(a, x, ld, b, out, stream)
+                          : launch_few_rows<XDT, 4>(a, x, ld, b, out, stream);
 }
 
 // --------------------------------------------- short sums, straight from memory
@@ -644,20 +661,28 @@ bool mx4_launchable(int64_t M, int64_t N, int64_t K) {
     return ((M + 31) / 32 + (N + 31) / 32) * kNT < top;
 }
 
-bool mx4_few_ok(int64_t M, int64_t K) { return M <= 16 && M * ((K + 127) / 128 * 128) <= kFewElements; }
+// One launch with the left operand quantised by every workgroup: for up to 16
+// rows, and for more where the workgroups are one round (61 x 26, K 407: 8.5
+// us, in two launches 9.9; two and a half rounds at 33 x 5853, K 385: 12.3 against
+// 10.0)
+bool mx4_few_ok(int64_t M, int64_t N, int64_t K) {
+    const int64_t k4 = (K + 127) / 128 * 128, nt = (N + 15) / 16;
+    if ((M < 64 ? M : 64) * k4 > kFewElements) return false;
+    return M <= 16 || nt * ((M + 63) / 64) <= kComputeUnits;
+}
 
 hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                           hipStream_t stream) {
     const Mx4Mat a{nullptr, nullptr, M, b.cols};
-    if (dtype == IQLH_F32) return launch_few_rows<IQLH_F32>(a, x, ld, b, out, stream);
-    if (dtype == IQLH_BF16) return launch_few_rows<IQLH_BF16>(a, x, ld, b, out, stream);
-    return launch_few_rows<IQLH_F16>(a, x, ld, b, out, stream);
+    if (dtype == IQLH_F32) return launch_few_rows_of<IQLH_F32>(a, x, ld, b, out, stream);
+    if (dtype == IQLH_BF16) return launch_few_rows_of<IQLH_BF16>(a, x, ld, b, out, stream);
+    return launch_few_rows_of<IQLH_F16>(a, x, ld, b, out, stream);
 }
 
 hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace,
                              hipStream_t stream) {
     switch (pick(a.rows, b.rows, a.cols)) {
-        case Path::few: return launch_few_rows<-1>(a, nullptr, 0, b, out, stream);
+        case Path::few: return launch_few_rows<-1, 1>(a, nullptr, 0, b, out, stream);
         case Path::tile256: return launch_tiles<256>(a, b, out, workspace, stream);
         case Path::tile128: return launch_tiles<128>(a, b, out, workspace, stream);
         case Path::split4: return launch_split<4, 4>(a, b, out, stream);
