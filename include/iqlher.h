@@ -571,12 +571,14 @@ typedef struct iqlh_mx4 {
  *   transposed 0: x is [out->rows][ld], ld >= out->cols, blocks along x's
  *              rows.  1: x is [out->cols][ld], ld >= out->rows, and the
  *              transpose is quantised: blocks along x's columns (the operand
- *              of a product that sums over x's rows). */
+ *              of a product that sums over x's rows).
+ * x and out must not share memory.  Sizes whose launch would hold 2^32 threads
+ * or more (from about 2^35 elements on) are refused, here and below. */
 int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transposed, const iqlh_mx4* out,
                       void* stream);
 
 /* out[r][c] = value of element (r, c), rounded once to `dtype` (exact in
- * binary32); ld >= q->cols. */
+ * binary32); ld >= q->cols; out and q must not share memory. */
 int iqlh_mx4_dequantize(const iqlh_mx4* q, void* out, int32_t dtype, int64_t ld, void* stream);
 
 /* out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]), a [M, K] and b [N, K]

@@ -418,7 +418,7 @@ class TensorSet:
         self._home = _stream(None).value  # the allocator reuses the table's memory in this stream's order
         self.struct.d_table = self.table.data_ptr()
         self.ref = ctypes.byref(self.struct)
-        self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
+        self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
 
     @property
     def numel(self):
@@ -527,7 +527,7 @@ def _matrix(t, rows, cols, device, what):
 def mx4_quantize(x, out, axis=1, stream=None):
     """Quantises x [rows, cols] (float32, bfloat16, float16; rows may be
     strided) in blocks along its rows (axis=1) or, transposed, its columns
-    (axis=0) into the Mx4 `out`."""
+    (axis=0) into the Mx4 `out`, which must not share memory with it."""
     if axis not in (0, 1):
         raise ValueError("axis must be 0 or 1")
     _need_current(out.device)
@@ -561,7 +561,8 @@ def _need_product(rows, b, out, workspace, bias):
 
 
 def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
-    """out[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]) of two Mx4."""
+    """out[m, n] = act(sum_k a[m, k] b[n, k] + bias[n]) of two Mx4; out must not
+    share memory with an operand."""
     if a.device != b.device:
         raise ValueError(f"a is on {a.device}, b on {b.device}")
     dt, ld = _need_product(a.rows, b, out, workspace, bias)

@@ -712,6 +712,9 @@ int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transpos
     if (transposed != 0 && transposed != 1) return fail(IQLH_EINVAL, "iqlh_mx4_quantize: transposed must be 0 or 1");
     rc = check_float_matrix("iqlh_mx4_quantize", x, dtype, ld, transposed ? q.rows : q.cols);
     if (rc) return rc;
+    if (!mx4_quantizable(q.rows, q.cols, transposed != 0))
+        return fail(IQLH_ESHAPE, "iqlh_mx4_quantize: %lld x %lld is more than one launch takes", (long long)q.rows,
+                    (long long)q.cols);
     hipError_t e = launch_mx4_quantize(x, dtype, ld, transposed != 0, q, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_quantize launch");
     return IQLH_OK;
@@ -723,6 +726,9 @@ int iqlh_mx4_dequantize(const iqlh_mx4* in, void* out, int32_t dtype, int64_t ld
     if (rc) return rc;
     rc = check_float_matrix("iqlh_mx4_dequantize", out, dtype, ld, q.cols);
     if (rc) return rc;
+    if (!mx4_dequantizable(q.rows, q.cols, dtype_bytes(dtype)))
+        return fail(IQLH_ESHAPE, "iqlh_mx4_dequantize: %lld x %lld is more than one launch takes", (long long)q.rows,
+                    (long long)q.cols);
     hipError_t e = launch_mx4_dequantize(q, out, dtype, ld, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_dequantize launch");
     return IQLH_OK;
@@ -782,6 +788,9 @@ int iqlh_mx4_linear(const void* x, int32_t dtype, int64_t ld, int64_t M, const i
     if (!rc) rc = check_mx4_product("iqlh_mx4_linear", M, bm, bias, relu, out, out_dtype, ld_out, workspace,
                                     workspace_bytes, &o);
     if (rc) return rc;
+    if (!mx4_linear_launchable(M, bm.rows, bm.cols))
+        return fail(IQLH_ESHAPE, "iqlh_mx4_linear: x of %lld x %lld is more than one launch takes", (long long)M,
+                    (long long)bm.cols);
     hipError_t e = launch_mx4_linear(x, dtype, ld, M, bm, o, workspace, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_linear launch");
     return IQLH_OK;

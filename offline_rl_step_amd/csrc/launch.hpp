@@ -256,18 +256,23 @@ struct Mx4Out {
     int64_t ld;
     const float* bias;  // or null
 };
-// workspace of a product: the left operand quantised on the way, then the
-// partial sums of a split summed axis
+// whether the launches of a conversion (es: bytes of an element) or a product stay
+// below 2^32 threads
+bool mx4_quantizable(int64_t rows, int64_t cols, bool transposed);
+bool mx4_dequantizable(int64_t rows, int64_t cols, int es);
 bool mx4_launchable(int64_t M, int64_t N, int64_t K);
+bool mx4_linear_launchable(int64_t M, int64_t N, int64_t K);  // beside mx4_launchable
+// workspace of a product: the scales of both operands regrouped
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 // many rows times a small b, quantisation and product in one launch
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                            hipStream_t stream);
-// few or short rows, in one launch too
+// few rows, in one launch too
 bool mx4_few_ok(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
                           hipStream_t stream);
+// and of a linear: the left operand quantised on the way
 size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream);

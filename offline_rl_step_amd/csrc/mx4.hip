@@ -163,6 +163,7 @@ struct Shape {
     int c_log, col_tiles;
     int64_t blocks;
 };
+constexpr int64_t kMostBlocks = ((int64_t)1 << 32) / kNT - 1;  // launches hold less than 2^32 threads
 Shape shape_for(int64_t rows, int64_t across) {
     Shape s;
     s.c_log = 2;
@@ -173,7 +174,33 @@ Shape shape_for(int64_t rows, int64_t across) {
     return s;
 }
 
+// Columns a workgroup (2^c_log) and workgroups of a quantisation along x's columns:
+// no more columns than x has, as long as there is a workgroup for every
+// compute unit (2^22 rows of 1: 10.5 us, of 64 82; 2^14: 9.4 against 4.0)
+struct ColumnShape {
+    int c_log;
+    int64_t row_tiles, blocks;
+};
+ColumnShape column_shape_for(int64_t rows, int64_t kb) {
+    ColumnShape s;
+    s.c_log = 0;
+    while (s.c_log < 6 && ((int64_t)1 << s.c_log < rows || kb >> (9 - s.c_log) < 256)) ++s.c_log;
+    s.row_tiles = (rows + (1 << s.c_log) - 1) >> s.c_log;
+    s.blocks = s.row_tiles * ((kb + (1 << (9 - s.c_log)) - 1) >> (9 - s.c_log));
+    return s;
+}
+
+int64_t dequantize_across(int64_t cols, int es) { return (cols * es + 15) / 16; }
+
 }  // namespace
+
+bool mx4_quantizable(int64_t rows, int64_t cols, bool transposed) {
+    const int64_t kb = (cols + 31) / 32;
+    return (transposed ? column_shape_for(rows, kb).blocks : shape_for(rows, kb * 4).blocks) <= kMostBlocks;
+}
+bool mx4_dequantizable(int64_t rows, int64_t cols, int es) {
+    return shape_for(rows, dequantize_across(cols, es)).blocks <= kMostBlocks;
+}
 
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream) {
@@ -181,13 +208,9 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transp
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
         if (transposed) {
-            // no more columns than x has, as long as there is a workgroup for
-            // every compute unit (2^22 rows of 1: 10.5 us, of 64 82; 2^14: 9.4 against 4.0)
-            int c_log = 0;
-            while (c_log < 6 && ((int64_t)1 << c_log < q.rows || q.kb() >> (9 - c_log) < 256)) ++c_log;
-            const int64_t row_tiles = (q.rows + (1 << c_log) - 1) >> c_log, k_tiles = (q.kb() + (1 << (9 - c_log)) - 1) >> (9 - c_log);
-            hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)(row_tiles * k_tiles)), dim3(kNT), 0, stream,
-                               (const T*)x, ld, q, c_log, (int)row_tiles);
+            const ColumnShape s = column_shape_for(q.rows, q.kb());
+            hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld,
+                               q, s.c_log, (int)s.row_tiles);
         } else {
             const Shape s = shape_for(q.rows, q.kb() * 4);
             hipLaunchKernelGGL(mx4_quantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld, q,
@@ -200,7 +223,7 @@ hipError_t launch_mx4_dequantize(const Mx4Mat& q, void* out, int dtype, int64_t 
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
-        const Shape s = shape_for(q.rows, (q.cols * (int64_t)sizeof(T) + 15) / 16);
+        const Shape s = shape_for(q.rows, dequantize_across(q.cols, sizeof(T)));
         hipLaunchKernelGGL(mx4_dequantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, q, (T*)out, ld, s.c_log,
                            s.col_tiles);
     });
@@ -209,6 +232,10 @@ hipError_t launch_mx4_dequantize(const Mx4Mat& q, void* out, int dtype, int64_t 
 size_t mx4_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const size_t kb = (size_t)(K + 31) / 32;
     return (size_t)M * kb * 16 + ((size_t)M * kb + 15) / 16 * 16 + mx4_matmul_workspace_bytes(M, N, K);
+}
+
+bool mx4_linear_launchable(int64_t M, int64_t N, int64_t K) {
+    return mx4_few_ok(M, N, K) || mx4_rows_ok(M, N, K) || mx4_quantizable(M, K, false);
 }
 
 hipError_t launch_mx4_linear(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,

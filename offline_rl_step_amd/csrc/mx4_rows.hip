@@ -77,9 +77,10 @@ __global__ __launch_bounds__(kNT, 4) void mx4_rows_kernel(const typename MxFloat
 }  // namespace
 
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K) {
-    // rows enough for every compute unit, a b of at most 256 KB
+    // rows enough for every compute unit, and less than 2^32 threads of them; a b
+    // of at most 256 KB
     const int64_t kb = (K + 31) / 32;
-    return M >= 16384 && kb <= kRowsMaxBlocks && N * kb <= 16384;
+    return M >= 16384 && M <= 1 << 29 && kb <= kRowsMaxBlocks && N * kb <= 16384;
 }
 
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,

@@ -617,3 +617,16 @@ def test_binding_refusals(m):
         m.mx4_matmul(q, m.mx4_empty(4, 64), y, ws[:16])
     with pytest.raises(ValueError):
         m.Mx4(q.codes[:, :16], q.scales, 4, 64)
+
+
+@pytest.mark.parametrize("M", [1 << 29, 1 << 30])
+def test_most_rows_of_one_column(m, M):
+    """The most rows of the one-launch kernel and of a matrix.  Multiples of 1 up
+    to 3 are exact in 4 bits, and so are their doubles in bf16."""
+    import torch
+    x = (torch.arange(M, dtype=torch.int32, device="cuda") % 7 - 3).to(torch.bfloat16)[:, None]
+    b = m.mx4_empty(1, 1)
+    m.mx4_quantize(torch.full((1, 1), 2.0, device="cuda"), b)
+    out = torch.full((M, 1), 99.0, dtype=torch.bfloat16, device="cuda")
+    m.mx4_linear(x, b, out, m.mx4_matmul_workspace(M, 1, 1))
+    assert torch.equal(out, x * 2)

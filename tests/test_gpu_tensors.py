@@ -344,3 +344,14 @@ def test_feeds_the_gradient_budget(m):
     want, wn, _, _ = budget.accumulate(src, (0.7, 0.3), (1.0, 1.0), 1.0)
     assert np.linalg.norm(grad.double().cpu().numpy() - want) <= 1e-5 * np.linalg.norm(want)
     assert abs(float(norms[0]) - wn[0]) <= 1e-5 * wn[0]
+
+
+def test_flat_output_inside_a_tensor_is_refused_beside_empty_tensors(m):
+    import torch
+    base = torch.zeros(4096, device="cuda")
+    ts = m.TensorSet([base[:2048], base[1000:1000], base[3000:3000]])
+    ws, out = m.grad_norm_workspace(ts), torch.empty(2, device="cuda")
+    for lo in (0, 900, 2047 - 64):
+        with pytest.raises(ValueError, match="shares memory"):
+            m.grad_clip(ts, 1.0, out, ws, out_flat=base[lo:lo + 2048])
+    m.grad_clip(ts, 1.0, out, ws, out_flat=base[2048:])

@@ -68,6 +68,17 @@ def test_product_refusals(m):
     assert lin(b=_q(m, rows=1 << 29), ld=1 << 29, M=1, wb=1 << 60) == m.ESHAPE  # 2^25 workgroups of 512
 
 
+def test_launches_that_would_hold_too_many_threads_are_refused(m):
+    big = lambda rows, cols: _q(m, rows=rows, cols=cols)  # noqa: E731
+    assert m._lib_mx4_quantize(P(A), 1, 4096, 0, big(1 << 28, 4096), None) == m.ESHAPE and "launch" in m.last_error()
+    assert m._lib_mx4_quantize(P(A), 1, 1 << 28, 1, big(1 << 28, 4096), None) == m.ESHAPE
+    assert m._lib_mx4_dequantize(big(1 << 28, 4096), P(A), 1, 4096, None) == m.ESHAPE
+    assert m._lib_mx4_dequantize(big(1 << 30, 257), P(A), 0, 257, None) == m.ESHAPE
+    # a product whose tiles one launch takes, of an x whose quantisation it does not
+    assert m._lib_mx4_linear(P(A), 1, 8192, 1 << 28, big(1, 8192), None, 0, P(A), 1, 1, P(A), 1 << 60,
+                             None) == m.ESHAPE and "x of" in m.last_error()
+
+
 def test_forward_refusals(m):
     b = ctypes.c_size_t()
     assert m._lib_forward_mx4_ws(None, 4, ctypes.byref(b)) == m.EINVAL
