@@ -17,6 +17,7 @@ hipError_t by_dtype(int dtype, F f) {
 }
 
 // ------------------------------------------------------------ quantisation
+constexpr int kNarrowRows = 4;
 constexpr int kQRows = 4;  // rows (times the workgroup's) a thread converts
 
 // Blocks along x's rows.  HBM-bound.  A thread converts 8 elements (one dword
@@ -58,23 +59,72 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloa
     }
 }
 
+// The same for a matrix of one block a row and at most 8 G columns: a lane
+// takes a row, so that its codes leave as 16 bytes.  (2^22 x 1 bf16 47 -> 15 us,
+// 2^22 x 3 46 -> 18, 2^21 x 11 25 -> 15.5.)
+template <int DT, int G>
+__global__ __launch_bounds__(kNT) void mx4_quantize_narrow_kernel(const typename MxFloat<DT>::type* __restrict__ x,
+                                                                  int64_t ld, Mx4Mat q) {
+    const int64_t row0 = (int64_t)blockIdx.x * (kNT * kNarrowRows) + threadIdx.x;
+    const int cols = (int)q.cols;
+    const typename MxFloat<DT>::type* end = DT == IQLH_F32 || cols < 3 ? nullptr : x + (q.rows - 1) * ld + cols;
+    Eight<DT> raw[kNarrowRows][G];
+#pragma unroll
+    for (int i = 0; i < kNarrowRows; ++i) {
+        const int64_t row = row0 + i * kNT < q.rows ? row0 + i * kNT : q.rows - 1;
+#pragma unroll
+        for (int g = 0; g < G; ++g) raw[i][g].load(x + row * ld + 8 * g, cols - 8 * g < 8 ? cols - 8 * g : 8, end);
+    }
+#pragma unroll
+    for (int i = 0; i < kNarrowRows; ++i) {
+        float v[8 * G];
+        uint32_t amax = 0u;
+#pragma unroll
+        for (int g = 0; g < G; ++g) raw[i][g].get(v + 8 * g);
+#pragma unroll
+        for (int j = 0; j < 8 * G; ++j) amax = umax2(amax, abs_bits(v[j]));
+        const uint32_t s = mx4_scale(amax);
+        const int64_t row = row0 + i * kNT;
+        if (row < q.rows) {
+            uint4 w{0u, 0u, 0u, 0u};
+            if (s != 255u) {
+                const float inv = mx4_inverse(s);
+                w.x = mx4_codes8(v, inv);
+                if (G > 1) w.y = mx4_codes8(v + 8, inv);
+            }
+            ((uint4*)q.codes)[row] = w;
+            q.scales[row] = (uint8_t)s;
+        }
+    }
+}
+
 // Blocks along x's columns: x is [q.cols][ld].  HBM-bound.  A lane takes one
 // column of x, 32 rows a block, neighbouring lanes neighbouring addresses; a
 // workgroup 2^c_log columns (64, fewer of a narrow x) and 8 blocks per wave's
 // worth of them.  The codes pass through LDS so that a row of q is written 128 bytes
 // or more at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two 16-bit columns per
 // lane by dword loads 27.5, and 12.3 against 5.2 us at 5001 x 777, where they
-// leave half of the compute units without a workgroup.)
+// leave half of the compute units without a workgroup.  Runs of tiles per XCD:
+// 65536 x 777 fp32 52 -> 34 us, bf16 38 -> 21.5; rows on cache lines lose by them,
+// 4096 x 16384 fp32 49 -> 53.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typename MxFloat<DT>::type* __restrict__ x,
-                                                                   int64_t ld, Mx4Mat q, int c_log, int row_tiles) {
+                                                                   int64_t ld, Mx4Mat q, int c_log, int row_tiles,
+                                                                   int shared_lines) {
     __shared__ uint4 codes[576];  // [columns][blocks + 1]: the lanes of a store to one block fall on different banks
     __shared__ uint8_t scales[576];
     const int64_t kb = q.kb();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int columns = 1 << c_log, b_log = 9 - c_log, blocks = 1 << b_log;
     const int c = lane & (columns - 1);
-    const int64_t r0 = (int64_t)(blockIdx.x % row_tiles) * columns, b0 = (int64_t)(blockIdx.x / row_tiles) << b_log;
+    // rows of x that do not start on cache lines: neighbouring tiles share the lines at
+    // their border, so each XCD (every eighth workgroup) gets a run of tiles
+    uint32_t id = blockIdx.x;
+    if (shared_lines) {
+        const uint32_t per = gridDim.x / 8, rest = gridDim.x % 8, xcd = id & 7;
+        id = xcd * per + (xcd < rest ? xcd : rest) + (id >> 3);
+    }
+    const int64_t r0 = (int64_t)(id % row_tiles) * columns, b0 = (int64_t)(id / row_tiles) << b_log;
     const int64_t r = r0 + c < q.rows ? r0 + c : q.rows - 1;  // lanes past the end: not written below
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -204,13 +254,19 @@ bool mx4_dequantizable(int64_t rows, int64_t cols, int es) {
 
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream) {
+    // a column without gaps is a row (2^26 x 1 fp32: 132 us column by column)
+    if (transposed && q.rows == 1 && ld == 1) return launch_mx4_quantize(x, dtype, q.cols, false, q, stream);
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
         if (transposed) {
             const ColumnShape s = column_shape_for(q.rows, q.kb());
             hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld,
-                               q, s.c_log, (int)s.row_tiles);
+                               q, s.c_log, (int)s.row_tiles, (((uintptr_t)x | (uint64_t)ld * sizeof(T)) & 127u) != 0);
+        } else if (q.cols <= 16) {
+            const dim3 grid((uint32_t)((q.rows + kNT * kNarrowRows - 1) / (kNT * kNarrowRows)));
+            if (q.cols <= 8) hipLaunchKernelGGL((mx4_quantize_narrow_kernel<DT, 1>), grid, dim3(kNT), 0, stream, (const T*)x, ld, q);
+            else hipLaunchKernelGGL((mx4_quantize_narrow_kernel<DT, 2>), grid, dim3(kNT), 0, stream, (const T*)x, ld, q);
         } else {
             const Shape s = shape_for(q.rows, q.kb() * 4);
             hipLaunchKernelGGL(mx4_quantize_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld, q,

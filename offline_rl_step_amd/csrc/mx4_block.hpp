@@ -62,14 +62,6 @@ IQLH_DEV uint32_t mx4_codes8(const float* x, float inv) {
     return w;
 }
 
-// The value of a code (sign and 0, .5, 1, 1.5, 2, 3, 4, 6): exponent field
-// c >> 1 over one mantissa bit, the subnormal code 1 being 0.5.
-IQLH_DEV float mx4_value(uint32_t code) {
-    const uint32_t c = code & 7u;
-    const uint32_t mag = c < 2u ? (c ? 0x3F000000u : 0u) : ((c >> 1) + 126u) << 23 | (c & 1u) << 22;
-    return __uint_as_float(mag | (code & 8u) << 28);
-}
-
 // Eight neighbouring elements at p, which is aligned to its element only (the
 // hardware takes 16-byte loads at any address), as they lie in memory.
 // count < 8: the rest are 0, and all eight are read where that does not pass
@@ -143,14 +135,6 @@ IQLH_DEV mx_f4 mx4_mma(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) {
     const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// The same with the scales in byte OA of sa and byte OB of sb.
-template <int OA, int OB>
-IQLH_DEV mx_f4 mx4_mma_sel(uint4 a, uint4 b, mx_f4 c, uint32_t sa, uint32_t sb) {
-    const mx_i8 a8 = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    const mx_i8 b8 = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, OA, (int)sa, OB, (int)sb);
 }
 
 // D[i][j] += sum over 64 k of A[i][k] B[j][k], both 32 x 64: lane l holds row

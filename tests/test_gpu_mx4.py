@@ -81,6 +81,30 @@ def test_quantize_both_axes_bit_exact(m, size, dtype, lead, pad):
             assert torch.equal(out, torch.from_numpy(want).to(dev()).to(_t(od))), (axis, od)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [(1, 1), (1023, 1), (1024, 2), (2050, 3), (5001, 7), (3000, 8), (4099, 9), (1500, 15),
+                                  (9000, 16), (70001, 1)])
+def test_quantize_narrow_matrices_along_their_rows(m, size, dtype):
+    """One block a row, with and without a gap between rows, non-finite rows
+    among them; and of one column the column too."""
+    import torch
+    r, c = size
+    x = _float(_wide(r + c, r, c), dtype)
+    x[r // 2, c - 1] = float("nan")
+    x[r // 3, 0] = float("-inf")
+    gap = torch.full((r, c + 3), 7.0, dtype=x.dtype, device=dev())
+    gap[:, 1:c + 1] = x
+    for y, axis in ((x, 1), (gap[:, 1:c + 1], 1)) + (((x, 0), (gap[:, 1:2], 0)) if c == 1 else ()):
+        q = m.mx4_empty(r, c, axis)
+        q.codes.fill_(0xA5)
+        q.scales.fill_(0xA5)
+        m.mx4_quantize(y, q, axis=axis)
+        sync()
+        codes, scales = ref.quantize(_f64(x) if axis else _f64(x).T)
+        assert np.array_equal(q.scales.cpu().numpy(), scales.astype(np.uint8))
+        assert np.array_equal(q.codes.cpu().numpy(), ref.pack(codes))
+
+
 @pytest.mark.parametrize("size", [(140_000, 20), (270_003, 9), (1_100_007, 3), (4_200_005, 1)])
 def test_quantize_narrow_matrices_along_their_columns(m, size):
     """Few columns and many rows, where a wave takes several blocks of one."""
