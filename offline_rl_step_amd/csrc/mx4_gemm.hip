@@ -39,7 +39,7 @@ hipError_t by_dtype(int dtype, F f) {
 // scales come as 4 bytes per row to 16 lanes.  The waves' sums meet in LDS, added in
 // wave order.
 constexpr int kFewWaves = 8;
-constexpr int kFewElements = 32768;  // of a workgroup's part of a float left operand, padded
+constexpr int kFewElements = 16384;  // of a workgroup's part of a float left operand, padded
 template <int XDT, int ODT, int MF>
 __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, const void* x, int64_t ld, Mx4Mat b,
                                                                       Mx4Out o, int n_tiles) {
@@ -94,14 +94,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_rows_kernel(Mx4Mat a, 
             if ((g & 3) == 0) scales[row * kb4 + (g >> 2)] = (uint8_t)s;
         }
     } else {
-        for (int e = threadIdx.x; e < rows * kb4; e += NT) {
-            const int row = e / kb4, k = e - row * kb4;
-            const bool in = k < kb;
-            const int64_t at = (m0 + row) * kb + (in ? k : 0);
-            const uint4 w = ((const uint4*)a.codes)[at];
-            const uint32_t s = a.scales[at], keep = in ? 0xFFFFFFFFu : 0u;
-            *(uint4*)(codes + row * rb + k * 16) = uint4{w.x & keep, w.y & keep, w.z & keep, w.w & keep};
-            scales[e] = (uint8_t)(in ? s : 127u);
+        for (int e0 = threadIdx.x; e0 < rows * kb4; e0 += NT * U) {
+            uint4 w[U];
+            uint32_t s[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + i * NT, row = e / kb4, k = e - row * kb4;
+                const bool in = e < rows * kb4 && k < kb;
+                const int64_t at = in ? (m0 + row) * kb + k : 0;
+                w[i] = ((const uint4*)a.codes)[at];
+                s[i] = in ? a.scales[at] : 127u;
+                const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
+                w[i] = uint4{w[i].x & keep, w[i].y & keep, w[i].z & keep, w[i].w & keep};
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int e = e0 + i * NT, row = e / kb4, k = e - row * kb4;
+                if (e >= rows * kb4) break;
+                *(uint4*)(codes + row * rb + k * 16) = w[i];
+                scales[e] = (uint8_t)s[i];
+            }
         }
     }
     __syncthreads();
@@ -200,80 +212,44 @@ __global__ __launch_bounds__(kNT) void mx4_direct_kernel(Mx4Mat a, Mx4Mat b, Mx4
         }
 }
 
+// ------------------------------------------------ asynchronous copies to LDS
+__device__ __align__(16) const uint4 kZeroChunk[1] = {};
+
+template <int N>
+IQLH_DEV void wait_vm() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// Asynchronous copy of 16 (4) bytes per lane, global -> LDS, to lds_at + 16 (4)
+// lane.  As an instruction of its own and not the compiler's builtin: behind
+// the builtin the compiler waits for every copy in flight before each LDS
+// read that may alias one, which is all of them, and the ring runs empty.  It
+// has no output registers; wait_vm orders it against the reads.  (One wait
+// state between writing M0 and its use by the copy.)
+IQLH_DEV void copy16(const void* src, uint32_t lds_at) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
+}
+IQLH_DEV void copy4(const void* src, uint32_t lds_at) {
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
+}
+// Workgroup barrier after this wave's LDS reads, leaving the asynchronous
+// copies it has in flight
+IQLH_DEV void bar() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ------------------------------------------------------- waves that split k
-// A workgroup takes 16 MF x 16 NF outputs, its eight waves every eighth k step
-// each, the next step's fragments on their way while this one's are
-// multiplied.  The sums meet in LDS: waves 4..7 add to waves 0..3, then those
-// four are added in wave order.  For few outputs, where what counts is how
-// many loads are in flight over the chip.
+// The eight waves' sums of 16 MF x 16 NF outputs, through 4 MF NF KB of LDS: waves
+// 4..7 add to waves 0..3, then those four are added in wave order.
 template <int DT, int MF, int NF>
-__global__ __launch_bounds__(512) void mx4_split_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o, int n_tiles) {
-    extern __shared__ __align__(16) uint8_t lds[];
+IQLH_DEV void add_split_waves(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& o, int64_t m0, int64_t n0, uint8_t* lds,
+                              const mx_f4 (&acc)[MF][NF]) {
     mx_f4(*part)[MF * NF][64] = (mx_f4(*)[MF * NF][64])lds;  // [4]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, blk = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * (16 * MF), n0 = (int64_t)(blockIdx.x % n_tiles) * (16 * NF);
-    const int64_t kb = a.kb();
-    const uint4* ac[MF];
-    const uint8_t* as_[MF];
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-        const RowFrag f(a, m0 + 16 * i + r);
-        ac[i] = f.codes;
-        as_[i] = f.scales;
-    }
-    const uint4* bc[NF];
-    const uint8_t* bs_[NF];
-#pragma unroll
-    for (int j = 0; j < NF; ++j) {
-        const RowFrag f(b, n0 + 16 * j + r);
-        bc[j] = f.codes;
-        bs_[j] = f.scales;
-    }
-    struct Frags {
-        uint4 a[MF], b[NF];
-        uint32_t as[MF], bs[NF];
-    } f[2];
-    auto load = [&](int64_t s, Frags& g) __attribute__((always_inline)) {
-        const int64_t block = s * 4 + blk;
-        const bool in = block < kb;
-        const int64_t at = in ? block : 0;
-        const uint32_t keep = in ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-        for (int j = 0; j < NF; ++j) {
-            g.b[j] = bc[j][at];
-            g.bs[j] = bs_[j][at];
-        }
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const uint4 v = ac[i][at];
-            g.a[i] = uint4{v.x & keep, v.y & keep, v.z & keep, v.w & keep};  // zeros behind the last block
-            g.as[i] = in ? as_[i][at] : 127u;
-        }
-#pragma unroll
-        for (int j = 0; j < NF; ++j) g.bs[j] = in ? g.bs[j] : 127u;
-    };
-    mx_f4 acc[MF][NF];
-#pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
-    auto mma = [&](const Frags& g) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-            for (int j = 0; j < NF; ++j) acc[i][j] = mx4_mma(g.b[j], g.a[i], acc[i][j], g.bs[j], g.as[i]);
-    };
-    const int64_t steps = (kb + 3) / 4;
-    load(wave, f[0]);
-    int64_t s = wave;
-    for (; s + 8 < steps; s += 16) {
-        load(s + 8, f[1]);
-        mma(f[0]);
-        load(s + 16, f[0]);  // zeros behind the last step
-        mma(f[1]);
-    }
-    if (s < steps) mma(f[0]);
     if (wave >= 4) {
 #pragma unroll
         for (int i = 0; i < MF; ++i)
@@ -295,6 +271,105 @@ __global__ __launch_bounds__(512) void mx4_split_kernel(Mx4Mat a, Mx4Mat b, Mx4O
         const int64_t m = m0 + 16 * (e / NF) + r, n = n0 + 16 * (e % NF) + 4 * blk;
         if (m < a.rows) mx4_store4<DT>(o, m, n, b.rows, v);
     }
+}
+
+// A workgroup takes 16 MF x 16 NF outputs, its eight waves every eighth k step
+// each.  For few outputs, where what counts is how many loads are in flight over
+// the chip, and the L1's lookups: straight from memory a fragment of 16 rows is
+// 64 of them per KB, so each wave copies the rows of its step, 64 bytes each, to its
+// own D buffers in LDS, 4 neighbouring lanes a row, 16 lookups per KB.  The scales of all
+// rows lie in LDS before, for up to kSplitSteps steps at a time.  Within a
+// wave's buffer the 16 bytes of block b of row r lie at 64 r + 16 (b ^ (r >> 2 &
+// 3)), so that 16 rows' reads fall on all banks; the scales of step d at dword d ^ (r
+// & 15) of the row's.  (512^3 3.4 us, straight from memory 6.2; 64 x 4096 x 4096 5.5
+// against 12.9; 1024 x 1024 x 4096 10.0 against 21.0.)
+template <int MF, int NF, int D>
+constexpr int kSplitRing = 8 * D * (MF + NF) * 1024;
+constexpr int split_scale_row(int64_t steps) { return (int)((steps + 15) / 16 * 64); }
+// steps whose scales fit beside the buffers, a multiple of 16
+template <int MF, int NF, int D>
+constexpr int kSplitSteps = (160 * 1024 - kSplitRing<MF, NF, D>) / (16 * (MF + NF)) / 64 * 16;
+template <int DT, int MF, int NF, int D>
+__global__ __launch_bounds__(512, 2) void mx4_split_kernel(Mx4Mat a, Mx4Mat b, Mx4Out o, int n_tiles) {
+    constexpr int P = MF + NF;           // copies a step
+    extern __shared__ __align__(16) uint8_t lds[];
+    uint8_t* scales = lds + kSplitRing<MF, NF, D>;  // [16 P rows][split_scale_row], b's rows, then a's
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, blk = lane >> 4;
+    const int64_t m0 = (int64_t)(blockIdx.x / n_tiles) * (16 * MF), n0 = (int64_t)(blockIdx.x % n_tiles) * (16 * NF);
+    const int kb = (int)a.kb(), all = (kb + 3) / 4;
+    const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds + wave * (D * P * 1024);
+    const int cr = lane >> 2, u = (lane & 3) ^ (cr >> 2 & 3);  // row and block a lane copies
+    const uint8_t* src[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const Mx4Mat& q = i < NF ? b : a;
+        const int64_t row = (i < NF ? n0 + 16 * i : m0 + 16 * (i - NF)) + cr;
+        src[i] = q.codes + (row < q.rows ? row : q.rows - 1) * kb * 16 + 16 * u;
+    }
+    auto issue = [&](int s, int buf) __attribute__((always_inline)) {
+        const bool in = 4 * s + u < kb;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            copy16(in ? src[i] + (int64_t)s * 64 : (const uint8_t*)kZeroChunk, ring + (buf * P + i) * 1024);
+    };
+    mx_f4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = mx_f4{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < all; s0 += kSplitSteps<MF, NF, D>) {
+        const int n = all - s0 < kSplitSteps<MF, NF, D> ? all - s0 : kSplitSteps<MF, NF, D>;
+        const int steps = s0 + n, rs = split_scale_row(n);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (s0 + wave + 8 * d < steps) issue(s0 + wave + 8 * d, d);
+#pragma unroll 8
+        for (int e = threadIdx.x; e < 16 * P * n; e += 512) {
+            const int row = e / n, d = e - row * n, block = (s0 + d) * 4;
+            const bool is_b = row < 16 * NF;
+            const Mx4Mat& q = is_b ? b : a;
+            const int64_t at = is_b ? n0 + row : m0 + row - 16 * NF;
+            const uint8_t* p = q.scales + (at < q.rows ? at : q.rows - 1) * kb + block;
+            uint32_t w = 0x7F7F7F7Fu;
+            if (block + 4 <= kb) {
+                typedef uint32_t u1 __attribute__((aligned(1)));
+                w = *(const u1*)p;
+            } else {
+                for (int j = 0; block + j < kb; ++j) w = (w & ~(255u << (8 * j))) | (uint32_t)p[j] << (8 * j);
+            }
+            *(uint32_t*)(scales + row * rs + 4 * (d ^ (row & 15))) = w;
+        }
+        bar();
+        int buf = 0;
+        for (int s = s0 + wave; s < steps; s += 8) {
+            const int behind = (steps - 1 - s) >> 3;  // of the wave's steps
+            if (behind >= D - 1) wait_vm<(D - 1) * P>();
+            else if (D > 3 && behind == 2) wait_vm<2 * P>();
+            else if (D > 2 && behind == 1) wait_vm<P>();
+            else wait_vm<0>();
+            asm volatile("" ::: "memory");
+            const uint8_t* at = lds + (wave * D + buf) * (P * 1024) + r * 64 + 16 * (blk ^ (r >> 2 & 3));
+            uint4 f[P];
+            uint32_t fs[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                f[i] = *(const uint4*)(at + i * 1024);
+                fs[i] = *(const uint32_t*)(scales + (16 * i + r) * rs + 4 * ((s - s0) ^ r)) >> (8 * blk);
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the buffer is read
+            asm volatile("" ::: "memory");
+            if (s + 8 * D < steps) issue(s + 8 * D, buf);
+            buf = buf + 1 < D ? buf + 1 : 0;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j) acc[i][j] = mx4_mma(f[j], f[NF + i], acc[i][j], fs[j], fs[NF + i]);
+        }
+        bar();  // no wave reads its buffers or the scales any more
+    }
+    add_split_waves<DT, MF, NF>(a, b, o, m0, n0, lds, acc);
 }
 
 // ------------------------------------------------------- tiles through LDS
@@ -335,39 +410,11 @@ __global__ __launch_bounds__(kNT) void mx4_scale_groups_kernel(Mx4Mat a, Mx4Mat 
     g[32 + r] = odd;
 }
 
-__device__ __align__(16) const uint4 kZeroChunk[1] = {};
-
 // Workgroups of TILE x TILE outputs, 2 TILE threads
 constexpr int stage_bytes(int tile) { return 2 * tile * 128; }  // codes of both operands, 256 k
 constexpr int buf_bytes(int tile) { return stage_bytes(tile) + 2 * (tile / 32) * 256; }  // and scales; two in LDS
 constexpr int kCodeCopies = 8;   // asynchronous copies a thread issues per step: 2 TILE 128 / 16 / (2 TILE)
 constexpr int kScaleCopies = 2;  // 2 TILE 8 / 4 / (2 TILE)
-
-template <int N>
-IQLH_DEV void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-// Asynchronous copy of 16 (4) bytes per lane, global -> LDS, to lds_at + 16 (4)
-// lane.  As an instruction of its own and not the compiler's builtin: behind
-// the builtin the compiler waits for every copy in flight before each LDS
-// read that may alias one, which is all of them, and the ring runs empty.  It
-// has no output registers; wait_vm orders it against the reads.  (One wait
-// state between writing M0 and its use by the copy.)
-IQLH_DEV void copy16(const void* src, uint32_t lds_at) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
-}
-IQLH_DEV void copy4(const void* src, uint32_t lds_at) {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds_at), "v"(src) : "memory");
-}
-// Workgroup barrier after this wave's LDS reads, leaving the asynchronous
-// copies it has in flight
-IQLH_DEV void bar() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 struct TileArgs {
     Mx4Mat a, b;
@@ -585,7 +632,7 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
 size_t group_bytes(int64_t rows, int64_t kb) { return (size_t)((rows + 31) / 32) * (size_t)((kb + 7) / 8) * 256; }
 
 // Which kernel a product runs on.
-enum class Path { few, direct, split1, split2, split4, tile128, tile256 };
+enum class Path { few, direct, split32x16, split32, split64, tile128, tile256 };
 int64_t tiles_of(int64_t M, int64_t N, int64_t T) { return ((M + T - 1) / T) * ((N + T - 1) / T); }
 Path pick(int64_t M, int64_t N, int64_t K) {
     if (M <= 16 && few_bytes(M, K) <= 80 << 10) return Path::few;  // two workgroups to a compute unit
@@ -593,23 +640,17 @@ Path pick(int64_t M, int64_t N, int64_t K) {
     // 256 tiles for most compute units (2048 x 4096 x 4096, 128 of them: 39.1 us
     // against 30.5 with 128 tiles; 4096^3, 256 of them: 45.0)
     if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
-    // a step or two: the waves that split k have little to split, but eight of
-    // them store a 64 x 64 tile; more tiles than two rounds go to 128 x 128 by four
-    // waves (1000 x 1000 x 128: 5.4 against 6.5 us, 2000 x 2000 x 200 15.9 against 8.2)
-    const int64_t tiles64 = tiles_of(M, N, 64);
-    if (K <= 256) return tiles64 <= 512 ? Path::split4 : Path::direct;
-    // 128 tiles against waves that split k, both as measured up to a round of
-    // tiles: the tiles take 8 us and 2.1 per 1000 k whatever their number, the
-    // splitting waves 3 us and 5 per 10^9 products (as many at K 1024 and below,
-    // where waves go without a step).  768 x 1024 x 4096: 16.3 against 29.5 us;
-    // 512 x 512 x 2048: 11.7 against 8.5; 6281 x 1202 x 454: 13.3 against 32.2
-    const double split_us = 3.0 + 5e-9 * (double)M * (double)N * (double)(K < 1024 ? 1024 : K);
-    if (lds_tiles && split_us > 8.0 + 2.1e-3 * (double)K) return Path::tile128;
-    // the largest of the splitting tiles that gives every compute unit one,
-    // where there are steps for all eight waves
-    if (K <= 512 || tiles64 >= 256) return Path::split4;
-    if (M > 32 && ((M + 63) / 64) * ((N + 31) / 32) >= 256) return Path::split2;
-    return Path::split1;
+    // waves that split k, the smallest outputs a workgroup that a round of workgroups
+    // covers: 32 x 16 (20 x 4096 x 4096: 4.8 us, with 32 x 32 5.2), 32 x 32, two to a
+    // compute unit (512^3: 3.4, with 64 x 64 5.1; 1000^3, two rounds, 7.2 against
+    // 6.0), 64 x 64 (900 x 900 x 3000: 10.5; by 128 tiles 14.9)
+    if ((M + 31) / 32 * ((N + 15) / 16) <= kComputeUnits) return Path::split32x16;
+    if (tiles_of(M, N, 32) <= 2 * kComputeUnits) return Path::split32;
+    if (tiles_of(M, N, 64) <= kComputeUnits) return Path::split64;
+    // more: straight from memory where the sums are short (1500 x 1500 x 256: 8.8
+    // us, 128 tiles 9.0; K 384 8.7 against 10.0, K 512 11.7 against 9.7)
+    if (K <= 384) return Path::direct;
+    return lds_tiles ? Path::tile128 : Path::split64;
 }
 
 template <int TILE>
@@ -629,12 +670,18 @@ hipError_t launch_tiles(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, voi
     });
 }
 
-template <int MF, int NF>
+template <int MF, int NF, int D>
 hipError_t launch_split(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, hipStream_t stream) {
     const int64_t mt = (a.rows + 16 * MF - 1) / (16 * MF), nt = (b.rows + 16 * NF - 1) / (16 * NF);
+    const int64_t steps = (a.kb() + 3) / 4;
+    const int most = kSplitSteps<MF, NF, D>;
+    const int bytes = kSplitRing<MF, NF, D> + 16 * (MF + NF) * split_scale_row(steps < most ? steps : most);
+    static_assert(kSplitRing<MF, NF, D> + 16 * (MF + NF) * split_scale_row(kSplitSteps<MF, NF, D>) <= 160 * 1024 &&
+                      4 * MF * NF * 1024 <= kSplitRing<MF, NF, D>, "LDS of a compute unit");
     return by_dtype(out.dtype, [&](auto dt) {
-        hipLaunchKernelGGL((mx4_split_kernel<decltype(dt)::value, MF, NF>), dim3((uint32_t)(mt * nt)), dim3(512),
-                           4 * MF * NF * 1024, stream, a, b, out, (int)nt);
+        auto kernel = mx4_split_kernel<decltype(dt)::value, MF, NF, D>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(mt * nt)), dim3(512), bytes, stream, a, b, out, (int)nt);
     });
 }
 
@@ -652,23 +699,23 @@ bool mx4_launchable(int64_t M, int64_t N, int64_t K) {
     switch (pick(M, N, K)) {
         case Path::few: return (N + 15) / 16 * 512 < top;
         case Path::direct: return tiles_of(M, N, 128) * kNT < top;
-        case Path::split1: return (M + (M <= 32 ? 31 : 63)) / (M <= 32 ? 32 : 64) * ((N + 15) / 16) < top / 512;
-        case Path::split2: return (M + 63) / 64 * ((N + 31) / 32) < top / 512;
-        case Path::split4: return tiles_of(M, N, 64) < top / 512;
+        case Path::split32x16:
+        case Path::split32: break;
+        case Path::split64: return tiles_of(M, N, 64) < top / 512;
         case Path::tile128:
         case Path::tile256: break;  // bounded by pick; the scales' regrouping by their rows
     }
     return ((M + 31) / 32 + (N + 31) / 32) * kNT < top;
 }
 
-// One launch with the left operand quantised by every workgroup: for up to 16
-// rows, and for more where the workgroups are one round (61 x 26, K 407: 8.5
-// us, in two launches 9.9; two and a half rounds at 33 x 5853, K 385: 12.3 against
-// 10.0)
+// One launch with the left operand quantised by every workgroup, which is its time
+// where its part is large: for up to 16 rows (16 x 1024 x 1024 4.7 us, in two
+// launches 7), and for more where the workgroups are one round (300 x 300, K 100:
+// 5.0; 61 x 26, K 407, 30000 elements a workgroup: 8.3 against 6.4)
 bool mx4_few_ok(int64_t M, int64_t N, int64_t K) {
     const int64_t k4 = (K + 127) / 128 * 128, nt = (N + 15) / 16;
-    if ((M < 64 ? M : 64) * k4 > kFewElements) return false;
-    return M <= 16 || nt * ((M + 63) / 64) <= kComputeUnits;
+    if (M <= 16) return M * k4 <= 2 * kFewElements;
+    return (M < 64 ? M : 64) * k4 <= kFewElements && nt * ((M + 63) / 64) <= kComputeUnits;
 }
 
 hipError_t launch_mx4_few(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,
@@ -685,9 +732,9 @@ hipError_t launch_mx4_matmul(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out
         case Path::few: return launch_few_rows<-1, 1>(a, nullptr, 0, b, out, stream);
         case Path::tile256: return launch_tiles<256>(a, b, out, workspace, stream);
         case Path::tile128: return launch_tiles<128>(a, b, out, workspace, stream);
-        case Path::split4: return launch_split<4, 4>(a, b, out, stream);
-        case Path::split2: return launch_split<4, 2>(a, b, out, stream);
-        case Path::split1: return a.rows <= 32 ? launch_split<2, 1>(a, b, out, stream) : launch_split<4, 1>(a, b, out, stream);
+        case Path::split32x16: return launch_split<2, 1, 4>(a, b, out, stream);
+        case Path::split32: return launch_split<2, 2, 2>(a, b, out, stream);
+        case Path::split64: return launch_split<4, 4, 2>(a, b, out, stream);
         case Path::direct: break;
     }
     const int64_t mt = (a.rows + 127) / 128, nt = (b.rows + 127) / 128;

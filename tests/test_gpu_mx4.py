@@ -194,7 +194,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 32), (2, 3, 33), (1, 512, 256), (1, 4096, 1024), 
             (300, 17, 4100), (1024, 1, 200), (1000, 513, 256), (515, 777, 130), (16, 8, 8192), (40, 40, 6500),
             (1030, 1031, 400), (1500, 1411, 600), (500, 1040, 700), (20, 3000, 2000), (32, 500, 288), (129, 700, 4000),
             (16, 24, 9000), (500, 1040, 900), (1030, 1031, 300),
-            (1700, 1300, 70), (1601, 1333, 256), (2001, 1500, 300), (600, 40, 513)]
+            (1700, 1300, 70), (1601, 1333, 256), (2001, 1500, 300), (600, 40, 513),
+            (40, 40, 50_000), (300, 330, 50_001), (700, 760, 9000), (1000, 1000, 8200), (20, 4000, 400), (513, 500, 600)]
 
 
 @pytest.mark.parametrize("mnk", PRODUCTS)
