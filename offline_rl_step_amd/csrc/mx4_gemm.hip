@@ -413,6 +413,8 @@ __global__ __launch_bounds__(kNT) void mx4_scale_groups_kernel(Mx4Mat a, Mx4Mat 
 // Workgroups of TILE x TILE outputs, 2 TILE threads
 constexpr int stage_bytes(int tile) { return 2 * tile * 128; }  // codes of both operands, 256 k
 constexpr int buf_bytes(int tile) { return stage_bytes(tile) + 2 * (tile / 32) * 256; }  // and scales; two in LDS
+constexpr int kShortSteps = 8;
+constexpr int short_bytes(int tile) { return 2 * stage_bytes(tile) + 2 * tile * 8 * kShortSteps; }
 constexpr int kCodeCopies = 8;   // asynchronous copies a thread issues per step: 2 TILE 128 / 16 / (2 TILE)
 constexpr int kScaleCopies = 2;  // 2 TILE 8 / 4 / (2 TILE)
 
@@ -492,10 +494,13 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[FA][2], uint8_t*
 // instructions of the quarter run.  A row's chunk u (16 bytes) lies at
 // 128 row + 16 (u ^ ((row >> 1) & 7)): 16 lanes of a fragment column fall on
 // all 64 banks.
-template <int DT, int TILE>
+// SHORT: K of at most kShortSteps steps, the scales of all of it in LDS before
+// the first step, [2 TILE rows][kShortSteps] of 8 bytes, step s of row r at s ^ (r >> 2
+// & 7) so that 32 rows' reads fall on all banks; no launch before this one.
+template <int DT, int TILE, bool SHORT>
 __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
     constexpr int NT = 2 * TILE, FA = TILE / 64, WN = TILE / 64;  // threads, row fragments a wave, waves along n
-    constexpr int STAGE = stage_bytes(TILE), BUF = buf_bytes(TILE);
+    constexpr int STAGE = stage_bytes(TILE), BUF = SHORT ? STAGE : buf_bytes(TILE);
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -528,7 +533,7 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
         off[i] = (uint32_t)((row < left ? row : (int)left) * kb * 16) + 16u * u;
     }
     const uint32_t* sbase[kScaleCopies];  // scale groups `wave` of b and of a
-    {
+    if constexpr (!SHORT) {
         const int64_t gb = n0 / 32 + wave, ga = m0 / 32 + wave;
         const int64_t lb = (t.b.rows + 31) / 32 - 1, la = (t.a.rows + 31) / 32 - 1;
         sbase[0] = t.gb + (gb < lb ? gb : lb) * steps * 64 + lane;
@@ -545,9 +550,11 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
             const uint8_t* src = (i < 4 ? bbase : abase) + k0 + off[i];
             copy16(in ? src : (const uint8_t*)kZeroChunk, dst + i * NT * 16 + wave * 1024);
         }
+        if constexpr (!SHORT) {
 #pragma unroll
-        for (int i = 0; i < kScaleCopies; ++i)
-            copy4(sbase[i] + (int64_t)(s < steps ? s : steps - 1) * 64, dst + STAGE + (TILE / 32 * i + wave) * 256);
+            for (int i = 0; i < kScaleCopies; ++i)
+                copy4(sbase[i] + (int64_t)(s < steps ? s : steps - 1) * 64, dst + STAGE + (TILE / 32 * i + wave) * 256);
+        }
     };
     const int wm = wave / WN * (32 * FA), wn = wave % WN * 64;
     struct Frags {
@@ -564,7 +571,21 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
 #pragma unroll
         for (int i = 0; i < FA; ++i) g.a[i] = *(const uint4*)(src + (TILE + wm + 32 * i) * 128 + foff);
     };
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
     auto load_scales = [&](int s, uint32_t (&pa)[FA], uint32_t (&pb)[2]) __attribute__((always_inline)) {
+        if constexpr (SHORT) {
+            const uint8_t* src = lds + 2 * STAGE + r * (8 * kShortSteps) + 8 * ((s < steps ? s : steps - 1) ^ (r >> 2 & 7));
+            const uint32_t sel = h ? 0x07050301u : 0x06040200u;  // the bytes of blocks h, 2 + h, 4 + h, 6 + h
+            auto group = [&](int row) __attribute__((always_inline)) {
+                const u2 w = *(const u2*)(src + row * (8 * kShortSteps));
+                return __builtin_amdgcn_perm(w.y, w.x, sel);
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pb[i] = group(wn + 32 * i);
+#pragma unroll
+            for (int i = 0; i < FA; ++i) pa[i] = group(TILE + wm + 32 * i);
+            return;
+        }
         const uint8_t* src = lds + (s & 1) * BUF + STAGE + lane * 4;
 #pragma unroll
         for (int i = 0; i < 2; ++i) pb[i] = *(const uint32_t*)(src + (wn / 32 + i) * 256);
@@ -589,6 +610,27 @@ __global__ __launch_bounds__(2 * TILE, 2) void mx4_tile_kernel(TileArgs t) {
     typedef std::integral_constant<int, 2> C2;
     typedef std::integral_constant<int, 3> C3;
     issue(0);
+    if constexpr (SHORT) {  // a thread takes a row: b's, then a's
+        const Mx4Mat& q = tid < TILE ? t.b : t.a;
+        const int64_t row = tid < TILE ? n0 + tid : m0 + tid - TILE;
+        const uint8_t* p = q.scales + (row < q.rows ? row : q.rows - 1) * kb;
+        u2 w[kShortSteps];
+#pragma unroll
+        for (int d = 0; d < kShortSteps; ++d) {
+            w[d] = u2{0x7F7F7F7Fu, 0x7F7F7F7Fu};
+            if (8 * d + 8 <= kb) {
+                typedef uint32_t u2u __attribute__((ext_vector_type(2), aligned(1)));
+                w[d] = *(const u2u*)(p + 8 * d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * d + j < kb) w[d][j >> 2] = (w[d][j >> 2] & ~(255u << (8 * (j & 3)))) | (uint32_t)p[8 * d + j] << (8 * (j & 3));
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kShortSteps; ++d)
+            if (d < steps) *(u2*)(lds + 2 * STAGE + tid * (8 * kShortSteps) + 8 * (d ^ (tid >> 2 & 7))) = w[d];
+    }
     wait_vm<0>();
     bar();
     issue(1);
@@ -656,18 +698,23 @@ Path pick(int64_t M, int64_t N, int64_t K) {
 template <int TILE>
 hipError_t launch_tiles(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, void* workspace, hipStream_t stream) {
     TileArgs t{a, b, nullptr, nullptr, out, (int)((a.rows + TILE - 1) / TILE), (int)((b.rows + TILE - 1) / TILE)};
+    auto launch = [&](auto is_short) {
+        constexpr bool SHORT = decltype(is_short)::value;
+        return by_dtype(out.dtype, [&](auto dt) {
+            constexpr int bytes = SHORT ? short_bytes(TILE) : 2 * buf_bytes(TILE);
+            static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+            auto kernel = mx4_tile_kernel<decltype(dt)::value, TILE, SHORT>;
+            (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            hipLaunchKernelGGL(kernel, dim3((uint32_t)(t.m_tiles * t.n_tiles)), dim3(2 * TILE), bytes, stream, t);
+        });
+    };
+    if (a.cols <= kShortSteps * 256) return launch(std::true_type());
     t.ga = (const uint32_t*)workspace;
     t.gb = (const uint32_t*)((const char*)workspace + group_bytes(a.rows, a.kb()));
     const uint32_t ag = (uint32_t)((a.rows + 31) / 32), bg = (uint32_t)((b.rows + 31) / 32);
     hipLaunchKernelGGL(mx4_scale_groups_kernel, dim3(ag + bg, (uint32_t)((a.kb() + 63) / 64)), dim3(kNT), 0, stream, a, b,
                        (uint32_t*)t.ga, (uint32_t*)t.gb, (int)ag);
-    return by_dtype(out.dtype, [&](auto dt) {
-        constexpr int bytes = 2 * buf_bytes(TILE);
-        static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-        auto kernel = mx4_tile_kernel<decltype(dt)::value, TILE>;
-        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)(t.m_tiles * t.n_tiles)), dim3(2 * TILE), bytes, stream, t);
-    });
+    return launch(std::false_type());
 }
 
 template <int MF, int NF, int D>
@@ -690,7 +737,7 @@ hipError_t launch_split(const Mx4Mat& a, const Mx4Mat& b, const Mx4Out& out, hip
 size_t mx4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     const int64_t kb = (K + 31) / 32;
     const Path p = pick(M, N, K);
-    return p == Path::tile256 || p == Path::tile128 ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
+    return K > kShortSteps * 256 && (p == Path::tile256 || p == Path::tile128) ? group_bytes(M, kb) + group_bytes(N, kb) : 16;
 }
 
 // Launches hold less than 2^32 threads
