@@ -606,7 +606,7 @@ int iqlh_mx4_linear(const void* x, int32_t dtype, int64_t ld, int64_t M, const i
  *   h1 = relu(q(s) q(W1)^T + b1), h2 = relu(q(h1) q(W2)^T + b2), V = w3 . h2 + b3.
  * For networks and batches whose full-precision pass costs too much: at
  * random parameters V is off by about 0.2 to 0.3 of its spread over the batch
- * (each 4-bit operand by an eighth of its size).
+ * (each 4-bit operand by about an eighth of its size).
  * The current parameters are quantised in every call.  Arguments as iql_forward_values;
  *   workspace  device, >= iql_forward_values_mx4_workspace_bytes(h, batch),
  *              16-byte aligned, no initial contents required. */

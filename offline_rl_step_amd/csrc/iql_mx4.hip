@@ -3,6 +3,11 @@
 // the value network of iql_forward_values ("GPU IQL + HER Porting Plan",
 // "Rust Integration: gpu_iql_trainer.rs", forward_values) on the 4-bit product.
 //
+// Bound by the 4-bit fragments' way from L2 and the conversions between the layers:
+// S 256, H 512, B 65536 48 us (bf16 pass 66, fp32 754), S 128, H 1024 82 (677); two
+// networks of H 128, S 128, B 16384 15 us, more than their bf16 pass (6.5), for the
+// weights' launch.
+//
 // Up to 1024 states and hidden units: two launches, the weights' quantisation
 // and the whole network (a workgroup takes 64 or 128 rows through both layers, h1 in
 // 4 bits in LDS, V from registers).  Wider: layer by layer on the linear

@@ -23,7 +23,9 @@ constexpr int kQRows = 4;  // rows (times the workgroup's) a thread converts
 // Blocks along x's rows.  HBM-bound.  A thread converts 8 elements (one dword
 // of codes) of kQRows rows, all loaded before the first is used; four
 // neighbouring lanes share a block.  A workgroup is 2^c_log groups of 8 wide
-// and 256 / 2^c_log rows high.
+// and 256 / 2^c_log rows high.  (8192 x 8192 fp32 47 us, 6.4 TB/s, bf16 29, 5.9; 65536 x
+// 777 fp32 35, bf16 27, all from the Infinity Cache; 8192 x 8192 bf16 from HBM 47; a
+// batch of 16384 x 128 fp32 3.2, where the launch counts.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloat<DT>::type* __restrict__ x, int64_t ld,
                                                            Mx4Mat q, int c_log, int col_tiles) {
@@ -161,7 +163,8 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
 }
 
 // HBM-bound on its stores: a thread writes 16 bytes of kQRows rows, so that
-// neighbouring lanes write neighbouring 16 bytes.
+// neighbouring lanes write neighbouring 16 bytes.  (8192 x 8192 to fp32 45 us, 6.7
+// TB/s; stores past the caches: no gain.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_dequantize_kernel(Mx4Mat q, typename MxFloat<DT>::type* __restrict__ out,
                                                              int64_t ld, int c_log, int col_tiles) {
@@ -254,7 +257,7 @@ bool mx4_dequantizable(int64_t rows, int64_t cols, int es) {
 
 hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transposed, const Mx4Mat& q,
                                hipStream_t stream) {
-    // a column without gaps is a row (2^26 x 1 fp32: 132 us column by column)
+    // a column without gaps is a row (2^26 x 1 bf16: 63 us, column by column 116)
     if (transposed && q.rows == 1 && ld == 1) return launch_mx4_quantize(x, dtype, q.cols, false, q, stream);
     return by_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;

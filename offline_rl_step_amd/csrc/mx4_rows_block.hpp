@@ -81,7 +81,7 @@ struct RowsOfB {
 // hold them (1 KB in 16 lookups of the L1, not the 64 of a fragment of 16 rows,
 // and the scale bytes' 64 more), and one dword of scales per lane for four
 // steps, byte s & 3 that of step s.  Rows are padded to a multiple of 128, blocks
-// to whole steps, with zeros of scale 1.
+// to whole steps, with zeros.
 struct FragsOfB {
     const uint4* codes;      // [rows128 / 16][steps][64]
     const uint32_t* scales;  // [rows128 / 16][(steps + 3) / 4][64]
