@@ -401,6 +401,38 @@ def test_non_finite_blocks_reach_their_outputs_only(m):
         assert torch.equal(torch.isnan(y), bad)
 
 
+@pytest.mark.parametrize("mnk", [(12, 90, 700), (20, 40, 100), (60, 300, 100), (17, 300, 500), (300, 500, 1000), (700, 760, 1500),
+                                 (700, 760, 8300), (1500, 1411, 300), (1500, 1411, 600), (1400, 1500, 2100), (4096, 3700, 520),
+                                 (4096, 3700, 2100), (16400, 96, 100), (40, 50, 44_000)])
+def test_non_finite_rows_of_every_kernel(m, mnk):
+    """NaN and infinities in the first, a middle and the last block of rows at
+    tile edges: their outputs and no others are NaN."""
+    import torch
+    M, N, K = mnk
+    gen = torch.Generator(device=dev()).manual_seed(M + N + K)
+    a = torch.randn((M, K), generator=gen, device=dev())
+    b = torch.randn((N, K), generator=gen, device=dev())
+    bad = torch.zeros((M, N), dtype=torch.bool, device=dev())
+    for row, k, v in ((0, K - 1, "nan"), (M // 2, K // 2, "inf"), (M - 1, 0, "-inf")):
+        a[row, k] = float(v)
+        bad[row] = True
+    for row, k, v in ((1, K - 1, "inf"), (N // 2, K // 3, "nan"), (N - 1, K - 1, "nan")):
+        b[row, k] = float(v)
+        bad[:, row] = True
+    aq, bq = m.mx4_empty(M, K), m.mx4_empty(N, K)
+    m.mx4_quantize(a, aq)
+    m.mx4_quantize(b, bq)
+    ws = m.mx4_matmul_workspace(M, N, K)
+    y, z = torch.zeros((M, N), device=dev()), torch.zeros((M, N), device=dev())
+    ws.fill_(0xFF)
+    m.mx4_matmul(aq, bq, y, ws)
+    ws.fill_(0xFF)
+    m.mx4_linear(a, bq, z, ws, relu=True)
+    sync()
+    assert torch.equal(torch.isnan(y), bad) and torch.equal(torch.isnan(z), bad)
+    assert bool(torch.isfinite(y[~bad]).all()) and bool((z[~bad] >= 0).all())
+
+
 def test_products_captured_with_a_shared_workspace(m):
     import torch
     g = np.random.default_rng(0)
