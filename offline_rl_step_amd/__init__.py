@@ -191,6 +191,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_of(stream, device_index):
+    """The same as an address, where CUDA is known to be initialised."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device_index)
+    return _stream(stream).value or 0
+
+
 def last_error():
     return _lib_last_error().decode(errors="replace")
 
@@ -379,11 +386,13 @@ def _need_f32(t, numel, device, what):
 
 
 def _need_current(device):
-    """The library enqueues on the current device."""
+    """The library enqueues on the current device; returns its index."""
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: the kernels read device memory")
-    if device.index != _get_device():  # tensors on it exist, so CUDA is initialised
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{_get_device()}")
+    index = _get_device()  # tensors on it exist, so CUDA is initialised
+    if device.index != index:
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{index}")
+    return index
 
 
 class TensorSet:
@@ -415,25 +424,24 @@ class TensorSet:
                "iqlh_tensor_set_fill")
         # a copy from pageable memory: complete when it returns, for any stream
         self.table = host[:self.struct.table_bytes].to(self.device)
-        self._home = _stream(None).value  # the allocator reuses the table's memory in this stream's order
+        self._home = _stream_of(None, self.device.index)  # the allocator reuses the table's memory in this stream's order
         self.struct.d_table = self.table.data_ptr()
         self.ref = ctypes.byref(self.struct)
+        self.numel, self.count = self.struct.numel, self.struct.count
         self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
 
-    @property
-    def numel(self):
-        return self.struct.numel
-
     def _used_on(self, stream):
-        """Keeps the table's memory from being handed out again, should the set be
+        """`stream`, an address.  Keeps the table's memory from being handed out again, should the set be
         dropped, before a call on another stream has read it."""
-        if stream.value != self._home and not torch.cuda.is_current_stream_capturing():
-            self.table.record_stream(torch.cuda.ExternalStream(stream.value or 0, device=self.device))
+        if stream != self._home and not torch.cuda.is_current_stream_capturing():
+            self.table.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
         return stream
 
     def overlaps(self, t):
         """Whether t (contiguous) shares memory with a tensor of the set."""
-        lo, hi = t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+        return self._overlaps_range(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+
+    def _overlaps_range(self, lo, hi):
         if self.struct.overlap:  # ranges are not disjoint: look at each
             return any(a < hi and lo < b for a, b in self._ranges)
         i = bisect.bisect_left(self._ranges, (hi,))
@@ -460,28 +468,29 @@ def grad_norm(tensor_set, out_norm, workspace, kind=NORM_L2, out_each=None, flag
     """Norm over all tensors of the set into out_norm [1], with out_each
     [count] each tensor's own too."""
     s = tensor_set
-    _need_current(s.device)
+    index = _need_current(s.device)
     _need_f32(out_norm, 1, s.device, "out_norm")
     if out_each is not None:
-        _need_f32(out_each, s.struct.count, s.device, "out_each")
+        _need_f32(out_each, s.count, s.device, "out_each")
     _need_aux(s.device, workspace, flags)
     _check(_lib_grad_norm(s.ref, kind, out_norm.data_ptr(), _ptr(out_each), _ptr(flags), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), s._used_on(_stream(stream))), "iqlh_grad_norm")
+                          workspace.nbytes, s._used_on(_stream_of(stream, index))), "iqlh_grad_norm")
 
 
 def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None, flags=None, stream=None):
     """Clips the set to max_norm: in place, or into the flat float32 vector
     out_flat [numel] with the tensors unchanged.  out [2]: norm and factor."""
     s = tensor_set
-    _need_current(s.device)
+    index = _need_current(s.device)
     _need_f32(out, 2, s.device, "out")
+    flat = None
     if out_flat is not None:
         _need_f32(out_flat, s.numel, s.device, "out_flat")
-        _need(not s.overlaps(out_flat[:s.numel]), "out_flat shares memory with a tensor of the set")
+        flat = out_flat.data_ptr()
+        _need(not s._overlaps_range(flat, flat + 4 * s.numel), "out_flat shares memory with a tensor of the set")
     _need_aux(s.device, workspace, flags)
-    _check(_lib_grad_clip(s.ref, kind, max_norm, _ptr(out_flat), out.data_ptr(), _ptr(flags), workspace.data_ptr(),
-                          workspace.numel() * workspace.element_size(), s._used_on(_stream(stream))),
-           "iqlh_grad_clip")
+    _check(_lib_grad_clip(s.ref, kind, max_norm, flat, out.data_ptr(), _ptr(flags), workspace.data_ptr(),
+                          workspace.nbytes, s._used_on(_stream_of(stream, index))), "iqlh_grad_clip")
 
 
 # --------------------------------------------- microscaled 4-bit matrices
@@ -530,18 +539,17 @@ def mx4_quantize(x, out, axis=1, stream=None):
     (axis=0) into the Mx4 `out`, which must not share memory with it."""
     if axis not in (0, 1):
         raise ValueError("axis must be 0 or 1")
-    _need_current(out.device)
+    index = _need_current(out.device)
     r, c = (out.rows, out.cols) if axis == 1 else (out.cols, out.rows)
     dt, ld = _matrix(x, r, c, out.device, "x")
-    _check(_lib_mx4_quantize(x.data_ptr(), dt, ld, 1 - axis, out.ref, _stream(stream)),
-           "iqlh_mx4_quantize")
+    _check(_lib_mx4_quantize(x.data_ptr(), dt, ld, 1 - axis, out.ref, _stream_of(stream, index)), "iqlh_mx4_quantize")
 
 
 def mx4_dequantize(q, out, stream=None):
     """Values of q into out [rows, cols] (float32, bfloat16, float16)."""
-    _need_current(q.device)
+    index = _need_current(q.device)
     dt, ld = _matrix(out, q.rows, q.cols, q.device, "out")
-    _check(_lib_mx4_dequantize(q.ref, out.data_ptr(), dt, ld, _stream(stream)), "iqlh_mx4_dequantize")
+    _check(_lib_mx4_dequantize(q.ref, out.data_ptr(), dt, ld, _stream_of(stream, index)), "iqlh_mx4_dequantize")
 
 
 def mx4_matmul_workspace(m, n, k, device=None):
@@ -553,11 +561,11 @@ def mx4_matmul_workspace(m, n, k, device=None):
 
 
 def _need_product(rows, b, out, workspace, bias):
-    _need_current(b.device)
+    index = _need_current(b.device)
     _need_aux(b.device, workspace, None)
     if bias is not None:
         _need_f32(bias, b.rows, b.device, "bias")
-    return _matrix(out, rows, b.rows, b.device, "out")
+    return *_matrix(out, rows, b.rows, b.device, "out"), index
 
 
 def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
@@ -565,19 +573,19 @@ def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
     share memory with an operand."""
     if a.device != b.device:
         raise ValueError(f"a is on {a.device}, b on {b.device}")
-    dt, ld = _need_product(a.rows, b, out, workspace, bias)
-    _check(_lib_mx4_matmul(a.ref, b.ref, _ptr(bias), int(relu), out.data_ptr(), dt, ld, workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), _stream(stream)),
-           "iqlh_mx4_matmul")
+    dt, ld, index = _need_product(a.rows, b, out, workspace, bias)
+    _check(_lib_mx4_matmul(a.ref, b.ref, None if bias is None else bias.data_ptr(), int(relu), out.data_ptr(), dt, ld,
+                           workspace.data_ptr(), workspace.nbytes, _stream_of(stream, index)), "iqlh_mx4_matmul")
 
 
 def mx4_linear(x, b, out, workspace, bias=None, relu=False, stream=None):
     """mx4_matmul with a = x [m, k] (float32, bfloat16, float16) quantised on the way."""
-    dt, ld = _need_product(x.shape[0], b, out, workspace, bias)
-    xdt, xld = _matrix(x, x.shape[0], b.cols, b.device, "x")
-    _check(_lib_mx4_linear(x.data_ptr(), xdt, xld, x.shape[0], b.ref, _ptr(bias), int(relu), out.data_ptr(), dt, ld,
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)),
-           "iqlh_mx4_linear")
+    rows = x.shape[0]
+    dt, ld, index = _need_product(rows, b, out, workspace, bias)
+    xdt, xld = _matrix(x, rows, b.cols, b.device, "x")
+    _check(_lib_mx4_linear(x.data_ptr(), xdt, xld, rows, b.ref, None if bias is None else bias.data_ptr(), int(relu),
+                           out.data_ptr(), dt, ld, workspace.data_ptr(), workspace.nbytes,
+                           _stream_of(stream, index)), "iqlh_mx4_linear")
 
 
 def iql_forward_values_mx4_workspace(h, batch):
