@@ -102,14 +102,14 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_narrow_kernel(const typename
 
 // Blocks along x's columns: x is [q.cols][ld].  HBM-bound.  A lane takes one
 // column of x, 32 rows a block, neighbouring lanes neighbouring addresses; a
-// workgroup 2^c_log columns (64, fewer of a narrow x) and 8 blocks per wave's
-// worth of them.  The codes pass through LDS so that a row of q is written 128 bytes
+// workgroup 2^c_log columns (64, fewer of a narrow x) and 4 HALVES blocks per
+// wave's worth of them.  The codes pass through LDS so that a row of q is written 64 bytes
 // or more at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two 16-bit columns per
 // lane by dword loads 27.5, and 12.3 against 5.2 us at 5001 x 777, where they
 // leave half of the compute units without a workgroup.  Runs of tiles per XCD:
 // 65536 x 777 fp32 52 -> 34 us, bf16 38 -> 21.5; rows on cache lines lose by them,
 // 4096 x 16384 fp32 49 -> 53.)
-template <int DT>
+template <int DT, int HALVES>
 __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typename MxFloat<DT>::type* __restrict__ x,
                                                                    int64_t ld, Mx4Mat q, int c_log, int row_tiles,
                                                                    int shared_lines) {
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
     __shared__ uint8_t scales[576];
     const int64_t kb = q.kb();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int columns = 1 << c_log, b_log = 9 - c_log, blocks = 1 << b_log;
+    const int columns = 1 << c_log, b_log = 7 + HALVES - c_log, blocks = 1 << b_log;
     const int c = lane & (columns - 1);
     // rows of x that do not start on cache lines: neighbouring tiles share the lines at
     // their border, so each XCD (every eighth workgroup) gets a run of tiles
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
     const int64_t r0 = (int64_t)(id % row_tiles) * columns, b0 = (int64_t)(id / row_tiles) << b_log;
     const int64_t r = r0 + c < q.rows ? r0 + c : q.rows - 1;  // lanes past the end: not written below
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < HALVES; ++half) {
         const int i = ((wave + 4 * half) << (6 - c_log)) + (lane >> c_log);
         const int64_t k0 = (b0 + i) * 32;
         if (b0 + i < kb) {
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 512; e += kNT) {
+    for (int e = threadIdx.x; e < HALVES * kNT; e += kNT) {
         const int rr = e >> b_log, i = e & (blocks - 1);
         if (r0 + rr < q.rows && b0 + i < kb) {
             ((uint4*)q.codes)[(r0 + rr) * kb + b0 + i] = codes[rr * (blocks + 1) + i];
@@ -231,15 +231,21 @@ Shape shape_for(int64_t rows, int64_t across) {
 // no more columns than x has, as long as there is a workgroup for every
 // compute unit (2^22 rows of 1: 10.5 us, of 64 82; 2^14: 9.4 against 4.0)
 struct ColumnShape {
-    int c_log;
+    int c_log, halves;
     int64_t row_tiles, blocks;
 };
-ColumnShape column_shape_for(int64_t rows, int64_t kb) {
+ColumnShape column_shape_for(int64_t rows, int64_t kb, int es, bool on_lines) {
     ColumnShape s;
     s.c_log = 0;
     while (s.c_log < 6 && ((int64_t)1 << s.c_log < rows || kb >> (9 - s.c_log) < 256)) ++s.c_log;
     s.row_tiles = (rows + (1 << s.c_log) - 1) >> s.c_log;
-    s.blocks = s.row_tiles * ((kb + (1 << (9 - s.c_log)) - 1) >> (9 - s.c_log));
+    // one block a lane, two of wide binary32 rows on cache lines (5001 x 777 fp16: 4.5
+    // against 5.5 us, 8192 x 8192 bf16 26.8 against 27.8; fp32 57.0 against 52.5, and 262144 x
+    // 200 fp32, whose rows end inside a line, 33.8 against 37.0)
+    const int64_t two = s.row_tiles * ((kb + (1 << (9 - s.c_log)) - 1) >> (9 - s.c_log));
+    s.halves = on_lines && es == 4 && two >= 2048 ? 2 : 1;
+    const int b_log = 7 + s.halves - s.c_log;
+    s.blocks = s.row_tiles * ((kb + (1 << b_log) - 1) >> b_log);
     return s;
 }
 
@@ -249,7 +255,7 @@ int64_t dequantize_across(int64_t cols, int es) { return (cols * es + 15) / 16; 
 
 bool mx4_quantizable(int64_t rows, int64_t cols, bool transposed) {
     const int64_t kb = (cols + 31) / 32;
-    return (transposed ? column_shape_for(rows, kb).blocks : shape_for(rows, kb * 4).blocks) <= kMostBlocks;
+    return (transposed ? column_shape_for(rows, kb, 2, false).blocks : shape_for(rows, kb * 4).blocks) <= kMostBlocks;
 }
 bool mx4_dequantizable(int64_t rows, int64_t cols, int es) {
     return shape_for(rows, dequantize_across(cols, es)).blocks <= kMostBlocks;
@@ -263,9 +269,15 @@ hipError_t launch_mx4_quantize(const void* x, int dtype, int64_t ld, bool transp
         constexpr int DT = decltype(dt)::value;
         typedef typename MxFloat<DT>::type T;
         if (transposed) {
-            const ColumnShape s = column_shape_for(q.rows, q.kb());
-            hipLaunchKernelGGL(mx4_quantize_columns_kernel<DT>, dim3((uint32_t)s.blocks), dim3(kNT), 0, stream, (const T*)x, ld,
-                               q, s.c_log, (int)s.row_tiles, (((uintptr_t)x | (uint64_t)ld * sizeof(T)) & 127u) != 0);
+            const int shared_lines = (((uintptr_t)x | (uint64_t)ld * sizeof(T)) & 127u) != 0;
+            const ColumnShape s = column_shape_for(q.rows, q.kb(), sizeof(T), !shared_lines);
+            const dim3 grid((uint32_t)s.blocks);
+            if (s.halves == 1)
+                hipLaunchKernelGGL((mx4_quantize_columns_kernel<DT, 1>), grid, dim3(kNT), 0, stream, (const T*)x, ld, q, s.c_log,
+                                   (int)s.row_tiles, shared_lines);
+            else
+                hipLaunchKernelGGL((mx4_quantize_columns_kernel<DT, 2>), grid, dim3(kNT), 0, stream, (const T*)x, ld, q, s.c_log,
+                                   (int)s.row_tiles, shared_lines);
         } else if (q.cols <= 16) {
             const dim3 grid((uint32_t)((q.rows + kNT * kNarrowRows - 1) / (kNT * kNarrowRows)));
             if (q.cols <= 8) hipLaunchKernelGGL((mx4_quantize_narrow_kernel<DT, 1>), grid, dim3(kNT), 0, stream, (const T*)x, ld, q);
