@@ -198,6 +198,12 @@ def _stream_of(stream, device_index):
     return _stream(stream).value or 0
 
 
+def _stream_object(stream, device):
+    """torch's stream of an address.  ExternalStream takes 0, the default
+    stream's, for none given and returns a stream of torch's pool."""
+    return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
 def last_error():
     return _lib_last_error().decode(errors="replace")
 
@@ -434,7 +440,7 @@ class TensorSet:
         """`stream`, an address.  Keeps the table's memory from being handed out again, should the set be
         dropped, before a call on another stream has read it."""
         if stream != self._home and not torch.cuda.is_current_stream_capturing():
-            self.table.record_stream(torch.cuda.ExternalStream(stream, device=self.device))
+            self.table.record_stream(_stream_object(stream, self.device))
         return stream
 
     def overlaps(self, t):
