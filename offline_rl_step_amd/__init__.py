@@ -191,17 +191,31 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _stream_of(stream, device_index):
-    """The same as an address, where CUDA is known to be initialised."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device_index)
-    return _stream(stream).value or 0
-
-
 def _stream_object(stream, device):
     """torch's stream of an address.  ExternalStream takes 0, the default
     stream's, for none given and returns a stream of torch's pool."""
     return torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+
+
+def _stream_of(stream, device_index, *tensors):
+    """The call's stream as an address, where CUDA is known to be initialised.
+    torch's allocator knows of the current stream only: for another one the
+    memory of the call's tensors (or None) is kept until the call has run, should
+    they be dropped before.  (Tensors of a captured call have to outlive the
+    graph anyway.)"""
+    if _raw_stream is not None:
+        current = _raw_stream(device_index)
+    else:
+        current = torch.cuda.current_stream().cuda_stream
+    if stream is None:
+        return current
+    address = _stream(stream).value or 0
+    if address != current and not torch.cuda.is_current_stream_capturing():
+        other = _stream_object(address, device_index)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
+    return address
 
 
 def last_error():
@@ -430,17 +444,21 @@ class TensorSet:
                "iqlh_tensor_set_fill")
         # a copy from pageable memory: complete when it returns, for any stream
         self.table = host[:self.struct.table_bytes].to(self.device)
-        self._home = _stream_of(None, self.device.index)  # the allocator reuses the table's memory in this stream's order
+        # the allocator reuses the table's memory in this stream's order
+        self._streams = {_stream_of(None, self.device.index)}
         self.struct.d_table = self.table.data_ptr()
         self.ref = ctypes.byref(self.struct)
         self.numel, self.count = self.struct.numel, self.struct.count
         self._ranges = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel())
 
     def _used_on(self, stream):
-        """`stream`, an address.  Keeps the table's memory from being handed out again, should the set be
-        dropped, before a call on another stream has read it."""
-        if stream != self._home and not torch.cuda.is_current_stream_capturing():
-            self.table.record_stream(_stream_object(stream, self.device))
+        """`stream`, an address.  Keeps the memory of the table and the tensors from being handed out
+        again, should the set be dropped, before the calls on another stream have read it."""
+        if stream not in self._streams and not torch.cuda.is_current_stream_capturing():
+            other = _stream_object(stream, self.device)
+            for t in (self.table, *self.tensors):
+                t.record_stream(other)
+            self._streams.add(stream)  # good until the memory is freed
         return stream
 
     def overlaps(self, t):
@@ -480,7 +498,8 @@ def grad_norm(tensor_set, out_norm, workspace, kind=NORM_L2, out_each=None, flag
         _need_f32(out_each, s.count, s.device, "out_each")
     _need_aux(s.device, workspace, flags)
     _check(_lib_grad_norm(s.ref, kind, out_norm.data_ptr(), _ptr(out_each), _ptr(flags), workspace.data_ptr(),
-                          workspace.nbytes, s._used_on(_stream_of(stream, index))), "iqlh_grad_norm")
+                          workspace.nbytes, s._used_on(_stream_of(stream, index, out_norm, out_each, flags, workspace))),
+           "iqlh_grad_norm")
 
 
 def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None, flags=None, stream=None):
@@ -496,7 +515,8 @@ def grad_clip(tensor_set, max_norm, out, workspace, kind=NORM_L2, out_flat=None,
         _need(not s._overlaps_range(flat, flat + 4 * s.numel), "out_flat shares memory with a tensor of the set")
     _need_aux(s.device, workspace, flags)
     _check(_lib_grad_clip(s.ref, kind, max_norm, flat, out.data_ptr(), _ptr(flags), workspace.data_ptr(),
-                          workspace.nbytes, s._used_on(_stream_of(stream, index))), "iqlh_grad_clip")
+                          workspace.nbytes, s._used_on(_stream_of(stream, index, out, out_flat, flags, workspace))),
+           "iqlh_grad_clip")
 
 
 # --------------------------------------------- microscaled 4-bit matrices
@@ -548,14 +568,16 @@ def mx4_quantize(x, out, axis=1, stream=None):
     index = _need_current(out.device)
     r, c = (out.rows, out.cols) if axis == 1 else (out.cols, out.rows)
     dt, ld = _matrix(x, r, c, out.device, "x")
-    _check(_lib_mx4_quantize(x.data_ptr(), dt, ld, 1 - axis, out.ref, _stream_of(stream, index)), "iqlh_mx4_quantize")
+    _check(_lib_mx4_quantize(x.data_ptr(), dt, ld, 1 - axis, out.ref,
+                             _stream_of(stream, index, x, out.codes, out.scales)), "iqlh_mx4_quantize")
 
 
 def mx4_dequantize(q, out, stream=None):
     """Values of q into out [rows, cols] (float32, bfloat16, float16)."""
     index = _need_current(q.device)
     dt, ld = _matrix(out, q.rows, q.cols, q.device, "out")
-    _check(_lib_mx4_dequantize(q.ref, out.data_ptr(), dt, ld, _stream_of(stream, index)), "iqlh_mx4_dequantize")
+    _check(_lib_mx4_dequantize(q.ref, out.data_ptr(), dt, ld, _stream_of(stream, index, q.codes, q.scales, out)),
+           "iqlh_mx4_dequantize")
 
 
 def mx4_matmul_workspace(m, n, k, device=None):
@@ -581,7 +603,9 @@ def mx4_matmul(a, b, out, workspace, bias=None, relu=False, stream=None):
         raise ValueError(f"a is on {a.device}, b on {b.device}")
     dt, ld, index = _need_product(a.rows, b, out, workspace, bias)
     _check(_lib_mx4_matmul(a.ref, b.ref, None if bias is None else bias.data_ptr(), int(relu), out.data_ptr(), dt, ld,
-                           workspace.data_ptr(), workspace.nbytes, _stream_of(stream, index)), "iqlh_mx4_matmul")
+                           workspace.data_ptr(), workspace.nbytes,
+                           _stream_of(stream, index, a.codes, a.scales, b.codes, b.scales, bias, out, workspace)),
+           "iqlh_mx4_matmul")
 
 
 def mx4_linear(x, b, out, workspace, bias=None, relu=False, stream=None):
@@ -591,7 +615,7 @@ def mx4_linear(x, b, out, workspace, bias=None, relu=False, stream=None):
     xdt, xld = _matrix(x, rows, b.cols, b.device, "x")
     _check(_lib_mx4_linear(x.data_ptr(), xdt, xld, rows, b.ref, None if bias is None else bias.data_ptr(), int(relu),
                            out.data_ptr(), dt, ld, workspace.data_ptr(), workspace.nbytes,
-                           _stream_of(stream, index)), "iqlh_mx4_linear")
+                           _stream_of(stream, index, x, b.codes, b.scales, bias, out, workspace)), "iqlh_mx4_linear")
 
 
 def iql_forward_values_mx4_workspace(h, batch):
@@ -607,7 +631,9 @@ def iql_forward_values_mx4(h, next_states, batch, out_v, workspace, rewards=None
     ld = states_ld if states_ld is not None else next_states.stride(0)
     _check(_lib_forward_mx4(h, _ptr(next_states), _DTYPES[next_states.dtype], ld, batch, _ptr(out_v), _ptr(rewards),
                             _ptr(dones), gamma, _ptr(out_target), _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream(stream)), "iql_forward_values_mx4")
+                            workspace.numel() * workspace.element_size(),
+                            _stream_of(stream, _get_device(), next_states, out_v, workspace, rewards, dones, out_target)),
+           "iql_forward_values_mx4")
 
 
 # ------------------------------------------------------------------- HER

@@ -36,7 +36,7 @@ def streams(m, monkeypatch):
 def _set(m, home):
     import torch
     s = object.__new__(m.TensorSet)
-    s.table, s.device, s._home = Recorded(), torch.device("cuda", 0), home
+    s.table, s.device, s._streams, s.tensors = Recorded(), torch.device("cuda", 0), {home}, []
     return s
 
 
@@ -52,3 +52,64 @@ def test_a_sets_table_needs_nothing_on_its_own_stream(m, streams):
         s = _set(m, home)
         s._used_on(home)
         assert s.table.streams == []
+
+
+@pytest.fixture
+def calls(m, streams, monkeypatch):
+    """The library's calls succeed without doing anything, tensors in host memory
+    pass for device memory, HOME is the current stream; the log of
+    record_stream, (address of the tensor's memory, stream)."""
+    import torch
+    log = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: log.append((self.data_ptr(), s)), raising=False)
+    monkeypatch.setattr(m, "_need_current", lambda device: 0)
+    monkeypatch.setattr(m, "_get_device", lambda: 0)
+    monkeypatch.setattr(m, "_raw_stream", lambda index: HOME)
+    for name in ("grad_norm", "grad_clip", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "forward_mx4"):
+        monkeypatch.setattr(m, f"_lib_{name}", lambda *args: m.OK)
+    return log
+
+
+def _jobs(m):
+    """(call, the tensors whose memory it touches)"""
+    import torch
+    f = lambda *shape: torch.zeros(shape)  # noqa: E731
+    u = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    grads = [f(40), f(3)]
+    s = m.TensorSet(grads)
+    norm, each, flags, ws, out, flat = f(1), f(2), torch.zeros(1, dtype=torch.int32), u(1 << 16), f(2), f(43)
+    a, b = (m.Mx4(u(64).view(4, 16), u(4).view(4, 1), 4, 32) for _ in range(2))
+    x, y, bias, work = f(4, 32), f(4, 4), f(4), u(64)
+    values, target, rewards, dones = f(4), f(4), f(4), f(4)
+    qa, qb = [a.codes, a.scales], [b.codes, b.scales]
+    kept = [s.table, *grads]
+    return {
+        "grad_norm": (lambda st: m.grad_norm(s, norm, ws, out_each=each, flags=flags, stream=st),
+                      kept + [norm, each, flags, ws]),
+        "grad_clip": (lambda st: m.grad_clip(s, 1.0, out, ws, out_flat=flat, flags=flags, stream=st),
+                      kept + [out, flat, flags, ws]),
+        "mx4_quantize": (lambda st: m.mx4_quantize(x, a, stream=st), [x] + qa),
+        "mx4_dequantize": (lambda st: m.mx4_dequantize(a, x, stream=st), [x] + qa),
+        "mx4_matmul": (lambda st: m.mx4_matmul(a, b, y, work, bias=bias, stream=st), qa + qb + [y, work, bias]),
+        "mx4_linear": (lambda st: m.mx4_linear(x, b, y, work, bias=bias, stream=st), qb + [x, y, work, bias]),
+        "forward_values_mx4": (lambda st: m.iql_forward_values_mx4(None, x, 4, values, work, rewards, dones, 0.9, target,
+                                                                   stream=st), [x, values, work, rewards, dones, target]),
+    }
+
+
+JOBS = ["grad_norm", "grad_clip", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_linear", "forward_values_mx4"]
+
+
+@pytest.mark.parametrize("name", JOBS)
+def test_a_calls_tensors_are_kept_for_the_stream_it_names(m, calls, name):
+    call, tensors = _jobs(m)[name]
+    call(SIDE)
+    assert sorted(calls) == sorted((t.data_ptr(), ("external", SIDE)) for t in tensors)
+
+
+@pytest.mark.parametrize("name", JOBS)
+def test_calls_on_the_current_stream_record_nothing(m, calls, name):
+    call, _ = _jobs(m)[name]
+    call(None)
+    call(HOME)
+    assert calls == []
