@@ -473,11 +473,14 @@ class TensorSet:
 
 
 def grad_norm_workspace(tensor_set):
-    """A workspace for grad_norm / grad_clip calls on the set (its counter at 0)."""
+    """A workspace for grad_norm / grad_clip calls on the set, on any stream (its counter is at 0 when this returns)."""
     out = ctypes.c_size_t()
     _check(_lib_norm_ws(ctypes.byref(tensor_set.struct), ctypes.byref(out)), "iqlh_grad_norm_workspace_bytes")
     ws = torch.empty(out.value, dtype=torch.uint8, device=tensor_set.device)
-    ws[:64].zero_()
+    if torch.cuda.is_current_stream_capturing():
+        ws[:64].zero_()  # recorded in front of the graph's calls
+    else:
+        ws[:64].copy_(torch.zeros(64, dtype=torch.uint8))  # from pageable memory: complete when it returns, for any stream
     return ws
 
 

@@ -113,3 +113,21 @@ def test_calls_on_the_current_stream_record_nothing(m, calls, name):
     call(None)
     call(HOME)
     assert calls == []
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_a_workspaces_counter_is_zero_for_any_stream(m, calls, monkeypatch, capturing):
+    """When grad_norm_workspace returns, the counter is 0 whatever fills the
+    current stream still has to run (here: none has run).  Into a captured graph
+    the fill is recorded."""
+    import torch
+    s = m.TensorSet([torch.zeros(5)])
+    empty, fills = torch.empty, []
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **k).fill_(0xA5))
+    monkeypatch.setattr(torch.Tensor, "zero_", lambda self: fills.append(self.numel()) or self)
+    ws = m.grad_norm_workspace(s)
+    if capturing:
+        assert fills == [64]
+    else:
+        assert ws[:64].tolist() == [0] * 64

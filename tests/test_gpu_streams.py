@@ -1,0 +1,53 @@
+"""Tensor lists and 4-bit matrices on streams other than the one that their
+tensors come from: nothing here waits for the device between a call's
+preparation and the call unless its documentation asks for it."""
+import numpy as np
+import pytest
+
+from oracle import tensors as ref
+from tests.gpu_util import dev, sync
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def m():
+    import offline_rl_step_amd as m
+    return m
+
+
+def _grads(seed, lens):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(n, generator=g).to(dev()) for n in lens]
+
+
+def _host(ts):
+    return [t.double().cpu().numpy() for t in ts]
+
+
+def test_a_new_workspace_serves_another_stream_at_once(m):
+    """The workspace's counter is in place when grad_norm_workspace returns,
+    with other work queued on the stream that made it and non-zero bytes where
+    the workspace comes to lie."""
+    import torch
+    ts = _grads(1, [30_000, 77])
+    want = ref.norm(_host(ts), 0)
+    s = m.TensorSet(ts)
+    out = torch.full((8,), -7.0, device=dev())
+    busy = torch.empty(1 << 28, device=dev())
+    side = torch.cuda.Stream()
+    size = m.grad_norm_workspace(s).numel()
+    sync()
+    for rep in range(8):
+        used = torch.full((size,), 0xFF, dtype=torch.uint8, device=dev())
+        del used
+        busy.fill_(float(rep))
+        ws = m.grad_norm_workspace(s)
+        m.grad_norm(s, out[rep:rep + 1], ws, stream=side)
+        del ws
+    sync()
+    for x in out.tolist():
+        assert abs(x - want) <= (U32 * 1.0001 + 30_077 * 2.0 ** -53) * want
