@@ -288,26 +288,70 @@ __global__ __launch_bounds__(kNT) void grad_norm_finish_kernel(TensorSetArgs a, 
     if (threadIdx.x == 0) out_each[t] = (float)n;
 }
 
+// Products of a clip in place are rounded once.  To binary16 the multiplication
+// and the conversion are one instruction, which does so.  To bfloat16 the product
+// passes through binary32, and where that puts it onto the middle of two values
+// the conversion would go to the even one: such a round of products is taken again
+// from the exact ones (32 bits, exact in binary64), rounded to odd, that is cut off
+// with the last bit set, so that the conversion sees the side they lie on.
+// (537 MB of bf16, norm and clip: 290 us, without this 285.)
+// 0 for a binary32 value in the middle of two bfloat16:
+IQLH_DEV uint32_t off_middle(float f) { return (__float_as_uint(f) << 16) + 0x80000000u; }
+IQLH_DEV float product_to_odd(float x, float c) {
+    const double p = (double)x * (double)c;
+    const float f = (float)p;
+    const double d = (double)f;
+    const uint32_t b = __float_as_uint(f);
+    const uint32_t outward = fabs(d) < fabs(p) ? 1u : 0xFFFFFFFFu;
+    return __uint_as_float(d != p && !(b & 1u) ? b + outward : b);  // an even f: its neighbour on p's side
+}
+
 // Elements [0, n) of q times c in place, whole 16-byte quads, kAhead loads in
 // flight per thread.
 template <int DT>
 IQLH_DEV void scale_quads(uint4* q, int nq, float c) {
     typedef Elem<DT> E;
-    auto scaled = [c](uint4 x) __attribute__((always_inline)) {
+    uint32_t nearest = 1u;  // 0: a product of this round lies in the middle
+    auto scaled = [&](uint4 x) __attribute__((always_inline)) {
         float v[E::kQ];
 #pragma unroll
-        for (int j = 0; j < E::kQ; ++j) v[j] = E::get(x, j) * c;
+        for (int j = 0; j < E::kQ; ++j) {
+            v[j] = E::get(x, j) * c;
+            if constexpr (DT == IQLH_BF16) {
+                const uint32_t o = off_middle(v[j]);
+                nearest = o < nearest ? o : nearest;
+            }
+        }
+        return E::pack(v);
+    };
+    auto exactly = [&](uint4 x) __attribute__((always_inline)) {
+        float v[E::kQ];
+#pragma unroll
+        for (int j = 0; j < E::kQ; ++j) v[j] = product_to_odd(E::get(x, j), c);
         return E::pack(v);
     };
     int i = threadIdx.x;
     for (; i + (kAhead - 1) * kNT < nq; i += kAhead * kNT) {
-        uint4 x[kAhead];
+        uint4 x[kAhead], y[kAhead];
+        nearest = 1u;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) x[k] = q[i + k * kNT];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) q[i + k * kNT] = scaled(x[k]);
+        for (int k = 0; k < kAhead; ++k) y[k] = scaled(x[k]);
+        if (DT == IQLH_BF16 && !nearest) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) y[k] = exactly(x[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) q[i + k * kNT] = y[k];
     }
-    for (; i < nq; i += kNT) q[i] = scaled(q[i]);
+    for (; i < nq; i += kNT) {
+        const uint4 x = q[i];
+        nearest = 1u;
+        uint4 y = scaled(x);
+        if (DT == IQLH_BF16 && !nearest) y = exactly(x);
+        q[i] = y;
+    }
 }
 
 // Four elements of a body that starts on a 16-byte boundary, times c, to the
@@ -353,7 +397,10 @@ IQLH_DEV void scale_piece(const TensorPiece& p, float c, float* flat) {
     const int e = cut.edge();
     if (!flat) {
         scale_quads<DT>((uint4*)cut.q, cut.nq, c);
-        if (e >= 0) E::store((void*)p.ptr, e, E::load((const void*)p.ptr, e) * c);
+        if (e >= 0) {
+            const float x = E::load((const void*)p.ptr, e);
+            E::store((void*)p.ptr, e, DT == IQLH_BF16 ? product_to_odd(x, c) : x * c);
+        }
         return;
     }
     scale_flat<DT>(cut.q, flat + p.off + cut.head, cut.nq * (E::kQ / 4), c);
