@@ -79,3 +79,22 @@ def test_products_next_to_a_middle_round_once(m, name, scale):
             assert np.array_equal(got, want), (c, x[got != want], got[got != want], want[got != want])
     if scale >= 2.0 ** -10:
         assert different >= 24  # the crafted elements are there
+
+
+@pytest.mark.parametrize("name", sorted(TYPES))
+def test_whole_pieces_round_once(m, name):
+    """The same over a tensor of many whole pieces (32 MB and more)."""
+    import torch
+    bits, smallest = TYPES[name]
+    pairs = _factors(bits, 3)
+    x = np.concatenate([np.arange(1 << (bits - 1), 1 << bits) / 2.0 ** bits, [p for p, _ in pairs], [1.0]])
+    reps = (20 << 20) // len(x) + 1
+    for _, c in pairs:
+        t = torch.from_numpy(x).to(getattr(torch, name)).to(dev()).repeat(reps)
+        s = m.TensorSet([t])
+        out = torch.zeros(2, device=dev())
+        m.grad_clip(s, c, out, m.grad_norm_workspace(s), kind=m.NORM_MAX)
+        sync()
+        assert out.tolist() == [1.0, c]
+        want = torch.from_numpy(_round(x * c, bits, smallest)).to(getattr(torch, name)).to(dev())
+        assert bool((t.view(reps, -1) == want).all())
