@@ -572,13 +572,14 @@ typedef struct iqlh_mx4 {
  *              rows.  1: x is [out->cols][ld], ld >= out->rows, and the
  *              transpose is quantised: blocks along x's columns (the operand
  *              of a product that sums over x's rows).
- * x and out must not share memory.  Sizes whose launch would hold 2^32 threads
- * or more (from about 2^35 elements on) are refused, here and below. */
+ * Here and below, what a call writes must not share memory with anything else it
+ * takes (IQLH_EINVAL; rows that only interleave do not), and sizes whose launch would
+ * hold 2^32 threads or more (from about 2^35 elements on) are refused. */
 int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transposed, const iqlh_mx4* out,
                       void* stream);
 
 /* out[r][c] = value of element (r, c), rounded once to `dtype` (exact in
- * binary32); ld >= q->cols; out and q must not share memory. */
+ * binary32); ld >= q->cols. */
 int iqlh_mx4_dequantize(const iqlh_mx4* q, void* out, int32_t dtype, int64_t ld, void* stream);
 
 /* out[m][n] = act(sum_k a[m][k] b[n][k] + bias[n]), a [M, K] and b [N, K]
@@ -586,7 +587,7 @@ int iqlh_mx4_dequantize(const iqlh_mx4* q, void* out, int32_t dtype, int64_t ld,
  * out_dtype.
  *   bias   device [N] f32, or NULL (0).
  *   relu   0: act is the identity; 1: max(., 0) (a NaN stays).
- *   out    device [M][ld_out], ld_out >= N; must not overlap an operand.
+ *   out    device [M][ld_out], ld_out >= N.
  *   workspace  device, >= iqlh_mx4_workspace_bytes(M, N, K), 16-byte
  *          aligned, no initial contents required; calls that overlap in time
  *          need one each.

@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -704,6 +705,58 @@ static int check_float_matrix(const char* who, const void* x, int32_t dtype, int
     return IQLH_OK;
 }
 
+namespace {
+// Rows of memory, `pitch` bytes from one to the next
+struct MemRows {
+    const char* what;
+    __int128 at, bytes, pitch, rows;
+    MemRows(const char* w, const void* p, int64_t n) : what(w), at((uintptr_t)p), bytes(p ? n : 0), pitch(bytes), rows(1) {}
+    MemRows(const char* w, const void* p, int64_t r, int64_t c, int64_t ld, int es)
+        : what(w), at((uintptr_t)p), bytes((__int128)c * es), pitch((__int128)ld * es), rows(r) {
+        if (pitch != bytes) return;
+        bytes *= r;  // no gaps: one row
+        pitch = bytes;
+        rows = 1;
+    }
+    __int128 end() const { return at + (rows - 1) * pitch + bytes; }
+};
+}  // namespace
+
+// Whether a byte belongs to both.  Matrices whose rows interleave, such as columns
+// of one buffer, need not share any.
+static bool share_memory(const MemRows& a, const MemRows& b) {
+    if (!a.bytes || !b.bytes || a.at >= b.end() || b.at >= a.end()) return false;
+    if (a.rows == 1 && b.rows == 1) return true;
+    auto floor_div = [](__int128 x, __int128 y) { return x >= 0 ? x / y : -((-x + y - 1) / y); };
+    // rows i of a and j of b, t = i - j: they meet where -a.bytes < a.at - b.at + t pitch < b.bytes
+    if (a.pitch == b.pitch) {
+        __int128 t = floor_div(b.at - a.at - a.bytes, a.pitch) + 1;
+        if (t < 1 - b.rows) t = 1 - b.rows;
+        return t < a.rows && a.at - b.at + t * a.pitch < b.bytes;
+    }
+    const MemRows &few = a.rows < b.rows ? a : b, &many = a.rows < b.rows ? b : a;
+    for (__int128 i = 0; i < few.rows; ++i) {
+        const __int128 lo = few.at + i * few.pitch, hi = lo + few.bytes;
+        __int128 t = floor_div(lo - many.at - many.bytes, many.pitch) + 1;  // the first row that ends behind lo
+        if (t < 0) t = 0;
+        if (t < many.rows && many.at + t * many.pitch < hi) return true;
+    }
+    return false;
+}
+
+// What a call writes must be apart from all else it takes
+static int check_apart(const char* who, std::initializer_list<MemRows> written, std::initializer_list<MemRows> read) {
+    for (const MemRows* w = written.begin(); w != written.end(); ++w) {
+        for (const MemRows* o = w + 1; o != written.end(); ++o)
+            if (share_memory(*w, *o)) return fail(IQLH_EINVAL, "%s: %s and %s share memory", who, w->what, o->what);
+        for (const MemRows& r : read)
+            if (share_memory(*w, r)) return fail(IQLH_EINVAL, "%s: %s and %s share memory", who, w->what, r.what);
+    }
+    return IQLH_OK;
+}
+static MemRows codes_of(const char* what, const Mx4Mat& q) { return MemRows(what, q.codes, q.rows * q.kb() * 16); }
+static MemRows scales_of(const char* what, const Mx4Mat& q) { return MemRows(what, q.scales, q.rows * q.kb()); }
+
 int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transposed, const iqlh_mx4* out,
                       void* stream) {
     Mx4Mat q;
@@ -715,6 +768,9 @@ int iqlh_mx4_quantize(const void* x, int32_t dtype, int64_t ld, int32_t transpos
     if (!mx4_quantizable(q.rows, q.cols, transposed != 0))
         return fail(IQLH_ESHAPE, "iqlh_mx4_quantize: %lld x %lld is more than one launch takes", (long long)q.rows,
                     (long long)q.cols);
+    rc = check_apart("iqlh_mx4_quantize", {codes_of("the codes", q), scales_of("the scales", q)},
+                     {MemRows("x", x, transposed ? q.cols : q.rows, transposed ? q.rows : q.cols, ld, dtype_bytes(dtype))});
+    if (rc) return rc;
     hipError_t e = launch_mx4_quantize(x, dtype, ld, transposed != 0, q, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_quantize launch");
     return IQLH_OK;
@@ -729,6 +785,9 @@ int iqlh_mx4_dequantize(const iqlh_mx4* in, void* out, int32_t dtype, int64_t ld
     if (!mx4_dequantizable(q.rows, q.cols, dtype_bytes(dtype)))
         return fail(IQLH_ESHAPE, "iqlh_mx4_dequantize: %lld x %lld is more than one launch takes", (long long)q.rows,
                     (long long)q.cols);
+    rc = check_apart("iqlh_mx4_dequantize", {MemRows("out", out, q.rows, q.cols, ld, dtype_bytes(dtype))},
+                     {codes_of("the codes", q), scales_of("the scales", q)});
+    if (rc) return rc;
     hipError_t e = launch_mx4_dequantize(q, out, dtype, ld, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_dequantize launch");
     return IQLH_OK;
@@ -773,6 +832,12 @@ int iqlh_mx4_matmul(const iqlh_mx4* a, const iqlh_mx4* b, const float* bias, int
     rc = check_mx4_product("iqlh_mx4_matmul", am.rows, bm, bias, relu, out, out_dtype, ld_out, workspace,
                            workspace_bytes, &o);
     if (rc) return rc;
+    rc = check_apart("iqlh_mx4_matmul",
+                     {MemRows("out", out, am.rows, bm.rows, ld_out, dtype_bytes(out_dtype)),
+                      MemRows("the workspace", workspace, mx4_workspace_bytes(am.rows, bm.rows, bm.cols))},
+                     {codes_of("a's codes", am), scales_of("a's scales", am), codes_of("b's codes", bm),
+                      scales_of("b's scales", bm), MemRows("bias", bias, bm.rows * 4)});
+    if (rc) return rc;
     hipError_t e = launch_mx4_matmul(am, bm, o, workspace, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_matmul launch");
     return IQLH_OK;
@@ -791,6 +856,12 @@ int iqlh_mx4_linear(const void* x, int32_t dtype, int64_t ld, int64_t M, const i
     if (!mx4_linear_launchable(M, bm.rows, bm.cols))
         return fail(IQLH_ESHAPE, "iqlh_mx4_linear: x of %lld x %lld is more than one launch takes", (long long)M,
                     (long long)bm.cols);
+    rc = check_apart("iqlh_mx4_linear",
+                     {MemRows("out", out, M, bm.rows, ld_out, dtype_bytes(out_dtype)),
+                      MemRows("the workspace", workspace, mx4_workspace_bytes(M, bm.rows, bm.cols))},
+                     {MemRows("x", x, M, bm.cols, ld, dtype_bytes(dtype)), codes_of("b's codes", bm),
+                      scales_of("b's scales", bm), MemRows("bias", bias, bm.rows * 4)});
+    if (rc) return rc;
     hipError_t e = launch_mx4_linear(x, dtype, ld, M, bm, o, workspace, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_mx4_linear launch");
     return IQLH_OK;
