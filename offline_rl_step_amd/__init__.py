@@ -629,13 +629,25 @@ def iql_forward_values_mx4_workspace(h, batch):
 
 def iql_forward_values_mx4(h, next_states, batch, out_v, workspace, rewards=None, dones=None, gamma=0.99,
                            out_target=None, states_ld=None, stream=None):
-    """iql_forward_values with both hidden layers' operands in 4 bits."""
+    """iql_forward_values with both hidden layers' operands in 4 bits.  next_states:
+    [batch or more, S] with neighbouring columns, or of any shape with states_ld."""
+    device = next_states.device
+    index = _need_current(device)
     _need(next_states.dtype in (torch.float32, torch.bfloat16), "next_states must be float32 or bfloat16")
+    _need(next_states.dim() > 0 and (next_states.shape[-1] <= 1 or next_states.stride(-1) == 1),
+          "next_states must have neighbouring columns")
+    if states_ld is None:
+        _need(next_states.dim() == 2 and next_states.shape[0] >= batch, f"next_states must be {batch} rows or more")
+    _need_f32(out_v, batch, device, "out_v")
+    for t, what in ((rewards, "rewards"), (dones, "dones"), (out_target, "out_target")):
+        if t is not None:
+            _need_f32(t, batch, device, what)
+    _need_aux(device, workspace, None)
     ld = states_ld if states_ld is not None else next_states.stride(0)
     _check(_lib_forward_mx4(h, _ptr(next_states), _DTYPES[next_states.dtype], ld, batch, _ptr(out_v), _ptr(rewards),
                             _ptr(dones), gamma, _ptr(out_target), _ptr(workspace),
                             workspace.numel() * workspace.element_size(),
-                            _stream_of(stream, _get_device(), next_states, out_v, workspace, rewards, dones, out_target)),
+                            _stream_of(stream, index, next_states, out_v, workspace, rewards, dones, out_target)),
            "iql_forward_values_mx4")
 
 
@@ -816,6 +828,11 @@ class IqlTrainer:
 
     def forward_values_mx4(self, next_states, batch, out_v, workspace, rewards=None, dones=None, gamma=0.99,
                            out_target=None, states_ld=None, stream=None):
+        S, groups = self.cfg.state_dim, self.cfg.num_groups
+        _need(next_states.dim() != 2 or next_states.shape[1] >= S, f"next_states must have {S} columns or more")
+        for t, what in ((out_v, "out_v"), (out_target, "out_target")):
+            if t is not None:
+                _need_f32(t, groups * batch, next_states.device, what)
         iql_forward_values_mx4(self.h, next_states, batch, out_v, workspace, rewards, dones, gamma, out_target,
                                states_ld, stream)
 
