@@ -418,11 +418,14 @@ def _need_current(device):
 class TensorSet:
     """The tensors of one network (float32, bfloat16, float16 in any mix, each
     contiguous, all on the current device), cut into pieces once for any number of
-    grad_norm / grad_clip calls.  Keeps the tensors; their storage must stay
-    where it is (``p.grad`` cleared with ``set_to_none=False``)."""
+    grad_norm / grad_clip calls.  Keeps the tensors' memory and goes by it:
+    gradients must stay where they are from step to step (cleared with
+    ``set_to_none=False``; new ones need a new set, the old set's calls go on
+    reading and clipping the old memory)."""
 
     def __init__(self, tensors):
         self.tensors = tensors = list(tensors)
+        self._memory = [t.detach() for t in tensors]  # what the table's addresses lie in, should t.data be replaced
         _need(len(tensors) > 0, "TensorSet needs at least one tensor")
         self.device = tensors[0].device
         _need_current(self.device)
@@ -456,7 +459,7 @@ class TensorSet:
         again, should the set be dropped, before the calls on another stream have read it."""
         if stream not in self._streams and not torch.cuda.is_current_stream_capturing():
             other = _stream_object(stream, self.device)
-            for t in (self.table, *self.tensors):
+            for t in (self.table, *self._memory):
                 t.record_stream(other)
             self._streams.add(stream)  # good until the memory is freed
         return stream

@@ -36,7 +36,7 @@ def streams(m, monkeypatch):
 def _set(m, home):
     import torch
     s = object.__new__(m.TensorSet)
-    s.table, s.device, s._streams, s.tensors = Recorded(), torch.device("cuda", 0), {home}, []
+    s.table, s.device, s._streams, s._memory = Recorded(), torch.device("cuda", 0), {home}, []
     return s
 
 
@@ -131,3 +131,28 @@ def test_a_workspaces_counter_is_zero_for_any_stream(m, calls, monkeypatch, capt
         assert fills == [64]
     else:
         assert ws[:64].tolist() == [0] * 64
+
+
+def test_a_sets_memory_stays_when_its_tensors_move(m, calls):
+    """The storage that the table's addresses lie in lives as long as the set."""
+    import gc
+    import weakref
+    import torch
+    t = torch.zeros(1000)
+    s = m.TensorSet([t])
+    freed = []
+
+    class Canary:
+        pass
+    canary = Canary()
+    weakref.finalize(canary, lambda: freed.append(1))
+    t.untyped_storage()._kept = canary  # the storage's Python object lives with it
+    old = t.untyped_storage()._cdata
+    del canary
+    t.data = torch.ones(1000)
+    assert t.untyped_storage()._cdata != old
+    gc.collect()
+    assert not freed
+    s = None
+    gc.collect()
+    assert freed

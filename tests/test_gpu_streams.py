@@ -51,3 +51,20 @@ def test_a_new_workspace_serves_another_stream_at_once(m):
     sync()
     for x in out.tolist():
         assert abs(x - want) <= (U32 * 1.0001 + 30_077 * 2.0 ** -53) * want
+
+
+def test_a_sets_memory_stays_when_its_tensors_move(m):
+    """A tensor of the set that is given other storage (t.data = ..) leaves its
+    old memory to the set: nothing else gets it while the set lives."""
+    import torch
+    n = 3_000_000
+    t = torch.ones(n, device=dev())
+    at = t.data_ptr()
+    s = m.TensorSet([t])
+    t.data = torch.full((n,), 2.0, device=dev())
+    others = [torch.full((n,), 9.0, device=dev()) for _ in range(4)]
+    assert all(o.data_ptr() != at for o in others)
+    out = torch.zeros(1, device=dev())
+    m.grad_norm(s, out, m.grad_norm_workspace(s))
+    sync()
+    assert abs(float(out[0]) - n ** 0.5) <= U32 * 1.0001 * n ** 0.5
