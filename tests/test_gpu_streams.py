@@ -53,6 +53,48 @@ def test_a_new_workspace_serves_another_stream_at_once(m):
         assert abs(x - want) <= (U32 * 1.0001 + 30_077 * 2.0 ** -53) * want
 
 
+def test_norms_and_factors_of_clips_on_several_streams(m):
+    """Sets dropped right after their calls on four streams, outputs that live
+    to the end: every norm, factor and flat vector."""
+    import torch
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    lists = [_grads(30 + k, [50_000 + 7 * k, 33, 2000]) for k in range(4)]
+    want = [ref.norm(_host(ts), 0) for ts in lists]
+    outs = [torch.zeros((8, 2), device=dev()) for _ in range(4)]
+    flats = [torch.zeros(sum(t.numel() for t in ts), device=dev()) for ts in lists]
+    sync()
+    for rep in range(8):
+        for k, st in enumerate(streams):
+            s = m.TensorSet(lists[k])
+            m.grad_clip(s, 0.5, outs[k][rep], m.grad_norm_workspace(s), out_flat=flats[k], stream=st)
+            del s
+    sync()
+    for k in range(4):
+        c = 0.5 / want[k]
+        for n, f in outs[k].tolist():
+            assert abs(n - want[k]) <= (U32 * 1.0001 + 60_000 * 2.0 ** -53) * want[k] and abs(f - c) <= 1.01 * U32 * c
+        x = np.concatenate(_host(lists[k]))
+        assert np.all(np.abs(flats[k].double().cpu().numpy() - x * c) <= 2 * U32 * 1.001 * np.abs(x * c) + 2.0 ** -149)
+
+
+def test_calls_on_the_default_stream_of_a_set_made_on_another(m):
+    import torch
+    ts = _grads(9, [300_000, 5])
+    want = ref.norm(_host(ts), 0)
+    out = torch.zeros(6, device=dev())
+    side = torch.cuda.Stream()
+    sync()
+    for rep in range(6):
+        with torch.cuda.stream(side):
+            s = m.TensorSet(ts)
+            ws = m.grad_norm_workspace(s)
+            m.grad_norm(s, out[rep:rep + 1], ws, stream=torch.cuda.default_stream())
+            del s, ws
+    sync()
+    for x in out.tolist():
+        assert abs(x - want) <= (U32 * 1.0001 + 300_005 * 2.0 ** -53) * want
+
+
 def test_a_sets_memory_stays_when_its_tensors_move(m):
     """A tensor of the set that is given other storage (t.data = ..) leaves its
     old memory to the set: nothing else gets it while the set lives."""
