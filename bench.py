@@ -65,12 +65,13 @@ def parse():
     p.add_argument("--kernel-reps", type=int, default=200)
     p.add_argument("--copy-probe", type=int, default=0, metavar="MIB",
                    help="only run 10 plain device copies of MIB MiB (counter calibration) and exit")
-    p.add_argument("--probe", choices=("team-fold", "xcc-map", "stream-sum"), default=None,
+    p.add_argument("--probe", choices=("team-fold", "xcc-map", "stream-sum", "mx4-rate"), default=None,
                    help="only run one measurement probe of libiqlh_probes.so and print one JSON line: "
                         "team-fold (the split-K partials summed inside the writing launch, against a "
                         "separate summing launch), xcc-map (the XCD of each block of a launch of the "
                         "forward/backward kernel's shape), stream-sum (a read-only four-array sum of squares "
-                        "of 1 GiB cut into blocks three ways)")
+                        "of 1 GiB cut into blocks three ways), mx4-rate (the scaled 4-bit matrix instructions "
+                        "on registers alone, with the clock)")
     p.add_argument("--phases", action="store_true",
                    help="only run the headline step through iql_aux_step_phase_stamps and print one JSON line: "
                         "the forward/backward kernel's phase durations per workgroup (median over steps and "
@@ -135,6 +136,15 @@ def run_probe(name, reps=50):
             out[f"nb{nb}"] = {"strided_us": us[0], "chunked_us": us[1], "per_piece_us": us[2],
                               "strided_TBs": 16 * n / us[0] / 1e6, "chunked_TBs": 16 * n / us[1] / 1e6,
                               "per_piece_TBs": 16 * n / us[2] / 1e6}
+    elif name == "mx4-rate":
+        iters, runs = 40000, 8
+        r = (ctypes.c_double * 12)()
+        rc = lib.iqlh_probe_mx4_rate(ctypes.c_int(iters), ctypes.c_int(runs), r)
+        if rc != 0:
+            raise RuntimeError(f"iqlh_probe_mx4_rate returned {rc}")
+        out = {"probe": name, "instructions_per_wave": 8 * iters, "launches": runs}
+        for i, v in enumerate(("32x32x64_zeros", "32x32x64_random", "16x16x128_zeros", "16x16x128_random")):
+            out[v] = {"TFLOPs": r[3 * i], "clock_GHz": r[3 * i + 1], "cycles_per_instruction": r[3 * i + 2]}
     else:
         blocks, lds = 256, 154 * 1024
         xcc = (ctypes.c_int * blocks)()

@@ -79,10 +79,14 @@ __global__ __launch_bounds__(kNT, 4) void mx4_rows_kernel(const typename MxFloat
 }  // namespace
 
 bool mx4_rows_ok(int64_t M, int64_t N, int64_t K) {
-    // rows enough for every compute unit, and less than 2^32 threads of them; a b
-    // of at most 256 KB
+    // Rows enough for every compute unit, and less than 2^32 threads of them; a b of at
+    // most 256 KB, above K 896 of 96 KB.  fp32 -> bf16, quantisation and product | one
+    // launch, us, at M 16384, 65536:
+    //   N 512, K 256: 19 | 14, 40 | 28 (M 4096: 12.2 | 11.5, 2048: 8.5 | 11.1); K 768:
+    //   23 | 26, 71 | 72; K 1000: 28 | 40, 106 | 130; N 128, K 1024: 23 | 20, 71 | 62;
+    //   N 2048, K 256: 33 | 34, 113 | 107; N 4096, K 256 (512 KB): 57 | 63, 224 | 229
     const int64_t kb = (K + 31) / 32;
-    return M >= 16384 && M <= 1 << 29 && kb <= kRowsMaxBlocks && N * kb <= 16384;
+    return M >= 16384 && M <= 1 << 29 && kb <= kRowsMaxBlocks && N * kb <= (kb <= 28 ? 16384 : 6144);
 }
 
 hipError_t launch_mx4_rows(const void* x, int dtype, int64_t ld, int64_t M, const Mx4Mat& b, const Mx4Out& out,

@@ -27,10 +27,15 @@
 //   striding over the arrays (block b, thread t takes quads b 256 + t +
 //   i nb 256); the same grid with each block owning one contiguous range;
 //   and one block per 8 KB of each array (no loop).
+// mx4_rate: the scaled 4-bit matrix instructions on registers alone, two waves a
+//   SIMD on every SIMD, with operands of zeros and of random codes, turned by one
+//   code every eight instructions: their rate, the shader clock meanwhile, and the
+//   clock cycles of a SIMD per instruction.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
 #include <vector>
 
 namespace {
@@ -149,6 +154,55 @@ __global__ __launch_bounds__(1024) void probe_xcc_kernel(int* out) {
         asm volatile("s_getreg_b32 %0, hwreg(HW_REG_XCC_ID)" : "=s"(v));
         out[blockIdx.x] = (int)(v & 15u);
         lds[0] = 0.f;
+    }
+}
+
+// iters rounds of eight independent products, four operands by two.  out is
+// written for a sum that no operands give.  clocks: shader clock cycles and
+// 100 MHz ticks of the rounds of the first and the last block (of two waves on a SIMD
+// the older one runs first).
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+template <bool WIDE>
+__global__ __launch_bounds__(256, 2) void probe_mx4_kernel(uint32_t seed, int iters, float* out, int64_t* clocks) {
+    i8v op[6];
+    uint32_t h = seed ? seed + blockIdx.x * 256u + threadIdx.x : 0u;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        op[i] = i8v{};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (seed) h = (h ^ (h >> 15)) * 0x2C1B3C6Du + 0x9E3779B9u;
+            op[i][k] = (int)h;
+        }
+    }
+    typedef std::conditional_t<WIDE, f16v, f4> Acc;
+    Acc acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = Acc{};
+    const int64_t c0 = clock64(), w0 = wall_clock64();
+    for (int it = 0; it < iters; ++it) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (WIDE)
+                acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
+            else
+                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
+        }
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) op[i][k] = (int)(((uint32_t)op[i][k] << 4) | ((uint32_t)op[i][k] >> 28));
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        for (int k = 0; k < (WIDE ? 16 : 4); ++k) sum += acc[i][k];
+    if (sum == 1.2345e30f) out[0] = sum;
+    if ((blockIdx.x == 0 || blockIdx.x == gridDim.x - 1) && threadIdx.x == 0) {
+        int64_t* c = clocks + (blockIdx.x ? 2 : 0);
+        c[0] = clock64() - c0;
+        c[1] = wall_clock64() - w0;
     }
 }
 
@@ -314,6 +368,45 @@ int iqlh_probe_stream_sum(int64_t n, int nb, int reps, double* out_us) {
     for (auto& x : arr) hipFree(x);
     hipFree(out);
     hipFree(dptr);
+    return 0;
+}
+
+// out[4][3]: for 32 x 32 x 64 on zeros, on random codes, 16 x 16 x 128 on zeros, on
+// random codes: TFLOP/s over the last of `reps` launches, shader clock in GHz,
+// cycles of a SIMD per instruction.  iters rounds of eight instructions a wave.
+int iqlh_probe_mx4_rate(int iters, int reps, double* out) {
+    if (iters < 1 || iters > 1 << 20 || reps < 1 || reps > 100 || !out) return -1;
+    constexpr int kBlocks = 512;  // of four waves: two a SIMD on 256 compute units
+    float* sink = nullptr;
+    int64_t* clocks = nullptr;
+    PCK(hipMalloc(&sink, sizeof(float)));
+    PCK(hipMalloc(&clocks, 4 * sizeof(int64_t)));
+    hipEvent_t e0, e1;
+    PCK(hipEventCreate(&e0));
+    PCK(hipEventCreate(&e1));
+    for (int v = 0; v < 4; ++v) {
+        const uint32_t seed = v & 1 ? 0x1234567u : 0u;
+        float ms = 0.f;
+        for (int r = 0; r < reps; ++r) {
+            PCK(hipEventRecord(e0, 0));
+            if (v < 2) hipLaunchKernelGGL(probe_mx4_kernel<true>, dim3(kBlocks), dim3(256), 0, 0, seed, iters, sink, clocks);
+            else hipLaunchKernelGGL(probe_mx4_kernel<false>, dim3(kBlocks), dim3(256), 0, 0, seed, iters, sink, clocks);
+            PCK(hipGetLastError());
+            PCK(hipEventRecord(e1, 0));
+            PCK(hipEventSynchronize(e1));
+            PCK(hipEventElapsedTime(&ms, e0, e1));
+        }
+        int64_t c[4] = {0, 0, 0, 0};
+        PCK(hipMemcpy(c, clocks, sizeof(c), hipMemcpyDeviceToHost));
+        const double flops = v < 2 ? 2.0 * 32 * 32 * 64 : 2.0 * 16 * 16 * 128;
+        out[3 * v] = flops * 8 * iters * kBlocks * 4 / (ms * 1e-3) / 1e12;
+        out[3 * v + 1] = c[1] + c[3] > 0 ? (double)(c[0] + c[2]) / (c[1] + c[3]) * 0.1 : 0.0;
+        out[3 * v + 2] = out[3 * v + 1] * 1e9 * (ms * 1e-3) / (8.0 * iters * 2);
+    }
+    hipEventDestroy(e0);
+    hipEventDestroy(e1);
+    hipFree(sink);
+    hipFree(clocks);
     return 0;
 }
 
