@@ -526,7 +526,8 @@ int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, fl
                    int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Global clip: c = max_norm / norm when norm > max_norm, else 1 (the norm of
- * iqlh_grad_norm in binary64, c rounded to binary32), and x -> c x.
+ * iqlh_grad_norm and the quotient in binary64, c rounded to binary32 once), and
+ * x -> c x.
  *   out_flat   NULL: in place, each product rounded once to the tensor's type;
  *              nothing is written when c is 1, and a set whose tensors
  *              overlap is refused (they would be scaled twice).
@@ -538,7 +539,7 @@ int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, fl
  *   d_flags    device sticky flag word or NULL: a set with a NaN or an
  *              infinity sets IQLH_FLAG_NONFINITE_GRAD; c is then 1.
  * max_norm > 0 (infinity: never clips). */
-int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, float* out_flat,
+int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, double max_norm, float* out_flat,
                    float* out, int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------

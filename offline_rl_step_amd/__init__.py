@@ -139,7 +139,7 @@ _lib_norm_ws = _sig("iqlh_grad_norm_workspace_bytes", _i32, [ctypes.POINTER(Tens
                                                              ctypes.POINTER(ctypes.c_size_t)])
 _lib_grad_norm = _sig("iqlh_grad_norm", _i32, [ctypes.POINTER(TensorSetStruct), _i32, _p, _p, _p, _p,
                                                ctypes.c_size_t, _p])
-_lib_grad_clip = _sig("iqlh_grad_clip", _i32, [ctypes.POINTER(TensorSetStruct), _i32, _f, _p, _p, _p, _p,
+_lib_grad_clip = _sig("iqlh_grad_clip", _i32, [ctypes.POINTER(TensorSetStruct), _i32, ctypes.c_double, _p, _p, _p, _p,
                                                ctypes.c_size_t, _p])
 _lib_mx4_quantize = _sig("iqlh_mx4_quantize", _i32, [_p, _i32, _i64, _i32, ctypes.POINTER(Mx4Struct), _p])
 _lib_mx4_dequantize = _sig("iqlh_mx4_dequantize", _i32, [ctypes.POINTER(Mx4Struct), _p, _i32, _i64, _p])

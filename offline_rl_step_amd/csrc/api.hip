@@ -669,13 +669,13 @@ int iqlh_grad_norm(const iqlh_tensor_set* set, int32_t kind, float* out_norm, fl
     return IQLH_OK;
 }
 
-int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, float max_norm, float* out_flat, float* out,
+int iqlh_grad_clip(const iqlh_tensor_set* set, int32_t kind, double max_norm, float* out_flat, float* out,
                    int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream) {
     TensorSetArgs a;
     int rc = make_tensor_set_args("iqlh_grad_clip", set, kind, d_flags, workspace, workspace_bytes, &a);
     if (rc) return rc;
     if (!out) return fail(IQLH_EINVAL, "iqlh_grad_clip: out is NULL");
-    if (!(max_norm > 0.f)) return fail(IQLH_EINVAL, "iqlh_grad_clip: max_norm must be > 0");
+    if (!(max_norm > 0.0)) return fail(IQLH_EINVAL, "iqlh_grad_clip: max_norm must be > 0");
     if (!out_flat && set->overlap)
         return fail(IQLH_EINVAL, "iqlh_grad_clip: tensors that share memory cannot be clipped in place");
     hipError_t e = launch_grad_clip(a, kind, max_norm, out_flat, out, (hipStream_t)stream);

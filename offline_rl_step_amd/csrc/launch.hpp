@@ -239,7 +239,7 @@ struct TensorSetArgs {
     int32_t* flags;
 };
 hipError_t launch_grad_norm(const TensorSetArgs& a, int kind, float* out_norm, float* out_each, hipStream_t stream);
-hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, float max_norm, float* flat, float* out,
+hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, double max_norm, float* flat, float* out,
                             hipStream_t stream);
 
 // ------------------------------------------- microscaled 4-bit matrices

@@ -410,12 +410,12 @@ IQLH_DEV void scale_piece(const TensorPiece& p, float c, float* flat) {
 }
 
 template <int KIND>
-__global__ __launch_bounds__(kNT) void grad_scale_kernel(TensorSetArgs a, int nb, float max_norm,
+__global__ __launch_bounds__(kNT) void grad_scale_kernel(TensorSetArgs a, int nb, double max_norm,
                                                          float* __restrict__ flat, float* __restrict__ out) {
     __shared__ uint64_t red[kNT / kWave];
     const double n = norm_of_parts<KIND>(a.part, nb, red);
     const bool ok = finite64(n);
-    const float c = ok && n > (double)max_norm ? (float)((double)max_norm / n) : 1.f;
+    const float c = ok && n > max_norm ? (float)(max_norm / n) : 1.f;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         out[0] = (float)n;
         out[1] = c;
@@ -459,7 +459,7 @@ hipError_t norm_launch(const TensorSetArgs& a, float* out_norm, float* out_each,
 }
 
 template <int KIND>
-hipError_t clip_launch(const TensorSetArgs& a, float max_norm, float* flat, float* out, hipStream_t stream) {
+hipError_t clip_launch(const TensorSetArgs& a, double max_norm, float* flat, float* out, hipStream_t stream) {
     hipError_t e = norm_pass<KIND, false, false>(a, nullptr, nullptr, stream);
     if (e != hipSuccess) return e;
     const int nb = norm_blocks(a.npieces);
@@ -474,7 +474,7 @@ hipError_t launch_grad_norm(const TensorSetArgs& a, int kind, float* out_norm, f
                                 : norm_launch<IQLH_NORM_MAX>(a, out_norm, out_each, stream);
 }
 
-hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, float max_norm, float* flat, float* out,
+hipError_t launch_grad_clip(const TensorSetArgs& a, int kind, double max_norm, float* flat, float* out,
                             hipStream_t stream) {
     return kind == IQLH_NORM_L2 ? clip_launch<IQLH_NORM_L2>(a, max_norm, flat, out, stream)
                                 : clip_launch<IQLH_NORM_MAX>(a, max_norm, flat, out, stream);

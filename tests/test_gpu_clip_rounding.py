@@ -98,3 +98,26 @@ def test_whole_pieces_round_once(m, name):
         assert out.tolist() == [1.0, c]
         want = torch.from_numpy(_round(x * c, bits, smallest)).to(getattr(torch, name)).to(dev())
         assert bool((t.view(reps, -1) == want).all())
+
+
+@pytest.mark.parametrize("flat", [False, True])
+def test_the_factor_of_any_bound_is_rounded_once(m, flat):
+    """c = bound / norm for bounds that binary32 does not hold: at most half a
+    step of binary32 from the quotient (the norm's own error, n 2^-53 of it, far
+    below); rounding the bound first would take up to two halves."""
+    import torch
+    x = torch.tensor([3.0, 4.0], device=dev())  # norm 5, exact
+    s = m.TensorSet([x])
+    ws, out, dst = m.grad_norm_workspace(s), torch.zeros(2, device=dev()), torch.zeros(2, device=dev())
+    g = np.random.default_rng(3)
+    apart = 0
+    for bound in g.uniform(0.5, 5.0, 400):
+        x.copy_(torch.tensor([3.0, 4.0]))
+        m.grad_clip(s, float(bound), out, ws, out_flat=dst if flat else None)
+        sync()
+        c, want = float(out[1]), bound / 5.0
+        assert c == float(np.float32(want)), bound
+        apart += c != float(np.float32(np.float64(np.float32(bound)) / 5.0))
+        y = (dst if flat else x).cpu().numpy()
+        assert np.array_equal(y, np.float32(c) * np.array([3.0, 4.0], np.float32))
+    assert apart > 20  # bounds whose rounding shows in the factor are among them
