@@ -4,9 +4,11 @@
 // "Rust Integration: gpu_iql_trainer.rs", forward_values) on the 4-bit product.
 //
 // Bound by the 4-bit fragments' way from L2 and the conversions between the layers:
-// S 256, H 512, B 65536 48 us (bf16 pass 66, fp32 754), S 128, H 1024 82 (677); two
-// networks of H 128, S 128, B 16384 15 us, more than their bf16 pass (6.5), for the
-// weights' launch.
+// S 256, H 512, B 65536 46 to 48 us (bf16 pass 61, fp32 751; the least is 6.5 us of
+// bytes, 8.3 of products at 6.2 PF and two launches), S 128, H 1024 83 to 87 (677); two
+// networks of H 128, S 128, B 16384 15 us, more than their bf16 pass (6.9), for the
+// weights' launch.  Layer by layer: S 1100, H 1056, B 65536 576 (fp32 4029), S 256, H
+// 2048, B 65536 749 (7712).
 //
 // Up to 1024 states and hidden units: two launches, the weights' quantisation
 // and the whole network (a workgroup takes 64 or 128 rows through both layers, h1 in
@@ -238,8 +240,10 @@ hipError_t launch_net(const NetArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 // 128 rows a workgroup halve the weights' traffic from L2, 64 rows give twice
-// the workgroups: H 512, S 256, B 65536 54.6 against 63.1 us, H 1024, S 128,
-// B 65536 101 against 154; two networks of H 128, S 128, B 16384 17.3 against 13.6
+// the workgroups.  64 | 128 rows, us: S 256, H 512, B 65536 53.8 | 45.6, 32768 29.6 | 26.2, 16384
+// 26.8 | 24.3; S 128, H 1024, B 65536 103 | 83; S 128, H 256, B 32768 16.8 | 15.5, 16384
+// 14.9 | 15.2; S 64, H 192, B 65536 30.2 | 27.5; S 128, H 128, B 65536 21.5 | 23.2, two networks
+// of 16384 15.2 | 18.9
 template <int XDT>
 hipError_t launch_net(const NetArgs& a, hipStream_t stream) {
     const bool wide = a.H >= 256 && a.B >= 128 * 256;

@@ -23,9 +23,11 @@ constexpr int kQRows = 4;  // rows (times the workgroup's) a thread converts
 // Blocks along x's rows.  HBM-bound.  A thread converts 8 elements (one dword
 // of codes) of kQRows rows, all loaded before the first is used; four
 // neighbouring lanes share a block.  A workgroup is 2^c_log groups of 8 wide
-// and 256 / 2^c_log rows high.  (8192 x 8192 fp32 47 us, 6.4 TB/s, bf16 29, 5.9; 65536 x
-// 777 fp32 35, bf16 27, all from the Infinity Cache; 8192 x 8192 bf16 from HBM 47; a
-// batch of 16384 x 128 fp32 3.2, where the launch counts.)
+// and 256 / 2^c_log rows high.  (8192 x 8192 bf16 29 us, 5.9 TB/s of 170 MB, with an
+// input that the Infinity Cache holds, 37 from HBM, and 48 right behind a pass whose 268
+// MB of output are still on their way there; fp32, 304 MB, 49 with the same input
+// again, 58 with others; 65536 x 777 with the same input fp32 35, bf16 27; a batch of
+// 16384 x 128 fp32 3.2 to 3.6, where the launch counts.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_quantize_kernel(const typename MxFloat<DT>::type* __restrict__ x, int64_t ld,
                                                            Mx4Mat q, int c_log, int col_tiles) {
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_narrow_kernel(const typename
 // column of x, 32 rows a block, neighbouring lanes neighbouring addresses; a
 // workgroup 2^c_log columns (64, fewer of a narrow x) and 4 HALVES blocks per
 // wave's worth of them.  The codes pass through LDS so that a row of q is written 64 bytes
-// or more at a time.  (8192^2 bf16 27.0 us, 6.3 TB/s; two 16-bit columns per
+// or more at a time.  (8192^2 bf16 from the Infinity Cache 27.0 us, 6.3 TB/s; two 16-bit columns per
 // lane by dword loads 27.5, and 12.3 against 5.2 us at 5001 x 777, where they
 // leave half of the compute units without a workgroup.  Runs of tiles per XCD:
 // 65536 x 777 fp32 52 -> 34 us, bf16 38 -> 21.5; rows on cache lines lose by them,
@@ -163,8 +165,9 @@ __global__ __launch_bounds__(kNT) void mx4_quantize_columns_kernel(const typenam
 }
 
 // HBM-bound on its stores: a thread writes 16 bytes of kQRows rows, so that
-// neighbouring lanes write neighbouring 16 bytes.  (8192 x 8192 to fp32 45 us, 6.7
-// TB/s; stores past the caches: no gain.)
+// neighbouring lanes write neighbouring 16 bytes.  (8192 x 8192 to fp32, 304 MB, 45 us
+// behind the quantisation, whose codes the caches still hold, 55 otherwise; stores past
+// the caches: no gain.)
 template <int DT>
 __global__ __launch_bounds__(kNT) void mx4_dequantize_kernel(Mx4Mat q, typename MxFloat<DT>::type* __restrict__ out,
                                                              int64_t ld, int c_log, int col_tiles) {

@@ -36,8 +36,8 @@ hipError_t by_dtype(int dtype, F f) {
 // step per thread at 4096 elements, while b's loads are under way.  A wave's
 // 16-byte loads of 16 rows are 64 lookups in the L1, so only b's are made; b's
 // scales come as 4 bytes per row to 16 lanes.  The waves' sums meet in LDS, added in
-// wave order.  (One row of 4096 x 4096 in bf16: 4.1 us, 2.2 TB/s; of 8192 x 8192 9.0,
-// 4.0 TB/s; 16 rows of that in 4 bits 11.4.)
+// wave order.  (One row of 4096 x 4096 in bf16: 4.1 to 4.4 us, 2.2 TB/s; of 8192 x 8192
+// 9.4, 3.8 TB/s, in 4 bits already 8.0; 16 rows of that in 4 bits 11.3.)
 constexpr int kFewWaves = 8;
 constexpr int kFewElements = 16384;  // of a workgroup's part of a float left operand, padded
 template <int XDT, int ODT, int MF>
@@ -497,9 +497,10 @@ IQLH_DEV void store_tile(const TileArgs& t, const mx_f16 (&acc)[FA][2], uint8_t*
 // that buffer and reads the first fragments of step s + 1 while the matrix
 // instructions of the quarter run.  A row's chunk u (16 bytes) lies at
 // 128 row + 16 (u ^ ((row >> 1) & 7)): 16 lanes of a fragment column fall on
-// all 64 banks.  Bound by the matrix instructions and the clock that the chip's power
-// leaves them: 8192^3 279 to 314 us, 3.5 to 3.9 PF; instructions on registers alone
-// reach 4.7 PF on random bits and 6.0 on zeros, and 16 x 16 ones 4.1.  Where a tile
+// all 64 banks.  8192^3 280 to 314 us, 3.5 to 3.9 PF: by the counters the matrix units
+// are busy 47 % of the cycles, at 1.93 GHz.  On registers alone the instruction
+// reaches 6.2 PF on random codes, for which the clock falls to 1.5 GHz, and 9.8 on zeros
+// at 2.4 GHz (16 x 16 ones 6.7 and 9.4; bench.py --probe mx4-rate).  Where a tile
 // has a few steps only, by the chain of first load, steps and stores: 2048^3 12.3 us,
 // 8192 x 8192 x 256 52.
 // SHORT: K of at most kShortSteps steps, the scales of all of it in LDS before
@@ -687,8 +688,11 @@ int64_t tiles_of(int64_t M, int64_t N, int64_t T) { return ((M + T - 1) / T) * (
 Path pick(int64_t M, int64_t N, int64_t K) {
     if (M <= 16 && few_bytes(M, K) <= 80 << 10) return Path::few;  // two workgroups to a compute unit
     const bool lds_tiles = K <= 1 << 22 && tiles_of(M, N, 128) < 1 << 22;  // 32-bit offsets in a tile, grid sizes
-    // 256 tiles for most compute units (2048 x 4096 x 4096, 128 of them: 39.1 us
-    // against 30.5 with 128 tiles; 4096^3, 256 of them: 45.0)
+    // 256 tiles for most compute units.  128 | 256 tiles, us, at K 512, 1500, 4096: 128 of
+    // the large ones 12.3 | 14.8, 18.9 | 21.9, 33.8 | 39.7; 169: 17.6 | 15.3, 26.6 | 23.7, 42.5 |
+    // 42.4; 196: 19.5 | 15.9, 31.6 | 25.3, 51.4 | 43.0; 256: 20.5 | 17.1, 35.1 | 27.8, 56.1 | 47.2; 289,
+    // the first of a second round: 25.2 | 26.7, 41.7 | 43.2, 68.0 | 74.7; 1024: 64.7 | 57.9, 117
+    // | 97, 198 | 168
     if (lds_tiles && K >= 256 && tiles_of(M, N, 256) >= 192) return Path::tile256;
     // waves that split k, the smallest outputs a workgroup that a round of workgroups
     // covers: 32 x 16 (20 x 4096 x 4096: 4.8 us, with 32 x 32 5.2), 32 x 32, two to a

@@ -28,8 +28,8 @@
 //   i nb 256); the same grid with each block owning one contiguous range;
 //   and one block per 8 KB of each array (no loop).
 // mx4_rate: the scaled 4-bit matrix instructions on registers alone, two waves a
-//   SIMD on every SIMD, with operands of zeros and of random codes, turned by one
-//   code every eight instructions: their rate, the shader clock meanwhile, and the
+//   SIMD on every SIMD, with operands of zeros and of random codes, a quarter of which
+//   is turned by one code every eight instructions: their rate, the shader clock meanwhile, and the
 //   clock cycles of a SIMD per instruction.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(1024) void probe_xcc_kernel(int* out) {
     }
 }
 
-// iters rounds of eight independent products, four operands by two.  out is
+// iters (a multiple of 4) rounds of eight independent products, four operands by two.  out is
 // written for a sum that no operands give.  clocks: shader clock cycles and
 // 100 MHz ticks of the rounds of the first and the last block (of two waves on a SIMD
 // the older one runs first).
@@ -181,18 +181,19 @@ __global__ __launch_bounds__(256, 2) void probe_mx4_kernel(uint32_t seed, int it
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = Acc{};
     const int64_t c0 = clock64(), w0 = wall_clock64();
-    for (int it = 0; it < iters; ++it) {
+    for (int it = 0; it < iters; it += 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (WIDE)
-                acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
-            else
-                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (WIDE)
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
+                else
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(op[i & 3], op[4 + (i >> 2)], acc[i], 4, 4, 0, 127, 0, 127);
+            }
+#pragma unroll
+            for (int i = 0; i < 6; ++i) op[i][j] = (int)(((uint32_t)op[i][j] << 4) | ((uint32_t)op[i][j] >> 28));
         }
-#pragma unroll
-        for (int i = 0; i < 6; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) op[i][k] = (int)(((uint32_t)op[i][k] << 4) | ((uint32_t)op[i][k] >> 28));
     }
     float sum = 0.f;
 #pragma unroll
@@ -375,7 +376,7 @@ int iqlh_probe_stream_sum(int64_t n, int nb, int reps, double* out_us) {
 // random codes: TFLOP/s over the last of `reps` launches, shader clock in GHz,
 // cycles of a SIMD per instruction.  iters rounds of eight instructions a wave.
 int iqlh_probe_mx4_rate(int iters, int reps, double* out) {
-    if (iters < 1 || iters > 1 << 20 || reps < 1 || reps > 100 || !out) return -1;
+    if (iters < 4 || iters % 4 || iters > 1 << 20 || reps < 1 || reps > 100 || !out) return -1;
     constexpr int kBlocks = 512;  // of four waves: two a SIMD on 256 compute units
     float* sink = nullptr;
     int64_t* clocks = nullptr;
