@@ -294,7 +294,7 @@ __global__ __launch_bounds__(kNT) void grad_norm_finish_kernel(TensorSetArgs a, 
 // Products of a clip in place are rounded once.  To binary16 the multiplication
 // and the conversion are one instruction, which does so.  To bfloat16 the product
 // passes through binary32, and where that puts it onto the middle of two values
-// the conversion would go to the even one: such a round of products is taken again
+// the conversion would go to the even one: the thread's products are then taken again
 // from the exact ones (32 bits, exact in binary64), rounded to odd, that is cut off
 // with the last bit set, so that the conversion sees the side they lie on.
 // (537 MB of bf16, norm and clip: 290 us, without this 285.)
@@ -314,7 +314,7 @@ IQLH_DEV float product_to_odd(float x, float c) {
 template <int DT>
 IQLH_DEV void scale_quads(uint4* q, int nq, float c) {
     typedef Elem<DT> E;
-    uint32_t nearest = 1u;  // 0: a product of this round lies in the middle
+    uint32_t nearest = 1u;  // 0: one of the products below lies in the middle
     auto scaled = [&](uint4 x) __attribute__((always_inline)) {
         float v[E::kQ];
 #pragma unroll

@@ -173,3 +173,27 @@ def test_value_network_of_many_rows_with_trained_like_weights(m, net):
         err = np.abs(_f64(v[k])[rows] - want)
         assert np.all(err <= bound), (k, np.max(err / bound))
     tr.close()
+
+
+@pytest.mark.parametrize("mnk", [(1, 64, 96), (40, 24, 96), (300, 500, 700), (17000, 96, 160)])
+def test_column_blocks_of_one_buffer(m, mnk):
+    """x and out side by side in one buffer: taken, and equal to separate ones;
+    one column over the border: refused."""
+    import torch
+    M, N, K = mnk
+    buf = torch.zeros((M, K + N + 5), device=dev())
+    buf[:, :K] = _values(5, M, K).float()
+    x, y = buf[:, :K], buf[:, K:K + N]
+    b = _quantized(m, _values(6, N, K).float())
+    ws = m.mx4_matmul_workspace(M, N, K)
+    want = torch.zeros((M, N), device=dev())
+    m.mx4_linear(x.clone(), b, want, ws)
+    before = x.clone()
+    m.mx4_linear(x, b, y, ws)
+    sync()
+    assert torch.equal(y, want) and torch.equal(x, before) and int(buf[:, K + N:].count_nonzero()) == 0
+    with pytest.raises(m.IqlhError, match="share memory"):
+        m.mx4_linear(x, b, buf[:, K - 1:K - 1 + N], ws)
+    region = torch.zeros(max(want.nbytes, ws.numel()), dtype=torch.uint8, device=dev())
+    with pytest.raises(m.IqlhError, match="share memory"):
+        m.mx4_linear(x, b, region[:want.nbytes].view(torch.float32).view(M, N), region[:ws.numel()])
