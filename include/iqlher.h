@@ -618,6 +618,147 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
                            float gamma, float* out_target, void* workspace, size_t workspace_bytes,
                            void* stream);
 
+/* ------------------------------------------------------------------------
+ * Loss of a policy over a large set of discrete actions, and its gradients: the
+ * softmax cross entropy of a linear head on the actions taken in a batch, with the
+ * batch's importance weights.  The logits are never held in memory.
+ *   z = hidden weight^T + bias,  lse[r] = log sum_v exp z[r][v],
+ *   nll[r] = lse[r] - z[r][taken[r]]  (minus the log-probability of the action),
+ *   loss = scale sum_r row_weights[r] nll[r].
+ *
+ *   hidden   device [rows][ld_hidden], weight device [actions][ld_weight], both of
+ *            `dtype` (IQLH_F32, IQLH_BF16, IQLH_F16), `dim` columns, aligned to
+ *            their element.
+ *   bias     device [actions] f32 or NULL (0).  Minus infinity: an action that is
+ *            never taken, probability 0.
+ *   taken    device [rows] int32.  -1: a row without an action; it adds nothing to
+ *            the loss or the gradients (nll 0).  Others outside [0, actions) count as
+ *            -1 and set IQLH_FLAG_BAD_INDEX.
+ *   row_weights  device [rows] f32 or NULL (1).  A row of weight 0 adds nothing,
+ *            whatever its nll is.
+ *   scale    of the loss, finite (1 / rows for the mean).
+ * 1 <= rows, actions <= 2^24, 1 <= dim <= 2^14, each product of two of them at most
+ * 2^38.
+ *
+ * Products are exact and sums in binary32 for bfloat16 and binary16; binary32
+ * inputs are held in 22 bits.  Where an action taken has probability 0, nll and the
+ * loss are infinite; a row whose logits hold a NaN or plus infinity gets NaN.
+ *
+ * iqlh_policy_loss writes nll [rows] f32, lse [rows] f32 and, unless it is NULL, loss
+ * [1] f32 (from a binary64 sum); d_flags (or NULL) gets IQLH_FLAG_NONFINITE_LOSS for a
+ * loss that is not finite.
+ *
+ * iqlh_policy_loss_grad writes the gradients of that loss, given the lse that
+ * iqlh_policy_loss wrote for the same arguments:
+ *   G[r][v] = scale row_weights[r] (exp(z[r][v] - lse[r]) - [v == taken[r]]),
+ *   d_hidden = G weight   [rows][ld_d_hidden] of `dtype`,
+ *   d_weight = G^T hidden [actions][ld_d_weight] of `dtype`,
+ *   d_bias   = column sums of G [actions] f32,
+ * each of them unless it is NULL.  G is rounded to `dtype` (binary32: 22 bits) in the
+ * two products, whose sums are binary32, and not in d_bias.
+ *
+ *   workspace  device, >= iqlh_policy_loss_workspace_bytes(.., grad 1 for the gradients),
+ *              16-byte aligned, no initial contents required; calls that overlap in
+ *              time need one each.
+ * What a call writes must not share memory with anything else it takes.  The
+ * results do not depend on timing. */
+typedef struct iqlh_policy_head {
+    const void* hidden;
+    const void* weight;
+    const float* bias;
+    int64_t rows, actions, dim;
+    int64_t ld_hidden, ld_weight;
+    int32_t dtype;
+    int32_t reserved0;
+} iqlh_policy_head;
+
+int iqlh_policy_loss_workspace_bytes(int64_t rows, int64_t actions, int64_t dim, int32_t dtype, int32_t grad,
+                                     size_t* bytes);
+int iqlh_policy_loss(const iqlh_policy_head* head, const int32_t* taken, const float* row_weights, double scale,
+                     float* nll, float* lse, float* loss, int32_t* d_flags, void* workspace,
+                     size_t workspace_bytes, void* stream);
+int iqlh_policy_loss_grad(const iqlh_policy_head* head, const int32_t* taken, const float* row_weights,
+                          double scale, const float* lse, void* d_hidden, int64_t ld_d_hidden, void* d_weight,
+                          int64_t ld_d_weight, float* d_bias, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates of weight matrices (the update rule known as Muon),
+ * over a list of matrices.
+ *
+ * With X = U / (|U|_F + eps), `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X,  (a, b, c) = (3.4445, -4.7750, 2.0315),
+ * the products on the smaller side (X^T X for matrices with more rows than
+ * columns): the singular values of U all end near 1, its singular vectors stay.
+ *
+ * A matrix set describes the list as a tensor set does above:
+ * iqlh_matrix_set_fill writes a table into host memory, the caller copies its
+ * table_bytes to the device once and puts that address into set->d_table.  The
+ * table holds the matrices' addresses; any number of calls, on any stream, may
+ * read it.
+ *   x         device [rows][ld_x] x_dtype: the updates or gradients, read only.
+ *   out       device [rows][ld_out] out_dtype: the results or the weights.
+ *   momentum  device [rows][ld_momentum] f32, or NULL in every matrix.
+ *   compute_dtype  IQLH_F16: operands of 11 bits, the result is off by about 1e-3
+ *             of its size (a bfloat16 result's own rounding is 1.7e-3); IQLH_F32: 22 bits,
+ *             about 1e-6, at up to three times the time.
+ *   host_table >= iqlh_matrix_set_bytes bytes, 16-byte aligned, and so must be
+ *             its device copy.
+ * Types are IQLH_F32, IQLH_BF16, IQLH_F16 in any mix, pointers aligned to their
+ * element, 1 <= rows, cols <= 65536, row strides >= cols, 1 <= count <= 4096.  No
+ * out or momentum may share memory with anything else of the list (rows that
+ * interleave do not).  Host only, no HIP call. */
+typedef struct iqlh_matrix {
+    const void* x;
+    void* out;
+    float* momentum;
+    int64_t rows, cols;
+    int64_t ld_x, ld_out, ld_momentum;
+    int32_t x_dtype, out_dtype;
+    int32_t compute_dtype;
+    int32_t reserved0;
+} iqlh_matrix;
+
+typedef struct iqlh_matrix_set {
+    const void* d_table;      /* device copy of the table (set by the caller)  */
+    size_t table_bytes;       /* bytes of the table to copy                    */
+    size_t workspace_bytes;   /* what iqlh_orthogonalize and iqlh_muon_step take */
+    int32_t count;            /* matrices                                      */
+    int32_t units;            /* pieces of the elementwise passes              */
+    int32_t sym_tiles, rect_tiles;  /* tiles of the products                   */
+    int32_t momentum;         /* 1 when the matrices have one                  */
+    int32_t reserved0;
+} iqlh_matrix_set;
+
+int iqlh_matrix_set_bytes(const iqlh_matrix* matrices, int32_t count, size_t* bytes);
+int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_table, size_t bytes,
+                         iqlh_matrix_set* set);
+
+/* out of every matrix = its x orthogonalised (U = x).  A matrix whose x holds a
+ * NaN or an infinity gets NaN; one of zeros gets zeros.  Momenta are not used.
+ *   steps      1 to 32 (5 is the usual choice).
+ *   eps        > 0 (1e-7 is the usual choice).
+ *   d_flags    device sticky flag word or NULL: IQLH_FLAG_NONFINITE_GRAD.
+ *   workspace  device, >= set->workspace_bytes, 16-byte aligned, no initial
+ *              contents required; calls that overlap in time need one each.
+ * The results do not depend on timing. */
+int iqlh_orthogonalize(const iqlh_matrix_set* set, int32_t steps, double eps, int32_t* d_flags,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One step of every matrix of the list: gradient x, weights out,
+ *   momentum <- mu momentum + x,
+ *   U = x + mu momentum (nesterov 1) or momentum (0),
+ *   out <- (1 - lr weight_decay) out - lr s X,
+ * with s = sqrt(max(1, rows / cols)) (IQLH_MUON_SCALE_SHAPE) or 0.2 sqrt(max(rows,
+ * cols)) (IQLH_MUON_SCALE_RMS, which gives the update Adam's usual size).  The
+ * momentum is kept in f32; the new weight is rounded once.  A matrix whose U is not
+ * finite keeps its weights and its momentum (IQLH_FLAG_NONFINITE_GRAD).
+ *   lr finite, 0 <= mu < 1, weight_decay finite; every matrix has a momentum. */
+typedef enum { IQLH_MUON_SCALE_SHAPE = 0, IQLH_MUON_SCALE_RMS = 1 } iqlh_muon_scale;
+int iqlh_muon_step(const iqlh_matrix_set* set, double lr, double mu, int32_t nesterov, double weight_decay,
+                   int32_t scale, int32_t steps, double eps, int32_t* d_flags, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
 /* Thread-local text of the last error returned on this thread ("" if none). */
 const char* iqlh_last_error(void);
 

@@ -24,6 +24,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 OK, EINVAL, ESHAPE, ENOMEM, EHIP, ENONFINITE = 0, -1, -2, -3, -4, -5
 F32, BF16, F16 = 0, 1, 2
 NORM_L2, NORM_MAX = 0, 1
+MUON_SCALE_SHAPE, MUON_SCALE_RMS = 0, 1
 HER_FINAL, HER_FUTURE, HER_RANDOM = 0, 1, 2
 FLAG_NONFINITE_GRAD, FLAG_BAD_INDEX, FLAG_NONFINITE_LOSS, FLAG_NONFINITE_STATE = 0x1, 0x2, 0x4, 0x8
 MAX_SOURCES = 8
@@ -81,6 +82,23 @@ class TensorSetStruct(ctypes.Structure):
 
 class Mx4Struct(ctypes.Structure):
     _fields_ = [("codes", _p), ("scales", _p), ("rows", _i64), ("cols", _i64)]
+
+
+class PolicyHeadStruct(ctypes.Structure):
+    _fields_ = [("hidden", _p), ("weight", _p), ("bias", _p), ("rows", _i64), ("actions", _i64), ("dim", _i64),
+                ("ld_hidden", _i64), ("ld_weight", _i64), ("dtype", _i32), ("reserved0", _i32)]
+
+
+class MatrixStruct(ctypes.Structure):
+    _fields_ = [("x", _p), ("out", _p), ("momentum", _p), ("rows", _i64), ("cols", _i64), ("ld_x", _i64),
+                ("ld_out", _i64), ("ld_momentum", _i64), ("x_dtype", _i32), ("out_dtype", _i32),
+                ("compute_dtype", _i32), ("reserved0", _i32)]
+
+
+class MatrixSetStruct(ctypes.Structure):
+    _fields_ = [("d_table", _p), ("table_bytes", ctypes.c_size_t), ("workspace_bytes", ctypes.c_size_t),
+                ("count", _i32), ("units", _i32), ("sym_tiles", _i32), ("rect_tiles", _i32), ("momentum", _i32),
+                ("reserved0", _i32)]
 
 
 def _sig(name, res, args):
@@ -152,6 +170,21 @@ _lib_forward_mx4_ws = _sig("iql_forward_values_mx4_workspace_bytes", _i32, [_p, 
                                                                             ctypes.POINTER(ctypes.c_size_t)])
 _lib_forward_mx4 = _sig("iql_forward_values_mx4", _i32, [_p, _p, _i32, _i64, _i32, _p, _p, _p, _f, _p, _p,
                                                          ctypes.c_size_t, _p])
+_lib_policy_ws = _sig("iqlh_policy_loss_workspace_bytes", _i32, [_i64, _i64, _i64, _i32, _i32,
+                                                                 ctypes.POINTER(ctypes.c_size_t)])
+_lib_policy_loss = _sig("iqlh_policy_loss", _i32, [ctypes.POINTER(PolicyHeadStruct), _p, _p, ctypes.c_double, _p, _p, _p,
+                                                   _p, _p, ctypes.c_size_t, _p])
+_lib_policy_grad = _sig("iqlh_policy_loss_grad", _i32, [ctypes.POINTER(PolicyHeadStruct), _p, _p, ctypes.c_double, _p, _p,
+                                                        _i64, _p, _i64, _p, _p, ctypes.c_size_t, _p])
+_lib_matrix_bytes = _sig("iqlh_matrix_set_bytes", _i32, [ctypes.POINTER(MatrixStruct), _i32,
+                                                         ctypes.POINTER(ctypes.c_size_t)])
+_lib_matrix_fill = _sig("iqlh_matrix_set_fill", _i32, [ctypes.POINTER(MatrixStruct), _i32, _p, ctypes.c_size_t,
+                                                       ctypes.POINTER(MatrixSetStruct)])
+_lib_orthogonalize = _sig("iqlh_orthogonalize", _i32, [ctypes.POINTER(MatrixSetStruct), _i32, ctypes.c_double, _p, _p,
+                                                       ctypes.c_size_t, _p])
+_lib_muon_step = _sig("iqlh_muon_step", _i32, [ctypes.POINTER(MatrixSetStruct), ctypes.c_double, ctypes.c_double, _i32,
+                                               ctypes.c_double, _i32, _i32, ctypes.c_double, _p, _p, ctypes.c_size_t,
+                                               _p])
 _lib_last_error = _sig("iqlh_last_error", ctypes.c_char_p, [])
 
 
@@ -652,6 +685,160 @@ def iql_forward_values_mx4(h, next_states, batch, out_v, workspace, rewards=None
                             workspace.numel() * workspace.element_size(),
                             _stream_of(stream, index, next_states, out_v, workspace, rewards, dones, out_target)),
            "iql_forward_values_mx4")
+
+
+# -------------------------------------------- policy loss over many actions
+def policy_loss_workspace(rows, actions, dim, dtype, grad=False, device=None):
+    """A workspace for policy_loss calls of these sizes and (grad) policy_loss_grad
+    calls too."""
+    out = ctypes.c_size_t()
+    _need(dtype in _DTYPES, f"{dtype} is none of float32, bfloat16, float16")
+    size = 0
+    for g in (0, 1) if grad else (0,):
+        _check(_lib_policy_ws(rows, actions, dim, _DTYPES[dtype], g, ctypes.byref(out)), "iqlh_policy_loss_workspace_bytes")
+        size = max(size, out.value)
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace):
+    """(head, scale, device, device index) of the arguments both calls share."""
+    device = hidden.device
+    index = _need_current(device)
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden and weight must be matrices")
+    rows, dim = hidden.shape
+    actions = weight.shape[0]
+    dt, ldh = _matrix(hidden, rows, dim, device, "hidden")
+    wdt, ldw = _matrix(weight, actions, dim, device, "weight")
+    if dt != wdt:
+        raise ValueError(f"hidden is {hidden.dtype}, weight {weight.dtype}")
+    if taken.dtype != torch.int32 or not taken.is_contiguous() or taken.numel() != rows or taken.device != device:
+        raise ValueError(f"taken must be a contiguous int32 tensor of {rows} elements on {device}")
+    if bias is not None:
+        _need_f32(bias, actions, device, "bias")
+    if row_weights is not None:
+        _need_f32(row_weights, rows, device, "row_weights")
+    head = PolicyHeadStruct(hidden.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), rows, actions,
+                            dim, ldh, ldw, dt)
+    return head, (1.0 / rows if scale is None else scale), device, index
+
+
+def policy_loss(hidden, weight, taken, out_nll, out_lse, workspace, bias=None, row_weights=None, scale=None,
+                out_loss=None, flags=None, stream=None):
+    """Softmax cross entropy of the actions `taken` [rows] int32 under the logits hidden [rows,
+    dim] weight [actions, dim]^T + bias: minus the log-probabilities, the rows' log-sum-exp and
+    scale (default 1 / rows) sum row_weights nll into out_loss."""
+    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace)
+    _need_f32(out_nll, head.rows, device, "out_nll")
+    _need_f32(out_lse, head.rows, device, "out_lse")
+    if out_loss is not None:
+        _need_f32(out_loss, 1, device, "out_loss")
+    _need_aux(device, workspace, flags)
+    _check(_lib_policy_loss(ctypes.byref(head), taken.data_ptr(), _ptr(row_weights), scale, out_nll.data_ptr(),
+                            out_lse.data_ptr(), _ptr(out_loss), _ptr(flags), workspace.data_ptr(), workspace.nbytes,
+                            _stream_of(stream, index, hidden, weight, taken, bias, row_weights, out_nll, out_lse, out_loss,
+                                       flags, workspace)), "iqlh_policy_loss")
+
+
+def policy_loss_grad(hidden, weight, taken, lse, workspace, bias=None, row_weights=None, scale=None, d_hidden=None,
+                     d_weight=None, d_bias=None, stream=None):
+    """Gradients of policy_loss's loss, given the lse that it wrote for the same arguments: d_hidden
+    and d_weight of the inputs' type, d_bias [actions] float32, each unless it is None."""
+    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace)
+    _need_f32(lse, head.rows, device, "lse")
+    ldh = ldw = 0
+    if d_hidden is not None:
+        dt, ldh = _matrix(d_hidden, head.rows, head.dim, device, "d_hidden")
+        _need(dt == head.dtype, "d_hidden must have the type of hidden")
+    if d_weight is not None:
+        dt, ldw = _matrix(d_weight, head.actions, head.dim, device, "d_weight")
+        _need(dt == head.dtype, "d_weight must have the type of weight")
+    if d_bias is not None:
+        _need_f32(d_bias, head.actions, device, "d_bias")
+    _need_aux(device, workspace, None)
+    _check(_lib_policy_grad(ctypes.byref(head), taken.data_ptr(), _ptr(row_weights), scale, lse.data_ptr(),
+                            _ptr(d_hidden), ldh, _ptr(d_weight), ldw, _ptr(d_bias), workspace.data_ptr(),
+                            workspace.nbytes,
+                            _stream_of(stream, index, hidden, weight, taken, bias, row_weights, lse, d_hidden, d_weight,
+                                       d_bias, workspace)), "iqlh_policy_loss_grad")
+
+
+# ------------------------------------- orthogonalised updates of matrices
+class MatrixSet:
+    """Weight matrices and their updates for any number of orthogonalize /
+    muon_step calls: x (updates or gradients, read) and out (results or weights), lists
+    of [rows, cols] tensors (float32, bfloat16, float16 in any mix, rows may be
+    strided), and with `momentum` a float32 one each.  compute_dtype: F16 or F32 for all of
+    them, by default F16 where out is bfloat16 and F32 elsewhere.  Keeps the tensors'
+    memory and goes by it, as a TensorSet does."""
+
+    def __init__(self, x, out, momentum=None, compute_dtype=None):
+        self.x, self.out = list(x), list(out)
+        self.momentum = None if momentum is None else list(momentum)
+        k = len(self.x)
+        _need(k > 0, "MatrixSet needs at least one matrix")
+        _need(len(self.out) == k and (momentum is None or len(self.momentum) == k),
+              "x, out and momentum must be lists of the same length")
+        _need(compute_dtype in (None, F16, F32), "compute_dtype must be F16 or F32")
+        self.device = self.x[0].device
+        _need_current(self.device)
+        entries = (MatrixStruct * k)()
+        for i in range(k):
+            _need(self.x[i].dim() == 2, f"x[{i}] is no matrix")
+            rows, cols = self.x[i].shape
+            e = entries[i]
+            e.x, e.out, e.rows, e.cols = self.x[i].data_ptr(), self.out[i].data_ptr(), rows, cols
+            e.x_dtype, e.ld_x = _matrix(self.x[i], rows, cols, self.device, f"x[{i}]")
+            e.out_dtype, e.ld_out = _matrix(self.out[i], rows, cols, self.device, f"out[{i}]")
+            if momentum is not None:
+                dt, e.ld_momentum = _matrix(self.momentum[i], rows, cols, self.device, f"momentum[{i}]")
+                _need(dt == F32, f"momentum[{i}] must be float32")
+                e.momentum = self.momentum[i].data_ptr()
+            e.compute_dtype = compute_dtype if compute_dtype is not None else F16 if e.out_dtype == BF16 else F32
+        # what the table's addresses lie in, should t.data be replaced
+        self._memory = [t.detach() for t in (*self.x, *self.out, *(self.momentum or []))]
+        need = ctypes.c_size_t()
+        _check(_lib_matrix_bytes(entries, k, ctypes.byref(need)), "iqlh_matrix_set_bytes")
+        host = torch.empty(need.value + 16, dtype=torch.uint8)
+        lead = -host.data_ptr() % 16
+        host = host[lead:lead + need.value]
+        self.struct = MatrixSetStruct()
+        _check(_lib_matrix_fill(entries, k, host.data_ptr(), need.value, ctypes.byref(self.struct)),
+               "iqlh_matrix_set_fill")
+        # a copy from pageable memory: complete when it returns, for any stream
+        self.table = host[:self.struct.table_bytes].to(self.device)
+        self._streams = {_stream_of(None, self.device.index)}
+        self.struct.d_table = self.table.data_ptr()
+        self.ref = ctypes.byref(self.struct)
+        self.count = k
+
+    _used_on = TensorSet._used_on
+
+
+def orthogonalize_workspace(matrix_set):
+    """A workspace for orthogonalize / muon_step calls on the set, on any stream."""
+    return torch.empty(matrix_set.struct.workspace_bytes, dtype=torch.uint8, device=matrix_set.device)
+
+
+def orthogonalize(matrix_set, workspace, steps=5, eps=1e-7, flags=None, stream=None):
+    """out of every matrix of the set = its x with all singular values near 1."""
+    s = matrix_set
+    index = _need_current(s.device)
+    _need_aux(s.device, workspace, flags)
+    _check(_lib_orthogonalize(s.ref, steps, eps, _ptr(flags), workspace.data_ptr(), workspace.nbytes,
+                              s._used_on(_stream_of(stream, index, flags, workspace))), "iqlh_orthogonalize")
+
+
+def muon_step(matrix_set, workspace, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=MUON_SCALE_SHAPE,
+              steps=5, eps=1e-7, flags=None, stream=None):
+    """One step of every matrix: momentum, its orthogonalised update, weights (out)."""
+    s = matrix_set
+    index = _need_current(s.device)
+    _need_aux(s.device, workspace, flags)
+    _check(_lib_muon_step(s.ref, lr, momentum, int(nesterov), weight_decay, scale, steps, eps, _ptr(flags),
+                          workspace.data_ptr(), workspace.nbytes,
+                          s._used_on(_stream_of(stream, index, flags, workspace))), "iqlh_muon_step")
 
 
 # ------------------------------------------------------------------- HER

@@ -712,7 +712,7 @@ struct MemRows {
     __int128 at, bytes, pitch, rows;
     MemRows(const char* w, const void* p, int64_t n) : what(w), at((uintptr_t)p), bytes(p ? n : 0), pitch(bytes), rows(1) {}
     MemRows(const char* w, const void* p, int64_t r, int64_t c, int64_t ld, int es)
-        : what(w), at((uintptr_t)p), bytes((__int128)c * es), pitch((__int128)ld * es), rows(r) {
+        : what(w), at((uintptr_t)p), bytes(p ? (__int128)c * es : 0), pitch((__int128)ld * es), rows(r) {
         if (pitch != bytes) return;
         bytes *= r;  // no gaps: one row
         pitch = bytes;
@@ -1118,6 +1118,297 @@ int iql_aux_step_phase_stamps(iql_handle h, const iqlh_her_step* her, const void
                                    out_loss, out_grad_norm, p.budget ? &p.ba : nullptr, (hipStream_t)stream, nullptr,
                                    nullptr, d_stamps);
     if (e != hipSuccess) return hip_fail(e, "iql_aux_step_phase_stamps launch");
+    return IQLH_OK;
+}
+
+// -------------------------------------------- policy loss over many actions
+static int check_policy_sizes(const char* who, int64_t rows, int64_t actions, int64_t dim, int32_t dtype) {
+    const int64_t top = (int64_t)1 << 24, most = (int64_t)1 << 38;
+    if (!dtype_bytes(dtype)) return fail(IQLH_EINVAL, "%s: dtype %d is no float type", who, dtype);
+    if (rows < 1 || rows > top || actions < 1 || actions > top || dim < 1 || dim > 1 << 14)
+        return fail(IQLH_ESHAPE, "%s: %lld rows, %lld actions, dim %lld: must be in [1, 2^24], [1, 2^24], [1, 2^14]", who,
+                    (long long)rows, (long long)actions, (long long)dim);
+    if (rows * actions > most || rows * dim > most || actions * dim > most)
+        return fail(IQLH_ESHAPE, "%s: a product of two sizes is above 2^38", who);
+    return IQLH_OK;
+}
+
+int iqlh_policy_loss_workspace_bytes(int64_t rows, int64_t actions, int64_t dim, int32_t dtype, int32_t grad,
+                                     size_t* bytes) {
+    const char* who = "iqlh_policy_loss_workspace_bytes";
+    if (!bytes) return fail(IQLH_EINVAL, "%s: bytes is NULL", who);
+    int rc = check_policy_sizes(who, rows, actions, dim, dtype);
+    if (rc) return rc;
+    if (grad != 0 && grad != 1) return fail(IQLH_EINVAL, "%s: grad must be 0 or 1", who);
+    *bytes = policy_plan(rows, actions, dim, dtype, grad != 0).bytes;
+    return IQLH_OK;
+}
+
+static int make_policy_args(const char* who, const iqlh_policy_head* q, const int32_t* taken, const float* row_weights,
+                            double scale, bool grad, void* workspace, size_t workspace_bytes, PolicyArgs* a) {
+    if (!q || !taken) return fail(IQLH_EINVAL, "%s: NULL argument", who);
+    int rc = check_policy_sizes(who, q->rows, q->actions, q->dim, q->dtype);
+    if (!rc) rc = check_float_matrix(who, q->hidden, q->dtype, q->ld_hidden, q->dim);
+    if (!rc) rc = check_float_matrix(who, q->weight, q->dtype, q->ld_weight, q->dim);
+    if (rc) return rc;
+    if (!std::isfinite(scale)) return fail(IQLH_EINVAL, "%s: scale must be finite", who);
+    if (!workspace || ((uintptr_t)workspace & 15u)) return fail(IQLH_EINVAL, "%s: workspace NULL or not 16-byte aligned", who);
+    const size_t need = policy_plan(q->rows, q->actions, q->dim, q->dtype, grad).bytes;
+    if (workspace_bytes < need) return fail(IQLH_EINVAL, "%s: workspace too small: %zu < %zu", who, workspace_bytes, need);
+    std::memset(a, 0, sizeof(*a));
+    a->h = PolicyMat{q->hidden, q->rows, q->dim, q->ld_hidden, q->dtype};
+    a->w = PolicyMat{q->weight, q->actions, q->dim, q->ld_weight, q->dtype};
+    a->bias = q->bias, a->taken = taken, a->row_weights = row_weights, a->scale = scale, a->workspace = workspace;
+    return IQLH_OK;
+}
+static MemRows rows_of(const char* what, const PolicyMat& q) {
+    return MemRows(what, q.p, q.rows, q.cols, q.ld, dtype_bytes(q.dtype));
+}
+
+int iqlh_policy_loss(const iqlh_policy_head* head, const int32_t* taken, const float* row_weights, double scale,
+                     float* nll, float* lse, float* loss, int32_t* d_flags, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    const char* who = "iqlh_policy_loss";
+    PolicyArgs a;
+    int rc = make_policy_args(who, head, taken, row_weights, scale, false, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    if (!nll || !lse) return fail(IQLH_EINVAL, "%s: nll or lse is NULL", who);
+    const int64_t n = a.h.rows * 4;
+    rc = check_apart(who, {MemRows("nll", nll, n), MemRows("lse", lse, n), MemRows("loss", loss, 4), MemRows("the flags", d_flags, 4),
+                           MemRows("the workspace", workspace, (int64_t)workspace_bytes)},
+                     {rows_of("hidden", a.h), rows_of("weight", a.w), MemRows("bias", a.bias, a.w.rows * 4),
+                      MemRows("taken", taken, n), MemRows("row_weights", row_weights, n)});
+    if (rc) return rc;
+    a.nll = nll, a.lse_out = lse, a.loss = loss, a.flags = d_flags;
+    hipError_t e = launch_policy_loss(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_policy_loss launch");
+    return IQLH_OK;
+}
+
+int iqlh_policy_loss_grad(const iqlh_policy_head* head, const int32_t* taken, const float* row_weights, double scale,
+                          const float* lse, void* d_hidden, int64_t ld_d_hidden, void* d_weight, int64_t ld_d_weight,
+                          float* d_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* who = "iqlh_policy_loss_grad";
+    PolicyArgs a;
+    int rc = make_policy_args(who, head, taken, row_weights, scale, true, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    if (!lse) return fail(IQLH_EINVAL, "%s: lse is NULL", who);
+    if (!d_hidden && !d_weight && !d_bias) return fail(IQLH_EINVAL, "%s: no gradient is asked for", who);
+    const PolicyMat dh{d_hidden, a.h.rows, a.h.cols, ld_d_hidden, a.h.dtype}, dw{d_weight, a.w.rows, a.w.cols, ld_d_weight, a.w.dtype};
+    if (d_hidden) rc = check_float_matrix(who, d_hidden, dh.dtype, dh.ld, dh.cols);
+    if (!rc && d_weight) rc = check_float_matrix(who, d_weight, dw.dtype, dw.ld, dw.cols);
+    if (rc) return rc;
+    const int64_t n = a.h.rows * 4;
+    rc = check_apart(who, {rows_of("d_hidden", dh), rows_of("d_weight", dw), MemRows("d_bias", d_bias, a.w.rows * 4),
+                           MemRows("the workspace", workspace, (int64_t)workspace_bytes)},
+                     {rows_of("hidden", a.h), rows_of("weight", a.w), MemRows("bias", a.bias, a.w.rows * 4),
+                      MemRows("taken", taken, n), MemRows("row_weights", row_weights, n), MemRows("lse", lse, n)});
+    if (rc) return rc;
+    a.lse_in = lse, a.d_hidden = d_hidden, a.d_weight = d_weight, a.d_bias = d_bias, a.ld_dh = ld_d_hidden, a.ld_dw = ld_d_weight;
+    hipError_t e = launch_policy_loss_grad(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_policy_loss_grad launch");
+    return IQLH_OK;
+}
+
+// ------------------------------------- orthogonalised updates of matrices
+namespace {
+int32_t pad64(int64_t n) { return (int32_t)((n + 63) / 64 * 64); }
+struct OrthoCounts {
+    int64_t units, sym, rect;
+};
+// pieces and tiles of one matrix
+OrthoCounts ortho_counts(const iqlh_matrix& m, OrthoMat* q) {
+    const int32_t rp = pad64(m.rows), cp = pad64(m.cols), kp = rp < cp ? rp : cp;
+    // pieces of 8192 elements or more, 512 of them at most: their sums are added by every piece's workgroup
+    int32_t ur = (8192 + cp - 1) / cp;
+    if (ur < (rp + 511) / 512) ur = (rp + 511) / 512;
+    const int64_t t = kOrthoTile, ts = (kp + t - 1) / t;
+    q->rows = (int32_t)m.rows, q->cols = (int32_t)m.cols, q->rows_pad = rp, q->cols_pad = cp, q->k_pad = kp;
+    q->unit_rows = ur, q->units = (rp + ur - 1) / ur;
+    return OrthoCounts{q->units, ts * (ts + 1) / 2, ((rp + t - 1) / t) * ((cp + t - 1) / t)};
+}
+struct MatrixRange {
+    uint64_t begin, end;
+    int64_t cols, ld;
+    int32_t matrix, what, es, reserved;  // what: 0 x, 1 out, 2 momentum
+};
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+}  // namespace
+
+static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count, OrthoCounts* all) {
+    if (!ms) return fail(IQLH_EINVAL, "%s: NULL argument", who);
+    if (count < 1 || count > 4096) return fail(IQLH_EINVAL, "%s: count must be in [1, 4096]", who);
+    *all = OrthoCounts{0, 0, 0};
+    for (int i = 0; i < count; ++i) {
+        const iqlh_matrix& m = ms[i];
+        if (m.rows < 1 || m.rows > 65536 || m.cols < 1 || m.cols > 65536)
+            return fail(IQLH_ESHAPE, "%s: matrix %d of %lld x %lld, sizes must be in [1, 65536]", who, i, (long long)m.rows,
+                        (long long)m.cols);
+        if (!dtype_bytes(m.x_dtype) || !dtype_bytes(m.out_dtype))
+            return fail(IQLH_EINVAL, "%s: matrix %d has a type that is no float type", who, i);
+        if (m.compute_dtype != IQLH_F16 && m.compute_dtype != IQLH_F32)
+            return fail(IQLH_EINVAL, "%s: matrix %d: compute_dtype must be IQLH_F16 or IQLH_F32", who, i);
+        OrthoMat q;
+        const OrthoCounts c = ortho_counts(m, &q);
+        all->units += c.units, all->sym += c.sym, all->rect += c.rect;
+    }
+    if (all->units > 1 << 22 || all->sym > 1 << 22 || all->rect > 1 << 22)
+        return fail(IQLH_ESHAPE, "%s: the list is more than one launch takes", who);
+    return IQLH_OK;
+}
+
+int iqlh_matrix_set_bytes(const iqlh_matrix* matrices, int32_t count, size_t* bytes) {
+    if (!bytes) return fail(IQLH_EINVAL, "iqlh_matrix_set_bytes: bytes is NULL");
+    OrthoCounts n;
+    int rc = check_matrices("iqlh_matrix_set_bytes", matrices, count, &n);
+    if (rc) return rc;
+    const size_t table = up16(sizeof(OrthoMat) * (size_t)count + sizeof(OrthoTile) * (size_t)(n.units + n.sym + n.rect));
+    // fill sorts the address ranges where the table comes to lie, before it writes it
+    const size_t ranges = sizeof(MatrixRange) * 3 * (size_t)count;
+    *bytes = table > ranges ? table : ranges;
+    return IQLH_OK;
+}
+
+// Writes the tiles of one product of matrix i, mt x nt of them or (sym) those on and below
+// the diagonal: in blocks of 8 x 8, whose operands an L2 holds, and eight runs of blocks in
+// turn, since consecutive workgroups go to different XCDs.
+static OrthoTile* put_tiles(OrthoTile* to, int32_t i, int64_t mt, int64_t nt, bool sym, int64_t total) {
+    const int64_t per = total / 8, rest = total % 8;
+    int64_t at = 0, run = 0, in_run = 0;
+    for (int64_t bm = 0; bm < mt; bm += 8)
+        for (int64_t bn = 0; bn < (sym ? bm + 1 : nt); bn += 8)
+            for (int64_t m = bm; m < mt && m < bm + 8; ++m)
+                for (int64_t n = bn; n < nt && n < bn + 8 && (!sym || n <= m); ++n) {
+                    // place `at` of run `run`: runs of `per` tiles, the first `rest` of them one longer
+                    to[in_run * 8 + run] = OrthoTile{i, (uint16_t)m, (uint16_t)n};
+                    ++at;
+                    if (++in_run == per + (run < rest)) in_run = 0, ++run;
+                }
+    return to + at;
+}
+
+int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_table, size_t bytes,
+                         iqlh_matrix_set* set) {
+    const char* who = "iqlh_matrix_set_fill";
+    OrthoCounts n;
+    size_t need = 0;
+    int rc = check_matrices(who, matrices, count, &n);
+    if (rc) return rc;
+    if (!host_table || !set) return fail(IQLH_EINVAL, "%s: NULL argument", who);
+    iqlh_matrix_set_bytes(matrices, count, &need);
+    if (bytes < need) return fail(IQLH_EINVAL, "%s: table of %zu bytes, needs %zu", who, bytes, need);
+    if ((uintptr_t)host_table & 15u) return fail(IQLH_EINVAL, "%s: table not 16-byte aligned", who);
+    MatrixRange* range = (MatrixRange*)host_table;
+    int nr = 0;
+    for (int i = 0; i < count; ++i) {
+        const iqlh_matrix& m = matrices[i];
+        if (!m.x || !m.out) return fail(IQLH_EINVAL, "%s: matrix %d has a NULL address", who, i);
+        if (!m.momentum != !matrices[0].momentum) return fail(IQLH_EINVAL, "%s: all matrices have a momentum or none", who);
+        const void* p[3] = {m.x, m.out, m.momentum};
+        const int64_t ld[3] = {m.ld_x, m.ld_out, m.ld_momentum};
+        const int es[3] = {dtype_bytes(m.x_dtype), dtype_bytes(m.out_dtype), 4};
+        for (int k = 0; k < (m.momentum ? 3 : 2); ++k) {
+            if ((uintptr_t)p[k] % es[k]) return fail(IQLH_EINVAL, "%s: matrix %d not aligned to its element", who, i);
+            if (ld[k] < m.cols || ld[k] > (int64_t)1 << 40)
+                return fail(IQLH_EINVAL, "%s: matrix %d: row stride %lld below %lld columns", who, i, (long long)ld[k],
+                            (long long)m.cols);
+            const uint64_t at = (uint64_t)(uintptr_t)p[k];
+            range[nr++] = MatrixRange{at, at + ((uint64_t)(m.rows - 1) * ld[k] + m.cols) * es[k], m.cols, ld[k], i, k, es[k], 0};
+        }
+    }
+    std::sort(range, range + nr, [](const MatrixRange& a, const MatrixRange& b) { return a.begin < b.begin; });
+    auto rows_of = [&](const MatrixRange& r) {
+        return MemRows("", (const void*)(uintptr_t)r.begin, matrices[r.matrix].rows, r.cols, r.ld, r.es);
+    };
+    for (int i = 0; i < nr; ++i)
+        for (int j = i + 1; j < nr && range[j].begin < range[i].end; ++j)
+            if ((range[i].what || range[j].what) && share_memory(rows_of(range[i]), rows_of(range[j]))) {
+                static const char* const names[3] = {"x", "out", "momentum"};
+                return fail(IQLH_EINVAL, "%s: %s of matrix %d and %s of matrix %d share memory", who, names[range[i].what],
+                            range[i].matrix, names[range[j].what], range[j].matrix);
+            }
+    OrthoMat* mats = (OrthoMat*)host_table;
+    OrthoTile* units = (OrthoTile*)(mats + count);
+    OrthoTile* sym = units + n.units;
+    OrthoTile* rect = sym + n.sym;
+    size_t at = up16(sizeof(double) * (size_t)n.units + sizeof(int32_t) * (size_t)count);
+    int32_t unit0 = 0;
+    for (int i = 0; i < count; ++i) {
+        const iqlh_matrix& m = matrices[i];
+        OrthoMat q;
+        std::memset(&q, 0, sizeof(q));
+        const OrthoCounts c = ortho_counts(m, &q);
+        q.x = (uint64_t)(uintptr_t)m.x, q.out = (uint64_t)(uintptr_t)m.out, q.momentum = (uint64_t)(uintptr_t)m.momentum;
+        q.ld_x = m.ld_x, q.ld_out = m.ld_out, q.ld_momentum = m.ld_momentum;
+        q.x_dtype = m.x_dtype, q.out_dtype = m.out_dtype, q.planes = m.compute_dtype == IQLH_F32 || m.rows < 64 || m.cols < 64 ? 2 : 1;
+        q.unit0 = unit0;
+        const size_t x = (size_t)q.rows_pad * q.cols_pad * 2 * q.planes, s = (size_t)q.k_pad * q.k_pad * 2 * q.planes;
+        q.x_at[0] = (int64_t)at, q.x_at[1] = (int64_t)(at + x), q.gram_at = (int64_t)(at + 2 * x), q.poly_at = (int64_t)(at + 2 * x + s);
+        at += 2 * (x + s);
+        mats[i] = q;
+        for (int32_t u = 0; u < q.units; ++u) *units++ = OrthoTile{i, (uint16_t)u, 0};
+        unit0 += q.units;
+        const int64_t nt = (q.cols_pad + kOrthoTile - 1) / kOrthoTile, mt = (q.rows_pad + kOrthoTile - 1) / kOrthoTile;
+        sym = put_tiles(sym, i, (q.k_pad + kOrthoTile - 1) / kOrthoTile, mt, true, c.sym);
+        rect = put_tiles(rect, i, mt, nt, false, c.rect);
+    }
+    std::memset(set, 0, sizeof(*set));
+    set->table_bytes = up16((size_t)((char*)rect - (char*)host_table));
+    set->workspace_bytes = at;
+    set->count = count;
+    set->units = (int32_t)n.units, set->sym_tiles = (int32_t)n.sym, set->rect_tiles = (int32_t)n.rect;
+    set->momentum = matrices[0].momentum != nullptr;
+    return IQLH_OK;
+}
+
+static int make_ortho_args(const char* who, const iqlh_matrix_set* set, int32_t steps, double eps, int32_t* d_flags,
+                           void* workspace, size_t workspace_bytes, OrthoArgs* a) {
+    if (!set) return fail(IQLH_EINVAL, "%s: set is NULL", who);
+    if (!set->d_table || set->count < 1) return fail(IQLH_EINVAL, "%s: set->d_table is NULL", who);
+    if ((uintptr_t)set->d_table & 15u) return fail(IQLH_EINVAL, "%s: set->d_table not 16-byte aligned", who);
+    if (steps < 1 || steps > 32) return fail(IQLH_EINVAL, "%s: steps must be in [1, 32]", who);
+    if (!(eps > 0.0) || !std::isfinite(eps)) return fail(IQLH_EINVAL, "%s: eps must be > 0", who);
+    if (!workspace || ((uintptr_t)workspace & 15u)) return fail(IQLH_EINVAL, "%s: workspace NULL or not 16-byte aligned", who);
+    if (workspace_bytes < set->workspace_bytes)
+        return fail(IQLH_EINVAL, "%s: workspace too small: %zu < %zu", who, workspace_bytes, set->workspace_bytes);
+    std::memset(a, 0, sizeof(*a));
+    a->mats = (const OrthoMat*)set->d_table;
+    a->units = (const OrthoTile*)(a->mats + set->count);
+    a->sym = a->units + set->units;
+    a->rect = a->sym + set->sym_tiles;
+    a->base = (uint8_t*)workspace;
+    a->part = (double*)workspace;
+    a->ok = (int32_t*)(a->part + set->units);
+    a->nunits = set->units, a->nsym = set->sym_tiles, a->nrect = set->rect_tiles;
+    a->h.eps = eps, a->h.flags = d_flags, a->h.steps = steps;
+    return IQLH_OK;
+}
+
+int iqlh_orthogonalize(const iqlh_matrix_set* set, int32_t steps, double eps, int32_t* d_flags, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    OrthoArgs a;
+    int rc = make_ortho_args("iqlh_orthogonalize", set, steps, eps, d_flags, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    hipError_t e = launch_orthogonalize(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_orthogonalize launch");
+    return IQLH_OK;
+}
+
+int iqlh_muon_step(const iqlh_matrix_set* set, double lr, double mu, int32_t nesterov, double weight_decay, int32_t scale,
+                   int32_t steps, double eps, int32_t* d_flags, void* workspace, size_t workspace_bytes, void* stream) {
+    OrthoArgs a;
+    int rc = make_ortho_args("iqlh_muon_step", set, steps, eps, d_flags, workspace, workspace_bytes, &a);
+    if (rc) return rc;
+    if (!set->momentum) return fail(IQLH_EINVAL, "iqlh_muon_step: the matrices have no momentum");
+    if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return fail(IQLH_EINVAL, "iqlh_muon_step: lr and weight_decay must be finite");
+    if (!(mu >= 0.0 && mu < 1.0)) return fail(IQLH_EINVAL, "iqlh_muon_step: mu must be in [0, 1)");
+    if (nesterov != 0 && nesterov != 1) return fail(IQLH_EINVAL, "iqlh_muon_step: nesterov must be 0 or 1");
+    if (scale != IQLH_MUON_SCALE_SHAPE && scale != IQLH_MUON_SCALE_RMS)
+        return fail(IQLH_EINVAL, "iqlh_muon_step: unknown scale %d", scale);
+    a.h.step = 1, a.h.nesterov = nesterov, a.h.scale = scale;
+    a.h.lr = lr, a.h.mu = (float)mu, a.h.keep = (float)(1.0 - lr * weight_decay);
+    hipError_t e = launch_orthogonalize(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "iqlh_muon_step launch");
     return IQLH_OK;
 }
 

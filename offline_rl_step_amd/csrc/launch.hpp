@@ -286,6 +286,76 @@ size_t iql_mx4_workspace_bytes(const IqlDims& d, int B);
 hipError_t launch_iql_mx4_forward(const IqlDims& d, const IqlBuffers& b, const void* states, int dtype, int64_t ld,
                                   int B, const ValueOut& vo, void* workspace, hipStream_t stream);
 
+// ------------------------------------- orthogonalised updates of matrices
+// One matrix of the list; addresses as integers, *_at: byte offsets in the workspace.
+struct OrthoMat {
+    uint64_t x, out, momentum;
+    int64_t ld_x, ld_out, ld_momentum;
+    int64_t x_at[2], gram_at, poly_at;
+    int32_t rows, cols, rows_pad, cols_pad;  // padded to 64
+    int32_t k_pad;                           // the smaller side's
+    int32_t x_dtype, out_dtype, planes;
+    int32_t unit0, units, unit_rows, reserved;
+};
+static_assert(sizeof(OrthoMat) % 16 == 0, "table entry");
+struct OrthoTile {
+    int32_t mat;
+    uint16_t m, n;  // tile (units: m)
+};
+constexpr int kOrthoTile = 128;
+struct OrthoHyper {
+    double lr, eps;
+    float mu, keep;  // keep: 1 - lr weight_decay
+    int32_t* flags;
+    int32_t steps, step, nesterov, scale;  // step: with momentum and weights
+};
+struct OrthoArgs {
+    const OrthoMat* mats;
+    const OrthoTile* units;
+    const OrthoTile* sym;   // tiles of the symmetric products, m >= n
+    const OrthoTile* rect;
+    uint8_t* base;          // workspace
+    double* part;           // [nunits]
+    int32_t* ok;            // [count]
+    int32_t nunits, nsym, nrect;
+    OrthoHyper h;
+};
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);
+
+// -------------------------------------------- policy loss over many actions
+struct PolicyMat {
+    const void* p;
+    int64_t rows, cols, ld;
+    int32_t dtype;
+};
+struct PolicyArgs {
+    PolicyMat h, w;            // hidden [rows, dim], weight [actions, dim]
+    const float* bias;         // or null
+    const int32_t* taken;
+    const float* row_weights;  // or null
+    double scale;
+    float* nll;
+    float* lse_out;
+    float* loss;               // or null
+    const float* lse_in;       // gradients
+    void* d_hidden;            // or null
+    void* d_weight;            // or null
+    float* d_bias;             // or null
+    int64_t ld_dh, ld_dw;
+    int32_t* flags;
+    void* workspace;
+};
+constexpr int kAbsBlocks = 256;
+// Byte offsets in the workspace and the pieces the actions are taken in
+struct PolicyPlan {
+    size_t factors, absmax, row_factor, h, h_dw, w, part, z_taken, loss_part, g, db_part, dh_sums, dw_sums, bytes;
+    int64_t ld, piece;
+    int32_t planes, g_planes, pieces;
+};
+PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bool grad);
+hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream);
+hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream);
+
 // ------------------------------------------------------- whole step
 // One pass of the hot path in four launches:
 //   A  HER relabelling + budget source norms   (independent of each other)

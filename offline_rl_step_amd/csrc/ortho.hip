@@ -1,0 +1,239 @@
+// Orthogonalised updates of a list of weight matrices.
+//
+// For an update U [rows, cols] of the list, with X = U / (|U|_F + eps):
+//   steps times   A = X X^T,   X <- a X + (b A + c A A) X       (X X^T on the smaller side)
+// with (a, b, c) = (3.4445, -4.7750, 2.0315): every singular value s of X goes to p(s) = a s + b
+// s^3 + c s^5, which five times over takes all but the smallest of (0, 1] into about [0.68, 1.2], so
+// that X tends to U V^T of U = U S V^T.  With momentum the list's weights are updated by it:
+//   m <- mu m + g,   U = g + mu m (Nesterov) or m,   w <- (1 - lr wd) w - lr s X.
+//
+// Launches, each over all matrices of the list: norms, normalisation (and momentum), then
+// three products a step.  A and b A + c A A are symmetric: tiles on and below the
+// diagonal only, each stored in both places, half the matrix instructions.
+//
+// Operands are binary16 times 2^13, not bfloat16: |X| <= 1.2025 (p's maximum on [0, 1], and p maps [0,
+// 1.2025] into itself), |A| <= 1.45 and |b A + c A A| <= 2.81 bound every element, so binary16 holds
+// them with three bits more than bfloat16 and down to 2^-27 at full length.  Matrices
+// whose result is binary32 or binary16 are held in two planes (tile16.hpp), 22 bits.
+// p's slope at 0 is a: an error in a small singular value's direction grows up to a^5 = 485 times
+// with the value itself, which is what one plane of 11 bits leaves at about 1e-3 of the result
+// and two at 1e-6.
+#include "iqlher.h"
+#include "launch.hpp"
+#include "tile16.hpp"
+
+namespace iqlh {
+
+namespace {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kUp = 8192.f, kDown = 1.f / 8192.f;  // of every operand
+constexpr int kNT = 256;
+
+IQLH_DEV double wave_sum64(double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    return v;
+}
+IQLH_DEV double block_sum64(double v, double* red) {
+    v = wave_sum64(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kNT / kWave; ++i) s += red[i];
+    return s;
+}
+
+// Eight neighbouring elements of the update, and the momentum behind it
+IQLH_DEV void update8(const OrthoMat& q, const OrthoHyper& h, int64_t row, int col, float (&u)[8], float (&m)[8]) {
+    const int n = q.cols - col;
+    load8_of(q.x_dtype, (const void*)q.x, row * q.ld_x + col, n, u);
+    if (!h.step) return;
+    load8_of(IQLH_F32, (const void*)q.momentum, row * q.ld_momentum + col, n, m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        m[i] = fmaf(h.mu, m[i], u[i]);
+        u[i] = h.nesterov ? fmaf(h.mu, m[i], u[i]) : m[i];
+    }
+}
+
+// Sum of squares of a unit (unit_rows rows of a matrix)
+__global__ __launch_bounds__(kNT) void ortho_norm_kernel(OrthoArgs a) {
+    __shared__ double red[kNT / kWave];
+    const OrthoTile w = a.units[blockIdx.x];
+    const OrthoMat& q = a.mats[w.mat];
+    const int row0 = w.m * q.unit_rows, rows = q.rows - row0 < q.unit_rows ? q.rows - row0 : q.unit_rows;
+    const int groups = (q.cols + 7) / 8;
+    double s0 = 0.0, s1 = 0.0;
+    for (int e = threadIdx.x; e < rows * groups; e += kNT) {
+        const int row = e / groups, col = 8 * (e - row * groups);
+        float u[8], m[8];
+        update8(q, a.h, row0 + row, col, u, m);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {  // elements behind the row's end are 0
+            s0 = fma((double)u[i], (double)u[i], s0);
+            s1 = fma((double)u[i + 1], (double)u[i + 1], s1);
+        }
+    }
+    s0 = block_sum64(s0 + s1, red);
+    if (threadIdx.x == 0) a.part[blockIdx.x] = s0;
+}
+
+// X of a unit, zeros in the padding, and the momentum
+__global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
+    __shared__ double red[kNT / kWave];
+    const OrthoTile w = a.units[blockIdx.x];
+    const OrthoMat& q = a.mats[w.mat];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < q.units; i += kNT) sum += a.part[q.unit0 + i];
+    const double norm = sqrt(block_sum64(sum, red));
+    const bool ok = norm < __longlong_as_double(0x7FF0000000000000ll);
+    if (w.m == 0 && threadIdx.x == 0) {
+        a.ok[w.mat] = ok;
+        if (!ok) set_flag(a.h.flags, IQLH_FLAG_NONFINITE_GRAD);
+    }
+    const double scale = ok ? (double)kUp / (norm + a.h.eps) : 0.0;
+    const int row0 = w.m * q.unit_rows, rows = q.rows_pad - row0 < q.unit_rows ? q.rows_pad - row0 : q.unit_rows;
+    const int groups = q.cols_pad / 8;
+    uint16_t* x = (uint16_t*)(a.base + q.x_at[0]);
+    for (int e = threadIdx.x; e < rows * groups; e += kNT) {
+        const int row = row0 + e / groups, col = 8 * (e % groups);
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m[8];
+        if (ok && row < q.rows && col < q.cols) {
+            update8(q, a.h, row, col, u, m);
+            if (a.h.step) store8_of(IQLH_F32, (void*)q.momentum, row * q.ld_momentum + col, q.cols - col, m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = (float)((double)u[i] * scale);
+        }
+        put_planes(x + (int64_t)row * q.cols_pad + col, (int64_t)q.rows_pad * q.cols_pad, q.planes == 2, u);
+    }
+}
+
+// X X^T and the polynomial of it (kGram, kPoly): symmetric, tiles m >= n.
+// kApply: the next X.  kLast: the result.
+enum { kGram, kPoly, kApply, kLast };
+template <int TILE, int PHASE>
+__global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void ortho_product_kernel(OrthoArgs a, int from) {
+    typedef Tile16<TILE> T;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const OrthoTile w = (PHASE <= kPoly ? a.sym : a.rect)[blockIdx.x];
+    const OrthoMat& q = a.mats[w.mat];
+    const bool two = q.planes == 2, tall = q.rows > q.cols;
+    const int segs = two ? 3 : 1;
+    const int64_t m0 = (int64_t)w.m * TILE, n0 = (int64_t)w.n * TILE;
+    const int64_t plane_x = (int64_t)q.rows_pad * q.cols_pad, plane_s = (int64_t)q.k_pad * q.k_pad;
+    const uint16_t* x = (const uint16_t*)(a.base + q.x_at[from]);
+    uint16_t* gram = (uint16_t*)(a.base + q.gram_at);
+    uint16_t* poly = (uint16_t*)(a.base + q.poly_at);
+    mm_f16 acc[T::FA][T::FB];
+    if (PHASE == kGram) {
+        const Side16 s{x, plane_x, q.cols_pad, q.k_pad};
+        if (tall) tile_product<false, TILE, true, true>(s, s, m0, n0, 0, q.rows_pad, segs, lds, acc);
+        else tile_product<false, TILE, false, false>(s, s, m0, n0, 0, q.cols_pad, segs, lds, acc);
+    } else if (PHASE == kPoly) {
+        const Side16 s{gram, plane_s, q.k_pad, q.k_pad};
+        tile_product<false, TILE, false, false>(s, s, m0, n0, 0, q.k_pad, segs, lds, acc);
+    } else {
+        const Side16 p{poly, plane_s, q.k_pad, q.k_pad};
+        if (tall) tile_product<false, TILE, false, false>(Side16{x, plane_x, q.cols_pad, q.rows_pad}, p, m0, n0, 0, q.k_pad, segs, lds, acc);
+        else tile_product<false, TILE, false, true>(p, Side16{x, plane_x, q.cols_pad, q.cols_pad}, m0, n0, 0, q.k_pad, segs, lds, acc);
+    }
+    const int rows = PHASE <= kPoly ? q.k_pad : q.rows_pad, cols = PHASE <= kPoly ? q.k_pad : q.cols_pad;
+    bool ok = true;
+    float rate = 0.f;
+    if (PHASE == kLast) {
+        ok = a.ok[w.mat];
+        if (a.h.step) {
+            if (!ok) return;
+            const double shape = a.h.scale == IQLH_MUON_SCALE_SHAPE ? sqrt(fmax(1.0, (double)q.rows / q.cols))
+                                                                    : 0.2 * sqrt((double)(q.rows > q.cols ? q.rows : q.cols));
+            rate = (float)(a.h.lr * shape);
+        }
+    }
+    // eight neighbouring sums v of row m from column n on, as they are stored
+    auto put = [&](int m, int n, float (&v)[8]) __attribute__((always_inline)) {
+        float y[8];
+        if (PHASE == kGram) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = v[i] * kDown;
+            put_planes(gram + (int64_t)m * q.k_pad + n, plane_s, two, y);
+        } else if (PHASE == kPoly) {
+            get_planes(gram + (int64_t)m * q.k_pad + n, plane_s, two, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(kB, y[i], (kC * kDown) * v[i]);
+            put_planes(poly + (int64_t)m * q.k_pad + n, plane_s, two, y);
+        } else {
+            get_planes(x + (int64_t)m * q.cols_pad + n, plane_x, two, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = fmaf(kA, y[i], kDown * v[i]);
+            if (PHASE == kApply) {
+                put_planes((uint16_t*)(a.base + q.x_at[from ^ 1]) + (int64_t)m * q.cols_pad + n, plane_x, two, y);
+                return;
+            }
+            if (m >= q.rows || n >= q.cols) return;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = ok ? y[i] * kDown : __uint_as_float(0x7FC00000u);
+            const int64_t at = (int64_t)m * q.ld_out + n;
+            if (a.h.step) {
+                float old[8];
+                load8_of(q.out_dtype, (const void*)q.out, at, q.cols - n, old);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = fmaf(-rate, y[i], a.h.keep * old[i]);
+            }
+            store8_of(q.out_dtype, (void*)q.out, at, q.cols - n, y);
+        }
+    };
+#pragma unroll
+    for (int band = 0; band < T::BANDS; ++band) {
+        stage_band<TILE>(acc, lds, band);
+#pragma unroll 2
+        for (int c = threadIdx.x; c < T::BAND * (TILE / 8); c += T::NT) {
+            const int row = c / (TILE / 8), u = c % (TILE / 8);
+            const int m = (int)m0 + band * T::BAND + row, n = (int)n0 + 8 * u;
+            if (m >= rows || n >= cols) continue;
+            const float4 lo = *stage_at<TILE>(lds, row, 2 * u), hi = *stage_at<TILE>(lds, row, 2 * u + 1);
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            put(m, n, v);
+        }
+        if (PHASE <= kPoly && w.m != w.n) {
+#pragma unroll 2
+            for (int c = threadIdx.x; c < T::BAND / 8 * TILE; c += T::NT) {
+                const int u = c % (T::BAND / 8), col = c / (T::BAND / 8);
+                const int m = (int)m0 + band * T::BAND + 8 * u, n = (int)n0 + col;
+                if (m >= rows || n >= cols) continue;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = ((const float*)stage_at<TILE>(lds, 8 * u + i, col / 4))[col & 3];
+                put(n, m, v);
+            }
+        }
+    }
+}
+
+template <int PHASE>
+hipError_t launch_product(const OrthoArgs& a, int from, hipStream_t stream) {
+    constexpr int TILE = kOrthoTile, bytes = Tile16<TILE>::LDS;
+    auto kernel = ortho_product_kernel<TILE, PHASE>;
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    hipLaunchKernelGGL(kernel, dim3(PHASE <= kPoly ? a.nsym : a.nrect), dim3(Tile16<TILE>::NT), bytes, stream, a, from);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL(ortho_norm_kernel, dim3(a.nunits), dim3(kNT), 0, stream, a);
+    hipLaunchKernelGGL(ortho_start_kernel, dim3(a.nunits), dim3(kNT), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    for (int s = 0; s < a.h.steps && e == hipSuccess; ++s) {
+        e = launch_product<kGram>(a, s & 1, stream);
+        if (e == hipSuccess) e = launch_product<kPoly>(a, s & 1, stream);
+        if (e == hipSuccess)
+            e = s + 1 < a.h.steps ? launch_product<kApply>(a, s & 1, stream) : launch_product<kLast>(a, s & 1, stream);
+    }
+    return e;
+}
+
+}  // namespace iqlh

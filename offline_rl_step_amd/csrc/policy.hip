@@ -1,0 +1,832 @@
+// Loss of a policy over many actions: softmax cross entropy of a linear head, with
+// its gradients, without the logits in memory.
+//
+//   z = H W^T + b,  lse_r = log sum_v exp z_rv,  nll_r = lse_r - z_{r, a_r},
+//   loss = s sum_r w_r nll_r,  G_rv = s w_r (exp(z_rv - lse_r) - [v = a_r]),
+//   dH = G W,  dW = G^T H,  db = column sums of G.
+//
+// Loss: tiles of z on the matrix instructions; a tile leaves the maximum and the sum of
+// exponentials of each of its rows (8 bytes for 128 or 256 logits), which a second
+// launch joins.  Gradients: for one piece of the actions after another, the
+// tiles of z again, now with lse known, leave G in 16 bits (a piece is chosen so that it
+// stays in the Infinity Cache), and two products read it: dW of the piece, and
+// dH summed over the pieces in binary32.
+//
+// Bfloat16 inputs: G is bfloat16.  Binary16 inputs: G is binary16 times a power of
+// two by the largest |w|, so that probabilities down to 1e-12 are held.  Binary32
+// inputs: H, W and G are two planes of binary16 each (tile16.hpp), times powers of two by
+// their largest elements, 22 bits.
+#include "iqlher.h"
+#include "launch.hpp"
+#include "tile16.hpp"
+
+namespace iqlh {
+
+namespace {
+
+constexpr int kNT = 256;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+constexpr float kNone = -__builtin_huge_valf();
+
+// 2^(x - m); 0 for x of minus infinity, whatever m is
+IQLH_DEV float exp_below(float x, float m) { return x == kNone ? 0.f : __builtin_amdgcn_exp2f(x - m); }
+
+// Maximum of logits times log2(e), and sum of 2^(. - maximum)
+struct Soft {
+    float m, s;
+    IQLH_DEV void join(Soft o) {
+        const float top = fmaxf(m, o.m);
+        s = s * exp_below(m, top) + o.s * exp_below(o.m, top);  // NaN stays NaN
+        m = top;
+    }
+};
+IQLH_DEV Soft soft_xor(Soft v, int lanes) {
+    v.join(Soft{__shfl_xor(v.m, lanes, kWave), __shfl_xor(v.s, lanes, kWave)});
+    return v;
+}
+
+// Factors of a call, powers of two (times the loss's scale): of sums to logits, of G as it is stored, of the gradients' sums
+struct Factors {
+    float z, g, dh, dw, db, reserved[3];
+};
+IQLH_DEV float up_to(uint32_t bits, int top) {  // 2^n that takes a finite value of these bits to [2^(top - 1), 2^top)
+    const int e = (int)(bits >> 23);            // subnormal ones count as 2^-126
+    int n = top - (e ? e - 126 : -125);
+    n = bits == 0u ? 0 : n < -126 ? -126 : n > 126 ? 126 : n;
+    return __uint_as_float((uint32_t)(n + 127) << 23);
+}
+
+// ------------------------------------------------------------ preparation
+// A row that adds nothing: no action, or none of these, or weight 0
+IQLH_DEV bool row_off(const int32_t* taken, const float* row_weights, int64_t actions, int64_t m) {
+    const int32_t t = taken[m];
+    return t < 0 || t >= actions || (row_weights && row_weights[m] == 0.f);
+}
+
+IQLH_DEV uint32_t finite_bits(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+IQLH_DEV uint32_t wave_umax(uint32_t v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        const uint32_t b = (uint32_t)__shfl_xor((int)v, o, kWave);
+        v = b > v ? b : v;
+    }
+    return v;
+}
+
+// Largest finite |x| of up to three matrices, kAbsBlocks workgroups each; of the
+// first without rows that are off where `taken` is given
+struct AbsMaxArgs {
+    PolicyMat m[3];
+    uint32_t* part;  // [3][kAbsBlocks]
+    const int32_t* taken;
+    const float* row_weights;
+    int64_t actions;
+};
+__global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
+    __shared__ uint32_t red[kNT / kWave];
+    const PolicyMat& q = a.m[blockIdx.y];
+    const bool skip = blockIdx.y == 0 && a.taken;
+    uint32_t top = 0u;
+    if (q.p) {
+        const int64_t groups = (q.cols + 7) / 8;
+        for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < q.rows * groups; e += (int64_t)kAbsBlocks * kNT) {
+            const int64_t row = e / groups, col = 8 * (e - row * groups);
+            if (skip && row_off(a.taken, a.row_weights, a.actions, row)) continue;
+            float v[8];
+            load8_of(q.dtype, q.p, row * q.ld + col, q.cols - col, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = finite_bits(v[i]);
+                top = b > top ? b : top;
+            }
+        }
+    }
+    top = wave_umax(top);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < kNT / kWave; ++i) top = red[i] > top ? red[i] : top;
+        a.part[blockIdx.y * kAbsBlocks + blockIdx.x] = top;
+    }
+}
+
+// The factors, and matrices as operands: 16-bit rows of whole 64 elements, zeros
+// behind the end, binary32 in two planes.
+struct Convert {
+    PolicyMat m;
+    uint16_t* to;         // [rows][ld_to]
+    int64_t ld_to;
+    float* row_factor;    // null: one factor for the matrix (binary32), by part `top`
+    int top, zero_off;    // zero_off: zeros in the place of rows that are off
+    int blocks;
+};
+struct ConvertArgs {
+    Convert c[3];
+    const uint32_t* part;  // or null: no factors
+    Factors* f;
+    const int32_t* taken;
+    const float* row_weights;
+    int64_t actions;
+    float scale;
+    int dtype;
+};
+__global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
+    __shared__ uint32_t tops[3];
+    const int lane = threadIdx.x & 63;
+    const bool f32 = a.dtype == IQLH_F32;
+    if (a.part) {
+        if (threadIdx.x < 3 * kWave) {
+            uint32_t top = 0u;
+            for (int i = lane; i < kAbsBlocks; i += kWave) {
+                const uint32_t b = a.part[(threadIdx.x >> 6) * kAbsBlocks + i];
+                top = b > top ? b : top;
+            }
+            top = wave_umax(top);
+            if (lane == 0) tops[threadIdx.x >> 6] = top;
+        }
+        __syncthreads();
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            const float h = f32 ? up_to(tops[0], 14) : 1.f, w = f32 ? up_to(tops[1], 14) : 1.f;
+            const float g = up_to(a.row_weights ? tops[2] : __float_as_uint(1.f), 14), s = a.scale / g;
+            *a.f = Factors{1.f / w, g, s / w, s / h, s, {0.f, 0.f, 0.f}};
+        }
+    }
+    int k = 0, block = blockIdx.x;
+    while (k < 2 && block >= a.c[k].blocks) block -= a.c[k++].blocks;
+    const Convert& c = a.c[k];
+    const PolicyMat& q = c.m;
+    if (!q.p) return;
+    const int groups = (int)(c.ld_to / 8);
+    const int64_t plane = q.rows * c.ld_to;
+    // eight elements of a row, times `up`
+    auto put = [&](int64_t row, int col, bool off, float up) __attribute__((always_inline)) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (col < q.cols && !off) load8_of(a.dtype, q.p, row * q.ld + col, q.cols - col, v);
+        uint16_t* to = c.to + row * c.ld_to + col;
+        if (f32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= up;
+            put_planes(to, plane, true, v);
+        } else {
+            store8_of(a.dtype, to, 0, 8, v);
+        }
+    };
+    if (c.row_factor) {  // a wave a row: its largest element, then the planes
+        for (int64_t row = (int64_t)block * (kNT / kWave) + (threadIdx.x >> 6); row < q.rows; row += (int64_t)c.blocks * (kNT / kWave)) {
+            const bool off = c.zero_off && row_off(a.taken, a.row_weights, a.actions, row);
+            uint32_t top = 0u;
+            if (!off)
+                for (int g = lane; 8 * g < q.cols; g += kWave) {
+                    float v[8];
+                    load8_of(a.dtype, q.p, row * q.ld + 8 * g, q.cols - 8 * g, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t b = finite_bits(v[i]);
+                        top = b > top ? b : top;
+                    }
+                }
+            const float up = up_to(wave_umax(top), 14);
+            if (lane == 0) c.row_factor[row] = 1.f / up;
+            for (int g = lane; g < groups; g += kWave) put(row, 8 * g, off, up);
+        }
+        return;
+    }
+    const float up = f32 ? up_to(tops[c.top], 14) : 1.f;
+    for (int64_t e = (int64_t)block * kNT + threadIdx.x; e < q.rows * groups; e += (int64_t)c.blocks * kNT) {
+        const int64_t row = e / groups;
+        put(row, 8 * (int)(e - row * groups), c.zero_off && row_off(a.taken, a.row_weights, a.actions, row), up);
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+// blockIdx -> tile: each XCD takes a run of tiles, walked in columns of 4 tile
+// rows, so that its L2 serves a patch of about 4 x 8 tiles at a time
+IQLH_DEV void tile_of(int id, int m_tiles, int n_tiles, int& tm, int& tn) {
+    const int total = m_tiles * n_tiles;
+    const int per = total / 8, rest = total % 8, x = id & 7, k = id >> 3;
+    id = x * per + (x < rest ? x : rest) + k;
+    const int band = id / (4 * n_tiles), in_band = id - band * 4 * n_tiles;
+    const int rows_in = m_tiles - band * 4 < 4 ? m_tiles - band * 4 : 4;
+    tm = band * 4 + in_band % rows_in;
+    tn = in_band / rows_in;
+}
+
+struct LogitArgs {
+    Side16 h, w;             // w: of the piece
+    const float* bias;       // of the piece, or null
+    const int32_t* taken;
+    const float* row_weights;  // or null
+    const float* lse;
+    const Factors* f;        // or null: 1, scale, 1, 1
+    const float* row_factor;  // of the sums, or null: 1
+    Soft* part;              // [n_tiles][rows]
+    float* z_taken;          // [rows]
+    uint16_t* g;             // [rows][ldg], planes apart by plane
+    float* db_part;          // [m_tiles][ldg], or null
+    int64_t rows, actions, first, ldg, plane;  // actions of the piece; its first one
+    int64_t all_actions;
+    int64_t k;               // summed elements
+    float scale;
+    int segs, g_planes, m_tiles, n_tiles;
+};
+
+// The logits of a tile, times log2(e).  GRAD false: maxima and sums of its rows, and the taken
+// actions' logits.  true: G.
+template <bool BRAIN, int TILE, bool GRAD>
+__global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void policy_logits_kernel(LogitArgs a) {
+    typedef Tile16<TILE> T;
+    constexpr int FA = T::FA, FB = T::FB;
+    extern __shared__ __align__(16) uint8_t lds[];
+    int tm, tn;
+    tile_of(blockIdx.x, a.m_tiles, a.n_tiles, tm, tn);
+    const int64_t m0 = (int64_t)tm * TILE, n0 = (int64_t)tn * TILE;
+    const int there = (int)(a.actions - n0 < TILE ? a.actions - n0 : TILE);  // columns of the tile
+    // of the columns: the bias, minus infinity behind the end.  Of the rows: the column of the action
+    // taken (or -1), the weight and the lse
+    float* col_bias = (float*)(lds + T::RING);
+    int* row_col = (int*)(col_bias + TILE);
+    float* row_w = (float*)(row_col + TILE);
+    float* row_lse = row_w + TILE;
+    if (threadIdx.x < TILE) {
+        const int n = threadIdx.x;
+        const int64_t m = m0 + n;
+        float b = n < there ? 0.f : kNone, w = 0.f, lse = __builtin_huge_valf();
+        if (a.bias && n < there) b = a.bias[n0 + n] * kLog2e;
+        int64_t col = -1;
+        if (m < a.rows) {
+            col = a.taken[m] - a.first - n0;
+            if (GRAD && !row_off(a.taken, a.row_weights, a.all_actions, m)) {
+                w = (a.row_weights ? a.row_weights[m] : 1.f) * (a.f ? a.f->g : a.scale);
+                lse = a.lse[m] == kNone ? 0.f : a.lse[m] * kLog2e;  // no logit above minus infinity: no probabilities
+            }
+        }
+        col_bias[n] = b;
+        row_col[n] = col >= 0 && col < there ? (int)col : -1;
+        row_w[n] = w;
+        row_lse[n] = lse;
+    }
+    mm_f16 acc[FA][FB];
+    tile_product<BRAIN, TILE, false, false>(a.h, a.w, m0, n0, 0, a.k, a.segs, lds, acc);
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wm = wave_m<TILE>(), wn = wave_n<TILE>();
+    const float zf = (a.f ? a.f->z : 1.f) * kLog2e;
+    float zr[FA], sub[FA];
+    int col[FA];
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+        const int row = wm + 32 * i + r;
+        zr[i] = a.row_factor && m0 + row < a.rows ? a.row_factor[m0 + row] * zf : zf;
+        sub[i] = GRAD ? row_lse[row] : 0.f;
+        col[i] = row_col[row] - wn;
+    }
+#pragma unroll
+    for (int j = 0; j < FB; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const float4 b4 = *(const float4*)(col_bias + wn + 32 * j + 8 * g + 4 * h);
+            const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+            for (int i = 0; i < FA; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = fmaf(acc[i][j][4 * g + e], zr[i], GRAD ? b[e] - sub[i] : b[e]);
+        }
+    if constexpr (!GRAD) {
+        Soft(*rows)[T::WN] = (Soft(*)[T::WN])lds;  // [TILE]
+#pragma unroll
+        for (int i = 0; i < FA; ++i) {
+            Soft v{kNone, 0.f};
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v.m = fmaxf(v.m, acc[i][j][e]);
+            const float top = v.m == kNone ? 0.f : v.m;
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v.s += __builtin_amdgcn_exp2f(acc[i][j][e] - top);
+            if (__any(col[i] >= 0 && col[i] < 32 * FB)) {
+#pragma unroll
+                for (int j = 0; j < FB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (col[i] == 32 * j + 8 * (e >> 2) + 4 * h + (e & 3)) a.z_taken[m0 + wm + 32 * i + r] = acc[i][j][e];
+            }
+            v = soft_xor(v, 32);
+            if (h == 0) rows[wm + 32 * i + r][wn / (32 * FB)] = v;
+        }
+        __syncthreads();
+        if (threadIdx.x < TILE && m0 + threadIdx.x < a.rows) {
+            Soft v = rows[threadIdx.x][0];
+#pragma unroll
+            for (int k = 1; k < T::WN; ++k) v.join(rows[threadIdx.x][k]);
+            a.part[(int64_t)tn * a.rows + m0 + threadIdx.x] = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < FA; ++i) {
+            const float w = row_w[wm + 32 * i + r];
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = w * __builtin_amdgcn_exp2f(acc[i][j][e]);
+            if (__any(col[i] >= 0 && col[i] < 32 * FB)) {
+#pragma unroll
+                for (int j = 0; j < FB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (col[i] == 32 * j + 8 * (e >> 2) + 4 * h + (e & 3)) acc[i][j][e] -= w;
+            }
+        }
+        if (a.db_part) {  // sums over the tile's rows
+            float(*sums)[TILE] = (float(*)[TILE])lds;  // [WM]
+#pragma unroll
+            for (int jj = 0; jj < FB; jj += 2) {
+                float v[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    v[k] = acc[0][jj + k / 16][k % 16];
+#pragma unroll
+                    for (int i = 1; i < FA; ++i) v[k] += acc[i][jj + k / 16][k % 16];
+                }
+                // 32 values of 32 lanes: each exchange halves the values a lane has; lane r ends with value r
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                    for (int k = 0; k < o; ++k) {
+                        const float keep = r & o ? v[k + o] : v[k], send = r & o ? v[k] : v[k + o];
+                        v[k] = keep + __shfl_xor(send, o, kWave);
+                    }
+                sums[wm / (32 * FA)][wn + 32 * (jj + (r >> 4)) + 8 * (r >> 2 & 3) + 4 * h + (r & 3)] = v[0];
+            }
+            __syncthreads();
+            for (int n = threadIdx.x; n < TILE; n += T::NT)
+                if (n0 + n < a.ldg) a.db_part[(int64_t)tm * a.ldg + n0 + n] = sums[0][n] + sums[1][n];
+            __syncthreads();
+        }
+        // To memory through LDS, 16 bits an element, so that rows leave in 16-byte stores: the 16 bytes of columns
+        // 8 u .. of row m lie at place u ^ (m & 15).  A second plane holds what the first rounds off.
+        for (int plane = 0; plane < a.g_planes; ++plane) {
+            const bool more = plane + 1 < a.g_planes;
+            if (plane) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < FA; ++i)
+#pragma unroll
+                for (int j = 0; j < FB; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int m = wm + 32 * i + r, u = (wn + 32 * j) / 8 + g;
+                        const uint32_t lo = pack16<BRAIN>(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
+                        const uint32_t hi = pack16<BRAIN>(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+                        if (more)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] -= of16<BRAIN>(e < 2 ? lo : hi, e & 1);
+                        *(uint2*)(lds + m * (TILE * 2) + 16 * (u ^ (m & 15)) + 8 * h) = uint2{lo, hi};
+                    }
+            __syncthreads();
+            uint16_t* to = a.g + plane * a.plane + n0;
+#pragma unroll 4
+            for (int c = threadIdx.x; c < TILE * (TILE / 8); c += T::NT) {
+                const int row = c / (TILE / 8), u = c % (TILE / 8);
+                if (m0 + row >= a.rows || n0 + 8 * u >= a.ldg) continue;
+                *(uint4*)(to + (m0 + row) * a.ldg + 8 * u) = *(const uint4*)(lds + row * (TILE * 2) + 16 * (u ^ (row & 15)));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ row statistics
+struct FinishArgs {
+    const Soft* part;        // [parts][rows]
+    const float* z_taken;
+    const int32_t* taken;
+    const float* row_weights;
+    float* nll;
+    float* lse;
+    float* loss;             // or null
+    double* loss_part;       // [workgroups]
+    int32_t* flags;
+    int64_t rows, actions;
+    int parts;
+    double scale;
+};
+IQLH_DEV void put_loss(const FinishArgs& a, double sum) {
+    const float loss = (float)(sum * a.scale);
+    if (a.loss) *a.loss = loss;
+    if (!(fabsf(loss) < __uint_as_float(0x7F800000u))) set_flag(a.flags, IQLH_FLAG_NONFINITE_LOSS);
+}
+IQLH_DEV double block_sum64(double v, double* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kNT / kWave; ++i) s += red[i];
+    return s;
+}
+// R rows a workgroup, 256 / R threads a row
+template <int R>
+__global__ __launch_bounds__(kNT) void policy_finish_kernel(FinishArgs a) {
+    constexpr int S = kNT / R;
+    __shared__ Soft each[S][R];
+    __shared__ double red[kNT / kWave];
+    const int row = threadIdx.x % R, slice = threadIdx.x / R;
+    const int64_t m = (int64_t)blockIdx.x * R + row;
+    Soft v{kNone, 0.f};
+    if (m < a.rows)
+#pragma unroll 4
+        for (int k = slice; k < a.parts; k += S) v.join(a.part[(int64_t)k * a.rows + m]);
+    each[slice][row] = v;
+    for (int half = S / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (slice < half) {
+            v.join(each[slice + half][row]);
+            each[slice][row] = v;
+        }
+    }
+    double term = 0.0;
+    if (slice == 0 && m < a.rows) {
+        const float l2 = v.s == 0.f ? kNone : v.m + log2f(v.s);
+        const int32_t t = a.taken[m];
+        float nll = 0.f;
+        if (t >= 0 && t < a.actions) {
+            const float z = a.z_taken[m];
+            nll = z == kNone && l2 == l2 ? __builtin_huge_valf() : (l2 - z) * kLn2;
+            const float w = a.row_weights ? a.row_weights[m] : 1.f;
+            if (w != 0.f) term = (double)w * (double)nll;
+        } else if (t != -1) {
+            set_flag(a.flags, IQLH_FLAG_BAD_INDEX);
+        }
+        a.lse[m] = l2 * kLn2;
+        a.nll[m] = nll;
+    }
+    term = block_sum64(term, red);
+    if (threadIdx.x == 0) {
+        if (gridDim.x == 1) put_loss(a, term);
+        else a.loss_part[blockIdx.x] = term;
+    }
+}
+__global__ __launch_bounds__(kNT) void policy_loss_sum_kernel(FinishArgs a, int n) {
+    __shared__ double red[kNT / kWave];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += kNT) s += a.loss_part[i];
+    s = block_sum64(s, red);
+    if (threadIdx.x == 0) put_loss(a, s);
+}
+int finish_rows(int64_t rows) { return rows >= 1024 ? 64 : rows >= 64 ? 16 : 1; }
+hipError_t launch_finish(const FinishArgs& a, hipStream_t stream) {
+    const int R = finish_rows(a.rows);
+    const uint32_t n = (uint32_t)((a.rows + R - 1) / R);
+    auto kernel = R == 64 ? policy_finish_kernel<64> : R == 16 ? policy_finish_kernel<16> : policy_finish_kernel<1>;
+    hipLaunchKernelGGL(kernel, dim3(n), dim3(kNT), 0, stream, a);
+    if (n > 1) hipLaunchKernelGGL(policy_loss_sum_kernel, dim3(1), dim3(kNT), 0, stream, a, (int)n);
+    return hipGetLastError();
+}
+
+// ----------------------------------------------------------------- products
+struct GradArgs {
+    Side16 a, b;
+    int64_t m, n, k;         // outputs, summed elements
+    int64_t k_split;         // of one workgroup, a multiple of 64
+    int segs, m_tiles, n_tiles, splits;
+    const float* factor;     // or null (1): of the result
+    float* sums;             // [splits][m][ld_sums]: partial sums
+    int64_t ld_sums;
+    int add;                 // to what lies in sums
+    void* out;               // the result, or null: sums only
+    int64_t ld_out;
+    int out_dtype;
+};
+// One of the products of G: with `out` null, or several splits, the sums in binary32.
+template <bool BRAIN, int TILE, bool AC>
+__global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void policy_grad_kernel(GradArgs a) {
+    typedef Tile16<TILE> T;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tiles = a.m_tiles * a.n_tiles, split = blockIdx.x / tiles;
+    int tm, tn;
+    tile_of(blockIdx.x - split * tiles, a.m_tiles, a.n_tiles, tm, tn);
+    const int64_t m0 = (int64_t)tm * TILE, n0 = (int64_t)tn * TILE;
+    const int64_t k0 = split * a.k_split, k1 = k0 + a.k_split < a.k ? k0 + a.k_split : a.k;
+    mm_f16 acc[T::FA][T::FB];
+    tile_product<BRAIN, TILE, AC, true>(a.a, a.b, m0, n0, k0, k1, a.segs, lds, acc);
+    const float f = a.out && a.factor ? *a.factor : 1.f;
+    float* sums = a.sums + (int64_t)split * a.m * a.ld_sums;
+#pragma unroll
+    for (int band = 0; band < T::BANDS; ++band) {
+        stage_band<TILE>(acc, lds, band);
+#pragma unroll 2
+        for (int c = threadIdx.x; c < T::BAND * (TILE / 8); c += T::NT) {
+            const int row = c / (TILE / 8), u = c % (TILE / 8);
+            const int64_t m = m0 + band * T::BAND + row, n = n0 + 8 * u;
+            if (m >= a.m || n >= a.n) continue;
+            const float4 lo = *stage_at<TILE>(lds, row, 2 * u), hi = *stage_at<TILE>(lds, row, 2 * u + 1);
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            float4* s = (float4*)(sums + m * a.ld_sums + n);  // rows of whole 8 elements
+            if (a.add) {
+                const float4 x = s[0], y = s[1];
+                v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+            }
+            if (a.out) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= f;
+                store8_of(a.out_dtype, a.out, m * a.ld_out + n, a.n - n, v);
+            } else {
+                s[0] = float4{v[0], v[1], v[2], v[3]};
+                s[1] = float4{v[4], v[5], v[6], v[7]};
+            }
+        }
+    }
+}
+
+// out = factor times the sum over the splits
+__global__ __launch_bounds__(kNT) void policy_join_kernel(GradArgs a) {
+    const int64_t groups = (a.n + 7) / 8, total = a.m * groups;
+    const float f = a.factor ? *a.factor : 1.f;
+    for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < total; e += (int64_t)gridDim.x * kNT) {
+        const int64_t m = e / groups, n = 8 * (e - m * groups);
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < a.splits; ++k) {
+            const float4* s = (const float4*)(a.sums + ((int64_t)k * a.m + m) * a.ld_sums + n);
+            const float4 x = s[0], y = s[1];
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= f;
+        store8_of(a.out_dtype, a.out, m * a.ld_out + n, a.n - n, v);
+    }
+}
+// db of a piece
+__global__ __launch_bounds__(kNT) void policy_bias_kernel(const float* part, int parts, int64_t ld, const float* factor,
+                                                          float* out, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    if (i >= n) return;
+    double s = 0.0;
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) s += part[k * ld + i];
+    out[i] = (float)s * (factor ? *factor : 1.f);
+}
+
+// Rows up to which G has two planes whatever its type: its rounding does not average
+// out over few rows, and the products are bound by W and dW there
+constexpr int64_t kFewRows = 64;
+
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t tiles_of(int64_t m, int64_t n, int t) { return ((m + t - 1) / t) * ((n + t - 1) / t); }
+// 256 tiles where they occupy most compute units
+int tile_for(int64_t m, int64_t n) { return tiles_of(m, n, 256) >= 192 ? 256 : 128; }
+
+// Parts of the summed axis, so that there are about two workgroups of 128 tiles to a
+// compute unit, of 512 elements or more
+struct Split {
+    int tile, n;
+    int64_t k;
+};
+Split split_for(int64_t m, int64_t n, int64_t k) {
+    Split s{tile_for(m, n), 1, up(k, 64)};
+    if (s.tile == 256) return s;
+    int64_t want = 512 / tiles_of(m, n, 128), most = (k + 511) / 512;
+    want = want < 1 ? 1 : want > most ? most : want;
+    s.k = up((k + want - 1) / want, 64);
+    s.n = (int)((k + s.k - 1) / s.k);
+    return s;
+}
+
+}  // namespace
+
+// Actions of a piece: G of about 256 MB, which the Infinity Cache holds between its
+// three uses, but enough for dW to have tiles
+PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bool grad) {
+    PolicyPlan p{};
+    p.planes = dtype == IQLH_F32 ? 2 : 1;
+    p.g_planes = dtype == IQLH_F32 || rows <= kFewRows ? 2 : 1;
+    p.ld = up(dim, 64);
+    int64_t piece = ((int64_t)1 << 27) / (rows * p.g_planes) / 256 * 256;
+    piece = piece < 1024 ? 1024 : piece;
+    p.piece = piece < actions ? piece : up(actions, 64);
+    p.pieces = (int)((actions + p.piece - 1) / p.piece);
+    size_t at = 0;
+    auto take = [&at](size_t bytes) {
+        const size_t was = at;
+        at += (bytes + 255) / 256 * 256;
+        return was;
+    };
+    p.factors = take(sizeof(Factors));
+    p.absmax = take(3 * kAbsBlocks * 4);
+    p.row_factor = take((size_t)rows * 4);
+    p.h = take((size_t)rows * p.ld * 2 * p.planes);
+    p.w = take((size_t)actions * p.ld * 2 * p.planes);
+    const size_t begin = at;  // the loss's and the gradients' own
+    p.part = take((size_t)((actions + 127) / 128) * rows * sizeof(Soft));
+    p.z_taken = take((size_t)rows * 4);
+    p.loss_part = take((size_t)rows * 8);
+    p.bytes = at;
+    if (grad) {
+        at = begin;
+        const Split dh = split_for(rows, dim, p.piece);
+        const int64_t full = p.pieces > 1 ? p.piece : actions, last = actions - (p.pieces - 1) * p.piece;
+        const int64_t dw_full = split_for(full, dim, rows).n * full, dw_last = split_for(last, dim, rows).n * last;
+        p.h_dw = take(p.planes == 2 ? (size_t)rows * p.ld * 4 : 0);
+        p.g = take((size_t)rows * p.piece * 2 * p.g_planes);
+        p.db_part = take((size_t)((rows + 127) / 128) * p.piece * 4);
+        p.dh_sums = take((size_t)dh.n * rows * up(dim, 8) * 4);
+        p.dw_sums = take((size_t)(dw_full > dw_last ? dw_full : dw_last) * up(dim, 8) * 4);
+        if (at > p.bytes) p.bytes = at;
+    }
+    return p;
+}
+
+namespace {
+
+struct Operands {
+    Side16 h, w;      // of the logits
+    Side16 h_dw;      // H of dW
+    int64_t k;        // summed elements of the logits; columns of H and W as operands
+    const Factors* f;
+    const float* row_factor;
+};
+
+bool in_place(const PolicyMat& q) {
+    return q.dtype != IQLH_F32 && (uintptr_t)q.p % 16 == 0 && q.ld % 8 == 0 && q.ld < 1 << 22 && q.cols % 8 == 0;
+}
+
+// H and W as operands.  For the gradients rows of H that are off become zeros, since they would add
+// 0 times what they hold to dW, NaN or infinities as it may be.  Binary32: in the logits each row
+// of H has its own factor, so that none loses bits to a larger one; in dW the rows are summed
+// and share one.
+hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands* o, hipStream_t stream) {
+    const bool f32 = a.h.dtype == IQLH_F32, sized = f32 || (grad && a.h.dtype == IQLH_F16);
+    uint8_t* base = (uint8_t*)a.workspace;
+    ConvertArgs c{};
+    c.dtype = a.h.dtype, c.scale = (float)a.scale, c.f = (Factors*)(base + p.factors);
+    c.taken = a.taken, c.row_weights = a.row_weights, c.actions = a.w.rows;
+    int n = 0;
+    auto convert = [&](const PolicyMat& q, size_t at, bool by_row, int top, bool zero_off) {
+        const int64_t blocks = by_row ? (q.rows + 3) / 4 : (q.rows * (p.ld / 8) + 4 * kNT - 1) / (4 * kNT);
+        c.c[n++] = Convert{q, (uint16_t*)(base + at), p.ld, by_row ? (float*)(base + p.row_factor) : nullptr, top, zero_off,
+                           (int)(blocks < 4096 ? blocks : 4096)};
+        return Side16{(const uint16_t*)(base + at), q.rows * p.ld, p.ld, q.rows};
+    };
+    // both in place or both converted, but for H of the gradients: the summed axis is as long in one as in the other
+    const bool copy = !in_place(a.w) || (!grad && !in_place(a.h));
+    o->k = copy ? p.ld : a.h.cols;
+    o->f = sized ? c.f : nullptr;
+    o->row_factor = f32 ? (const float*)(base + p.row_factor) : nullptr;
+    o->h = copy || grad ? convert(a.h, p.h, f32, 0, grad) : Side16{(const uint16_t*)a.h.p, 0, a.h.ld, a.h.rows};
+    o->h_dw = f32 && grad ? convert(a.h, p.h_dw, false, 0, true) : o->h;
+    o->w = copy ? convert(a.w, p.w, false, 1, false) : Side16{(const uint16_t*)a.w.p, 0, a.w.ld, a.w.rows};
+    if (sized) {
+        const PolicyMat none{};
+        AbsMaxArgs m{};
+        m.part = (uint32_t*)(base + p.absmax);
+        m.m[0] = f32 && grad ? a.h : none;
+        m.m[1] = f32 ? a.w : none;
+        m.m[2] = grad && a.row_weights ? PolicyMat{a.row_weights, 1, a.h.rows, a.h.rows, IQLH_F32} : none;
+        m.taken = a.taken, m.row_weights = a.row_weights, m.actions = a.w.rows;
+        hipLaunchKernelGGL(policy_absmax_kernel, dim3(kAbsBlocks, 3), dim3(kNT), 0, stream, m);
+        c.part = m.part;
+    }
+    if (n) {
+        const uint32_t blocks = c.c[0].blocks + c.c[1].blocks + c.c[2].blocks;
+        hipLaunchKernelGGL(policy_convert_kernel, dim3(blocks), dim3(kNT), 0, stream, c);
+    }
+    return hipGetLastError();
+}
+
+template <bool GRAD>
+hipError_t launch_logits(LogitArgs a, bool brain, hipStream_t stream) {
+    const int tile = tile_for(a.rows, a.actions);
+    a.m_tiles = (int)((a.rows + tile - 1) / tile);
+    a.n_tiles = (int)(((GRAD ? a.ldg : a.actions) + tile - 1) / tile);
+    auto launch = [&](auto is_brain, auto t) {
+        constexpr int TILE = decltype(t)::value;
+        auto kernel = policy_logits_kernel<decltype(is_brain)::value, TILE, GRAD>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile16<TILE>::LDS);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles)), dim3(Tile16<TILE>::NT), Tile16<TILE>::LDS, stream, a);
+        return hipGetLastError();
+    };
+    typedef std::integral_constant<int, 128> T128;
+    typedef std::integral_constant<int, 256> T256;
+    if (tile == 256) return brain ? launch(std::true_type(), T256()) : launch(std::false_type(), T256());
+    return brain ? launch(std::true_type(), T128()) : launch(std::false_type(), T128());
+}
+
+// `joined`: partial sums that make up the result, at least those of this launch
+template <bool AC>
+hipError_t launch_grad_product(GradArgs a, const Split& s, int joined, bool brain, hipStream_t stream) {
+    a.m_tiles = (int)((a.m + s.tile - 1) / s.tile);
+    a.n_tiles = (int)((a.n + s.tile - 1) / s.tile);
+    a.splits = s.n;
+    a.k_split = s.k;
+    void* out = a.out;
+    if (joined > 1) a.out = nullptr;
+    auto launch = [&](auto is_brain, auto t) {
+        constexpr int TILE = decltype(t)::value;
+        auto kernel = policy_grad_kernel<decltype(is_brain)::value, TILE, AC>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile16<TILE>::LDS);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles * a.splits)), dim3(Tile16<TILE>::NT), Tile16<TILE>::LDS,
+                           stream, a);
+    };
+    typedef std::integral_constant<int, 128> T128;
+    typedef std::integral_constant<int, 256> T256;
+    if (s.tile == 256) brain ? launch(std::true_type(), T256()) : launch(std::false_type(), T256());
+    else brain ? launch(std::true_type(), T128()) : launch(std::false_type(), T128());
+    if (joined > 1 && out) {
+        a.out = out;
+        a.splits = joined;
+        const int64_t blocks = (a.m * ((a.n + 7) / 8) + kNT - 1) / kNT;
+        hipLaunchKernelGGL(policy_join_kernel, dim3((uint32_t)(blocks < 2048 ? blocks : 2048)), dim3(kNT), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream) {
+    const PolicyPlan p = policy_plan(a.h.rows, a.w.rows, a.h.cols, a.h.dtype, false);
+    uint8_t* base = (uint8_t*)a.workspace;
+    Operands o;
+    hipError_t e = prepare(a, p, false, &o, stream);
+    if (e != hipSuccess) return e;
+    LogitArgs l{};
+    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor, l.segs = p.planes == 2 ? 3 : 1;
+    l.bias = a.bias, l.taken = a.taken;
+    l.rows = a.h.rows, l.actions = l.all_actions = a.w.rows;
+    l.part = (Soft*)(base + p.part), l.z_taken = (float*)(base + p.z_taken);
+    e = launch_logits<false>(l, a.h.dtype == IQLH_BF16, stream);
+    if (e != hipSuccess) return e;
+    const int tile = tile_for(l.rows, l.actions);
+    const FinishArgs f{l.part, l.z_taken, a.taken, a.row_weights, a.nll, a.lse_out, a.loss, (double*)(base + p.loss_part),
+                       a.flags, l.rows, l.actions, (int)((l.actions + tile - 1) / tile), a.scale};
+    return launch_finish(f, stream);
+}
+
+hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
+    const PolicyPlan p = policy_plan(a.h.rows, a.w.rows, a.h.cols, a.h.dtype, true);
+    uint8_t* base = (uint8_t*)a.workspace;
+    const int64_t rows = a.h.rows, actions = a.w.rows, dim = a.h.cols;
+    const bool brain = a.h.dtype == IQLH_BF16;
+    const int es = a.h.dtype == IQLH_F32 ? 4 : 2;
+    Operands o;
+    hipError_t e = prepare(a, p, true, &o, stream);
+    LogitArgs l{};
+    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor, l.segs = p.planes == 2 ? 3 : 1;
+    l.taken = a.taken, l.row_weights = a.row_weights, l.lse = a.lse_in;
+    l.rows = rows, l.all_actions = actions, l.scale = (float)a.scale;
+    l.g = (uint16_t*)(base + p.g), l.g_planes = p.g_planes;
+    const Split dh = split_for(rows, dim, p.piece);
+    for (int k = 0; k < p.pieces && e == hipSuccess; ++k) {
+        const int64_t first = k * p.piece, n = actions - first < p.piece ? actions - first : p.piece;
+        l.first = first, l.actions = n, l.ldg = up(n, 64), l.plane = rows * l.ldg;
+        l.w.p = o.w.p + first * o.w.ld, l.w.n = n;
+        l.bias = a.bias ? a.bias + first : nullptr;
+        l.db_part = a.d_bias ? (float*)(base + p.db_part) : nullptr;
+        e = launch_logits<true>(l, brain, stream);
+        if (e != hipSuccess) break;
+        if (a.d_bias) {
+            const int tile = tile_for(rows, n);
+            hipLaunchKernelGGL(policy_bias_kernel, dim3((uint32_t)((n + kNT - 1) / kNT)), dim3(kNT), 0, stream, l.db_part,
+                               (int)((rows + tile - 1) / tile), l.ldg, o.f ? &o.f->db : nullptr, a.d_bias + first, n);
+            e = hipGetLastError();
+        }
+        GradArgs g{};
+        g.n = dim, g.segs = p.planes == 2 ? 3 : p.g_planes == 2 ? 2 : 1, g.ld_sums = up(dim, 8), g.out_dtype = a.h.dtype;
+        const Side16 gs{l.g, l.plane, l.ldg, rows};
+        if (a.d_weight && e == hipSuccess) {
+            g.a = Side16{l.g, l.plane, l.ldg, l.ldg};
+            g.b = o.h_dw;
+            g.b.n = o.k;
+            g.m = n, g.k = rows;
+            g.factor = o.f ? &o.f->dw : nullptr;
+            g.sums = (float*)(base + p.dw_sums);
+            g.out = (uint8_t*)a.d_weight + first * a.ld_dw * es;
+            g.ld_out = a.ld_dw;
+            const Split s = split_for(n, dim, rows);
+            e = launch_grad_product<true>(g, s, s.n, brain, stream);
+        }
+        if (a.d_hidden && e == hipSuccess) {
+            g.a = gs;
+            g.b = l.w;
+            g.b.n = o.k;
+            g.m = rows, g.k = n;
+            g.factor = o.f ? &o.f->dh : nullptr;
+            g.sums = (float*)(base + p.dh_sums);
+            g.add = k > 0;
+            g.out = k + 1 == p.pieces ? a.d_hidden : nullptr;
+            g.ld_out = a.ld_dh;
+            Split s = dh;
+            s.n = (int)((n + s.k - 1) / s.k);
+            e = launch_grad_product<false>(g, s, p.pieces > 1 ? dh.n : s.n, brain, stream);
+        }
+    }
+    return e;
+}
+
+}  // namespace iqlh

@@ -29,10 +29,12 @@ budget   budgeted clipped-SAXPY gradient accumulation.
 bf16     round-to-nearest-even float32 -> bfloat16 (storage rounding).
 tensors  norm and clip over a list of tensors.
 mx4      microscaled 4-bit quantisation and the value network on it.
+policy   loss of the actions taken under a linear policy head, and its gradients.
+ortho    orthogonalised updates of weight matrices, with momentum.
 
 Parity status: every function is pinned by tests in ``tests/test_oracle_*.py``
 (closed forms, library special cases, finite differences, brute force and
 hand-worked fixtures); none is "parity unpinned".
 """
 
-from . import philox, her, iql, aw, budget, bf16, tensors, mx4  # noqa: F401
+from . import philox, her, iql, aw, budget, bf16, tensors, mx4, policy, ortho  # noqa: F401
