@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) u[i] = (float)((double)u[i] * scale);
         }
-        put_planes(x + (int64_t)row * q.cols_pad + col, (int64_t)q.rows_pad * q.cols_pad, q.planes == 2, u);
+        put_planes(x, row, q.cols_pad, col, q.planes == 2, u);
     }
 }
 
@@ -121,25 +121,28 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
     const OrthoTile w = (PHASE <= kPoly ? a.sym : a.rect)[blockIdx.x];
     const OrthoMat& q = a.mats[w.mat];
     const bool two = q.planes == 2, tall = q.rows > q.cols;
-    const int segs = two ? 3 : 1;
     const int64_t m0 = (int64_t)w.m * TILE, n0 = (int64_t)w.n * TILE;
-    const int64_t plane_x = (int64_t)q.rows_pad * q.cols_pad, plane_s = (int64_t)q.k_pad * q.k_pad;
     const uint16_t* x = (const uint16_t*)(a.base + q.x_at[from]);
     uint16_t* gram = (uint16_t*)(a.base + q.gram_at);
     uint16_t* poly = (uint16_t*)(a.base + q.poly_at);
     mm_f16 acc[T::FA][T::FB];
-    if (PHASE == kGram) {
-        const Side16 s{x, plane_x, q.cols_pad, q.k_pad};
-        if (tall) tile_product<false, TILE, true, true>(s, s, m0, n0, 0, q.rows_pad, segs, lds, acc);
-        else tile_product<false, TILE, false, false>(s, s, m0, n0, 0, q.cols_pad, segs, lds, acc);
-    } else if (PHASE == kPoly) {
-        const Side16 s{gram, plane_s, q.k_pad, q.k_pad};
-        tile_product<false, TILE, false, false>(s, s, m0, n0, 0, q.k_pad, segs, lds, acc);
-    } else {
-        const Side16 p{poly, plane_s, q.k_pad, q.k_pad};
-        if (tall) tile_product<false, TILE, false, false>(Side16{x, plane_x, q.cols_pad, q.rows_pad}, p, m0, n0, 0, q.k_pad, segs, lds, acc);
-        else tile_product<false, TILE, false, true>(p, Side16{x, plane_x, q.cols_pad, q.cols_pad}, m0, n0, 0, q.k_pad, segs, lds, acc);
-    }
+    auto product = [&](auto planes) __attribute__((always_inline)) {
+        constexpr int PL = decltype(planes)::value;
+        if (PHASE == kGram) {
+            const Side16 s{x, 0, q.cols_pad, q.k_pad};
+            if (tall) tile_product<false, TILE, true, true, PL>(s, s, m0, n0, 0, q.rows_pad, false, lds, acc);
+            else tile_product<false, TILE, false, false, PL>(s, s, m0, n0, 0, q.cols_pad, false, lds, acc);
+        } else if (PHASE == kPoly) {
+            const Side16 s{gram, 0, q.k_pad, q.k_pad};
+            tile_product<false, TILE, false, false, PL>(s, s, m0, n0, 0, q.k_pad, false, lds, acc);
+        } else {
+            const Side16 p{poly, 0, q.k_pad, q.k_pad};
+            if (tall) tile_product<false, TILE, false, false, PL>(Side16{x, 0, q.cols_pad, q.rows_pad}, p, m0, n0, 0, q.k_pad, false, lds, acc);
+            else tile_product<false, TILE, false, true, PL>(p, Side16{x, 0, q.cols_pad, q.cols_pad}, m0, n0, 0, q.k_pad, false, lds, acc);
+        }
+    };
+    if (two) product(std::integral_constant<int, 2>());
+    else product(std::integral_constant<int, 1>());
     const int rows = PHASE <= kPoly ? q.k_pad : q.rows_pad, cols = PHASE <= kPoly ? q.k_pad : q.cols_pad;
     bool ok = true;
     float rate = 0.f;
@@ -158,18 +161,18 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
         if (PHASE == kGram) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = v[i] * kDown;
-            put_planes(gram + (int64_t)m * q.k_pad + n, plane_s, two, y);
+            put_planes(gram, m, q.k_pad, n, two, y);
         } else if (PHASE == kPoly) {
-            get_planes(gram + (int64_t)m * q.k_pad + n, plane_s, two, y);
+            get_planes(gram, m, q.k_pad, n, two, y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = fmaf(kB, y[i], (kC * kDown) * v[i]);
-            put_planes(poly + (int64_t)m * q.k_pad + n, plane_s, two, y);
+            put_planes(poly, m, q.k_pad, n, two, y);
         } else {
-            get_planes(x + (int64_t)m * q.cols_pad + n, plane_x, two, y);
+            get_planes(x, m, q.cols_pad, n, two, y);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = fmaf(kA, y[i], kDown * v[i]);
             if (PHASE == kApply) {
-                put_planes((uint16_t*)(a.base + q.x_at[from ^ 1]) + (int64_t)m * q.cols_pad + n, plane_x, two, y);
+                put_planes((uint16_t*)(a.base + q.x_at[from ^ 1]), m, q.cols_pad, n, two, y);
                 return;
             }
             if (m >= q.rows || n >= q.cols) return;

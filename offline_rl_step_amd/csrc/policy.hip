@@ -114,8 +114,8 @@ __global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
     }
 }
 
-// The factors, and matrices as operands: 16-bit rows of whole 64 elements, zeros
-// behind the end, binary32 in two planes.
+// The factors, and matrices as operands: rows of whole 64 16-bit elements, zeros behind the
+// end, binary32 in two planes.
 struct Convert {
     PolicyMat m;
     uint16_t* to;         // [rows][ld_to]
@@ -161,18 +161,16 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     const PolicyMat& q = c.m;
     if (!q.p) return;
     const int groups = (int)(c.ld_to / 8);
-    const int64_t plane = q.rows * c.ld_to;
     // eight elements of a row, times `up`
     auto put = [&](int64_t row, int col, bool off, float up) __attribute__((always_inline)) {
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (col < q.cols && !off) load8_of(a.dtype, q.p, row * q.ld + col, q.cols - col, v);
-        uint16_t* to = c.to + row * c.ld_to + col;
         if (f32) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= up;
-            put_planes(to, plane, true, v);
+            put_planes(c.to, row, c.ld_to, col, true, v);
         } else {
-            store8_of(a.dtype, to, 0, 8, v);
+            store8_of(a.dtype, c.to, row * c.ld_to + col, 8, v);
         }
     };
     if (c.row_factor) {  // a wave a row: its largest element, then the planes
@@ -225,20 +223,20 @@ struct LogitArgs {
     const float* row_factor;  // of the sums, or null: 1
     Soft* part;              // [n_tiles][rows]
     float* z_taken;          // [rows]
-    uint16_t* g;             // [rows][ldg], planes apart by plane
+    uint16_t* g;             // [rows][ldg], for binary32 in two planes; else a second matrix behind `plane`
     float* db_part;          // [m_tiles][ldg], or null
     int64_t rows, actions, first, ldg, plane;  // actions of the piece; its first one
     int64_t all_actions;
     int64_t k;               // summed elements
     float scale;
-    int segs, g_planes, m_tiles, n_tiles;
+    int g_planes, m_tiles, n_tiles;
 };
 
 // The logits of a tile, times log2(e).  GRAD false: maxima and sums of its rows, and the taken
 // actions' logits.  true: G.
-template <bool BRAIN, int TILE, bool GRAD>
+template <bool BRAIN, int TILE, bool GRAD, int PL>
 __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void policy_logits_kernel(LogitArgs a) {
-    typedef Tile16<TILE> T;
+    typedef Tile16<TILE, PL> T;
     constexpr int FA = T::FA, FB = T::FB;
     extern __shared__ __align__(16) uint8_t lds[];
     int tm, tn;
@@ -270,7 +268,7 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
         row_lse[n] = lse;
     }
     mm_f16 acc[FA][FB];
-    tile_product<BRAIN, TILE, false, false>(a.h, a.w, m0, n0, 0, a.k, a.segs, lds, acc);
+    tile_product<BRAIN, TILE, false, false, PL>(a.h, a.w, m0, n0, 0, a.k, false, lds, acc);
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wm = wave_m<TILE>(), wn = wave_n<TILE>();
     const float zf = (a.f ? a.f->z : 1.f) * kLog2e;
@@ -387,12 +385,13 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
                         *(uint2*)(lds + m * (TILE * 2) + 16 * (u ^ (m & 15)) + 8 * h) = uint2{lo, hi};
                     }
             __syncthreads();
-            uint16_t* to = a.g + plane * a.plane + n0;
+            uint16_t* to = a.g + (PL == 2 ? 32 * plane : plane * a.plane);
 #pragma unroll 4
             for (int c = threadIdx.x; c < TILE * (TILE / 8); c += T::NT) {
                 const int row = c / (TILE / 8), u = c % (TILE / 8);
                 if (m0 + row >= a.rows || n0 + 8 * u >= a.ldg) continue;
-                *(uint4*)(to + (m0 + row) * a.ldg + 8 * u) = *(const uint4*)(lds + row * (TILE * 2) + 16 * (u ^ (row & 15)));
+                *(uint4*)(to + (PL == 2 ? planes_at(m0 + row, a.ldg, n0 + 8 * u) : (m0 + row) * a.ldg + n0 + 8 * u)) =
+                    *(const uint4*)(lds + row * (TILE * 2) + 16 * (u ^ (row & 15)));
             }
         }
     }
@@ -493,7 +492,8 @@ struct GradArgs {
     Side16 a, b;
     int64_t m, n, k;         // outputs, summed elements
     int64_t k_split;         // of one workgroup, a multiple of 64
-    int segs, m_tiles, n_tiles, splits;
+    bool both;               // a's second matrix too
+    int m_tiles, n_tiles, splits;
     const float* factor;     // or null (1): of the result
     float* sums;             // [splits][m][ld_sums]: partial sums
     int64_t ld_sums;
@@ -503,9 +503,9 @@ struct GradArgs {
     int out_dtype;
 };
 // One of the products of G: with `out` null, or several splits, the sums in binary32.
-template <bool BRAIN, int TILE, bool AC>
+template <bool BRAIN, int TILE, bool AC, int PL>
 __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void policy_grad_kernel(GradArgs a) {
-    typedef Tile16<TILE> T;
+    typedef Tile16<TILE, PL> T;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tiles = a.m_tiles * a.n_tiles, split = blockIdx.x / tiles;
     int tm, tn;
@@ -513,7 +513,7 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
     const int64_t m0 = (int64_t)tm * TILE, n0 = (int64_t)tn * TILE;
     const int64_t k0 = split * a.k_split, k1 = k0 + a.k_split < a.k ? k0 + a.k_split : a.k;
     mm_f16 acc[T::FA][T::FB];
-    tile_product<BRAIN, TILE, AC, true>(a.a, a.b, m0, n0, k0, k1, a.segs, lds, acc);
+    tile_product<BRAIN, TILE, AC, true, PL>(a.a, a.b, m0, n0, k0, k1, a.both, lds, acc);
     const float f = a.out && a.factor ? *a.factor : 1.f;
     float* sums = a.sums + (int64_t)split * a.m * a.ld_sums;
 #pragma unroll
@@ -581,7 +581,7 @@ constexpr int64_t kFewRows = 64;
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tiles_of(int64_t m, int64_t n, int t) { return ((m + t - 1) / t) * ((n + t - 1) / t); }
 // 256 tiles where they occupy most compute units
-int tile_for(int64_t m, int64_t n) { return tiles_of(m, n, 256) >= 192 ? 256 : 128; }
+int tile_for(int64_t m, int64_t n, int planes) { return planes == 1 && tiles_of(m, n, 256) >= 192 ? 256 : 128; }
 
 // Parts of the summed axis, so that there are about two workgroups of 128 tiles to a
 // compute unit, of 512 elements or more
@@ -589,8 +589,8 @@ struct Split {
     int tile, n;
     int64_t k;
 };
-Split split_for(int64_t m, int64_t n, int64_t k) {
-    Split s{tile_for(m, n), 1, up(k, 64)};
+Split split_for(int64_t m, int64_t n, int64_t k, int planes) {
+    Split s{tile_for(m, n, planes), 1, up(k, 64)};
     if (s.tile == 256) return s;
     int64_t want = 512 / tiles_of(m, n, 128), most = (k + 511) / 512;
     want = want < 1 ? 1 : want > most ? most : want;
@@ -630,9 +630,9 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
     p.bytes = at;
     if (grad) {
         at = begin;
-        const Split dh = split_for(rows, dim, p.piece);
+        const Split dh = split_for(rows, dim, p.piece, p.planes);
         const int64_t full = p.pieces > 1 ? p.piece : actions, last = actions - (p.pieces - 1) * p.piece;
-        const int64_t dw_full = split_for(full, dim, rows).n * full, dw_last = split_for(last, dim, rows).n * last;
+        const int64_t dw_full = split_for(full, dim, rows, p.planes).n * full, dw_last = split_for(last, dim, rows, p.planes).n * last;
         p.h_dw = take(p.planes == 2 ? (size_t)rows * p.ld * 4 : 0);
         p.g = take((size_t)rows * p.piece * 2 * p.g_planes);
         p.db_part = take((size_t)((rows + 127) / 128) * p.piece * 4);
@@ -672,7 +672,7 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
         const int64_t blocks = by_row ? (q.rows + 3) / 4 : (q.rows * (p.ld / 8) + 4 * kNT - 1) / (4 * kNT);
         c.c[n++] = Convert{q, (uint16_t*)(base + at), p.ld, by_row ? (float*)(base + p.row_factor) : nullptr, top, zero_off,
                            (int)(blocks < 4096 ? blocks : 4096)};
-        return Side16{(const uint16_t*)(base + at), q.rows * p.ld, p.ld, q.rows};
+        return Side16{(const uint16_t*)(base + at), 0, p.ld, q.rows};
     };
     // both in place or both converted, but for H of the gradients: the summed axis is as long in one as in the other
     const bool copy = !in_place(a.w) || (!grad && !in_place(a.h));
@@ -700,51 +700,55 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
     return hipGetLastError();
 }
 
-template <bool GRAD>
-hipError_t launch_logits(LogitArgs a, bool brain, hipStream_t stream) {
-    const int tile = tile_for(a.rows, a.actions);
-    a.m_tiles = (int)((a.rows + tile - 1) / tile);
-    a.n_tiles = (int)(((GRAD ? a.ldg : a.actions) + tile - 1) / tile);
-    auto launch = [&](auto is_brain, auto t) {
-        constexpr int TILE = decltype(t)::value;
-        auto kernel = policy_logits_kernel<decltype(is_brain)::value, TILE, GRAD>;
-        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile16<TILE>::LDS);
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles)), dim3(Tile16<TILE>::NT), Tile16<TILE>::LDS, stream, a);
-        return hipGetLastError();
-    };
+// f(binary16 or bfloat16, tile, planes); two planes take tiles of 128
+template <typename F>
+hipError_t by_operands(bool brain, int planes, int tile, F f) {
+    typedef std::integral_constant<int, 1> One;
+    typedef std::integral_constant<int, 2> Two;
     typedef std::integral_constant<int, 128> T128;
     typedef std::integral_constant<int, 256> T256;
-    if (tile == 256) return brain ? launch(std::true_type(), T256()) : launch(std::false_type(), T256());
-    return brain ? launch(std::true_type(), T128()) : launch(std::false_type(), T128());
+    if (planes == 2) f(std::false_type(), T128(), Two());
+    else if (tile == 256) brain ? f(std::true_type(), T256(), One()) : f(std::false_type(), T256(), One());
+    else brain ? f(std::true_type(), T128(), One()) : f(std::false_type(), T128(), One());
+    return hipGetLastError();
+}
+
+template <bool GRAD>
+hipError_t launch_logits(LogitArgs a, bool brain, int planes, hipStream_t stream) {
+    const int tile = tile_for(a.rows, a.actions, planes);
+    a.m_tiles = (int)((a.rows + tile - 1) / tile);
+    a.n_tiles = (int)(((GRAD ? a.ldg : a.actions) + tile - 1) / tile);
+    return by_operands(brain, planes, tile, [&](auto is_brain, auto t, auto pl) {
+        typedef Tile16<decltype(t)::value, decltype(pl)::value> T;
+        auto kernel = policy_logits_kernel<decltype(is_brain)::value, decltype(t)::value, GRAD, decltype(pl)::value>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles)), dim3(T::NT), T::LDS, stream, a);
+    });
 }
 
 // `joined`: partial sums that make up the result, at least those of this launch
 template <bool AC>
-hipError_t launch_grad_product(GradArgs a, const Split& s, int joined, bool brain, hipStream_t stream) {
+hipError_t launch_grad_product(GradArgs a, const Split& s, int joined, bool brain, int planes, hipStream_t stream) {
     a.m_tiles = (int)((a.m + s.tile - 1) / s.tile);
     a.n_tiles = (int)((a.n + s.tile - 1) / s.tile);
     a.splits = s.n;
     a.k_split = s.k;
     void* out = a.out;
     if (joined > 1) a.out = nullptr;
-    auto launch = [&](auto is_brain, auto t) {
-        constexpr int TILE = decltype(t)::value;
-        auto kernel = policy_grad_kernel<decltype(is_brain)::value, TILE, AC>;
-        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, Tile16<TILE>::LDS);
-        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles * a.splits)), dim3(Tile16<TILE>::NT), Tile16<TILE>::LDS,
-                           stream, a);
-    };
-    typedef std::integral_constant<int, 128> T128;
-    typedef std::integral_constant<int, 256> T256;
-    if (s.tile == 256) brain ? launch(std::true_type(), T256()) : launch(std::false_type(), T256());
-    else brain ? launch(std::true_type(), T128()) : launch(std::false_type(), T128());
-    if (joined > 1 && out) {
+    hipError_t e = by_operands(brain, planes, s.tile, [&](auto is_brain, auto t, auto pl) {
+        typedef Tile16<decltype(t)::value, decltype(pl)::value> T;
+        auto kernel = policy_grad_kernel<decltype(is_brain)::value, decltype(t)::value, AC, decltype(pl)::value>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+        hipLaunchKernelGGL(kernel, dim3((uint32_t)(a.m_tiles * a.n_tiles * a.splits)), dim3(T::NT), T::LDS, stream, a);
+    });
+    if (e == hipSuccess && joined > 1 && out) {
         a.out = out;
         a.splits = joined;
         const int64_t blocks = (a.m * ((a.n + 7) / 8) + kNT - 1) / kNT;
         hipLaunchKernelGGL(policy_join_kernel, dim3((uint32_t)(blocks < 2048 ? blocks : 2048)), dim3(kNT), 0, stream, a);
+        e = hipGetLastError();
     }
-    return hipGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -756,13 +760,13 @@ hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream) {
     hipError_t e = prepare(a, p, false, &o, stream);
     if (e != hipSuccess) return e;
     LogitArgs l{};
-    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor, l.segs = p.planes == 2 ? 3 : 1;
+    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor;
     l.bias = a.bias, l.taken = a.taken;
     l.rows = a.h.rows, l.actions = l.all_actions = a.w.rows;
     l.part = (Soft*)(base + p.part), l.z_taken = (float*)(base + p.z_taken);
-    e = launch_logits<false>(l, a.h.dtype == IQLH_BF16, stream);
+    e = launch_logits<false>(l, a.h.dtype == IQLH_BF16, p.planes, stream);
     if (e != hipSuccess) return e;
-    const int tile = tile_for(l.rows, l.actions);
+    const int tile = tile_for(l.rows, l.actions, p.planes);
     const FinishArgs f{l.part, l.z_taken, a.taken, a.row_weights, a.nll, a.lse_out, a.loss, (double*)(base + p.loss_part),
                        a.flags, l.rows, l.actions, (int)((l.actions + tile - 1) / tile), a.scale};
     return launch_finish(f, stream);
@@ -777,27 +781,27 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
     Operands o;
     hipError_t e = prepare(a, p, true, &o, stream);
     LogitArgs l{};
-    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor, l.segs = p.planes == 2 ? 3 : 1;
+    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor;
     l.taken = a.taken, l.row_weights = a.row_weights, l.lse = a.lse_in;
     l.rows = rows, l.all_actions = actions, l.scale = (float)a.scale;
     l.g = (uint16_t*)(base + p.g), l.g_planes = p.g_planes;
-    const Split dh = split_for(rows, dim, p.piece);
+    const Split dh = split_for(rows, dim, p.piece, p.planes);
     for (int k = 0; k < p.pieces && e == hipSuccess; ++k) {
         const int64_t first = k * p.piece, n = actions - first < p.piece ? actions - first : p.piece;
         l.first = first, l.actions = n, l.ldg = up(n, 64), l.plane = rows * l.ldg;
-        l.w.p = o.w.p + first * o.w.ld, l.w.n = n;
+        l.w.p = o.w.p + p.planes * first * o.w.ld, l.w.n = n;
         l.bias = a.bias ? a.bias + first : nullptr;
         l.db_part = a.d_bias ? (float*)(base + p.db_part) : nullptr;
-        e = launch_logits<true>(l, brain, stream);
+        e = launch_logits<true>(l, brain, p.planes, stream);
         if (e != hipSuccess) break;
         if (a.d_bias) {
-            const int tile = tile_for(rows, n);
+            const int tile = tile_for(rows, n, p.planes);
             hipLaunchKernelGGL(policy_bias_kernel, dim3((uint32_t)((n + kNT - 1) / kNT)), dim3(kNT), 0, stream, l.db_part,
                                (int)((rows + tile - 1) / tile), l.ldg, o.f ? &o.f->db : nullptr, a.d_bias + first, n);
             e = hipGetLastError();
         }
         GradArgs g{};
-        g.n = dim, g.segs = p.planes == 2 ? 3 : p.g_planes == 2 ? 2 : 1, g.ld_sums = up(dim, 8), g.out_dtype = a.h.dtype;
+        g.n = dim, g.both = p.planes == 1 && p.g_planes == 2, g.ld_sums = up(dim, 8), g.out_dtype = a.h.dtype;
         const Side16 gs{l.g, l.plane, l.ldg, rows};
         if (a.d_weight && e == hipSuccess) {
             g.a = Side16{l.g, l.plane, l.ldg, l.ldg};
@@ -808,8 +812,8 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
             g.sums = (float*)(base + p.dw_sums);
             g.out = (uint8_t*)a.d_weight + first * a.ld_dw * es;
             g.ld_out = a.ld_dw;
-            const Split s = split_for(n, dim, rows);
-            e = launch_grad_product<true>(g, s, s.n, brain, stream);
+            const Split s = split_for(n, dim, rows, p.planes);
+            e = launch_grad_product<true>(g, s, s.n, brain, p.planes, stream);
         }
         if (a.d_hidden && e == hipSuccess) {
             g.a = gs;
@@ -823,7 +827,7 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
             g.ld_out = a.ld_dh;
             Split s = dh;
             s.n = (int)((n + s.k - 1) / s.k);
-            e = launch_grad_product<false>(g, s, p.pieces > 1 ? dh.n : s.n, brain, stream);
+            e = launch_grad_product<false>(g, s, p.pieces > 1 ? dh.n : s.n, brain, p.planes, stream);
         }
     }
     return e;

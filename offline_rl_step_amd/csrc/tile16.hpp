@@ -8,9 +8,10 @@
 //
 // An operand that stands for binary32 values is two binary16 matrices (planes):
 // x = (hi + lo) 2^-s, hi the nearest binary16 to 2^s x and lo the nearest to the rest,
-// 22 bits together.  A product of two such operands is three products (lo hi, hi lo,
-// hi hi; lo lo lies below the last bit), taken as one sum of three times the length.
-// That is 2.5 PF / 3 against the 0.16 PF of the binary32 matrix instructions.
+// 22 bits together.  A product of two such operands is three products, lo hi + hi lo + hi
+// hi (lo lo lies below the last bit): 2.5 PF / 3 against the 0.16 PF of the binary32
+// matrix instructions.  The planes lie in one matrix of twice the row length, 32 elements of hi and their 32
+// of lo in turn, so that a step of 32 k reads whole cache lines.
 #pragma once
 #include <type_traits>
 
@@ -27,12 +28,15 @@ typedef float mm_f16 __attribute__((ext_vector_type(16)));
 typedef _Float16 mm_h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 mm_b8 __attribute__((ext_vector_type(8)));
 
-// One operand.  n: bound of i (rows: the last row is read again behind it; columns: zeros, n a multiple
-// of 8).  p 16-byte aligned, ld a multiple of 8, planes `plane` elements apart.
+// One operand.  n: bound of i (rows: the last row is read again behind it; columns: another element, n a
+// multiple of 8).  p 16-byte aligned, ld a multiple of 8, of 64 with two planes.  plane: elements to a second
+// matrix that holds what this one rounds off (tile_product's `both`).
 struct Side16 {
     const uint16_t* p;
     int64_t plane, ld, n;
 };
+// Place of element (row, col) of two planes, ld columns; that of the rest is 32 elements behind
+IQLH_DEV int64_t planes_at(int64_t row, int64_t ld, int64_t col) { return 2 * (row * ld + col) - (col & 31); }
 
 template <bool BRAIN>
 IQLH_DEV mm_f16 mma16(uint4 a, uint4 b, mm_f16 c) {
@@ -42,18 +46,16 @@ IQLH_DEV mm_f16 mma16(uint4 a, uint4 b, mm_f16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(mm_h8, a), __builtin_bit_cast(mm_h8, b), c, 0, 0, 0);
 }
 
-#ifndef WN256
-#define WN256 4
-#endif
-template <int TILE>
+template <int TILE, int PL = 1>
 struct Tile16 {
-    static constexpr int WM = 2, WN = TILE == 256 ? WN256 : 2;    // waves
+    static constexpr int WM = 2, WN = TILE / 64;                    // waves
     static constexpr int FA = TILE / 32 / WM, FB = TILE / 32 / WN;  // fragments of 32 x 32 of a wave
     static constexpr int NT = 64 * WM * WN;
-    static constexpr int SIDE = TILE * 128;    // one operand's part of a step: 64 k
+    static constexpr int BK = PL == 2 ? 32 : 64;  // k of a step
+    static constexpr int SIDE = TILE * 128;       // one operand in a step
     static constexpr int STAGE = 2 * SIDE;
-    static constexpr int CP = SIDE / 16 / NT;  // copies of a thread, side and step
-    static constexpr int RING = 2 * STAGE;     // two steps; also the staged sums of BAND rows
+    static constexpr int CP = SIDE / 16 / NT;     // copies of a thread, operand and step
+    static constexpr int RING = 2 * STAGE;        // also the staged sums of BAND rows
     static constexpr int LDS = RING + 16 * TILE;  // and what an epilogue keeps of rows and columns meanwhile
     static constexpr int BANDS = TILE == 256 ? 2 : 1, BAND = TILE / BANDS;
     static constexpr int PER_CU = TILE == 256 ? 1 : 2, PER_SIMD = PER_CU * NT / 256;
@@ -64,36 +66,40 @@ struct Tile16 {
 template <int TILE> IQLH_DEV int wave_m() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / Tile16<TILE>::WN * (32 * Tile16<TILE>::FA); }
 template <int TILE> IQLH_DEV int wave_n() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % Tile16<TILE>::WN * (32 * Tile16<TILE>::FB); }
 
-// The sums over k in [k0, k1) (multiples of 64 but for k1, which is one of 8 for operands in rows; SEGS
-// 1, or 3 for operands of two planes).  Lane l: acc[i][j][4 g + e] is m = wave_m + 32 i + (l & 31), n
-// = wave_n + 32 j + 8 g + 4 (l >> 5) + e.  When it returns, LDS is free.
+// The sums over k in [k0, k1): multiples of 64 but for k1, which is one of 8 for operands in rows.  PL 2: operands
+// of two planes, binary16.  both: a's second matrix and a, each times b.  Lane l: acc[i][j][4 g + e] is m =
+// wave_m + 32 i + (l & 31), n = wave_n + 32 j + 8 g + 4 (l >> 5) + e.  Every step of 16 k is added in
+// the same order whatever the tile.  When it returns, the ring in LDS is free.
 //
-// Two buffers of 64 k in LDS, filled by asynchronous copies: in the last quarter of
-// step s every wave waits for its copies of step s + 1, passes the barrier (behind
-// which all reads of step s's buffer are done), issues step s + 2 into that buffer and
-// reads the first fragments of step s + 1 while the quarter's matrix instructions run.
-// Rows: 128 bytes of a row, its 16-byte chunk u at u ^ ((row >> 1) & 7), so that 16
+// Two steps in LDS, filled by asynchronous copies: in its last part of 16 k step s waits
+// for the copies of step s + 1, passes the barrier (behind which all reads of its own buffer are
+// done), issues those of step s + 2 into that buffer and reads the first fragments of
+// step s + 1 while the part's matrix instructions run; LDS reads and matrix instructions alternate.
+// Rows: 128 bytes of a row, a whole cache line, its 16-byte chunk u at u ^ ((row >> 1) & 7), so that 16
 // lanes' reads fall on all banks.  Columns: TILE elements of one k, chunk u at u ^ 4 (k
 // & 3): a transposing read takes 4 k of 16 neighbouring elements in 16 lanes, 32 lanes
 // all banks.
-template <bool BRAIN, int TILE, bool AC, bool BC>
-IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1, int segs,
+template <bool BRAIN, int TILE, bool AC, bool BC, int PL = 1>
+IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1, bool both,
                            uint8_t* lds, mm_f16 (&acc)[Tile16<TILE>::FA][Tile16<TILE>::FB]) {
-    typedef Tile16<TILE> T;
-    constexpr int NT = T::NT, FA = T::FA, FB = T::FB, CPR = TILE / 8, CP = T::CP, KR = NT / CPR;
+    typedef Tile16<TILE, PL> T;
+    constexpr int NT = T::NT, FA = T::FA, FB = T::FB, BK = T::BK, CP = T::CP;
+    constexpr int CPR = PL * TILE / 8, KR = NT / CPR, PARTS = BK / 16;
+    static_assert(CP * KR == BK && CP * (NT / 8) == TILE, "copies of a step");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 31, h = lane >> 5, li = lane & 15, half = lane >> 4 & 1;
     const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-    const int per = (int)((k1 - k0 + 63) / 64), steps = per * segs;
+    const int per = (int)((k1 - k0 + BK - 1) / BK), steps = both ? 2 * per : per;
     // what a thread copies: chunk i NT + tid of a side
-    const int ru = (tid & 7) ^ ((tid >> 4) & 7);                    // rows: chunk of the row
-    const int ck = tid / CPR, cu = (tid % CPR) ^ (4 * (ck & 3));    // columns: k, chunk of it
+    const int ru = (tid & 7) ^ ((tid >> 4) & 7), rk = 8 * (PL == 2 ? ru & 3 : ru);  // rows: chunk of the row, its k
+    const int ck = tid / CPR, cu = (tid % CPR) ^ (4 * (ck & 3));                    // columns: k, chunk of it
+    const int ci = PL == 2 ? cu / 8 * 32 + (cu & 3) * 8 : cu * 8;
     auto offset = [&](const Side16& s, bool cols, int64_t i0, int i) __attribute__((always_inline)) -> uint32_t {
-        if (cols) return (uint32_t)((KR * i + ck) * s.ld * 2) + 16u * (i0 + 8 * cu < s.n ? cu : 0);
+        if (cols) return (uint32_t)((KR * i + ck) * s.ld * (2 * PL)) + 16u * (i0 + ci < s.n ? cu : 0);
         const int row = i * (NT / 8) + (tid >> 3);
         const int64_t left = s.n - i0 - 1;
-        return (uint32_t)((row < left ? row : (int)left) * s.ld * 2) + 16u * ru;
+        return (uint32_t)((row < left ? row : (int)left) * s.ld * (2 * PL)) + 16u * ru;
     };
     uint32_t offa[CP], offb[CP];
 #pragma unroll
@@ -101,20 +107,21 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
         offa[i] = offset(a, AC, m0, i);
         offb[i] = offset(b, BC, n0, i);
     }
-    int seg = segs == 1 ? 2 : 0, step_in = 0;
+    int step_in = 0;
+    bool rest = both;
     auto issue = [&](int s) __attribute__((always_inline)) {
         if (s >= steps) return;
         const uint32_t dst = lds_at + (s & 1) * T::STAGE + wave * 1024;
-        const int64_t kk = k0 + (int64_t)step_in * 64;
-        const uint8_t* pa = (const uint8_t*)(a.p + (seg == 0 ? a.plane : 0) + (AC ? kk * a.ld + m0 : m0 * a.ld + kk));
-        const uint8_t* pb = (const uint8_t*)(b.p + (seg == 1 ? b.plane : 0) + (BC ? kk * b.ld + n0 : n0 * b.ld + kk));
-        if (kk + 64 <= k1) {
+        const int64_t kk = k0 + (int64_t)step_in * BK;
+        const uint8_t* pb = (const uint8_t*)(b.p + PL * (BC ? kk * b.ld + n0 : n0 * b.ld + kk));
+        const uint8_t* pa = (const uint8_t*)(a.p + (rest ? a.plane : 0) + PL * (AC ? kk * a.ld + m0 : m0 * a.ld + kk));
+        if (kk + BK <= k1) {
 #pragma unroll
             for (int i = 0; i < CP; ++i) copy16(pb, offb[i], dst + i * NT * 16);
 #pragma unroll
             for (int i = 0; i < CP; ++i) copy16(pa, offa[i], dst + T::SIDE + i * NT * 16);
         } else {  // zeros behind k1
-            const bool row_in = kk + 8 * ru < k1;
+            const bool row_in = kk + rk < k1;
 #pragma unroll
             for (int i = 0; i < CP; ++i)
                 copy16((BC ? kk + KR * i + ck < k1 : row_in) ? pb + offb[i] : (const uint8_t*)kZeroChunk, dst + i * NT * 16);
@@ -123,73 +130,76 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
                 copy16((AC ? kk + KR * i + ck < k1 : row_in) ? pa + offa[i] : (const uint8_t*)kZeroChunk,
                        dst + T::SIDE + i * NT * 16);
         }
-        step_in = step_in + 1 == per ? 0 : step_in + 1;
-        seg += step_in == 0 ? (segs == 2 ? 2 : 1) : 0;
+        if (++step_in == per) step_in = 0, rest = false;
     };
     const int wm = wave / T::WN * (32 * FA), wn = wave % T::WN * (32 * FB);
-    // where a lane reads: rows, the row's start (the chunk goes by the quarter); columns, the fragment's chunk of the lane's k
-    const int row_at = r * 128;
+    // where a lane reads: rows, the row's start (the chunk goes by the part); columns, the fragment's chunk of the lane's k
     auto col_at = [&](int i0) __attribute__((always_inline)) {
-        return (8 * h + (li >> 2)) * (2 * TILE) + 16 * ((i0 / 8 + 2 * half + ((li & 3) >> 1)) ^ (4 * (li >> 2))) + 8 * (li & 1);
+        return (8 * h + (li >> 2)) * (2 * PL * TILE) + 16 * ((PL * i0 / 8 + 2 * half + ((li & 3) >> 1)) ^ (4 * (li >> 2))) + 8 * (li & 1);
     };
     int ca[FA], cb[FB];
 #pragma unroll
-    for (int i = 0; i < FA; ++i) ca[i] = AC ? T::SIDE + col_at(wm + 32 * i) : T::SIDE + (wm + 32 * i) * 128 + row_at;
+    for (int i = 0; i < FA; ++i) ca[i] = T::SIDE + (AC ? col_at(wm + 32 * i) : (wm + 32 * i + r) * 128);
 #pragma unroll
-    for (int i = 0; i < FB; ++i) cb[i] = BC ? col_at(wn + 32 * i) : (wn + 32 * i) * 128 + row_at;
+    for (int i = 0; i < FB; ++i) cb[i] = BC ? col_at(wn + 32 * i) : (wn + 32 * i + r) * 128;
     struct Frags {
-        uint4 a[FA], b[FB];
+        uint4 a[PL][FA], b[PL][FB];
     } f[2];
     typedef short s4 __attribute__((ext_vector_type(4)));
-    auto read = [&](const uint8_t* buf, int at, auto cols, auto quarter) __attribute__((always_inline)) -> uint4 {
-        constexpr int Q = decltype(quarter)::value;
+    auto read = [&](const uint8_t* buf, int at, auto cols, auto part, int p) __attribute__((always_inline)) -> uint4 {
+        constexpr int Q = decltype(part)::value;
         if constexpr (decltype(cols)::value) {
             typedef __attribute__((address_space(3))) s4 lds_s4;
-            const uint8_t* p = buf + at + Q * (32 * TILE);
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 8 * TILE));
+            const uint8_t* q = buf + (at ^ (p * 64)) + Q * (32 * PL * TILE);  // the rest: 4 chunks on
+            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)q);
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(q + 8 * PL * TILE));
             const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
             return uint4{l.x, l.y, u.x, u.y};
         } else {
-            return *(const uint4*)(buf + at + 16 * ((2 * Q + h) ^ ((r >> 1) & 7)));
+            return *(const uint4*)(buf + at + 16 * ((2 * Q + h + 4 * p) ^ ((r >> 1) & 7)));
         }
     };
     typedef std::integral_constant<bool, AC> CA;
     typedef std::integral_constant<bool, BC> CB;
-    auto load = [&](int s, auto quarter, auto p) __attribute__((always_inline)) {
+    auto load = [&](int s, auto part, auto set) __attribute__((always_inline)) {
         const uint8_t* buf = lds + (s & 1) * T::STAGE;
-        Frags& g = f[decltype(p)::value];
+        Frags& g = f[decltype(set)::value];
 #pragma unroll
-        for (int i = 0; i < FB; ++i) g.b[i] = read(buf, cb[i], CB(), quarter);
+        for (int p = PL - 1; p >= 0; --p) {
 #pragma unroll
-        for (int i = 0; i < FA; ++i) g.a[i] = read(buf, ca[i], CA(), quarter);
+            for (int i = 0; i < FB; ++i) g.b[p][i] = read(buf, cb[i], CB(), part, p);
+#pragma unroll
+            for (int i = 0; i < FA; ++i) g.a[p][i] = read(buf, ca[i], CA(), part, p);
+        }
     };
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FB; ++j) acc[i][j] = mm_f16{};
-    auto mma = [&](auto p) __attribute__((always_inline)) {
-        const Frags& g = f[decltype(p)::value];
+    auto mma = [&](auto set) __attribute__((always_inline)) {
+        const Frags& g = f[decltype(set)::value];
 #pragma unroll
-        for (int i = 0; i < FA; ++i)
+        for (int t = PL == 2 ? 0 : 2; t < 3; ++t)  // lo hi, hi lo, hi hi
 #pragma unroll
-            for (int j = 0; j < FB; ++j) acc[i][j] = mma16<BRAIN>(g.b[j], g.a[i], acc[i][j]);
+            for (int i = 0; i < FA; ++i)
+#pragma unroll
+                for (int j = 0; j < FB; ++j) acc[i][j] = mma16<BRAIN>(g.b[t == 1][j], g.a[t == 0][i], acc[i][j]);
     };
-    typedef std::integral_constant<int, 0> C0;
-    typedef std::integral_constant<int, 1> C1;
-    typedef std::integral_constant<int, 2> C2;
-    typedef std::integral_constant<int, 3> C3;
-    // per quarter: the next one's LDS reads, then this one's matrix instructions
-    constexpr int READS = (AC ? 2 : 1) * FA + (BC ? 2 : 1) * FB;
-    auto reads_first = [] __attribute__((always_inline)) {
-        constexpr int M = FB * FA, EACH = (READS + M - 1) / M;
+    // a part's matrix instructions, with the next one's LDS reads between them
+    constexpr int READS = PL * ((AC ? 2 : 1) * FA + (BC ? 2 : 1) * FB), MMAS = FA * FB * (PL == 2 ? 3 : 1);
+    auto interleave = [] __attribute__((always_inline)) {
+        constexpr int EACH = (READS + MMAS - 1) / MMAS;
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
+        for (int i = 0; i < MMAS; ++i) {
             if (i * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    typedef std::integral_constant<int, 0> C0;
+    typedef std::integral_constant<int, 1> C1;
+    typedef std::integral_constant<int, 2> C2;
+    typedef std::integral_constant<int, 3> C3;
     issue(0);
     wait_vm<0>();
     bar();
@@ -198,19 +208,21 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     for (int s = 0; s < steps; ++s) {
         load(s, C1(), C1());
         mma(C0());
-        reads_first();
-        load(s, C2(), C0());
-        mma(C1());
-        reads_first();
-        load(s, C3(), C1());
-        mma(C0());
-        reads_first();
+        interleave();
+        if constexpr (PARTS == 4) {
+            load(s, C2(), C0());
+            mma(C1());
+            interleave();
+            load(s, C3(), C1());
+            mma(C0());
+            interleave();
+        }
         wait_vm<0>();  // step s + 1 has landed
         bar();
         issue(s + 2);
         load(s + 1, C0(), C0());
         mma(C1());
-        reads_first();
+        interleave();
     }
     wait_vm<0>();  // the copies behind the last step, before their buffers are used again
     bar();
@@ -327,9 +339,10 @@ IQLH_DEV void store8_of(int dtype, void* base, int64_t at, int64_t n, const floa
     }
 }
 
-// Eight values as binary16 planes: hi, and with lo the rest.  A value that is not
-// finite has no rest.
-IQLH_DEV void put_planes(uint16_t* p, int64_t plane, bool two, const float (&v)[8]) {
+// Eight values of row `row`, columns col.. (col a multiple of 8), of a binary16 matrix of one or two
+// planes.  A value that is not finite has no rest.
+IQLH_DEV void put_planes(uint16_t* base, int64_t row, int64_t ld, int64_t col, bool two, const float (&v)[8]) {
+    uint16_t* p = base + (two ? planes_at(row, ld, col) : row * ld + col);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -340,15 +353,16 @@ IQLH_DEV void put_planes(uint16_t* p, int64_t plane, bool two, const float (&v)[
         }
     }
     *(uint4*)p = uint4{hi[0], hi[1], hi[2], hi[3]};
-    if (two) *(uint4*)(p + plane) = uint4{lo[0], lo[1], lo[2], lo[3]};
+    if (two) *(uint4*)(p + 32) = uint4{lo[0], lo[1], lo[2], lo[3]};
 }
-IQLH_DEV void get_planes(const uint16_t* p, int64_t plane, bool two, float (&v)[8]) {
+IQLH_DEV void get_planes(const uint16_t* base, int64_t row, int64_t ld, int64_t col, bool two, float (&v)[8]) {
+    const uint16_t* p = base + (two ? planes_at(row, ld, col) : row * ld + col);
     const uint4 h = *(const uint4*)p;
     const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = half_of(hw[i >> 1], i & 1);
     if (two) {
-        const uint4 l = *(const uint4*)(p + plane);
+        const uint4 l = *(const uint4*)(p + 32);
         const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += half_of(lw[i >> 1], i & 1);
