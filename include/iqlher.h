@@ -725,7 +725,8 @@ typedef struct iqlh_matrix_set {
     size_t workspace_bytes;   /* what iqlh_orthogonalize and iqlh_muon_step take */
     int32_t count;            /* matrices                                      */
     int32_t units;            /* pieces of the elementwise passes              */
-    int32_t sym_tiles, rect_tiles;  /* tiles of the products                   */
+    int32_t sym_tiles, rect_tiles;  /* tiles of the products,                  */
+    int32_t sym_tile, rect_tile;    /* and their outputs along each side       */
     int32_t momentum;         /* 1 when the matrices have one                  */
     int32_t reserved0;
 } iqlh_matrix_set;

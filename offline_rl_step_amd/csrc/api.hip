@@ -1212,20 +1212,82 @@ int iqlh_policy_loss_grad(const iqlh_policy_head* head, const int32_t* taken, co
 
 // ------------------------------------- orthogonalised updates of matrices
 namespace {
+constexpr int32_t kMostMatrices = 4096;
 int32_t pad64(int64_t n) { return (int32_t)((n + 63) / 64 * 64); }
 struct OrthoCounts {
     int64_t units, sym, rect;
+    int32_t sym_tile, rect_tile;
 };
-// pieces and tiles of one matrix
-OrthoCounts ortho_counts(const iqlh_matrix& m, OrthoMat* q) {
-    const int32_t rp = pad64(m.rows), cp = pad64(m.cols), kp = rp < cp ? rp : cp;
+int64_t tiles_along(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+// sizes and pieces of one matrix
+OrthoMat ortho_sizes(const iqlh_matrix& m) {
+    OrthoMat q;
+    std::memset(&q, 0, sizeof(q));
+    const int32_t rp = pad64(m.rows), cp = pad64(m.cols);
     // pieces of 8192 elements or more, 512 of them at most: their sums are added by every piece's workgroup
     int32_t ur = (8192 + cp - 1) / cp;
     if (ur < (rp + 511) / 512) ur = (rp + 511) / 512;
-    const int64_t t = kOrthoTile, ts = (kp + t - 1) / t;
-    q->rows = (int32_t)m.rows, q->cols = (int32_t)m.cols, q->rows_pad = rp, q->cols_pad = cp, q->k_pad = kp;
-    q->unit_rows = ur, q->units = (rp + ur - 1) / ur;
-    return OrthoCounts{q->units, ts * (ts + 1) / 2, ((rp + t - 1) / t) * ((cp + t - 1) / t)};
+    q.rows = (int32_t)m.rows, q.cols = (int32_t)m.cols, q.rows_pad = rp, q.cols_pad = cp, q.k_pad = rp < cp ? rp : cp;
+    q.unit_rows = ur, q.units = (rp + ur - 1) / ur;
+    q.planes = m.compute_dtype == IQLH_F32 || m.rows < 64 || m.cols < 64 ? 2 : 1;
+    return q;
+}
+int64_t sym_tiles(const OrthoMat& q, int64_t tile) { return tiles_along(q.k_pad, tile) * (tiles_along(q.k_pad, tile) + 1) / 2; }
+int64_t rect_tiles(const OrthoMat& q, int64_t tile) { return tiles_along(q.rows_pad, tile) * tiles_along(q.cols_pad, tile); }
+
+// Time of one tile of a product of `length` summed elements, us: a part for its start and its results, and one
+// for each step (64 elements, 32 of two planes).  Measured, tiles filling the chip | fewer than compute units:
+//   256: 19 + 1.9 a step, two planes 19 + 2.8 | 10 + 1.6, 10 + 1.7      (one to a compute unit)
+//   128: 12 + 1.27, 12 + 1.65                 | 8 + 0.75, 8 + 0.96     (two)
+//   64:  6 + 0.6, 6 + 0.62                    | 4 + 0.4, 4 + 0.42      (two)
+double tile_time(int32_t tile, int32_t planes, int64_t length, bool full) {
+    static const double start[3][2] = {{4, 6}, {8, 12}, {10, 19}};
+    static const double step[3][2][2] = {{{0.4, 0.6}, {0.42, 0.62}}, {{0.75, 1.27}, {0.96, 1.65}}, {{1.6, 1.9}, {1.7, 2.8}}};
+    const int t = tile / 128;
+    const int64_t n = planes == 2 ? (length + 31) / 32 : (length + 63) / 64;
+    return start[t][full] + step[t][planes - 1][full] * (double)n;
+}
+// Time of one launch over the list's tiles, longest sums first, each taken by the first place that is free; above 16384
+// tiles the places' common share.
+//   which 0: X X^T, 1: its square, 2: the product with X
+double launch_time(const iqlh_matrix* ms, const int32_t* order, int32_t count, int32_t tile, int which) {
+    const int slots = tile == 256 ? 256 : 512;
+    int64_t all = 0;
+    for (int i = 0; i < count; ++i) {
+        const OrthoMat q = ortho_sizes(ms[i]);
+        all += which == 2 ? rect_tiles(q, tile) : sym_tiles(q, tile);
+    }
+    const bool full = all > 256 - 64 * (tile == 256);
+    double busy[512] = {}, sum = 0.0, end = 0.0;
+    auto later = [](double a, double b) { return a > b; };
+    for (int k = 0; k < count; ++k) {
+        const OrthoMat q = ortho_sizes(ms[order[k]]);
+        const int64_t n = which == 2 ? rect_tiles(q, tile) : sym_tiles(q, tile);
+        const double t = tile_time(tile, q.planes, which == 0 ? (q.rows_pad > q.cols_pad ? q.rows_pad : q.cols_pad) : q.k_pad, full);
+        sum += t * (double)n;
+        if (all > 16384) continue;
+        for (int64_t j = 0; j < n; ++j) {
+            std::pop_heap(busy, busy + slots, later);
+            busy[slots - 1] += t;
+            end = busy[slots - 1] > end ? busy[slots - 1] : end;
+            std::push_heap(busy, busy + slots, later);
+        }
+    }
+    return all > 16384 ? sum / slots : end;
+}
+// The tile that takes the least time.  (Lists of one stack of four square weights and three of width 4 H, us a
+// launch by 64 | 128 | 256: H 1024 in two planes 114 | 118 | 229, 61 | 60 | 101, 192 | 130 | 109 for the three products; H
+// 777 81 | 102 | 180, 45 | 47 | 85, 108 | 89 | 81; H 2048 in one 393 | 215 | 224, 158 | 122 | 97, 655 | 424 | 327; 512 x 256
+// and 512 x 512, twice: 10 | 23 | 46, 11 | 29 | 58, 10 | 21 | 45.)
+int32_t best_tile(const iqlh_matrix* ms, const int32_t* order, int32_t count, bool sym) {
+    int32_t best = 0;
+    double least = 0.0;
+    for (int32_t tile = 64; tile <= 256; tile *= 2) {
+        const double t = sym ? launch_time(ms, order, count, tile, 0) + launch_time(ms, order, count, tile, 1)
+                             : launch_time(ms, order, count, tile, 2);
+        if (!best || t < least) best = tile, least = t;
+    }
+    return best;
 }
 struct MatrixRange {
     uint64_t begin, end;
@@ -1235,10 +1297,10 @@ struct MatrixRange {
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 }  // namespace
 
-static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count, OrthoCounts* all) {
+static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count, int32_t sym_tile, int32_t rect_tile, OrthoCounts* all) {
     if (!ms) return fail(IQLH_EINVAL, "%s: NULL argument", who);
-    if (count < 1 || count > 4096) return fail(IQLH_EINVAL, "%s: count must be in [1, 4096]", who);
-    *all = OrthoCounts{0, 0, 0};
+    if (count < 1 || count > kMostMatrices)
+        return fail(IQLH_EINVAL, "%s: count must be in [1, %d]", who, kMostMatrices);
     for (int i = 0; i < count; ++i) {
         const iqlh_matrix& m = ms[i];
         if (m.rows < 1 || m.rows > 65536 || m.cols < 1 || m.cols > 65536)
@@ -1248,9 +1310,11 @@ static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count,
             return fail(IQLH_EINVAL, "%s: matrix %d has a type that is no float type", who, i);
         if (m.compute_dtype != IQLH_F16 && m.compute_dtype != IQLH_F32)
             return fail(IQLH_EINVAL, "%s: matrix %d: compute_dtype must be IQLH_F16 or IQLH_F32", who, i);
-        OrthoMat q;
-        const OrthoCounts c = ortho_counts(m, &q);
-        all->units += c.units, all->sym += c.sym, all->rect += c.rect;
+    }
+    *all = OrthoCounts{0, 0, 0, sym_tile, rect_tile};
+    for (int i = 0; i < count; ++i) {
+        const OrthoMat q = ortho_sizes(ms[i]);
+        all->units += q.units, all->sym += sym_tiles(q, all->sym_tile), all->rect += rect_tiles(q, all->rect_tile);
     }
     if (all->units > 1 << 22 || all->sym > 1 << 22 || all->rect > 1 << 22)
         return fail(IQLH_ESHAPE, "%s: the list is more than one launch takes", who);
@@ -1260,7 +1324,7 @@ static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count,
 int iqlh_matrix_set_bytes(const iqlh_matrix* matrices, int32_t count, size_t* bytes) {
     if (!bytes) return fail(IQLH_EINVAL, "iqlh_matrix_set_bytes: bytes is NULL");
     OrthoCounts n;
-    int rc = check_matrices("iqlh_matrix_set_bytes", matrices, count, &n);
+    int rc = check_matrices("iqlh_matrix_set_bytes", matrices, count, 64, 64, &n);  // the most tiles
     if (rc) return rc;
     const size_t table = up16(sizeof(OrthoMat) * (size_t)count + sizeof(OrthoTile) * (size_t)(n.units + n.sym + n.rect));
     // fill sorts the address ranges where the table comes to lie, before it writes it
@@ -1292,7 +1356,7 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
     const char* who = "iqlh_matrix_set_fill";
     OrthoCounts n;
     size_t need = 0;
-    int rc = check_matrices(who, matrices, count, &n);
+    int rc = check_matrices(who, matrices, count, 64, 64, &n);
     if (rc) return rc;
     if (!host_table || !set) return fail(IQLH_EINVAL, "%s: NULL argument", who);
     iqlh_matrix_set_bytes(matrices, count, &need);
@@ -1327,6 +1391,16 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
                 return fail(IQLH_EINVAL, "%s: %s of matrix %d and %s of matrix %d share memory", who, names[range[i].what],
                             range[i].matrix, names[range[j].what], range[j].matrix);
             }
+    // the longest sums first, so that the last tiles are short ones
+    int32_t order[kMostMatrices];
+    for (int i = 0; i < count; ++i) order[i] = i;
+    std::sort(order, order + count, [&](int32_t a, int32_t b) {
+        const OrthoMat x = ortho_sizes(matrices[a]), y = ortho_sizes(matrices[b]);
+        const int64_t lx = (int64_t)x.planes * (x.rows_pad + x.cols_pad), ly = (int64_t)y.planes * (y.rows_pad + y.cols_pad);
+        return lx != ly ? lx > ly : a < b;
+    });
+    check_matrices(who, matrices, count, best_tile(matrices, order, count, true), best_tile(matrices, order, count, false), &n);
+    std::memset(host_table, 0, need);
     OrthoMat* mats = (OrthoMat*)host_table;
     OrthoTile* units = (OrthoTile*)(mats + count);
     OrthoTile* sym = units + n.units;
@@ -1335,12 +1409,10 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
     int32_t unit0 = 0;
     for (int i = 0; i < count; ++i) {
         const iqlh_matrix& m = matrices[i];
-        OrthoMat q;
-        std::memset(&q, 0, sizeof(q));
-        const OrthoCounts c = ortho_counts(m, &q);
+        OrthoMat q = ortho_sizes(m);
         q.x = (uint64_t)(uintptr_t)m.x, q.out = (uint64_t)(uintptr_t)m.out, q.momentum = (uint64_t)(uintptr_t)m.momentum;
         q.ld_x = m.ld_x, q.ld_out = m.ld_out, q.ld_momentum = m.ld_momentum;
-        q.x_dtype = m.x_dtype, q.out_dtype = m.out_dtype, q.planes = m.compute_dtype == IQLH_F32 || m.rows < 64 || m.cols < 64 ? 2 : 1;
+        q.x_dtype = m.x_dtype, q.out_dtype = m.out_dtype;
         q.unit0 = unit0;
         const size_t x = (size_t)q.rows_pad * q.cols_pad * 2 * q.planes, s = (size_t)q.k_pad * q.k_pad * 2 * q.planes;
         q.x_at[0] = (int64_t)at, q.x_at[1] = (int64_t)(at + x), q.gram_at = (int64_t)(at + 2 * x), q.poly_at = (int64_t)(at + 2 * x + s);
@@ -1348,9 +1420,13 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
         mats[i] = q;
         for (int32_t u = 0; u < q.units; ++u) *units++ = OrthoTile{i, (uint16_t)u, 0};
         unit0 += q.units;
-        const int64_t nt = (q.cols_pad + kOrthoTile - 1) / kOrthoTile, mt = (q.rows_pad + kOrthoTile - 1) / kOrthoTile;
-        sym = put_tiles(sym, i, (q.k_pad + kOrthoTile - 1) / kOrthoTile, mt, true, c.sym);
-        rect = put_tiles(rect, i, mt, nt, false, c.rect);
+    }
+    for (int k = 0; k < count; ++k) {
+        const int32_t i = order[k];
+        const OrthoMat& q = mats[i];
+        sym = put_tiles(sym, i, tiles_along(q.k_pad, n.sym_tile), tiles_along(q.k_pad, n.sym_tile), true, sym_tiles(q, n.sym_tile));
+        rect = put_tiles(rect, i, tiles_along(q.rows_pad, n.rect_tile), tiles_along(q.cols_pad, n.rect_tile), false,
+                         rect_tiles(q, n.rect_tile));
     }
     std::memset(set, 0, sizeof(*set));
     set->table_bytes = up16((size_t)((char*)rect - (char*)host_table));
@@ -1358,6 +1434,7 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
     set->count = count;
     set->units = (int32_t)n.units, set->sym_tiles = (int32_t)n.sym, set->rect_tiles = (int32_t)n.rect;
     set->momentum = matrices[0].momentum != nullptr;
+    set->sym_tile = n.sym_tile, set->rect_tile = n.rect_tile;
     return IQLH_OK;
 }
 
@@ -1380,6 +1457,7 @@ static int make_ortho_args(const char* who, const iqlh_matrix_set* set, int32_t 
     a->part = (double*)workspace;
     a->ok = (int32_t*)(a->part + set->units);
     a->nunits = set->units, a->nsym = set->sym_tiles, a->nrect = set->rect_tiles;
+    a->sym_tile = set->sym_tile, a->rect_tile = set->rect_tile;
     a->h.eps = eps, a->h.flags = d_flags, a->h.steps = steps;
     return IQLH_OK;
 }

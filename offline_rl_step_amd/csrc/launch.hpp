@@ -302,7 +302,6 @@ struct OrthoTile {
     int32_t mat;
     uint16_t m, n;  // tile (units: m)
 };
-constexpr int kOrthoTile = 128;
 struct OrthoHyper {
     double lr, eps;
     float mu, keep;  // keep: 1 - lr weight_decay
@@ -318,6 +317,7 @@ struct OrthoArgs {
     double* part;           // [nunits]
     int32_t* ok;            // [count]
     int32_t nunits, nsym, nrect;
+    int32_t sym_tile, rect_tile;  // 64, 128 or 256
     OrthoHyper h;
 };
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);

@@ -217,10 +217,16 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
 
 template <int PHASE>
 hipError_t launch_product(const OrthoArgs& a, int from, hipStream_t stream) {
-    constexpr int TILE = kOrthoTile, bytes = Tile16<TILE>::LDS;
-    auto kernel = ortho_product_kernel<TILE, PHASE>;
-    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    hipLaunchKernelGGL(kernel, dim3(PHASE <= kPoly ? a.nsym : a.nrect), dim3(Tile16<TILE>::NT), bytes, stream, a, from);
+    auto launch = [&](auto tile) {
+        typedef Tile16<decltype(tile)::value> T;
+        auto kernel = ortho_product_kernel<decltype(tile)::value, PHASE>;
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
+        hipLaunchKernelGGL(kernel, dim3(PHASE <= kPoly ? a.nsym : a.nrect), dim3(T::NT), T::LDS, stream, a, from);
+    };
+    const int tile = PHASE <= kPoly ? a.sym_tile : a.rect_tile;
+    if (tile == 256) launch(std::integral_constant<int, 256>());
+    else if (tile == 128) launch(std::integral_constant<int, 128>());
+    else launch(std::integral_constant<int, 64>());
     return hipGetLastError();
 }
 

@@ -46,16 +46,19 @@ IQLH_DEV mm_f16 mma16(uint4 a, uint4 b, mm_f16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(mm_h8, a), __builtin_bit_cast(mm_h8, b), c, 0, 0, 0);
 }
 
+// TILE 256: eight waves, 2 x 4, each 128 x 64 outputs (4 x 2 fragments of 32 x 32).  TILE 128 and 64: four
+// waves, 2 x 2, each 64 x 64 or 32 x 32; two workgroups to a compute unit.
 template <int TILE, int PL = 1>
 struct Tile16 {
-    static constexpr int WM = 2, WN = TILE / 64;                    // waves
+    static constexpr int WM = 2, WN = TILE == 256 ? 4 : 2;          // waves
     static constexpr int FA = TILE / 32 / WM, FB = TILE / 32 / WN;  // fragments of 32 x 32 of a wave
     static constexpr int NT = 64 * WM * WN;
     static constexpr int BK = PL == 2 ? 32 : 64;  // k of a step
     static constexpr int SIDE = TILE * 128;       // one operand in a step
     static constexpr int STAGE = 2 * SIDE;
     static constexpr int CP = SIDE / 16 / NT;     // copies of a thread, operand and step
-    static constexpr int RING = 2 * STAGE;        // also the staged sums of BAND rows
+    static constexpr int NB = TILE == 64 ? 4 : 2;  // steps in LDS
+    static constexpr int RING = NB * STAGE;       // also the staged sums of BAND rows
     static constexpr int LDS = RING + 16 * TILE;  // and what an epilogue keeps of rows and columns meanwhile
     static constexpr int BANDS = TILE == 256 ? 2 : 1, BAND = TILE / BANDS;
     static constexpr int PER_CU = TILE == 256 ? 1 : 2, PER_SIMD = PER_CU * NT / 256;
@@ -71,20 +74,21 @@ template <int TILE> IQLH_DEV int wave_n() { return __builtin_amdgcn_readfirstlan
 // wave_m + 32 i + (l & 31), n = wave_n + 32 j + 8 g + 4 (l >> 5) + e.  Every step of 16 k is added in
 // the same order whatever the tile.  When it returns, the ring in LDS is free.
 //
-// Two steps in LDS, filled by asynchronous copies: in its last part of 16 k step s waits
+// NB steps in LDS, filled by asynchronous copies: in its last part of 16 k step s waits
 // for the copies of step s + 1, passes the barrier (behind which all reads of its own buffer are
-// done), issues those of step s + 2 into that buffer and reads the first fragments of
+// done), issues those of step s + NB into that buffer and reads the first fragments of
 // step s + 1 while the part's matrix instructions run; LDS reads and matrix instructions alternate.
 // Rows: 128 bytes of a row, a whole cache line, its 16-byte chunk u at u ^ ((row >> 1) & 7), so that 16
 // lanes' reads fall on all banks.  Columns: TILE elements of one k, chunk u at u ^ 4 (k
-// & 3): a transposing read takes 4 k of 16 neighbouring elements in 16 lanes, 32 lanes
+// & 3) (rows of 128 bytes: u ^ 2 (k & 2)): a transposing read takes 4 k of 16 neighbouring elements in 16 lanes, 32 lanes
 // all banks.
 template <bool BRAIN, int TILE, bool AC, bool BC, int PL = 1>
 IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1, bool both,
                            uint8_t* lds, mm_f16 (&acc)[Tile16<TILE>::FA][Tile16<TILE>::FB]) {
     typedef Tile16<TILE, PL> T;
-    constexpr int NT = T::NT, FA = T::FA, FB = T::FB, BK = T::BK, CP = T::CP;
+    constexpr int NT = T::NT, FA = T::FA, FB = T::FB, BK = T::BK, CP = T::CP, NB = T::NB;
     constexpr int CPR = PL * TILE / 8, KR = NT / CPR, PARTS = BK / 16;
+    auto col_mix = [](int k) __attribute__((always_inline)) { return CPR == 8 ? 2 * (k & 2) : 4 * (k & 3); };
     static_assert(CP * KR == BK && CP * (NT / 8) == TILE, "copies of a step");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -93,7 +97,7 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     const int per = (int)((k1 - k0 + BK - 1) / BK), steps = both ? 2 * per : per;
     // what a thread copies: chunk i NT + tid of a side
     const int ru = (tid & 7) ^ ((tid >> 4) & 7), rk = 8 * (PL == 2 ? ru & 3 : ru);  // rows: chunk of the row, its k
-    const int ck = tid / CPR, cu = (tid % CPR) ^ (4 * (ck & 3));                    // columns: k, chunk of it
+    const int ck = tid / CPR, cu = (tid % CPR) ^ col_mix(ck);                  // columns: k, chunk of it
     const int ci = PL == 2 ? cu / 8 * 32 + (cu & 3) * 8 : cu * 8;
     auto offset = [&](const Side16& s, bool cols, int64_t i0, int i) __attribute__((always_inline)) -> uint32_t {
         if (cols) return (uint32_t)((KR * i + ck) * s.ld * (2 * PL)) + 16u * (i0 + ci < s.n ? cu : 0);
@@ -111,7 +115,7 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     bool rest = both;
     auto issue = [&](int s) __attribute__((always_inline)) {
         if (s >= steps) return;
-        const uint32_t dst = lds_at + (s & 1) * T::STAGE + wave * 1024;
+        const uint32_t dst = lds_at + (s & (NB - 1)) * T::STAGE + wave * 1024;
         const int64_t kk = k0 + (int64_t)step_in * BK;
         const uint8_t* pb = (const uint8_t*)(b.p + PL * (BC ? kk * b.ld + n0 : n0 * b.ld + kk));
         const uint8_t* pa = (const uint8_t*)(a.p + (rest ? a.plane : 0) + PL * (AC ? kk * a.ld + m0 : m0 * a.ld + kk));
@@ -135,7 +139,7 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     const int wm = wave / T::WN * (32 * FA), wn = wave % T::WN * (32 * FB);
     // where a lane reads: rows, the row's start (the chunk goes by the part); columns, the fragment's chunk of the lane's k
     auto col_at = [&](int i0) __attribute__((always_inline)) {
-        return (8 * h + (li >> 2)) * (2 * PL * TILE) + 16 * ((PL * i0 / 8 + 2 * half + ((li & 3) >> 1)) ^ (4 * (li >> 2))) + 8 * (li & 1);
+        return (8 * h + (li >> 2)) * (2 * PL * TILE) + 16 * ((PL * i0 / 8 + 2 * half + ((li & 3) >> 1)) ^ col_mix(li >> 2)) + 8 * (li & 1);
     };
     int ca[FA], cb[FB];
 #pragma unroll
@@ -162,7 +166,7 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     typedef std::integral_constant<bool, AC> CA;
     typedef std::integral_constant<bool, BC> CB;
     auto load = [&](int s, auto part, auto set) __attribute__((always_inline)) {
-        const uint8_t* buf = lds + (s & 1) * T::STAGE;
+        const uint8_t* buf = lds + (s & (NB - 1)) * T::STAGE;
         Frags& g = f[decltype(set)::value];
 #pragma unroll
         for (int p = PL - 1; p >= 0; --p) {
@@ -200,10 +204,16 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     typedef std::integral_constant<int, 1> C1;
     typedef std::integral_constant<int, 2> C2;
     typedef std::integral_constant<int, 3> C3;
-    issue(0);
-    wait_vm<0>();
-    bar();
-    issue(1);
+    // the copies of step s are here; those of the NB - 2 steps behind it may be on their way
+    auto landed = [&](int s) __attribute__((always_inline)) {
+        if (NB == 2 || s + NB - 2 >= steps) wait_vm<0>();
+        else wait_vm<(NB - 2) * 2 * CP>();
+        bar();
+    };
+#pragma unroll
+    for (int i = 0; i < NB - 1; ++i) issue(i);
+    landed(0);
+    issue(NB - 1);
     load(0, C0(), C0());
     for (int s = 0; s < steps; ++s) {
         load(s, C1(), C1());
@@ -217,9 +227,8 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
             mma(C0());
             interleave();
         }
-        wait_vm<0>();  // step s + 1 has landed
-        bar();
-        issue(s + 2);
+        landed(s + 1);
+        issue(s + NB);
         load(s + 1, C0(), C0());
         mma(C1());
         interleave();

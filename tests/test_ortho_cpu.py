@@ -37,7 +37,7 @@ def _fill(m, ms, short=0, skew=0):
 
 MAT = np.dtype([("addr", "<u8", 3), ("ld", "<i8", 3), ("at", "<i8", 4), ("rows", "<i4"), ("cols", "<i4"),
                 ("rows_pad", "<i4"), ("cols_pad", "<i4"), ("k_pad", "<i4"), ("x_dtype", "<i4"), ("out_dtype", "<i4"),
-                ("planes", "<i4"), ("unit0", "<i4"), ("units", "<i4"), ("unit_rows", "<i4"), ("tile", "<i4")])
+                ("planes", "<i4"), ("unit0", "<i4"), ("units", "<i4"), ("unit_rows", "<i4"), ("reserved", "<i4")])
 TILE = np.dtype([("mat", "<i4"), ("m", "<u2"), ("n", "<u2")])
 
 
@@ -65,12 +65,10 @@ def test_tiles_and_pieces_cover_every_matrix_once(m, seed):
         ranges += [(a, a + int(b)) for a, b in zip(q["at"], (x, x, s, s))]
     for i, q in enumerate(mats):
         mine = [(int(t["m"]), int(t["n"])) for t in rect if t["mat"] == i]
-        if mine:
-            size = int(q["tile"]) or 128
-            mt, nt = -(-q["rows_pad"] // size), -(-q["cols_pad"] // size)
-            assert sorted(mine) == [(a, b) for a in range(mt) for b in range(nt)]
-            k = -(-q["k_pad"] // size)
-            assert sorted((int(t["m"]), int(t["n"])) for t in sym if t["mat"] == i) == [(a, b) for a in range(k) for b in range(a + 1)]
+        mt, nt = -(-q["rows_pad"] // st.rect_tile), -(-q["cols_pad"] // st.rect_tile)
+        assert sorted(mine) == [(a, b) for a in range(mt) for b in range(nt)]
+        k = -(-q["k_pad"] // st.sym_tile)
+        assert sorted((int(t["m"]), int(t["n"])) for t in sym if t["mat"] == i) == [(a, b) for a in range(k) for b in range(a + 1)]
     ranges.sort()
     assert all(a[1] <= b[0] for a, b in zip(ranges, ranges[1:])) and ranges[-1][1] <= st.workspace_bytes
 
