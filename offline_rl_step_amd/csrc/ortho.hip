@@ -155,61 +155,83 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
             rate = (float)(a.h.lr * shape);
         }
     }
+    // What is combined with the sums: the element's own row of X X^T or X, and in a step the old weights.  All
+    // of a batch's loads are made before its first use, so that their time is paid once.
+    constexpr int BATCH = 4;
+    struct Own {
+        uint4 hi, lo;
+        float old[8];
+    };
+    const uint16_t* own = PHASE == kPoly ? gram : x;
+    const int own_ld = PHASE == kPoly ? q.k_pad : q.cols_pad;
+    auto fetch = [&](int m, int n, Own& o) __attribute__((always_inline)) {
+        if (PHASE == kGram) return;
+        const uint16_t* p = own + (two ? planes_at(m, own_ld, n) : (int64_t)m * own_ld + n);
+        o.hi = *(const uint4*)p;
+        o.lo = two ? *(const uint4*)(p + 32) : uint4{0u, 0u, 0u, 0u};
+        if (PHASE == kLast && a.h.step && m < q.rows && n < q.cols)
+            load8_of(q.out_dtype, (const void*)q.out, (int64_t)m * q.ld_out + n, q.cols - n, o.old);
+    };
     // eight neighbouring sums v of row m from column n on, as they are stored
-    auto put = [&](int m, int n, float (&v)[8]) __attribute__((always_inline)) {
+    auto put = [&](int m, int n, const float (&v)[8], const Own& o) __attribute__((always_inline)) {
         float y[8];
-        if (PHASE == kGram) {
+        const uint32_t hw[4] = {o.hi.x, o.hi.y, o.hi.z, o.hi.w}, lw[4] = {o.lo.x, o.lo.y, o.lo.z, o.lo.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[i] * kDown;
-            put_planes(gram, m, q.k_pad, n, two, y);
-        } else if (PHASE == kPoly) {
-            get_planes(gram, m, q.k_pad, n, two, y);
+        for (int i = 0; i < 8; ++i) {
+            const float s = v[i] * (PHASE == kPoly ? kC * kDown : kDown);
+            const float e = PHASE == kGram ? 0.f : half_of(hw[i >> 1], i & 1) + half_of(lw[i >> 1], i & 1);
+            y[i] = PHASE == kGram ? s : fmaf(PHASE == kPoly ? kB : kA, e, s);
+        }
+        if (PHASE == kGram) put_planes(gram, m, q.k_pad, n, two, y);
+        if (PHASE == kPoly) put_planes(poly, m, q.k_pad, n, two, y);
+        if (PHASE == kApply) put_planes((uint16_t*)(a.base + q.x_at[from ^ 1]), m, q.cols_pad, n, two, y);
+        if (PHASE == kLast && m < q.rows && n < q.cols) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(kB, y[i], (kC * kDown) * v[i]);
-            put_planes(poly, m, q.k_pad, n, two, y);
-        } else {
-            get_planes(x, m, q.cols_pad, n, two, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = fmaf(kA, y[i], kDown * v[i]);
-            if (PHASE == kApply) {
-                put_planes((uint16_t*)(a.base + q.x_at[from ^ 1]), m, q.cols_pad, n, two, y);
-                return;
+            for (int i = 0; i < 8; ++i) {
+                y[i] = ok ? y[i] * kDown : __uint_as_float(0x7FC00000u);
+                if (a.h.step) y[i] = fmaf(-rate, y[i], a.h.keep * o.old[i]);
             }
-            if (m >= q.rows || n >= q.cols) return;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = ok ? y[i] * kDown : __uint_as_float(0x7FC00000u);
-            const int64_t at = (int64_t)m * q.ld_out + n;
-            if (a.h.step) {
-                float old[8];
-                load8_of(q.out_dtype, (const void*)q.out, at, q.cols - n, old);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fmaf(-rate, y[i], a.h.keep * old[i]);
-            }
-            store8_of(q.out_dtype, (void*)q.out, at, q.cols - n, y);
+            store8_of(q.out_dtype, (void*)q.out, (int64_t)m * q.ld_out + n, q.cols - n, y);
         }
     };
 #pragma unroll
     for (int band = 0; band < T::BANDS; ++band) {
         stage_band<TILE>(acc, lds, band);
-#pragma unroll 2
-        for (int c = threadIdx.x; c < T::BAND * (TILE / 8); c += T::NT) {
-            const int row = c / (TILE / 8), u = c % (TILE / 8);
-            const int m = (int)m0 + band * T::BAND + row, n = (int)n0 + 8 * u;
-            if (m >= rows || n >= cols) continue;
-            const float4 lo = *stage_at<TILE>(lds, row, 2 * u), hi = *stage_at<TILE>(lds, row, 2 * u + 1);
-            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            put(m, n, v);
-        }
-        if (PHASE <= kPoly && w.m != w.n) {
-#pragma unroll 2
-            for (int c = threadIdx.x; c < T::BAND / 8 * TILE; c += T::NT) {
-                const int u = c % (T::BAND / 8), col = c / (T::BAND / 8);
-                const int m = (int)m0 + band * T::BAND + 8 * u, n = (int)n0 + col;
-                if (m >= rows || n >= cols) continue;
-                float v[8];
+        const int mb = (int)m0 + band * T::BAND;
+        constexpr int UNITS = T::BAND * (TILE / 8);
+        for (int c0 = threadIdx.x; c0 < UNITS; c0 += BATCH * T::NT) {
+            Own o[BATCH];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = ((const float*)stage_at<TILE>(lds, 8 * u + i, col / 4))[col & 3];
-                put(n, m, v);
+            for (int k = 0; k < BATCH; ++k) {
+                const int c = c0 + k * T::NT, m = mb + c / (TILE / 8), n = (int)n0 + 8 * (c % (TILE / 8));
+                if (c < UNITS && m < rows && n < cols) fetch(m, n, o[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int c = c0 + k * T::NT, row = c / (TILE / 8), u = c % (TILE / 8), m = mb + row, n = (int)n0 + 8 * u;
+                if (c >= UNITS || m >= rows || n >= cols) continue;
+                const float4 lo = *stage_at<TILE>(lds, row, 2 * u), hi = *stage_at<TILE>(lds, row, 2 * u + 1);
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                put(m, n, v, o[k]);
+            }
+        }
+        if (PHASE <= kPoly && w.m != w.n) {  // and in the mirrored place
+            for (int c0 = threadIdx.x; c0 < UNITS; c0 += BATCH * T::NT) {
+                Own o[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int c = c0 + k * T::NT, m = mb + 8 * (c % (T::BAND / 8)), n = (int)n0 + c / (T::BAND / 8);
+                    if (c < UNITS && m < rows && n < cols) fetch(n, m, o[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int c = c0 + k * T::NT, u = c % (T::BAND / 8), col = c / (T::BAND / 8), m = mb + 8 * u, n = (int)n0 + col;
+                    if (c >= UNITS || m >= rows || n >= cols) continue;
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = ((const float*)stage_at<TILE>(lds, 8 * u + i, col / 4))[col & 3];
+                    put(n, m, v, o[k]);
+                }
             }
         }
     }
