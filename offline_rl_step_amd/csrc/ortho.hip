@@ -114,9 +114,9 @@ __global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
 // X X^T and the polynomial of it (kGram, kPoly): symmetric, tiles m >= n.
 // kApply: the next X.  kLast: the result.
 enum { kGram, kPoly, kApply, kLast };
-template <int TILE, int PHASE>
-__global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void ortho_product_kernel(OrthoArgs a, int from) {
-    typedef Tile16<TILE> T;
+template <int TILE, int PHASE, int STEPS>
+__global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD)) void ortho_product_kernel(OrthoArgs a, int from) {
+    typedef Tile16<TILE, 1, STEPS> T;
     extern __shared__ __align__(16) uint8_t lds[];
     const OrthoTile w = (PHASE <= kPoly ? a.sym : a.rect)[blockIdx.x];
     const OrthoMat& q = a.mats[w.mat];
@@ -130,15 +130,15 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
         constexpr int PL = decltype(planes)::value;
         if (PHASE == kGram) {
             const Side16 s{x, 0, q.cols_pad, q.k_pad};
-            if (tall) tile_product<false, TILE, true, true, PL>(s, s, m0, n0, 0, q.rows_pad, false, lds, acc);
-            else tile_product<false, TILE, false, false, PL>(s, s, m0, n0, 0, q.cols_pad, false, lds, acc);
+            if (tall) tile_product<false, TILE, true, true, PL, STEPS>(s, s, m0, n0, 0, q.rows_pad, false, lds, acc);
+            else tile_product<false, TILE, false, false, PL, STEPS>(s, s, m0, n0, 0, q.cols_pad, false, lds, acc);
         } else if (PHASE == kPoly) {
             const Side16 s{gram, 0, q.k_pad, q.k_pad};
-            tile_product<false, TILE, false, false, PL>(s, s, m0, n0, 0, q.k_pad, false, lds, acc);
+            tile_product<false, TILE, false, false, PL, STEPS>(s, s, m0, n0, 0, q.k_pad, false, lds, acc);
         } else {
             const Side16 p{poly, 0, q.k_pad, q.k_pad};
-            if (tall) tile_product<false, TILE, false, false, PL>(Side16{x, 0, q.cols_pad, q.rows_pad}, p, m0, n0, 0, q.k_pad, false, lds, acc);
-            else tile_product<false, TILE, false, true, PL>(p, Side16{x, 0, q.cols_pad, q.cols_pad}, m0, n0, 0, q.k_pad, false, lds, acc);
+            if (tall) tile_product<false, TILE, false, false, PL, STEPS>(Side16{x, 0, q.cols_pad, q.rows_pad}, p, m0, n0, 0, q.k_pad, false, lds, acc);
+            else tile_product<false, TILE, false, true, PL, STEPS>(p, Side16{x, 0, q.cols_pad, q.cols_pad}, m0, n0, 0, q.k_pad, false, lds, acc);
         }
     };
     if (two) product(std::integral_constant<int, 2>());
@@ -239,16 +239,20 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void orth
 
 template <int PHASE>
 hipError_t launch_product(const OrthoArgs& a, int from, hipStream_t stream) {
-    auto launch = [&](auto tile) {
-        typedef Tile16<decltype(tile)::value> T;
-        auto kernel = ortho_product_kernel<decltype(tile)::value, PHASE>;
+    const int n = PHASE <= kPoly ? a.nsym : a.nrect;
+    auto launch = [&](auto tile, auto steps) {
+        typedef Tile16<decltype(tile)::value, 1, decltype(steps)::value> T;
+        auto kernel = ortho_product_kernel<decltype(tile)::value, PHASE, decltype(steps)::value>;
         (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
-        hipLaunchKernelGGL(kernel, dim3(PHASE <= kPoly ? a.nsym : a.nrect), dim3(T::NT), T::LDS, stream, a, from);
+        hipLaunchKernelGGL(kernel, dim3(n), dim3(T::NT), T::LDS, stream, a, from);
     };
+    typedef std::integral_constant<int, 2> Two;
+    typedef std::integral_constant<int, 4> Four;
     const int tile = PHASE <= kPoly ? a.sym_tile : a.rect_tile;
-    if (tile == 256) launch(std::integral_constant<int, 256>());
-    else if (tile == 128) launch(std::integral_constant<int, 128>());
-    else launch(std::integral_constant<int, 64>());
+    if (tile == 256) launch(std::integral_constant<int, 256>(), Two());
+    else if (tile == 64) launch(std::integral_constant<int, 64>(), Four());
+    else if (n <= 256) launch(std::integral_constant<int, 128>(), Four());
+    else launch(std::integral_constant<int, 128>(), Two());
     return hipGetLastError();
 }
 

@@ -48,7 +48,7 @@ IQLH_DEV mm_f16 mma16(uint4 a, uint4 b, mm_f16 c) {
 
 // TILE 256: eight waves, 2 x 4, each 128 x 64 outputs (4 x 2 fragments of 32 x 32).  TILE 128 and 64: four
 // waves, 2 x 2, each 64 x 64 or 32 x 32; two workgroups to a compute unit.
-template <int TILE, int PL = 1>
+template <int TILE, int PL = 1, int STEPS = TILE == 64 ? 4 : 2>
 struct Tile16 {
     static constexpr int WM = 2, WN = TILE == 256 ? 4 : 2;          // waves
     static constexpr int FA = TILE / 32 / WM, FB = TILE / 32 / WN;  // fragments of 32 x 32 of a wave
@@ -57,11 +57,11 @@ struct Tile16 {
     static constexpr int SIDE = TILE * 128;       // one operand in a step
     static constexpr int STAGE = 2 * SIDE;
     static constexpr int CP = SIDE / 16 / NT;     // copies of a thread, operand and step
-    static constexpr int NB = TILE == 64 ? 4 : 2;  // steps in LDS
+    static constexpr int NB = STEPS;              // steps in LDS, a power of two
     static constexpr int RING = NB * STAGE;       // also the staged sums of BAND rows
     static constexpr int LDS = RING + 16 * TILE;  // and what an epilogue keeps of rows and columns meanwhile
     static constexpr int BANDS = TILE == 256 ? 2 : 1, BAND = TILE / BANDS;
-    static constexpr int PER_CU = TILE == 256 ? 1 : 2, PER_SIMD = PER_CU * NT / 256;
+    static constexpr int PER_CU = RING > 64 << 10 ? 1 : 2, PER_SIMD = PER_CU * NT / 256;
     static_assert(BAND * TILE * 4 <= RING && PER_CU * LDS <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -77,15 +77,16 @@ template <int TILE> IQLH_DEV int wave_n() { return __builtin_amdgcn_readfirstlan
 // NB steps in LDS, filled by asynchronous copies: in its last part of 16 k step s waits
 // for the copies of step s + 1, passes the barrier (behind which all reads of its own buffer are
 // done), issues those of step s + NB into that buffer and reads the first fragments of
-// step s + 1 while the part's matrix instructions run; LDS reads and matrix instructions alternate.
+// step s + 1 while the part's matrix instructions run.  The copies are made in that part and in the next
+// step's first one.
 // Rows: 128 bytes of a row, a whole cache line, its 16-byte chunk u at u ^ ((row >> 1) & 7), so that 16
 // lanes' reads fall on all banks.  Columns: TILE elements of one k, chunk u at u ^ 4 (k
 // & 3) (rows of 128 bytes: u ^ 2 (k & 2)): a transposing read takes 4 k of 16 neighbouring elements in 16 lanes, 32 lanes
 // all banks.
-template <bool BRAIN, int TILE, bool AC, bool BC, int PL = 1>
+template <bool BRAIN, int TILE, bool AC, bool BC, int PL = 1, int STEPS = Tile16<TILE>::NB>
 IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t n0, int64_t k0, int64_t k1, bool both,
                            uint8_t* lds, mm_f16 (&acc)[Tile16<TILE>::FA][Tile16<TILE>::FB]) {
-    typedef Tile16<TILE, PL> T;
+    typedef Tile16<TILE, PL, STEPS> T;
     constexpr int NT = T::NT, FA = T::FA, FB = T::FB, BK = T::BK, CP = T::CP, NB = T::NB;
     constexpr int CPR = PL * TILE / 8, KR = NT / CPR, PARTS = BK / 16;
     auto col_mix = [](int k) __attribute__((always_inline)) { return CPR == 8 ? 2 * (k & 2) : 4 * (k & 3); };
@@ -111,30 +112,40 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
         offa[i] = offset(a, AC, m0, i);
         offb[i] = offset(b, BC, n0, i);
     }
+    // the copies of one step: `next` takes it up, `copy` makes copy c of 2 CP, b's first
     int step_in = 0;
     bool rest = both;
-    auto issue = [&](int s) __attribute__((always_inline)) {
-        if (s >= steps) return;
-        const uint32_t dst = lds_at + (s & (NB - 1)) * T::STAGE + wave * 1024;
-        const int64_t kk = k0 + (int64_t)step_in * BK;
-        const uint8_t* pb = (const uint8_t*)(b.p + PL * (BC ? kk * b.ld + n0 : n0 * b.ld + kk));
-        const uint8_t* pa = (const uint8_t*)(a.p + (rest ? a.plane : 0) + PL * (AC ? kk * a.ld + m0 : m0 * a.ld + kk));
-        if (kk + BK <= k1) {
-#pragma unroll
-            for (int i = 0; i < CP; ++i) copy16(pb, offb[i], dst + i * NT * 16);
-#pragma unroll
-            for (int i = 0; i < CP; ++i) copy16(pa, offa[i], dst + T::SIDE + i * NT * 16);
-        } else {  // zeros behind k1
-            const bool row_in = kk + rk < k1;
-#pragma unroll
-            for (int i = 0; i < CP; ++i)
-                copy16((BC ? kk + KR * i + ck < k1 : row_in) ? pb + offb[i] : (const uint8_t*)kZeroChunk, dst + i * NT * 16);
-#pragma unroll
-            for (int i = 0; i < CP; ++i)
-                copy16((AC ? kk + KR * i + ck < k1 : row_in) ? pa + offa[i] : (const uint8_t*)kZeroChunk,
-                       dst + T::SIDE + i * NT * 16);
-        }
+    const uint8_t *pa = nullptr, *pb = nullptr;
+    uint32_t dst = 0u;
+    int64_t kk = 0;
+    bool there = false, whole = false;
+    auto next = [&](int s) __attribute__((always_inline)) {
+        there = s < steps;
+        dst = lds_at + (s & (NB - 1)) * T::STAGE + wave * 1024;
+        kk = k0 + (int64_t)step_in * BK;
+        whole = there && kk + BK <= k1;
+        pb = (const uint8_t*)(b.p + PL * (BC ? kk * b.ld + n0 : n0 * b.ld + kk));
+        pa = (const uint8_t*)(a.p + (rest ? a.plane : 0) + PL * (AC ? kk * a.ld + m0 : m0 * a.ld + kk));
         if (++step_in == per) step_in = 0, rest = false;
+    };
+    auto copy = [&](int c) __attribute__((always_inline)) {
+        if (c < CP) copy16(pb, offb[c], dst + c * NT * 16);
+        else copy16(pa, offa[c - CP], dst + c * NT * 16);
+    };
+    auto copy_edge = [&](int c) __attribute__((always_inline)) {  // zeros behind k1
+        const bool cols = c < CP ? BC : AC;
+        const bool in = cols ? kk + KR * (c % CP) + ck < k1 : kk + rk < k1;
+        copy16(in ? (c < CP ? pb + offb[c] : pa + offa[c - CP]) : (const uint8_t*)kZeroChunk, dst + c * NT * 16);
+    };
+    auto issue = [&](int s) __attribute__((always_inline)) {
+        next(s);
+        if (whole) {
+#pragma unroll
+            for (int c = 0; c < 2 * CP; ++c) copy(c);
+        } else if (there) {
+#pragma unroll
+            for (int c = 0; c < 2 * CP; ++c) copy_edge(c);
+        }
     };
     const int wm = wave / T::WN * (32 * FA), wn = wave % T::WN * (32 * FB);
     // where a lane reads: rows, the row's start (the chunk goes by the part); columns, the fragment's chunk of the lane's k
@@ -165,40 +176,44 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     };
     typedef std::integral_constant<bool, AC> CA;
     typedef std::integral_constant<bool, BC> CB;
-    auto load = [&](int s, auto part, auto set) __attribute__((always_inline)) {
-        const uint8_t* buf = lds + (s & (NB - 1)) * T::STAGE;
+    constexpr int FRAGS = PL * (FA + FB), MMAS = FA * FB * (PL == 2 ? 3 : 1);
+    // fragment e of a part: the smaller plane's first, b's before a's
+    auto load_one = [&](const uint8_t* buf, int e, auto part, auto set) __attribute__((always_inline)) {
         Frags& g = f[decltype(set)::value];
-#pragma unroll
-        for (int p = PL - 1; p >= 0; --p) {
-#pragma unroll
-            for (int i = 0; i < FB; ++i) g.b[p][i] = read(buf, cb[i], CB(), part, p);
-#pragma unroll
-            for (int i = 0; i < FA; ++i) g.a[p][i] = read(buf, ca[i], CA(), part, p);
-        }
+        const int p = PL - 1 - e / (FA + FB), i = e % (FA + FB);
+        if (i < FB) g.b[p][i] = read(buf, cb[i], CB(), part, p);
+        else g.a[p][i - FB] = read(buf, ca[i - FB], CA(), part, p);
+    };
+    auto mma_one = [&](int e, auto set) __attribute__((always_inline)) {
+        const Frags& g = f[decltype(set)::value];
+        const int t = PL == 2 ? e / (FA * FB) : 2, i = e / FB % FA, j = e % FB;  // lo hi, hi lo, hi hi
+        acc[i][j] = mma16<BRAIN>(g.b[t == 1][j], g.a[t == 0][i], acc[i][j]);
     };
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
         for (int j = 0; j < FB; ++j) acc[i][j] = mm_f16{};
-    auto mma = [&](auto set) __attribute__((always_inline)) {
-        const Frags& g = f[decltype(set)::value];
+    // A part's matrix instructions, with the LDS reads of part `load` of step s and a half of the copies taken up
+    // (0 the first, 1 the second, 2 none) between them: neither LDS nor the path of the copies
+    // takes more than one wave's at a time, and what waits for either holds up the wave.
+    auto run = [&](int s, auto load, auto load_set, auto set, auto copies) __attribute__((always_inline)) {
+        constexpr int H = decltype(copies)::value;
+        const uint8_t* buf = lds + (s & (NB - 1)) * T::STAGE;
+        if (H < 2 && there && !whole) {
 #pragma unroll
-        for (int t = PL == 2 ? 0 : 2; t < 3; ++t)  // lo hi, hi lo, hi hi
-#pragma unroll
-            for (int i = 0; i < FA; ++i)
-#pragma unroll
-                for (int j = 0; j < FB; ++j) acc[i][j] = mma16<BRAIN>(g.b[t == 1][j], g.a[t == 0][i], acc[i][j]);
-    };
-    // a part's matrix instructions, with the next one's LDS reads between them
-    constexpr int READS = PL * ((AC ? 2 : 1) * FA + (BC ? 2 : 1) * FB), MMAS = FA * FB * (PL == 2 ? 3 : 1);
-    auto interleave = [] __attribute__((always_inline)) {
-        constexpr int EACH = (READS + MMAS - 1) / MMAS;
-#pragma unroll
-        for (int i = 0; i < MMAS; ++i) {
-            if (i * EACH < READS) __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            for (int c = 0; c < CP; ++c) copy_edge(H * CP + c);
         }
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 0; e < MMAS; ++e) {
+#pragma unroll
+            for (int x = e * FRAGS / MMAS; x < (e + 1) * FRAGS / MMAS; ++x) load_one(buf, x, load, load_set);
+            mma_one(e, set);
+            if (H < 2 && e * CP / MMAS < (e + 1) * CP / MMAS && whole) {
+#pragma unroll
+                for (int c = e * CP / MMAS; c < (e + 1) * CP / MMAS; ++c) copy(H * CP + c);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
     typedef std::integral_constant<int, 0> C0;
     typedef std::integral_constant<int, 1> C1;
@@ -214,24 +229,18 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
     for (int i = 0; i < NB - 1; ++i) issue(i);
     landed(0);
     issue(NB - 1);
-    load(0, C0(), C0());
+    there = whole = false;  // all made
+#pragma unroll
+    for (int e = 0; e < FRAGS; ++e) load_one(lds, e, C0(), C0());
     for (int s = 0; s < steps; ++s) {
-        load(s, C1(), C1());
-        mma(C0());
-        interleave();
+        run(s, C1(), C1(), C0(), C1());
         if constexpr (PARTS == 4) {
-            load(s, C2(), C0());
-            mma(C1());
-            interleave();
-            load(s, C3(), C1());
-            mma(C0());
-            interleave();
+            run(s, C2(), C0(), C1(), C2());
+            run(s, C3(), C1(), C0(), C2());
         }
         landed(s + 1);
-        issue(s + NB);
-        load(s + 1, C0(), C0());
-        mma(C1());
-        interleave();
+        next(s + NB);
+        run(s + 1, C0(), C0(), C1(), C0());
     }
     wait_vm<0>();  // the copies behind the last step, before their buffers are used again
     bar();
