@@ -249,29 +249,27 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
     int* row_col = (int*)(col_bias + TILE);
     float* row_w = (float*)(row_col + TILE);
     float* row_lse = row_w + TILE;
-    if (threadIdx.x < TILE) {
-        const int n = threadIdx.x;
-        const int64_t m = m0 + n;
-        float b = n < there ? 0.f : kNone, w = 0.f, lse = __builtin_huge_valf();
-        if (a.bias && n < there) b = a.bias[n0 + n] * kLog2e;
-        int64_t col = -1;
-        if (m < a.rows) {
-            col = a.taken[m] - a.first - n0;
-            if (GRAD && !row_off(a.taken, a.row_weights, a.all_actions, m)) {
-                w = (a.row_weights ? a.row_weights[m] : 1.f) * (a.f ? a.f->g : a.scale);
-                lse = a.lse[m] == kNone ? 0.f : a.lse[m] * kLog2e;  // no logit above minus infinity: no probabilities
-            }
-        }
-        col_bias[n] = b;
-        row_col[n] = col >= 0 && col < there ? (int)col : -1;
-        row_w[n] = w;
-        row_lse[n] = lse;
-    }
+    // (loaded before the product and put there behind it, so that the product does not wait for them)
+    const int64_t mine = m0 + (threadIdx.x % TILE), mine_in = mine < a.rows ? mine : a.rows - 1;
+    const int32_t t_in = a.taken[mine_in];
+    const float b_in = a.bias && (int)(threadIdx.x % TILE) < there ? a.bias[n0 + threadIdx.x % TILE] : 0.f;
+    const float w_in = GRAD && a.row_weights ? a.row_weights[mine_in] : 1.f, lse_in = GRAD ? a.lse[mine_in] : 0.f;
+    const float zf = (a.f ? a.f->z : 1.f) * kLog2e, gf = a.f ? a.f->g : a.scale;
     mm_f16 acc[FA][FB];
     tile_product<BRAIN, TILE, false, false, PL>(a.h, a.w, m0, n0, 0, a.k, false, lds, acc);
+    if (threadIdx.x < TILE) {
+        const int n = threadIdx.x;
+        const bool off = mine >= a.rows || t_in < 0 || t_in >= a.all_actions || w_in == 0.f;
+        const int64_t col = t_in - a.first - n0;
+        col_bias[n] = n < there ? b_in * kLog2e : kNone;
+        row_col[n] = mine < a.rows && col >= 0 && col < there ? (int)col : -1;
+        row_w[n] = off ? 0.f : w_in * gf;
+        // no logit above minus infinity: no probabilities
+        row_lse[n] = off ? __builtin_huge_valf() : lse_in == kNone ? 0.f : lse_in * kLog2e;
+    }
+    __syncthreads();
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wm = wave_m<TILE>(), wn = wave_n<TILE>();
-    const float zf = (a.f ? a.f->z : 1.f) * kLog2e;
     float zr[FA], sub[FA];
     int col[FA];
 #pragma unroll
@@ -351,13 +349,17 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
                     for (int i = 1; i < FA; ++i) v[k] += acc[i][jj + k / 16][k % 16];
                 }
                 // 32 values of 32 lanes: each exchange halves the values a lane has; lane r ends with value r
+                // (by masks: a selection of two elements becomes one of all 32)
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
+                for (int o = 16; o > 0; o >>= 1) {
+                    const uint32_t upper = r & o ? 0xFFFFFFFFu : 0u;
 #pragma unroll
                     for (int k = 0; k < o; ++k) {
-                        const float keep = r & o ? v[k + o] : v[k], send = r & o ? v[k] : v[k + o];
-                        v[k] = keep + __shfl_xor(send, o, kWave);
+                        const uint32_t lo = __float_as_uint(v[k]), hi = __float_as_uint(v[k + o]);
+                        const float send = __uint_as_float((lo & upper) | (hi & ~upper));
+                        v[k] = __uint_as_float((hi & upper) | (lo & ~upper)) + __shfl_xor(send, o, kWave);
                     }
+                }
                 sums[wm / (32 * FA)][wn + 32 * (jj + (r >> 4)) + 8 * (r >> 2 & 3) + 4 * h + (r & 3)] = v[0];
             }
             __syncthreads();
