@@ -351,8 +351,17 @@ struct PolicyPlan {
     size_t factors, absmax, row_factor, h, h_dw, w, part, z_taken, loss_part, g, db_part, dh_sums, dw_sums, bytes;
     int64_t ld, piece;
     int32_t planes, g_planes, pieces;
+    bool few_actions, few_rows;
 };
 PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bool grad);
+// up to 16 actions, and the loss alone of up to 16 rows, on kernels of their own
+bool policy_few_actions_ok(int64_t actions, int64_t dim);
+size_t policy_few_actions_bytes(int64_t rows, int64_t actions, int64_t dim);
+hipError_t launch_policy_few_actions(const PolicyArgs& a, double* loss_part, int* parts, hipStream_t stream);
+hipError_t launch_policy_few_actions_grad(const PolicyArgs& a, void* work, hipStream_t stream);
+bool policy_few_rows_ok(int64_t rows, int64_t dim, int dtype);
+int policy_few_rows_parts(int64_t actions);
+hipError_t launch_policy_few_rows(const PolicyArgs& a, void* part, float* z_taken, hipStream_t stream);
 hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream);
 hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream);
 

@@ -16,34 +16,13 @@
 // two by the largest |w|, so that probabilities down to 1e-12 are held.  Binary32
 // inputs: H, W and G are two planes of binary16 each (tile16.hpp), times powers of two by
 // their largest elements, 22 bits.
-#include "iqlher.h"
-#include "launch.hpp"
-#include "tile16.hpp"
+#include "policy_block.hpp"
 
 namespace iqlh {
 
+using namespace policy;
+
 namespace {
-
-constexpr int kNT = 256;
-constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-constexpr float kNone = -__builtin_huge_valf();
-
-// 2^(x - m); 0 for x of minus infinity, whatever m is
-IQLH_DEV float exp_below(float x, float m) { return x == kNone ? 0.f : __builtin_amdgcn_exp2f(x - m); }
-
-// Maximum of logits times log2(e), and sum of 2^(. - maximum)
-struct Soft {
-    float m, s;
-    IQLH_DEV void join(Soft o) {
-        const float top = fmaxf(m, o.m);
-        s = s * exp_below(m, top) + o.s * exp_below(o.m, top);  // NaN stays NaN
-        m = top;
-    }
-};
-IQLH_DEV Soft soft_xor(Soft v, int lanes) {
-    v.join(Soft{__shfl_xor(v.m, lanes, kWave), __shfl_xor(v.s, lanes, kWave)});
-    return v;
-}
 
 // Factors of a call, powers of two (times the loss's scale): of sums to logits, of G as it is stored, of the gradients' sums
 struct Factors {
@@ -57,12 +36,6 @@ IQLH_DEV float up_to(uint32_t bits, int top) {  // 2^n that takes a finite value
 }
 
 // ------------------------------------------------------------ preparation
-// A row that adds nothing: no action, or none of these, or weight 0
-IQLH_DEV bool row_off(const int32_t* taken, const float* row_weights, int64_t actions, int64_t m) {
-    const int32_t t = taken[m];
-    return t < 0 || t >= actions || (row_weights && row_weights[m] == 0.f);
-}
-
 IQLH_DEV uint32_t finite_bits(float x) {
     const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
     return b < 0x7F800000u ? b : 0u;
@@ -400,36 +373,6 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
 }
 
 // ------------------------------------------------------------ row statistics
-struct FinishArgs {
-    const Soft* part;        // [parts][rows]
-    const float* z_taken;
-    const int32_t* taken;
-    const float* row_weights;
-    float* nll;
-    float* lse;
-    float* loss;             // or null
-    double* loss_part;       // [workgroups]
-    int32_t* flags;
-    int64_t rows, actions;
-    int parts;
-    double scale;
-};
-IQLH_DEV void put_loss(const FinishArgs& a, double sum) {
-    const float loss = (float)(sum * a.scale);
-    if (a.loss) *a.loss = loss;
-    if (!(fabsf(loss) < __uint_as_float(0x7F800000u))) set_flag(a.flags, IQLH_FLAG_NONFINITE_LOSS);
-}
-IQLH_DEV double block_sum64(double v, double* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kNT / kWave; ++i) s += red[i];
-    return s;
-}
 // R rows a workgroup, 256 / R threads a row
 template <int R>
 __global__ __launch_bounds__(kNT) void policy_finish_kernel(FinishArgs a) {
@@ -620,6 +563,16 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
         at += (bytes + 255) / 256 * 256;
         return was;
     };
+    p.z_taken = take((size_t)rows * 4);
+    p.loss_part = take((size_t)rows * 8);
+    p.few_actions = policy_few_actions_ok(actions, dim);
+    p.few_rows = !p.few_actions && !grad && policy_few_rows_ok(rows, dim, dtype);
+    if (p.few_actions || p.few_rows) {
+        p.part = take(p.few_rows ? (size_t)policy_few_rows_parts(actions) * rows * sizeof(Soft) : 0);
+        p.g = take(grad ? policy_few_actions_bytes(rows, actions, dim) : 0);
+        p.bytes = at;
+        return p;
+    }
     p.factors = take(sizeof(Factors));
     p.absmax = take(3 * kAbsBlocks * 4);
     p.row_factor = take((size_t)rows * 4);
@@ -627,8 +580,6 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
     p.w = take((size_t)actions * p.ld * 2 * p.planes);
     const size_t begin = at;  // the loss's and the gradients' own
     p.part = take((size_t)((actions + 127) / 128) * rows * sizeof(Soft));
-    p.z_taken = take((size_t)rows * 4);
-    p.loss_part = take((size_t)rows * 8);
     p.bytes = at;
     if (grad) {
         at = begin;
@@ -758,6 +709,23 @@ hipError_t launch_grad_product(GradArgs a, const Split& s, int joined, bool brai
 hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream) {
     const PolicyPlan p = policy_plan(a.h.rows, a.w.rows, a.h.cols, a.h.dtype, false);
     uint8_t* base = (uint8_t*)a.workspace;
+    FinishArgs f{};
+    f.part = (Soft*)(base + p.part), f.z_taken = (float*)(base + p.z_taken), f.taken = a.taken, f.row_weights = a.row_weights;
+    f.nll = a.nll, f.lse = a.lse_out, f.loss = a.loss, f.loss_part = (double*)(base + p.loss_part), f.flags = a.flags;
+    f.rows = a.h.rows, f.actions = a.w.rows, f.scale = a.scale;
+    if (p.few_actions) {
+        int n = 0;
+        hipError_t e = launch_policy_few_actions(a, f.loss_part, &n, stream);
+        if (e != hipSuccess || n == 1) return e;
+        hipLaunchKernelGGL(policy_loss_sum_kernel, dim3(1), dim3(kNT), 0, stream, f, n);
+        return hipGetLastError();
+    }
+    if (p.few_rows) {
+        hipError_t e = launch_policy_few_rows(a, base + p.part, (float*)(base + p.z_taken), stream);
+        if (e != hipSuccess) return e;
+        f.parts = policy_few_rows_parts(a.w.rows);
+        return launch_finish(f, stream);
+    }
     Operands o;
     hipError_t e = prepare(a, p, false, &o, stream);
     if (e != hipSuccess) return e;
@@ -769,14 +737,14 @@ hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream) {
     e = launch_logits<false>(l, a.h.dtype == IQLH_BF16, p.planes, stream);
     if (e != hipSuccess) return e;
     const int tile = tile_for(l.rows, l.actions, p.planes);
-    const FinishArgs f{l.part, l.z_taken, a.taken, a.row_weights, a.nll, a.lse_out, a.loss, (double*)(base + p.loss_part),
-                       a.flags, l.rows, l.actions, (int)((l.actions + tile - 1) / tile), a.scale};
+    f.parts = (int)((l.actions + tile - 1) / tile);
     return launch_finish(f, stream);
 }
 
 hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
     const PolicyPlan p = policy_plan(a.h.rows, a.w.rows, a.h.cols, a.h.dtype, true);
     uint8_t* base = (uint8_t*)a.workspace;
+    if (p.few_actions) return launch_policy_few_actions_grad(a, base + p.g, stream);
     const int64_t rows = a.h.rows, actions = a.w.rows, dim = a.h.cols;
     const bool brain = a.h.dtype == IQLH_BF16;
     const int es = a.h.dtype == IQLH_F32 ? 4 : 2;
