@@ -727,6 +727,8 @@ typedef struct iqlh_matrix_set {
     int32_t units;            /* pieces of the elementwise passes              */
     int32_t sym_tiles, rect_tiles;  /* tiles of the products,                  */
     int32_t sym_tile, rect_tile;    /* and their outputs along each side       */
+    int32_t small;            /* matrices that one workgroup takes             */
+    int32_t small_bytes;      /* LDS of such a workgroup                       */
     int32_t momentum;         /* 1 when the matrices have one                  */
     int32_t reserved0;
 } iqlh_matrix_set;

@@ -98,7 +98,7 @@ class MatrixStruct(ctypes.Structure):
 class MatrixSetStruct(ctypes.Structure):
     _fields_ = [("d_table", _p), ("table_bytes", ctypes.c_size_t), ("workspace_bytes", ctypes.c_size_t),
                 ("count", _i32), ("units", _i32), ("sym_tiles", _i32), ("rect_tiles", _i32), ("sym_tile", _i32),
-                ("rect_tile", _i32), ("momentum", _i32), ("reserved0", _i32)]
+                ("rect_tile", _i32), ("small", _i32), ("small_bytes", _i32), ("momentum", _i32), ("reserved0", _i32)]
 
 
 def _sig(name, res, args):

@@ -1215,7 +1215,7 @@ namespace {
 constexpr int32_t kMostMatrices = 4096;
 int32_t pad64(int64_t n) { return (int32_t)((n + 63) / 64 * 64); }
 struct OrthoCounts {
-    int64_t units, sym, rect;
+    int64_t units, sym, rect, small, small_bytes;
     int32_t sym_tile, rect_tile;
 };
 int64_t tiles_along(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
@@ -1230,10 +1230,11 @@ OrthoMat ortho_sizes(const iqlh_matrix& m) {
     q.rows = (int32_t)m.rows, q.cols = (int32_t)m.cols, q.rows_pad = rp, q.cols_pad = cp, q.k_pad = rp < cp ? rp : cp;
     q.unit_rows = ur, q.units = (rp + ur - 1) / ur;
     q.planes = m.compute_dtype == IQLH_F32 || m.rows < 64 || m.cols < 64 ? 2 : 1;
+    if (ortho_small_ok(q.rows_pad, q.cols_pad, q.k_pad, q.planes)) q.units = 0;  // one workgroup's
     return q;
 }
-int64_t sym_tiles(const OrthoMat& q, int64_t tile) { return tiles_along(q.k_pad, tile) * (tiles_along(q.k_pad, tile) + 1) / 2; }
-int64_t rect_tiles(const OrthoMat& q, int64_t tile) { return tiles_along(q.rows_pad, tile) * tiles_along(q.cols_pad, tile); }
+int64_t sym_tiles(const OrthoMat& q, int64_t tile) { return !q.units ? 0 : tiles_along(q.k_pad, tile) * (tiles_along(q.k_pad, tile) + 1) / 2; }
+int64_t rect_tiles(const OrthoMat& q, int64_t tile) { return !q.units ? 0 : tiles_along(q.rows_pad, tile) * tiles_along(q.cols_pad, tile); }
 
 // Time of one tile of a product of `length` summed elements, us: a part for its start and its results, and one
 // for each step (64 elements, 32 of two planes).  Measured, tiles filling the chip | fewer than compute units:
@@ -1311,10 +1312,14 @@ static int check_matrices(const char* who, const iqlh_matrix* ms, int32_t count,
         if (m.compute_dtype != IQLH_F16 && m.compute_dtype != IQLH_F32)
             return fail(IQLH_EINVAL, "%s: matrix %d: compute_dtype must be IQLH_F16 or IQLH_F32", who, i);
     }
-    *all = OrthoCounts{0, 0, 0, sym_tile, rect_tile};
+    *all = OrthoCounts{0, 0, 0, 0, 0, sym_tile, rect_tile};
     for (int i = 0; i < count; ++i) {
         const OrthoMat q = ortho_sizes(ms[i]);
         all->units += q.units, all->sym += sym_tiles(q, all->sym_tile), all->rect += rect_tiles(q, all->rect_tile);
+        if (q.units) continue;
+        ++all->small;
+        const int64_t b = ortho_small_bytes(q.rows_pad, q.cols_pad, q.k_pad, q.planes);
+        all->small_bytes = b > all->small_bytes ? b : all->small_bytes;
     }
     if (all->units > 1 << 22 || all->sym > 1 << 22 || all->rect > 1 << 22)
         return fail(IQLH_ESHAPE, "%s: the list is more than one launch takes", who);
@@ -1326,7 +1331,7 @@ int iqlh_matrix_set_bytes(const iqlh_matrix* matrices, int32_t count, size_t* by
     OrthoCounts n;
     int rc = check_matrices("iqlh_matrix_set_bytes", matrices, count, 64, 64, &n);  // the most tiles
     if (rc) return rc;
-    const size_t table = up16(sizeof(OrthoMat) * (size_t)count + sizeof(OrthoTile) * (size_t)(n.units + n.sym + n.rect));
+    const size_t table = up16(sizeof(OrthoMat) * (size_t)count + sizeof(OrthoTile) * (size_t)(n.units + n.sym + n.rect + n.small));
     // fill sorts the address ranges where the table comes to lie, before it writes it
     const size_t ranges = sizeof(MatrixRange) * 3 * (size_t)count;
     *bytes = table > ranges ? table : ranges;
@@ -1405,6 +1410,7 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
     OrthoTile* units = (OrthoTile*)(mats + count);
     OrthoTile* sym = units + n.units;
     OrthoTile* rect = sym + n.sym;
+    OrthoTile* small = rect + n.rect;
     size_t at = up16(sizeof(double) * (size_t)n.units + sizeof(int32_t) * (size_t)count);
     int32_t unit0 = 0;
     for (int i = 0; i < count; ++i) {
@@ -1414,6 +1420,11 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
         q.ld_x = m.ld_x, q.ld_out = m.ld_out, q.ld_momentum = m.ld_momentum;
         q.x_dtype = m.x_dtype, q.out_dtype = m.out_dtype;
         q.unit0 = unit0;
+        if (!q.units) {
+            *small++ = OrthoTile{i, 0, 0};
+            mats[i] = q;
+            continue;
+        }
         const size_t x = (size_t)q.rows_pad * q.cols_pad * 2 * q.planes, s = (size_t)q.k_pad * q.k_pad * 2 * q.planes;
         q.x_at[0] = (int64_t)at, q.x_at[1] = (int64_t)(at + x), q.gram_at = (int64_t)(at + 2 * x), q.poly_at = (int64_t)(at + 2 * x + s);
         at += 2 * (x + s);
@@ -1424,16 +1435,18 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
     for (int k = 0; k < count; ++k) {
         const int32_t i = order[k];
         const OrthoMat& q = mats[i];
+        if (!q.units) continue;
         sym = put_tiles(sym, i, tiles_along(q.k_pad, n.sym_tile), tiles_along(q.k_pad, n.sym_tile), true, sym_tiles(q, n.sym_tile));
         rect = put_tiles(rect, i, tiles_along(q.rows_pad, n.rect_tile), tiles_along(q.cols_pad, n.rect_tile), false,
                          rect_tiles(q, n.rect_tile));
     }
     std::memset(set, 0, sizeof(*set));
-    set->table_bytes = up16((size_t)((char*)rect - (char*)host_table));
+    set->table_bytes = up16((size_t)((char*)small - (char*)host_table));
     set->workspace_bytes = at;
     set->count = count;
     set->units = (int32_t)n.units, set->sym_tiles = (int32_t)n.sym, set->rect_tiles = (int32_t)n.rect;
     set->momentum = matrices[0].momentum != nullptr;
+    set->small = (int32_t)n.small, set->small_bytes = (int32_t)n.small_bytes;
     set->sym_tile = n.sym_tile, set->rect_tile = n.rect_tile;
     return IQLH_OK;
 }
@@ -1457,6 +1470,7 @@ static int make_ortho_args(const char* who, const iqlh_matrix_set* set, int32_t 
     a->part = (double*)workspace;
     a->ok = (int32_t*)(a->part + set->units);
     a->nunits = set->units, a->nsym = set->sym_tiles, a->nrect = set->rect_tiles;
+    a->small = a->rect + set->rect_tiles, a->nsmall = set->small, a->small_bytes = set->small_bytes;
     a->sym_tile = set->sym_tile, a->rect_tile = set->rect_tile;
     a->h.eps = eps, a->h.flags = d_flags, a->h.steps = steps;
     return IQLH_OK;

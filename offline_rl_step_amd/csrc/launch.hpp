@@ -318,9 +318,19 @@ struct OrthoArgs {
     int32_t* ok;            // [count]
     int32_t nunits, nsym, nrect;
     int32_t sym_tile, rect_tile;  // 64, 128 or 256
+    const OrthoTile* small;       // matrices that one workgroup takes (mat)
+    int32_t nsmall, small_bytes;  // their LDS
     OrthoHyper h;
 };
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);
+int64_t ortho_small_bytes(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
+bool ortho_small_ok(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
+hipError_t launch_ortho_small(const OrthoArgs& a, hipStream_t stream);
+// s of the weights' update
+__host__ __device__ inline double ortho_shape(int rows, int cols, int scale) {
+    const double r = rows, c = cols;
+    return scale == 0 ? sqrt(r > c ? r / c : 1.0) : 0.2 * sqrt(r > c ? r : c);  // IQLH_MUON_SCALE_SHAPE, _RMS
+}
 
 // -------------------------------------------- policy loss over many actions
 struct PolicyMat {

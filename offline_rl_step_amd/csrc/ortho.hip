@@ -150,9 +150,7 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD
         ok = a.ok[w.mat];
         if (a.h.step) {
             if (!ok) return;
-            const double shape = a.h.scale == IQLH_MUON_SCALE_SHAPE ? sqrt(fmax(1.0, (double)q.rows / q.cols))
-                                                                    : 0.2 * sqrt((double)(q.rows > q.cols ? q.rows : q.cols));
-            rate = (float)(a.h.lr * shape);
+            rate = (float)(a.h.lr * ortho_shape(q.rows, q.cols, a.h.scale));
         }
     }
     // What is combined with the sums: the element's own row of X X^T or X, and in a step the old weights.  All
@@ -259,6 +257,10 @@ hipError_t launch_product(const OrthoArgs& a, int from, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream) {
+    if (a.nsmall) {
+        const hipError_t e = launch_ortho_small(a, stream);
+        if (e != hipSuccess || !a.nunits) return e;
+    }
     hipLaunchKernelGGL(ortho_norm_kernel, dim3(a.nunits), dim3(kNT), 0, stream, a);
     hipLaunchKernelGGL(ortho_start_kernel, dim3(a.nunits), dim3(kNT), 0, stream, a);
     hipError_t e = hipGetLastError();

@@ -1,0 +1,261 @@
+// Orthogonalised updates of matrices that fit into the LDS of a compute unit: one
+// workgroup a matrix takes it through the whole step, norm, momentum, all products and the
+// weights, in one launch.  (Formulas and operands as in ortho.hip.)
+//
+// X [rows][cols] and S = X X^T, then b S + c S S, lie in LDS as binary16 in one or two
+// planes.  Eight waves take 64 x 32 outputs each at a time, with a matrix's fragments read
+// straight from LDS: rows as they are, columns by the transposing read, from the same
+// place.  Bound by one compute unit's matrix instructions (15 products of 128^3 in two planes 19 us at
+// 2.4 GHz, in one 6.4); with a launch a product four matrices of 128 x 128 took 97 us, here
+// 36.
+#include "iqlher.h"
+#include "launch.hpp"
+#include "tile16.hpp"
+
+namespace iqlh {
+
+namespace {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kUp = 8192.f, kDown = 1.f / 8192.f;  // of every operand
+constexpr int kNT = 512, kWaves = kNT / 64;
+constexpr int kTiles = 3;                 // most outputs of 64 x 32 a wave
+constexpr int kMostElements = kTiles * kWaves * 2048;
+
+// Chunks of 16 bytes of a row in LDS, a multiple of 16; chunk c of row r lies at c ^ place_mix(r), so that
+// both 16 rows' reads of one chunk and the transposing reads of 4 rows fall on all banks
+__host__ __device__ inline int row_chunks(int planes, int cols_pad) { return (planes * cols_pad / 8 + 15) / 16 * 16; }
+IQLH_DEV int place_mix(int r) { return (r & 3) << 2 | (r >> 2 & 3); }
+
+template <int PL>
+struct Matrix {
+    uint8_t* p;
+    int chunks;  // of a row
+    IQLH_DEV uint8_t* chunk(int r, int c) const { return p + (r * chunks + (c ^ place_mix(r))) * 16; }
+    // chunk of column col (a multiple of 8) and plane
+    static IQLH_DEV int at(int col, int plane) { return PL == 2 ? col / 32 * 8 + (col & 31) / 8 + 4 * plane : col / 8; }
+    // fragment of 32 i from i0, 16 k from k0: element (i, k) in row i
+    IQLH_DEV uint4 rows(int i0, int k0, int plane) const {
+        const int lane = threadIdx.x & 63;
+        return *(const uint4*)chunk(i0 + (lane & 31), at(k0 + 8 * (lane >> 5), plane));
+    }
+    // element (i, k) in column i of row k
+    IQLH_DEV uint4 cols(int i0, int k0, int plane) const {
+        typedef short s4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s4 lds_s4;
+        const int lane = threadIdx.x & 63, li = lane & 15, half = lane >> 4 & 1, h = lane >> 5;
+        const int k = k0 + 8 * h + (li >> 2), c = at(i0 + 16 * half, plane) + ((li & 3) >> 1);
+        const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(chunk(k, c) + 8 * (li & 1)));
+        const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(chunk(k + 4, c) + 8 * (li & 1)));
+        const uint2 l = __builtin_bit_cast(uint2, lo), u = __builtin_bit_cast(uint2, hi);
+        return uint4{l.x, l.y, u.x, u.y};
+    }
+    // four neighbouring elements of row r from column col (a multiple of 4) on
+    IQLH_DEV void get4(int r, int col, float (&v)[4]) const {
+        const int c = col & ~7, half = (col & 4) * 2;
+        const uint2 hi = *(const uint2*)(chunk(r, at(c, 0)) + half);
+        v[0] = half_of(hi.x, 0), v[1] = half_of(hi.x, 1), v[2] = half_of(hi.y, 0), v[3] = half_of(hi.y, 1);
+        if (PL == 2) {
+            const uint2 lo = *(const uint2*)(chunk(r, at(c, 1)) + half);
+            v[0] += half_of(lo.x, 0), v[1] += half_of(lo.x, 1), v[2] += half_of(lo.y, 0), v[3] += half_of(lo.y, 1);
+        }
+    }
+    IQLH_DEV void put4(int r, int col, const float (&v)[4]) const {
+        const int c = col & ~7, half = (col & 4) * 2;
+        const uint2 hi = {pack_half(v[0], v[1]), pack_half(v[2], v[3])};
+        *(uint2*)(chunk(r, at(c, 0)) + half) = hi;
+        if (PL == 2)
+            *(uint2*)(chunk(r, at(c, 1)) + half) = uint2{pack_half(v[0] - half_of(hi.x, 0), v[1] - half_of(hi.x, 1)),
+                                                        pack_half(v[2] - half_of(hi.y, 0), v[3] - half_of(hi.y, 1))};
+    }
+};
+
+// acc = sum over k < K of a(m, k) b(n, k) for the wave's tiles t = wave, wave + 8, .. of 64 x 32, nt of them along n
+template <int PL, bool AC, bool BC>
+IQLH_DEV void product(const Matrix<PL>& a, const Matrix<PL>& b, int tiles, int nt, int K, mm_f16 (&acc)[kTiles][2]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int f = 0; f < kTiles; ++f) {
+        acc[f][0] = mm_f16{};
+        acc[f][1] = mm_f16{};
+        const int t = wave + kWaves * f;
+        if (t >= tiles) continue;
+        const int m0 = t / nt * 64, n0 = t % nt * 32;
+        for (int k0 = 0; k0 < K; k0 += 32) {  // K is a multiple of 64
+            uint4 x[2][PL][2], y[2][PL];
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    const int k = k0 + 16 * d;
+                    y[d][p] = BC ? b.cols(n0, k, p) : b.rows(n0, k, p);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x[d][p][i] = AC ? a.cols(m0 + 32 * i, k, p) : a.rows(m0 + 32 * i, k, p);
+                }
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int s = PL == 2 ? 0 : 2; s < 3; ++s)  // lo hi, hi lo, hi hi
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) acc[f][i] = mma16<false>(y[d][s == 1], x[d][s == 0][i], acc[f][i]);
+        }
+    }
+}
+
+// f(row, column, four sums) for the wave's outputs
+template <typename F>
+IQLH_DEV void each4(int tiles, int nt, mm_f16 (&acc)[kTiles][2], F f) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int tile = wave + kWaves * t;
+        if (tile >= tiles) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[t][i][4 * g + e];
+                f(tile / nt * 64 + 32 * i + r, tile % nt * 32 + 8 * g + 4 * h, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][i][4 * g + e] = v[e];
+            }
+    }
+}
+
+template <int PL>
+IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
+    __shared__ double red[kWaves];
+    const Matrix<PL> X{lds, row_chunks(PL, q.cols_pad)}, S{lds + q.rows_pad * X.chunks * 16, row_chunks(PL, q.k_pad)};
+    const int gc = q.cols_pad / 8, groups = q.rows_pad * gc;
+    // eight elements of the update, and the momentum behind it; twice, since they would not stay in registers
+    auto update8 = [&](int row, int col, int n, float (&u)[8], float (&m)[8]) __attribute__((always_inline)) {
+        load8_of(q.x_dtype, (const void*)q.x, row * q.ld_x + col, n, u);
+        if (!a.h.step) return;
+        load8_of(IQLH_F32, (const void*)q.momentum, row * q.ld_momentum + col, n, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = fmaf(a.h.mu, m[i], u[i]);
+            u[i] = a.h.nesterov ? fmaf(a.h.mu, m[i], u[i]) : m[i];
+        }
+    };
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = threadIdx.x; e < groups; e += kNT) {
+        const int row = e / gc, col = 8 * (e - row * gc), n = q.cols - col;
+        float u[8], m[8];
+        if (row >= q.rows || n <= 0) continue;
+        update8(row, col, n, u, m);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fma((double)u[i], (double)u[i], sum);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) sum += red[i];
+    const double norm = sqrt(sum);
+    const bool ok = norm < __longlong_as_double(0x7FF0000000000000ll);
+    if (!ok) {  // the weights and the momentum stay; results are NaN
+        if (threadIdx.x == 0) set_flag(a.h.flags, IQLH_FLAG_NONFINITE_GRAD);
+        if (a.h.step) return;
+    }
+    const double scale = ok ? (double)kUp / (norm + a.h.eps) : 0.0;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < groups; e += kNT) {
+        const int row = e / gc, col = 8 * (e - row * gc), n = q.cols - col;
+        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m[8];
+        if (row < q.rows && n > 0) {
+            update8(row, col, n, u, m);
+            if (a.h.step) store8_of(IQLH_F32, (void*)q.momentum, row * q.ld_momentum + col, n, m);
+        }
+        float lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = (float)((double)u[i] * scale);
+            hi[i] = (float)((double)u[4 + i] * scale);
+        }
+        X.put4(row, col, lo);
+        X.put4(row, col + 4, hi);
+    }
+    __syncthreads();
+    const bool tall = q.rows > q.cols;
+    const int nts = q.k_pad / 32, ts = q.k_pad / 64 * nts, ntx = q.cols_pad / 32, tx = q.rows_pad / 64 * ntx;
+    mm_f16 acc[kTiles][2];
+    for (int s = 0; s < a.h.steps; ++s) {
+        if (tall) product<PL, true, true>(X, X, ts, nts, q.rows_pad, acc);
+        else product<PL, false, false>(X, X, ts, nts, q.cols_pad, acc);
+        each4(ts, nts, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= kDown;
+            S.put4(m, n, v);
+        });
+        __syncthreads();
+        product<PL, false, false>(S, S, ts, nts, q.k_pad, acc);
+        each4(ts, nts, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
+            float own[4];
+            S.get4(m, n, own);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(kB, own[e], (kC * kDown) * v[e]);
+        });
+        __syncthreads();  // S is read
+        each4(ts, nts, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) { S.put4(m, n, v); });
+        __syncthreads();
+        if (tall) product<PL, false, false>(X, S, tx, ntx, q.k_pad, acc);
+        else product<PL, false, true>(S, X, tx, ntx, q.k_pad, acc);
+        each4(tx, ntx, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
+            float own[4];
+            X.get4(m, n, own);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(kA, own[e], kDown * v[e]);
+        });
+        if (s + 1 == a.h.steps) break;
+        __syncthreads();  // X is read
+        each4(tx, ntx, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) { X.put4(m, n, v); });
+        __syncthreads();
+    }
+    const float rate = a.h.step ? (float)(a.h.lr * ortho_shape(q.rows, q.cols, a.h.scale)) : 0.f;
+    each4(tx, ntx, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
+        if (m >= q.rows || n >= q.cols) return;
+        const int64_t at = m * q.ld_out + n;
+        float old[8], y[8];
+        const int left = q.cols - n < 4 ? q.cols - n : 4;
+        if (a.h.step) load8_of(q.out_dtype, (const void*)q.out, at, left, old);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[e] = ok ? v[e] * kDown : __uint_as_float(0x7FC00000u);
+            if (a.h.step) y[e] = fmaf(-rate, y[e], a.h.keep * old[e]);
+            y[4 + e] = 0.f;
+        }
+        store8_of(q.out_dtype, (void*)q.out, at, left, y);
+    });
+}
+
+__global__ __launch_bounds__(kNT, 2) void ortho_small_kernel(OrthoArgs a) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const OrthoMat& q = a.mats[a.small[blockIdx.x].mat];
+    if (q.planes == 2) small_step<2>(a, q, lds);
+    else small_step<1>(a, q, lds);
+}
+
+}  // namespace
+
+int64_t ortho_small_bytes(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes) {
+    return (int64_t)rows_pad * row_chunks(planes, cols_pad) * 16 + (int64_t)k_pad * row_chunks(planes, k_pad) * 16;
+}
+// 158 KB: what the sums take is in LDS too
+bool ortho_small_ok(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes) {
+    return (int64_t)rows_pad * cols_pad <= kMostElements && (int64_t)k_pad * k_pad <= kMostElements &&
+           ortho_small_bytes(rows_pad, cols_pad, k_pad, planes) <= 158 << 10;
+}
+
+hipError_t launch_ortho_small(const OrthoArgs& a, hipStream_t stream) {
+    (void)hipFuncSetAttribute((const void*)ortho_small_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, a.small_bytes);
+    hipLaunchKernelGGL(ortho_small_kernel, dim3(a.nsmall), dim3(kNT), a.small_bytes, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace iqlh

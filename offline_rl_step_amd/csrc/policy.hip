@@ -49,6 +49,18 @@ IQLH_DEV uint32_t wave_umax(uint32_t v) {
     return v;
 }
 
+// Row and group of 8 columns of element group at + i (i below 2^30), `at` the same for the workgroup: one
+// division of 64 bits for all of it
+struct Place {
+    int64_t row;
+    int group;
+};
+IQLH_DEV Place place_of(int64_t at, int i, int groups) {
+    const int64_t row = at / groups;
+    const uint32_t g = (uint32_t)(at - row * groups) + (uint32_t)i, r = g / (uint32_t)groups;
+    return Place{row + r, (int)(g - r * (uint32_t)groups)};
+}
+
 // Largest finite |x| of up to three matrices, kAbsBlocks workgroups each; of the
 // first without rows that are off where `taken` is given
 struct AbsMaxArgs {
@@ -64,9 +76,11 @@ __global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
     const bool skip = blockIdx.y == 0 && a.taken;
     uint32_t top = 0u;
     if (q.p) {
-        const int64_t groups = (q.cols + 7) / 8;
-        for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < q.rows * groups; e += (int64_t)kAbsBlocks * kNT) {
-            const int64_t row = e / groups, col = 8 * (e - row * groups);
+        const int groups = (int)((q.cols + 7) / 8);
+        for (int64_t at = (int64_t)blockIdx.x * kNT; at < q.rows * groups; at += (int64_t)kAbsBlocks * kNT) {
+            const Place p = place_of(at, threadIdx.x, groups);
+            const int64_t row = p.row, col = 8 * p.group;
+            if (row >= q.rows) continue;
             if (skip && row_off(a.taken, a.row_weights, a.actions, row)) continue;
             float v[8];
             load8_of(q.dtype, q.p, row * q.ld + col, q.cols - col, v);
@@ -134,10 +148,12 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     const PolicyMat& q = c.m;
     if (!q.p) return;
     const int groups = (int)(c.ld_to / 8);
-    // eight elements of a row, times `up`
-    auto put = [&](int64_t row, int col, bool off, float up) __attribute__((always_inline)) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (col < q.cols && !off) load8_of(a.dtype, q.p, row * q.ld + col, q.cols - col, v);
+    auto fetch = [&](int64_t row, int col, bool off, float (&v)[8]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        if (row < q.rows && col < q.cols && !off) load8_of(a.dtype, q.p, row * q.ld + col, q.cols - col, v);
+    };
+    auto put = [&](int64_t row, int col, float (&v)[8], float up) __attribute__((always_inline)) {
         if (f32) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= up;
@@ -162,14 +178,27 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
                 }
             const float up = up_to(wave_umax(top), 14);
             if (lane == 0) c.row_factor[row] = 1.f / up;
-            for (int g = lane; g < groups; g += kWave) put(row, 8 * g, off, up);
+            for (int g = lane; g < groups; g += kWave) {
+                float v[8];
+                fetch(row, 8 * g, off, v);
+                put(row, 8 * g, v, up);
+            }
         }
         return;
     }
     const float up = f32 ? up_to(tops[c.top], 14) : 1.f;
-    for (int64_t e = (int64_t)block * kNT + threadIdx.x; e < q.rows * groups; e += (int64_t)c.blocks * kNT) {
-        const int64_t row = e / groups;
-        put(row, 8 * (int)(e - row * groups), c.zero_off && row_off(a.taken, a.row_weights, a.actions, row), up);
+    constexpr int AHEAD = 4;
+    for (int64_t at = (int64_t)block * (AHEAD * kNT); at < q.rows * groups; at += (int64_t)c.blocks * (AHEAD * kNT)) {
+        float v[AHEAD][8];
+        Place p[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            p[k] = place_of(at, threadIdx.x + k * kNT, groups);
+            fetch(p[k].row, 8 * p[k].group, c.zero_off && p[k].row < q.rows && row_off(a.taken, a.row_weights, a.actions, p[k].row), v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (p[k].row < q.rows) put(p[k].row, 8 * p[k].group, v[k], up);
     }
 }
 

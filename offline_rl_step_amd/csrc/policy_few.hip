@@ -44,6 +44,10 @@ __global__ __launch_bounds__(kNT) void policy_few_actions_kernel(FewArgs a) {
     __shared__ double red[kNT / kWave];
     const int64_t rows = a.h.rows;
     const int dim = (int)a.h.cols, groups = (dim + 7) / 8, ld = 8 * groups, V = (int)a.w.rows, lane = threadIdx.x & 15;
+    // the first elements of the first row, on their way while the weights come to LDS
+    const int64_t m_first = (int64_t)blockIdx.x * kGroups + threadIdx.x / 16;
+    float x0[8];
+    if (m_first < rows && 8 * lane < dim) load8_of(a.h.dtype, a.h.p, m_first * a.h.ld + 8 * lane, dim - 8 * lane, x0);
     for (int e = threadIdx.x; e < VM * groups; e += kNT) {
         const int v = e / groups, col = 8 * (e - v * groups);
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -53,7 +57,7 @@ __global__ __launch_bounds__(kNT) void policy_few_actions_kernel(FewArgs a) {
     }
     __syncthreads();
     double term = 0.0;
-    for (int64_t m = (int64_t)blockIdx.x * kGroups + threadIdx.x / 16; m < rows; m += (int64_t)gridDim.x * kGroups) {
+    for (int64_t m = m_first; m < rows; m += (int64_t)gridDim.x * kGroups) {
         const int32_t t = a.f.taken[m];
         const float weight = a.f.row_weights ? a.f.row_weights[m] : 1.f;
         const float lse_in = GRAD ? a.lse[m] : 0.f;
@@ -62,7 +66,12 @@ __global__ __launch_bounds__(kNT) void policy_few_actions_kernel(FewArgs a) {
         for (int v = 0; v < VM; ++v) z[v] = 0.f;
         for (int col = 8 * lane; col < dim; col += 128) {
             float x[8];
-            load8_of(a.h.dtype, a.h.p, m * a.h.ld + col, dim - col, x);
+            if (m == m_first && col == 8 * lane) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x0[i];
+            } else {
+                load8_of(a.h.dtype, a.h.p, m * a.h.ld + col, dim - col, x);
+            }
 #pragma unroll
             for (int v = 0; v < VM; ++v) {
                 const float4 p = *(const float4*)(w_lds + v * ld + col), q = *(const float4*)(w_lds + v * ld + col + 4);
@@ -113,8 +122,8 @@ __global__ __launch_bounds__(kNT) void policy_few_actions_kernel(FewArgs a) {
 
 // dH, and the parts of dW and db, of 128 columns (blockIdx.y)
 template <int VM>
-__global__ __launch_bounds__(kNT) void policy_few_grads_kernel(FewArgs a) {
-    constexpr int AHEAD = 4;
+__global__ __launch_bounds__(kNT, 2) void policy_few_grads_kernel(FewArgs a) {
+    constexpr int AHEAD = 2;
     __shared__ __align__(16) float w_lds[VM][128];
     __shared__ __align__(16) float sums[kNT / kWave][VM][128];
     __shared__ float b_sums[kNT / kWave][VM];
@@ -139,6 +148,7 @@ __global__ __launch_bounds__(kNT) void policy_few_grads_kernel(FewArgs a) {
     const int64_t step = (int64_t)a.blocks * kGroups;
     for (int64_t m0 = (int64_t)blockIdx.x * kGroups + threadIdx.x / 16; m0 < rows; m0 += AHEAD * step) {
         float x[AHEAD][8], g[AHEAD][VM];
+        asm volatile("" ::: "memory");  // the weights stay in LDS: kept in registers they displace the sums
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int64_t m = m0 + k * step;

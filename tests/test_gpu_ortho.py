@@ -319,8 +319,9 @@ def test_binding_refuses(m):
     ws = m.orthogonalize_workspace(s)
     with pytest.raises(m.IqlhError, match="no momentum"):
         m.muon_step(s, ws, 0.1)
+    large = m.MatrixSet([z(300, 300)], [z(300, 300)])
     with pytest.raises(m.IqlhError, match="too small"):
-        m.orthogonalize(s, ws[:16])
+        m.orthogonalize(large, m.orthogonalize_workspace(large)[:-1])
     with pytest.raises(m.IqlhError, match="steps"):
         m.orthogonalize(s, ws, steps=0)
     with pytest.raises(ValueError, match="workspace"):

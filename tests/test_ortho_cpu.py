@@ -48,9 +48,10 @@ def test_tiles_and_pieces_cover_every_matrix_once(m, seed):
     rc, img, st = _fill(m, ms)
     assert rc == m.OK and st.count == len(ms) and st.momentum == 1
     mats = img[:st.count * MAT.itemsize].view(MAT)
-    n = st.units + st.sym_tiles + st.rect_tiles
+    n = st.units + st.sym_tiles + st.rect_tiles + st.small
     tiles = img[st.count * MAT.itemsize:][:n * 8].view(TILE)
-    units, sym, rect = np.split(tiles, [st.units, st.units + st.sym_tiles])
+    units, sym, rect, small = np.split(tiles, np.cumsum([st.units, st.sym_tiles, st.rect_tiles]))
+    assert sorted(int(t["mat"]) for t in small) == [i for i, q in enumerate(mats) if q["units"] == 0]
     assert st.count * MAT.itemsize + 8 * n <= st.table_bytes <= img.size
     ranges = [(0, 8 * st.units + 4 * st.count)]
     unit0 = 0
@@ -58,12 +59,18 @@ def test_tiles_and_pieces_cover_every_matrix_once(m, seed):
         assert (q["rows"], q["cols"]) == (ms[i].rows, ms[i].cols)
         assert q["rows_pad"] == -(-q["rows"] // 64) * 64 and q["cols_pad"] == -(-q["cols"] // 64) * 64
         assert q["k_pad"] == min(q["rows_pad"], q["cols_pad"]) and q["unit0"] == unit0 and q["units"] <= 512
+        if q["units"] == 0:
+            assert int(q["rows_pad"]) * int(q["cols_pad"]) <= 49152 and st.small_bytes <= 158 * 1024
+            continue
         assert q["units"] * q["unit_rows"] >= q["rows_pad"] > (q["units"] - 1) * q["unit_rows"]
         assert sorted(u["m"] for u in units if u["mat"] == i) == list(range(q["units"]))
         unit0 += q["units"]
         x, s = q["rows_pad"] * q["cols_pad"] * 2 * q["planes"], int(q["k_pad"]) ** 2 * 2 * q["planes"]
         ranges += [(a, a + int(b)) for a, b in zip(q["at"], (x, x, s, s))]
     for i, q in enumerate(mats):
+        if q["units"] == 0:
+            assert not any(t["mat"] == i for part in (units, sym, rect) for t in part)
+            continue
         mine = [(int(t["m"]), int(t["n"])) for t in rect if t["mat"] == i]
         mt, nt = -(-q["rows_pad"] // st.rect_tile), -(-q["cols_pad"] // st.rect_tile)
         assert sorted(mine) == [(a, b) for a in range(mt) for b in range(nt)]
