@@ -70,6 +70,38 @@ struct Matrix {
     }
 };
 
+// One element, and four neighbouring ones of any alignment
+IQLH_DEV float load1_of(int dtype, const void* p, int64_t at) {
+    if (dtype == IQLH_F32) return ((const float*)p)[at];
+    const uint32_t w = ((const uint16_t*)p)[at];
+    return dtype == IQLH_BF16 ? brain_of(w, 0) : half_of(w, 0);
+}
+IQLH_DEV void store1_of(int dtype, void* p, int64_t at, float v) {
+    if (dtype == IQLH_F32) ((float*)p)[at] = v;
+    else ((uint16_t*)p)[at] = dtype == IQLH_BF16 ? f2bf(v) : (uint16_t)pack_half(v, 0.f);
+}
+typedef uint32_t u2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+IQLH_DEV void load4_of(int dtype, const void* p, int64_t at, float (&v)[4]) {
+    if (dtype == IQLH_F32) {
+        const u4_a4 w = *(const u4_a4*)((const float*)p + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(w[e]);
+        return;
+    }
+    const u2_a2 w = *(const u2_a2*)((const uint16_t*)p + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = dtype == IQLH_BF16 ? brain_of(w[e >> 1], e & 1) : half_of(w[e >> 1], e & 1);
+}
+IQLH_DEV void store4_of(int dtype, void* p, int64_t at, const float (&v)[4]) {
+    if (dtype == IQLH_F32) {
+        *(u4_a4*)((float*)p + at) = u4_a4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    } else {
+        const bool brain = dtype == IQLH_BF16;
+        *(u2_a2*)((uint16_t*)p + at) = u2_a2{brain ? pack_bf2(v[0], v[1]) : pack_half(v[0], v[1]),
+                                            brain ? pack_bf2(v[2], v[3]) : pack_half(v[2], v[3])};
+    }
+}
+
 // acc = sum over k < K of a(m, k) b(n, k) for the wave's tiles t = wave, wave + 8, .. of 64 x 32, nt of them along n
 template <int PL, bool AC, bool BC>
 IQLH_DEV void product(const Matrix<PL>& a, const Matrix<PL>& b, int tiles, int nt, int K, mm_f16 (&acc)[kTiles][2]) {
@@ -81,23 +113,33 @@ IQLH_DEV void product(const Matrix<PL>& a, const Matrix<PL>& b, int tiles, int n
         const int t = wave + kWaves * f;
         if (t >= tiles) continue;
         const int m0 = t / nt * 64, n0 = t % nt * 32;
-        for (int k0 = 0; k0 < K; k0 += 32) {  // K is a multiple of 64
-            uint4 x[2][PL][2], y[2][PL];
+        struct Frags {
+            uint4 x[PL][2], y[PL];
+        } g[2];
+        auto load = [&](Frags& q, int k) __attribute__((always_inline)) {
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
+            for (int p = PL - 1; p >= 0; --p) {
+                q.y[p] = BC ? b.cols(n0, k, p) : b.rows(n0, k, p);
 #pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    const int k = k0 + 16 * d;
-                    y[d][p] = BC ? b.cols(n0, k, p) : b.rows(n0, k, p);
+                for (int i = 0; i < 2; ++i) q.x[p][i] = AC ? a.cols(m0 + 32 * i, k, p) : a.rows(m0 + 32 * i, k, p);
+            }
+        };
+        auto mma = [&](const Frags& q) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) x[d][p][i] = AC ? a.cols(m0 + 32 * i, k, p) : a.rows(m0 + 32 * i, k, p);
-                }
+            for (int s = PL == 2 ? 0 : 2; s < 3; ++s)  // lo hi, hi lo, hi hi
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-                for (int s = PL == 2 ? 0 : 2; s < 3; ++s)  // lo hi, hi lo, hi hi
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) acc[f][i] = mma16<false>(y[d][s == 1], x[d][s == 0][i], acc[f][i]);
+                for (int i = 0; i < 2; ++i) acc[f][i] = mma16<false>(q.y[s == 1], q.x[s == 0][i], acc[f][i]);
+        };
+        load(g[0], 0);
+        for (int k = 0; k < K; k += 32) {  // K is a multiple of 64; the next 16 k's reads before these ones' products
+            load(g[1], k + 16);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(g[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(g[0], k + 32 < K ? k + 32 : k);
+            __builtin_amdgcn_sched_barrier(0);
+            mma(g[1]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -129,27 +171,41 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
     __shared__ double red[kWaves];
     const Matrix<PL> X{lds, row_chunks(PL, q.cols_pad)}, S{lds + q.rows_pad * X.chunks * 16, row_chunks(PL, q.k_pad)};
     const int gc = q.cols_pad / 8, groups = q.rows_pad * gc;
-    // eight elements of the update, and the momentum behind it; twice, since they would not stay in registers
-    auto update8 = [&](int row, int col, int n, float (&u)[8], float (&m)[8]) __attribute__((always_inline)) {
-        load8_of(q.x_dtype, (const void*)q.x, row * q.ld_x + col, n, u);
-        if (!a.h.step) return;
-        load8_of(IQLH_F32, (const void*)q.momentum, row * q.ld_momentum + col, n, m);
+    // f(row, column, elements in the row, eight elements of the update, of the momentum behind it), for every group of eight; in
+    // batches whose loads are made together.  Called twice, since the update would not stay in registers.
+    constexpr int BATCH = 4;
+    auto each8 = [&](auto f) __attribute__((always_inline)) {
+        for (int e0 = threadIdx.x; e0 < groups; e0 += BATCH * kNT) {
+            float u[BATCH][8], m[BATCH][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            m[i] = fmaf(a.h.mu, m[i], u[i]);
-            u[i] = a.h.nesterov ? fmaf(a.h.mu, m[i], u[i]) : m[i];
+            for (int j = 0; j < BATCH; ++j) {
+                const int e = e0 + j * kNT, row = e / gc, col = 8 * (e - row * gc), n = row < q.rows ? q.cols - col : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[j][i] = 0.f;
+                if (n <= 0) continue;
+                load8_of(q.x_dtype, (const void*)q.x, row * q.ld_x + col, n, u[j]);
+                if (a.h.step) load8_of(IQLH_F32, (const void*)q.momentum, row * q.ld_momentum + col, n, m[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                const int e = e0 + j * kNT, row = e / gc, col = 8 * (e - row * gc), n = row < q.rows ? q.cols - col : 0;
+                if (e >= groups) continue;
+                if (a.h.step && n > 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        m[j][i] = fmaf(a.h.mu, m[j][i], u[j][i]);
+                        u[j][i] = a.h.nesterov ? fmaf(a.h.mu, m[j][i], u[j][i]) : m[j][i];
+                    }
+                }
+                f(row, col, n, u[j], m[j]);
+            }
         }
     };
     double sum = 0.0;
-#pragma unroll 4
-    for (int e = threadIdx.x; e < groups; e += kNT) {
-        const int row = e / gc, col = 8 * (e - row * gc), n = q.cols - col;
-        float u[8], m[8];
-        if (row >= q.rows || n <= 0) continue;
-        update8(row, col, n, u, m);
+    each8([&](int, int, int, const float (&u)[8], const float (&)[8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fma((double)u[i], (double)u[i], sum);
-    }
+    });
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
@@ -164,14 +220,8 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
         if (a.h.step) return;
     }
     const double scale = ok ? (double)kUp / (norm + a.h.eps) : 0.0;
-#pragma unroll 2
-    for (int e = threadIdx.x; e < groups; e += kNT) {
-        const int row = e / gc, col = 8 * (e - row * gc), n = q.cols - col;
-        float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m[8];
-        if (row < q.rows && n > 0) {
-            update8(row, col, n, u, m);
-            if (a.h.step) store8_of(IQLH_F32, (void*)q.momentum, row * q.ld_momentum + col, n, m);
-        }
+    each8([&](int row, int col, int n, const float (&u)[8], const float (&m)[8]) __attribute__((always_inline)) {
+        if (a.h.step && n > 0) store8_of(IQLH_F32, (void*)q.momentum, row * q.ld_momentum + col, n, m);
         float lo[4], hi[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -180,7 +230,7 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
         }
         X.put4(row, col, lo);
         X.put4(row, col + 4, hi);
-    }
+    });
     __syncthreads();
     const bool tall = q.rows > q.cols;
     const int nts = q.k_pad / 32, ts = q.k_pad / 64 * nts, ntx = q.cols_pad / 32, tx = q.rows_pad / 64 * ntx;
@@ -221,16 +271,21 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
     each4(tx, ntx, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
         if (m >= q.rows || n >= q.cols) return;
         const int64_t at = m * q.ld_out + n;
-        float old[8], y[8];
-        const int left = q.cols - n < 4 ? q.cols - n : 4;
-        if (a.h.step) load8_of(q.out_dtype, (const void*)q.out, at, left, old);
+        const bool four = n + 4 <= q.cols;
+        float old[4] = {0.f, 0.f, 0.f, 0.f}, y[4];
+        if (a.h.step) {
+            if (four) load4_of(q.out_dtype, (const void*)q.out, at, old);
+            else
+                for (int e = 0; n + e < q.cols; ++e) old[e] = load1_of(q.out_dtype, (const void*)q.out, at + e);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             y[e] = ok ? v[e] * kDown : __uint_as_float(0x7FC00000u);
             if (a.h.step) y[e] = fmaf(-rate, y[e], a.h.keep * old[e]);
-            y[4 + e] = 0.f;
         }
-        store8_of(q.out_dtype, (void*)q.out, at, left, y);
+        if (four) store4_of(q.out_dtype, (void*)q.out, at, y);
+        else
+            for (int e = 0; n + e < q.cols; ++e) store1_of(q.out_dtype, (void*)q.out, at + e, y[e]);
     });
 }
 
