@@ -239,7 +239,12 @@ IQLH_DEV void tile_product(const Side16& a, const Side16& b, int64_t m0, int64_t
             run(s, C3(), C1(), C0(), C2());
         }
         landed(s + 1);
-        next(s + NB);
+        if constexpr (TILE == 64) {
+            issue(s + NB);
+            there = whole = false;
+        } else {
+            next(s + NB);
+        }
         run(s + 1, C0(), C0(), C1(), C0());
     }
     wait_vm<0>();  // the copies behind the last step, before their buffers are used again
