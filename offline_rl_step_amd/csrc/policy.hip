@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     __shared__ uint32_t tops[3];
     const int lane = threadIdx.x & 63;
     const bool f32 = a.dtype == IQLH_F32;
-    if (a.part) {
+    if (a.part && (f32 || blockIdx.x == 0)) {  // 16-bit matrices need no factor of their own
         if (threadIdx.x < 3 * kWave) {
             uint32_t top = 0u;
             for (int i = lane; i < kAbsBlocks; i += kWave) {
@@ -188,18 +188,64 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     }
     const float up = f32 ? up_to(tops[c.top], 14) : 1.f;
     constexpr int AHEAD = 4;
-    for (int64_t at = (int64_t)block * (AHEAD * kNT); at < q.rows * groups; at += (int64_t)c.blocks * (AHEAD * kNT)) {
-        float v[AHEAD][8];
-        Place p[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            p[k] = place_of(at, threadIdx.x + k * kNT, groups);
-            fetch(p[k].row, 8 * p[k].group, c.zero_off && p[k].row < q.rows && row_off(a.taken, a.row_weights, a.actions, p[k].row), v[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (p[k].row < q.rows) put(p[k].row, 8 * p[k].group, v[k], up);
+    const int64_t total = q.rows * groups;
+    if (q.cols < 8) {
+        for (int64_t at = (int64_t)block * (AHEAD * kNT) + threadIdx.x; at < total; at += (int64_t)c.blocks * (AHEAD * kNT))
+            for (int64_t e = at; e < total && e < at + AHEAD * kNT; e += kNT) {
+                const int64_t row = e / groups;
+                const int col = 8 * (int)(e - row * groups);
+                float v[8];
+                fetch(row, col, c.zero_off && row_off(a.taken, a.row_weights, a.actions, row), v);
+                put(row, col, v, up);
+            }
+        return;
     }
+    // The loads of AHEAD groups with nothing between them that waits: a row's last group is read from its last 8
+    // elements and moved, a row that is off is read too (10007 x 501 and 777 x 501, f16: 11 -> 7 us)
+    auto sweep = [&](auto wide) __attribute__((always_inline)) {
+        constexpr bool F32 = decltype(wide)::value;
+        for (int64_t at = (int64_t)block * (AHEAD * kNT); at < total; at += (int64_t)c.blocks * (AHEAD * kNT)) {
+            u4_a2 x[AHEAD];
+            u4_a4 y[AHEAD];
+            Place p[AHEAD];
+            int32_t t[AHEAD];
+            float w[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                p[k] = place_of(at, threadIdx.x + k * kNT, groups);
+                const int64_t row = p[k].row < q.rows ? p[k].row : q.rows - 1;
+                const int64_t from = row * q.ld + (8 * (int64_t)p[k].group < q.cols - 8 ? 8 * p[k].group : q.cols - 8);
+                if constexpr (F32) {
+                    const u4_a4* s = (const u4_a4*)((const float*)q.p + from);
+                    x[k] = s[0], y[k] = s[1];
+                } else {
+                    x[k] = *(const u4_a2*)((const uint16_t*)q.p + from);
+                }
+                t[k] = c.zero_off ? a.taken[row] : 0;
+                w[k] = c.zero_off && a.row_weights ? a.row_weights[row] : 1.f;
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (p[k].row >= q.rows) continue;
+                const int64_t past = 8 * (int64_t)p[k].group - (q.cols - 8);
+                const int move = past < 0 ? 0 : past > 8 ? 8 : (int)past;
+                const bool off = t[k] < 0 || t[k] >= a.actions || w[k] == 0.f || move == 8;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (F32) v[i] = __uint_as_float(i < 4 ? x[k][i] : y[k][i - 4]);
+                    else v[i] = a.dtype == IQLH_BF16 ? brain_of(x[k][i >> 1], i & 1) : half_of(x[k][i >> 1], i & 1);
+                    v[i] = off ? 0.f : v[i];
+                }
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = move & o ? (i + o < 8 ? v[i + o] : 0.f) : v[i];
+                put(p[k].row, 8 * p[k].group, v, up);
+            }
+        }
+    };
+    f32 ? sweep(std::true_type()) : sweep(std::false_type());
 }
 
 // ------------------------------------------------------------------ tiles
@@ -554,11 +600,16 @@ constexpr int64_t kFewRows = 64;
 
 int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 int64_t tiles_of(int64_t m, int64_t n, int t) { return ((m + t - 1) / t) * ((n + t - 1) / t); }
-// 256 tiles where they occupy most compute units
-int tile_for(int64_t m, int64_t n, int planes) { return planes == 1 && tiles_of(m, n, 256) >= 192 ? 256 : 128; }
+// Tiles of 256 where those of 128, two to a compute unit, would need more than one round: loss and gradients' two
+// products of logits of 1280 x 8192 x 512 bf16 (160 tiles) 42 us against 48, of 2048 x 16384 x 512 87 against 106;
+// but of 1024 x 8192 x 512 (128 tiles) 41 against 33.  With two planes from 192 tiles on: 1280 x 9000 x 1024 (180
+// tiles) 166 against 160 us, 4096 x 16384 x 512 486 against 502.
+int tile_for(int64_t m, int64_t n, int planes) { return tiles_of(m, n, 256) > (planes == 1 ? 128 : 192) ? 256 : 128; }
 
-// Parts of the summed axis, so that there are about two workgroups of 128 tiles to a
-// compute unit, of 512 elements or more
+// Parts of the summed axis, of 512 elements or more, so that there are 384 workgroups of 128 tiles, 512 with two
+// planes, and none where half as many are there without.  dH of 777 x 501 over 10007 actions: 21 us and the join 7,
+// unsplit 109.  More parts gain less than their join takes: dW of 8192 x 512 over 1280 rows 20 us and the join 22 in
+// two parts, 21.5 whole; dH of 4096 x 512 over 16384 actions in two planes, three parts 239 and 13, four 202 and 8.
 struct Split {
     int tile, n;
     int64_t k;
@@ -566,7 +617,7 @@ struct Split {
 Split split_for(int64_t m, int64_t n, int64_t k, int planes) {
     Split s{tile_for(m, n, planes), 1, up(k, 64)};
     if (s.tile == 256) return s;
-    int64_t want = 512 / tiles_of(m, n, 128), most = (k + 511) / 512;
+    int64_t want = (planes == 1 ? 384 : 512) / tiles_of(m, n, 128), most = (k + 511) / 512;
     want = want < 1 ? 1 : want > most ? most : want;
     s.k = up((k + want - 1) / want, 64);
     s.n = (int)((k + s.k - 1) / s.k);
@@ -575,8 +626,8 @@ Split split_for(int64_t m, int64_t n, int64_t k, int planes) {
 
 }  // namespace
 
-// Actions of a piece: G of about 256 MB, which the Infinity Cache holds between its
-// three uses, but enough for dW to have tiles
+// Actions of a piece: G of 256 MB, what the Infinity Cache holds, but enough for dW to have tiles.  8192 x 65536
+// x 2048 bf16, loss and gradients: four pieces 7.37 ms, one of 1 GB 7.27 ms: not worth four times the workspace.
 PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bool grad) {
     PolicyPlan p{};
     p.planes = dtype == IQLH_F32 ? 2 : 1;
@@ -682,14 +733,15 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
     return hipGetLastError();
 }
 
-// f(binary16 or bfloat16, tile, planes); two planes take tiles of 128
+// f(binary16 or bfloat16, tile, planes); two planes are binary16's
 template <typename F>
 hipError_t by_operands(bool brain, int planes, int tile, F f) {
     typedef std::integral_constant<int, 1> One;
     typedef std::integral_constant<int, 2> Two;
     typedef std::integral_constant<int, 128> T128;
     typedef std::integral_constant<int, 256> T256;
-    if (planes == 2) f(std::false_type(), T128(), Two());
+    if (planes == 2 && tile == 256) f(std::false_type(), T256(), Two());
+    else if (planes == 2) f(std::false_type(), T128(), Two());
     else if (tile == 256) brain ? f(std::true_type(), T256(), One()) : f(std::false_type(), T256(), One());
     else brain ? f(std::true_type(), T128(), One()) : f(std::false_type(), T128(), One());
     return hipGetLastError();
