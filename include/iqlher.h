@@ -641,7 +641,7 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  * 2^38.
  *
  * Products are exact and sums in binary32 for bfloat16 and binary16; binary32
- * inputs are held in 22 bits.  Where an action taken has probability 0, nll and the
+ * inputs are held in 22 bits or more.  Where an action taken has probability 0, nll and the
  * loss are infinite; a row whose logits hold a NaN or plus infinity gets NaN.
  *
  * iqlh_policy_loss writes nll [rows] f32, lse [rows] f32 and, unless it is NULL, loss
@@ -654,8 +654,8 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  *   d_hidden = G weight   [rows][ld_d_hidden] of `dtype`,
  *   d_weight = G^T hidden [actions][ld_d_weight] of `dtype`,
  *   d_bias   = column sums of G [actions] f32,
- * each of them unless it is NULL.  G is rounded to `dtype` (binary32: 22 bits) in the
- * two products, whose sums are binary32, and not in d_bias.
+ * each of them unless it is NULL.  G is rounded to `dtype` (binary32: 22 bits) or less in
+ * the two products, whose sums are binary32, and not in d_bias.
  *
  *   workspace  device, >= iqlh_policy_loss_workspace_bytes(.., grad 1 for the gradients),
  *              16-byte aligned, no initial contents required; calls that overlap in
@@ -701,7 +701,8 @@ int iqlh_policy_loss_grad(const iqlh_policy_head* head, const int32_t* taken, co
  *   momentum  device [rows][ld_momentum] f32, or NULL in every matrix.
  *   compute_dtype  IQLH_F16: operands of 11 bits, the result is off by about 1e-3
  *             of its size (a bfloat16 result's own rounding is 1.7e-3); IQLH_F32: 22 bits,
- *             about 1e-6, at up to three times the time.
+ *             about 1e-6, at up to three times the time.  Matrices with a side under 64
+ *             always take the latter.
  *   host_table >= iqlh_matrix_set_bytes bytes, 16-byte aligned, and so must be
  *             its device copy.
  * Types are IQLH_F32, IQLH_BF16, IQLH_F16 in any mix, pointers aligned to their

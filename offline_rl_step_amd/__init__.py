@@ -701,7 +701,7 @@ def policy_loss_workspace(rows, actions, dim, dtype, grad=False, device=None):
     return torch.empty(size, dtype=torch.uint8, device=device)
 
 
-def _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace):
+def _policy_head(hidden, weight, taken, bias, row_weights, scale):
     """(head, scale, device, device index) of the arguments both calls share."""
     device = hidden.device
     index = _need_current(device)
@@ -729,7 +729,7 @@ def policy_loss(hidden, weight, taken, out_nll, out_lse, workspace, bias=None, r
     """Softmax cross entropy of the actions `taken` [rows] int32 under the logits hidden [rows,
     dim] weight [actions, dim]^T + bias: minus the log-probabilities, the rows' log-sum-exp and
     scale (default 1 / rows) sum row_weights nll into out_loss."""
-    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace)
+    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale)
     _need_f32(out_nll, head.rows, device, "out_nll")
     _need_f32(out_lse, head.rows, device, "out_lse")
     if out_loss is not None:
@@ -745,7 +745,7 @@ def policy_loss_grad(hidden, weight, taken, lse, workspace, bias=None, row_weigh
                      d_weight=None, d_bias=None, stream=None):
     """Gradients of policy_loss's loss, given the lse that it wrote for the same arguments: d_hidden
     and d_weight of the inputs' type, d_bias [actions] float32, each unless it is None."""
-    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale, workspace)
+    head, scale, device, index = _policy_head(hidden, weight, taken, bias, row_weights, scale)
     _need_f32(lse, head.rows, device, "lse")
     ldh = ldw = 0
     if d_hidden is not None:
