@@ -137,7 +137,11 @@ def test_a_run_in_a_graph_and_two_runs_at_once(m, rows, dim, actions, dtype):
 @pytest.mark.parametrize("rows,dim,actions,dtype", [(2100, 24, 6500, "float32"),  # 234 tiles of 256, two planes
                                                     (1100, 24, 8200, "bfloat16"),  # 165, one
                                                     (300, 16, 17, "float16"), (300, 16, 16, "float16"),
-                                                    (16, 40, 5000, "float32"), (17, 40, 5000, "float32")])
+                                                    (16, 40, 5000, "float32"), (17, 40, 5000, "float32"),
+                                                    # the widest that few actions' and few rows' kernels take, and wider
+                                                    (40, 1024, 16, "float32"), (40, 1025, 16, "float32"),
+                                                    (16, 1980, 300, "float32"), (16, 4000, 300, "bfloat16"),
+                                                    (16, 4104, 300, "bfloat16"), (3, 16384, 40, "float16")])
 def test_where_the_kernels_change(m, rows, dim, actions, dtype):
     c = policy._case(7, rows, dim, actions, dtype)
     out = policy._run(m, c)
