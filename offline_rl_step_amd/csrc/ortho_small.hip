@@ -302,13 +302,14 @@ int64_t ortho_small_bytes(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int
     return (int64_t)rows_pad * row_chunks(planes, cols_pad) * 16 + (int64_t)k_pad * row_chunks(planes, k_pad) * 16;
 }
 // 158 KB: what the sums take is in LDS too
+constexpr int kMostBytes = 158 << 10;
 bool ortho_small_ok(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes) {
     return (int64_t)rows_pad * cols_pad <= kMostElements && (int64_t)k_pad * k_pad <= kMostElements &&
-           ortho_small_bytes(rows_pad, cols_pad, k_pad, planes) <= 158 << 10;
+           ortho_small_bytes(rows_pad, cols_pad, k_pad, planes) <= kMostBytes;
 }
 
 hipError_t launch_ortho_small(const OrthoArgs& a, hipStream_t stream) {
-    (void)hipFuncSetAttribute((const void*)ortho_small_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, a.small_bytes);
+    (void)hipFuncSetAttribute((const void*)ortho_small_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kMostBytes);
     hipLaunchKernelGGL(ortho_small_kernel, dim3(a.nsmall), dim3(kNT), a.small_bytes, stream, a);
     return hipGetLastError();
 }
