@@ -66,7 +66,7 @@ IQLH_DEV Place place_of(int64_t at, int i, int groups) {
 }
 
 // Largest finite |x| of up to three matrices, kAbsBlocks workgroups each; of the
-// first without rows that are off where `taken` is given
+// first (hidden) and the last (the rows' weights) without rows that are off
 struct AbsMaxArgs {
     PolicyMat m[3];
     uint32_t* part;  // [3][kAbsBlocks]
@@ -77,7 +77,7 @@ struct AbsMaxArgs {
 __global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
     __shared__ uint32_t red[kNT / kWave];
     const PolicyMat& q = a.m[blockIdx.y];
-    const bool skip = blockIdx.y == 0 && a.taken;
+    const bool skip = blockIdx.y == 0, weights = blockIdx.y == 2;
     uint32_t top = 0u;
     if (q.p) {
         const int groups = (int)((q.cols + 7) / 8);
@@ -90,7 +90,8 @@ __global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
             load8_of(q.dtype, q.p, row * q.ld + col, q.cols - col, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t b = finite_bits(v[i]);
+                uint32_t b = finite_bits(v[i]);
+                if (weights && b > top && row_off(a.taken, a.row_weights, a.actions, col + i)) b = 0u;
                 top = b > top ? b : top;
             }
         }
