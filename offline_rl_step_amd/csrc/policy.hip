@@ -382,6 +382,12 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
             for (int j = 0; j < FB; ++j)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = w * __builtin_amdgcn_exp2f(acc[i][j][e]);
+            if (__any(w == 0.f)) {  // rows that are off, also where an infinite weight made NaN of their zeros
+#pragma unroll
+                for (int j = 0; j < FB; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[i][j][e] = w == 0.f ? 0.f : acc[i][j][e];
+            }
             if (__any(col[i] >= 0 && col[i] < 32 * FB)) {
 #pragma unroll
                 for (int j = 0; j < FB; ++j)

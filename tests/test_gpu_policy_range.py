@@ -1,4 +1,6 @@
 """Policy loss: rows that are off, whatever their weights are."""
+import math
+
 import pytest
 
 from tests.gpu_util import sync
@@ -28,3 +30,24 @@ def test_finite_weights_of_rows_that_are_off(m, rows, dtype, weight):
         sync()
         for k in out:
             assert torch.equal(out[k], clean[k]), (k, row)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("rows", [9, 200])
+def test_off_rows_next_to_an_infinite_weight(m, rows, dtype):
+    """An action whose weights hold minus infinity where hidden is positive has probability 0: nothing of it in
+    its weight's and bias's gradients, whatever the rows that are off hold."""
+    import torch
+    c = _case(27, rows, 48, 90, dtype)
+    c["taken"][:3] = torch.tensor([-1, 90, -1], dtype=torch.int32)
+    c["taken"][c["taken"] == 17] = 18
+    c["bias"].copy_(torch.nan_to_num(c["bias"], neginf=0.0))
+    c["hidden"][:, 5] = 1.0
+    c["weight"][17, 5] = -math.inf
+    out = _run(m, c)
+    sync()
+    on = c["taken"] >= 0
+    on &= c["taken"] < 90
+    assert bool(out["lse"][on].isfinite().all()) and math.isfinite(float(out["loss"]))
+    assert bool(out["dw"].isfinite().all()) and bool(out["db"].isfinite().all())
+    assert bool((out["dw"][17] == 0).all()) and float(out["db"][17]) == 0
