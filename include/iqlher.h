@@ -640,9 +640,14 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  * 1 <= rows, actions <= 2^24, 1 <= dim <= 2^14, each product of two of them at most
  * 2^38.
  *
- * Products are exact and sums in binary32 for bfloat16 and binary16; binary32
- * inputs are held in 22 bits or more.  Where an action taken has probability 0, nll and the
- * loss are infinite; a row whose logits hold a NaN or plus infinity gets NaN.
+ * Sums are binary32.  Products of bfloat16 and binary16 inputs are exact.  Binary32 inputs
+ * take part as they are for up to 16 actions (of dim up to 1024) and in the loss of up to 16
+ * rows (of dim up to about 32768 / rows); else they are held in 22 bits, and no finer than 2^-38
+ * of the largest of what they share a power of two with.  In the logits that is, with c the
+ * largest |weight| of each column, the row's largest |hidden c| and the action's largest
+ * |weight / c|.  (An infinity among them may make NaN of the rows it is multiplied into.)
+ * Where an action taken has probability 0, nll and the loss are infinite; a row whose
+ * logits hold a NaN or plus infinity gets NaN.
  *
  * iqlh_policy_loss writes nll [rows] f32, lse [rows] f32 and, unless it is NULL, loss
  * [1] f32 (from a binary64 sum); d_flags (or NULL) gets IQLH_FLAG_NONFINITE_LOSS for a
@@ -654,8 +659,13 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  *   d_hidden = G weight   [rows][ld_d_hidden] of `dtype`,
  *   d_weight = G^T hidden [actions][ld_d_weight] of `dtype`,
  *   d_bias   = column sums of G [actions] f32,
- * each of them unless it is NULL.  G is rounded to `dtype` (binary32: 22 bits) or less in
- * the two products, whose sums are binary32, and not in d_bias.
+ * each of them unless it is NULL.  In the two products, not in d_bias, G is rounded to
+ * `dtype`, up to 64 rows to twice as many bits; binary16 (2^-25 at the smallest) after a power
+ * of two that takes the largest |row_weights| of rows that count to [2^13, 2^14): probabilities below
+ * about 2^-27 of that lose bits, below 2^-38 all.  Binary32 (unless as it is, above): G in 22 bits, no finer than
+ * 2^-38 of |scale row_weights| of its row, so that an action's own d_weight is held to 2^-38 of
+ * what it would be with probability 1; weight, in d_hidden, and hidden times its row's weight, in
+ * d_weight, in 22 bits and no finer than 2^-38 of their column's largest.
  *
  *   workspace  device, >= iqlh_policy_loss_workspace_bytes(.., grad 1 for the gradients),
  *              16-byte aligned, no initial contents required; calls that overlap in

@@ -358,7 +358,8 @@ struct PolicyArgs {
 constexpr int kAbsBlocks = 256;
 // Byte offsets in the workspace and the pieces the actions are taken in
 struct PolicyPlan {
-    size_t factors, absmax, row_factor, h, h_dw, w, part, z_taken, loss_part, g, db_part, dh_sums, dw_sums, bytes;
+    size_t row_exp, act_exp, cols, g_top, weight_top, h, h_dw, w, w_dh, part, z_taken, loss_part, g, db_part, dh_sums, dw_sums,
+        bytes;
     int64_t ld, piece;
     int32_t planes, g_planes, pieces;
     bool few_actions, few_rows;

@@ -13,9 +13,16 @@
 // dH summed over the pieces in binary32.
 //
 // Bfloat16 inputs: G is bfloat16.  Binary16 inputs: G is binary16 times a power of
-// two by the largest |w|, so that probabilities down to 1e-12 are held.  Binary32
-// inputs: H, W and G are two planes of binary16 each (tile16.hpp), times powers of two by
-// their largest elements, 22 bits.
+// two by the largest |w|: 11 bits down to p |w| of 2^-27 of that, 0 below 2^-38.
+//
+// Binary32 inputs: H, W and G are two planes of binary16 each (tile16.hpp) behind a power of two that takes
+// the largest of what shares it to [2^13, 2^14): 22 bits for what is within 2^-17 of that largest, and to 2^-38 of
+// it below.  What is not summed together, or can be moved to the other side of the product, shares none.  With
+// c_d the largest |W_vd| of a column, as powers of two all of them:
+//   z = sum_d (H_rd c_d) (W_vd / c_d)      a factor for each row and each action,
+//   dH = sum_v G_rv W_vd                   for each row of G (by |w_r|) and each column of W,
+//   dW = sum_r (G_rv / |w_r|) (H_rd |w_r|) for each column of H |w|, G as for dH.
+// One factor for a matrix lost all bits of a column that another is 2^30 times as large as.
 //
 // Bound by the products, the logits' twice: 8192 x 65536 x 2048 bf16 7.1 ms, 1.17 to 1.26 PF each; 16384 x 32768 x
 // 512 bf16, loss alone, 0.51 ms, 1.08 PF; 4096 x 16384 x 512 fp32 0.84 ms, 0.9 to 1.1 PF of binary16 products.  What is not
@@ -28,26 +35,22 @@ using namespace policy;
 
 namespace {
 
-// Factors of a call, powers of two (times the loss's scale): of sums to logits, of G as it is stored, of the gradients' sums
-struct Factors {
-    float z, g, dh, dw, db, reserved[3];
-};
-IQLH_DEV float up_to(uint32_t bits, int top) {  // 2^n that takes a finite value of these bits to [2^(top - 1), 2^top)
-    const int e = (int)(bits >> 23);            // subnormal ones count as 2^-126
-    int n = top - (e ? e - 126 : -125);
-    n = bits == 0u ? 0 : n < -126 ? -126 : n > 126 ? 126 : n;
-    return __uint_as_float((uint32_t)(n + 127) << 23);
+// Magnitude of x: b with |x| in [2^(b - 1), 2^b), subnormal ones as 2^-126; kNoBits for 0 and what is not finite
+constexpr int kNoBits = -100000, kTop = 14;  // kTop: magnitude of the largest element in planes
+IQLH_DEV int bits_of(float x) {
+    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+    return b == 0u || b >= 0x7F800000u ? kNoBits : b >> 23 ? (int)(b >> 23) - 126 : -125;
 }
+IQLH_DEV int or_zero(int bits) { return bits < -1000 ? 0 : bits; }  // of nothing but zeros: any power of two will do
+// Of a row's weight, or the largest: 2^(kTop - b) is a normal binary32 number, as its inverse is
+IQLH_DEV int weight_bits(int bits) { return or_zero(bits) < kTop - 126 ? kTop - 126 : or_zero(bits); }
+IQLH_DEV int weight_bits(const float* row_weights, int64_t m) { return row_weights ? weight_bits(bits_of(row_weights[m])) : 1; }
 
 // ------------------------------------------------------------ preparation
-IQLH_DEV uint32_t finite_bits(float x) {
-    const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
-    return b < 0x7F800000u ? b : 0u;
-}
-IQLH_DEV uint32_t wave_umax(uint32_t v) {
+IQLH_DEV int wave_imax(int v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) {
-        const uint32_t b = (uint32_t)__shfl_xor((int)v, o, kWave);
+        const int b = __shfl_xor(v, o, kWave);
         v = b > v ? b : v;
     }
     return v;
@@ -65,90 +68,127 @@ IQLH_DEV Place place_of(int64_t at, int i, int groups) {
     return Place{row + r, (int)(g - r * (uint32_t)groups)};
 }
 
-// Largest finite |x| of up to three matrices, kAbsBlocks workgroups each; of the
-// first (hidden) and the last (the rows' weights) without rows that are off
-struct AbsMaxArgs {
-    PolicyMat m[3];
-    uint32_t* part;  // [3][kAbsBlocks]
-    const int32_t* taken;
-    const float* row_weights;
-    int64_t actions;
-};
-__global__ __launch_bounds__(kNT) void policy_absmax_kernel(AbsMaxArgs a) {
-    __shared__ uint32_t red[kNT / kWave];
-    const PolicyMat& q = a.m[blockIdx.y];
-    const bool skip = blockIdx.y == 0, weights = blockIdx.y == 2;
-    uint32_t top = 0u;
-    if (q.p) {
-        const int groups = (int)((q.cols + 7) / 8);
-        for (int64_t at = (int64_t)blockIdx.x * kNT; at < q.rows * groups; at += (int64_t)kAbsBlocks * kNT) {
-            const Place p = place_of(at, threadIdx.x, groups);
-            const int64_t row = p.row, col = 8 * p.group;
-            if (row >= q.rows) continue;
-            if (skip && row_off(a.taken, a.row_weights, a.actions, row)) continue;
-            float v[8];
-            load8_of(q.dtype, q.p, row * q.ld + col, q.cols - col, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t b = finite_bits(v[i]);
-                if (weights && b > top && row_off(a.taken, a.row_weights, a.actions, col + i)) b = 0u;
-                top = b > top ? b : top;
-            }
-        }
+// Magnitude of the largest weight of a row that is on, of kAbsBlocks workgroups each
+__global__ __launch_bounds__(kNT) void policy_weights_kernel(const int32_t* taken, const float* row_weights, int64_t rows, int64_t actions,
+                                                             int32_t* part) {
+    __shared__ int red[kNT / kWave];
+    int top = kNoBits;
+    for (int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x; m < rows; m += (int64_t)kAbsBlocks * kNT) {
+        const int b = row_off(taken, row_weights, actions, m) ? kNoBits : bits_of(row_weights[m]);
+        top = b > top ? b : top;
     }
-    top = wave_umax(top);
+    top = wave_imax(top);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 1; i < kNT / kWave; ++i) top = red[i] > top ? red[i] : top;
-        a.part[blockIdx.y * kAbsBlocks + blockIdx.x] = top;
+        part[blockIdx.x] = top;
     }
 }
 
-// The factors, and matrices as operands: rows of whole 64 16-bit elements, zeros behind the
-// end, binary32 in two planes.
+__global__ __launch_bounds__(kNT) void policy_empty_kernel(int32_t* cols, int n) {
+    const int i = blockIdx.x * kNT + threadIdx.x;
+    if (i < n) cols[i] = kNoBits;
+}
+
+// Magnitudes of the columns of hidden (blockIdx.z 0; its rows' weights times them, rows that are off left out) and of
+// the head's weights (1), binary32: 8 `lanes` columns a workgroup, each lane 8 of every (gridDim.x kNT / lanes)-th row.
+// gridDim.x above 1: columns that policy_empty_kernel left.
+struct ColumnArgs {
+    PolicyMat m[2];
+    int32_t* to[2];
+    const int32_t* taken;
+    const float* row_weights;
+    int64_t actions, ld;
+    int lanes;
+};
+__global__ __launch_bounds__(kNT) void policy_columns_kernel(ColumnArgs a) {
+    constexpr int AHEAD = 8;
+    __shared__ int red[kNT][8];
+    const PolicyMat& q = a.m[blockIdx.z];
+    if (!q.p) return;
+    const int lane = threadIdx.x % a.lanes, own = threadIdx.x / a.lanes, at_once = kNT / a.lanes;
+    const int first = blockIdx.y * 8 * a.lanes, col = first + 8 * lane, n = (int)q.cols - col;
+    int top[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = kNoBits;
+    auto sweep = [&](auto hidden) __attribute__((always_inline)) {
+        const int64_t step = (int64_t)gridDim.x * at_once;
+        for (int64_t row0 = (int64_t)blockIdx.x * at_once + own; row0 < q.rows; row0 += AHEAD * step) {
+            float v[AHEAD][8];
+            int32_t t[AHEAD];
+            float w[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {  // behind the end: the first row again
+                const int64_t row = row0 + k * step < q.rows ? row0 + k * step : row0;
+                t[k] = decltype(hidden)::value ? a.taken[row] : 0;
+                w[k] = decltype(hidden)::value && a.row_weights ? a.row_weights[row] : 1.f;
+                load8_of(IQLH_F32, q.p, row * q.ld + col, n, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const bool off = t[k] < 0 || t[k] >= a.actions || w[k] == 0.f;
+                const int add = !decltype(hidden)::value ? 0 : off ? kNoBits : weight_bits(bits_of(w[k]));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int b = bits_of(v[k][i]) + add;
+                    top[i] = b > top[i] ? b : top[i];
+                }
+            }
+        }
+    };
+    if (n > 0) blockIdx.z == 0 ? sweep(std::true_type()) : sweep(std::false_type());
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = top[i];
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c < 8 * a.lanes && first + c < a.ld) {
+        int t = kNoBits;
+        for (int k = 0; k < at_once; ++k) {
+            const int b = red[k * a.lanes + c / 8][c % 8];
+            t = b > t ? b : t;
+        }
+        int32_t* to = a.to[blockIdx.z] + first + c;
+        if (gridDim.x == 1) *to = t;
+        // mostly there already: many workgroups' atomics on one line wait for each other
+        else if (t > -1000 && t > __hip_atomic_load(to, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(to, t);
+    }
+}
+
+// Matrices as operands: rows of whole 64 16-bit elements, zeros behind the end.  Binary32 in two planes: x in row r
+// and column d times 2^(kTop + sign cols[d]) and (weighted) the weight's magnitude, or, by rows, times 2^(sign cols[d] - row_exp[r]) with
+// row_exp of the row's largest, which is written.
 struct Convert {
     PolicyMat m;
-    uint16_t* to;         // [rows][ld_to]
+    uint16_t* to;             // [rows][ld_to]
     int64_t ld_to;
-    float* row_factor;    // null: one factor for the matrix (binary32), by part `top`
-    int top, zero_off;    // zero_off: zeros in the place of rows that are off
-    int blocks;
+    const int32_t* cols;      // binary32: [ld_to]
+    int32_t* row_exp;         // or null: not by rows
+    int sign, zero_off;       // zero_off: zeros in the place of rows that are off
+    int weighted;
+    int lanes, blocks;        // lanes: of a row, a power of two
 };
 struct ConvertArgs {
-    Convert c[3];
-    const uint32_t* part;  // or null: no factors
-    Factors* f;
+    Convert c[4];
+    const int32_t* part;  // binary16: [kAbsBlocks], or null
+    int32_t* g_top;       // their largest
     const int32_t* taken;
     const float* row_weights;
     int64_t actions;
-    float scale;
     int dtype;
 };
 __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
-    __shared__ uint32_t tops[3];
     const int lane = threadIdx.x & 63;
     const bool f32 = a.dtype == IQLH_F32;
-    if (a.part && (f32 || blockIdx.x == 0)) {  // 16-bit matrices need no factor of their own
-        if (threadIdx.x < 3 * kWave) {
-            uint32_t top = 0u;
-            for (int i = lane; i < kAbsBlocks; i += kWave) {
-                const uint32_t b = a.part[(threadIdx.x >> 6) * kAbsBlocks + i];
-                top = b > top ? b : top;
-            }
-            top = wave_umax(top);
-            if (lane == 0) tops[threadIdx.x >> 6] = top;
-        }
-        __syncthreads();
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            const float h = f32 ? up_to(tops[0], 14) : 1.f, w = f32 ? up_to(tops[1], 14) : 1.f;
-            const float g = up_to(a.row_weights ? tops[2] : __float_as_uint(1.f), 14), s = a.scale / g;
-            *a.f = Factors{1.f / w, g, s / w, s / h, s, {0.f, 0.f, 0.f}};
-        }
+    if (a.part && blockIdx.x == 0 && threadIdx.x < kWave) {
+        int top = kNoBits;
+        for (int i = lane; i < kAbsBlocks; i += kWave) top = a.part[i] > top ? a.part[i] : top;
+        top = wave_imax(top);
+        if (lane == 0) *a.g_top = weight_bits(top);
     }
     int k = 0, block = blockIdx.x;
-    while (k < 2 && block >= a.c[k].blocks) block -= a.c[k++].blocks;
+    while (k < 3 && block >= a.c[k].blocks) block -= a.c[k++].blocks;
     const Convert& c = a.c[k];
     const PolicyMat& q = c.m;
     if (!q.p) return;
@@ -158,40 +198,64 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
         if (row < q.rows && col < q.cols && !off) load8_of(a.dtype, q.p, row * q.ld + col, q.cols - col, v);
     };
-    auto put = [&](int64_t row, int col, float (&v)[8], float up) __attribute__((always_inline)) {
+    auto column_bits = [&](int col, int (&b)[8]) __attribute__((always_inline)) {
+        const int4 x = *(const int4*)(c.cols + col), y = *(const int4*)(c.cols + col + 4);
+        b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w, b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = c.sign * or_zero(b[i]);
+    };
+    // times 2^(e + b)
+    auto put = [&](int64_t row, int col, float (&v)[8], int e, const int (&b)[8]) __attribute__((always_inline)) {
         if (f32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= up;
+            for (int i = 0; i < 8; ++i) v[i] = ldexpf(v[i], e + b[i]);
             put_planes(c.to, row, c.ld_to, col, true, v);
         } else {
             store8_of(a.dtype, c.to, row * c.ld_to + col, 8, v);
         }
     };
-    if (c.row_factor) {  // a wave a row: its largest element, then the planes
-        for (int64_t row = (int64_t)block * (kNT / kWave) + (threadIdx.x >> 6); row < q.rows; row += (int64_t)c.blocks * (kNT / kWave)) {
-            const bool off = c.zero_off && row_off(a.taken, a.row_weights, a.actions, row);
-            uint32_t top = 0u;
-            if (!off)
-                for (int g = lane; 8 * g < q.cols; g += kWave) {
-                    float v[8];
-                    load8_of(a.dtype, q.p, row * q.ld + 8 * g, q.cols - 8 * g, v);
+    // By rows: as many lanes a row as it has groups, 64 at most; its largest element, then the planes.  A lane's first
+    // elements stay in registers.
+    if (c.row_exp) {
+        const int lanes = c.lanes, in = lane & (lanes - 1), rows_at_once = kNT / lanes;
+        int b0[8];
+        column_bits(8 * (in < groups ? in : 0), b0);
+        for (int64_t row0 = (int64_t)block * rows_at_once; row0 < q.rows; row0 += (int64_t)c.blocks * rows_at_once) {
+            const int64_t row = row0 + threadIdx.x / lanes;
+            const bool off = row < q.rows && c.zero_off && row_off(a.taken, a.row_weights, a.actions, row);
+            float v0[8];
+            fetch(row, 8 * in, off, v0);
+            int top = kNoBits;
+            auto largest = [&](const float (&v)[8], const int (&b)[8]) __attribute__((always_inline)) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t b = finite_bits(v[i]);
-                        top = b > top ? b : top;
-                    }
-                }
-            const float up = up_to(wave_umax(top), 14);
-            if (lane == 0) c.row_factor[row] = 1.f / up;
-            for (int g = lane; g < groups; g += kWave) {
+                for (int i = 0; i < 8; ++i) top = bits_of(v[i]) + b[i] > top ? bits_of(v[i]) + b[i] : top;
+            };
+            largest(v0, b0);
+            for (int g = in + kWave; g < groups; g += kWave) {
                 float v[8];
+                int b[8];
                 fetch(row, 8 * g, off, v);
-                put(row, 8 * g, v, up);
+                column_bits(8 * g, b);
+                largest(v, b);
+            }
+            for (int o = lanes / 2; o > 0; o >>= 1) {
+                const int b = __shfl_xor(top, o, kWave);
+                top = b > top ? b : top;
+            }
+            if (row >= q.rows) continue;
+            const int e = or_zero(top) - kTop;
+            if (in == 0) c.row_exp[row] = e;
+            if (in < groups) put(row, 8 * in, v0, -e, b0);
+            for (int g = in + kWave; g < groups; g += kWave) {
+                float v[8];
+                int b[8];
+                fetch(row, 8 * g, off, v);
+                column_bits(8 * g, b);
+                put(row, 8 * g, v, -e, b);
             }
         }
         return;
     }
-    const float up = f32 ? up_to(tops[c.top], 14) : 1.f;
     constexpr int AHEAD = 4;
     const int64_t total = q.rows * groups;
     if (q.cols < 8) {
@@ -200,8 +264,10 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
                 const int64_t row = e / groups;
                 const int col = 8 * (int)(e - row * groups);
                 float v[8];
+                int b[8] = {};
                 fetch(row, col, c.zero_off && row_off(a.taken, a.row_weights, a.actions, row), v);
-                put(row, col, v, up);
+                if (f32) column_bits(col, b);
+                put(row, col, v, kTop + (c.weighted ? weight_bits(a.row_weights, row) : 0), b);
             }
         return;
     }
@@ -246,7 +312,9 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
                 for (int o = 4; o > 0; o >>= 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = move & o ? (i + o < 8 ? v[i + o] : 0.f) : v[i];
-                put(p[k].row, 8 * p[k].group, v, up);
+                int b[8] = {};
+                if constexpr (F32) column_bits(8 * p[k].group, b);
+                put(p[k].row, 8 * p[k].group, v, kTop + (!F32 || !c.weighted ? 0 : a.row_weights ? weight_bits(bits_of(w[k])) : 1), b);
             }
         }
     };
@@ -272,8 +340,9 @@ struct LogitArgs {
     const int32_t* taken;
     const float* row_weights;  // or null
     const float* lse;
-    const Factors* f;        // or null: 1, scale, 1, 1
-    const float* row_factor;  // of the sums, or null: 1
+    const int32_t *row_exp, *act_exp;  // binary32: exponents of the sums' rows and columns (of the piece)
+    const int32_t* g_top;    // or null: of all weights
+    float g_factor;          // of G without either of them
     Soft* part;              // [n_tiles][rows]
     float* z_taken;          // [rows]
     uint16_t* g;             // [rows][ldg], for binary32 in two planes; else a second matrix behind `plane`
@@ -281,7 +350,6 @@ struct LogitArgs {
     int64_t rows, actions, first, ldg, plane;  // actions of the piece; its first one
     int64_t all_actions;
     int64_t k;               // summed elements
-    float scale;
     int g_planes, m_tiles, n_tiles;
 };
 
@@ -302,12 +370,23 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
     int* row_col = (int*)(col_bias + TILE);
     float* row_w = (float*)(row_col + TILE);
     float* row_lse = row_w + TILE;
+    int* row_exp = (int*)(row_lse + TILE);  // PL 2: exponents of the sums, and what takes G back to its size
+    int* col_exp = row_exp + TILE;
+    float* row_back = (float*)(col_exp + TILE);
     // (loaded before the product and put there behind it, so that the product does not wait for them)
     const int64_t mine = m0 + (threadIdx.x % TILE), mine_in = mine < a.rows ? mine : a.rows - 1;
     const int32_t t_in = a.taken[mine_in];
     const float b_in = a.bias && (int)(threadIdx.x % TILE) < there ? a.bias[n0 + threadIdx.x % TILE] : 0.f;
     const float w_in = GRAD && a.row_weights ? a.row_weights[mine_in] : 1.f, lse_in = GRAD ? a.lse[mine_in] : 0.f;
-    const float zf = (a.f ? a.f->z : 1.f) * kLog2e, gf = a.f ? a.f->g : a.scale;
+    int re_in = 0, ce_in = 0;
+    float gf = a.g_factor;
+    if constexpr (PL == 2) {
+        re_in = a.row_exp[mine_in];
+        ce_in = (int)(threadIdx.x % TILE) < there ? a.act_exp[n0 + threadIdx.x % TILE] : 0;
+        if (GRAD) gf = ldexpf(1.f, kTop - (a.row_weights ? weight_bits(bits_of(w_in)) : 1));
+    } else if (GRAD && a.g_top) {
+        gf = ldexpf(1.f, kTop - *a.g_top);
+    }
     mm_f16 acc[FA][FB];
     tile_product<BRAIN, TILE, false, false, PL>(a.h, a.w, m0, n0, 0, a.k, false, lds, acc);
     if (threadIdx.x < TILE) {
@@ -319,16 +398,18 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
         row_w[n] = off ? 0.f : w_in * gf;
         // no logit above minus infinity: no probabilities
         row_lse[n] = off ? __builtin_huge_valf() : lse_in == kNone ? 0.f : lse_in * kLog2e;
+        if (PL == 2) row_exp[n] = re_in, col_exp[n] = ce_in;
+        if (PL == 2 && GRAD) row_back[n] = 1.f / gf;
     }
     __syncthreads();
     const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
     const int wm = wave_m<TILE>(), wn = wave_n<TILE>();
-    float zr[FA], sub[FA];
-    int col[FA];
+    float sub[FA];
+    int col[FA], re[FA];
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
         const int row = wm + 32 * i + r;
-        zr[i] = a.row_factor && m0 + row < a.rows ? a.row_factor[m0 + row] * zf : zf;
+        re[i] = PL == 2 ? row_exp[row] : 0;
         sub[i] = GRAD ? row_lse[row] : 0.f;
         col[i] = row_col[row] - wn;
     }
@@ -338,10 +419,18 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
         for (int g = 0; g < 4; ++g) {
             const float4 b4 = *(const float4*)(col_bias + wn + 32 * j + 8 * g + 4 * h);
             const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+            int ce[4] = {};
+            if constexpr (PL == 2) {
+                const int4 e4 = *(const int4*)(col_exp + wn + 32 * j + 8 * g + 4 * h);
+                ce[0] = e4.x, ce[1] = e4.y, ce[2] = e4.z, ce[3] = e4.w;
+            }
 #pragma unroll
             for (int i = 0; i < FA; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][4 * g + e] = fmaf(acc[i][j][4 * g + e], zr[i], GRAD ? b[e] - sub[i] : b[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const float z = PL == 2 ? ldexpf(acc[i][j][4 * g + e], re[i] + ce[e]) : acc[i][j][4 * g + e];
+                    acc[i][j][4 * g + e] = fmaf(z, kLog2e, GRAD ? b[e] - sub[i] : b[e]);
+                }
         }
     if constexpr (!GRAD) {
         Soft(*rows)[T::WN] = (Soft(*)[T::WN])lds;  // [TILE]
@@ -398,14 +487,17 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
         }
         if (a.db_part) {  // sums over the tile's rows
             float(*sums)[TILE] = (float(*)[TILE])lds;  // [WM]
+            float back[FA];
+#pragma unroll
+            for (int i = 0; i < FA; ++i) back[i] = PL == 2 ? row_back[wm + 32 * i + r] : 1.f;
 #pragma unroll
             for (int jj = 0; jj < FB; jj += 2) {
                 float v[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    v[k] = acc[0][jj + k / 16][k % 16];
+                    v[k] = acc[0][jj + k / 16][k % 16] * back[0];
 #pragma unroll
-                    for (int i = 1; i < FA; ++i) v[k] += acc[i][jj + k / 16][k % 16];
+                    for (int i = 1; i < FA; ++i) v[k] = fmaf(acc[i][jj + k / 16][k % 16], back[i], v[k]);
                 }
                 // 32 values of 32 lanes: each exchange halves the values a lane has; lane r ends with value r
                 // (by masks: a selection of two elements becomes one of all 32)
@@ -519,13 +611,24 @@ hipError_t launch_finish(const FinishArgs& a, hipStream_t stream) {
 }
 
 // ----------------------------------------------------------------- products
+// Sums to gradients: times mant 2^(exp + the magnitudes)
+struct Back {
+    float mant;
+    int exp;
+    const int32_t *g_top, *cols;  // or null: 0; cols [whole 8]
+    const float* row_weights;     // or null: 0
+    IQLH_DEV int all() const { return exp + (g_top ? *g_top : 0); }
+    IQLH_DEV int row(int64_t m) const { return row_weights ? weight_bits(row_weights, m) : 0; }
+    IQLH_DEV int col(int64_t n) const { return cols ? or_zero(cols[n]) : 0; }
+    IQLH_DEV float apply(float v, int e) const { return ldexpf(v * mant, e); }
+};
 struct GradArgs {
     Side16 a, b;
     int64_t m, n, k;         // outputs, summed elements
     int64_t k_split;         // of one workgroup, a multiple of 64
     bool both;               // a's second matrix too
     int m_tiles, n_tiles, splits;
-    const float* factor;     // or null (1): of the result
+    Back back;
     float* sums;             // [splits][m][ld_sums]: partial sums
     int64_t ld_sums;
     int add;                 // to what lies in sums
@@ -543,9 +646,18 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
     tile_of(blockIdx.x - split * tiles, a.m_tiles, a.n_tiles, tm, tn);
     const int64_t m0 = (int64_t)tm * TILE, n0 = (int64_t)tn * TILE;
     const int64_t k0 = split * a.k_split, k1 = k0 + a.k_split < a.k ? k0 + a.k_split : a.k;
+    // exponents of the results' rows and columns, loaded before the product
+    int* row_e = (int*)(lds + T::RING);
+    int* col_e = row_e + TILE;
+    const int all = a.back.all(), own = threadIdx.x % TILE;
+    int re_in = 0, ce_in = 0;
+    if (PL == 2 && a.out) {
+        re_in = all + a.back.row(m0 + own < a.m ? m0 + own : a.m - 1);
+        ce_in = n0 + own < a.n ? a.back.col(n0 + own) : 0;
+    }
     mm_f16 acc[T::FA][T::FB];
     tile_product<BRAIN, TILE, AC, true, PL>(a.a, a.b, m0, n0, k0, k1, a.both, lds, acc);
-    const float f = a.out && a.factor ? *a.factor : 1.f;
+    if (PL == 2 && threadIdx.x < TILE) row_e[own] = re_in, col_e[own] = ce_in;
     float* sums = a.sums + (int64_t)split * a.m * a.ld_sums;
 #pragma unroll
     for (int band = 0; band < T::BANDS; ++band) {
@@ -564,8 +676,9 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
                 v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
             }
             if (a.out) {
+                const int re = PL == 2 ? row_e[band * T::BAND + row] : all;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= f;
+                for (int i = 0; i < 8; ++i) v[i] = a.back.apply(v[i], PL == 2 ? re + col_e[8 * u + i] : re);
                 store8_of(a.out_dtype, a.out, m * a.ld_out + n, a.n - n, v);
             } else {
                 s[0] = float4{v[0], v[1], v[2], v[3]};
@@ -578,9 +691,15 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, Tile16<TILE>::PER_SIMD) void poli
 // out = factor times the sum over the splits
 __global__ __launch_bounds__(kNT) void policy_join_kernel(GradArgs a) {
     const int64_t groups = (a.n + 7) / 8, total = a.m * groups;
-    const float f = a.factor ? *a.factor : 1.f;
+    const int all = a.back.all();
     for (int64_t e = (int64_t)blockIdx.x * kNT + threadIdx.x; e < total; e += (int64_t)gridDim.x * kNT) {
         const int64_t m = e / groups, n = 8 * (e - m * groups);
+        const int re = all + a.back.row(m);
+        int ce[8] = {};
+        if (a.back.cols) {
+            const int4 x = *(const int4*)(a.back.cols + n), y = *(const int4*)(a.back.cols + n + 4);
+            ce[0] = x.x, ce[1] = x.y, ce[2] = x.z, ce[3] = x.w, ce[4] = y.x, ce[5] = y.y, ce[6] = y.z, ce[7] = y.w;
+        }
         float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
         for (int k = 0; k < a.splits; ++k) {
@@ -590,19 +709,19 @@ __global__ __launch_bounds__(kNT) void policy_join_kernel(GradArgs a) {
             v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= f;
+        for (int i = 0; i < 8; ++i) v[i] = a.back.apply(v[i], re + or_zero(ce[i]));
         store8_of(a.out_dtype, a.out, m * a.ld_out + n, a.n - n, v);
     }
 }
 // db of a piece
-__global__ __launch_bounds__(kNT) void policy_bias_kernel(const float* part, int parts, int64_t ld, const float* factor,
-                                                          float* out, int64_t n) {
+__global__ __launch_bounds__(kNT) void policy_bias_kernel(const float* part, int parts, int64_t ld, Back back, float* out,
+                                                          int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * kNT + threadIdx.x;
     if (i >= n) return;
     double s = 0.0;
 #pragma unroll 8
     for (int k = 0; k < parts; ++k) s += part[k * ld + i];
-    out[i] = (float)s * (factor ? *factor : 1.f);
+    out[i] = back.apply((float)s, back.all());
 }
 
 // Rows up to which G has two planes whatever its type: its rounding does not average
@@ -664,9 +783,9 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
         p.bytes = at;
         return p;
     }
-    p.factors = take(sizeof(Factors));
-    p.absmax = take(3 * kAbsBlocks * 4);
-    p.row_factor = take((size_t)rows * 4);
+    p.row_exp = take(p.planes == 2 ? (size_t)rows * 4 : 0);
+    p.act_exp = take(p.planes == 2 ? (size_t)actions * 4 : 0);
+    p.cols = take(p.planes == 2 ? (size_t)p.ld * 8 : 0);
     p.h = take((size_t)rows * p.ld * 2 * p.planes);
     p.w = take((size_t)actions * p.ld * 2 * p.planes);
     const size_t begin = at;  // the loss's and the gradients' own
@@ -677,7 +796,10 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
         const Split dh = split_for(rows, dim, p.piece, p.planes);
         const int64_t full = p.pieces > 1 ? p.piece : actions, last = actions - (p.pieces - 1) * p.piece;
         const int64_t dw_full = split_for(full, dim, rows, p.planes).n * full, dw_last = split_for(last, dim, rows, p.planes).n * last;
+        p.g_top = take(4);
+        p.weight_top = take(kAbsBlocks * 4);
         p.h_dw = take(p.planes == 2 ? (size_t)rows * p.ld * 4 : 0);
+        p.w_dh = take(p.planes == 2 ? (size_t)actions * p.ld * 4 : 0);
         p.g = take((size_t)rows * p.piece * 2 * p.g_planes);
         p.db_part = take((size_t)((rows + 127) / 128) * p.piece * 4);
         p.dh_sums = take((size_t)dh.n * rows * up(dim, 8) * 4);
@@ -690,11 +812,10 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
 namespace {
 
 struct Operands {
-    Side16 h, w;      // of the logits
-    Side16 h_dw;      // H of dW
-    int64_t k;        // summed elements of the logits; columns of H and W as operands
-    const Factors* f;
-    const float* row_factor;
+    Side16 h, w;       // of the logits
+    Side16 h_dw, w_dh;  // of the gradients' products
+    int64_t k;         // summed elements of the logits; columns of H and W as operands
+    const int32_t *row_exp, *act_exp, *cols_h, *cols_w, *g_top;
 };
 
 bool in_place(const PolicyMat& q) {
@@ -702,43 +823,64 @@ bool in_place(const PolicyMat& q) {
 }
 
 // H and W as operands.  For the gradients rows of H that are off become zeros, since they would add
-// 0 times what they hold to dW, NaN or infinities as it may be.  Binary32: in the logits each row
-// of H has its own factor, so that none loses bits to a larger one; in dW the rows are summed
-// and share one.
+// 0 times what they hold to dW, NaN or infinities as it may be.
 hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands* o, hipStream_t stream) {
-    const bool f32 = a.h.dtype == IQLH_F32, sized = f32 || (grad && a.h.dtype == IQLH_F16);
+    const bool f32 = a.h.dtype == IQLH_F32, sized = grad && a.h.dtype == IQLH_F16 && a.row_weights;
     uint8_t* base = (uint8_t*)a.workspace;
+    const PolicyMat none{};
     ConvertArgs c{};
-    c.dtype = a.h.dtype, c.scale = (float)a.scale, c.f = (Factors*)(base + p.factors);
+    c.dtype = a.h.dtype;
     c.taken = a.taken, c.row_weights = a.row_weights, c.actions = a.w.rows;
+    *o = Operands{};
+    if (sized) {
+        c.part = (int32_t*)(base + p.weight_top);
+        o->g_top = c.g_top = (int32_t*)(base + p.g_top);
+        hipLaunchKernelGGL(policy_weights_kernel, dim3(kAbsBlocks), dim3(kNT), 0, stream, a.taken, a.row_weights, a.h.rows, a.w.rows,
+                           (int32_t*)(base + p.weight_top));
+    }
+    if (f32) {
+        ColumnArgs m{};
+        m.m[0] = grad && a.d_weight ? a.h : none, m.m[1] = a.w;
+        m.to[0] = (int32_t*)(base + p.cols), m.to[1] = m.to[0] + p.ld;
+        m.taken = a.taken, m.row_weights = a.row_weights, m.actions = a.w.rows, m.ld = p.ld;
+        m.lanes = a.h.cols <= 64 ? 8 : 16;
+        o->cols_h = m.to[0], o->cols_w = m.to[1];
+        o->row_exp = (int32_t*)(base + p.row_exp), o->act_exp = (int32_t*)(base + p.act_exp);
+        // one workgroup to a column for up to 512 rows: as long as the launch that empties the columns takes
+        const int64_t most = m.m[0].p && a.h.rows > a.w.rows ? a.h.rows : a.w.rows, chunks = (p.ld + 8 * m.lanes - 1) / (8 * m.lanes);
+        int64_t slabs = most <= 512 ? 1 : 512 / chunks < 32 ? 32 : 512 / chunks;
+        if (slabs > (most + 63) / 64) slabs = (most + 63) / 64;
+        if (slabs > 1)
+            hipLaunchKernelGGL(policy_empty_kernel, dim3((uint32_t)((2 * p.ld + kNT - 1) / kNT)), dim3(kNT), 0, stream, m.to[0], (int)(2 * p.ld));
+        hipLaunchKernelGGL(policy_columns_kernel, dim3((uint32_t)slabs, (uint32_t)chunks, 2), dim3(kNT), 0, stream, m);
+    }
     int n = 0;
-    auto convert = [&](const PolicyMat& q, size_t at, bool by_row, int top, bool zero_off) {
-        const int64_t blocks = by_row ? (q.rows + 3) / 4 : (q.rows * (p.ld / 8) + 4 * kNT - 1) / (4 * kNT);
-        c.c[n++] = Convert{q, (uint16_t*)(base + at), p.ld, by_row ? (float*)(base + p.row_factor) : nullptr, top, zero_off,
+    auto convert = [&](const PolicyMat& q, size_t at, bool zero_off, int32_t* row_exp, const int32_t* cols, int sign,
+                       bool weighted) {
+        int lanes = 8;  // rows are of 8 groups or more
+        while (lanes < kWave && lanes < p.ld / 8) lanes *= 2;
+        const int64_t blocks = row_exp ? (q.rows * lanes + kNT - 1) / kNT : (q.rows * (p.ld / 8) + 4 * kNT - 1) / (4 * kNT);
+        c.c[n++] = Convert{q,       (uint16_t*)(base + at), p.ld, cols, row_exp, sign, zero_off, weighted, lanes,
                            (int)(blocks < 4096 ? blocks : 4096)};
         return Side16{(const uint16_t*)(base + at), 0, p.ld, q.rows};
     };
-    // both in place or both converted, but for H of the gradients: the summed axis is as long in one as in the other
-    const bool copy = !in_place(a.w) || (!grad && !in_place(a.h));
-    o->k = copy ? p.ld : a.h.cols;
-    o->f = sized ? c.f : nullptr;
-    o->row_factor = f32 ? (const float*)(base + p.row_factor) : nullptr;
-    o->h = copy || grad ? convert(a.h, p.h, f32, 0, grad) : Side16{(const uint16_t*)a.h.p, 0, a.h.ld, a.h.rows};
-    o->h_dw = f32 && grad ? convert(a.h, p.h_dw, false, 0, true) : o->h;
-    o->w = copy ? convert(a.w, p.w, false, 1, false) : Side16{(const uint16_t*)a.w.p, 0, a.w.ld, a.w.rows};
-    if (sized) {
-        const PolicyMat none{};
-        AbsMaxArgs m{};
-        m.part = (uint32_t*)(base + p.absmax);
-        m.m[0] = f32 && grad ? a.h : none;
-        m.m[1] = f32 ? a.w : none;
-        m.m[2] = grad && a.row_weights ? PolicyMat{a.row_weights, 1, a.h.rows, a.h.rows, IQLH_F32} : none;
-        m.taken = a.taken, m.row_weights = a.row_weights, m.actions = a.w.rows;
-        hipLaunchKernelGGL(policy_absmax_kernel, dim3(kAbsBlocks, 3), dim3(kNT), 0, stream, m);
-        c.part = m.part;
+    if (f32) {
+        o->k = p.ld;
+        o->h = convert(a.h, p.h, grad, (int32_t*)o->row_exp, o->cols_w, 1, false);
+        o->w = convert(a.w, p.w, false, (int32_t*)o->act_exp, o->cols_w, -1, false);
+        if (grad && a.d_weight) o->h_dw = convert(a.h, p.h_dw, true, nullptr, o->cols_h, -1, true);
+        if (grad && a.d_hidden) o->w_dh = convert(a.w, p.w_dh, false, nullptr, o->cols_w, -1, false);
+    } else {
+        // both in place or both converted, but for H of the gradients: the summed axis is as long in one as in the other
+        const bool copy = !in_place(a.w) || (!grad && !in_place(a.h));
+        o->k = copy ? p.ld : a.h.cols;
+        o->h = copy || grad ? convert(a.h, p.h, grad, nullptr, nullptr, 0, false)
+                            : Side16{(const uint16_t*)a.h.p, 0, a.h.ld, a.h.rows};
+        o->w = copy ? convert(a.w, p.w, false, nullptr, nullptr, 0, false) : Side16{(const uint16_t*)a.w.p, 0, a.w.ld, a.w.rows};
+        o->h_dw = o->h, o->w_dh = o->w;
     }
     if (n) {
-        const uint32_t blocks = c.c[0].blocks + c.c[1].blocks + c.c[2].blocks;
+        const uint32_t blocks = c.c[0].blocks + c.c[1].blocks + c.c[2].blocks + c.c[3].blocks;
         hipLaunchKernelGGL(policy_convert_kernel, dim3(blocks), dim3(kNT), 0, stream, c);
     }
     return hipGetLastError();
@@ -822,7 +964,7 @@ hipError_t launch_policy_loss(const PolicyArgs& a, hipStream_t stream) {
     hipError_t e = prepare(a, p, false, &o, stream);
     if (e != hipSuccess) return e;
     LogitArgs l{};
-    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor;
+    l.h = o.h, l.w = o.w, l.k = o.k, l.row_exp = o.row_exp, l.act_exp = o.act_exp;
     l.bias = a.bias, l.taken = a.taken;
     l.rows = a.h.rows, l.actions = l.all_actions = a.w.rows;
     l.part = (Soft*)(base + p.part), l.z_taken = (float*)(base + p.z_taken);
@@ -842,16 +984,24 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
     const int es = a.h.dtype == IQLH_F32 ? 4 : 2;
     Operands o;
     hipError_t e = prepare(a, p, true, &o, stream);
+    // Bfloat16: G holds the scale.  Else G is times 2^(kTop - magnitude of the weights), 1 of weights that are not given,
+    // and binary32's other operands too
+    const bool f32 = a.h.dtype == IQLH_F32;
+    Back back{1.f, 0, o.g_top, nullptr, nullptr};
+    if (!brain) back.mant = (float)std::frexp(a.scale, &back.exp);
+    if (a.h.dtype == IQLH_F16) back.exp += (o.g_top ? 0 : 1) - kTop;
     LogitArgs l{};
-    l.h = o.h, l.w = o.w, l.k = o.k, l.f = o.f, l.row_factor = o.row_factor;
+    l.h = o.h, l.w = o.w, l.k = o.k, l.row_exp = o.row_exp;
+    l.g_top = o.g_top, l.g_factor = brain ? (float)a.scale : (float)(1 << (kTop - 1));
     l.taken = a.taken, l.row_weights = a.row_weights, l.lse = a.lse_in;
-    l.rows = rows, l.all_actions = actions, l.scale = (float)a.scale;
+    l.rows = rows, l.all_actions = actions;
     l.g = (uint16_t*)(base + p.g), l.g_planes = p.g_planes;
     const Split dh = split_for(rows, dim, p.piece, p.planes);
     for (int k = 0; k < p.pieces && e == hipSuccess; ++k) {
         const int64_t first = k * p.piece, n = actions - first < p.piece ? actions - first : p.piece;
         l.first = first, l.actions = n, l.ldg = up(n, 64), l.plane = rows * l.ldg;
         l.w.p = o.w.p + p.planes * first * o.w.ld, l.w.n = n;
+        l.act_exp = f32 ? o.act_exp + first : nullptr;
         l.bias = a.bias ? a.bias + first : nullptr;
         l.db_part = a.d_bias ? (float*)(base + p.db_part) : nullptr;
         e = launch_logits<true>(l, brain, p.planes, stream);
@@ -859,7 +1009,7 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
         if (a.d_bias) {
             const int tile = tile_for(rows, n, p.planes);
             hipLaunchKernelGGL(policy_bias_kernel, dim3((uint32_t)((n + kNT - 1) / kNT)), dim3(kNT), 0, stream, l.db_part,
-                               (int)((rows + tile - 1) / tile), l.ldg, o.f ? &o.f->db : nullptr, a.d_bias + first, n);
+                               (int)((rows + tile - 1) / tile), l.ldg, back, a.d_bias + first, n);
             e = hipGetLastError();
         }
         GradArgs g{};
@@ -870,7 +1020,8 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
             g.b = o.h_dw;
             g.b.n = o.k;
             g.m = n, g.k = rows;
-            g.factor = o.f ? &o.f->dw : nullptr;
+            g.back = back;
+            if (f32) g.back.exp -= 2 * kTop, g.back.cols = o.cols_h;
             g.sums = (float*)(base + p.dw_sums);
             g.out = (uint8_t*)a.d_weight + first * a.ld_dw * es;
             g.ld_out = a.ld_dw;
@@ -879,10 +1030,12 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
         }
         if (a.d_hidden && e == hipSuccess) {
             g.a = gs;
-            g.b = l.w;
+            g.b = o.w_dh;
+            g.b.p += p.planes * first * g.b.ld;
             g.b.n = o.k;
             g.m = rows, g.k = n;
-            g.factor = o.f ? &o.f->dh : nullptr;
+            g.back = back;
+            if (f32) g.back.exp -= 2 * kTop, g.back.cols = o.cols_w, g.back.exp += a.row_weights ? 0 : 1, g.back.row_weights = a.row_weights;
             g.sums = (float*)(base + p.dh_sums);
             g.add = k > 0;
             g.out = k + 1 == p.pieces ? a.d_hidden : nullptr;

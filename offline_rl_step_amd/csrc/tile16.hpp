@@ -59,7 +59,7 @@ struct Tile16 {
     static constexpr int CP = SIDE / 16 / NT;     // copies of a thread, operand and step
     static constexpr int NB = STEPS;              // steps in LDS, a power of two
     static constexpr int RING = NB * STAGE;       // also the staged sums of BAND rows
-    static constexpr int LDS = RING + 16 * TILE;  // and what an epilogue keeps of rows and columns meanwhile
+    static constexpr int LDS = RING + 28 * TILE;  // and what an epilogue keeps of rows and columns meanwhile
     static constexpr int BANDS = TILE == 256 ? 2 : 1, BAND = TILE / BANDS;
     static constexpr int PER_CU = RING > 64 << 10 ? 1 : 2, PER_SIMD = PER_CU * NT / 256;
     static_assert(BAND * TILE * 4 <= RING && PER_CU * LDS <= 160 * 1024, "LDS of a compute unit");

@@ -1,10 +1,21 @@
-"""Policy loss: rows that are off, whatever their weights are."""
+"""Policy loss: rows that are off with weights of any size, operands of many magnitudes.
+
+Binary32 operands of the tile kernels are two binary16 planes behind a power of two that takes the
+largest of what shares it to [2^13, 2^14): 22 bits, and no better than half of binary16's smallest step, 2^-25
+there, 2^-38 of that largest.  With c[d] the largest |weight| of column d:
+* logits: hidden[r][d] c[d] shares a row's, weight[v][d] / c[d] an action's, c within a factor of 2, so
+  a product is off by up to 2^-36 of the two largest;
+* d_hidden: G shares |scale w| of its row, weight[.][d] its column's;
+* d_weight: hidden[r][d] w[r] shares its column's, w within a factor of 2.
+The other terms as in test_gpu_policy.py."""
 import math
 
+import numpy as np
 import pytest
 
-from tests.gpu_util import sync
-from tests.test_gpu_policy import TYPES, _case, _run
+from oracle import policy as ref
+from tests.gpu_util import dev, sync
+from tests.test_gpu_policy import TYPES, U, _case, _host, _near, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +62,94 @@ def test_off_rows_next_to_an_infinite_weight(m, rows, dtype):
     assert bool(out["lse"][on].isfinite().all()) and math.isfinite(float(out["loss"]))
     assert bool(out["dw"].isfinite().all()) and bool(out["db"].isfinite().all())
     assert bool((out["dw"][17] == 0).all()) and float(out["db"][17]) == 0
+
+
+def _check_planes(c, out):
+    """float32 on the tiles' kernels, element by element."""
+    h, w, b, taken, rw = (_host(c[k]) for k in ("hidden", "weight", "bias", "taken", "row_weights"))
+    rows, dim = h.shape
+    actions, scale = w.shape[0], 1.0 / rows
+    kw = dict(bias=b, row_weights=rw, scale=scale)
+    loss, nll, lse = ref.loss(h, w, taken, **kw)
+    _, on = ref.on_rows(taken, actions, rw)
+    ah, aw = np.abs(h), np.abs(w)
+    col = aw.max(0)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        z = ref.logits(h, w, b)
+        ez = (dim + 8) * U * (ah @ aw.T) + 8 * U * np.where(np.isfinite(z), np.abs(z) + 1, 0)
+        ez += 8 * U * np.where(np.isfinite(b), np.abs(b), 0)[None, :]
+        ez += 2.0 ** -21 * (ah @ aw.T) + 2.0 ** -36 * dim * np.outer((ah * col).max(1), (aw / col).max(1))
+        ez = np.where(np.isfinite(b)[None, :], ez, 0)
+        ez += 8 * U * np.abs(lse)[:, None]
+    err = ez.max(axis=1) + 16 * U * (1 + np.abs(lse))
+    _near(out["lse"], lse, err, "lse")
+    _near(out["nll"], nll, 2 * err, "nll")
+    g = ref.logit_grads(h, w, taken, **kw)
+    mine = np.where(on, np.abs(scale * rw), 0)[:, None]  # |scale w|
+    p = np.abs(g)
+    p[np.arange(rows)[on], taken[on]] = mine[on, 0]
+    eg = p * (ez + err[:, None] + 4 * U) + 2.0 ** -22 * np.abs(g) + mine * (2.0 ** -38 + 2.0 ** -125)
+    eg[:, np.isneginf(b)] = 0
+    ag, hh = np.abs(g) + eg, np.where(on[:, None], ah, 0)
+    dh, dw, db = ref.grads(h, w, taken, **kw)
+    half, least = 2.0 ** -24, 2.0 ** -149
+    bound = eg @ aw + ((actions + 8) * U + 2.0 ** -21) * (ag @ aw) + 2.0 ** -38 * ag.sum(1)[:, None] * col
+    _near(out["dh"], dh, bound + half * (np.abs(dh) + bound) + least, "d_hidden")
+    rel = np.divide(ag, mine, out=np.zeros_like(ag), where=mine > 0).sum(0)
+    bound = eg.T @ hh + ((rows + 8) * U + 2.0 ** -21) * (ag.T @ hh) + 2.0 ** -37 * np.outer(rel, (hh * mine).max(0))
+    _near(out["dw"], dw, bound + half * (np.abs(dw) + bound) + least, "d_weight")
+    e = p * (ez + err[:, None] + 4 * U) + 2.0 ** -125 * mine
+    e[:, np.isneginf(b)] = 0
+    _near(out["db"], db, e.sum(0) + (rows + 8) * U * ag.sum(0) + U * np.abs(db) + least, "d_bias")
+
+
+def _spread(c, kind, seed=5):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    h, w, b, rw = (c[k] for k in ("hidden", "weight", "bias", "row_weights"))
+    rows, dim = h.shape
+    if kind == "a feature":  # large activations that the head hardly uses
+        h[:, 5] *= 2.0 ** 30
+        w[:, 5] *= 2.0 ** -30
+    elif kind == "features":
+        e = torch.exp2(torch.randint(-40, 41, (dim,), generator=g).float()).to(dev())
+        h *= e
+        w /= e
+    elif kind == "an action":  # forbidden, with weights far from the others'
+        b[7] = -math.inf
+        c["taken"][c["taken"] == 7] = 8
+        b[8] = 0.25
+        w[7] *= 2.0 ** 30
+    elif kind == "actions":
+        w *= torch.exp2(torch.randint(-30, 1, (w.shape[0], 1), generator=g).float()).to(dev())
+    elif kind == "rows":
+        h *= torch.exp2(torch.randint(-40, 1, (rows, 1), generator=g).float()).to(dev())
+    elif kind == "weights":
+        rw *= torch.exp2(torch.randint(-40, 1, (rows,), generator=g).float()).to(dev())
+    elif kind == "large":  # products near the largest binary32 values, logits of the usual size
+        h *= 2.0 ** 120
+        w *= 2.0 ** -120
+    elif kind == "small":
+        h *= 2.0 ** -100
+        w *= 2.0 ** 100
+        rw *= 2.0 ** -100
+
+
+@pytest.mark.parametrize("kind", ["a feature", "features", "an action", "actions", "rows", "weights", "large", "small"])
+@pytest.mark.parametrize("rows,dim,actions", [(30, 24, 70), (200, 72, 300), (150, 600, 130)])
+def test_float32_of_many_magnitudes(m, rows, dim, actions, kind):
+    c = _case(29, rows, dim, actions, "float32")
+    _spread(c, kind)
+    out = _run(m, c)
+    sync()
+    _check_planes(c, out)
+
+
+@pytest.mark.parametrize("kind", ["features", "weights"])
+def test_float32_of_many_magnitudes_in_pieces(m, kind):
+    """33000 rows take 1900 actions in pieces of 1792."""
+    c = _case(63, 33000, 24, 1900, "float32")
+    _spread(c, kind)
+    out = _run(m, c)
+    sync()
+    _check_planes(c, out)
