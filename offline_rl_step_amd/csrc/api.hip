@@ -1468,7 +1468,7 @@ static int make_ortho_args(const char* who, const iqlh_matrix_set* set, int32_t 
     a->rect = a->sym + set->sym_tiles;
     a->base = (uint8_t*)workspace;
     a->part = (double*)workspace;
-    a->ok = (int32_t*)(a->part + set->units);
+    a->small_by = (int32_t*)(a->part + set->units);
     a->nunits = set->units, a->nsym = set->sym_tiles, a->nrect = set->rect_tiles;
     a->small = a->rect + set->rect_tiles, a->nsmall = set->small, a->small_bytes = set->small_bytes;
     a->sym_tile = set->sym_tile, a->rect_tile = set->rect_tile;

@@ -315,7 +315,7 @@ struct OrthoArgs {
     const OrthoTile* rect;
     uint8_t* base;          // workspace
     double* part;           // [nunits]
-    int32_t* ok;            // [count]
+    int32_t* small_by;      // [count]: X's first exponent (ortho_exponent), -1 for an update that is not finite
     int32_t nunits, nsym, nrect;
     int32_t sym_tile, rect_tile;  // 64, 128 or 256
     const OrthoTile* small;       // matrices that one workgroup takes (mat)
@@ -326,6 +326,18 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);
 int64_t ortho_small_bytes(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
 bool ortho_small_ok(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
 hipError_t launch_ortho_small(const OrthoArgs& a, hipStream_t stream);
+// X is held times 2^e, e >= 0, so that a norm far below eps leaves it its bits.  e of an update of this norm, X's
+// being norm / (norm + eps), which 2^e takes to [1/2, 1)
+__host__ __device__ inline int32_t ortho_exponent(double norm, double eps) {
+    int e = 0;
+    (void)frexp(norm / (norm + eps), &e);
+    return e >= 0 ? 0 : e < -120 ? 120 : -e;  // (results below 2^-110 in any case)
+}
+// e after `step` steps: a step takes X's norm up by a = 3.4445 < 2^(29/16) at most, so 2^e |X| stays below 1 or e is 0
+__host__ __device__ inline int32_t ortho_exponent_at(int32_t e, int32_t step) {
+    const int32_t left = e - (29 * step + 15) / 16;
+    return left > 0 ? left : 0;
+}
 // s of the weights' update
 __host__ __device__ inline double ortho_shape(int rows, int cols, int scale) {
     const double r = rows, c = cols;

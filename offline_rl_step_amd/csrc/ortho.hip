@@ -13,7 +13,9 @@
 //
 // Operands are binary16 times 2^13, not bfloat16: |X| <= 1.2025 (p's maximum on [0, 1], and p maps [0,
 // 1.2025] into itself), |A| <= 1.45 and |b A + c A A| <= 2.81 bound every element, so binary16 holds
-// them with three bits more than bfloat16 and down to 2^-27 at full length.  Matrices
+// them with three bits more than bfloat16 and down to 2^-27 at full length.  Where |U| is below eps, X, A and the
+// polynomial are held times 2^e, 2^2e and 2^2e, with e from the norm and the step alone (ortho_exponent_at): 2^e |X| <= 1
+// then, and |b A + c 2^-2e A A| <= 4.8.  Matrices
 // whose result is binary32 or binary16 are held in two planes (tile16.hpp), 22 bits.
 // p's slope at 0 is a: an error in a small singular value's direction grows up to a^5 = 485 times
 // with the value itself, which is what one plane of 11 bits leaves at about 1e-3 of the result
@@ -96,10 +98,10 @@ __global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
     const double norm = sqrt(block_sum64(sum, red));
     const bool ok = norm < __longlong_as_double(0x7FF0000000000000ll);
     if (w.m == 0 && threadIdx.x == 0) {
-        a.ok[w.mat] = ok;
+        a.small_by[w.mat] = ok ? ortho_exponent(norm, a.h.eps) : -1;
         if (!ok) set_flag(a.h.flags, IQLH_FLAG_NONFINITE_GRAD);
     }
-    const double scale = ok ? (double)kUp / (norm + a.h.eps) : 0.0;
+    const double scale = ok ? ldexp((double)kUp / (norm + a.h.eps), ortho_exponent(norm, a.h.eps)) : 0.0;
     const int row0 = w.m * q.unit_rows, rows = q.rows_pad - row0 < q.unit_rows ? q.rows_pad - row0 : q.unit_rows;
     const int groups = q.cols_pad / 8;
     uint16_t* x = (uint16_t*)(a.base + q.x_at[0]);
@@ -120,11 +122,12 @@ __global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
 // kApply: the next X.  kLast: the result.
 enum { kGram, kPoly, kApply, kLast };
 template <int TILE, int PHASE, int STEPS>
-__global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD)) void ortho_product_kernel(OrthoArgs a, int from) {
+__global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD)) void ortho_product_kernel(OrthoArgs a, int step) {
     typedef Tile16<TILE, 1, STEPS> T;
     extern __shared__ __align__(16) uint8_t lds[];
     const OrthoTile w = (PHASE <= kPoly ? a.sym : a.rect)[blockIdx.x];
     const OrthoMat& q = a.mats[w.mat];
+    const int from = step & 1, small_by = a.small_by[w.mat];
     const bool two = q.planes == 2, tall = q.rows > q.cols;
     const int64_t m0 = (int64_t)w.m * TILE, n0 = (int64_t)w.n * TILE;
     const uint16_t* x = (const uint16_t*)(a.base + q.x_at[from]);
@@ -149,10 +152,13 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD
     if (two) product(std::integral_constant<int, 2>());
     else product(std::integral_constant<int, 1>());
     const int rows = PHASE <= kPoly ? q.k_pad : q.rows_pad, cols = PHASE <= kPoly ? q.k_pad : q.cols_pad;
-    bool ok = true;
+    const bool ok = small_by >= 0;
+    // X' = 2^(e' - e) (a X + 2^-2e S X) of X, S and X' as they are held
+    const int e = ortho_exponent_at(small_by, step), e_next = PHASE == kLast ? 0 : ortho_exponent_at(small_by, step + 1);
+    const float of_sum = PHASE == kGram ? kDown : ldexpf(PHASE == kPoly ? kC * kDown : kDown, (PHASE == kPoly ? -2 : -3) * e + e_next);
+    const float of_own = PHASE == kPoly ? kB : ldexpf(kA, e_next - e);
     float rate = 0.f;
     if (PHASE == kLast) {
-        ok = a.ok[w.mat];
         if (a.h.step) {
             if (!ok) return;
             rate = (float)(a.h.lr * ortho_shape(q.rows, q.cols, a.h.scale));
@@ -181,9 +187,9 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD
         const uint32_t hw[4] = {o.hi.x, o.hi.y, o.hi.z, o.hi.w}, lw[4] = {o.lo.x, o.lo.y, o.lo.z, o.lo.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float s = v[i] * (PHASE == kPoly ? kC * kDown : kDown);
+            const float s = v[i] * of_sum;
             const float e = PHASE == kGram ? 0.f : half_of(hw[i >> 1], i & 1) + half_of(lw[i >> 1], i & 1);
-            y[i] = PHASE == kGram ? s : fmaf(PHASE == kPoly ? kB : kA, e, s);
+            y[i] = PHASE == kGram ? s : fmaf(of_own, e, s);
         }
         if (PHASE == kGram) put_planes(gram, m, q.k_pad, n, two, y);
         if (PHASE == kPoly) put_planes(poly, m, q.k_pad, n, two, y);
@@ -241,13 +247,13 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD
 }
 
 template <int PHASE>
-hipError_t launch_product(const OrthoArgs& a, int from, hipStream_t stream) {
+hipError_t launch_product(const OrthoArgs& a, int step, hipStream_t stream) {
     const int n = PHASE <= kPoly ? a.nsym : a.nrect;
     auto launch = [&](auto tile, auto steps) {
         typedef Tile16<decltype(tile)::value, 1, decltype(steps)::value> T;
         auto kernel = ortho_product_kernel<decltype(tile)::value, PHASE, decltype(steps)::value>;
         (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS);
-        hipLaunchKernelGGL(kernel, dim3(n), dim3(T::NT), T::LDS, stream, a, from);
+        hipLaunchKernelGGL(kernel, dim3(n), dim3(T::NT), T::LDS, stream, a, step);
     };
     typedef std::integral_constant<int, 2> Two;
     typedef std::integral_constant<int, 4> Four;
@@ -270,10 +276,9 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(ortho_start_kernel, dim3(a.nunits), dim3(kNT), 0, stream, a);
     hipError_t e = hipGetLastError();
     for (int s = 0; s < a.h.steps && e == hipSuccess; ++s) {
-        e = launch_product<kGram>(a, s & 1, stream);
-        if (e == hipSuccess) e = launch_product<kPoly>(a, s & 1, stream);
-        if (e == hipSuccess)
-            e = s + 1 < a.h.steps ? launch_product<kApply>(a, s & 1, stream) : launch_product<kLast>(a, s & 1, stream);
+        e = launch_product<kGram>(a, s, stream);
+        if (e == hipSuccess) e = launch_product<kPoly>(a, s, stream);
+        if (e == hipSuccess) e = s + 1 < a.h.steps ? launch_product<kApply>(a, s, stream) : launch_product<kLast>(a, s, stream);
     }
     return e;
 }

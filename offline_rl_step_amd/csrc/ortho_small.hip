@@ -219,7 +219,8 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
         if (threadIdx.x == 0) set_flag(a.h.flags, IQLH_FLAG_NONFINITE_GRAD);
         if (a.h.step) return;
     }
-    const double scale = ok ? (double)kUp / (norm + a.h.eps) : 0.0;
+    const int small_by = ok ? ortho_exponent(norm, a.h.eps) : 0;
+    const double scale = ok ? ldexp((double)kUp / (norm + a.h.eps), small_by) : 0.0;
     each8([&](int row, int col, int n, const float (&u)[8], const float (&m)[8]) __attribute__((always_inline)) {
         if (a.h.step && n > 0) store8_of(IQLH_F32, (void*)q.momentum, row * q.ld_momentum + col, n, m);
         float lo[4], hi[4];
@@ -236,6 +237,9 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
     const int nts = q.k_pad / 32, ts = q.k_pad / 64 * nts, ntx = q.cols_pad / 32, tx = q.rows_pad / 64 * ntx;
     mm_f16 acc[kTiles][2];
     for (int s = 0; s < a.h.steps; ++s) {
+        // X' = 2^(e' - e) (a X + 2^-2e S X) of X, S and X' as they are held
+        const int e0 = ortho_exponent_at(small_by, s), e1 = s + 1 < a.h.steps ? ortho_exponent_at(small_by, s + 1) : 0;
+        const float of_poly = ldexpf(kC * kDown, -2 * e0), of_sum = ldexpf(kDown, e1 - 3 * e0), of_own = ldexpf(kA, e1 - e0);
         if (tall) product<PL, true, true>(X, X, ts, nts, q.rows_pad, acc);
         else product<PL, false, false>(X, X, ts, nts, q.cols_pad, acc);
         each4(ts, nts, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) {
@@ -249,7 +253,7 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
             float own[4];
             S.get4(m, n, own);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = fmaf(kB, own[e], (kC * kDown) * v[e]);
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(kB, own[e], of_poly * v[e]);
         });
         __syncthreads();  // S is read
         each4(ts, nts, acc, [&](int m, int n, float (&v)[4]) __attribute__((always_inline)) { S.put4(m, n, v); });
@@ -260,7 +264,7 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
             float own[4];
             X.get4(m, n, own);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = fmaf(kA, own[e], kDown * v[e]);
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(of_own, own[e], of_sum * v[e]);
         });
         if (s + 1 == a.h.steps) break;
         __syncthreads();  // X is read
