@@ -765,7 +765,8 @@ int iqlh_orthogonalize(const iqlh_matrix_set* set, int32_t steps, double eps, in
  *   out <- (1 - lr weight_decay) out - lr s X,
  * with s = sqrt(max(1, rows / cols)) (IQLH_MUON_SCALE_SHAPE) or 0.2 sqrt(max(rows,
  * cols)) (IQLH_MUON_SCALE_RMS, which gives the update Adam's usual size).  The
- * momentum is kept in f32; the new weight is rounded once.  A matrix whose U is not
+ * momentum is kept in f32, with mu as f32; the new weight is two binary32 multiply-adds
+ * on the old one, lr s and lr weight_decay as f32, then rounded to out_dtype.  A matrix whose U is not
  * finite keeps its weights and its momentum (IQLH_FLAG_NONFINITE_GRAD).
  *   lr finite, 0 <= mu < 1, weight_decay finite; every matrix has a momentum. */
 typedef enum { IQLH_MUON_SCALE_SHAPE = 0, IQLH_MUON_SCALE_RMS = 1 } iqlh_muon_scale;

@@ -1498,7 +1498,7 @@ int iqlh_muon_step(const iqlh_matrix_set* set, double lr, double mu, int32_t nes
     if (scale != IQLH_MUON_SCALE_SHAPE && scale != IQLH_MUON_SCALE_RMS)
         return fail(IQLH_EINVAL, "iqlh_muon_step: unknown scale %d", scale);
     a.h.step = 1, a.h.nesterov = nesterov, a.h.scale = scale;
-    a.h.lr = lr, a.h.mu = (float)mu, a.h.keep = (float)(1.0 - lr * weight_decay);
+    a.h.lr = lr, a.h.mu = (float)mu, a.h.decay = (float)(lr * weight_decay);
     hipError_t e = launch_orthogonalize(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "iqlh_muon_step launch");
     return IQLH_OK;

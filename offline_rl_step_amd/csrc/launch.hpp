@@ -304,7 +304,7 @@ struct OrthoTile {
 };
 struct OrthoHyper {
     double lr, eps;
-    float mu, keep;  // keep: 1 - lr weight_decay
+    float mu, decay;  // decay: lr weight_decay (1 - decay in binary32 would be off by up to 2^-25, 3 % of a decay of 1e-6)
     int32_t* flags;
     int32_t steps, step, nesterov, scale;  // step: with momentum and weights
 };
@@ -337,6 +337,11 @@ __host__ __device__ inline int32_t ortho_exponent(double norm, double eps) {
 __host__ __device__ inline int32_t ortho_exponent_at(int32_t e, int32_t step) {
     const int32_t left = e - (29 * step + 15) / 16;
     return left > 0 ? left : 0;
+}
+// (1 - decay) w - rate x in two multiply-adds; an infinite w stays one
+__device__ inline float ortho_weight(float w, float x, float rate, float decay) {
+    const float y = fmaf(-decay, w, fmaf(-rate, x, w));
+    return fabsf(w) == __builtin_huge_valf() ? (1.f - decay) * w : y;
 }
 // s of the weights' update
 __host__ __device__ inline double ortho_shape(int rows, int cols, int scale) {

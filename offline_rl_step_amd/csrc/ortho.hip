@@ -198,7 +198,7 @@ __global__ __launch_bounds__(Tile16<TILE>::NT, (Tile16<TILE, 1, STEPS>::PER_SIMD
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 y[i] = ok ? y[i] * kDown : __uint_as_float(0x7FC00000u);
-                if (a.h.step) y[i] = fmaf(-rate, y[i], a.h.keep * o.old[i]);
+                if (a.h.step) y[i] = ortho_weight(o.old[i], y[i], rate, a.h.decay);
             }
             store8_of(q.out_dtype, (void*)q.out, (int64_t)m * q.ld_out + n, q.cols - n, y);
         }

@@ -285,7 +285,7 @@ IQLH_DEV void small_step(const OrthoArgs& a, const OrthoMat& q, uint8_t* lds) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             y[e] = ok ? v[e] * kDown : __uint_as_float(0x7FC00000u);
-            if (a.h.step) y[e] = fmaf(-rate, y[e], a.h.keep * old[e]);
+            if (a.h.step) y[e] = ortho_weight(old[e], y[e], rate, a.h.decay);
         }
         if (four) store4_of(q.out_dtype, (void*)q.out, at, y);
         else

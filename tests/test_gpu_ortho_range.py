@@ -32,3 +32,39 @@ def test_norms_below_eps(m, shape, norm, steps):
         n = np.linalg.norm(want)
         off = np.linalg.norm(_host(o) - want)
         assert off <= 2 * _moved(_host(u), planes, want, steps=steps) + HALF[out] * n, (out, off / n)
+
+
+@pytest.mark.parametrize("shape", [(100, 100), (400, 300)])
+def test_decay_alone_is_rounded_once(m, shape):
+    """Without a gradient the weights shrink by lr weight_decay, here 1e-6: as a binary32 factor 1 - 1e-6 is off by
+    a hundredth of that decay, step after step."""
+    import torch
+    g = torch.Generator().manual_seed(3)
+    w = torch.randn(shape, generator=g).to(dev())
+    x, mom = torch.zeros(shape, device=dev()), torch.zeros(shape, device=dev())
+    s = m.MatrixSet([x], [w], [mom])
+    ws = m.orthogonalize_workspace(s)
+    was = _host(w)
+    m.muon_step(s, ws, 1e-4, weight_decay=1e-2)
+    sync()
+    want = was * (1.0 - 1e-6)
+    # half a step, and that of lr weight_decay itself and of its product
+    assert np.all(np.abs(_host(w) - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -23 * 1e-6 * np.abs(was))
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+@pytest.mark.parametrize("shape", [(40, 60), (200, 180)])
+def test_infinite_weights_stay_infinite(m, shape, decay):
+    import torch
+    g = torch.Generator().manual_seed(4)
+    clean = torch.randn(shape, generator=g).to(dev())
+    got = clean.clone()
+    got[3, 5], got[7, 9] = np.inf, -np.inf
+    for w in (clean, got):
+        x, mom = _update(2, shape, "float32"), torch.zeros(shape, device=dev())
+        s = m.MatrixSet([x], [w], [mom])
+        m.muon_step(s, m.orthogonalize_workspace(s), 0.1, weight_decay=decay)
+    sync()
+    assert got[3, 5].item() == np.inf and got[7, 9].item() == -np.inf
+    got[3, 5], got[7, 9] = clean[3, 5], clean[7, 9]
+    assert torch.equal(got, clean)
