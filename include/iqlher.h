@@ -636,7 +636,7 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  *            -1 and set IQLH_FLAG_BAD_INDEX.
  *   row_weights  device [rows] f32 or NULL (1).  A row of weight 0 adds nothing,
  *            whatever its nll is.
- *   scale    of the loss, finite (1 / rows for the mean).
+ *   scale    of the loss, finite in binary32 (1 / rows for the mean).
  * 1 <= rows, actions <= 2^24, 1 <= dim <= 2^14, each product of two of them at most
  * 2^38.
  *

@@ -1151,7 +1151,7 @@ static int make_policy_args(const char* who, const iqlh_policy_head* q, const in
     if (!rc) rc = check_float_matrix(who, q->hidden, q->dtype, q->ld_hidden, q->dim);
     if (!rc) rc = check_float_matrix(who, q->weight, q->dtype, q->ld_weight, q->dim);
     if (rc) return rc;
-    if (!std::isfinite(scale)) return fail(IQLH_EINVAL, "%s: scale must be finite", who);
+    if (!std::isfinite((float)scale)) return fail(IQLH_EINVAL, "%s: scale must be finite in binary32", who);
     if (!workspace || ((uintptr_t)workspace & 15u)) return fail(IQLH_EINVAL, "%s: workspace NULL or not 16-byte aligned", who);
     const size_t need = policy_plan(q->rows, q->actions, q->dim, q->dtype, grad).bytes;
     if (workspace_bytes < need) return fail(IQLH_EINVAL, "%s: workspace too small: %zu < %zu", who, workspace_bytes, need);
