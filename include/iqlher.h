@@ -768,7 +768,8 @@ int iqlh_orthogonalize(const iqlh_matrix_set* set, int32_t steps, double eps, in
  * momentum is kept in f32, with mu as f32; the new weight is two binary32 multiply-adds
  * on the old one, lr s and lr weight_decay as f32, then rounded to out_dtype.  A matrix whose U is not
  * finite keeps its weights and its momentum (IQLH_FLAG_NONFINITE_GRAD).
- *   lr finite, 0 <= mu < 1, weight_decay finite; every matrix has a momentum. */
+ *   256 lr, weight_decay and lr weight_decay finite in binary32, 0 <= mu < 1; every
+ * matrix has a momentum. */
 typedef enum { IQLH_MUON_SCALE_SHAPE = 0, IQLH_MUON_SCALE_RMS = 1 } iqlh_muon_scale;
 int iqlh_muon_step(const iqlh_matrix_set* set, double lr, double mu, int32_t nesterov, double weight_decay,
                    int32_t scale, int32_t steps, double eps, int32_t* d_flags, void* workspace,

@@ -1492,7 +1492,9 @@ int iqlh_muon_step(const iqlh_matrix_set* set, double lr, double mu, int32_t nes
     int rc = make_ortho_args("iqlh_muon_step", set, steps, eps, d_flags, workspace, workspace_bytes, &a);
     if (rc) return rc;
     if (!set->momentum) return fail(IQLH_EINVAL, "iqlh_muon_step: the matrices have no momentum");
-    if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return fail(IQLH_EINVAL, "iqlh_muon_step: lr and weight_decay must be finite");
+    // (256: the largest s)
+    if (!std::isfinite((float)(256.0 * lr)) || !std::isfinite((float)weight_decay) || !std::isfinite((float)(lr * weight_decay)))
+        return fail(IQLH_EINVAL, "iqlh_muon_step: 256 lr, weight_decay and lr weight_decay must be finite in binary32");
     if (!(mu >= 0.0 && mu < 1.0)) return fail(IQLH_EINVAL, "iqlh_muon_step: mu must be in [0, 1)");
     if (nesterov != 0 && nesterov != 1) return fail(IQLH_EINVAL, "iqlh_muon_step: nesterov must be 0 or 1");
     if (scale != IQLH_MUON_SCALE_SHAPE && scale != IQLH_MUON_SCALE_RMS)
