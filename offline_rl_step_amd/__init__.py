@@ -721,7 +721,7 @@ def _policy_head(hidden, weight, taken, bias, row_weights, scale):
         _need_f32(row_weights, rows, device, "row_weights")
     head = PolicyHeadStruct(hidden.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), rows, actions,
                             dim, ldh, ldw, dt)
-    return head, (1.0 / rows if scale is None else scale), device, index
+    return head, (1.0 / max(rows, 1) if scale is None else scale), device, index  # the library refuses 0 rows
 
 
 def policy_loss(hidden, weight, taken, out_nll, out_lse, workspace, bias=None, row_weights=None, scale=None,

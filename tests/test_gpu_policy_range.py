@@ -153,3 +153,15 @@ def test_float32_of_many_magnitudes_in_pieces(m, kind):
     out = _run(m, c)
     sync()
     _check_planes(c, out)
+
+
+def test_no_rows_and_no_actions_are_refused_as_sizes(m):
+    import torch
+    z = lambda *s: torch.zeros(s, device=dev())  # noqa: E731
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device=dev())
+    for rows, actions in ((0, 4), (4, 0)):
+        taken = torch.zeros(rows, dtype=torch.int32, device=dev())
+        with pytest.raises(m.IqlhError):
+            m.policy_loss(z(rows, 8), z(actions, 8), taken, z(rows), z(rows), ws)
+        with pytest.raises(m.IqlhError):
+            m.policy_loss_grad(z(rows, 8), z(actions, 8), taken, z(rows), ws, d_hidden=z(rows, 8))
