@@ -795,14 +795,16 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
         at = begin;
         const Split dh = split_for(rows, dim, p.piece, p.planes);
         const int64_t full = p.pieces > 1 ? p.piece : actions, last = actions - (p.pieces - 1) * p.piece;
-        const int64_t dw_full = split_for(full, dim, rows, p.planes).n * full, dw_last = split_for(last, dim, rows, p.planes).n * last;
+        // parts of dW, none where one workgroup has the whole sum
+        auto dw_parts = [&](int64_t n) { const int64_t k = split_for(n, dim, rows, p.planes).n; return k > 1 ? k * n : 0; };
+        const int64_t dw_full = dw_parts(full), dw_last = dw_parts(last);
         p.g_top = take(4);
         p.weight_top = take(kAbsBlocks * 4);
         p.h_dw = take(p.planes == 2 ? (size_t)rows * p.ld * 4 : 0);
         p.w_dh = take(p.planes == 2 ? (size_t)actions * p.ld * 4 : 0);
         p.g = take((size_t)rows * p.piece * 2 * p.g_planes);
         p.db_part = take((size_t)((rows + 127) / 128) * p.piece * 4);
-        p.dh_sums = take((size_t)dh.n * rows * up(dim, 8) * 4);
+        p.dh_sums = take(p.pieces > 1 || dh.n > 1 ? (size_t)dh.n * rows * up(dim, 8) * 4 : 0);
         p.dw_sums = take((size_t)(dw_full > dw_last ? dw_full : dw_last) * up(dim, 8) * 4);
         if (at > p.bytes) p.bytes = at;
     }

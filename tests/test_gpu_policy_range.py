@@ -165,3 +165,17 @@ def test_no_rows_and_no_actions_are_refused_as_sizes(m):
             m.policy_loss(z(rows, 8), z(actions, 8), taken, z(rows), z(rows), ws)
         with pytest.raises(m.IqlhError):
             m.policy_loss_grad(z(rows, 8), z(actions, 8), taken, z(rows), ws, d_hidden=z(rows, 8))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,dim,actions", [(1, 8, 2), (7, 33, 400), (65, 40, 300), (200, 72, 3000), (1300, 520, 8200),
+                                              (16384, 24, 9001)])
+def test_nothing_is_written_behind_the_workspace(m, rows, dim, actions, dtype):
+    import torch
+    c = _case(33, rows, dim, actions, dtype)
+    for grad in (False, True):
+        n = m.policy_loss_workspace(rows, actions, dim, c["hidden"].dtype, grad=grad).numel()
+        buf = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=dev())
+        _run(m, c, grad=grad, ws=buf[:n])
+        sync()
+        assert bool((buf[n:] == 0x5A).all()), grad

@@ -32,3 +32,17 @@ def test_rates_above_binary32(m):
     for lr, wd in ((1e300, 0.0), (-2e36, 0.0), (1.0, 1e39), (1e20, 1e20)):
         assert step(lr, wd) == m.EINVAL and "lr" in m.last_error(), (lr, wd, m.last_error())
     assert step(1e36, 1.0, mu=1.0) == m.EINVAL and "mu" in m.last_error()
+
+
+def test_workspace_has_no_partial_sums_where_products_are_whole(m):
+    """8192 rows, 65536 actions, dim 2048 in bfloat16: the copies of hidden and weight, a piece of G of 256 MB, d_hidden
+    over the pieces, a part of the bias's gradient, and a few numbers a row; not d_weight's sums in binary32."""
+    rows, actions, dim = 8192, 65536, 2048
+    rc, n = policy._bytes(m, rows, actions, dim, m.BF16, 1)
+    piece = 1 << 14
+    assert rc == m.OK
+    assert n <= 2 * dim * (rows + actions) + 2 * rows * piece + 4 * rows * dim + 4 * piece * rows // 128 + 64 * rows
+    # one piece, d_hidden in one part too
+    rows, actions, dim = 1024, 8192, 8192
+    rc, n = policy._bytes(m, rows, actions, dim, m.BF16, 1)
+    assert rc == m.OK and n <= 2 * dim * (rows + actions) + 2 * rows * actions + 4 * actions * rows // 128 + 64 * rows
