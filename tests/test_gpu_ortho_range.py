@@ -68,3 +68,27 @@ def test_infinite_weights_stay_infinite(m, shape, decay):
     assert got[3, 5].item() == np.inf and got[7, 9].item() == -np.inf
     got[3, 5], got[7, 9] = clean[3, 5], clean[7, 9]
     assert torch.equal(got, clean)
+
+
+def test_more_than_2_to_31_elements(m):
+    """65536 x 32784 of one sign pattern, u v^T: one step gives p(1) of it, every element of one size.  Sums of up to
+    65536 equal terms, 16 to an addition, are off by up to 4096 half steps of binary32, operands by one of binary16."""
+    import torch
+    r, c = 65536, 32784
+    g = torch.Generator(device=dev()).manual_seed(5)
+    sign = lambda n: torch.where(torch.rand(n, generator=g, device=dev()) < 0.5, -1.0, 1.0)  # noqa: E731
+    u, v = sign(r), sign(c)
+    x = torch.empty(r, c, dtype=torch.bfloat16, device=dev())
+    torch.mul(u[:, None].bfloat16(), v[None, :].bfloat16(), out=x)
+    out = torch.full((r, c), 3.0, dtype=torch.bfloat16, device=dev())
+    s = m.MatrixSet([x], [out])
+    ws = m.orthogonalize_workspace(s)
+    m.orthogonalize(s, ws, steps=1)
+    sync()
+    want = (ref.A + ref.B + ref.C) / np.sqrt(r * c)
+    # each of the three products and of the four operands moves p(1) = A + B + C by up to its coefficients' sum
+    tol = (abs(ref.A) + abs(ref.B) + abs(ref.C)) / (ref.A + ref.B + ref.C) * (4 * 2.0 ** -11 + 3 * 2.0 ** -12) + HALF["bfloat16"]
+    for a in range(0, r, 4096):
+        got = out[a:a + 4096].float() * u[a:a + 4096, None] * v
+        lo, hi = float(got.min()), float(got.max())
+        assert want * (1 - tol) <= lo and hi <= want * (1 + tol), (a, lo, hi, want)

@@ -179,3 +179,73 @@ def test_nothing_is_written_behind_the_workspace(m, rows, dim, actions, dtype):
         _run(m, c, grad=grad, ws=buf[:n])
         sync()
         assert bool((buf[n:] == 0x5A).all()), grad
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [3, 300])
+def test_stream_argument(m, rows, dtype):
+    """stream=: the results of the call on a side stream, whose buffers are there before it, are those of the current
+    one's, also while that one is busy."""
+    import torch
+    c = _case(71, rows, 72, 1500, dtype)
+    first = _run(m, c)
+    side = torch.cuda.Stream()
+    sync()
+    busy = torch.empty(1 << 26, device=dev())
+    kw = dict(bias=c["bias"], row_weights=c["row_weights"])
+    for rep in range(3):
+        ws = m.policy_loss_workspace(rows, 1500, 72, c["hidden"].dtype, grad=True)
+        ws.fill_(0xFF)
+        out = {k: torch.full_like(t, -7.0) for k, t in first.items()}
+        side.wait_stream(torch.cuda.current_stream())
+        busy.fill_(rep)
+        m.policy_loss(c["hidden"], c["weight"], c["taken"], out["nll"], out["lse"], ws, out_loss=out["loss"], stream=side, **kw)
+        m.policy_loss_grad(c["hidden"], c["weight"], c["taken"], out["lse"], ws, d_hidden=out["dh"], d_weight=out["dw"],
+                           d_bias=out["db"], stream=side, **kw)
+        sync()
+        for k in first:
+            assert torch.equal(out[k], first[k]), (rep, k)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+@pytest.mark.parametrize("rows", [3, 20])
+def test_more_than_2_to_31_weights(m, rows, dtype):
+    """262221 actions of dim 8200: offsets beyond 32 bits in weight, its planes and its gradient.  Only the last
+    actions and one in the middle have a bias above the others', so that all of the batch's probability is there."""
+    import torch
+    dim, actions = 8200, 262221
+    t = getattr(torch, dtype)
+    g = torch.Generator(device=dev()).manual_seed(3)
+    weight = torch.empty(actions, dim, dtype=t, device=dev())
+    for a in range(0, actions, 16384):
+        weight[a:a + 16384] = torch.randn(weight[a:a + 16384].shape, generator=g, device=dev()) / 64
+    hidden = torch.relu(torch.randn(rows, dim, generator=g, device=dev())).to(t)
+    far = torch.tensor([131072, *range(actions - 40, actions)], device=dev())
+    bias = torch.full((actions,), -60.0, device=dev())
+    bias[far] = torch.randn(41, generator=g, device=dev())
+    taken = far[torch.randint(0, 41, (rows,), generator=g, device=dev())].int()
+    new = lambda *s: torch.full(s, -7.0, device=dev())  # noqa: E731
+    nll, lse, loss, db = new(rows), new(rows), new(1), new(actions)
+    ws = m.policy_loss_workspace(rows, actions, dim, t, grad=True)
+    dh, dw = torch.full_like(hidden, -7.0), torch.full_like(weight, -7.0)
+    m.policy_loss(hidden, weight, taken, nll, lse, ws, bias=bias, out_loss=loss)
+    m.policy_loss_grad(hidden, weight, taken, lse, ws, bias=bias, d_hidden=dh, d_weight=dw, d_bias=db)
+    sync()
+    h, w = hidden.double(), weight[far].double()
+    z = h @ w.t() + bias[far].double()
+    want = torch.logsumexp(z, 1)  # the others add below e^-50
+    at = (far[None, :] == taken[:, None]).double()
+    # dim + 8 binary32 roundings of the terms, of sign at random: 2^-18 of |z| and of the largest term sizes
+    tol = 2.0 ** -18 * (1 + float(z.abs().max()))
+    assert float((lse.double() - want).abs().max()) <= tol
+    assert float((nll.double() - (want - (z * at).sum(1))).abs().max()) <= 2 * tol
+    gr = (torch.exp(z - want[:, None]) - at) / rows
+    rel = {"float16": 2.0 ** -9, "float32": 2.0 ** -16}[dtype]
+    for got, ref64 in ((dh, gr @ w), (dw[far], gr.t() @ h), (db[far], gr.sum(0))):
+        assert float((got.double() - ref64).norm()) <= (rel + tol) * float(ref64.norm())
+    others = torch.ones(actions, dtype=torch.bool, device=dev())
+    others[far] = False
+    assert float(db[others].abs().max()) < 1e-20
+    for a in range(0, actions, 16384):
+        rows_there = others[a:a + 16384]
+        assert float(dw[a:a + 16384][rows_there].abs().max()) < 1e-7
