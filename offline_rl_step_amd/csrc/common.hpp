@@ -88,6 +88,20 @@ IQLH_DEV float block_sum(float v, float* red) {
     return s;
 }
 
+// The same in binary64
+template <int NT>
+IQLH_DEV double block_sum64(double v, double* red) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+    __syncthreads();
+    if ((threadIdx.x & (kWave - 1)) == 0) red[threadIdx.x / kWave] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < NT / kWave; ++i) s += red[i];
+    return s;
+}
+
 // Workgroup barrier for data exchanged through LDS only: waits for this
 // wave's LDS operations (lgkmcnt 0), not for its global stores, which
 // __syncthreads' release fence would drain first (about a microsecond after

@@ -326,28 +326,6 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);
 int64_t ortho_small_bytes(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
 bool ortho_small_ok(int32_t rows_pad, int32_t cols_pad, int32_t k_pad, int32_t planes);
 hipError_t launch_ortho_small(const OrthoArgs& a, hipStream_t stream);
-// X is held times 2^e, e >= 0, so that a norm far below eps leaves it its bits.  e of an update of this norm, X's
-// being norm / (norm + eps), which 2^e takes to [1/2, 1)
-__host__ __device__ inline int32_t ortho_exponent(double norm, double eps) {
-    int e = 0;
-    (void)frexp(norm / (norm + eps), &e);
-    return e >= 0 ? 0 : e < -120 ? 120 : -e;  // (results below 2^-110 in any case)
-}
-// e after `step` steps: a step takes X's norm up by a = 3.4445 < 2^(29/16) at most, so 2^e |X| stays below 1 or e is 0
-__host__ __device__ inline int32_t ortho_exponent_at(int32_t e, int32_t step) {
-    const int32_t left = e - (29 * step + 15) / 16;
-    return left > 0 ? left : 0;
-}
-// (1 - decay) w - rate x in two multiply-adds; an infinite w stays one
-__device__ inline float ortho_weight(float w, float x, float rate, float decay) {
-    const float y = fmaf(-decay, w, fmaf(-rate, x, w));
-    return fabsf(w) == __builtin_huge_valf() ? (1.f - decay) * w : y;
-}
-// s of the weights' update
-__host__ __device__ inline double ortho_shape(int rows, int cols, int scale) {
-    const double r = rows, c = cols;
-    return scale == 0 ? sqrt(r > c ? r / c : 1.0) : 0.2 * sqrt(r > c ? r : c);  // IQLH_MUON_SCALE_SHAPE, _RMS
-}
 
 // -------------------------------------------- policy loss over many actions
 struct PolicyMat {

@@ -27,31 +27,14 @@
 // product of 512 x 512 x 256.  Norm and start move 12 and 6 (planes: 8) bytes an element at the copy's rate.
 #include "iqlher.h"
 #include "launch.hpp"
+#include "ortho_block.hpp"
 #include "tile16.hpp"
 
 namespace iqlh {
 
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kUp = 8192.f, kDown = 1.f / 8192.f;  // of every operand
 constexpr int kNT = 256;
-
-IQLH_DEV double wave_sum64(double v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
-}
-IQLH_DEV double block_sum64(double v, double* red) {
-    v = wave_sum64(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kNT / kWave; ++i) s += red[i];
-    return s;
-}
 
 // Eight neighbouring elements of the update, and the momentum behind it
 IQLH_DEV void update8(const OrthoMat& q, const OrthoHyper& h, int64_t row, int col, float (&u)[8], float (&m)[8]) {
@@ -84,7 +67,7 @@ __global__ __launch_bounds__(kNT) void ortho_norm_kernel(OrthoArgs a) {
             s1 = fma((double)u[i + 1], (double)u[i + 1], s1);
         }
     }
-    s0 = block_sum64(s0 + s1, red);
+    s0 = block_sum64<kNT>(s0 + s1, red);
     if (threadIdx.x == 0) a.part[blockIdx.x] = s0;
 }
 
@@ -95,7 +78,7 @@ __global__ __launch_bounds__(kNT) void ortho_start_kernel(OrthoArgs a) {
     const OrthoMat& q = a.mats[w.mat];
     double sum = 0.0;
     for (int i = threadIdx.x; i < q.units; i += kNT) sum += a.part[q.unit0 + i];
-    const double norm = sqrt(block_sum64(sum, red));
+    const double norm = sqrt(block_sum64<kNT>(sum, red));
     const bool ok = norm < __longlong_as_double(0x7FF0000000000000ll);
     if (w.m == 0 && threadIdx.x == 0) {
         a.small_by[w.mat] = ok ? ortho_exponent(norm, a.h.eps) : -1;

@@ -10,14 +10,13 @@
 // Four matrices of 128 x 128 among a step's list: 70 us, with a launch a product 97.
 #include "iqlher.h"
 #include "launch.hpp"
+#include "ortho_block.hpp"
 #include "tile16.hpp"
 
 namespace iqlh {
 
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kUp = 8192.f, kDown = 1.f / 8192.f;  // of every operand
 constexpr int kNT = 512, kWaves = kNT / 64;
 constexpr int kTiles = 3;                 // most outputs of 64 x 32 a wave
 constexpr int kMostElements = kTiles * kWaves * 2048;

@@ -587,7 +587,7 @@ __global__ __launch_bounds__(kNT) void policy_finish_kernel(FinishArgs a) {
         a.lse[m] = l2 * kLn2;
         a.nll[m] = nll;
     }
-    term = block_sum64(term, red);
+    term = block_sum64<kNT>(term, red);
     if (threadIdx.x == 0) {
         if (gridDim.x == 1) put_loss(a, term);
         else a.loss_part[blockIdx.x] = term;
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(kNT) void policy_loss_sum_kernel(FinishArgs a, int 
     __shared__ double red[kNT / kWave];
     double s = 0.0;
     for (int i = threadIdx.x; i < n; i += kNT) s += a.loss_part[i];
-    s = block_sum64(s, red);
+    s = block_sum64<kNT>(s, red);
     if (threadIdx.x == 0) put_loss(a, s);
 }
 int finish_rows(int64_t rows) { return rows >= 1024 ? 64 : rows >= 64 ? 16 : 1; }

@@ -53,16 +53,5 @@ IQLH_DEV void put_loss(const FinishArgs& a, double sum) {
     if (a.loss) *a.loss = loss;
     if (!(fabsf(loss) < __uint_as_float(0x7F800000u))) set_flag(a.flags, IQLH_FLAG_NONFINITE_LOSS);
 }
-IQLH_DEV double block_sum64(double v, double* red) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kNT / kWave; ++i) s += red[i];
-    return s;
-}
 }  // namespace policy
 }  // namespace iqlh

@@ -112,7 +112,7 @@ __global__ __launch_bounds__(kNT) void policy_few_actions_kernel(FewArgs a) {
         }
     }
     if constexpr (!GRAD) {
-        term = block_sum64(term, red);
+        term = block_sum64<kNT>(term, red);
         if (threadIdx.x == 0) {
             if (gridDim.x == 1) put_loss(a.f, term);
             else a.f.loss_part[blockIdx.x] = term;
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kNT) void policy_few_join_kernel(FewArgs a) {
     if (blockIdx.y == 0 && a.d_bias) {
         double b = 0.0;
         for (int k = threadIdx.x; k < a.blocks; k += kNT) b += a.part[(int64_t)a.blocks * VM * ld + k * VM + v];
-        b = block_sum64(b, red);
+        b = block_sum64<kNT>(b, red);
         if (threadIdx.x == 0) a.d_bias[v] = (float)b;
     }
 }
