@@ -249,3 +249,41 @@ def test_more_than_2_to_31_weights(m, rows, dtype):
     for a in range(0, actions, 16384):
         rows_there = others[a:a + 16384]
         assert float(dw[a:a + 16384][rows_there].abs().max()) < 1e-7
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,actions", [(1 << 24, 3), (1 << 24, 17), (1, 1 << 24), (5, 1 << 24), (70, 3000000)])
+def test_the_most_rows_and_actions(m, rows, actions, dtype):
+    """Up to 2^24 of each, against binary64 on the device, norm-wise: the types' rounding of G and the result, and
+    2^-16 for binary32 sums of 2^24 terms in parts of thousands."""
+    import torch
+    dim = 8
+    c = _case(35, rows, dim, actions, dtype, off=0.1 if rows > 5 else 0)
+    out = _run(m, c)
+    sync()
+    h, w, b, taken = c["hidden"].double(), c["weight"].double(), c["bias"].double(), c["taken"]
+    on = taken >= 0
+    wn = torch.where(on, c["row_weights"].double(), 0.0) / rows
+    nll, lse = torch.zeros(rows, dtype=torch.float64, device=dev()), torch.zeros(rows, dtype=torch.float64, device=dev())
+    dh, dw, db = torch.zeros_like(h), torch.zeros_like(w), torch.zeros_like(b)
+    step = max(1, (1 << 27) // actions)
+    for r in range(0, rows, step):
+        s = slice(r, min(r + step, rows))
+        z = torch.addmm(b, h[s], w.t())
+        lse[s] = torch.logsumexp(z, 1)
+        at = taken[s].clamp(min=0).long()[:, None]
+        nll[s] = torch.where(on[s], lse[s] - z.gather(1, at)[:, 0], 0.0)
+        g = z.sub_(lse[s][:, None]).exp_()
+        g.scatter_add_(1, at, torch.full_like(at, -1, dtype=torch.float64))
+        g *= wn[s][:, None]
+        dh[s] = g @ w
+        dw += g.t() @ h[s]
+        db += g.sum(0)
+    off = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+    assert off(out["lse"], lse) <= 2.0 ** -20 and off(out["nll"], nll) <= 2.0 ** -20
+    assert off(out["loss"], (wn * nll).sum().view(1)) <= 2.0 ** -20
+    tol = {"bfloat16": 2 * 2.0 ** -8, "float16": 2 * 2.0 ** -11, "float32": 0.0}[dtype] + 2.0 ** -16
+    least = {"bfloat16": 0.0, "float16": 2.0 ** -25, "float32": 0.0}[dtype]  # half of the smallest step, each element's
+    for key, want in (("dh", dh), ("dw", dw)):
+        assert float((out[key].double() - want).norm()) <= tol * float(want.norm()) + least * math.sqrt(want.numel()), key
+    assert off(out["db"], db) <= 2.0 ** -16
