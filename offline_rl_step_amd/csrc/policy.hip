@@ -986,15 +986,16 @@ hipError_t launch_policy_loss_grad(const PolicyArgs& a, hipStream_t stream) {
     const int es = a.h.dtype == IQLH_F32 ? 4 : 2;
     Operands o;
     hipError_t e = prepare(a, p, true, &o, stream);
-    // Bfloat16: G holds the scale.  Else G is times 2^(kTop - magnitude of the weights), 1 of weights that are not given,
-    // and binary32's other operands too
+    // The scale is mant 2^exp.  Bfloat16: G holds mant.  Else G is times 2^(kTop - magnitude of the weights), 1 of weights
+    // that are not given, and binary32's other operands too
     const bool f32 = a.h.dtype == IQLH_F32;
     Back back{1.f, 0, o.g_top, nullptr, nullptr};
-    if (!brain) back.mant = (float)std::frexp(a.scale, &back.exp);
+    const float mant = (float)std::frexp(a.scale, &back.exp);
+    if (!brain) back.mant = mant;
     if (a.h.dtype == IQLH_F16) back.exp += (o.g_top ? 0 : 1) - kTop;
     LogitArgs l{};
     l.h = o.h, l.w = o.w, l.k = o.k, l.row_exp = o.row_exp;
-    l.g_top = o.g_top, l.g_factor = brain ? (float)a.scale : (float)(1 << (kTop - 1));
+    l.g_top = o.g_top, l.g_factor = brain ? mant : (float)(1 << (kTop - 1));
     l.taken = a.taken, l.row_weights = a.row_weights, l.lse = a.lse_in;
     l.rows = rows, l.all_actions = actions;
     l.g = (uint16_t*)(base + p.g), l.g_planes = p.g_planes;

@@ -15,7 +15,7 @@ import pytest
 
 from oracle import policy as ref
 from tests.gpu_util import dev, sync
-from tests.test_gpu_policy import TYPES, U, _case, _host, _near, _run
+from tests.test_gpu_policy import TYPES, U, _case, _check, _host, _near, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -287,3 +287,14 @@ def test_the_most_rows_and_actions(m, rows, actions, dtype):
     for key, want in (("dh", dh), ("dw", dw)):
         assert float((out[key].double() - want).norm()) <= tol * float(want.norm()) + least * math.sqrt(want.numel()), key
     assert off(out["db"], db) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("rows,actions", [(300, 12), (30, 200), (200, 300)])
+@pytest.mark.parametrize("scale", [2.0 ** -118, -1e-30, 1e30])
+def test_scales_far_from_one(m, rows, actions, dtype, scale):
+    """G of a small scale is not below what the products take."""
+    c = _case(37, rows, 40, actions, dtype)
+    out = _run(m, c, scale=scale)
+    sync()
+    _check(c, out, scale)
