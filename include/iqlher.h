@@ -754,7 +754,9 @@ int iqlh_matrix_set_fill(const iqlh_matrix* matrices, int32_t count, void* host_
  *   eps        > 0 (1e-7 is the usual choice).
  *   d_flags    device sticky flag word or NULL: IQLH_FLAG_NONFINITE_GRAD.
  *   workspace  device, >= set->workspace_bytes, 16-byte aligned, no initial
- *              contents required; calls that overlap in time need one each.
+ *              contents required; calls that overlap in time need one each.  Neither it
+ *              nor d_flags may share memory with the matrices or the table (not checked:
+ *              the call does not see their addresses).
  * The results do not depend on timing. */
 int iqlh_orthogonalize(const iqlh_matrix_set* set, int32_t steps, double eps, int32_t* d_flags,
                        void* workspace, size_t workspace_bytes, void* stream);

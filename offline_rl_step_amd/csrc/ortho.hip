@@ -21,9 +21,9 @@
 // with the value itself, which is what one plane of 11 bits leaves at about 1e-3 of the result
 // and two at 1e-6.
 //
-// Bound by the products: 8192 x 8192 in one plane 990 us for X's (1.1 PF), 685 and 725 for the symmetric ones, whose
-// 528 tiles are three rounds of 256 compute units for 2.06; four of 1024 x 1024 and three of width 4096 in two planes
-// 112, 63 and 114.  Small lists by what a launch and a tile's start and results take, 9 to 11 us a
+// Bound by the products: 8192 x 8192 in one plane 990 to 1020 us for X's (1.1 PF), 670 to 700 and 725 to 745 for the
+// symmetric ones, whose 528 tiles are three rounds of 256 compute units for 2.06; four of 1024 x 1024 and three of width
+// 4096 in two planes 109, 63 and 114 to 128.  Small lists by what a launch and a tile's start and results take, 9 to 11 us a
 // product of 512 x 512 x 256.  Norm and start move 12 and 6 (planes: 8) bytes an element at the copy's rate.
 #include "iqlher.h"
 #include "launch.hpp"

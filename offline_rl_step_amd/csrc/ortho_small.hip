@@ -7,7 +7,7 @@
 // straight from LDS: rows as they are, columns by the transposing read, from the same
 // place.  Bound by one compute unit's matrix instructions (15 products of 128^3 in two planes 19 us at
 // 2.4 GHz, in one 6.4): a product is 3.4 us, of which 1.3 are theirs, the rest reads, barriers and results.
-// Four matrices of 128 x 128 among a step's list: 70 us, with a launch a product 97.
+// Four matrices of 128 x 128 among a step's list: 71 us, with a launch a product 97.
 #include "iqlher.h"
 #include "launch.hpp"
 #include "ortho_block.hpp"

@@ -25,8 +25,9 @@
 // One factor for a matrix lost all bits of a column that another is 2^30 times as large as.
 //
 // Bound by the products, the logits' twice: 8192 x 65536 x 2048 bf16 7.1 ms, 1.17 to 1.26 PF each; 16384 x 32768 x
-// 512 bf16, loss alone, 0.51 ms, 1.08 PF; 4096 x 16384 x 512 fp32 0.84 ms, 0.9 to 1.1 PF of binary16 products.  What is not
-// a product there: conversions of binary32 and of rows that are not whole 16-byte chunks, 19 of 116 us at 777 x 10007 x 501.
+// 512 bf16, loss alone, 0.51 to 0.58 ms, 0.95 to 1.08 PF; 4096 x 16384 x 512 fp32 0.85 to 0.89 ms, 0.9 to 1.1 PF of binary16
+// products, and 85 us for columns' magnitudes and planes.  What is not a product else: copies of rows that are not whole 16-byte
+// chunks, 18 of 116 us at 777 x 10007 x 501.
 #include "policy_block.hpp"
 
 namespace iqlh {
