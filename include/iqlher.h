@@ -630,7 +630,9 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  *            `dtype` (IQLH_F32, IQLH_BF16, IQLH_F16), `dim` columns, aligned to
  *            their element.
  *   bias     device [actions] f32 or NULL (0).  Minus infinity: an action that is
- *            never taken, probability 0.
+ *            never taken (forbidden), probability 0; its weights must be finite all the
+ *            same.  What is below about -2.35e38, as binary32's lowest value is, counts
+ *            as minus infinity.
  *   taken    device [rows] int32.  -1: a row without an action; it adds nothing to
  *            the loss or the gradients (nll 0).  Others outside [0, actions) count as
  *            -1 and set IQLH_FLAG_BAD_INDEX.
@@ -644,7 +646,7 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  * take part as they are for up to 16 actions (of dim up to 1024) and in the loss of up to 16
  * rows (of dim up to about 32768 / rows); else they are held in 22 bits, and no finer than 2^-38
  * of the largest of what they share a power of two with.  In the logits that is, with c the
- * largest |weight| of each column, the row's largest |hidden c| and the action's largest
+ * largest |weight| of each column among actions that are not forbidden, the row's largest |hidden c| and the action's largest
  * |weight / c|.  (An infinity among them may make NaN of the rows it is multiplied into.)
  * Where an action taken has probability 0, nll and the loss are infinite; a row whose
  * logits hold a NaN or plus infinity gets NaN.
@@ -665,7 +667,8 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  * about 2^-27 of that lose bits, below 2^-38 all.  Binary32 (unless as it is, above): G in 22 bits, no finer than
  * 2^-38 of |scale row_weights| of its row, so that an action's own d_weight is held to 2^-38 of
  * what it would be with probability 1; weight, in d_hidden, and hidden times its row's weight, in
- * d_weight, in 22 bits and no finer than 2^-38 of their column's largest.
+ * d_weight, in 22 bits and no finer than 2^-38 of their column's largest, without forbidden actions
+ * unless one of them is taken.
  *
  *   workspace  device, >= iqlh_policy_loss_workspace_bytes(.., grad 1 for the gradients),
  *              16-byte aligned, no initial contents required; calls that overlap in

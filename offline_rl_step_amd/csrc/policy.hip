@@ -18,7 +18,7 @@
 // Binary32 inputs: H, W and G are two planes of binary16 each (tile16.hpp) behind a power of two that takes
 // the largest of what shares it to [2^13, 2^14): 22 bits for what is within 2^-17 of that largest, and to 2^-38 of
 // it below.  What is not summed together, or can be moved to the other side of the product, shares none.  With
-// c_d the largest |W_vd| of a column, as powers of two all of them:
+// c_d the largest |W_vd| of a column, without the actions that are forbidden, as powers of two all of them:
 //   z = sum_d (H_rd c_d) (W_vd / c_d)      a factor for each row and each action,
 //   dH = sum_v G_rv W_vd                   for each row of G (by |w_r|) and each column of W,
 //   dW = sum_r (G_rv / |w_r|) (H_rd |w_r|) for each column of H |w|, G as for dH.
@@ -88,19 +88,49 @@ __global__ __launch_bounds__(kNT) void policy_weights_kernel(const int32_t* take
     }
 }
 
-__global__ __launch_bounds__(kNT) void policy_empty_kernel(int32_t* cols, int n) {
-    const int i = blockIdx.x * kNT + threadIdx.x;
-    if (i < n) cols[i] = kNoBits;
+// An action that is never taken: 2^(its bias in bits) is 0
+IQLH_DEV bool forbidden(const float* bias, int64_t v) { return bias && bias[v] * kLog2e == kNone; }
+
+// Empty columns for policy_columns_kernel; and (part) whether a forbidden action was taken all the same in a row that is
+// on, of each wave of kStartBlocks workgroups
+constexpr int kStartBlocks = 64, kStartWaves = kStartBlocks * kNT / kWave;
+static_assert(kStartWaves <= kAbsBlocks, "their place in the workspace");
+struct StartArgs {
+    int32_t* cols;
+    int n_cols;
+    int32_t* part;  // [kStartWaves], or null
+    const int32_t* taken;
+    const float *row_weights, *bias;
+    int64_t rows, actions;
+};
+__global__ __launch_bounds__(kNT) void policy_start_kernel(StartArgs a) {
+    const int64_t first = (int64_t)blockIdx.x * kNT + threadIdx.x, step = (int64_t)gridDim.x * kNT;
+    for (int64_t i = first; i < a.n_cols; i += step) a.cols[i] = kNoBits;
+    if (!a.part) return;
+    bool any = false;
+    for (int64_t m = first; m < a.rows; m += step)
+        if (!row_off(a.taken, a.row_weights, a.actions, m)) any |= forbidden(a.bias, a.taken[m]);
+    any = __any(any);
+    if ((threadIdx.x & 63) == 0) a.part[first / kWave] = any;
+}
+// Of a whole wave: bias, or null where forbidden actions count as others do, one of them being taken
+IQLH_DEV const float* bias_that_forbids(const float* bias, const int32_t* part) {
+    if (!bias || !part) return bias;
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < kStartWaves; i += kWave) any |= part[i + (threadIdx.x & 63)];
+    return __any(any) ? nullptr : bias;
 }
 
 // Magnitudes of the columns of hidden (blockIdx.z 0; its rows' weights times them, rows that are off left out) and of
-// the head's weights (1), binary32: 8 `lanes` columns a workgroup, each lane 8 of every (gridDim.x kNT / lanes)-th row.
-// gridDim.x above 1: columns that policy_empty_kernel left.
+// the head's weights (1; forbidden actions left out), binary32: 8 `lanes` columns a workgroup, each lane 8 of every
+// (gridDim.x kNT / lanes)-th row.  gridDim.x above 1: columns that policy_start_kernel left.
 struct ColumnArgs {
     PolicyMat m[2];
     int32_t* to[2];
     const int32_t* taken;
-    const float* row_weights;
+    const float *row_weights, *bias;
+    const int32_t* part;  // of policy_start_kernel, or null
     int64_t actions, ld;
     int lanes;
 };
@@ -109,6 +139,7 @@ __global__ __launch_bounds__(kNT) void policy_columns_kernel(ColumnArgs a) {
     __shared__ int red[kNT][8];
     const PolicyMat& q = a.m[blockIdx.z];
     if (!q.p) return;
+    const float* bias = blockIdx.z ? bias_that_forbids(a.bias, a.part) : nullptr;
     const int lane = threadIdx.x % a.lanes, own = threadIdx.x / a.lanes, at_once = kNT / a.lanes;
     const int first = blockIdx.y * 8 * a.lanes, col = first + 8 * lane, n = (int)q.cols - col;
     int top[8];
@@ -124,13 +155,13 @@ __global__ __launch_bounds__(kNT) void policy_columns_kernel(ColumnArgs a) {
             for (int k = 0; k < AHEAD; ++k) {  // behind the end: the first row again
                 const int64_t row = row0 + k * step < q.rows ? row0 + k * step : row0;
                 t[k] = decltype(hidden)::value ? a.taken[row] : 0;
-                w[k] = decltype(hidden)::value && a.row_weights ? a.row_weights[row] : 1.f;
+                w[k] = decltype(hidden)::value ? (a.row_weights ? a.row_weights[row] : 1.f) : bias ? bias[row] : 0.f;
                 load8_of(IQLH_F32, q.p, row * q.ld + col, n, v[k]);
             }
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
-                const bool off = t[k] < 0 || t[k] >= a.actions || w[k] == 0.f;
-                const int add = !decltype(hidden)::value ? 0 : off ? kNoBits : weight_bits(bits_of(w[k]));
+                const bool off = decltype(hidden)::value ? t[k] < 0 || t[k] >= a.actions || w[k] == 0.f : w[k] * kLog2e == kNone;
+                const int add = off ? kNoBits : decltype(hidden)::value ? weight_bits(bits_of(w[k])) : 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int b = bits_of(v[k][i]) + add;
@@ -166,13 +197,15 @@ struct Convert {
     int64_t ld_to;
     const int32_t* cols;      // binary32: [ld_to]
     int32_t* row_exp;         // or null: not by rows
-    int sign, zero_off;       // zero_off: zeros in the place of rows that are off
+    int sign, zero_off;       // zero_off: zeros in the place of rows that are off; -1: of forbidden actions
     int weighted;
     int lanes, blocks;        // lanes: of a row, a power of two
 };
 struct ConvertArgs {
     Convert c[4];
     const int32_t* part;  // binary16: [kAbsBlocks], or null
+    const float* bias;            // binary32, or null
+    const int32_t* forbid_part;   // of policy_start_kernel, or null
     int32_t* g_top;       // their largest
     const int32_t* taken;
     const float* row_weights;
@@ -194,6 +227,10 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     const PolicyMat& q = c.m;
     if (!q.p) return;
     const int groups = (int)(c.ld_to / 8);
+    const float* bias = c.zero_off < 0 ? bias_that_forbids(a.bias, a.forbid_part) : nullptr;
+    auto off_row = [&](int64_t row) __attribute__((always_inline)) {
+        return c.zero_off < 0 ? forbidden(bias, row) : c.zero_off && row_off(a.taken, a.row_weights, a.actions, row);
+    };
     auto fetch = [&](int64_t row, int col, bool off, float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -202,8 +239,9 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
     auto column_bits = [&](int col, int (&b)[8]) __attribute__((always_inline)) {
         const int4 x = *(const int4*)(c.cols + col), y = *(const int4*)(c.cols + col + 4);
         b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w, b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
+        // what meets nothing but zeros: 0, and of no magnitude (a division of those zeros by any power of two will do)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = c.sign * or_zero(b[i]);
+        for (int i = 0; i < 8; ++i) b[i] = c.sign > 0 ? b[i] : -or_zero(b[i]);
     };
     // times 2^(e + b)
     auto put = [&](int64_t row, int col, float (&v)[8], int e, const int (&b)[8]) __attribute__((always_inline)) {
@@ -223,7 +261,7 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
         column_bits(8 * (in < groups ? in : 0), b0);
         for (int64_t row0 = (int64_t)block * rows_at_once; row0 < q.rows; row0 += (int64_t)c.blocks * rows_at_once) {
             const int64_t row = row0 + threadIdx.x / lanes;
-            const bool off = row < q.rows && c.zero_off && row_off(a.taken, a.row_weights, a.actions, row);
+            const bool off = row < q.rows && off_row(row);
             float v0[8];
             fetch(row, 8 * in, off, v0);
             int top = kNoBits;
@@ -266,7 +304,7 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
                 const int col = 8 * (int)(e - row * groups);
                 float v[8];
                 int b[8] = {};
-                fetch(row, col, c.zero_off && row_off(a.taken, a.row_weights, a.actions, row), v);
+                fetch(row, col, off_row(row), v);
                 if (f32) column_bits(col, b);
                 put(row, col, v, kTop + (c.weighted ? weight_bits(a.row_weights, row) : 0), b);
             }
@@ -293,15 +331,15 @@ __global__ __launch_bounds__(kNT) void policy_convert_kernel(ConvertArgs a) {
                 } else {
                     x[k] = *(const u4_a2*)((const uint16_t*)q.p + from);
                 }
-                t[k] = c.zero_off ? a.taken[row] : 0;
-                w[k] = c.zero_off && a.row_weights ? a.row_weights[row] : 1.f;
+                t[k] = c.zero_off > 0 ? a.taken[row] : 0;
+                w[k] = c.zero_off > 0 && a.row_weights ? a.row_weights[row] : bias ? bias[row] : 1.f;
             }
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 if (p[k].row >= q.rows) continue;
                 const int64_t past = 8 * (int64_t)p[k].group - (q.cols - 8);
                 const int move = past < 0 ? 0 : past > 8 ? 8 : (int)past;
-                const bool off = t[k] < 0 || t[k] >= a.actions || w[k] == 0.f || move == 8;
+                const bool off = t[k] < 0 || t[k] >= a.actions || (bias ? w[k] * kLog2e == kNone : w[k] == 0.f) || move == 8;
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -800,7 +838,7 @@ PolicyPlan policy_plan(int64_t rows, int64_t actions, int64_t dim, int dtype, bo
         auto dw_parts = [&](int64_t n) { const int64_t k = split_for(n, dim, rows, p.planes).n; return k > 1 ? k * n : 0; };
         const int64_t dw_full = dw_parts(full), dw_last = dw_parts(last);
         p.g_top = take(4);
-        p.weight_top = take(kAbsBlocks * 4);
+        p.weight_top = take(kAbsBlocks * 4);  // or kStartWaves
         p.h_dw = take(p.planes == 2 ? (size_t)rows * p.ld * 4 : 0);
         p.w_dh = take(p.planes == 2 ? (size_t)actions * p.ld * 4 : 0);
         p.g = take((size_t)rows * p.piece * 2 * p.g_planes);
@@ -845,7 +883,7 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
         ColumnArgs m{};
         m.m[0] = grad && a.d_weight ? a.h : none, m.m[1] = a.w;
         m.to[0] = (int32_t*)(base + p.cols), m.to[1] = m.to[0] + p.ld;
-        m.taken = a.taken, m.row_weights = a.row_weights, m.actions = a.w.rows, m.ld = p.ld;
+        m.taken = a.taken, m.row_weights = a.row_weights, m.bias = a.bias, m.actions = a.w.rows, m.ld = p.ld;
         m.lanes = a.h.cols <= 64 ? 8 : 16;
         o->cols_h = m.to[0], o->cols_w = m.to[1];
         o->row_exp = (int32_t*)(base + p.row_exp), o->act_exp = (int32_t*)(base + p.act_exp);
@@ -853,17 +891,24 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
         const int64_t most = m.m[0].p && a.h.rows > a.w.rows ? a.h.rows : a.w.rows, chunks = (p.ld + 8 * m.lanes - 1) / (8 * m.lanes);
         int64_t slabs = most <= 512 ? 1 : 512 / chunks < 32 ? 32 : 512 / chunks;
         if (slabs > (most + 63) / 64) slabs = (most + 63) / 64;
-        if (slabs > 1)
-            hipLaunchKernelGGL(policy_empty_kernel, dim3((uint32_t)((2 * p.ld + kNT - 1) / kNT)), dim3(kNT), 0, stream, m.to[0], (int)(2 * p.ld));
+        // d_hidden of a row that took a forbidden action has that action's weights
+        const bool forbids = grad && a.d_hidden && a.bias;
+        if (slabs > 1 || forbids) {
+            StartArgs s{m.to[0], (int)(2 * p.ld), forbids ? (int32_t*)(base + p.weight_top) : nullptr, a.taken, a.row_weights, a.bias,
+                        a.h.rows, a.w.rows};
+            m.part = c.forbid_part = s.part;
+            hipLaunchKernelGGL(policy_start_kernel, dim3(forbids ? kStartBlocks : (uint32_t)((2 * p.ld + kNT - 1) / kNT)), dim3(kNT), 0, stream, s);
+        }
+        c.bias = a.bias;
         hipLaunchKernelGGL(policy_columns_kernel, dim3((uint32_t)slabs, (uint32_t)chunks, 2), dim3(kNT), 0, stream, m);
     }
     int n = 0;
     auto convert = [&](const PolicyMat& q, size_t at, bool zero_off, int32_t* row_exp, const int32_t* cols, int sign,
-                       bool weighted) {
+                       bool weighted, bool forbids = false) {
         int lanes = 8;  // rows are of 8 groups or more
         while (lanes < kWave && lanes < p.ld / 8) lanes *= 2;
         const int64_t blocks = row_exp ? (q.rows * lanes + kNT - 1) / kNT : (q.rows * (p.ld / 8) + 4 * kNT - 1) / (4 * kNT);
-        c.c[n++] = Convert{q,       (uint16_t*)(base + at), p.ld, cols, row_exp, sign, zero_off, weighted, lanes,
+        c.c[n++] = Convert{q,       (uint16_t*)(base + at), p.ld, cols, row_exp, sign, forbids ? -1 : zero_off, weighted, lanes,
                            (int)(blocks < 4096 ? blocks : 4096)};
         return Side16{(const uint16_t*)(base + at), 0, p.ld, q.rows};
     };
@@ -872,7 +917,7 @@ hipError_t prepare(const PolicyArgs& a, const PolicyPlan& p, bool grad, Operands
         o->h = convert(a.h, p.h, grad, (int32_t*)o->row_exp, o->cols_w, 1, false);
         o->w = convert(a.w, p.w, false, (int32_t*)o->act_exp, o->cols_w, -1, false);
         if (grad && a.d_weight) o->h_dw = convert(a.h, p.h_dw, true, nullptr, o->cols_h, -1, true);
-        if (grad && a.d_hidden) o->w_dh = convert(a.w, p.w_dh, false, nullptr, o->cols_w, -1, false);
+        if (grad && a.d_hidden) o->w_dh = convert(a.w, p.w_dh, false, nullptr, o->cols_w, -1, false, true);
     } else {
         // both in place or both converted, but for H of the gradients: the summed axis is as long in one as in the other
         const bool copy = !in_place(a.w) || (!grad && !in_place(a.h));

@@ -2,7 +2,7 @@
 
 Binary32 operands of the tile kernels are two binary16 planes behind a power of two that takes the
 largest of what shares it to [2^13, 2^14): 22 bits, and no better than half of binary16's smallest step, 2^-25
-there, 2^-38 of that largest.  With c[d] the largest |weight| of column d:
+there, 2^-38 of that largest.  With c[d] the largest |weight| of column d among the actions that are not forbidden:
 * logits: hidden[r][d] c[d] shares a row's, weight[v][d] / c[d] an action's, c within a factor of 2, so
   a product is off by up to 2^-36 of the two largest;
 * d_hidden: G shares |scale w| of its row, weight[.][d] its column's;
@@ -73,12 +73,12 @@ def _check_planes(c, out):
     loss, nll, lse = ref.loss(h, w, taken, **kw)
     _, on = ref.on_rows(taken, actions, rw)
     ah, aw = np.abs(h), np.abs(w)
-    col = aw.max(0)
+    col = aw[np.isfinite(b)].max(0)
     with np.errstate(invalid="ignore", divide="ignore"):
         z = ref.logits(h, w, b)
         ez = (dim + 8) * U * (ah @ aw.T) + 8 * U * np.where(np.isfinite(z), np.abs(z) + 1, 0)
         ez += 8 * U * np.where(np.isfinite(b), np.abs(b), 0)[None, :]
-        ez += 2.0 ** -21 * (ah @ aw.T) + 2.0 ** -36 * dim * np.outer((ah * col).max(1), (aw / col).max(1))
+        ez += 2.0 ** -21 * (ah @ aw.T) + 2.0 ** -36 * dim * np.outer((ah * col).max(1), np.where(col > 0, aw / col, 0).max(1))
         ez = np.where(np.isfinite(b)[None, :], ez, 0)
         ez += 8 * U * np.abs(lse)[:, None]
     err = ez.max(axis=1) + 16 * U * (1 + np.abs(lse))
@@ -120,6 +120,11 @@ def _spread(c, kind, seed=5):
         c["taken"][c["taken"] == 7] = 8
         b[8] = 0.25
         w[7] *= 2.0 ** 30
+    elif kind == "unused":  # a feature without weights
+        h[:, 5] *= 2.0 ** 40
+        w[:, 5] = 0
+    elif kind == "padding":  # forbidden actions that hold anything finite
+        w[b == -math.inf] *= torch.exp2(torch.randint(-90, 91, (dim,), generator=g).float()).to(dev())
     elif kind == "actions":
         w *= torch.exp2(torch.randint(-30, 1, (w.shape[0], 1), generator=g).float()).to(dev())
     elif kind == "rows":
@@ -135,7 +140,8 @@ def _spread(c, kind, seed=5):
         rw *= 2.0 ** -100
 
 
-@pytest.mark.parametrize("kind", ["a feature", "features", "an action", "actions", "rows", "weights", "large", "small"])
+@pytest.mark.parametrize("kind", ["a feature", "features", "unused", "an action", "padding", "actions", "rows", "weights", "large",
+                                  "small"])
 @pytest.mark.parametrize("rows,dim,actions", [(30, 24, 70), (200, 72, 300), (150, 600, 130)])
 def test_float32_of_many_magnitudes(m, rows, dim, actions, kind):
     c = _case(29, rows, dim, actions, "float32")
@@ -298,3 +304,23 @@ def test_scales_far_from_one(m, rows, actions, dtype, scale):
     out = _run(m, c, scale=scale)
     sync()
     _check(c, out, scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows", [9, 200])
+def test_biases_of_the_lowest_value_forbid(m, rows, dtype):
+    """A bias of binary32's lowest value is that of a forbidden action, in the loss, the gradients and where it is
+    taken all the same."""
+    import torch
+    for actions in (12, 200):
+        c = _case(43, rows, 40, actions, dtype, off=0)
+        c["taken"][3] = 5
+        got = []
+        for low in (-math.inf, torch.finfo(torch.float32).min):
+            c["bias"][c["bias"] < -1e30] = low
+            c["bias"][5] = low
+            got.append(_run(m, c))
+        sync()
+        assert got[0]["nll"][3].item() == math.inf
+        for k in got[0]:
+            assert torch.equal(got[0][k], got[1][k]), (actions, k)
