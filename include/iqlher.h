@@ -631,7 +631,7 @@ int iql_forward_values_mx4(iql_handle h, const void* next_states, int32_t states
  *            their element.
  *   bias     device [actions] f32 or NULL (0).  Minus infinity: an action that is
  *            never taken (forbidden), probability 0; its weights must be finite all the
- *            same.  What is below about -2.35e38, as binary32's lowest value is, counts
+ *            same, and so must their products with hidden.  What is below about -2.35e38, as binary32's lowest value is, counts
  *            as minus infinity.
  *   taken    device [rows] int32.  -1: a row without an action; it adds nothing to
  *            the loss or the gradients (nll 0).  Others outside [0, actions) count as

@@ -108,8 +108,20 @@ __global__ __launch_bounds__(kNT) void policy_start_kernel(StartArgs a) {
     for (int64_t i = first; i < a.n_cols; i += step) a.cols[i] = kNoBits;
     if (!a.part) return;
     bool any = false;
-    for (int64_t m = first; m < a.rows; m += step)
-        if (!row_off(a.taken, a.row_weights, a.actions, m)) any |= forbidden(a.bias, a.taken[m]);
+    constexpr int AHEAD = 8;
+    for (int64_t m0 = first; m0 < a.rows; m0 += AHEAD * step) {
+        int32_t t[AHEAD];
+        bool on[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {  // behind the end: the first row again
+            const int64_t m = m0 + k * step < a.rows ? m0 + k * step : m0;
+            const float w = a.row_weights ? a.row_weights[m] : 1.f;
+            t[k] = a.taken[m];
+            on[k] = t[k] >= 0 && t[k] < a.actions && w != 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) any |= on[k] & forbidden(a.bias, on[k] ? t[k] : 0);
+    }
     any = __any(any);
     if ((threadIdx.x & 63) == 0) a.part[first / kWave] = any;
 }
@@ -189,8 +201,8 @@ __global__ __launch_bounds__(kNT) void policy_columns_kernel(ColumnArgs a) {
 }
 
 // Matrices as operands: rows of whole 64 16-bit elements, zeros behind the end.  Binary32 in two planes: x in row r
-// and column d times 2^(kTop + sign cols[d]) and (weighted) the weight's magnitude, or, by rows, times 2^(sign cols[d] - row_exp[r]) with
-// row_exp of the row's largest, which is written.
+// and column d times 2^(kTop + sign cols[d]) and (weighted) the weight's magnitude, or, by rows, times 2^(sign cols[d] -
+// row_exp[r]) with row_exp of the row's largest, which is written.
 struct Convert {
     PolicyMat m;
     uint16_t* to;             // [rows][ld_to]
@@ -203,10 +215,10 @@ struct Convert {
 };
 struct ConvertArgs {
     Convert c[4];
-    const int32_t* part;  // binary16: [kAbsBlocks], or null
-    const float* bias;            // binary32, or null
-    const int32_t* forbid_part;   // of policy_start_kernel, or null
-    int32_t* g_top;       // their largest
+    const int32_t* part;         // binary16: [kAbsBlocks], or null
+    int32_t* g_top;              // their largest
+    const float* bias;           // binary32, or null
+    const int32_t* forbid_part;  // of policy_start_kernel, or null
     const int32_t* taken;
     const float* row_weights;
     int64_t actions;

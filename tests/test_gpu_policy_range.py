@@ -324,3 +324,23 @@ def test_biases_of_the_lowest_value_forbid(m, rows, dtype):
         assert got[0]["nll"][3].item() == math.inf
         for k in got[0]:
             assert torch.equal(got[0][k], got[1][k]), (actions, k)
+
+
+@pytest.mark.parametrize("rows", [30, 20000])
+def test_a_forbidden_action_that_is_taken_has_its_weights_in_d_hidden(m, rows):
+    """float32: its row's d_hidden is -scale w of its weights (and what the other actions add), however large they are
+    beside the others'; the loss is infinite."""
+    import torch
+    c = _case(45, rows, 24, 70, "float32")
+    last = int((c["taken"] >= 0).nonzero()[-1])
+    c["bias"][7] = -math.inf
+    c["taken"][c["taken"] == 7] = 8
+    c["bias"][8] = 0.25
+    c["taken"][last] = 7
+    c["weight"][7] *= 2.0 ** 60
+    out = _run(m, c)
+    sync()
+    assert out["loss"].item() == math.inf and out["nll"][last].item() == math.inf
+    want = -c["weight"][7].double() * c["row_weights"][last].double() / rows
+    # G and the weight to 2^-22 each, the result's rounding
+    assert bool(((out["dh"][last].double() - want).abs() <= 2.0 ** -20 * want.abs()).all())
